@@ -584,7 +584,7 @@ def exact(case, seed):
     pool, ps = s["pool"], case["ps"]
     table, lens, refs = (pool[x].tolist() for x in ("table", "lens", "refs"))
     k, v = pool["k"].double(), pool["v"].double()
-    start = []
+    start = []                                       # of the new tokens
 
     def take():
         page = refs.index(0)
@@ -624,9 +624,8 @@ def exact(case, seed):
         lens[c] = keep
     for c, add in zip(s["child"].tolist(), s["add"].tolist()):
         start.append(lens[c])
-        while pages(c) * ps < lens[c] + add:
-            table[c][pages(c)] = take()
-            lens[c] = min(lens[c] + add, (pages(c) + 1) * ps)
+        for i in range(pages(c), -(-(lens[c] + add) // ps)):
+            table[c][i] = take()
         lens[c] = start[-1] + add
     for a, c in zip(s["src"].tolist(), s["dst"].tolist()):
         for x in (k, v):
