@@ -368,6 +368,166 @@ int mikv_channel_quantize(const uint16_t* k, int units, int n, int D, int bits, 
                           uint16_t* meta, void* stream);
 
 /*
+ * The paged cache (no counterpart in the papers: they give one prompt's tiers; a serving loop
+ * holds many sequences that differ in length, share prefixes and give memory back).
+ *
+ * One pool of pages for all layers, one table for all layers: slot j of sequence s lies, in
+ * every layer and for every key head, in row j % page_size of page table[s][j / page_size].
+ *   k, v    type FP16, BF16: 16-bit rows [layers][n_pages][Hkv][page_size][D]
+ *           type INT8: uint8 codes of the same shape, and k_meta, v_meta fp16
+ *           [layers][n_pages][Hkv][page_size][D/64][2] (scale, zero): the per-token quantiser
+ *           of mikv_quantize_append at 8 bits, unbalanced; rows handed in or out are fp16.
+ *   table   int32 [max_seqs][max_pages]; entries past a sequence's pages are not read
+ *           (-1 where a call has cleared them)
+ *   lens    int32 [max_seqs]: slots of each sequence, 0 for one that is not in use; the
+ *           sequence owns the first ceil(len / page_size) entries of its row
+ *   refs    int32 [n_pages]: how many sequences own the page; 0 = free.  A page whose count
+ *           the caller raises itself is never handed out.
+ * table, lens and refs are device arrays: the calls below read and change them on the stream,
+ * so a whole step can be captured into a CUDA graph.  A new cache has lens 0 and refs 0.
+ * Calls that change the same cache must be ordered (one stream, or events), like writes to any
+ * buffer.  page_size 1..4096; max_pages * page_size < 2^31 - 4096; n_pages * Hkv * page_size
+ * < 2^32 - 1; Hkv <= 1024; buffers 16-byte aligned.
+ *
+ * Calls over several sequences take their numbers in `seqs` int32 [n] (device), or NULL for
+ * 0 .. n - 1 (n <= max_seqs).  The calls that change tables report per request; a request is
+ * refused, and changes nothing, where
+ *   - a sequence number is outside 0 .. max_seqs - 1, or an earlier request of the same call
+ *     names the same sequence,
+ *   - its own rule below is broken, or
+ *   - the free pages do not suffice for it and all valid requests before it.
+ * New pages are the free pages of lowest number, in request order.  n is at most 4096 for
+ * reserve, fork and compact, 65535 otherwise; n == 0 does nothing.
+ */
+#define MIKV_PAGES_FP16 0
+#define MIKV_PAGES_BF16 1
+#define MIKV_PAGES_INT8 2
+
+typedef struct mikv_pages {
+  int32_t layers, n_pages, page_size, Hkv, D, type;
+  int32_t max_seqs, max_pages;
+  void* k;
+  void* v;
+  void* k_meta; /* INT8 only, else NULL */
+  void* v_meta;
+  int32_t* table;
+  int32_t* lens;
+  int32_t* refs;
+} mikv_pages;
+
+/* A strided view of 16-bit rows [B][H][T][D], D contiguous: element (b, h, t, d) at
+ * data[b * stride_b + h * stride_h + t * stride_t + d].  data and the strides are multiples
+ * of 16 bytes (8 elements), the strides not negative. */
+typedef struct mikv_rows {
+  void* data;
+  int64_t stride_b, stride_h, stride_t; /* in elements */
+} mikv_rows;
+
+/*
+ * Reserve: makes room for add[i] >= 0 more tokens behind each sequence, and lengthens it.
+ * start[i] (written) is the slot of the first new token, the length before the call, or -1
+ * where the request was refused.  Refused too: a length above max_pages * page_size.
+ * ws >= mikv_page_workspace_bytes(p, n) bytes, 16-byte aligned (here and below).
+ * Errors (all page calls): EINVAL (null), ESHAPE (dimensions, n, workspace), EALIGN,
+ * EUNSUPPORTED (D), ECUDA.
+ */
+int mikv_page_reserve(const mikv_pages* p, const int32_t* seqs, const int32_t* add, int n, int32_t* start, void* ws,
+                      size_t ws_bytes, void* stream);
+
+/*
+ * Fork: child[i] becomes a copy of parent[i].  Full pages are shared; a partly filled last
+ * page is copied in all layers (its filled rows), so either sequence can grow.  ok[i]
+ * (written) is 1, or 0 where refused: also where the child's length is not 0, or where the
+ * child is a parent of the same call.  One parent may have several children in one call.
+ */
+int mikv_page_fork(const mikv_pages* p, const int32_t* parent, const int32_t* child, int n, int32_t* ok, void* ws,
+                   size_t ws_bytes, void* stream);
+
+/*
+ * Free: the sequences give their pages back and have length 0.  ok[i] (written): 1, or 0
+ * where refused; freeing an empty sequence is fine.
+ */
+int mikv_page_free(const mikv_pages* p, const int32_t* seqs, int n, int32_t* ok, void* stream);
+
+/*
+ * Copy: page dst[i] takes what page src[i] holds, in all layers, whoever owns them.  ok[i]
+ * (written): 1, or 0 where refused: a page outside the pool, a destination that an earlier
+ * pair of the call names too, or one that another pair reads.  src[i] == dst[i] does nothing.
+ */
+int mikv_page_copy(const mikv_pages* p, const int32_t* src, const int32_t* dst, int n, int32_t* ok, void* stream);
+
+/*
+ * Compact: sequence i keeps keep_n[i] of its slots; slot j of key head h in layer l becomes
+ * what slot keep_pos[l][i][h][j] was (keep_pos int32 [layers][n][Hkv][max_keep], e.g. the
+ * keep_pos that mikv_select writes; any order, a slot may be kept twice).  The kept rows move
+ * into new pages and the old ones are given back, so a sequence that shares pages may be
+ * compacted; the new pages have to be free before the old ones are.  ok[i] (written): 1, or 0
+ * where refused: also keep_n[i] outside 0 .. min(max_keep, length), or a position outside the
+ * sequence among its keep_n[i].
+ */
+int mikv_page_compact(const mikv_pages* p, const int32_t* seqs, const int32_t* keep_pos, const int32_t* keep_n, int n,
+                      int max_keep, int32_t* ok, void* ws, size_t ws_bytes, void* stream);
+size_t mikv_page_workspace_bytes(const mikv_pages* p, int n);
+
+/*
+ * Append: tokens 0 .. counts[i] - 1 of row i of k and v ([n][Hkv][T][D], fp16; bf16 for BF16
+ * pages) go to slots start[i] .. of its sequence in one layer.  counts NULL: T each (a count
+ * above T is T, one below 1 writes nothing).  start: what mikv_page_reserve wrote, rows with
+ * start < 0 are skipped; NULL: the sequence's last counts[i] slots.  Slots at or past the
+ * sequence's length are not written, nor are rows whose sequence is out of range or named by
+ * an earlier row.  INT8: quantised as in mikv_quantize_append.
+ */
+int mikv_paged_append(const mikv_pages* p, int layer, const mikv_rows* k, const mikv_rows* v, int n, int T,
+                      const int32_t* seqs, const int32_t* start, const int32_t* counts, void* stream);
+
+/*
+ * Gather: the first T slots of each sequence, as far as it reaches, as rows k_out and v_out
+ * ([n][Hkv][T][D], fp16; bf16 for BF16 pages).  INT8: fp16(fl(fl(scale * code) + zero)).  Rows at
+ * or past the sequence's length are left as they were; so are all rows of a sequence number
+ * out of range.  The output rows must not overlap one another.
+ */
+int mikv_paged_gather(const mikv_pages* p, int layer, const int32_t* seqs, int n, int T, const mikv_rows* k_out,
+                      const mikv_rows* v_out, void* stream);
+
+/*
+ * Attention of one new token per sequence over one layer of the paged cache.  Row i's query
+ * stands at the last slot p = len - 1 of its sequence (append its key and value first) and
+ * sees slot j where
+ *   window == 0, or j > p - window, or j < sinks        (0 <= j <= p)
+ * i.e. the `window` most recent slots and the first `sinks` ones.
+ *   l_j = q_h . k~_j / sqrt(D), out_h = sum_j exp(l_j - lse) v~_j, lse_h = log sum_j exp(l_j)
+ * q, out [n][Hq][D] fp16 (bf16 for BF16 pages), lse fp32 [n][Hq] (natural log; NULL: not
+ * written).  A sequence of length 0, or a number out of range, gives out 0 and lse -inf.
+ * Hq a multiple of Hkv, any number of query heads per key head; slots that are not seen may
+ * hold anything.  ws >= mikv_paged_attention_workspace_bytes(p, n, Hq, window, sinks), 16-byte
+ * aligned; two calls must not share a workspace concurrently.
+ * Errors: EINVAL (null, window < 0, sinks < 0), ESHAPE (layer, n outside 0..65535, Hq, workspace), EALIGN,
+ * EUNSUPPORTED, ECUDA.
+ */
+int mikv_paged_attention(const void* q, const mikv_pages* p, int layer, const int32_t* seqs, int n, int Hq, int window,
+                         int sinks, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+size_t mikv_paged_attention_workspace_bytes(const mikv_pages* p, int n, int Hq, int window, int sinks);
+
+/*
+ * Attention of a prompt, or of a chunk of one, over contiguous keys and values under a sliding
+ * window with sinks.  q, out [B][Hq][Tq][D], k, v [B][Hkv][Tk][D], all fp16 (type
+ * MIKV_PAGES_FP16) or bf16 (MIKV_PAGES_BF16), strided views.  q_lens, k_lens int32 [B]
+ * (device; NULL: Tq, Tk each; held inside 0 .. Tq, 0 .. Tk): the first q_lens[b] query rows and
+ * k_lens[b] key rows of batch row b count.  Query i stands at position
+ * p = k_lens[b] - q_lens[b] + i, the last one at the last key, and sees key j as in
+ * mikv_paged_attention.  A query that sees nothing (p < 0) gives out 0 and lse -inf.
+ * lse fp32 [B][Hq][Tq], or NULL.  Query rows at or past q_lens[b] are neither read nor written;
+ * key and value rows at or past k_lens[b] may hold anything.
+ * Requires Tq, Tk >= 1, Hq a multiple of Hkv; B == 0 does nothing.
+ * The softmax weights are rounded to the inputs' type before they meet the values; sums and
+ * statistics are fp32.
+ * Errors: EINVAL (null, type, window, sinks), ESHAPE, EALIGN, EUNSUPPORTED (D), ECUDA.
+ */
+int mikv_window_attention(const mikv_rows* q, const mikv_rows* k, const mikv_rows* v, int B, int Hq, int Hkv, int Tq, int Tk,
+                          int D, int type, const int32_t* q_lens, const int32_t* k_lens, int window, int sinks,
+                          const mikv_rows* out, float* lse, void* stream);
+
+/*
  * Measurement hook (no counterpart in the papers): while set, every
  * mikv_decode_attention and mikv_decode_step call made by this thread records
  * `begin` (a cudaEvent_t) on its stream just before the split-K attention
@@ -382,7 +542,7 @@ int mikv_set_attention_events(void* begin, void* end);
  * Wait status of the tensor-core kernels (no counterpart in the papers; a failure report).
  * The tcgen05 kernels (K3's two prefill score passes in mikv_score_update(MIKV_PREFILL),
  * K6's V.W_O norms in mikv_select(MIKV_CRITICALKV) with w_o, K9 in
- * mikv_output_perturbation) hand tiles between a TMA/MMA thread and their consumer warps
+ * mikv_output_perturbation, and mikv_window_attention) hand tiles between a TMA/MMA thread and their consumer warps
  * through mbarriers, and every wait there gives up after ~4 million polls instead of
  * spinning for ever.  No wait is expected to run out; if one does, the thread that gave up
  * issues no further copy or MMA, its later waits poll only ~1000 times each (so a stuck
@@ -392,7 +552,9 @@ int mikv_set_attention_events(void* begin, void* end);
  * The call that launched it has already returned MIKV_OK (launches are asynchronous).
  * mikv_wait_status stores the OR of the bits set since the last clear in *bits:
  *   1 = K3 pass 1 (row log-sum-exp), 2 = K3 pass 2 (column sums), 4 = K6 (V.W_O norms),
- *   8 = K9 (output perturbation), 16 = mikv_wait_probe
+ *   8 = K9 (output perturbation), 16 = mikv_wait_probe, 32 = mikv_window_attention,
+ *   64 = no wait: an append, a gather or an attention over pages met a table entry outside the
+ *   pool (its slots are skipped, read as zeros, or not seen)
  * and clears them if `clear` is non-zero.  It copies synchronously: call it after the work
  * in question has completed (e.g. after synchronising its stream).
  * Errors: EINVAL (null bits), ECUDA (the copy failed).

@@ -17,6 +17,7 @@ MIKV_PREFILL, MIKV_DECODE = 0, 1
 MIKV_H2O, MIKV_CRITICALKV, MIKV_DEMOTE = 0, 1, 2
 MIKV_TIER_HI, MIKV_TIER_LO, MIKV_TIER_DEMOTE = 0, 1, 2
 MIKV_KEYS_PER_TOKEN, MIKV_KEYS_PER_CHANNEL = 0, 1
+MIKV_PAGES_FP16, MIKV_PAGES_BF16, MIKV_PAGES_INT8 = 0, 1, 2
 
 EXPORTS = (
     "mikv_balance_prefill", "mikv_balance_workspace_bytes", "mikv_balance_prefill_noalloc",
@@ -28,6 +29,9 @@ EXPORTS = (
     "mikv_output_perturbation", "mikv_output_perturbation_workspace_bytes",
     "mikv_topk_attention", "mikv_topk_attention_workspace_bytes",
     "mikv_channel_quantize",
+    "mikv_page_reserve", "mikv_page_fork", "mikv_page_free", "mikv_page_copy", "mikv_page_compact",
+    "mikv_page_workspace_bytes", "mikv_paged_append", "mikv_paged_gather",
+    "mikv_paged_attention", "mikv_paged_attention_workspace_bytes", "mikv_window_attention",
     "mikv_set_attention_events", "mikv_wait_status", "mikv_wait_probe", "mikv_last_error",
 )
 
@@ -54,6 +58,21 @@ class mikv_cache(ctypes.Structure):
     ]
 
 
+class mikv_pages(ctypes.Structure):
+    _fields_ = [
+        ("layers", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("type", ctypes.c_int32),
+        ("max_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_meta", ctypes.c_void_p), ("v_meta", ctypes.c_void_p),
+        ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+    ]
+
+
+class mikv_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_t", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -67,7 +86,7 @@ def load() -> ctypes.CDLL:
                            "python -m mixed_precision_kv_balancer_gb300.build")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, S, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
-    CP = ctypes.POINTER(mikv_cache)
+    CP, GP, RP = ctypes.POINTER(mikv_cache), ctypes.POINTER(mikv_pages), ctypes.POINTER(mikv_rows)
     sig = {
         "mikv_balance_prefill": (I, [P, P, I, I, I, I, I, P, P, S, P]),
         "mikv_balance_workspace_bytes": (S, [I, I, I]),
@@ -86,6 +105,17 @@ def load() -> ctypes.CDLL:
         "mikv_topk_attention": (I, [P, CP, I, P, P, P, P, S, P]),
         "mikv_topk_attention_workspace_bytes": (S, [CP, I]),
         "mikv_channel_quantize": (I, [P, I, I, I, I, P, P, P]),
+        "mikv_page_reserve": (I, [GP, P, P, I, P, P, S, P]),
+        "mikv_page_fork": (I, [GP, P, P, I, P, P, S, P]),
+        "mikv_page_free": (I, [GP, P, I, P, P]),
+        "mikv_page_copy": (I, [GP, P, P, I, P, P]),
+        "mikv_page_compact": (I, [GP, P, P, P, I, I, P, P, S, P]),
+        "mikv_page_workspace_bytes": (S, [GP, I]),
+        "mikv_paged_append": (I, [GP, I, RP, RP, I, I, P, P, P, P]),
+        "mikv_paged_gather": (I, [GP, I, P, I, I, RP, RP, P]),
+        "mikv_paged_attention": (I, [P, GP, I, P, I, I, I, I, P, P, P, S, P]),
+        "mikv_paged_attention_workspace_bytes": (S, [GP, I, I, I, I]),
+        "mikv_window_attention": (I, [RP, RP, RP, I, I, I, I, I, I, I, P, P, I, I, RP, P, P]),
         "mikv_set_attention_events": (I, [P, P]),
         "mikv_wait_status": (I, [ctypes.POINTER(ctypes.c_uint), I]),
         "mikv_wait_probe": (I, [ctypes.c_int64, I, P]),
@@ -227,6 +257,166 @@ def mikv_channel_quantize(k, bits, codes, meta, stream=None):
         _ptr(k), units, n, D, bits, _ptr(codes), _ptr(meta), _stream(stream)))
 
 
+# --- the paged cache and windowed attention --------------------------------------------
+
+_PAGE_DTYPE = {MIKV_PAGES_FP16: torch.float16, MIKV_PAGES_BF16: torch.bfloat16, MIKV_PAGES_INT8: torch.float16}
+
+
+class _on:
+    """Runs a call on the device its tensors are on: the stream is that device's current one
+    unless given, and the device is made current for the launch."""
+
+    def __init__(self, device, stream):
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _need(t, name, dtype, shape, device):
+    """Pointer of a contiguous tensor of this dtype, shape (None: any size) and device; None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != device or not t.is_contiguous() or t.dim() != len(shape) or any(
+            n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows(t, name, dtype, shape, device):
+    """mikv_rows of a [B][H][T][D] tensor whose last dimension is contiguous."""
+    if t.dtype != dtype or t.device != device or t.dim() != 4 or any(
+            n is not None and n != m for n, m in zip(shape, t.shape)) or (t.shape[3] > 1 and t.stride(3) != 1):
+        raise ValueError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)} on {device} with a contiguous "
+                         f"last dimension, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    # a dimension of one element is never stepped along: its stride may be anything
+    sb, sh, st = (t.stride(i) if t.shape[i] > 1 else 0 for i in range(3))
+    return ctypes.byref(mikv_rows(t.data_ptr(), sb, sh, st))
+
+
+def _ws_on(nbytes, device, ws):
+    if ws is None:
+        return (torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None), nbytes
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous tensor on {device}, got one on {ws.device}")
+    return ws, ws.numel() * ws.element_size()
+
+
+def mikv_page_reserve(pages, seqs, add, start, ws=None, stream=None):
+    """Room for add int32 [n] more tokens behind sequences seqs (int32 [n], None: 0 .. n - 1);
+    start int32 [n] receives each one's first new slot, or -1 where it was refused."""
+    lib, dev, n = load(), pages.device, add.shape[0]
+    with _on(dev, stream) as st:
+        w, nb = _ws_on(lib.mikv_page_workspace_bytes(pages.ref, n), dev, ws)
+        _check("mikv_page_reserve", lib.mikv_page_reserve(
+            pages.ref, _need(seqs, "seqs", torch.int32, (n,), dev), _need(add, "add", torch.int32, (n,), dev), n,
+            _need(start, "start", torch.int32, (n,), dev), None if w is None else w.data_ptr(), nb, st))
+
+
+def mikv_page_fork(pages, parent, child, ok, ws=None, stream=None):
+    """child[i] becomes a copy of parent[i] (int32 [n] each); ok int32 [n] receives 1, or 0 where refused."""
+    lib, dev, n = load(), pages.device, parent.shape[0]
+    with _on(dev, stream) as st:
+        w, nb = _ws_on(lib.mikv_page_workspace_bytes(pages.ref, n), dev, ws)
+        _check("mikv_page_fork", lib.mikv_page_fork(
+            pages.ref, _need(parent, "parent", torch.int32, (n,), dev), _need(child, "child", torch.int32, (n,), dev), n,
+            _need(ok, "ok", torch.int32, (n,), dev), None if w is None else w.data_ptr(), nb, st))
+
+
+def mikv_page_free(pages, seqs, ok, stream=None):
+    """Sequences seqs (int32 [n], None: 0 .. n - 1) give their pages back; ok int32 [n]."""
+    lib, dev, n = load(), pages.device, ok.shape[0]
+    with _on(dev, stream) as st:
+        _check("mikv_page_free", lib.mikv_page_free(
+            pages.ref, _need(seqs, "seqs", torch.int32, (n,), dev), n, _need(ok, "ok", torch.int32, (n,), dev), st))
+
+
+def mikv_page_copy(pages, src, dst, ok, stream=None):
+    """Page dst[i] takes what page src[i] holds, in all layers (int32 [n] each); ok int32 [n]."""
+    lib, dev, n = load(), pages.device, src.shape[0]
+    with _on(dev, stream) as st:
+        _check("mikv_page_copy", lib.mikv_page_copy(
+            pages.ref, _need(src, "src", torch.int32, (n,), dev), _need(dst, "dst", torch.int32, (n,), dev), n,
+            _need(ok, "ok", torch.int32, (n,), dev), st))
+
+
+def mikv_page_compact(pages, seqs, keep_pos, keep_n, ok, ws=None, stream=None):
+    """Sequence seqs[i] keeps keep_n[i] slots per key head: keep_pos int32 [layers][n][Hkv][max_keep],
+    keep_n and ok int32 [n]."""
+    lib, dev, n, s = load(), pages.device, keep_n.shape[0], pages.struct
+    with _on(dev, stream) as st:
+        w, nb = _ws_on(lib.mikv_page_workspace_bytes(pages.ref, n), dev, ws)
+        _check("mikv_page_compact", lib.mikv_page_compact(
+            pages.ref, _need(seqs, "seqs", torch.int32, (n,), dev),
+            _need(keep_pos, "keep_pos", torch.int32, (s.layers, n, s.Hkv, None), dev),
+            _need(keep_n, "keep_n", torch.int32, (n,), dev), n, keep_pos.shape[3],
+            _need(ok, "ok", torch.int32, (n,), dev), None if w is None else w.data_ptr(), nb, st))
+
+
+def mikv_paged_append(pages, layer, k, v, seqs=None, start=None, counts=None, stream=None):
+    """Rows k, v [n][Hkv][T][D] (strided; fp16, bf16 for BF16 pages) into one layer: counts int32 [n]
+    tokens each (None: T), from slot start int32 [n] (None: each sequence's last slots)."""
+    lib, dev, s = load(), pages.device, pages.struct
+    n, _, T, _ = k.shape
+    shape, dt = (n, s.Hkv, T, s.D), _PAGE_DTYPE[s.type]
+    with _on(dev, stream) as st:
+        _check("mikv_paged_append", lib.mikv_paged_append(
+            pages.ref, layer, _rows(k, "k", dt, shape, dev), _rows(v, "v", dt, shape, dev), n, T,
+            _need(seqs, "seqs", torch.int32, (n,), dev), _need(start, "start", torch.int32, (n,), dev),
+            _need(counts, "counts", torch.int32, (n,), dev), st))
+
+
+def mikv_paged_gather(pages, layer, k_out, v_out, seqs=None, stream=None):
+    """The first T slots of each sequence of one layer as rows k_out, v_out [n][Hkv][T][D] (strided)."""
+    lib, dev, s = load(), pages.device, pages.struct
+    n, _, T, _ = k_out.shape
+    shape, dt = (n, s.Hkv, T, s.D), _PAGE_DTYPE[s.type]
+    with _on(dev, stream) as st:
+        _check("mikv_paged_gather", lib.mikv_paged_gather(
+            pages.ref, layer, _need(seqs, "seqs", torch.int32, (n,), dev), n, T,
+            _rows(k_out, "k_out", dt, shape, dev), _rows(v_out, "v_out", dt, shape, dev), st))
+
+
+def mikv_paged_attention(q, pages, layer, window, sinks, out, lse=None, seqs=None, ws=None, stream=None):
+    """One new token per sequence: q, out [n][Hq][D] fp16 (bf16 for BF16 pages), lse fp32 [n][Hq]."""
+    lib, dev, s = load(), pages.device, pages.struct
+    n, Hq, _ = q.shape
+    shape, dt = (n, Hq, s.D), _PAGE_DTYPE[s.type]
+    with _on(dev, stream) as st:
+        w, nb = _ws_on(lib.mikv_paged_attention_workspace_bytes(pages.ref, n, Hq, window, sinks) if ws is None else 0,
+                       dev, ws)
+        _check("mikv_paged_attention", lib.mikv_paged_attention(
+            _need(q, "q", dt, shape, dev), pages.ref, layer, _need(seqs, "seqs", torch.int32, (n,), dev), n, Hq, window,
+            sinks, _need(out, "out", dt, shape, dev), _need(lse, "lse", torch.float32, (n, Hq), dev),
+            None if w is None else w.data_ptr(), nb, st))
+
+
+def mikv_window_attention(q, k, v, window, sinks, out, lse=None, q_lens=None, k_lens=None, stream=None):
+    """A prompt's or a chunk's attention: q, out [B][Hq][Tq][D], k, v [B][Hkv][Tk][D] (strided; all fp16 or
+    all bf16), lse fp32 [B][Hq][Tq], q_lens, k_lens int32 [B] (None: Tq, Tk)."""
+    lib, dev, dt = load(), q.device, q.dtype
+    B, Hq, Tq, D = q.shape
+    Hkv, Tk = k.shape[1], k.shape[2]
+    if not q.is_cuda or dt not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"q: expected fp16 or bf16 on a CUDA device, got {dt} on {dev}")
+    with _on(dev, stream) as st:
+        _check("mikv_window_attention", lib.mikv_window_attention(
+            _rows(q, "q", dt, (B, Hq, Tq, D), dev), _rows(k, "k", dt, (B, Hkv, Tk, D), dev),
+            _rows(v, "v", dt, (B, Hkv, Tk, D), dev), B, Hq, Hkv, Tq, Tk, D,
+            MIKV_PAGES_BF16 if dt == torch.bfloat16 else MIKV_PAGES_FP16, _need(q_lens, "q_lens", torch.int32, (B,), dev),
+            _need(k_lens, "k_lens", torch.int32, (B,), dev), window, sinks, _rows(out, "out", dt, (B, Hq, Tq, D), dev),
+            _need(lse, "lse", torch.float32, (B, Hq, Tq), dev), st))
+
+
 def mikv_set_attention_events(begin=None, end=None):
     """Record two torch.cuda.Event objects around the split-K attention launch of every
     following decode call of this thread (None, None clears).  Each event must have been
@@ -237,7 +427,8 @@ def mikv_set_attention_events(begin=None, end=None):
 
 
 WAIT_BITS = {1: "K3 pass 1 (row log-sum-exp)", 2: "K3 pass 2 (column sums)", 4: "K6 (V.W_O norms)",
-             8: "K9 (output perturbation)", 16: "mikv_wait_probe"}
+             8: "K9 (output perturbation)", 16: "mikv_wait_probe", 32: "mikv_window_attention",
+             64: "a page outside the pool"}
 
 
 def mikv_wait_status(clear=True) -> int:

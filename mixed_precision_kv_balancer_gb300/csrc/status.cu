@@ -3,6 +3,7 @@
 #include <stdio.h>
 
 #include "common.cuh"
+#include "paged.cuh"
 #include "tcgen05.cuh"
 
 namespace mikv {
@@ -63,6 +64,9 @@ extern "C" int mikv_wait_status(unsigned* bits, int clear) {
   if (int e = mikv::scores_wait_giveups(&v, clear != 0)) return e;
   if (int e = mikv::select_wait_giveups(&v, clear != 0)) return e;
   if (int e = mikv::perturb_wait_giveups(&v, clear != 0)) return e;
+  if (int e = mikv::window_attention_status(&v, clear != 0)) return e;
+  if (int e = mikv::paged_attention_status(&v, clear != 0)) return e;
+  if (int e = mikv::paged_rows_status(&v, clear != 0)) return e;
   if (int e = mikv::tc::wait_giveups(&v, clear != 0)) return e;  // the probe's word
   *bits = v;
   return MIKV_OK;

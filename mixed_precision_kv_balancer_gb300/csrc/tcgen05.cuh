@@ -86,6 +86,8 @@ constexpr unsigned kGiveupColSum = 2u;   // K3 pass 2, col_sum_tc_kernel
 constexpr unsigned kGiveupVwo = 4u;      // K6, vwo_norm_tc_kernel
 constexpr unsigned kGiveupPerturb = 8u;  // K9, perturb_tc_kernel
 constexpr unsigned kGiveupProbe = 16u;   // wait_probe_kernel (mikv_wait_probe)
+constexpr unsigned kGiveupWindow = 32u;  // window_attention_kernel
+constexpr unsigned kBadPage = 64u;       // no wait: a paged kernel met a table entry outside the pool
 
 // The wait-status word of the translation unit that includes this header (internal
 // linkage: one word per source file, each read by that file's wait_giveups()).

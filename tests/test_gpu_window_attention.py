@@ -1,0 +1,155 @@
+"""Prompt attention under a sliding window with sinks, against the oracle in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.paged as op
+import paged_helpers as ph
+from mixed_precision_kv_balancer_gb300 import _lib
+
+pytestmark = pytest.mark.gpu
+
+
+def _make(B, H, T, dtype, layout, seed):
+    if layout == "bthd":
+        return ph.normal((B, T, H, 128), seed, dtype).to(ph.DEV).transpose(1, 2)
+    if layout == "padded":
+        return ph.normal((B, H + 1, T + 5, 136), seed, dtype).to(ph.DEV)[:, 1:, 2:T + 2, :128]
+    if layout == "packed":            # q, k and v side by side, as one projection writes them
+        return ph.normal((B, T, 3, H, 128), seed, dtype).to(ph.DEV)[:, :, 1].transpose(1, 2)
+    return ph.normal((B, H, T, 128), seed, dtype).to(ph.DEV)
+
+
+def _run(q, k, v, window, sinks, ql=None, kl=None):
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device=ph.DEV)
+    lse = torch.full(q.shape[:3], 7.0, device=ph.DEV)
+    _lib.mikv_window_attention(q, k, v, window, sinks, out, lse, q_lens=None if ql is None else ph.ints(ql),
+                               k_lens=None if kl is None else ph.ints(kl))
+    return out, lse
+
+
+def _check(q, k, v, window, sinks, ql=None, kl=None):
+    out, lse = _run(q, k, v, window, sinks, ql, kl)
+    want, wl, mag = op.window_attention(ph.f64(q), ph.f64(k), ph.f64(v), window, sinks, ql, kl)
+    name = "bf16" if q.dtype == torch.bfloat16 else "fp16"
+    ph.close(out, want, mag, ph.HALF_STEP[name], weights=ph.HALF_STEP[name])    # weights rounded once
+    ph.close_lse(lse, wl)
+    left = np.isnan(wl)
+    assert (ph.f64(out)[left] == 7).all() and (ph.f64(lse)[left] == 7).all()    # rows past q_lens
+    assert _lib.mikv_wait_status() == 0
+    return out, lse
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("B,Hkv,rep,Tq,Tk,layout", [
+    (1, 1, 1, 1, 1, "bhtd"), (2, 1, 2, 1, 300, "bthd"), (1, 2, 4, 64, 64, "bhtd"), (3, 2, 1, 127, 127, "padded"),
+    (1, 1, 8, 128, 128, "bthd"), (1, 2, 5, 129, 129, "packed"), (2, 1, 3, 257, 400, "bhtd"), (1, 1, 2, 511, 640, "padded"),
+    (1, 1, 16, 300, 1200, "bthd"), (1, 4, 1, 1025, 1025, "bhtd"), (1, 1, 1, 17, 5, "bhtd"), (1, 1, 1, 600, 130, "bhtd")])
+def test_causal(dtype, B, Hkv, rep, Tq, Tk, layout):
+    q = _make(B, Hkv * rep, Tq, dtype, layout, 1)
+    _check(q, _make(B, Hkv, Tk, dtype, layout, 2), _make(B, Hkv, Tk, dtype, layout, 3), 0, 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("Tq,Tk", [(700, 700), (300, 1500), (1, 1000), (130, 129)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (17, 0), (64, 4), (128, 130), (200, 1), (513, 300), (5000, 9), (0, 5)])
+def test_window_and_sinks(dtype, Tq, Tk, window, sinks):
+    q, k, v = _make(1, 4, Tq, dtype, "bhtd", 1), _make(1, 2, Tk, dtype, "bhtd", 2), _make(1, 2, Tk, dtype, "bhtd", 3)
+    _check(q, k, v, window, sinks)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 3)])
+def test_padded_batches(dtype, window, sinks):
+    """Lengths from none to all, more queries than keys; NaN behind every row's end."""
+    ql, kl = [300, 0, 1, 130, 299, 5, 200, 0, 400, -3], [300, 0, 500, 131, 1, 0, 500, 20, 900, 7]
+    q, k, v = (_make(10, H, T, dtype, "bhtd", s) for H, T, s in ((2, 300, 1), (1, 500, 2), (1, 500, 3)))
+    for b in range(10):
+        q[b, :, max(0, ql[b]):] = float("nan")
+        k[b, :, kl[b]:] = float("nan")
+        v[b, :, kl[b]:] = float("inf")
+    _check(q, k, v, window, sinks, ql, kl)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("drop", [9.0, 10.5, 14.0])
+def test_many_small_weights_beside_a_large_one(dtype, drop):
+    q = torch.full((1, 1, 40, 128), 0.25, dtype=dtype, device=ph.DEV)
+    k = torch.zeros(1, 1, 3000, 128, dtype=dtype, device=ph.DEV)
+    k[0, 0, 1234] = drop / (0.25 * 128 ** 0.5)
+    _check(q, k, _make(1, 1, 3000, dtype, "bhtd", 3), 0, 0)
+
+
+def test_scores_that_grow_and_fall_along_the_keys():
+    """The running maximum moves in every tile, by a little and by a lot."""
+    for dtype in (torch.float16, torch.bfloat16):
+        T = 1000
+        q, k, v = (_make(1, 1, T, dtype, "bhtd", s) for s in (1, 2, 3))
+        q[..., 0] = 8.0
+        for sign in (1.0, -1.0):
+            k[..., 0] = (sign * torch.linspace(-8, 8, T, device=ph.DEV)).to(dtype)
+            _check(q, k, v, 0, 0)
+
+
+def test_the_same_bits_every_time_and_in_a_graph():
+    q, k, v = _make(2, 8, 700, torch.bfloat16, "bthd", 1), _make(2, 2, 900, torch.bfloat16, "bthd", 2), _make(2, 2, 900, torch.bfloat16, "bthd", 3)
+    kl = ph.ints([900, 700])
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:3], device=ph.DEV)
+    call = lambda: _lib.mikv_window_attention(q, k, v, 100, 4, out, lse, k_lens=kl)
+    call()
+    want = out.clone(), lse.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(3):
+        out.zero_()
+        lse.zero_()
+        graph.replay()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    kl.copy_(ph.ints([300, 900]))              # lengths are read when the graph runs
+    graph.replay()
+    again = out.clone()
+    out.zero_()
+    call()
+    assert torch.equal(out, again) and not torch.equal(out, want[0])
+
+
+def test_lse_may_be_left_out_and_rows_broadcast():
+    q, k, v = (_make(2, 2, 90, torch.float16, "bhtd", s) for s in (1, 2, 3))
+    k, v = k[:1].expand(2, 2, 90, 128), v[:, :1].expand(2, 2, 90, 128)
+    out = torch.empty_like(q)
+    _lib.mikv_window_attention(q, k, v, 0, 0, out)
+    want, _, mag = op.window_attention(ph.f64(q), ph.f64(k), ph.f64(v), 0, 0)
+    ph.close(out, want, mag, 2.0 ** -11, 2.0 ** -11)
+
+
+def test_the_binding_refuses():
+    q, k = _make(1, 4, 8, torch.float16, "bhtd", 1), _make(1, 2, 8, torch.float16, "bhtd", 2)
+    out = torch.empty_like(q)
+    wa = _lib.mikv_window_attention
+    with pytest.raises(ValueError, match="q:"):
+        wa(q.float(), k, k, 0, 0, out)
+    with pytest.raises(ValueError, match="k:"):
+        wa(q, k.bfloat16(), k, 0, 0, out)
+    with pytest.raises(ValueError, match="v:"):
+        wa(q, k, k[:, :, :7], 0, 0, out)
+    with pytest.raises(ValueError, match="out:"):
+        wa(q, k, k, 0, 0, out[:, :2])
+    with pytest.raises(ValueError, match="lse"):
+        wa(q, k, k, 0, 0, out, torch.empty(1, 4, 9, device=ph.DEV))
+    with pytest.raises(ValueError, match="k_lens"):
+        wa(q, k, k, 0, 0, out, k_lens=torch.tensor([3], dtype=torch.int32))
+    for kw in (dict(window=-1, sinks=0), dict(window=0, sinks=-2)):
+        with pytest.raises(_lib.MikvError) as e:
+            wa(q, k, k, kw["window"], kw["sinks"], out)
+        assert e.value.code == -1
+    with pytest.raises(_lib.MikvError) as e:
+        wa(q[..., :64].contiguous(), k[..., :64].contiguous(), k[..., :64].contiguous(), 0, 0, out[..., :64].contiguous())
+    assert e.value.code == -4
+    with pytest.raises(_lib.MikvError) as e:      # three query heads over two key heads
+        wa(q[:, :3], k, k, 0, 0, out[:, :3])
+    assert e.value.code == -2
+    odd = ph.normal((1, 2, 8, 129), 1, torch.float16).to(ph.DEV)[..., :128]
+    with pytest.raises(_lib.MikvError) as e:
+        wa(q, odd, k, 0, 0, out)
+    assert e.value.code == -3
