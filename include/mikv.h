@@ -516,9 +516,12 @@ size_t mikv_paged_attention_workspace_bytes(const mikv_pages* p, int n, int Hq, 
  * k_lens[b] key rows of batch row b count.  Query i stands at position
  * p = k_lens[b] - q_lens[b] + i, the last one at the last key, and sees key j as in
  * mikv_paged_attention.  A query that sees nothing (p < 0) gives out 0 and lse -inf.
- * lse fp32 [B][Hq][Tq], or NULL.  Query rows at or past q_lens[b] are neither read nor written;
- * key and value rows at or past k_lens[b] may hold anything.
- * Requires Tq, Tk >= 1, Hq a multiple of Hkv; B == 0 does nothing.
+ * lse fp32 [B][Hq][Tq], or NULL.  Query rows at or past q_lens[b] are not written and may hold
+ * anything, like key and value rows that no query of the call sees (those at or past k_lens[b],
+ * and those between the sinks and the first query's window); a value row that some query sees
+ * must be finite, or it may reach the other queries of the same head.
+ * Requires 1 <= Tq, Tk <= 2^30, Hq a multiple of Hkv; k and v may repeat one head or batch row
+ * (stride 0), rows of q, k, v along T and all rows of out are apart; B == 0 does nothing.
  * The softmax weights are rounded to the inputs' type before they meet the values; sums and
  * statistics are fp32.
  * Errors: EINVAL (null, type, window, sinks), ESHAPE, EALIGN, EUNSUPPORTED (D), ECUDA.

@@ -1,8 +1,29 @@
-// Attention of a prompt, or of a chunk of one, under a sliding window with sinks.
+// Attention of a prompt, or of a chunk of one, under a sliding window with sinks (tcgen05).
 //
-// Mathematics: one pass over the visible keys with a running maximum and sum per query row,
-// out = sum_j exp(l_j - m) v_j / sum_j exp(l_j - m).  A CTA holds 64 query rows of one head;
-// tiles of 64 keys that none of its rows sees are not read.
+// Mathematics: one pass over the visible keys, out = sum_j p_j v_j / sum_j p_j with
+// p_j = exp2(l_j - m) and a reference m per query row that follows the running maximum: it is
+// moved, and the accumulated sums rescaled, only where the maximum has outgrown it by 2^kGrow,
+// so almost every tile leaves the accumulators alone.  Bound by the tensor cores (4 * 128 flop
+// per visible query-key pair) and, close behind, by the exponentials.
+//
+// A CTA holds two tiles of 128 query rows over one key head: the same rows of two heads of the
+// group, or 256 rows of one head where the group is odd.  Key and value tiles of 128 rows come
+// through a ring of five 32 KB buffers (TMA, 128-byte swizzle); tiles that none of the rows sees
+// are not read.  Per key tile i and query tile t
+//   S_t = Q_t K_i^T     tcgen05, both operands in shared memory, 128 fp32 TMEM columns
+//   P_t = exp2(...)     four warps, one query row a thread, written over S_t as 16-bit pairs
+//   O_t += P_t V_i      tcgen05, P from TMEM, V as it lies (rows are the contraction)
+// The tensor core runs [O_0 += P_0 V_i, S_0 = Q_0 K_i+1] while the warps of tile 1 make their
+// weights, and the other way round.  S_t(i + 1) is committed behind O_t(i), so a thread that
+// holds new scores may rescale its accumulator row without another wait.
+//
+// Weights are rounded to the inputs' type once (2^-9 or 2^-12 of each on average); their sum is
+// taken before that, in fp32.  fp16 weights carry a factor 2^kShift, which keeps weights down
+// to 2^-27 of the row's largest out of fp16's subnormal range; 2^(kShift + kGrow) stays below
+// its largest number.
+//
+// Value rows that no query of the call sees may hold anything (0 * NaN is NaN): the TMA warp
+// clears them in shared memory, in the at most three tiles that hold such rows beside others.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -16,32 +37,99 @@ int window_attention_status(unsigned* out, bool clear) { return tc::wait_giveups
 
 namespace {
 
-constexpr int kWaThreads = 128, kWaQ = 64, kWaK = 64;
-constexpr int kWaTile = kWaK * kD * 2;
+constexpr int kWaRows = 128;                     // query rows and key rows of a tile
+constexpr int kWaRing = 5;
+constexpr int kMaxRows = 1 << 30;                // of q or k: positions and their differences fit 32 bits
+constexpr int kWaThreads = 320;                  // 2 x 4 softmax warps, the TMA warp, the MMA warp
+constexpr int kWaTmaWarp = 8, kWaMmaWarp = 9;
+constexpr int kWaSmem = (2 + kWaRing) * tc::kTileBytes + 1024;
+constexpr uint32_t kWaCols = 512;                // S_0, S_1, O_0, O_1: 128 columns each
+constexpr uint32_t kWaO = 256;
+
+template <bool BF>
+struct Weights {
+  static constexpr float shift = BF ? 0.f : 13.f;  // log2 of the weights' factor
+  static constexpr float grow = BF ? 8.f : 2.f;    // log2 of the growth that moves the reference
+};
 
 struct WindowArgs {
-  RowView q, k, v, out;
+  RowView out;
   float* lse;
   const int32_t *q_lens, *k_lens;
-  int B, Hq, Hkv, Tq, Tk, window, sinks;
-  float scale;
+  int Hq, rep, Tq, Tk, window, sinks, blocks;
+  bool pair_heads;               // the CTA's tiles are two heads' rows, else 256 rows of one head
+  int qb, qh, kb, kh, vb, vh;    // 1, or 0 where the view repeats one batch row or head
+  float scale;                   // log2(e) / sqrt(D)
 };
+
+struct WaBars {
+  uint64_t full[kWaRing], empty[kWaRing];   // buffer landed; the products that read it are done
+  uint64_t fix[kWaRing];                    // a value tile's hidden rows are cleared
+  uint64_t q, s[2], p[2], o[2];             // queries landed; scores, weights, last sums written
+};
+
+// What one CTA works on; every warp computes it alike.
+struct Work {
+  int ql, kl, off;        // lengths; position of query 0
+  int head[2], q0[2];     // per tile: head and first row
+  int pa[2], pb[2];       // positions of its first and last row
+  int tiles, ts, tw0;     // key tiles: ts of the sinks, then tw0, tw0 + 1, ...
+  int last[2];            // index of the last key tile that query tile t sees, -1 for none
+  int nt;                 // query tiles
+  __device__ __forceinline__ int j0(int i) const { return (i < ts ? i : tw0 + i - ts) * kWaRows; }
+};
+__device__ __forceinline__ Work work_of(const WindowArgs& a, int b, int hk, int x) {
+  Work w;
+  w.ql = a.q_lens ? min(max(a.q_lens[b], 0), a.Tq) : a.Tq;
+  w.kl = a.k_lens ? min(max(a.k_lens[b], 0), a.Tk) : a.Tk;
+  w.off = w.kl - w.ql;
+  const int per = a.pair_heads ? a.rep / 2 : a.rep;       // CTAs of one row block
+  const int blk = a.blocks - 1 - x / per, u = x % per;    // the last rows, which see the most, first
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    w.head[t] = hk * a.rep + (a.pair_heads ? 2 * u + t : u);
+    w.q0[t] = a.pair_heads ? blk * kWaRows : (2 * blk + t) * kWaRows;
+    w.pa[t] = w.off + w.q0[t];
+    w.pb[t] = w.off + min(w.q0[t] + kWaRows, w.ql) - 1;
+  }
+  w.nt = w.q0[0] >= w.ql ? 0 : w.q0[1] >= w.ql ? 1 : 2;
+  const int p1 = w.nt == 2 ? w.pb[1] : w.pb[0];           // the largest position (tile 1's rows are not below tile 0's)
+  const int lo = a.window > 0 ? max(w.pa[0] - a.window + 1, 0) : 0;
+  const int end = p1 < 0 ? 0 : p1 / kWaRows + 1;
+  w.tw0 = min(lo / kWaRows, end);
+  w.ts = a.window > 0 ? min((min(a.sinks, w.kl) + kWaRows - 1) / kWaRows, w.tw0) : 0;
+  w.tiles = w.ts + end - w.tw0;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int e = w.pb[t] < 0 ? -1 : w.pb[t] / kWaRows;
+    w.last[t] = t >= w.nt || e < 0 ? -1 : e < w.ts ? e : e - w.tw0 + w.ts;
+  }
+  return w;
+}
+// Whether any row of query tile t sees a key of the tile at j0, and whether all rows see all of it.
+__device__ __forceinline__ bool tile_seen(const WindowArgs& a, const Work& w, int t, int j0) {
+  return t < w.nt && j0 <= w.pb[t] && (a.window == 0 || j0 + kWaRows - 1 > w.pa[t] - a.window || j0 < a.sinks);
+}
+__device__ __forceinline__ bool tile_whole(const WindowArgs& a, const Work& w, int t, int j0) {
+  return j0 + kWaRows - 1 <= w.pa[t] && (a.window == 0 || j0 > w.pb[t] - a.window || j0 + kWaRows <= a.sinks);
+}
+// Rows [z0, z1) and [z2, 128) of the value tile at j0 that no query of the call sees.
+struct Hidden {
+  int z0, z1, z2;
+  __device__ __forceinline__ bool any() const { return z0 < z1 || z2 < kWaRows; }
+};
+__device__ __forceinline__ Hidden hidden_rows(const WindowArgs& a, const Work& w, int j0) {
+  Hidden h;
+  h.z0 = min(max(a.sinks - j0, 0), kWaRows);
+  h.z1 = a.window > 0 ? min(max(w.off - a.window + 1 - j0, 0), kWaRows) : 0;
+  h.z2 = min(max(w.kl - j0, 0), kWaRows);
+  return h;
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
-}
-template <bool BF>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if (BF)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};\n"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    mma16816(d, a[0], a[1], a[2], a[3], b0, b1);
 }
 template <bool BF>
 __device__ __forceinline__ uint32_t pack2(float x0, float x1) {
@@ -53,122 +141,313 @@ __device__ __forceinline__ uint32_t pack2(float x0, float x1) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// 32 fp32 columns of this thread's TMEM lane, without the wait.
+__device__ __forceinline__ void ld32(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// One thread: rows [row0, row0 + 128) of one (head, batch row) into the tile at `s`, two boxes of
+// 64 channels; rows past the end are zero-filled.  Completes 32 KB on the mbarrier.
+__device__ __forceinline__ void tma_rows(uint32_t s, const CUtensorMap* map, int row0, int h, int b, uint32_t mbar) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(s + j * tc::kKBlock),
+        "l"(map), "r"(j * 64), "r"(row0), "r"(h), "r"(b), "r"(mbar)
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] . B for one step of 16 along the contraction; B lies with its rows along it.
+__device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u));
+}
+// Descriptor of a value tile as the B operand [128 keys][128 channels], channels contiguous: the
+// two 64-channel blocks lie kKBlock apart (leading offset), groups of 8 keys 1024 B apart.
+__device__ __forceinline__ uint64_t value_desc(uint32_t saddr) {
+  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(tc::kKBlock >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// One thread's row of one query tile.
+struct Row {
+  float m = -INFINITY, l = 0.f;   // reference (raw scores) and sum of weights
+  bool first = true;              // no tile has been accumulated
+};
+
+// One tile of scores: 128 columns of this thread's lane at `ts` become weights; the accumulator
+// at `to` is rescaled where some row of the warp needs it.
 template <bool BF>
-__global__ void __launch_bounds__(kWaThreads) window_attention_kernel(const WindowArgs a) {
-  constexpr float kShift = BF ? 0.f : 15.f;  // fp16 weights carry 2^15: no subnormals down to 2^-29 of the largest
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int b = blockIdx.z, h = blockIdx.y, q0 = blockIdx.x * kWaQ, tid = threadIdx.x;
-  const int w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int ql = a.q_lens ? min(max(a.q_lens[b], 0), a.Tq) : a.Tq, kl = a.k_lens ? min(max(a.k_lens[b], 0), a.Tk) : a.Tk;
-  if (q0 >= ql) return;
-  const int hk = h / (a.Hq / a.Hkv), p0 = kl - ql + q0, p1 = min(p0 + kWaQ - 1, kl - 1);  // positions of the rows
-  // key tiles: the sinks', then from the first row's window to the last row
-  const int lo = a.window > 0 ? max(p0 - a.window + 1, 0) : 0;
-  const int tw0 = lo / kWaK, tw1 = p1 < 0 ? 0 : p1 / kWaK + 1;
-  const int ts = a.window > 0 ? min((min(a.sinks, kl) + kWaK - 1) / kWaK, min(tw0, tw1)) : 0;
-  const int tiles = ts + max(tw1 - tw0, 0);
-  const uint32_t s0 = smem_u32(smem);
-  const auto load = [&](int i) {
-    const int j0 = (i < ts ? i : tw0 + i - ts) * kWaK;
-    const uint32_t st = s0 + (i & 1) * 2 * kWaTile;
+__device__ __forceinline__ void softmax_tile(const WindowArgs& a, uint32_t ts, uint32_t to, bool whole, int p, int j0, Row& r) {
+  float s[kWaRows];
 #pragma unroll
-    for (int u = 0; u < kWaK * 16 / kWaThreads; ++u) {
-      const int c = tid + u * kWaThreads, r = c >> 4, p = c & 15;
-      const bool ok = j0 + r < kl;
-      const uint32_t off = r * (kD * 2) + ((p ^ (r & 7)) << 4);
-      cp_async16(st + off, ok ? a.k.row(b, hk, j0 + r) + p * 16 : a.k.p, ok);
-      cp_async16(st + kWaTile + off, ok ? a.v.row(b, hk, j0 + r) + p * 16 : a.v.p, ok);
-    }
-  };
-  uint32_t qf[kD / 16][4];
-  const int r0 = q0 + w * 16 + g;
+  for (int c = 0; c < 4; ++c) ld32(ts + c * 32, s + c * 32);
+  wait_ld();
+  if (!whole) {
+    const int hi = p - j0, lo = a.window > 0 ? hi - a.window + 1 : 0, sk = a.sinks - j0;
 #pragma unroll
-  for (int ks = 0; ks < kD / 16; ++ks)
+    for (int c = 0; c < kWaRows; ++c)
+      if (c > hi || (c < lo && c >= sk)) s[c] = -INFINITY;
+  }
+  float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = r0 + 8 * (j & 1);
-      qf[ks][j] = row < ql ? *reinterpret_cast<const uint32_t*>(a.q.row(b, h, row) + (16 * ks + 8 * (j >> 1) + 2 * t) * 2) : 0u;
-    }
-  float o[kD / 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  if (tiles > 0) load(0);
-  cp_async_commit();
-  for (int i = 0; i < tiles; ++i) {
-    if (i + 1 < tiles) load(i + 1);
-    cp_async_commit();
-    cp_async_wait<1>();
-    __syncthreads();
-    const uint32_t st = s0 + (i & 1) * 2 * kWaTile;
-    const int j0 = (i < ts ? i : tw0 + i - ts) * kWaK;
-    float s[kWaK / 8][4];
+  for (int c = 4; c < kWaRows; c += 8)
 #pragma unroll
-    for (int nt = 0; nt < kWaK / 8; ++nt) {
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int u = 0; u < 4; ++u) mx[u] = fmaxf(fmaxf(mx[u], s[c + u]), c + 4 + u < kWaRows ? s[c + 4 + u] : -INFINITY);
+  const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+  const bool grew = (top - r.m) * a.scale > Weights<BF>::grow;   // from -inf too; never by NaN
+  if (__any_sync(0xffffffffu, grew)) {
+    const float m = fmaxf(r.m, top);
+    const float alpha = m == -INFINITY ? 1.f : ex2((r.m - m) * a.scale);
+    r.m = m;
+    r.l *= alpha;
+    if (!r.first) {
+#pragma unroll 1
+      for (int c = 0; c < kD; c += 32) {
+        float o[32];
+        uint32_t u[32];
+        ld32(to + c, o);
+        wait_ld();
 #pragma unroll
-      for (int k2 = 0; k2 < kD / 32; ++k2) {
-        const int r = nt * 8 + (lane & 7), c = k2 * 4 + (lane >> 3);
-        uint32_t b0, b1, b2, b3;
-        ldsm_x4(st + r * (kD * 2) + ((c ^ (r & 7)) << 4), b0, b1, b2, b3);
-        mma<BF>(d, qf[2 * k2], b0, b1);
-        mma<BF>(d, qf[2 * k2 + 1], b2, b3);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int p = kl - ql + r0 + 8 * (j >> 1), key = j0 + nt * 8 + 2 * t + (j & 1);
-        const bool see = key <= p && (a.window == 0 || key > p - a.window || key < a.sinks);
-        s[nt][j] = see ? d[j] * a.scale : -INFINITY;
+        for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * alpha);
+        st16(to + c, u);
+        st16(to + c + 16, u + 16);
       }
     }
+  }
+  r.first = false;
+  const float neg = r.m == -INFINITY ? 0.f : Weights<BF>::shift - r.m * a.scale;
+  float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float mx = m[r];
+  for (int c = 0; c < kWaRows; c += 32) {
+    uint32_t u[16];
 #pragma unroll
-      for (int nt = 0; nt < kWaK / 8; ++nt) mx = fmaxf(mx, fmaxf(s[nt][2 * r], s[nt][2 * r + 1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float sub = mx == -INFINITY ? 0.f : mx - kShift, alpha = mx == -INFINITY ? 0.f : ex2(m[r] - mx);
-      m[r] = mx;
-      l[r] *= alpha;
-#pragma unroll
-      for (int c = 0; c < kD / 8; ++c) {
-        o[c][2 * r] *= alpha;
-        o[c][2 * r + 1] *= alpha;
+    for (int i = 0; i < 16; ++i) {
+      const float2 x = __ffma2_rn(make_float2(s[c + 2 * i], s[c + 2 * i + 1]), make_float2(a.scale, a.scale), make_float2(neg, neg));
+      const float2 e = make_float2(ex2(x.x), ex2(x.y));
+      sum[i & 1] = __fadd2_rn(sum[i & 1], e);
+      u[i] = pack2<BF>(e.x, e.y);
+    }
+    st16(ts + c / 2, u);
+  }
+  r.l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+  wait_st();
+}
+
+// CTA (pair of query tiles, key head, batch row).
+template <bool BF>
+__global__ void __launch_bounds__(kWaThreads, 1)
+    window_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                            const __grid_constant__ CUtensorMap vmap, const WindowArgs a) {
+  extern __shared__ uint8_t smem[];
+  __shared__ WaBars bar;
+  __shared__ uint32_t tslot;
+  const int b = blockIdx.z, hk = blockIdx.y;
+  const Work w = work_of(a, b, hk, blockIdx.x);
+  if (w.nt == 0) return;   // uniform over the CTA: no query row
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kWaRing; ++i) {
+      tc::mbar_init(smem_u32(&bar.full[i]), 1);
+      tc::mbar_init(smem_u32(&bar.empty[i]), 1);
+      tc::mbar_init(smem_u32(&bar.fix[i]), 1);
+    }
+    tc::mbar_init(smem_u32(&bar.q), 1);
+    for (int t = 0; t < 2; ++t) {
+      tc::mbar_init(smem_u32(&bar.s[t]), 1);
+      tc::mbar_init(smem_u32(&bar.p[t]), 4);
+      tc::mbar_init(smem_u32(&bar.o[t]), 1);
+    }
+    tc::mbar_init_fence();
+  }
+  if (warp == kWaMmaWarp) tc::tmem_alloc(smem_u32(&tslot), kWaCols);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = tslot;
+  const uint32_t sq = tc::smem_base(smem), ring = sq + 2 * tc::kTileBytes;
+  tc::Waits wait;
+
+  if (warp == kWaTmaWarp) {
+    if (lane == 0 && w.tiles > 0) {
+      tc::mbar_expect_tx(smem_u32(&bar.q), w.nt * tc::kTileBytes);
+      for (int t = 0; t < w.nt; ++t)
+        tma_rows(sq + t * tc::kTileBytes, &qmap, w.q0[t], w.head[t] * a.qh, b * a.qb, smem_u32(&bar.q));
+    }
+    // buffer n % kWaRing takes tile n: keys of key tile n / 2 (n even), values (n odd)
+    for (int n = 0; n < 2 * w.tiles; ++n) {
+      const int slot = n % kWaRing, j0 = w.j0(n >> 1);
+      if (n >= kWaRing) wait(smem_u32(&bar.empty[slot]), (n / kWaRing - 1) & 1);
+      const uint32_t dst = ring + slot * tc::kTileBytes, full = smem_u32(&bar.full[slot]);
+      if (lane == 0 && wait.ok) {
+        tc::mbar_expect_tx(full, tc::kTileBytes);
+        if (n & 1)
+          tma_rows(dst, &vmap, j0, hk * a.vh, b * a.vb, full);
+        else
+          tma_rows(dst, &kmap, j0, hk * a.kh, b * a.kb, full);
       }
-#pragma unroll
-      for (int nt = 0; nt < kWaK / 8; ++nt)
-#pragma unroll
-        for (int j = 2 * r; j < 2 * r + 2; ++j) {
-          s[nt][j] = ex2(s[nt][j] - sub);
-          l[r] += s[nt][j];
+      __syncwarp();
+      if (n & 1) {
+        const Hidden h = hidden_rows(a, w, j0);
+        if (h.any()) {
+          wait(full, (n / kWaRing) & 1);
+          for (int c = lane; c < kWaRows * 16; c += 32) {   // 16-byte pieces, both channel blocks
+            const int r = c >> 4, piece = c & 15;
+            if ((r >= h.z0 && r < h.z1) || r >= h.z2)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(dst + (piece >> 3) * tc::kKBlock + r * 128 + (piece & 7) * 16),
+                           "r"(0)
+                           : "memory");
+          }
+          tc::fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(smem_u32(&bar.fix[slot]));
         }
-    }
-#pragma unroll
-    for (int kt = 0; kt < kWaK / 16; ++kt) {
-      const uint32_t pf[4] = {pack2<BF>(s[2 * kt][0], s[2 * kt][1]), pack2<BF>(s[2 * kt][2], s[2 * kt][3]),
-                              pack2<BF>(s[2 * kt + 1][0], s[2 * kt + 1][1]), pack2<BF>(s[2 * kt + 1][2], s[2 * kt + 1][3])};
-#pragma unroll
-      for (int c = 0; c < kD / 8; c += 2) {
-        const int r = kt * 16 + (lane & 15), cc = c + (lane >> 4);
-        uint32_t b0, b1, b2, b3;
-        ldsm_x4_t(st + kWaTile + r * (kD * 2) + ((cc ^ (r & 7)) << 4), b0, b1, b2, b3);
-        mma<BF>(o[c], pf, b0, b1);
-        mma<BF>(o[c + 1], pf, b2, b3);
       }
     }
-    __syncthreads();
-  }
-  cp_async_wait<0>();
+  } else if (warp == kWaMmaWarp) {
+    if (lane == 0 && w.tiles > 0) {
+      constexpr uint32_t kType = BF ? (1u << 7) | (1u << 10) : 0u;
+      constexpr uint32_t kScores = tc::idesc_f16(kWaRows, kWaRows) | kType;
+      constexpr uint32_t kValues = tc::idesc_f16(kWaRows, kD) | kType | (1u << 16);   // B: rows along the contraction
+      int p_seen[2] = {0, 0};
+      uint32_t fixed = 0;   // parity of each buffer's next clearing
+      wait(smem_u32(&bar.q), 0);
+      for (int i = 0; i <= w.tiles; ++i) {
+        // this step's scores from key tile i, behind the last step's sums over value tile i - 1
+        const int kn = 2 * i, vn = 2 * i - 1, ks = kn % kWaRing, vs = i > 0 ? vn % kWaRing : 0;
+        const uint32_t sk = ring + ks * tc::kTileBytes, sv = ring + vs * tc::kTileBytes;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    const int row = r0 + 8 * r;
-    if (row >= ql) continue;
-    const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+        for (int t = 0; t < 2; ++t) {
+          if (i > 0) {
+            if (t == 0) {
+              wait(smem_u32(&bar.full[vs]), (vn / kWaRing) & 1);
+              if (hidden_rows(a, w, w.j0(i - 1)).any()) {
+                wait(smem_u32(&bar.fix[vs]), (fixed >> vs) & 1);
+                fixed ^= 1u << vs;
+              }
+            }
+            if (tile_seen(a, w, t, w.j0(i - 1))) {
+              wait(smem_u32(&bar.p[t]), p_seen[t]++ & 1);
+              tc::fence_after_sync();
+              if (wait.ok) {
 #pragma unroll
-    for (int c = 0; c < kD / 8; ++c)
-      *reinterpret_cast<uint32_t*>(a.out.row(b, h, row) + (c * 8 + 2 * t) * 2) = pack2<BF>(o[c][2 * r] * inv, o[c][2 * r + 1] * inv);
-    if (t == 0 && a.lse) a.lse[(static_cast<int64_t>(b) * a.Hq + h) * a.Tq + row] = (m[r] + (log2f(l[r]) - kShift)) * 0.6931471805599453f;
+                for (int c = 0; c < kWaRows / 16; ++c)
+                  mma_ts(tmem + kWaO + t * 128, tmem + t * 128 + c * 8, value_desc(sv + c * 2048), kValues, p_seen[t] > 1 || c > 0);
+                if (i - 1 == w.last[t]) tc::commit(smem_u32(&bar.o[t]));
+              }
+            }
+          }
+          if (i < w.tiles) {
+            if (t == 0) {
+              wait(smem_u32(&bar.full[ks]), (kn / kWaRing) & 1);
+              tc::fence_after_sync();
+            }
+            if (tile_seen(a, w, t, w.j0(i)) && wait.ok) {
+              tc::mma_tile(tmem + t * 128, sq + t * tc::kTileBytes, sk, kScores);
+              tc::commit(smem_u32(&bar.s[t]));
+            }
+          }
+        }
+        if (i < w.tiles && wait.ok) {   // nobody waits for the last buffers
+          if (i > 0) tc::commit(smem_u32(&bar.empty[vs]));
+          tc::commit(smem_u32(&bar.empty[ks]));
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    const int t = warp >> 2, row = (warp & 3) * 32 + lane;   // the thread's TMEM lane is its row
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + kWaO + t * 128;
+    const int p = w.pa[t] + row;
+    Row r;
+    int seen = 0;
+    for (int i = 0; i < w.tiles; ++i) {
+      const int j0 = w.j0(i);
+      if (!tile_seen(a, w, t, j0)) continue;
+      wait(smem_u32(&bar.s[t]), seen++ & 1);
+      tc::fence_after_sync();
+      softmax_tile<BF>(a, ts, to, tile_whole(a, w, t, j0), p, j0, r);
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(smem_u32(&bar.p[t]));
+    }
+    if (t < w.nt) {
+      if (w.last[t] >= 0) wait(smem_u32(&bar.o[t]), 0);
+      tc::fence_after_sync();
+      const int q = w.q0[t] + row;
+      float inv = r.l == 0.f ? 0.f : 1.f / r.l;
+      if (!wait.ok) inv = __int_as_float(0x7fffffff);
+      uint8_t* dst = a.out.row(b, w.head[t], q);
+#pragma unroll 1
+      for (int c = 0; c < kD; c += 32) {
+        float o[32];
+        if (seen > 0) {
+          ld32(to + c, o);
+          wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        }
+        if (q < w.ql) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(dst + (c + i) * 2) =
+                make_uint4(pack2<BF>(o[i] * inv, o[i + 1] * inv), pack2<BF>(o[i + 2] * inv, o[i + 3] * inv),
+                           pack2<BF>(o[i + 4] * inv, o[i + 5] * inv), pack2<BF>(o[i + 6] * inv, o[i + 7] * inv));
+        }
+      }
+      if (q < w.ql && a.lse) {
+        const float v = r.l == 0.f ? -INFINITY : (r.m * a.scale + (log2f(r.l) - Weights<BF>::shift)) * 0.6931471805599453f;
+        a.lse[(static_cast<int64_t>(b) * a.Hq + w.head[t]) * a.Tq + q] = wait.ok ? v : inv;
+      }
+    }
   }
+  if (!wait.ok) tc::report_giveup(tc::kGiveupWindow);
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kWaMmaWarp) tc::tmem_dealloc(tmem, kWaCols);
+}
+
+// 4-D tensor map (channel, row, head, batch row) of a strided view, box 64 x 128 x 1 x 1 with
+// 128-byte swizzle.  A dimension of stride 0 (a repeated head or batch row) has one entry in
+// the map; *mb and *mh tell whether the coordinate counts.
+int encode_view(CUtensorMap* map, const mikv_rows& r, int T, int H, int B, const char* name, int* mb, int* mh) {
+  const auto enc = tc::tensor_map_encoder();
+  if (!enc) return fail(MIKV_ECUDA, "window_attention: cuTensorMapEncodeTiled unavailable");
+  *mh = H > 1 && r.stride_h != 0;
+  *mb = B > 1 && r.stride_b != 0;
+  const cuuint64_t row = T > 1 ? static_cast<cuuint64_t>(r.stride_t) * 2 : kD * 2;
+  const cuuint64_t dims[4] = {kD, static_cast<cuuint64_t>(T), *mh ? static_cast<cuuint64_t>(H) : 1, *mb ? static_cast<cuuint64_t>(B) : 1};
+  const cuuint64_t strides[3] = {row, *mh ? static_cast<cuuint64_t>(r.stride_h) * 2 : row, *mb ? static_cast<cuuint64_t>(r.stride_b) * 2 : row};
+  const cuuint32_t box[4] = {64, kWaRows, 1, 1}, estr[4] = {1, 1, 1, 1};
+  const CUresult e = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, r.data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (e != CUDA_SUCCESS) return fail(MIKV_ECUDA, "window_attention: tensor map of %s (error %d)", name, static_cast<int>(e));
+  return MIKV_OK;
 }
 
 }  // namespace
@@ -183,18 +462,40 @@ extern "C" int mikv_window_attention(const mikv_rows* q, const mikv_rows* k, con
   if (type != MIKV_PAGES_FP16 && type != MIKV_PAGES_BF16) return fail(MIKV_EINVAL, "window_attention: type=%d", type);
   if (D != kD) return fail(MIKV_EUNSUPPORTED, "window_attention: D=%d (only %d)", D, kD);
   if (window < 0 || sinks < 0) return fail(MIKV_EINVAL, "window_attention: window=%d sinks=%d", window, sinks);
-  if (B < 0 || B > 65535 || Hkv < 1 || Hq < 1 || Hq > 65535 || Hq % Hkv || Tq < 1 || Tk < 1)
+  if (B < 0 || B > 65535 || Hkv < 1 || Hkv > 65535 || Hq < 1 || Hq % Hkv || Tq < 1 || Tk < 1 || Tq > kMaxRows || Tk > kMaxRows)
     return fail(MIKV_ESHAPE, "window_attention: B=%d Hq=%d Hkv=%d Tq=%d Tk=%d", B, Hq, Hkv, Tq, Tk);
   if (B == 0) return MIKV_OK;
   if (int e = check_rows(q, "window_attention", "q")) return e;
   if (int e = check_rows(k, "window_attention", "k")) return e;
   if (int e = check_rows(v, "window_attention", "v")) return e;
   if (int e = check_rows(out, "window_attention", "out")) return e;
-  const WindowArgs a = {row_view(*q), row_view(*k), row_view(*v), row_view(*out), lse, q_lens, k_lens,
-                        B, Hq, Hkv, Tq, Tk, window, sinks, 1.4426950408889634f * 0.08838834764831845f};
+  if ((Tq > 1 && (q->stride_t < kD || out->stride_t < kD)) || (Tk > 1 && (k->stride_t < kD || v->stride_t < kD)) ||
+      (Hq > 1 && out->stride_h < kD) || (B > 1 && out->stride_b < kD))
+    return fail(MIKV_EINVAL, "window_attention: rows overlap");
+  CUtensorMap qm, km, vm;
+  WindowArgs a;
+  a.out = row_view(*out);
+  a.lse = lse;
+  a.q_lens = q_lens;
+  a.k_lens = k_lens;
+  a.Hq = Hq;
+  a.rep = Hq / Hkv;
+  a.Tq = Tq;
+  a.Tk = Tk;
+  a.window = window >= Tk ? 0 : window;   // one that reaches every key is none
+  a.sinks = std::min(sinks, Tk);
+  a.pair_heads = a.rep % 2 == 0;
+  a.scale = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
+  const int rows = a.pair_heads ? kWaRows : 2 * kWaRows;
+  a.blocks = (Tq + rows - 1) / rows;
+  const int64_t ctas = static_cast<int64_t>(a.blocks) * (a.pair_heads ? a.rep / 2 : a.rep);
+  if (ctas > 0x7fffffffLL) return fail(MIKV_ESHAPE, "window_attention: Tq=%d Hq=%d", Tq, Hq);
+  if (int e = encode_view(&qm, *q, Tq, Hq, B, "q", &a.qb, &a.qh)) return e;
+  if (int e = encode_view(&km, *k, Tk, Hkv, B, "k", &a.kb, &a.kh)) return e;
+  if (int e = encode_view(&vm, *v, Tk, Hkv, B, "v", &a.vb, &a.vh)) return e;
   const auto kern = type == MIKV_PAGES_BF16 ? window_attention_kernel<true> : window_attention_kernel<false>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kWaTile);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kWaSmem);
   if (e != cudaSuccess) return check_launch_after(e, "window_attention_kernel");
-  kern<<<dim3((Tq + kWaQ - 1) / kWaQ, Hq, B), kWaThreads, 4 * kWaTile, as_stream(stream)>>>(a);
+  kern<<<dim3(static_cast<unsigned>(ctas), Hkv, B), kWaThreads, kWaSmem, as_stream(stream)>>>(qm, km, vm, a);
   return check_launch("window_attention_kernel");
 }

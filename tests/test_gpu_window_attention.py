@@ -72,6 +72,25 @@ def test_padded_batches(dtype, window, sinks):
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("Tq,Tk,window,sinks", [(20, 900, 100, 5), (300, 700, 30, 0), (1, 400, 1, 130), (5, 300, 40, 64),
+                                                (130, 1000, 513, 200)])
+def test_rows_that_no_query_sees_hold_anything(dtype, Tq, Tk, window, sinks):
+    """Between the sinks and the first query's window, and past the end, in tiles of every kind."""
+    for k_len in (Tk, Tk - 37):
+        q, k, v = (_make(1, H, T, dtype, "bhtd", s) for H, T, s in ((3, Tq, 1), (1, Tk, 2), (1, Tk, 3)))
+        gap = slice(sinks, k_len - Tq - window + 1)
+        for x, bad in ((k, float("nan")), (v, float("-inf"))):
+            if gap.stop > gap.start:
+                x[:, :, gap] = bad
+            x[:, :, k_len:] = bad
+        want, wl, mag = op.window_attention(*(ph.f64(torch.nan_to_num(x, 0, 0, 0)) for x in (q, k, v)), window, sinks, None, [k_len])
+        out, lse = _run(q, k, v, window, sinks, None, [k_len])
+        name = "bf16" if dtype == torch.bfloat16 else "fp16"
+        ph.close(out, want, mag, ph.HALF_STEP[name], weights=ph.HALF_STEP[name])
+        ph.close_lse(lse, wl)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("drop", [9.0, 10.5, 14.0])
 def test_many_small_weights_beside_a_large_one(dtype, drop):
     q = torch.full((1, 1, 40, 128), 0.25, dtype=dtype, device=ph.DEV)
