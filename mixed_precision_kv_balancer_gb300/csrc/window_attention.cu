@@ -65,8 +65,12 @@ struct WindowArgs {
 struct WaBars {
   uint64_t full[kWaRing], empty[kWaRing];   // buffer landed; the products that read it are done
   uint64_t fix[kWaRing];                    // a value tile's hidden rows are cleared
-  uint64_t q, s[2], p[2], o[2];             // queries landed; scores, weights, last sums written
+  uint64_t q, s[2], p[2][2], o[2];          // queries landed; scores, half the weights, last sums written
 };
+
+// The same value in every lane, told to the compiler: what depends on it stays in uniform
+// registers, which the matrix instructions read.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // What one CTA works on; every warp computes it alike.
 struct Work {
@@ -74,14 +78,25 @@ struct Work {
   int head[2], q0[2];     // per tile: head and first row
   int pa[2], pb[2];       // positions of its first and last row
   int tiles, ts, tw0;     // key tiles: ts of the sinks, then tw0, tw0 + 1, ...
-  int last[2];            // index of the last key tile that query tile t sees, -1 for none
+  int from[2], last[2];   // query tile t sees the sinks' key tiles and tiles from .. last; last -1: none
   int nt;                 // query tiles
   __device__ __forceinline__ int j0(int i) const { return (i < ts ? i : tw0 + i - ts) * kWaRows; }
 };
+// One query tile of it, in registers (an array indexed by a warp's number would not be).
+struct Tile {
+  bool live;
+  int head, q0, pa, pb, from, last;
+  // Whether any of its rows sees key tile i.
+  __device__ __forceinline__ bool sees(int i, int ts) const { return i <= last && (i < ts || i >= from); }
+};
+__device__ __forceinline__ Tile tile_of(const Work& w, int t) {
+  return {t < w.nt, t ? w.head[1] : w.head[0], t ? w.q0[1] : w.q0[0], t ? w.pa[1] : w.pa[0], t ? w.pb[1] : w.pb[0],
+          t ? w.from[1] : w.from[0], t ? w.last[1] : w.last[0]};
+}
 __device__ __forceinline__ Work work_of(const WindowArgs& a, int b, int hk, int x) {
   Work w;
-  w.ql = a.q_lens ? min(max(a.q_lens[b], 0), a.Tq) : a.Tq;
-  w.kl = a.k_lens ? min(max(a.k_lens[b], 0), a.Tk) : a.Tk;
+  w.ql = a.q_lens ? min(max(uniform(a.q_lens[b]), 0), a.Tq) : a.Tq;
+  w.kl = a.k_lens ? min(max(uniform(a.k_lens[b]), 0), a.Tk) : a.Tk;
   w.off = w.kl - w.ql;
   const int per = a.pair_heads ? a.rep / 2 : a.rep;       // CTAs of one row block
   const int blk = a.blocks - 1 - x / per, u = x % per;    // the last rows, which see the most, first
@@ -102,16 +117,14 @@ __device__ __forceinline__ Work work_of(const WindowArgs& a, int b, int hk, int 
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int e = w.pb[t] < 0 ? -1 : w.pb[t] / kWaRows;
-    w.last[t] = t >= w.nt || e < 0 ? -1 : e < w.ts ? e : e - w.tw0 + w.ts;
+    w.last[t] = t >= w.nt || e < 0 ? -1 : e - w.tw0 + w.ts;
+    w.from[t] = w.ts + (a.window > 0 ? max(w.pa[t] - a.window + 1, 0) / kWaRows - w.tw0 : 0);
   }
   return w;
 }
-// Whether any row of query tile t sees a key of the tile at j0, and whether all rows see all of it.
-__device__ __forceinline__ bool tile_seen(const WindowArgs& a, const Work& w, int t, int j0) {
-  return t < w.nt && j0 <= w.pb[t] && (a.window == 0 || j0 + kWaRows - 1 > w.pa[t] - a.window || j0 < a.sinks);
-}
-__device__ __forceinline__ bool tile_whole(const WindowArgs& a, const Work& w, int t, int j0) {
-  return j0 + kWaRows - 1 <= w.pa[t] && (a.window == 0 || j0 > w.pb[t] - a.window || j0 + kWaRows <= a.sinks);
+// Whether all rows of a query tile see all of the key tile at j0.
+__device__ __forceinline__ bool tile_whole(const WindowArgs& a, const Tile& t, int j0) {
+  return j0 + kWaRows - 1 <= t.pa && (a.window == 0 || j0 > t.pb - a.window || j0 + kWaRows <= a.sinks);
 }
 // Rows [z0, z1) and [z2, 128) of the value tile at j0 that no query of the call sees.
 struct Hidden {
@@ -126,6 +139,12 @@ __device__ __forceinline__ Hidden hidden_rows(const WindowArgs& a, const Work& w
   return h;
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -191,6 +210,9 @@ __device__ __forceinline__ uint64_t value_desc(uint32_t saddr) {
   d |= static_cast<uint64_t>(2) << 61;
   return d;
 }
+// The address field of a descriptor counts 16-byte units in its low bits; the tiles lie below
+// 256 KB, so a step inside a tile or to another one is an addition.
+constexpr uint64_t desc_step(uint32_t bytes) { return bytes >> 4; }
 
 // One thread's row of one query tile.
 struct Row {
@@ -200,8 +222,10 @@ struct Row {
 
 // One tile of scores: 128 columns of this thread's lane at `ts` become weights; the accumulator
 // at `to` is rescaled where some row of the warp needs it.
+// Each half of the weights is announced (`ready`, one arrival a warp) as soon as it is written.
 template <bool BF>
-__device__ __forceinline__ void softmax_tile(const WindowArgs& a, uint32_t ts, uint32_t to, bool whole, int p, int j0, Row& r) {
+__device__ __forceinline__ void softmax_tile(const WindowArgs& a, uint32_t ts, uint32_t to, bool whole, int p, int j0, Row& r,
+                                             const uint32_t (&ready)[2]) {
   float s[kWaRows];
 #pragma unroll
   for (int c = 0; c < 4; ++c) ld32(ts + c * 32, s + c * 32);
@@ -252,9 +276,14 @@ __device__ __forceinline__ void softmax_tile(const WindowArgs& a, uint32_t ts, u
       u[i] = pack2<BF>(e.x, e.y);
     }
     st16(ts + c / 2, u);
+    if (c % 64 == 32) {
+      wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) tc::mbar_arrive(ready[c / 64]);
+    }
   }
   r.l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-  wait_st();
 }
 
 // CTA (pair of query tiles, key head, batch row).
@@ -268,7 +297,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
   const int b = blockIdx.z, hk = blockIdx.y;
   const Work w = work_of(a, b, hk, blockIdx.x);
   if (w.nt == 0) return;   // uniform over the CTA: no query row
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kWaRing; ++i) {
       tc::mbar_init(smem_u32(&bar.full[i]), 1);
@@ -278,7 +307,8 @@ __global__ void __launch_bounds__(kWaThreads, 1)
     tc::mbar_init(smem_u32(&bar.q), 1);
     for (int t = 0; t < 2; ++t) {
       tc::mbar_init(smem_u32(&bar.s[t]), 1);
-      tc::mbar_init(smem_u32(&bar.p[t]), 4);
+      tc::mbar_init(smem_u32(&bar.p[t][0]), 4);
+      tc::mbar_init(smem_u32(&bar.p[t][1]), 4);
       tc::mbar_init(smem_u32(&bar.o[t]), 1);
     }
     tc::mbar_init_fence();
@@ -287,15 +317,15 @@ __global__ void __launch_bounds__(kWaThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = tslot;
+  const uint32_t tmem = uniform(tslot);
   const uint32_t sq = tc::smem_base(smem), ring = sq + 2 * tc::kTileBytes;
   tc::Waits wait;
 
   if (warp == kWaTmaWarp) {
     if (lane == 0 && w.tiles > 0) {
       tc::mbar_expect_tx(smem_u32(&bar.q), w.nt * tc::kTileBytes);
-      for (int t = 0; t < w.nt; ++t)
-        tma_rows(sq + t * tc::kTileBytes, &qmap, w.q0[t], w.head[t] * a.qh, b * a.qb, smem_u32(&bar.q));
+      tma_rows(sq, &qmap, w.q0[0], w.head[0] * a.qh, b * a.qb, smem_u32(&bar.q));
+      if (w.nt == 2) tma_rows(sq + tc::kTileBytes, &qmap, w.q0[1], w.head[1] * a.qh, b * a.qb, smem_u32(&bar.q));
     }
     // buffer n % kWaRing takes tile n: keys of key tile n / 2 (n even), values (n odd)
     for (int n = 0; n < 2 * w.tiles; ++n) {
@@ -328,53 +358,80 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       }
     }
   } else if (warp == kWaMmaWarp) {
-    if (lane == 0 && w.tiles > 0) {
+    // The whole warp walks the steps, so that addresses and descriptors stay uniform; one elected
+    // lane issues.
+    if (w.tiles > 0) {
+      bool lead = elect_one();
+      const Tile tile[2] = {tile_of(w, 0), tile_of(w, 1)};
       constexpr uint32_t kType = BF ? (1u << 7) | (1u << 10) : 0u;
       constexpr uint32_t kScores = tc::idesc_f16(kWaRows, kWaRows) | kType;
       constexpr uint32_t kValues = tc::idesc_f16(kWaRows, kD) | kType | (1u << 16);   // B: rows along the contraction
-      int p_seen[2] = {0, 0};
-      uint32_t fixed = 0;   // parity of each buffer's next clearing
+      const uint64_t q0 = tc::smem_desc(sq), k0 = tc::smem_desc(ring), v0 = value_desc(ring);
+      uint32_t fixed = 0;                          // parity of each buffer's next clearing
+      int p_par[2] = {0, 0};                       // parity of the next weights
+      bool more[2] = {false, false};               // sums begun
+      int slot = 0, par = 0, vslot = 0, vpar = 0;  // ring position and parity of this step's keys, and values
+      bool before[2] = {false, false}, clear = false;
       wait(smem_u32(&bar.q), 0);
+      // after a wait that gave up no lane leads, nothing more is issued, and the others' waits run out
       for (int i = 0; i <= w.tiles; ++i) {
         // this step's scores from key tile i, behind the last step's sums over value tile i - 1
-        const int kn = 2 * i, vn = 2 * i - 1, ks = kn % kWaRing, vs = i > 0 ? vn % kWaRing : 0;
-        const uint32_t sk = ring + ks * tc::kTileBytes, sv = ring + vs * tc::kTileBytes;
+        const bool here[2] = {i < w.tiles && tile[0].sees(i, w.ts), i < w.tiles && tile[1].sees(i, w.ts)};
+        const uint64_t kd = k0 + slot * desc_step(tc::kTileBytes), vd = v0 + vslot * desc_step(tc::kTileBytes);
+        if (i > 0) {
+          wait(smem_u32(&bar.full[vslot]), vpar);
+          if (clear) {
+            wait(smem_u32(&bar.fix[vslot]), (fixed >> vslot) & 1);
+            fixed ^= 1u << vslot;
+          }
+        }
+        if (i < w.tiles) wait(smem_u32(&bar.full[slot]), par);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (i > 0) {
-            if (t == 0) {
-              wait(smem_u32(&bar.full[vs]), (vn / kWaRing) & 1);
-              if (hidden_rows(a, w, w.j0(i - 1)).any()) {
-                wait(smem_u32(&bar.fix[vs]), (fixed >> vs) & 1);
-                fixed ^= 1u << vs;
-              }
-            }
-            if (tile_seen(a, w, t, w.j0(i - 1))) {
-              wait(smem_u32(&bar.p[t]), p_seen[t]++ & 1);
-              tc::fence_after_sync();
-              if (wait.ok) {
+          const uint32_t ts = tmem + t * 128, to = tmem + kWaO + t * 128;
+          if (before[t]) {
 #pragma unroll
-                for (int c = 0; c < kWaRows / 16; ++c)
-                  mma_ts(tmem + kWaO + t * 128, tmem + t * 128 + c * 8, value_desc(sv + c * 2048), kValues, p_seen[t] > 1 || c > 0);
-                if (i - 1 == w.last[t]) tc::commit(smem_u32(&bar.o[t]));
+            for (int half = 0; half < 2; ++half) {
+              wait(smem_u32(&bar.p[t][half]), p_par[t]);
+              lead &= __all_sync(0xffffffffu, wait.ok) != 0;
+              tc::fence_after_sync();
+              if (lead) {
+#pragma unroll
+                for (int c = half * 4; c < half * 4 + 4; ++c)
+                  mma_ts(to, ts + c * 8, vd + desc_step(c * 2048), kValues, more[t] || c > 0);
+                if (half == 1 && i - 1 == tile[t].last) tc::commit(smem_u32(&bar.o[t]));
               }
             }
+            p_par[t] ^= 1;
+            more[t] = true;
           }
-          if (i < w.tiles) {
-            if (t == 0) {
-              wait(smem_u32(&bar.full[ks]), (kn / kWaRing) & 1);
-              tc::fence_after_sync();
-            }
-            if (tile_seen(a, w, t, w.j0(i)) && wait.ok) {
-              tc::mma_tile(tmem + t * 128, sq + t * tc::kTileBytes, sk, kScores);
+          if (here[t]) {
+            lead &= __all_sync(0xffffffffu, wait.ok) != 0;
+            tc::fence_after_sync();
+            const uint64_t qd = q0 + t * desc_step(tc::kTileBytes);
+            if (lead) {
+#pragma unroll
+              for (int c = 0; c < kD / 16; ++c) {
+                const uint64_t off = desc_step((c >> 2) * tc::kKBlock + (c & 3) * 32);
+                tc::mma_f16(ts, qd + off, kd + off, kScores, c > 0);
+              }
               tc::commit(smem_u32(&bar.s[t]));
             }
           }
+          before[t] = here[t];
         }
-        if (i < w.tiles && wait.ok) {   // nobody waits for the last buffers
-          if (i > 0) tc::commit(smem_u32(&bar.empty[vs]));
-          tc::commit(smem_u32(&bar.empty[ks]));
+        if (i < w.tiles) {
+          if (lead) {   // nobody waits for the last buffers
+            if (i > 0) tc::commit(smem_u32(&bar.empty[vslot]));
+            tc::commit(smem_u32(&bar.empty[slot]));
+          }
+          clear = hidden_rows(a, w, w.j0(i)).any();
         }
+        // the values of tile i follow its keys in the ring
+        vslot = slot + 1 == kWaRing ? 0 : slot + 1;
+        vpar = vslot == 0 ? par ^ 1 : par;
+        slot = vslot + 1 == kWaRing ? 0 : vslot + 1;
+        par = slot == 0 ? vpar ^ 1 : vpar;
       }
     }
     __syncwarp();
@@ -382,26 +439,25 @@ __global__ void __launch_bounds__(kWaThreads, 1)
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;   // the thread's TMEM lane is its row
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + kWaO + t * 128;
-    const int p = w.pa[t] + row;
+    const Tile tile = tile_of(w, t);
+    const int p = tile.pa + row;
+    const uint32_t ready[2] = {smem_u32(&bar.p[t][0]), smem_u32(&bar.p[t][1])};
     Row r;
     int seen = 0;
     for (int i = 0; i < w.tiles; ++i) {
+      if (!tile.sees(i, w.ts)) continue;
       const int j0 = w.j0(i);
-      if (!tile_seen(a, w, t, j0)) continue;
       wait(smem_u32(&bar.s[t]), seen++ & 1);
       tc::fence_after_sync();
-      softmax_tile<BF>(a, ts, to, tile_whole(a, w, t, j0), p, j0, r);
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(smem_u32(&bar.p[t]));
+      softmax_tile<BF>(a, ts, to, tile_whole(a, tile, j0), p, j0, r, ready);
     }
-    if (t < w.nt) {
-      if (w.last[t] >= 0) wait(smem_u32(&bar.o[t]), 0);
+    if (tile.live) {
+      if (tile.last >= 0) wait(smem_u32(&bar.o[t]), 0);
       tc::fence_after_sync();
-      const int q = w.q0[t] + row;
+      const int q = tile.q0 + row;
       float inv = r.l == 0.f ? 0.f : 1.f / r.l;
       if (!wait.ok) inv = __int_as_float(0x7fffffff);
-      uint8_t* dst = a.out.row(b, w.head[t], q);
+      uint8_t* dst = a.out.row(b, tile.head, q);
 #pragma unroll 1
       for (int c = 0; c < kD; c += 32) {
         float o[32];
@@ -422,7 +478,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       }
       if (q < w.ql && a.lse) {
         const float v = r.l == 0.f ? -INFINITY : (r.m * a.scale + (log2f(r.l) - Weights<BF>::shift)) * 0.6931471805599453f;
-        a.lse[(static_cast<int64_t>(b) * a.Hq + w.head[t]) * a.Tq + q] = wait.ok ? v : inv;
+        a.lse[(static_cast<int64_t>(b) * a.Hq + tile.head) * a.Tq + q] = wait.ok ? v : inv;
       }
     }
   }
