@@ -40,7 +40,7 @@ namespace {
 constexpr int kWaRows = 128;                     // query rows and key rows of a tile
 constexpr int kWaRing = 5;
 constexpr int kMaxRows = 1 << 30;                // of q or k: positions and their differences fit 32 bits
-constexpr int kWaThreads = 320;                  // 2 x 4 softmax warps, the TMA warp, the MMA warp
+constexpr int kWaThreads = 352;                  // 2 x 4 softmax warps, the TMA warp, 2 MMA warps
 constexpr int kWaTmaWarp = 8, kWaMmaWarp = 9;
 constexpr int kWaSmem = (2 + kWaRing) * tc::kTileBytes + 1024;
 constexpr uint32_t kWaCols = 512;                // S_0, S_1, O_0, O_1: 128 columns each
@@ -65,6 +65,7 @@ struct WindowArgs {
 struct WaBars {
   uint64_t full[kWaRing], empty[kWaRing];   // buffer landed; the products that read it are done
   uint64_t fix[kWaRing];                    // a value tile's hidden rows are cleared
+  uint64_t turn[2];                         // the tile's products may be issued
   uint64_t q, s[2], p[2][2], o[2];          // queries landed; scores, half the weights, last sums written
 };
 
@@ -301,11 +302,12 @@ __global__ void __launch_bounds__(kWaThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kWaRing; ++i) {
       tc::mbar_init(smem_u32(&bar.full[i]), 1);
-      tc::mbar_init(smem_u32(&bar.empty[i]), 1);
+      tc::mbar_init(smem_u32(&bar.empty[i]), 2);
       tc::mbar_init(smem_u32(&bar.fix[i]), 1);
     }
     tc::mbar_init(smem_u32(&bar.q), 1);
     for (int t = 0; t < 2; ++t) {
+      tc::mbar_init(smem_u32(&bar.turn[t]), 1);
       tc::mbar_init(smem_u32(&bar.s[t]), 1);
       tc::mbar_init(smem_u32(&bar.p[t][0]), 4);
       tc::mbar_init(smem_u32(&bar.p[t][1]), 4);
@@ -357,26 +359,34 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         }
       }
     }
-  } else if (warp == kWaMmaWarp) {
-    // The whole warp walks the steps, so that addresses and descriptors stay uniform; one elected
-    // lane issues.
+  } else if (warp >= kWaMmaWarp) {
+    // One warp per query tile, so that neither waits in the other's place.  The whole warp walks
+    // the steps, so that addresses and descriptors stay uniform; one elected lane issues.
     if (w.tiles > 0) {
+      const int t = warp - kWaMmaWarp;
       bool lead = elect_one();
-      const Tile tile[2] = {tile_of(w, 0), tile_of(w, 1)};
+      const Tile tile = tile_of(w, t);
       constexpr uint32_t kType = BF ? (1u << 7) | (1u << 10) : 0u;
       constexpr uint32_t kScores = tc::idesc_f16(kWaRows, kWaRows) | kType;
       constexpr uint32_t kValues = tc::idesc_f16(kWaRows, kD) | kType | (1u << 16);   // B: rows along the contraction
-      const uint64_t q0 = tc::smem_desc(sq), k0 = tc::smem_desc(ring), v0 = value_desc(ring);
+      const uint32_t ts = tmem + t * 128, to = tmem + kWaO + t * 128;
+      const uint64_t qd = tc::smem_desc(sq + t * tc::kTileBytes), k0 = tc::smem_desc(ring), v0 = value_desc(ring);
       uint32_t fixed = 0;                          // parity of each buffer's next clearing
-      int p_par[2] = {0, 0};                       // parity of the next weights
-      bool more[2] = {false, false};               // sums begun
+      int p_par = 0;                               // parity of the next weights
       int slot = 0, par = 0, vslot = 0, vpar = 0;  // ring position and parity of this step's keys, and values
-      bool before[2] = {false, false}, clear = false;
+      bool more = false, before = false, clear = false;
+      // The two warps issue in turns, one step each: the tiles then stay half a step apart, and one's
+      // weights are made while the tensor core works for the other (in step, both would wait).
+      int turn = t;   // tile 0 begins without waiting
+      const auto take_turn = [&] {
+        if (turn > 0) wait(smem_u32(&bar.turn[t]), (turn - 1) & 1);
+        ++turn;
+      };
       wait(smem_u32(&bar.q), 0);
       // after a wait that gave up no lane leads, nothing more is issued, and the others' waits run out
       for (int i = 0; i <= w.tiles; ++i) {
         // this step's scores from key tile i, behind the last step's sums over value tile i - 1
-        const bool here[2] = {i < w.tiles && tile[0].sees(i, w.ts), i < w.tiles && tile[1].sees(i, w.ts)};
+        const bool here = i < w.tiles && tile.sees(i, w.ts);
         const uint64_t kd = k0 + slot * desc_step(tc::kTileBytes), vd = v0 + vslot * desc_step(tc::kTileBytes);
         if (i > 0) {
           wait(smem_u32(&bar.full[vslot]), vpar);
@@ -386,40 +396,37 @@ __global__ void __launch_bounds__(kWaThreads, 1)
           }
         }
         if (i < w.tiles) wait(smem_u32(&bar.full[slot]), par);
+        if (before) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const uint32_t ts = tmem + t * 128, to = tmem + kWaO + t * 128;
-          if (before[t]) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              wait(smem_u32(&bar.p[t][half]), p_par[t]);
-              lead &= __all_sync(0xffffffffu, wait.ok) != 0;
-              tc::fence_after_sync();
-              if (lead) {
-#pragma unroll
-                for (int c = half * 4; c < half * 4 + 4; ++c)
-                  mma_ts(to, ts + c * 8, vd + desc_step(c * 2048), kValues, more[t] || c > 0);
-                if (half == 1 && i - 1 == tile[t].last) tc::commit(smem_u32(&bar.o[t]));
-              }
-            }
-            p_par[t] ^= 1;
-            more[t] = true;
-          }
-          if (here[t]) {
+          for (int half = 0; half < 2; ++half) {
+            wait(smem_u32(&bar.p[t][half]), p_par);
+            if (half == 0) take_turn();
             lead &= __all_sync(0xffffffffu, wait.ok) != 0;
             tc::fence_after_sync();
-            const uint64_t qd = q0 + t * desc_step(tc::kTileBytes);
             if (lead) {
 #pragma unroll
-              for (int c = 0; c < kD / 16; ++c) {
-                const uint64_t off = desc_step((c >> 2) * tc::kKBlock + (c & 3) * 32);
-                tc::mma_f16(ts, qd + off, kd + off, kScores, c > 0);
-              }
-              tc::commit(smem_u32(&bar.s[t]));
+              for (int c = half * 4; c < half * 4 + 4; ++c) mma_ts(to, ts + c * 8, vd + desc_step(c * 2048), kValues, more || c > 0);
+              if (half == 1 && i - 1 == tile.last) tc::commit(smem_u32(&bar.o[t]));
             }
           }
-          before[t] = here[t];
+          p_par ^= 1;
+          more = true;
         }
+        if (!before) take_turn();
+        if (here) {
+          lead &= __all_sync(0xffffffffu, wait.ok) != 0;
+          tc::fence_after_sync();
+          if (lead) {
+#pragma unroll
+            for (int c = 0; c < kD / 16; ++c) {
+              const uint64_t off = desc_step((c >> 2) * tc::kKBlock + (c & 3) * 32);
+              tc::mma_f16(ts, qd + off, kd + off, kScores, c > 0);
+            }
+            tc::commit(smem_u32(&bar.s[t]));
+          }
+        }
+        if (lane == 0) tc::mbar_arrive(smem_u32(&bar.turn[t ^ 1]));
+        before = here;
         if (i < w.tiles) {
           if (lead) {   // nobody waits for the last buffers
             if (i > 0) tc::commit(smem_u32(&bar.empty[vslot]));
