@@ -65,7 +65,9 @@ struct WindowArgs {
 struct WaBars {
   uint64_t full[kWaRing], empty[kWaRing];   // buffer landed; the products that read it are done
   uint64_t fix[kWaRing];                    // a value tile's hidden rows are cleared
+  uint64_t told[2], heard[2];               // the next item is known; every warp has read it
   uint64_t turn[2];                         // the tile's products may be issued
+  uint64_t qfree;                           // the products that read the queries are done
   uint64_t q, s[2], p[2][2], o[2];          // queries landed; scores, half the weights, last sums written
 };
 
@@ -287,17 +289,49 @@ __device__ __forceinline__ void softmax_tile(const WindowArgs& a, uint32_t ts, u
   r.l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
-// CTA (pair of query tiles, key head, batch row).
+// A work item is (pair of query tiles, key head, batch row), one per CTA of the grid; a CTA that
+// is done takes over one that has not been launched (cluster launch control), so the SMs stay
+// busy whatever the lengths are, and the next item's queries, keys and scores are under way
+// while the last sums are written.  Every warp walks the items; lane 0 of the TMA warp asks for
+// the next one once it has requested all tiles of this one: two or three key tiles before the
+// end, early enough to hide the answer and late enough to keep long items from piling up (asked
+// at an item's start, 8192 causal tokens of 32 heads took 394 us instead of 349).
+struct Item {
+  int x, y, z;
+};
+__device__ __forceinline__ void ask_next(uint32_t answer, uint32_t mbar) {
+  tc::mbar_expect_tx(mbar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];\n" ::"r"(answer),
+               "r"(mbar)
+               : "memory");
+}
+// The answer to ask n, by the whole warp: false where nothing is left.
+__device__ __forceinline__ bool next_item(WaBars& bar, const uint4* answers, int n, tc::Waits& wait, Item& it) {
+  const uint32_t at = smem_u32(&answers[n & 1]);
+  wait(smem_u32(&bar.told[n & 1]), (n >> 1) & 1);
+  uint32_t x = 0, y = 0, z = 0, ok = 0;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 h;\n ld.shared.b128 h, [%4];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n selp.u32 %3, 1, 0, p;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, %1, %2, _}, h;\n}\n"
+      : "+r"(x), "+r"(y), "+r"(z), "=r"(ok)
+      : "r"(at)
+      : "memory");
+  tc::fence_proxy_async();   // the answer is read before another overwrites it
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(smem_u32(&bar.heard[n & 1]));
+  it = {uniform(x), uniform(y), uniform(z)};
+  return __all_sync(0xffffffffu, ok != 0 && wait.ok);
+}
+
 template <bool BF>
 __global__ void __launch_bounds__(kWaThreads, 1)
     window_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                             const __grid_constant__ CUtensorMap vmap, const WindowArgs a) {
   extern __shared__ uint8_t smem[];
   __shared__ WaBars bar;
+  __shared__ __align__(16) uint4 answers[2];
   __shared__ uint32_t tslot;
-  const int b = blockIdx.z, hk = blockIdx.y;
-  const Work w = work_of(a, b, hk, blockIdx.x);
-  if (w.nt == 0) return;   // uniform over the CTA: no query row
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kWaRing; ++i) {
@@ -306,7 +340,10 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       tc::mbar_init(smem_u32(&bar.fix[i]), 1);
     }
     tc::mbar_init(smem_u32(&bar.q), 1);
+    tc::mbar_init(smem_u32(&bar.qfree), 2);
     for (int t = 0; t < 2; ++t) {
+      tc::mbar_init(smem_u32(&bar.told[t]), 1);
+      tc::mbar_init(smem_u32(&bar.heard[t]), kWaThreads / 32);
       tc::mbar_init(smem_u32(&bar.turn[t]), 1);
       tc::mbar_init(smem_u32(&bar.s[t]), 1);
       tc::mbar_init(smem_u32(&bar.p[t][0]), 4);
@@ -322,171 +359,212 @@ __global__ void __launch_bounds__(kWaThreads, 1)
   const uint32_t tmem = uniform(tslot);
   const uint32_t sq = tc::smem_base(smem), ring = sq + 2 * tc::kTileBytes;
   tc::Waits wait;
+  Item it = {static_cast<int>(blockIdx.x), static_cast<int>(blockIdx.y), static_cast<int>(blockIdx.z)};
 
   if (warp == kWaTmaWarp) {
-    if (lane == 0 && w.tiles > 0) {
-      tc::mbar_expect_tx(smem_u32(&bar.q), w.nt * tc::kTileBytes);
-      tma_rows(sq, &qmap, w.q0[0], w.head[0] * a.qh, b * a.qb, smem_u32(&bar.q));
-      if (w.nt == 2) tma_rows(sq + tc::kTileBytes, &qmap, w.q0[1], w.head[1] * a.qh, b * a.qb, smem_u32(&bar.q));
-    }
-    // buffer n % kWaRing takes tile n: keys of key tile n / 2 (n even), values (n odd)
-    for (int n = 0; n < 2 * w.tiles; ++n) {
-      const int slot = n % kWaRing, j0 = w.j0(n >> 1);
-      if (n >= kWaRing) wait(smem_u32(&bar.empty[slot]), (n / kWaRing - 1) & 1);
-      const uint32_t dst = ring + slot * tc::kTileBytes, full = smem_u32(&bar.full[slot]);
-      if (lane == 0 && wait.ok) {
-        tc::mbar_expect_tx(full, tc::kTileBytes);
-        if (n & 1)
-          tma_rows(dst, &vmap, j0, hk * a.vh, b * a.vb, full);
-        else
-          tma_rows(dst, &kmap, j0, hk * a.kh, b * a.kb, full);
-      }
-      __syncwarp();
-      if (n & 1) {
-        const Hidden h = hidden_rows(a, w, j0);
-        if (h.any()) {
-          wait(full, (n / kWaRing) & 1);
-          for (int c = lane; c < kWaRows * 16; c += 32) {   // 16-byte pieces, both channel blocks
-            const int r = c >> 4, piece = c & 15;
-            if ((r >= h.z0 && r < h.z1) || r >= h.z2)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(dst + (piece >> 3) * tc::kKBlock + r * 128 + (piece & 7) * 16),
-                           "r"(0)
-                           : "memory");
+    int slot = 0, par = 1, qs = 0;   // ring position; parity that an empty buffer shows; query loads
+    for (int n = 0;; ++n) {
+      const int b = it.z, hk = it.y;
+      const Work w = work_of(a, b, hk, it.x);
+      if (w.nt > 0 && w.tiles > 0) {
+        if (qs > 0) wait(smem_u32(&bar.qfree), (qs - 1) & 1);
+        ++qs;
+        if (lane == 0 && wait.ok) {
+          tc::mbar_expect_tx(smem_u32(&bar.q), w.nt * tc::kTileBytes);
+          tma_rows(sq, &qmap, w.q0[0], w.head[0] * a.qh, b * a.qb, smem_u32(&bar.q));
+          if (w.nt == 2) tma_rows(sq + tc::kTileBytes, &qmap, w.q0[1], w.head[1] * a.qh, b * a.qb, smem_u32(&bar.q));
+        }
+        for (int c = 0; c < 2 * w.tiles; ++c) {   // keys of key tile c / 2 (c even), then its values
+          const int j0 = w.j0(c >> 1);
+          const uint32_t dst = ring + slot * tc::kTileBytes, full = smem_u32(&bar.full[slot]);
+          wait(smem_u32(&bar.empty[slot]), par);
+          if (lane == 0 && wait.ok) {
+            tc::mbar_expect_tx(full, tc::kTileBytes);
+            if (c & 1)
+              tma_rows(dst, &vmap, j0, hk * a.vh, b * a.vb, full);
+            else
+              tma_rows(dst, &kmap, j0, hk * a.kh, b * a.kb, full);
           }
-          tc::fence_proxy_async();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(smem_u32(&bar.fix[slot]));
+          if (c & 1) {
+            const Hidden h = hidden_rows(a, w, j0);
+            if (h.any()) {
+              wait(full, par ^ 1);
+              for (int e = lane; e < kWaRows * 16; e += 32) {   // 16-byte pieces, both channel blocks
+                const int r = e >> 4, piece = e & 15;
+                if ((r >= h.z0 && r < h.z1) || r >= h.z2)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(dst + (piece >> 3) * tc::kKBlock + r * 128 + (piece & 7) * 16),
+                               "r"(0)
+                               : "memory");
+              }
+              tc::fence_proxy_async();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(smem_u32(&bar.fix[slot]));
+            }
+          }
+          if (++slot == kWaRing) {
+            slot = 0;
+            par ^= 1;
+          }
         }
       }
+      if (n >= 2) wait(smem_u32(&bar.heard[n & 1]), ((n >> 1) - 1) & 1);
+      if (lane == 0 && wait.ok) ask_next(smem_u32(&answers[n & 1]), smem_u32(&bar.told[n & 1]));
+      if (!next_item(bar, answers, n, wait, it)) break;
     }
+    // every buffer's release has arrived before the CTA ends
+    for (int c = 0; c < kWaRing; ++c) {
+      wait(smem_u32(&bar.empty[slot]), par);
+      if (++slot == kWaRing) {
+        slot = 0;
+        par ^= 1;
+      }
+    }
+    if (qs > 0) wait(smem_u32(&bar.qfree), (qs - 1) & 1);
   } else if (warp >= kWaMmaWarp) {
     // One warp per query tile, so that neither waits in the other's place.  The whole warp walks
     // the steps, so that addresses and descriptors stay uniform; one elected lane issues.
-    if (w.tiles > 0) {
-      const int t = warp - kWaMmaWarp;
-      bool lead = elect_one();
-      const Tile tile = tile_of(w, t);
-      constexpr uint32_t kType = BF ? (1u << 7) | (1u << 10) : 0u;
-      constexpr uint32_t kScores = tc::idesc_f16(kWaRows, kWaRows) | kType;
-      constexpr uint32_t kValues = tc::idesc_f16(kWaRows, kD) | kType | (1u << 16);   // B: rows along the contraction
-      const uint32_t ts = tmem + t * 128, to = tmem + kWaO + t * 128;
-      const uint64_t qd = tc::smem_desc(sq + t * tc::kTileBytes), k0 = tc::smem_desc(ring), v0 = value_desc(ring);
-      uint32_t fixed = 0;                          // parity of each buffer's next clearing
-      int p_par = 0;                               // parity of the next weights
-      int slot = 0, par = 0, vslot = 0, vpar = 0;  // ring position and parity of this step's keys, and values
-      bool more = false, before = false, clear = false;
-      // The two warps issue in turns, one step each: the tiles then stay half a step apart, and one's
-      // weights are made while the tensor core works for the other (in step, both would wait).
-      int turn = t;   // tile 0 begins without waiting
-      const auto take_turn = [&] {
-        if (turn > 0) wait(smem_u32(&bar.turn[t]), (turn - 1) & 1);
-        ++turn;
-      };
-      wait(smem_u32(&bar.q), 0);
-      // after a wait that gave up no lane leads, nothing more is issued, and the others' waits run out
-      for (int i = 0; i <= w.tiles; ++i) {
-        // this step's scores from key tile i, behind the last step's sums over value tile i - 1
-        const bool here = i < w.tiles && tile.sees(i, w.ts);
-        const uint64_t kd = k0 + slot * desc_step(tc::kTileBytes), vd = v0 + vslot * desc_step(tc::kTileBytes);
-        if (i > 0) {
-          wait(smem_u32(&bar.full[vslot]), vpar);
-          if (clear) {
-            wait(smem_u32(&bar.fix[vslot]), (fixed >> vslot) & 1);
-            fixed ^= 1u << vslot;
+    const int t = warp - kWaMmaWarp;
+    bool lead = elect_one();
+    constexpr uint32_t kType = BF ? (1u << 7) | (1u << 10) : 0u;
+    constexpr uint32_t kScores = tc::idesc_f16(kWaRows, kWaRows) | kType;
+    constexpr uint32_t kValues = tc::idesc_f16(kWaRows, kD) | kType | (1u << 16);   // B: rows along the contraction
+    const uint32_t ts = tmem + t * 128, to = tmem + kWaO + t * 128;
+    const uint64_t qd = tc::smem_desc(sq + t * tc::kTileBytes), k0 = tc::smem_desc(ring), v0 = value_desc(ring);
+    uint32_t fixed = 0;              // parity of each buffer's next clearing
+    int p_par = 0, q_par = 0;        // parity of the next weights, and queries
+    int slot = 0, par = 0;           // ring position and parity
+    // The two warps issue in turns, one step each: the tiles then stay half a step apart, and one's
+    // weights are made while the tensor core works for the other (in step, both would wait).
+    int turn = t;   // tile 0 begins without waiting
+    const auto take_turn = [&] {
+      if (turn > 0) wait(smem_u32(&bar.turn[t]), (turn - 1) & 1);
+      ++turn;
+    };
+    for (int n = 0;; ++n) {
+      const Work w = work_of(a, it.z, it.y, it.x);
+      if (w.nt > 0 && w.tiles > 0) {
+        const Tile tile = tile_of(w, t);
+        bool more = false, before = false, clear = false;
+        int vslot = 0, vpar = 0;     // the last step's values
+        wait(smem_u32(&bar.q), q_par);
+        q_par ^= 1;
+        // after a wait that gave up no lane leads, nothing more is issued, and the others' waits run out
+        for (int i = 0; i <= w.tiles; ++i) {
+          // this step's scores from key tile i, behind the last step's sums over value tile i - 1
+          const bool keys = i < w.tiles, here = keys && tile.sees(i, w.ts);
+          const uint64_t kd = k0 + slot * desc_step(tc::kTileBytes), vd = v0 + vslot * desc_step(tc::kTileBytes);
+          if (i > 0) {
+            wait(smem_u32(&bar.full[vslot]), vpar);
+            if (clear) {
+              wait(smem_u32(&bar.fix[vslot]), (fixed >> vslot) & 1);
+              fixed ^= 1u << vslot;
+            }
           }
-        }
-        if (i < w.tiles) wait(smem_u32(&bar.full[slot]), par);
-        if (before) {
+          if (keys) wait(smem_u32(&bar.full[slot]), par);
+          if (before) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            wait(smem_u32(&bar.p[t][half]), p_par);
-            if (half == 0) take_turn();
+            for (int half = 0; half < 2; ++half) {
+              wait(smem_u32(&bar.p[t][half]), p_par);
+              if (half == 0) take_turn();
+              lead &= __all_sync(0xffffffffu, wait.ok) != 0;
+              tc::fence_after_sync();
+              if (lead) {
+#pragma unroll
+                for (int c = half * 4; c < half * 4 + 4; ++c) mma_ts(to, ts + c * 8, vd + desc_step(c * 2048), kValues, more || c > 0);
+                if (half == 1 && i - 1 == tile.last) tc::commit(smem_u32(&bar.o[t]));
+              }
+            }
+            p_par ^= 1;
+            more = true;
+          } else {
+            take_turn();
+          }
+          if (here) {
             lead &= __all_sync(0xffffffffu, wait.ok) != 0;
             tc::fence_after_sync();
             if (lead) {
 #pragma unroll
-              for (int c = half * 4; c < half * 4 + 4; ++c) mma_ts(to, ts + c * 8, vd + desc_step(c * 2048), kValues, more || c > 0);
-              if (half == 1 && i - 1 == tile.last) tc::commit(smem_u32(&bar.o[t]));
+              for (int c = 0; c < kD / 16; ++c) {
+                const uint64_t off = desc_step((c >> 2) * tc::kKBlock + (c & 3) * 32);
+                tc::mma_f16(ts, qd + off, kd + off, kScores, c > 0);
+              }
+              tc::commit(smem_u32(&bar.s[t]));
             }
           }
-          p_par ^= 1;
-          more = true;
-        }
-        if (!before) take_turn();
-        if (here) {
-          lead &= __all_sync(0xffffffffu, wait.ok) != 0;
-          tc::fence_after_sync();
+          if (lane == 0) tc::mbar_arrive(smem_u32(&bar.turn[t ^ 1]));
+          before = here;
           if (lead) {
-#pragma unroll
-            for (int c = 0; c < kD / 16; ++c) {
-              const uint64_t off = desc_step((c >> 2) * tc::kKBlock + (c & 3) * 32);
-              tc::mma_f16(ts, qd + off, kd + off, kScores, c > 0);
-            }
-            tc::commit(smem_u32(&bar.s[t]));
-          }
-        }
-        if (lane == 0) tc::mbar_arrive(smem_u32(&bar.turn[t ^ 1]));
-        before = here;
-        if (i < w.tiles) {
-          if (lead) {   // nobody waits for the last buffers
             if (i > 0) tc::commit(smem_u32(&bar.empty[vslot]));
-            tc::commit(smem_u32(&bar.empty[slot]));
+            if (keys) tc::commit(smem_u32(&bar.empty[slot]));
+            if (i == w.tiles - 1) tc::commit(smem_u32(&bar.qfree));   // the last scores
           }
-          clear = hidden_rows(a, w, w.j0(i)).any();
+          if (keys) {   // the values of tile i follow its keys in the ring
+            clear = hidden_rows(a, w, w.j0(i)).any();
+            vslot = slot + 1 == kWaRing ? 0 : slot + 1;
+            vpar = vslot == 0 ? par ^ 1 : par;
+            slot = vslot + 1 == kWaRing ? 0 : vslot + 1;
+            par = slot == 0 ? vpar ^ 1 : vpar;
+          }
         }
-        // the values of tile i follow its keys in the ring
-        vslot = slot + 1 == kWaRing ? 0 : slot + 1;
-        vpar = vslot == 0 ? par ^ 1 : par;
-        slot = vslot + 1 == kWaRing ? 0 : vslot + 1;
-        par = slot == 0 ? vpar ^ 1 : vpar;
       }
+      if (!next_item(bar, answers, n, wait, it)) break;
     }
-    __syncwarp();
   } else {
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;   // the thread's TMEM lane is its row
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + kWaO + t * 128;
-    const Tile tile = tile_of(w, t);
-    const int p = tile.pa + row;
     const uint32_t ready[2] = {smem_u32(&bar.p[t][0]), smem_u32(&bar.p[t][1])};
-    Row r;
-    int seen = 0;
-    for (int i = 0; i < w.tiles; ++i) {
-      if (!tile.sees(i, w.ts)) continue;
-      const int j0 = w.j0(i);
-      wait(smem_u32(&bar.s[t]), seen++ & 1);
-      tc::fence_after_sync();
-      softmax_tile<BF>(a, ts, to, tile_whole(a, tile, j0), p, j0, r, ready);
-    }
-    if (tile.live) {
-      if (tile.last >= 0) wait(smem_u32(&bar.o[t]), 0);
-      tc::fence_after_sync();
-      const int q = tile.q0 + row;
-      float inv = r.l == 0.f ? 0.f : 1.f / r.l;
-      if (!wait.ok) inv = __int_as_float(0x7fffffff);
-      uint8_t* dst = a.out.row(b, tile.head, q);
+    int s_par = 0, o_par = 0;
+    for (int n = 0;; ++n) {
+      const int b = it.z;
+      const Work w = work_of(a, b, it.y, it.x);
+      const Tile tile = tile_of(w, t);
+      if (tile.live) {
+        const int p = tile.pa + row;
+        Row r;
+        for (int i = 0; i < w.tiles; ++i) {
+          if (!tile.sees(i, w.ts)) continue;
+          const int j0 = w.j0(i);
+          wait(smem_u32(&bar.s[t]), s_par);
+          s_par ^= 1;
+          tc::fence_after_sync();
+          softmax_tile<BF>(a, ts, to, tile_whole(a, tile, j0), p, j0, r, ready);
+        }
+        if (tile.last >= 0) {
+          wait(smem_u32(&bar.o[t]), o_par);
+          o_par ^= 1;
+        }
+        tc::fence_after_sync();
+        const int q = tile.q0 + row;
+        float inv = r.l == 0.f ? 0.f : 1.f / r.l;
+        if (!wait.ok) inv = __int_as_float(0x7fffffff);
+        uint8_t* dst = a.out.row(b, tile.head, q);
 #pragma unroll 1
-      for (int c = 0; c < kD; c += 32) {
-        float o[32];
-        if (seen > 0) {
-          ld32(to + c, o);
-          wait_ld();
-        } else {
+        for (int c = 0; c < kD; c += 32) {
+          float o[32];
+          if (tile.last >= 0) {
+            ld32(to + c, o);
+            wait_ld();
+          } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0.f;
-        }
-        if (q < w.ql) {
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
+          if (q < w.ql) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(dst + (c + i) * 2) =
-                make_uint4(pack2<BF>(o[i] * inv, o[i + 1] * inv), pack2<BF>(o[i + 2] * inv, o[i + 3] * inv),
-                           pack2<BF>(o[i + 4] * inv, o[i + 5] * inv), pack2<BF>(o[i + 6] * inv, o[i + 7] * inv));
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4*>(dst + (c + e) * 2) =
+                  make_uint4(pack2<BF>(o[e] * inv, o[e + 1] * inv), pack2<BF>(o[e + 2] * inv, o[e + 3] * inv),
+                             pack2<BF>(o[e + 4] * inv, o[e + 5] * inv), pack2<BF>(o[e + 6] * inv, o[e + 7] * inv));
+          }
         }
+        if (q < w.ql && a.lse) {
+          const float v = r.l == 0.f ? -INFINITY : (r.m * a.scale + (log2f(r.l) - Weights<BF>::shift)) * 0.6931471805599453f;
+          a.lse[(static_cast<int64_t>(b) * a.Hq + tile.head) * a.Tq + q] = wait.ok ? v : inv;
+        }
+        tc::fence_before_sync();   // the sums are read before the next item's products overwrite them
       }
-      if (q < w.ql && a.lse) {
-        const float v = r.l == 0.f ? -INFINITY : (r.m * a.scale + (log2f(r.l) - Weights<BF>::shift)) * 0.6931471805599453f;
-        a.lse[(static_cast<int64_t>(b) * a.Hq + tile.head) * a.Tq + q] = wait.ok ? v : inv;
-      }
+      if (!next_item(bar, answers, n, wait, it)) break;
     }
   }
   if (!wait.ok) tc::report_giveup(tc::kGiveupWindow);
