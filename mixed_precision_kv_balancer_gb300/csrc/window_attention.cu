@@ -58,6 +58,7 @@ struct WindowArgs {
   const int32_t *q_lens, *k_lens;
   int Hq, rep, Tq, Tk, window, sinks, blocks;
   bool pair_heads;               // the CTA's tiles are two heads' rows, else 256 rows of one head
+  bool wide_out;                 // rows of out begin at multiples of 32 bytes
   int qb, qh, kb, kh, vb, vh;    // 1, or 0 where the view repeats one batch row or head
   float scale;                   // log2(e) / sqrt(D)
 };
@@ -184,6 +185,14 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
+// 32 bytes to a 32-byte boundary.  A thread writes its own row, 32 rows an instruction: what counts
+// is the number of instructions (16-byte pieces cost twice the store cycles).
+__device__ __forceinline__ void st_global32(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]),
+               "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // One thread: rows [row0, row0 + 128) of one (head, batch row) into the tile at `s`, two boxes of
 // 64 channels; rows past the end are zero-filled.  Completes 32 KB on the mbarrier.
 __device__ __forceinline__ void tma_rows(uint32_t s, const CUtensorMap* map, int row0, int h, int b, uint32_t mbar) {
@@ -223,6 +232,9 @@ struct Row {
   bool first = true;              // no tile has been accumulated
 };
 
+// The n lowest bits set, for any n.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
 // One tile of scores: 128 columns of this thread's lane at `ts` become weights; the accumulator
 // at `to` is rescaled where some row of the warp needs it.
 // Each half of the weights is announced (`ready`, one arrival a warp) as soon as it is written.
@@ -234,10 +246,17 @@ __device__ __forceinline__ void softmax_tile(const WindowArgs& a, uint32_t ts, u
   for (int c = 0; c < 4; ++c) ld32(ts + c * 32, s + c * 32);
   wait_ld();
   if (!whole) {
+    // the row sees columns lo .. hi and those below sk; 32 columns whole to the warp's rows are left alone
     const int hi = p - j0, lo = a.window > 0 ? hi - a.window + 1 : 0, sk = a.sinks - j0;
 #pragma unroll
-    for (int c = 0; c < kWaRows; ++c)
-      if (c > hi || (c < lo && c >= sk)) s[c] = -INFINITY;
+    for (int c = 0; c < kWaRows; c += 32) {
+      const uint32_t m = low_bits(hi + 1 - c) & (~low_bits(lo - c) | low_bits(sk - c));
+      if (!__all_sync(0xffffffffu, m == 0xffffffffu)) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (!(m & (1u << i))) s[c + i] = -INFINITY;
+      }
+    }
   }
   float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -551,11 +570,16 @@ __global__ void __launch_bounds__(kWaThreads, 1)
             for (int e = 0; e < 32; ++e) o[e] = 0.f;
           }
           if (q < w.ql) {
+            uint32_t u[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(dst + (c + e) * 2) =
-                  make_uint4(pack2<BF>(o[e] * inv, o[e + 1] * inv), pack2<BF>(o[e + 2] * inv, o[e + 3] * inv),
-                             pack2<BF>(o[e + 4] * inv, o[e + 5] * inv), pack2<BF>(o[e + 6] * inv, o[e + 7] * inv));
+            for (int e = 0; e < 16; ++e) u[e] = pack2<BF>(o[2 * e] * inv, o[2 * e + 1] * inv);
+            if (a.wide_out) {
+              st_global32(dst + c * 2, u);
+              st_global32(dst + c * 2 + 32, u + 8);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(dst + (c + 2 * e) * 2) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+            }
           }
         }
         if (q < w.ql && a.lse) {
@@ -626,6 +650,7 @@ extern "C" int mikv_window_attention(const mikv_rows* q, const mikv_rows* k, con
   a.window = window >= Tk ? 0 : window;   // one that reaches every key is none
   a.sinks = std::min(sinks, Tk);
   a.pair_heads = a.rep % 2 == 0;
+  a.wide_out = ((reinterpret_cast<uintptr_t>(out->data) | static_cast<uintptr_t>(a.out.sb | a.out.sh | a.out.st)) & 31u) == 0;
   a.scale = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
   const int rows = a.pair_heads ? kWaRows : 2 * kWaRows;
   a.blocks = (Tq + rows - 1) / rows;
