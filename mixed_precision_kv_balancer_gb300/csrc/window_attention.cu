@@ -481,37 +481,45 @@ __global__ void __launch_bounds__(kWaThreads, 1)
             }
           }
           if (keys) wait(smem_u32(&bar.full[slot]), par);
+          if (before) wait(smem_u32(&bar.p[t][0]), p_par);
+          take_turn();
+          lead &= __all_sync(0xffffffffu, wait.ok) != 0;
+          tc::fence_after_sync();
           if (before) {
+            const auto sums = [&](int c0, int c1) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              wait(smem_u32(&bar.p[t][half]), p_par);
-              if (half == 0) take_turn();
+              for (int c = c0; c < c1; ++c) mma_ts(to, ts + c * 8, vd + desc_step(c * 2048), kValues, more || c > 0);
+            };
+            // the tensor core's queue holds about two products: a wait between them leaves it idle
+            if (__all_sync(0xffffffffu, tc::mbar_wait(smem_u32(&bar.p[t][1]), p_par, 1))) {
+              tc::fence_after_sync();
+              if (lead) sums(0, kWaRows / 16);
+            } else {
+              if (lead) sums(0, kWaRows / 32);
+              wait(smem_u32(&bar.p[t][1]), p_par);
               lead &= __all_sync(0xffffffffu, wait.ok) != 0;
               tc::fence_after_sync();
-              if (lead) {
-#pragma unroll
-                for (int c = half * 4; c < half * 4 + 4; ++c) mma_ts(to, ts + c * 8, vd + desc_step(c * 2048), kValues, more || c > 0);
-                if (half == 1 && i - 1 == tile.last) tc::commit(smem_u32(&bar.o[t]));
-              }
+              if (lead) sums(kWaRows / 32, kWaRows / 16);
             }
             p_par ^= 1;
             more = true;
-          } else {
-            take_turn();
           }
-          if (here) {
-            lead &= __all_sync(0xffffffffu, wait.ok) != 0;
-            tc::fence_after_sync();
-            if (lead) {
+          if (lead) {
+            if (before && i - 1 == tile.last) tc::commit(smem_u32(&bar.o[t]));
+            // the turn passes on a little early: the other warp takes as long to wake as the
+            // last products take to issue
+            if (here) {
 #pragma unroll
               for (int c = 0; c < kD / 16; ++c) {
                 const uint64_t off = desc_step((c >> 2) * tc::kKBlock + (c & 3) * 32);
                 tc::mma_f16(ts, qd + off, kd + off, kScores, c > 0);
+                if (c == 4) tc::mbar_arrive(smem_u32(&bar.turn[t ^ 1]));
               }
               tc::commit(smem_u32(&bar.s[t]));
+            } else {
+              tc::mbar_arrive(smem_u32(&bar.turn[t ^ 1]));
             }
           }
-          if (lane == 0) tc::mbar_arrive(smem_u32(&bar.turn[t ^ 1]));
           before = here;
           if (lead) {
             if (i > 0) tc::commit(smem_u32(&bar.empty[vslot]));
