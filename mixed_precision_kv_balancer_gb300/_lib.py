@@ -262,104 +262,94 @@ def mikv_channel_quantize(k, bits, codes, meta, stream=None):
 _PAGE_DTYPE = {MIKV_PAGES_FP16: torch.float16, MIKV_PAGES_BF16: torch.bfloat16, MIKV_PAGES_INT8: torch.float16}
 
 
-class _on:
-    """Runs a call on the device its tensors are on: the stream is that device's current one
-    unless given, and the device is made current for the launch."""
-
-    def __init__(self, device, stream):
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        self.device, self.stream = device, stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _launch(device, stream, call, *args):
+    """call(*args, stream) on the device its tensors are on: on that device's current stream unless
+    one is given, with the device made current for the launch.  The status is checked under
+    the call's name."""
+    index = device.index
+    st = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        rc = call(*args, st)
+    else:
+        with torch.cuda.device(index):
+            rc = call(*args, st)
+    if rc != 0:
+        raise MikvError(call.__name__, rc, load().mikv_last_error().decode())
 
 
 def _need(t, name, dtype, shape, device):
-    """Pointer of a contiguous tensor of this dtype, shape (None: any size) and device; None for None."""
+    """Pointer of a contiguous tensor of this dtype, shape and device; None for None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != device or not t.is_contiguous() or t.dim() != len(shape) or any(
-            n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                     f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _rows(t, name, dtype, shape, device):
     """mikv_rows of a [B][H][T][D] tensor whose last dimension is contiguous."""
-    if t.dtype != dtype or t.device != device or t.dim() != 4 or any(
-            n is not None and n != m for n, m in zip(shape, t.shape)) or (t.shape[3] > 1 and t.stride(3) != 1):
-        raise ValueError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)} on {device} with a contiguous "
-                         f"last dimension, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
-    # a dimension of one element is never stepped along: its stride may be anything
-    sb, sh, st = (t.stride(i) if t.shape[i] > 1 else 0 for i in range(3))
-    return ctypes.byref(mikv_rows(t.data_ptr(), sb, sh, st))
+    if t.dtype is dtype and t.shape == shape and t.device == device:
+        sb, sh, st, sd = t.stride()
+        if sd == 1 or shape[3] <= 1:
+            # a dimension of one element is never stepped along: its stride may be anything
+            return ctypes.byref(mikv_rows(t.data_ptr(), sb if shape[0] > 1 else 0, sh if shape[1] > 1 else 0,
+                                          st if shape[2] > 1 else 0))
+    raise ValueError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)} on {device} with a contiguous "
+                     f"last dimension, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
 def _ws_on(nbytes, device, ws):
+    """(pointer, bytes, tensor to keep) of the workspace given, or of a new one of nbytes()."""
     if ws is None:
-        return (torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None), nbytes
+        n = nbytes()
+        ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+        return (None, 0, None) if ws is None else (ws.data_ptr(), n, ws)
     if ws.device != device or not ws.is_contiguous():
         raise ValueError(f"ws: expected a contiguous tensor on {device}, got one on {ws.device}")
-    return ws, ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 def mikv_page_reserve(pages, seqs, add, start, ws=None, stream=None):
     """Room for add int32 [n] more tokens behind sequences seqs (int32 [n], None: 0 .. n - 1);
     start int32 [n] receives each one's first new slot, or -1 where it was refused."""
     lib, dev, n = load(), pages.device, add.shape[0]
-    with _on(dev, stream) as st:
-        w, nb = _ws_on(lib.mikv_page_workspace_bytes(pages.ref, n), dev, ws)
-        _check("mikv_page_reserve", lib.mikv_page_reserve(
-            pages.ref, _need(seqs, "seqs", torch.int32, (n,), dev), _need(add, "add", torch.int32, (n,), dev), n,
-            _need(start, "start", torch.int32, (n,), dev), None if w is None else w.data_ptr(), nb, st))
+    w, nb, _keep = _ws_on(lambda: lib.mikv_page_workspace_bytes(pages.ref, n), dev, ws)
+    _launch(dev, stream, lib.mikv_page_reserve, pages.ref, _need(seqs, "seqs", torch.int32, (n,), dev),
+            _need(add, "add", torch.int32, (n,), dev), n, _need(start, "start", torch.int32, (n,), dev), w, nb)
 
 
 def mikv_page_fork(pages, parent, child, ok, ws=None, stream=None):
     """child[i] becomes a copy of parent[i] (int32 [n] each); ok int32 [n] receives 1, or 0 where refused."""
     lib, dev, n = load(), pages.device, parent.shape[0]
-    with _on(dev, stream) as st:
-        w, nb = _ws_on(lib.mikv_page_workspace_bytes(pages.ref, n), dev, ws)
-        _check("mikv_page_fork", lib.mikv_page_fork(
-            pages.ref, _need(parent, "parent", torch.int32, (n,), dev), _need(child, "child", torch.int32, (n,), dev), n,
-            _need(ok, "ok", torch.int32, (n,), dev), None if w is None else w.data_ptr(), nb, st))
+    w, nb, _keep = _ws_on(lambda: lib.mikv_page_workspace_bytes(pages.ref, n), dev, ws)
+    _launch(dev, stream, lib.mikv_page_fork, pages.ref, _need(parent, "parent", torch.int32, (n,), dev),
+            _need(child, "child", torch.int32, (n,), dev), n, _need(ok, "ok", torch.int32, (n,), dev), w, nb)
 
 
 def mikv_page_free(pages, seqs, ok, stream=None):
     """Sequences seqs (int32 [n], None: 0 .. n - 1) give their pages back; ok int32 [n]."""
     lib, dev, n = load(), pages.device, ok.shape[0]
-    with _on(dev, stream) as st:
-        _check("mikv_page_free", lib.mikv_page_free(
-            pages.ref, _need(seqs, "seqs", torch.int32, (n,), dev), n, _need(ok, "ok", torch.int32, (n,), dev), st))
+    _launch(dev, stream, lib.mikv_page_free, pages.ref, _need(seqs, "seqs", torch.int32, (n,), dev), n,
+            _need(ok, "ok", torch.int32, (n,), dev))
 
 
 def mikv_page_copy(pages, src, dst, ok, stream=None):
     """Page dst[i] takes what page src[i] holds, in all layers (int32 [n] each); ok int32 [n]."""
     lib, dev, n = load(), pages.device, src.shape[0]
-    with _on(dev, stream) as st:
-        _check("mikv_page_copy", lib.mikv_page_copy(
-            pages.ref, _need(src, "src", torch.int32, (n,), dev), _need(dst, "dst", torch.int32, (n,), dev), n,
-            _need(ok, "ok", torch.int32, (n,), dev), st))
+    _launch(dev, stream, lib.mikv_page_copy, pages.ref, _need(src, "src", torch.int32, (n,), dev),
+            _need(dst, "dst", torch.int32, (n,), dev), n, _need(ok, "ok", torch.int32, (n,), dev))
 
 
 def mikv_page_compact(pages, seqs, keep_pos, keep_n, ok, ws=None, stream=None):
     """Sequence seqs[i] keeps keep_n[i] slots per key head: keep_pos int32 [layers][n][Hkv][max_keep],
     keep_n and ok int32 [n]."""
     lib, dev, n, s = load(), pages.device, keep_n.shape[0], pages.struct
-    with _on(dev, stream) as st:
-        w, nb = _ws_on(lib.mikv_page_workspace_bytes(pages.ref, n), dev, ws)
-        _check("mikv_page_compact", lib.mikv_page_compact(
-            pages.ref, _need(seqs, "seqs", torch.int32, (n,), dev),
-            _need(keep_pos, "keep_pos", torch.int32, (s.layers, n, s.Hkv, None), dev),
-            _need(keep_n, "keep_n", torch.int32, (n,), dev), n, keep_pos.shape[3],
-            _need(ok, "ok", torch.int32, (n,), dev), None if w is None else w.data_ptr(), nb, st))
+    w, nb, _keep = _ws_on(lambda: lib.mikv_page_workspace_bytes(pages.ref, n), dev, ws)
+    most = keep_pos.shape[-1]
+    _launch(dev, stream, lib.mikv_page_compact, pages.ref, _need(seqs, "seqs", torch.int32, (n,), dev),
+            _need(keep_pos, "keep_pos", torch.int32, (s.layers, n, s.Hkv, most), dev),
+            _need(keep_n, "keep_n", torch.int32, (n,), dev), n, most, _need(ok, "ok", torch.int32, (n,), dev), w, nb)
 
 
 def mikv_paged_append(pages, layer, k, v, seqs=None, start=None, counts=None, stream=None):
@@ -368,11 +358,9 @@ def mikv_paged_append(pages, layer, k, v, seqs=None, start=None, counts=None, st
     lib, dev, s = load(), pages.device, pages.struct
     n, _, T, _ = k.shape
     shape, dt = (n, s.Hkv, T, s.D), _PAGE_DTYPE[s.type]
-    with _on(dev, stream) as st:
-        _check("mikv_paged_append", lib.mikv_paged_append(
-            pages.ref, layer, _rows(k, "k", dt, shape, dev), _rows(v, "v", dt, shape, dev), n, T,
-            _need(seqs, "seqs", torch.int32, (n,), dev), _need(start, "start", torch.int32, (n,), dev),
-            _need(counts, "counts", torch.int32, (n,), dev), st))
+    _launch(dev, stream, lib.mikv_paged_append, pages.ref, layer, _rows(k, "k", dt, shape, dev),
+            _rows(v, "v", dt, shape, dev), n, T, _need(seqs, "seqs", torch.int32, (n,), dev),
+            _need(start, "start", torch.int32, (n,), dev), _need(counts, "counts", torch.int32, (n,), dev))
 
 
 def mikv_paged_gather(pages, layer, k_out, v_out, seqs=None, stream=None):
@@ -380,10 +368,8 @@ def mikv_paged_gather(pages, layer, k_out, v_out, seqs=None, stream=None):
     lib, dev, s = load(), pages.device, pages.struct
     n, _, T, _ = k_out.shape
     shape, dt = (n, s.Hkv, T, s.D), _PAGE_DTYPE[s.type]
-    with _on(dev, stream) as st:
-        _check("mikv_paged_gather", lib.mikv_paged_gather(
-            pages.ref, layer, _need(seqs, "seqs", torch.int32, (n,), dev), n, T,
-            _rows(k_out, "k_out", dt, shape, dev), _rows(v_out, "v_out", dt, shape, dev), st))
+    _launch(dev, stream, lib.mikv_paged_gather, pages.ref, layer, _need(seqs, "seqs", torch.int32, (n,), dev), n, T,
+            _rows(k_out, "k_out", dt, shape, dev), _rows(v_out, "v_out", dt, shape, dev))
 
 
 def mikv_paged_attention(q, pages, layer, window, sinks, out, lse=None, seqs=None, ws=None, stream=None):
@@ -391,13 +377,10 @@ def mikv_paged_attention(q, pages, layer, window, sinks, out, lse=None, seqs=Non
     lib, dev, s = load(), pages.device, pages.struct
     n, Hq, _ = q.shape
     shape, dt = (n, Hq, s.D), _PAGE_DTYPE[s.type]
-    with _on(dev, stream) as st:
-        w, nb = _ws_on(lib.mikv_paged_attention_workspace_bytes(pages.ref, n, Hq, window, sinks) if ws is None else 0,
-                       dev, ws)
-        _check("mikv_paged_attention", lib.mikv_paged_attention(
-            _need(q, "q", dt, shape, dev), pages.ref, layer, _need(seqs, "seqs", torch.int32, (n,), dev), n, Hq, window,
-            sinks, _need(out, "out", dt, shape, dev), _need(lse, "lse", torch.float32, (n, Hq), dev),
-            None if w is None else w.data_ptr(), nb, st))
+    w, nb, _keep = _ws_on(lambda: lib.mikv_paged_attention_workspace_bytes(pages.ref, n, Hq, window, sinks), dev, ws)
+    _launch(dev, stream, lib.mikv_paged_attention, _need(q, "q", dt, shape, dev), pages.ref, layer,
+            _need(seqs, "seqs", torch.int32, (n,), dev), n, Hq, window, sinks, _need(out, "out", dt, shape, dev),
+            _need(lse, "lse", torch.float32, (n, Hq), dev), w, nb)
 
 
 def mikv_window_attention(q, k, v, window, sinks, out, lse=None, q_lens=None, k_lens=None, stream=None):
@@ -408,13 +391,12 @@ def mikv_window_attention(q, k, v, window, sinks, out, lse=None, q_lens=None, k_
     Hkv, Tk = k.shape[1], k.shape[2]
     if not q.is_cuda or dt not in (torch.float16, torch.bfloat16):
         raise ValueError(f"q: expected fp16 or bf16 on a CUDA device, got {dt} on {dev}")
-    with _on(dev, stream) as st:
-        _check("mikv_window_attention", lib.mikv_window_attention(
-            _rows(q, "q", dt, (B, Hq, Tq, D), dev), _rows(k, "k", dt, (B, Hkv, Tk, D), dev),
-            _rows(v, "v", dt, (B, Hkv, Tk, D), dev), B, Hq, Hkv, Tq, Tk, D,
-            MIKV_PAGES_BF16 if dt == torch.bfloat16 else MIKV_PAGES_FP16, _need(q_lens, "q_lens", torch.int32, (B,), dev),
-            _need(k_lens, "k_lens", torch.int32, (B,), dev), window, sinks, _rows(out, "out", dt, (B, Hq, Tq, D), dev),
-            _need(lse, "lse", torch.float32, (B, Hq, Tq), dev), st))
+    qs, ks = (B, Hq, Tq, D), (B, Hkv, Tk, D)
+    _launch(dev, stream, lib.mikv_window_attention, _rows(q, "q", dt, qs, dev), _rows(k, "k", dt, ks, dev),
+            _rows(v, "v", dt, ks, dev), B, Hq, Hkv, Tq, Tk, D,
+            MIKV_PAGES_BF16 if dt is torch.bfloat16 else MIKV_PAGES_FP16, _need(q_lens, "q_lens", torch.int32, (B,), dev),
+            _need(k_lens, "k_lens", torch.int32, (B,), dev), window, sinks, _rows(out, "out", dt, qs, dev),
+            _need(lse, "lse", torch.float32, (B, Hq, Tq), dev))
 
 
 def mikv_set_attention_events(begin=None, end=None):
