@@ -2,20 +2,19 @@
 //
 // Mathematics: out_h = sum_j p_j v_j / sum_j p_j with p_j = exp(l_j - m), one pass over the
 // visible slots with a running maximum and sum.  A unit is one (sequence, key head, group of up
-// to 16 of its query heads): the group's queries meet each key once, as the 16 rows of an
-// mma.sync m16n8k16 whose columns are slots (q . K^T) and then channels (P . V), so every
-// cached row is read from HBM once.  Bound by HBM: 512 (16-bit) or 272 (INT8) bytes per slot
-// and key head against 4 * 16 * 128 products, 16 flop a byte.
+// to 16 of its query heads): the group's queries meet each cached row once.  Bound by HBM: 512
+// (16-bit) or 272 (INT8) bytes per slot and key head against 4 * 16 * 128 products, 16 flop a
+// byte; mma.sync suffices, with 16 slots (or channels) as its M and 8 query heads as its N:
+// S = K Q^T, then O^T += V^T P^T, so that scores, weights and sums of a head stay in one lane's
+// columns and up to 8 heads waste nothing.
 //
-// Split: the visible slots of all units, cut into tiles, form one line; CTA c takes the c-th of
-// `grid` equal parts of it, whatever the sequences' lengths, so ragged batches stay balanced and
-// the grid does not depend on lengths that only the device knows.  A unit that one CTA holds
-// whole is finished there; the others' partial sums go to the workspace and are joined, in
-// order, by a second kernel.
-//
-// Inside a CTA four warps take 16 (16-bit) or 32 (INT8) slots each of every tile, through rings
-// of their own in shared memory (16-byte cp.async, rows of any page, zero-filled where no slot
-// is), and are joined at a unit's end.
+// Split: the visible slots of all units, cut into tiles of 16 (INT8: 32), form one line; warp c of
+// the grid takes the c-th of equal parts of it, whatever the sequences' lengths, so ragged batches
+// stay balanced and the grid does not depend on lengths that only the device knows.  A unit that
+// one warp holds whole is finished there; the others' partial sums go to the workspace and are
+// joined, in order, by a second kernel.  Warps never wait for one another: each streams its part
+// through a ring of its own in shared memory (16-byte cp.async, rows of any page, zero-filled
+// where no slot is) and requests tiles ahead of the one it works on across the units' ends.
 //
 // Precision: scores, maximum, sum and accumulators are fp32.  The weights p meet the values as
 // two 16-bit parts (p = hi + lo, 16 to 22 bits), so they add nothing to the rounding of the
@@ -39,14 +38,13 @@ namespace {
 
 constexpr int kPaThreads = 128;
 constexpr int kPaWarps = 4;
-constexpr int kPaRows = 16;       // query heads of a unit: the mma's M
+constexpr int kPaRows = 16;       // query heads of a unit at most: two column blocks of the mma
 constexpr int kPaCtasPerSM = 2;
 
 template <int TYPE>
 struct Shape {
   static constexpr bool q8 = TYPE == MIKV_PAGES_INT8;
-  static constexpr int tw = q8 ? 32 : 16;             // slots of one warp's stage
-  static constexpr int tile = tw * kPaWarps;          // slots of a tile
+  static constexpr int tw = q8 ? 32 : 16;             // slots of a tile
   static constexpr int row = q8 ? kD : kD * 2;        // bytes of a stored row
   static constexpr int shift = TYPE == MIKV_PAGES_FP16 ? 15 : 0;  // the weights' factor, log2
   static constexpr int pv = q8 ? MIKV_PAGES_BF16 : TYPE;          // type of the weights and values in products
@@ -65,7 +63,7 @@ struct AttendArgs {
   int window, sinks;
   uint16_t* out;
   float* lse;
-  float* part;    // [2 * grid][kPartFloats]
+  float* part;    // [2 * warps of the grid][kPartFloats]
   float scale;    // log2(e) / sqrt(D)
 };
 constexpr int kPartFloats = kPaRows * kD + 2 * kPaRows;  // O, then m, then l
@@ -142,15 +140,16 @@ __device__ __forceinline__ int64_t scan64(int64_t v, int64_t* warp_sums, int64_t
   return v + before;
 }
 
-// CTAs that get a part: with fewer tiles than CTAs one each, so that no part is empty.
-__device__ __forceinline__ int workers_of(int64_t total, int grid) { return static_cast<int>(min(total, static_cast<int64_t>(grid))); }
+// Warps that get a part: with fewer tiles than warps one each, so that no part is empty.
+__device__ __forceinline__ int workers_of(int64_t total, int warps) { return static_cast<int>(min(total, static_cast<int64_t>(warps))); }
 
-// One warp's accumulators over its slots of a unit.
-template <int TYPE, bool WIDE>
+// One warp's accumulators of a unit.  Column block nh, thread column j: query head 8 nh + 2 t + j.
+template <int NH>
 struct Acc {
-  float o[kD / 8][4];   // 16 rows x 128 channels, mma layout (INT8: even and odd channels apart)
-  float m[2], l[2];     // rows g and g + 8: maximum (log2 units) and this thread's part of the sum
-  float z[2][2];        // INT8: sum of p (z + 128 s) per row and group, this thread's part
+  float o[kD / 16][NH][4];   // O^T: 16 channels x 8 heads, mma layout
+  float m[NH][2];            // maximum, log2 units (the same in the 8 lanes of a column)
+  float l[NH][2];            // this thread's part of the sum
+  float z[NH][2][2];         // INT8: this thread's part of sum p (z + 128 s), per group of channels
 };
 
 // Shared-memory address of 16-byte piece c of row r of a stage's keys or values.
@@ -217,194 +216,169 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t x, uint32_t sel) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// One stage: scores of its slots, the running softmax, and their values.
-// `qf`: the queries as A fragments; `qsum`: INT8, sums of the query's two groups for rows g, g + 8.
-template <int TYPE, bool WIDE>
-__device__ __forceinline__ void consume(uint32_t st, const uint32_t (&qf)[kD / 16][4], const float (&qsum)[2][2], float scale,
-                                        Acc<TYPE, WIDE>& acc) {
+// One tile: scores of its slots, the running softmax, and their values.
+// `qf`: the queries as B fragments; `qsum`: INT8, sums of each query's two groups.
+template <int TYPE, int NH>
+__device__ __forceinline__ void consume(uint32_t st, const uint32_t (&qf)[kD / 16][NH][2], const float (&qsum)[NH][2][2], float scale,
+                                        Acc<NH>& acc) {
   using S = Shape<TYPE>;
-  constexpr int NT = S::tw / 8;
-  constexpr int R = WIDE ? 2 : 1;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  constexpr int KT = S::tw / 16;
+  const int lane = threadIdx.x & 31, g = lane >> 2;
   const uint32_t mask = lds32(st + 2 * S::k_bytes + 2 * S::meta);
-  float s[NT][4];
+  float s[KT][NH][4];   // slots 16 kt + g and + 8, heads as in Acc
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+  for (int kt = 0; kt < KT; ++kt) {
     if (!S::q8) {
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      float d[NH][4] = {};
 #pragma unroll
-      for (int k2 = 0; k2 < kD / 32; ++k2) {
-        uint32_t b0, b1, b2, b3;
-        ldsm_x4(k_at<S::q8>(st, nt * 8 + (lane & 7), k2 * 4 + (lane >> 3)), b0, b1, b2, b3);
-        mma<TYPE>(d, qf[2 * k2], b0, b1);
-        mma<TYPE>(d, qf[2 * k2 + 1], b2, b3);
+      for (int ks = 0; ks < kD / 16; ++ks) {
+        uint32_t a[4];
+        ldsm_x4(k_at<S::q8>(st, kt * 16 + (lane & 15), ks * 2 + (lane >> 4)), a[0], a[1], a[2], a[3]);
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh) mma<TYPE>(d[nh], a, qf[ks][nh][0], qf[ks][nh][1]);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[nt][j] = d[j] * scale;
+      for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[kt][nh][j] = d[nh][j] * scale;
     } else {
-      float d[2][4] = {};
+      float d[2][NH][4] = {};
 #pragma unroll
       for (int grp = 0; grp < 2; ++grp) {
-        const uint4 c = lds128(k_at<S::q8>(st, nt * 8 + g, grp * 4 + t));
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        // 16 codes of slots g and g + 8; the channels' order is the queries' too
+        const uint4 c0 = lds128(k_at<S::q8>(st, kt * 16 + g, grp * 4 + (lane & 3)));
+        const uint4 c1 = lds128(k_at<S::q8>(st, kt * 16 + g + 8, grp * 4 + (lane & 3)));
+        const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma<TYPE>(d[grp], qf[grp * 4 + kk], codes_f16(w[kk], 0x4140u), codes_f16(w[kk], 0x4342u));
-      }
-      const uint32_t ms = st + 2 * S::k_bytes + (nt * 8 + 2 * t) * kMetaBytes;
-      const uint2 m0 = lds64(ms), m1 = lds64(ms + kMetaBytes);
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint32_t a[4] = {codes_f16(w0[kk], 0x4140u), codes_f16(w1[kk], 0x4140u), codes_f16(w0[kk], 0x4342u),
+                                 codes_f16(w1[kk], 0x4342u)};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint2 mm = (j & 1) ? m1 : m0;
-        const int r = j >> 1;
-        s[nt][j] = scale * (meta_s(mm.x) * d[0][j] + meta_z(mm.x) * qsum[r][0] + (meta_s(mm.y) * d[1][j] + meta_z(mm.y) * qsum[r][1]));
+          for (int nh = 0; nh < NH; ++nh) mma<TYPE>(d[grp][nh], a, qf[grp * 4 + kk][nh][0], qf[grp * 4 + kk][nh][1]);
+        }
       }
+      const uint32_t ms = st + 2 * S::k_bytes + (kt * 16 + g) * kMetaBytes;
+      const uint2 m[2] = {lds64(ms), lds64(ms + 8 * kMetaBytes)};
+#pragma unroll
+      for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint2 mm = m[j >> 1];
+          s[kt][nh][j] = scale * (meta_s(mm.x) * d[0][nh][j] + meta_z(mm.x) * qsum[nh][j & 1][0] +
+                                  (meta_s(mm.y) * d[1][nh][j] + meta_z(mm.y) * qsum[nh][j & 1][1]));
+        }
     }
   }
   if (mask != (S::tw == 32 ? 0xffffffffu : 0xffffu)) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (!((mask >> (nt * 8 + 2 * t + (j & 1))) & 1u)) s[nt][j] = -INFINITY;
+      for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (!((mask >> (kt * 16 + g + 8 * (j >> 1))) & 1u)) s[kt][nh][j] = -INFINITY;
   }
-  float sub[2], alpha[2];
+  float sub[NH][2], alpha[NH][2];
   bool grew = false;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    float mx = -INFINITY;
+  for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(s[nt][2 * r], s[nt][2 * r + 1]));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    const float mn = fmaxf(acc.m[r], mx);
-    // nothing seen yet: all weights are exp2(-inf) = 0
-    alpha[r] = mn == -INFINITY ? 0.f : ex2(acc.m[r] - mn);
-    sub[r] = mn == -INFINITY ? 0.f : mn - S::shift;
-    grew |= mn > acc.m[r];
-    acc.m[r] = mn;
-  }
+    for (int j = 0; j < 2; ++j) {
+      float mx = fmaxf(s[0][nh][j], s[0][nh][j + 2]);
+#pragma unroll
+      for (int kt = 1; kt < KT; ++kt) mx = fmaxf(mx, fmaxf(s[kt][nh][j], s[kt][nh][j + 2]));
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+      const float mn = fmaxf(acc.m[nh][j], mx);
+      // nothing seen yet: all weights are exp2(-inf) = 0
+      alpha[nh][j] = mn == -INFINITY ? 0.f : ex2(acc.m[nh][j] - mn);
+      sub[nh][j] = mn == -INFINITY ? 0.f : mn - S::shift;
+      grew |= mn > acc.m[nh][j];
+      acc.m[nh][j] = mn;
+    }
   if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      acc.l[r] *= alpha[r];
-      if (S::q8) {
-        acc.z[r][0] *= alpha[r];
-        acc.z[r][1] *= alpha[r];
-      }
+    for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-      for (int i = 0; i < kD / 8; ++i) {
-        acc.o[i][2 * r] *= alpha[r];
-        acc.o[i][2 * r + 1] *= alpha[r];
+      for (int j = 0; j < 2; ++j) {
+        acc.l[nh][j] *= alpha[nh][j];
+        if (S::q8) {
+          acc.z[nh][j][0] *= alpha[nh][j];
+          acc.z[nh][j][1] *= alpha[nh][j];
+        }
+#pragma unroll
+        for (int mt = 0; mt < kD / 16; ++mt) {
+          acc.o[mt][nh][j] *= alpha[nh][j];
+          acc.o[mt][nh][j + 2] *= alpha[nh][j];
+        }
       }
-    }
   }
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-    for (int j = 0; j < 2 * R; ++j) {
-      s[nt][j] = ex2(s[nt][j] - sub[j >> 1]);
-      acc.l[j >> 1] += s[nt][j];
-    }
+    for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[kt][nh][j] = ex2(s[kt][nh][j] - sub[nh][j & 1]);
+        acc.l[nh][j & 1] += s[kt][nh][j];
+      }
   const uint32_t vs = st + S::k_bytes;
 #pragma unroll
-  for (int kt = 0; kt < S::tw / 16; ++kt) {
-    if (!S::q8) {
-      uint32_t hi[4] = {}, lo[4] = {};
+  for (int kt = 0; kt < KT; ++kt) {
+    // weights as B fragments (slots x heads): pairs of heads, transposed into pairs of slots
+    constexpr int G = S::q8 ? 2 : 1;   // INT8: one set per group of channels, scaled
+    uint32_t hi[G][NH][2], lo[G][NH][2];
 #pragma unroll
-      for (int half = 0; half < 2; ++half)
+    for (int r = 0; r < 2; ++r) {
+      uint2 m = make_uint2(0, 0);
+      if (S::q8) m = lds64(st + 2 * S::k_bytes + S::meta + (kt * 16 + g + 8 * r) * kMetaBytes);
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-          split_pair<TYPE>(s[2 * kt + half][2 * r], s[2 * kt + half][2 * r + 1], hi[half * 2 + r], lo[half * 2 + r]);
+      for (int grp = 0; grp < G; ++grp) {
+        const float sc = S::q8 ? meta_s(grp ? m.y : m.x) : 1.f;
+        const float z = S::q8 ? fmaf(128.f, sc, meta_z(grp ? m.y : m.x)) : 0.f;
 #pragma unroll
-      for (int c = 0; c < kD / 8; c += 2) {
-        uint32_t b0, b1, b2, b3;
-        ldsm_x4_t(v_at<S::q8>(vs, kt * 16 + (lane & 15), c + (lane >> 4)), b0, b1, b2, b3);
-        mma<TYPE>(acc.o[c], hi, b0, b1);
-        mma<TYPE>(acc.o[c], lo, b0, b1);
-        mma<TYPE>(acc.o[c + 1], hi, b2, b3);
-        mma<TYPE>(acc.o[c + 1], lo, b2, b3);
-      }
-    } else {
-      uint32_t hi[2][4] = {}, lo[2][4] = {};
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t ms = st + 2 * S::k_bytes + S::meta + ((2 * kt + half) * 8 + 2 * t) * kMetaBytes;
-        const uint2 m0 = lds64(ms), m1 = lds64(ms + kMetaBytes);
-#pragma unroll
-        for (int grp = 0; grp < 2; ++grp) {
-          const uint32_t w0 = grp ? m0.y : m0.x, w1 = grp ? m1.y : m1.x;
-          const float s0 = meta_s(w0), s1 = meta_s(w1);
-          const float z0 = fmaf(128.f, s0, meta_z(w0)), z1 = fmaf(128.f, s1, meta_z(w1));
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float p0 = s[2 * kt + half][2 * r], p1 = s[2 * kt + half][2 * r + 1];
-            split_pair<S::pv>(p0 * s0, p1 * s1, hi[grp][half * 2 + r], lo[grp][half * 2 + r]);
-            acc.z[r][grp] += p0 * z0 + p1 * z1;
+        for (int nh = 0; nh < NH; ++nh) {
+          const float p0 = s[kt][nh][2 * r], p1 = s[kt][nh][2 * r + 1];
+          uint32_t h, l;
+          split_pair<S::pv>(p0 * sc, p1 * sc, h, l);
+          hi[grp][nh][r] = movmatrix_t(h);
+          lo[grp][nh][r] = movmatrix_t(l);
+          if (S::q8) {
+            acc.z[nh][0][grp] += p0 * z;
+            acc.z[nh][1][grp] += p1 * z;
           }
         }
       }
-      // b16 pairs of codes, transposed: word = (slot 2t: channels 2g, 2g+1; slot 2t+1: the same)
+    }
+    if (!S::q8) {
 #pragma unroll
-      for (int c = 0; c < kD / 16; c += 2) {   // 16-channel blocks
+      for (int mt = 0; mt < kD / 16; ++mt) {
+        uint32_t a[4];
+        ldsm_x4_t(v_at<S::q8>(vs, kt * 16 + (lane & 7) + (lane >> 4) * 8, 2 * mt + ((lane >> 3) & 1)), a[0], a[1], a[2], a[3]);
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh) {
+          mma<S::pv>(acc.o[mt][nh], a, hi[0][nh][0], hi[0][nh][1]);
+          mma<S::pv>(acc.o[mt][nh], a, lo[0][nh][0], lo[0][nh][1]);
+        }
+      }
+    } else {
+      // b16 pairs of codes, transposed: a word holds channels 2g, 2g + 1 of slots 2t and 2t + 1, so
+      // row g of the product is channel 2g and row g + 8 channel 2g + 1
+#pragma unroll
+      for (int mt = 0; mt < kD / 16; mt += 2) {
         uint32_t x[4];
-        ldsm_x4_t(v_at<S::q8>(vs, kt * 16 + (lane & 15), c + (lane >> 4)), x[0], x[1], x[2], x[3]);
+        ldsm_x4_t(v_at<S::q8>(vs, kt * 16 + (lane & 15), mt + (lane >> 4)), x[0], x[1], x[2], x[3]);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const int grp = (c + b) >> 2;
+          const int grp = (mt + b) >> 2;
+          const uint32_t a[4] = {codes_bf16(x[2 * b], 0x4240u), codes_bf16(x[2 * b], 0x4341u), codes_bf16(x[2 * b + 1], 0x4240u),
+                                 codes_bf16(x[2 * b + 1], 0x4341u)};
 #pragma unroll
-          for (int odd = 0; odd < 2; ++odd) {
-            const uint32_t sel = odd ? 0x4341u : 0x4240u;
-            const uint32_t b0 = codes_bf16(x[2 * b], sel), b1 = codes_bf16(x[2 * b + 1], sel);
-            mma<S::pv>(acc.o[2 * (c + b) + odd], hi[grp], b0, b1);
-            mma<S::pv>(acc.o[2 * (c + b) + odd], lo[grp], b0, b1);
+          for (int nh = 0; nh < NH; ++nh) {
+            mma<S::pv>(acc.o[mt + b][nh], a, hi[grp][nh][0], hi[grp][nh][1]);
+            mma<S::pv>(acc.o[mt + b][nh], a, lo[grp][nh][0], lo[grp][nh][1]);
           }
         }
-      }
-    }
-  }
-}
-
-// The four warps' accumulators, joined: row r's maximum, sum and channel d.  `sm` floats:
-// [warp][16][128] O, then [warp][16] m, then [warp][16] l.
-template <int TYPE, bool WIDE>
-__device__ __forceinline__ void store_acc(float* sm, Acc<TYPE, WIDE>& acc) {
-  using S = Shape<TYPE>;
-  constexpr int R = WIDE ? 2 : 1;
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  float* so = sm + w * kPaRows * kD;
-  float* smax = sm + kPaWarps * kPaRows * kD;
-  float* ssum = smax + kPaWarps * kPaRows;
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int row = g + 8 * r;
-    float l = acc.l[r];
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    float z[2] = {0.f, 0.f};
-    if (S::q8) {
-#pragma unroll
-      for (int grp = 0; grp < 2; ++grp) {
-        z[grp] = acc.z[r][grp];
-        z[grp] += __shfl_xor_sync(0xffffffffu, z[grp], 1);
-        z[grp] += __shfl_xor_sync(0xffffffffu, z[grp], 2);
-      }
-    }
-    if (t == 0) {
-      smax[w * kPaRows + row] = acc.m[r];
-      ssum[w * kPaRows + row] = l;
-    }
-    if (!S::q8) {
-#pragma unroll
-      for (int c = 0; c < kD / 8; ++c)
-        *reinterpret_cast<float2*>(so + row * kD + c * 8 + 2 * t) = make_float2(acc.o[c][2 * r], acc.o[c][2 * r + 1]);
-    } else {
-#pragma unroll
-      for (int b = 0; b < kD / 16; ++b) {
-        const float zz = z[b >> 2];
-        const float4 x = make_float4(acc.o[2 * b][2 * r] + zz, acc.o[2 * b + 1][2 * r] + zz, acc.o[2 * b][2 * r + 1] + zz,
-                                     acc.o[2 * b + 1][2 * r + 1] + zz);
-        *reinterpret_cast<float4*>(so + row * kD + b * 16 + 4 * t) = x;
       }
     }
   }
@@ -414,214 +388,302 @@ template <int TYPE>
 __device__ __forceinline__ float lse_of(float m, float l) {
   return (m + (log2f(l) - Shape<TYPE>::shift)) * 0.6931471805599453f;
 }
+// Sum over the 8 lanes that share a column.
+__device__ __forceinline__ float column_sum(float x) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
 
-// CTA c of the split.
-template <int TYPE, bool WIDE>
-__global__ void __launch_bounds__(kPaThreads, kPaCtasPerSM) paged_partial_kernel(const AttendArgs a) {
-  using S = Shape<TYPE>;
-  constexpr int R = WIDE ? 2 : 1;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t warp_sums[kPaWarps];
-  __shared__ int64_t s_base;
-  __shared__ int s_seq;
-  pdl_trigger();
-  const Pool& p = a.p;
-  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int units = p.Hkv * a.groups;
-  // this CTA's part of the line of tiles, and the sequence it begins in
-  int64_t mine = 0, total;
-  for (int b = tid; b < a.n; b += kPaThreads) mine += row_tiles<S::tile>(a, b);
-  scan64(mine * units, warp_sums, total);
-  const int workers = workers_of(total, gridDim.x);
-  if (static_cast<int>(blockIdx.x) >= workers) return;
-  const int64_t begin = split_begin(total, workers, blockIdx.x), end = split_begin(total, workers, blockIdx.x + 1);
-  int64_t before = 0;
-  for (int b0 = 0;; b0 += kPaThreads) {   // ends: the last tile is below `total`
-    const int b = b0 + tid;
-    const int64_t v = b < a.n ? static_cast<int64_t>(row_tiles<S::tile>(a, b)) * units : 0;
-    int64_t sum;
-    const int64_t incl = before + scan64(v, warp_sums, sum);
-    if (begin < incl && begin >= incl - v) {
-      s_base = incl - v;
-      s_seq = b;
-    }
-    before += sum;
-    if (begin < before) break;
+// A warp's place in the line of tiles: tile t of `tiles` of unit u of row b.
+struct Cursor {
+  int b, u, t, tiles;
+  int32_t seq;
+  Visible vis;
+};
+template <int TYPE>
+__device__ __forceinline__ void open_row(const AttendArgs& a, Cursor& c) {   // the first row from c.b on that has tiles
+  for (;; ++c.b) {
+    c.vis = row_visible(a, c.b, c.seq);
+    c.tiles = (c.vis.count + Shape<TYPE>::tw - 1) / Shape<TYPE>::tw;
+    if (c.tiles > 0) return;
   }
-  __syncthreads();
-  int64_t base = s_base;
-  int b = s_seq;
+}
+// To the next unit; the caller knows that there is one.
+template <int TYPE>
+__device__ __forceinline__ void next_unit(const AttendArgs& a, Cursor& c) {
+  c.t = 0;
+  if (++c.u == a.p.Hkv * a.groups) {
+    c.u = 0;
+    ++c.b;
+    open_row<TYPE>(a, c);
+  }
+}
 
-  const uint32_t ring = smem_u32(smem) + w * S::stages * S::stage;
-  const size_t lrow = p.layer_rows() * a.layer;
-  const uint64_t policy = l2_evict_first_policy();
-  for (int64_t cur = begin; cur < end;) {
-    int32_t seq;
-    const Visible vis = row_visible(a, b, seq);
-    const int tiles = (vis.count + S::tile - 1) / S::tile;
-    if (tiles == 0) {
-      ++b;
-      continue;
-    }
-    const int u = static_cast<int>((cur - base) / tiles), t0 = static_cast<int>((cur - base) % tiles);
-    const int count = static_cast<int>(min(static_cast<int64_t>(tiles - t0), end - cur));
-    const int h = u / a.groups, head0 = h * a.rep + (u % a.groups) * a.heads;
-    const int rows = min(a.heads, a.rep - (u % a.groups) * a.heads);
-    const int32_t* table = p.table + static_cast<size_t>(seq) * p.max_pages;
-    // slots of this warp: i0 + tile * S::tile + lane
-    const int64_t i0 = static_cast<int64_t>(t0) * S::tile + w * S::tw + lane;
-    const auto find = [&](int it) {
-      return (lane < S::tw && it < count) ? slot_row(p, table, vis, h, i0 + static_cast<int64_t>(it) * S::tile) : kNoRow;
-    };
+// Writes a finished unit, or a part of one for the join (`part` not null).
+template <int TYPE, int NH>
+__device__ __forceinline__ void store_unit(const AttendArgs& a, int b, int u, Acc<NH>& acc, float* part) {
+  using S = Shape<TYPE>;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int head0 = u / a.groups * a.rep + u % a.groups * a.heads, rows = min(a.heads, a.rep - u % a.groups * a.heads);
+  const size_t at = static_cast<size_t>(b) * a.Hq + head0;
 #pragma unroll
-    for (int it = 0; it < S::stages - 1; ++it) {
-      const uint32_t r = find(it);
-      if (it < count) issue<TYPE>(p, lrow, ring + it * S::stage, r, policy);
-      cp_async_commit();
-    }
-    uint32_t next = find(S::stages - 1);
-    // the queries, as A fragments (INT8: channels in the order the codes are read)
-    uint32_t qf[kD / 16][4];
-    float qsum[2][2] = {};
+  for (int nh = 0; nh < NH; ++nh) {
+    float l[2], inv[2];
 #pragma unroll
-    for (int ks = 0; ks < kD / 16; ++ks)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = g + 8 * (j & 1);
-        const int ch = S::q8 ? 64 * (ks >> 2) + 16 * t + 4 * (ks & 3) + 2 * (j >> 1) : 16 * ks + 8 * (j >> 1) + 2 * t;
-        uint32_t x = 0;
-        if (row < rows)
-          x = *reinterpret_cast<const uint32_t*>(a.q + (static_cast<size_t>(b) * a.Hq + head0 + row) * kD + ch);
-        qf[ks][j] = x;
-        if (S::q8) {
-          const __half2 x2 = *reinterpret_cast<const __half2*>(&x);
-          qsum[j & 1][ks >> 2] += __low2float(x2) + __high2float(x2);
-        }
-      }
-    if (S::q8) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
+    for (int j = 0; j < 2; ++j) {
+      l[j] = column_sum(acc.l[nh][j]);
+      if (S::q8) {
 #pragma unroll
         for (int grp = 0; grp < 2; ++grp) {
-          qsum[r][grp] += __shfl_xor_sync(0xffffffffu, qsum[r][grp], 1);
-          qsum[r][grp] += __shfl_xor_sync(0xffffffffu, qsum[r][grp], 2);
+          const float z = column_sum(acc.z[nh][j][grp]);
+#pragma unroll
+          for (int mt = grp * 4; mt < grp * 4 + 4; ++mt) {
+            acc.o[mt][nh][j] += z;
+            acc.o[mt][nh][j + 2] += z;
+          }
         }
-    }
-    Acc<TYPE, WIDE> acc;
-#pragma unroll
-    for (int i = 0; i < kD / 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc.o[i][j] = 0.f;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      acc.m[r] = -INFINITY;
-      acc.l[r] = acc.z[r][0] = acc.z[r][1] = 0.f;
-    }
-    int rd = 0, wr = S::stages - 1;
-    for (int it = 0; it < count; ++it) {
-      cp_async_wait<S::stages - 2>();
-      __syncwarp();   // the stage has landed for all lanes, and the one to be refilled is read
-      if (it + S::stages - 1 < count) issue<TYPE>(p, lrow, ring + wr * S::stage, next, policy);
-      cp_async_commit();
-      next = find(it + S::stages);
-      consume<TYPE, WIDE>(ring + rd * S::stage, qf, qsum, a.scale, acc);
-      rd = rd + 1 == S::stages ? 0 : rd + 1;
-      wr = wr + 1 == S::stages ? 0 : wr + 1;
-    }
-    cp_async_wait<0>();
-    __syncthreads();   // every warp is done with its ring: its space holds the accumulators now
-    float* sm = reinterpret_cast<float*>(smem);
-    store_acc<TYPE, WIDE>(sm, acc);
-    __syncthreads();
-    const float* smax = sm + kPaWarps * kPaRows * kD;
-    const float* ssum = smax + kPaWarps * kPaRows;
-    const bool whole = t0 == 0 && count == tiles;
-    float* part = a.part + (static_cast<size_t>(blockIdx.x) * 2 + (cur == begin ? 0 : 1)) * kPartFloats;
-#pragma unroll 1
-    for (int row = 0; row < min(rows, 8 * R); ++row) {
-      float m = smax[row], l = 0.f, o = 0.f;
-#pragma unroll
-      for (int i = 1; i < kPaWarps; ++i) m = fmaxf(m, smax[i * kPaRows + row]);
-      const float sub = m == -INFINITY ? 0.f : m;
-#pragma unroll
-      for (int i = 0; i < kPaWarps; ++i) {
-        const float f = ex2(smax[i * kPaRows + row] - sub);
-        l += f * ssum[i * kPaRows + row];
-        o += f * sm[(i * kPaRows + row) * kD + tid];
       }
-      if (whole) {
-        const size_t at = static_cast<size_t>(b) * a.Hq + head0 + row;
-        a.out[at * kD + tid] = to_out<TYPE>(l == 0.f ? 0.f : o / l);   // all pages bad: nothing seen
-        if (tid == 0 && a.lse) a.lse[at] = lse_of<TYPE>(m, l);
-      } else {
-        part[row * kD + tid] = o;
-        if (tid == 0) {
-          part[kPaRows * kD + row] = m;
-          part[kPaRows * kD + kPaRows + row] = l;
+      inv[j] = l[j] == 0.f ? 0.f : 1.f / l[j];   // all pages bad: nothing seen
+      const int row = nh * 8 + 2 * t + j;
+      if (g == 0 && row < rows) {
+        if (part) {
+          part[kPaRows * kD + row] = acc.m[nh][j];
+          part[kPaRows * kD + kPaRows + row] = l[j];
+        } else if (a.lse) {
+          a.lse[at + row] = lse_of<TYPE>(acc.m[nh][j], l[j]);
         }
       }
     }
-    __syncthreads();   // the ring may be refilled
-    cur += count;
-    if (cur - base == static_cast<int64_t>(tiles) * units) {
-      base = cur;
-      ++b;
+    if (part) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int row = nh * 8 + 2 * t + j;
+        if (row >= rows) continue;
+#pragma unroll
+        for (int mt = 0; mt < kD / 16; ++mt) {
+          float* dst = part + row * kD + mt * 16;
+          if (S::q8) {
+            *reinterpret_cast<float2*>(dst + 2 * g) = make_float2(acc.o[mt][nh][j], acc.o[mt][nh][j + 2]);
+          } else {
+            dst[g] = acc.o[mt][nh][j];
+            dst[g + 8] = acc.o[mt][nh][j + 2];
+          }
+        }
+      }
+    } else {
+      const int row = nh * 8 + g;   // after the transposition
+      uint16_t* dst = a.out + (at + row) * kD;
+#pragma unroll
+      for (int mt = 0; mt < kD / 16; ++mt) {
+        const float* o = acc.o[mt][nh];
+        const uint32_t x0 = static_cast<uint32_t>(to_out<TYPE>(o[0] * inv[0])) | static_cast<uint32_t>(to_out<TYPE>(o[1] * inv[1])) << 16;
+        const uint32_t x1 = static_cast<uint32_t>(to_out<TYPE>(o[2] * inv[0])) | static_cast<uint32_t>(to_out<TYPE>(o[3] * inv[1])) << 16;
+        const uint32_t y0 = movmatrix_t(x0), y1 = movmatrix_t(x1);   // head g, rows 2t, 2t + 1 (and + 8) of the product
+        if (row >= rows) continue;
+        if (S::q8) {
+          *reinterpret_cast<uint2*>(dst + mt * 16 + 4 * t) = make_uint2(__byte_perm(y0, y1, 0x5410u), __byte_perm(y0, y1, 0x7632u));
+        } else {
+          *reinterpret_cast<uint32_t*>(dst + mt * 16 + 2 * t) = y0;
+          *reinterpret_cast<uint32_t*>(dst + mt * 16 + 8 + 2 * t) = y1;
+        }
+      }
     }
   }
 }
 
-// CTA (unit, row b): joins the parts of a unit that several CTAs held, in their order, and
-// answers for the units without a visible slot.
+template <int TYPE, int NH>
+__global__ void __launch_bounds__(kPaThreads, kPaCtasPerSM) paged_partial_kernel(const AttendArgs a) {
+  using S = Shape<TYPE>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t warp_sums[kPaWarps];
+  __shared__ int64_t s_incl[kPaThreads];
+  pdl_trigger();
+  const Pool& p = a.p;
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int units = p.Hkv * a.groups;
+  // this warp's part of the line of tiles, and the row it begins in; consecutive parts lie on
+  // different SMs, so that a few of them do not share one
+  int64_t mine = tid < a.n ? row_tiles<S::tw>(a, tid) : 0, total;
+  const int64_t head = mine;
+  for (int b = tid + kPaThreads; b < a.n; b += kPaThreads) mine += row_tiles<S::tw>(a, b);
+  int64_t incl = scan64(mine * units, warp_sums, total);
+  const int workers = workers_of(total, gridDim.x * kPaWarps), c = w * gridDim.x + blockIdx.x;
+  const int64_t begin = split_begin(total, workers, c), end = split_begin(total, workers, c + 1);
+  const bool idle = c >= workers;
+  Cursor at;
+  at.b = -1;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < a.n; b0 += kPaThreads) {
+    int64_t sum = total;
+    if (a.n > kPaThreads) {
+      const int b = b0 + tid;
+      const int64_t v = b0 == 0 ? head : b < a.n ? row_tiles<S::tw>(a, b) : 0;
+      incl = before + scan64(v * units, warp_sums, sum);
+    }
+    __syncthreads();   // the last round's sums have been read
+    s_incl[tid] = incl;
+    __syncthreads();
+    if (!idle && at.b < 0 && begin < before + sum) {
+      int below = 0;   // rows of this round that end at or before `begin`
+#pragma unroll
+      for (int i = 0; i < kPaThreads; i += 32) below += __popc(__ballot_sync(0xffffffffu, s_incl[i + lane] <= begin));
+      at.b = b0 + below;
+      before = below ? s_incl[below - 1] : before;   // the row's first tile; not read again once found
+    } else if (at.b < 0) {
+      before += sum;
+    }
+    if (__syncthreads_and(idle || at.b >= 0)) break;
+  }
+  if (idle) return;
+  const int n = static_cast<int>(end - begin);   // tiles of this warp: below 2^31 / tw a row, far fewer a warp
+  open_row<TYPE>(a, at);
+  at.u = static_cast<int>((begin - before) / at.tiles);
+  at.t = static_cast<int>((begin - before) % at.tiles);
+
+  const uint32_t ring = smem_u32(smem) + w * S::stages * S::stage;
+  const size_t lrow = p.layer_rows() * a.layer;
+  const uint64_t policy = l2_evict_first_policy();
+  Cursor ahead = at;   // the next tile to be requested
+  int asked = 0;
+  // the pool row of this lane's slot of that tile, and on to the next one
+  const auto find = [&] {
+    uint32_t r = kNoRow;
+    if (asked < n) {
+      if (lane < S::tw)
+        r = slot_row(p, p.table + static_cast<size_t>(ahead.seq) * p.max_pages, ahead.vis, ahead.u / a.groups,
+                     static_cast<int64_t>(ahead.t) * S::tw + lane);
+      if (++ahead.t == ahead.tiles && asked + 1 < n) next_unit<TYPE>(a, ahead);
+      ++asked;
+    }
+    return r;
+  };
+#pragma unroll
+  for (int i = 0; i < S::stages - 1; ++i) {
+    const uint32_t r = find();
+    if (i < n) issue<TYPE>(p, lrow, ring + i * S::stage, r, policy);
+    cp_async_commit();
+  }
+  uint32_t next = find();
+  int rd = 0, wr = S::stages - 1, left = n;
+  bool first = true;
+  while (left > 0) {
+    const int head0 = at.u / a.groups * a.rep + at.u % a.groups * a.heads;
+    const int rows = min(a.heads, a.rep - at.u % a.groups * a.heads);
+    // the queries as B fragments (INT8: channels in the order the codes are read)
+    uint32_t qf[kD / 16][NH][2];
+    float qsum[NH][2][2] = {};
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int ks = 0; ks < kD / 16; ++ks)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int ch = S::q8 ? 64 * (ks >> 2) + 16 * t + 4 * (ks & 3) + 2 * j : 16 * ks + 8 * j + 2 * t;
+          uint32_t x = 0;
+          if (nh * 8 + g < rows)
+            x = *reinterpret_cast<const uint32_t*>(a.q + (static_cast<size_t>(at.b) * a.Hq + head0 + nh * 8 + g) * kD + ch);
+          qf[ks][nh][j] = x;
+          if (S::q8) {
+            const __half2 x2 = *reinterpret_cast<const __half2*>(&x);
+            sum[ks >> 2] += __low2float(x2) + __high2float(x2);
+          }
+        }
+      if (S::q8) {
+#pragma unroll
+        for (int grp = 0; grp < 2; ++grp) {
+          float x = sum[grp];   // of head g, this lane's channels
+          x += __shfl_xor_sync(0xffffffffu, x, 1);
+          x += __shfl_xor_sync(0xffffffffu, x, 2);
+          qsum[nh][0][grp] = __shfl_sync(0xffffffffu, x, 8 * t);       // heads 2t, 2t + 1
+          qsum[nh][1][grp] = __shfl_sync(0xffffffffu, x, 8 * t + 4);
+        }
+      }
+    }
+    Acc<NH> acc;
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+#pragma unroll
+      for (int mt = 0; mt < kD / 16; ++mt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc.o[mt][nh][j] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        acc.m[nh][j] = -INFINITY;
+        acc.l[nh][j] = acc.z[nh][j][0] = acc.z[nh][j][1] = 0.f;
+      }
+    }
+    const int count = min(at.tiles - at.t, left);
+    for (int i = 0; i < count; ++i) {
+      cp_async_wait<S::stages - 2>();
+      __syncwarp();   // the tile has landed for all lanes, and the one to be refilled is read
+      if (left - i > S::stages - 1) issue<TYPE>(p, lrow, ring + wr * S::stage, next, policy);
+      cp_async_commit();
+      next = find();
+      consume<TYPE, NH>(ring + rd * S::stage, qf, qsum, a.scale, acc);
+      rd = rd + 1 == S::stages ? 0 : rd + 1;
+      wr = wr + 1 == S::stages ? 0 : wr + 1;
+    }
+    const bool whole = count == at.tiles;
+    store_unit<TYPE, NH>(a, at.b, at.u, acc, whole ? nullptr : a.part + (static_cast<size_t>(c) * 2 + (first ? 0 : 1)) * kPartFloats);
+    first = false;
+    left -= count;
+    if (left > 0) next_unit<TYPE>(a, at);
+  }
+}
+
+// CTA (unit, row b): joins the parts of a unit that several warps held, in their order, and
+// answers for the units without a visible slot.  A warp per query head, four channels a lane.
 template <int TYPE>
-__global__ void __launch_bounds__(kPaThreads) paged_merge_kernel(const AttendArgs a, int grid) {
+__global__ void __launch_bounds__(kPaThreads) paged_merge_kernel(const AttendArgs a, int warps) {
   using S = Shape<TYPE>;
   __shared__ int64_t warp_sums[kPaWarps];
-  const int units = a.p.Hkv * a.groups, b = blockIdx.y, u = blockIdx.x, tid = threadIdx.x;
-  const int h = u / a.groups, head0 = h * a.rep + (u % a.groups) * a.heads;
-  const int rows = min(a.heads, a.rep - (u % a.groups) * a.heads);
+  const int units = a.p.Hkv * a.groups, b = blockIdx.y, u = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  const int rows = min(a.heads, a.rep - u % a.groups * a.heads);
   int64_t mine = 0, below = 0, total, base;
   for (int i = tid; i < a.n; i += kPaThreads) {
-    const int x = row_tiles<S::tile>(a, i);
+    const int x = row_tiles<S::tw>(a, i);
     mine += x;
     if (i < b) below += x;
   }
   scan64(mine * units, warp_sums, total);
   scan64(below * units, warp_sums, base);
-  const int tiles = row_tiles<S::tile>(a, b);
-  pdl_wait();
-  const size_t at = static_cast<size_t>(b) * a.Hq + head0;
-  if (tiles == 0) {
-    for (int row = 0; row < rows; ++row) {
-      a.out[(at + row) * kD + tid] = 0;
-      if (tid == 0 && a.lse) a.lse[at + row] = -INFINITY;
-    }
-    return;
-  }
-  const int workers = workers_of(total, grid);
+  const int tiles = row_tiles<S::tw>(a, b);
+  const int workers = workers_of(total, warps);
   const int64_t first = base + static_cast<int64_t>(u) * tiles;
-  const int c0 = split_owner(total, workers, first), c1 = split_owner(total, workers, first + tiles - 1);
-  if (c0 == c1) return;
-  const int skip = split_begin(total, workers, c0) < first ? 1 : 0;   // c0 holds it as its second part
-  const float* p0 = a.part + (static_cast<size_t>(c0) * 2 + skip) * kPartFloats;
-  for (int row = 0; row < rows; ++row) {
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-      const float* q = c == c0 ? p0 : a.part + static_cast<size_t>(c) * 2 * kPartFloats;
-      const float mc = q[kPaRows * kD + row], lc = q[kPaRows * kD + kPaRows + row], oc = q[row * kD + tid];
-      const float mn = fmaxf(m, mc), sub = mn == -INFINITY ? 0.f : mn;
-      const float f = ex2(m - sub), fc = ex2(mc - sub);
-      l = l * f + lc * fc;
-      o = o * f + oc * fc;
-      m = mn;
+  const int c0 = tiles ? split_owner(total, workers, first) : 0, c1 = tiles ? split_owner(total, workers, first + tiles - 1) : 0;
+  pdl_wait();
+  if (tiles > 0 && c0 == c1) return;   // finished by its warp
+  const int skip = tiles && split_begin(total, workers, c0) < first ? 1 : 0;   // c0 holds it as its second part
+  for (int row = tid >> 5; row < rows; row += kPaWarps) {
+    const size_t at = static_cast<size_t>(b) * a.Hq + u / a.groups * a.rep + u % a.groups * a.heads + row;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (tiles > 0) {
+#pragma unroll 4
+      for (int c = c0; c <= c1; ++c) {
+        const float* q = a.part + (static_cast<size_t>(c) * 2 + (c == c0 ? skip : 0)) * kPartFloats;
+        const float mc = q[kPaRows * kD + row], lc = q[kPaRows * kD + kPaRows + row];
+        const float4 oc = reinterpret_cast<const float4*>(q + row * kD)[lane];
+        const float mn = fmaxf(m, mc), sub = mn == -INFINITY ? 0.f : mn;
+        const float f = ex2(m - sub), fc = ex2(mc - sub);
+        l = l * f + lc * fc;
+        o = make_float4(o.x * f + oc.x * fc, o.y * f + oc.y * fc, o.z * f + oc.z * fc, o.w * f + oc.w * fc);
+        m = mn;
+      }
     }
-    a.out[(at + row) * kD + tid] = to_out<TYPE>(l == 0.f ? 0.f : o / l);
-    if (tid == 0 && a.lse) a.lse[at + row] = lse_of<TYPE>(m, l);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint2*>(a.out + at * kD + 4 * lane) =
+        make_uint2(static_cast<uint32_t>(to_out<TYPE>(o.x * inv)) | static_cast<uint32_t>(to_out<TYPE>(o.y * inv)) << 16,
+                   static_cast<uint32_t>(to_out<TYPE>(o.z * inv)) | static_cast<uint32_t>(to_out<TYPE>(o.w * inv)) << 16);
+    if (lane == 0 && a.lse) a.lse[at] = lse_of<TYPE>(m, l);
   }
 }
 
-// CTAs of the split: two per SM, or one per tile where that is fewer.
+// CTAs of the split: two per SM, or as many as give every tile a warp where that is fewer.
 int grid_of(const mikv_pages* p, int n, int Hq, int window, int sinks) {
-  const int tile = p->type == MIKV_PAGES_INT8 ? Shape<MIKV_PAGES_INT8>::tile : Shape<MIKV_PAGES_FP16>::tile;
+  const int tile = p->type == MIKV_PAGES_INT8 ? Shape<MIKV_PAGES_INT8>::tw : Shape<MIKV_PAGES_FP16>::tw;
   const int rep = Hq / p->Hkv, groups = (rep + kPaRows - 1) / kPaRows;
   int64_t slots = static_cast<int64_t>(p->max_pages) * p->page_size;
   if (window > 0) slots = std::min(slots, static_cast<int64_t>(window) + sinks);
@@ -630,14 +692,14 @@ int grid_of(const mikv_pages* p, int n, int Hq, int window, int sinks) {
   return static_cast<int>(std::max<int64_t>(1, std::min(most, tiles * n * p->Hkv * groups)));
 }
 
-template <int TYPE, bool WIDE>
+template <int TYPE, int NH>
 int launch(const AttendArgs& a, int grid, cudaStream_t st) {
-  const auto kern = paged_partial_kernel<TYPE, WIDE>;
+  const auto kern = paged_partial_kernel<TYPE, NH>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<TYPE>::smem);
   if (e != cudaSuccess) return check_launch_after(e, "paged_partial_kernel");
   kern<<<grid, kPaThreads, Shape<TYPE>::smem, st>>>(a);
   if (int r = check_launch("paged_partial_kernel")) return r;
-  return check_launch_after(launch_after(paged_merge_kernel<TYPE>, dim3(a.p.Hkv * a.groups, a.n), dim3(kPaThreads), 0, st, a, grid),
+  return check_launch_after(launch_after(paged_merge_kernel<TYPE>, dim3(a.p.Hkv * a.groups, a.n), dim3(kPaThreads), 0, st, a, grid * kPaWarps),
                             "paged_merge_kernel");
 }
 
@@ -649,7 +711,7 @@ using namespace mikv;
 extern "C" size_t mikv_paged_attention_workspace_bytes(const mikv_pages* p, int n, int Hq, int window, int sinks) {
   Pool pool;
   if (check_pages(p, "paged_attention", &pool) || n < 1 || n > 65535 || Hq < 1 || Hq % p->Hkv || window < 0 || sinks < 0) return 0;
-  return static_cast<size_t>(grid_of(p, n, Hq, window, sinks)) * 2 * kPartFloats * sizeof(float);
+  return static_cast<size_t>(grid_of(p, n, Hq, window, sinks)) * kPaWarps * 2 * kPartFloats * sizeof(float);
 }
 
 extern "C" int mikv_paged_attention(const void* q, const mikv_pages* pages, int layer, const int32_t* seqs, int n, int Hq,
@@ -665,7 +727,7 @@ extern "C" int mikv_paged_attention(const void* q, const mikv_pages* pages, int 
   if (!q || !out || !ws) return fail(MIKV_EINVAL, "paged_attention: null pointer");
   if (!aligned16(q) || !aligned16(out) || !aligned16(ws)) return fail(MIKV_EALIGN, "paged_attention: 16-byte alignment");
   const int grid = grid_of(pages, n, Hq, window, sinks);
-  const size_t need = static_cast<size_t>(grid) * 2 * kPartFloats * sizeof(float);
+  const size_t need = static_cast<size_t>(grid) * kPaWarps * 2 * kPartFloats * sizeof(float);
   if (ws_bytes < need) return fail(MIKV_ESHAPE, "paged_attention: workspace %zu < %zu", ws_bytes, need);
   a.q = static_cast<const uint16_t*>(q);
   a.seqs = seqs;
@@ -684,8 +746,8 @@ extern "C" int mikv_paged_attention(const void* q, const mikv_pages* pages, int 
   const cudaStream_t st = as_stream(stream);
   const bool wide = a.heads > 8;
   switch (a.p.type) {
-    case MIKV_PAGES_FP16: return wide ? launch<MIKV_PAGES_FP16, true>(a, grid, st) : launch<MIKV_PAGES_FP16, false>(a, grid, st);
-    case MIKV_PAGES_BF16: return wide ? launch<MIKV_PAGES_BF16, true>(a, grid, st) : launch<MIKV_PAGES_BF16, false>(a, grid, st);
-    default: return wide ? launch<MIKV_PAGES_INT8, true>(a, grid, st) : launch<MIKV_PAGES_INT8, false>(a, grid, st);
+    case MIKV_PAGES_FP16: return wide ? launch<MIKV_PAGES_FP16, 2>(a, grid, st) : launch<MIKV_PAGES_FP16, 1>(a, grid, st);
+    case MIKV_PAGES_BF16: return wide ? launch<MIKV_PAGES_BF16, 2>(a, grid, st) : launch<MIKV_PAGES_BF16, 1>(a, grid, st);
+    default: return wide ? launch<MIKV_PAGES_INT8, 2>(a, grid, st) : launch<MIKV_PAGES_INT8, 1>(a, grid, st);
   }
 }
