@@ -524,11 +524,15 @@ size_t mikv_paged_attention_workspace_bytes(const mikv_pages* p, int n, int Hq, 
  * (stride 0), rows of q, k, v along T and all rows of out are apart; B == 0 does nothing.
  * The softmax weights are rounded to the inputs' type before they meet the values; sums and
  * statistics are fp32.
+ * ws >= mikv_window_attention_workspace_bytes(B, Hq, Hkv, Tq, Tk, window, sinks), 32-byte
+ * aligned: sums of calls with few query rows, whose keys are split over the SMs (0 bytes, and
+ * ws may be NULL, otherwise); two calls must not share a workspace concurrently.
  * Errors: EINVAL (null, type, window, sinks), ESHAPE, EALIGN, EUNSUPPORTED (D), ECUDA.
  */
 int mikv_window_attention(const mikv_rows* q, const mikv_rows* k, const mikv_rows* v, int B, int Hq, int Hkv, int Tq, int Tk,
                           int D, int type, const int32_t* q_lens, const int32_t* k_lens, int window, int sinks,
-                          const mikv_rows* out, float* lse, void* stream);
+                          const mikv_rows* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+size_t mikv_window_attention_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk, int window, int sinks);
 
 /*
  * Measurement hook (no counterpart in the papers): while set, every

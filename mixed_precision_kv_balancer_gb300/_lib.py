@@ -31,7 +31,8 @@ EXPORTS = (
     "mikv_channel_quantize",
     "mikv_page_reserve", "mikv_page_fork", "mikv_page_free", "mikv_page_copy", "mikv_page_compact",
     "mikv_page_workspace_bytes", "mikv_paged_append", "mikv_paged_gather",
-    "mikv_paged_attention", "mikv_paged_attention_workspace_bytes", "mikv_window_attention",
+    "mikv_paged_attention", "mikv_paged_attention_workspace_bytes",
+    "mikv_window_attention", "mikv_window_attention_workspace_bytes",
     "mikv_set_attention_events", "mikv_wait_status", "mikv_wait_probe", "mikv_last_error",
 )
 
@@ -115,7 +116,8 @@ def load() -> ctypes.CDLL:
         "mikv_paged_gather": (I, [GP, I, P, I, I, RP, RP, P]),
         "mikv_paged_attention": (I, [P, GP, I, P, I, I, I, I, P, P, P, S, P]),
         "mikv_paged_attention_workspace_bytes": (S, [GP, I, I, I, I]),
-        "mikv_window_attention": (I, [RP, RP, RP, I, I, I, I, I, I, I, P, P, I, I, RP, P, P]),
+        "mikv_window_attention": (I, [RP, RP, RP, I, I, I, I, I, I, I, P, P, I, I, RP, P, P, S, P]),
+        "mikv_window_attention_workspace_bytes": (S, [I, I, I, I, I, I, I]),
         "mikv_set_attention_events": (I, [P, P]),
         "mikv_wait_status": (I, [ctypes.POINTER(ctypes.c_uint), I]),
         "mikv_wait_probe": (I, [ctypes.c_int64, I, P]),
@@ -383,7 +385,7 @@ def mikv_paged_attention(q, pages, layer, window, sinks, out, lse=None, seqs=Non
             _need(lse, "lse", torch.float32, (n, Hq), dev), w, nb)
 
 
-def mikv_window_attention(q, k, v, window, sinks, out, lse=None, q_lens=None, k_lens=None, stream=None):
+def mikv_window_attention(q, k, v, window, sinks, out, lse=None, q_lens=None, k_lens=None, ws=None, stream=None):
     """A prompt's or a chunk's attention: q, out [B][Hq][Tq][D], k, v [B][Hkv][Tk][D] (strided; all fp16 or
     all bf16), lse fp32 [B][Hq][Tq], q_lens, k_lens int32 [B] (None: Tq, Tk)."""
     lib, dev, dt = load(), q.device, q.dtype
@@ -392,11 +394,12 @@ def mikv_window_attention(q, k, v, window, sinks, out, lse=None, q_lens=None, k_
     if not q.is_cuda or dt not in (torch.float16, torch.bfloat16):
         raise ValueError(f"q: expected fp16 or bf16 on a CUDA device, got {dt} on {dev}")
     qs, ks = (B, Hq, Tq, D), (B, Hkv, Tk, D)
+    w, nb, _keep = _ws_on(lambda: lib.mikv_window_attention_workspace_bytes(B, Hq, Hkv, Tq, Tk, window, sinks), dev, ws)
     _launch(dev, stream, lib.mikv_window_attention, _rows(q, "q", dt, qs, dev), _rows(k, "k", dt, ks, dev),
             _rows(v, "v", dt, ks, dev), B, Hq, Hkv, Tq, Tk, D,
             MIKV_PAGES_BF16 if dt is torch.bfloat16 else MIKV_PAGES_FP16, _need(q_lens, "q_lens", torch.int32, (B,), dev),
             _need(k_lens, "k_lens", torch.int32, (B,), dev), window, sinks, _rows(out, "out", dt, qs, dev),
-            _need(lse, "lse", torch.float32, (B, Hq, Tq), dev))
+            _need(lse, "lse", torch.float32, (B, Hq, Tq), dev), w, nb)
 
 
 def mikv_set_attention_events(begin=None, end=None):

@@ -7,9 +7,11 @@
 // per visible query-key pair) and, close behind, by the exponentials.
 //
 // A CTA holds two tiles of 128 query rows over one key head: the same rows of two heads of the
-// group, or 256 rows of one head where the group is odd.  Key and value tiles of 128 rows come
-// through a ring of five 32 KB buffers (TMA, 128-byte swizzle); tiles that none of the rows sees
-// are not read.  Per key tile i and query tile t
+// group, or 256 rows of one head where the group is odd.  Where a chunk has 64 rows or fewer, a
+// tile packs the rows of several heads of the group.  Where the items of a call leave SMs idle,
+// each is split over its key tiles and the parts are joined by a second kernel.  Key and value
+// tiles of 128 rows come through a ring of five 32 KB buffers (TMA, 128-byte swizzle); tiles
+// that none of the rows sees are not read.  Per key tile i and query tile t
 //   S_t = Q_t K_i^T     tcgen05, both operands in shared memory, 128 fp32 TMEM columns
 //   P_t = exp2(...)     four warps, one query row a thread, written over S_t as 16-bit pairs
 //   O_t += P_t V_i      tcgen05, P from TMEM, V as it lies (rows are the contraction)
@@ -55,9 +57,13 @@ struct Weights {
 struct WindowArgs {
   RowView out;
   float* lse;
+  float* part;                   // splits > 1: [splits][B Hq Tq][128] sums, then [splits][B Hq Tq] (maximum, sum)
   const int32_t *q_lens, *k_lens;
   int Hq, rep, Tq, Tk, window, sinks, blocks;
-  bool pair_heads;               // the CTA's tiles are two heads' rows, else 256 rows of one head
+  int64_t rows;                  // B Hq Tq
+  int tb, hb, groups;            // a tile: tb rows of each of hb heads; groups = ceil(rep / hb)
+  int splits;
+  bool pair_heads;               // the CTA's tiles are two groups of heads, else two row blocks of one
   bool wide_out;                 // rows of out begin at multiples of 32 bytes
   int qb, qh, kb, kh, vb, vh;    // 1, or 0 where the view repeats one batch row or head
   float scale;                   // log2(e) / sqrt(D)
@@ -79,9 +85,11 @@ __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, 
 // What one CTA works on; every warp computes it alike.
 struct Work {
   int ql, kl, off;        // lengths; position of query 0
-  int head[2], q0[2];     // per tile: head and first row
+  int split;
+  int group[2], q0[2];    // per tile: group of heads and first row
   int pa[2], pb[2];       // positions of its first and last row
-  int tiles, ts, tw0;     // key tiles: ts of the sinks, then tw0, tw0 + 1, ...
+  int begin, end;         // the item's key tiles: of ts of the sinks, then tw0, tw0 + 1, ...
+  int ts, tw0;
   int from[2], last[2];   // query tile t sees the sinks' key tiles and tiles from .. last; last -1: none
   int nt;                 // query tiles
   __device__ __forceinline__ int j0(int i) const { return (i < ts ? i : tw0 + i - ts) * kWaRows; }
@@ -89,40 +97,51 @@ struct Work {
 // One query tile of it, in registers (an array indexed by a warp's number would not be).
 struct Tile {
   bool live;
-  int head, q0, pa, pb, from, last;
+  int group, q0, pa, pb, from, last;
   // Whether any of its rows sees key tile i.
   __device__ __forceinline__ bool sees(int i, int ts) const { return i <= last && (i < ts || i >= from); }
 };
 __device__ __forceinline__ Tile tile_of(const Work& w, int t) {
-  return {t < w.nt, t ? w.head[1] : w.head[0], t ? w.q0[1] : w.q0[0], t ? w.pa[1] : w.pa[0], t ? w.pb[1] : w.pb[0],
+  return {t < w.nt, t ? w.group[1] : w.group[0], t ? w.q0[1] : w.q0[0], t ? w.pa[1] : w.pa[0], t ? w.pb[1] : w.pb[0],
           t ? w.from[1] : w.from[0], t ? w.last[1] : w.last[0]};
 }
-__device__ __forceinline__ Work work_of(const WindowArgs& a, int b, int hk, int x) {
+template <bool SPLIT>
+__device__ __forceinline__ Work work_of(const WindowArgs& a, int b, int x) {
   Work w;
   w.ql = a.q_lens ? min(max(uniform(a.q_lens[b]), 0), a.Tq) : a.Tq;
   w.kl = a.k_lens ? min(max(uniform(a.k_lens[b]), 0), a.Tk) : a.Tk;
   w.off = w.kl - w.ql;
-  const int per = a.pair_heads ? a.rep / 2 : a.rep;       // CTAs of one row block
-  const int blk = a.blocks - 1 - x / per, u = x % per;    // the last rows, which see the most, first
+  w.split = SPLIT ? x % a.splits : 0;
+  if (SPLIT) x /= a.splits;
+  const int per = a.pair_heads ? (a.groups + 1) / 2 : a.groups;   // items of one row block
+  const int blk = a.blocks - 1 - x / per, u = x % per;            // the last rows, which see the most, first
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    w.head[t] = hk * a.rep + (a.pair_heads ? 2 * u + t : u);
-    w.q0[t] = a.pair_heads ? blk * kWaRows : (2 * blk + t) * kWaRows;
+    w.group[t] = a.pair_heads ? 2 * u + t : u;
+    w.q0[t] = a.pair_heads ? blk * a.tb : (2 * blk + t) * a.tb;
     w.pa[t] = w.off + w.q0[t];
-    w.pb[t] = w.off + min(w.q0[t] + kWaRows, w.ql) - 1;
+    w.pb[t] = w.off + min(w.q0[t] + a.tb, w.ql) - 1;
   }
-  w.nt = w.q0[0] >= w.ql ? 0 : w.q0[1] >= w.ql ? 1 : 2;
+  w.nt = w.q0[0] >= w.ql ? 0 : w.q0[1] >= w.ql || w.group[1] >= a.groups ? 1 : 2;
   const int p1 = w.nt == 2 ? w.pb[1] : w.pb[0];           // the largest position (tile 1's rows are not below tile 0's)
   const int lo = a.window > 0 ? max(w.pa[0] - a.window + 1, 0) : 0;
   const int end = p1 < 0 ? 0 : p1 / kWaRows + 1;
   w.tw0 = min(lo / kWaRows, end);
   w.ts = a.window > 0 ? min((min(a.sinks, w.kl) + kWaRows - 1) / kWaRows, w.tw0) : 0;
-  w.tiles = w.ts + end - w.tw0;
+  const int tiles = w.ts + end - w.tw0;
+  w.begin = SPLIT ? static_cast<int>(static_cast<int64_t>(tiles) * w.split / a.splits) : 0;
+  w.end = SPLIT ? static_cast<int>(static_cast<int64_t>(tiles) * (w.split + 1) / a.splits) : tiles;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int e = w.pb[t] < 0 ? -1 : w.pb[t] / kWaRows;
-    w.last[t] = t >= w.nt || e < 0 ? -1 : e - w.tw0 + w.ts;
     w.from[t] = w.ts + (a.window > 0 ? max(w.pa[t] - a.window + 1, 0) / kWaRows - w.tw0 : 0);
+    int last = t >= w.nt || e < 0 ? -1 : e - w.tw0 + w.ts;
+    if (SPLIT) {   // the last one of this part
+      last = min(last, w.end - 1);
+      if (last < w.from[t]) last = min(last, w.ts - 1);
+      if (last < w.begin) last = -1;
+    }
+    w.last[t] = last;
   }
   return w;
 }
@@ -193,8 +212,8 @@ __device__ __forceinline__ void st_global32(void* p, const uint32_t* r) {
                : "memory");
 }
 
-// One thread: rows [row0, row0 + 128) of one (head, batch row) into the tile at `s`, two boxes of
-// 64 channels; rows past the end are zero-filled.  Completes 32 KB on the mbarrier.
+// One thread: rows row0 .. of one (head, batch row) into the tile at `s`, two boxes of 64
+// channels; rows past the end are zero-filled.  Completes the boxes' bytes on the mbarrier.
 __device__ __forceinline__ void tma_rows(uint32_t s, const CUtensorMap* map, int row0, int h, int b, uint32_t mbar) {
 #pragma unroll
   for (int j = 0; j < 2; ++j)
@@ -202,6 +221,17 @@ __device__ __forceinline__ void tma_rows(uint32_t s, const CUtensorMap* map, int
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(s + j * tc::kKBlock),
         "l"(map), "r"(j * 64), "r"(row0), "r"(h), "r"(b), "r"(mbar)
+        : "memory");
+}
+
+// The same for a query tile: tb rows of hb heads from head h of the group of key head hk.
+__device__ __forceinline__ void tma_queries(uint32_t s, const CUtensorMap* map, int row0, int h, int hk, int b, uint32_t mbar) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n" ::"r"(s + j * tc::kKBlock),
+        "l"(map), "r"(j * 64), "r"(row0), "r"(h), "r"(hk), "r"(b), "r"(mbar)
         : "memory");
 }
 
@@ -343,7 +373,7 @@ __device__ __forceinline__ bool next_item(WaBars& bar, const uint4* answers, int
   return __all_sync(0xffffffffu, ok != 0 && wait.ok);
 }
 
-template <bool BF>
+template <bool BF, bool SPLIT>
 __global__ void __launch_bounds__(kWaThreads, 1)
     window_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                             const __grid_constant__ CUtensorMap vmap, const WindowArgs a) {
@@ -376,6 +406,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = uniform(tslot);
+  if (SPLIT) pdl_trigger();   // the joining kernel may be placed; it waits for this one's end
   const uint32_t sq = tc::smem_base(smem), ring = sq + 2 * tc::kTileBytes;
   tc::Waits wait;
   Item it = {static_cast<int>(blockIdx.x), static_cast<int>(blockIdx.y), static_cast<int>(blockIdx.z)};
@@ -384,16 +415,17 @@ __global__ void __launch_bounds__(kWaThreads, 1)
     int slot = 0, par = 1, qs = 0;   // ring position; parity that an empty buffer shows; query loads
     for (int n = 0;; ++n) {
       const int b = it.z, hk = it.y;
-      const Work w = work_of(a, b, hk, it.x);
-      if (w.nt > 0 && w.tiles > 0) {
+      const Work w = work_of<SPLIT>(a, b, it.x);
+      if (w.nt > 0 && w.begin < w.end) {
         if (qs > 0) wait(smem_u32(&bar.qfree), (qs - 1) & 1);
         ++qs;
         if (lane == 0 && wait.ok) {
-          tc::mbar_expect_tx(smem_u32(&bar.q), w.nt * tc::kTileBytes);
-          tma_rows(sq, &qmap, w.q0[0], w.head[0] * a.qh, b * a.qb, smem_u32(&bar.q));
-          if (w.nt == 2) tma_rows(sq + tc::kTileBytes, &qmap, w.q0[1], w.head[1] * a.qh, b * a.qb, smem_u32(&bar.q));
+          tc::mbar_expect_tx(smem_u32(&bar.q), w.nt * a.tb * a.hb * kD * 2);
+          tma_queries(sq, &qmap, w.q0[0], w.group[0] * a.hb * a.qh, hk * a.qh, b * a.qb, smem_u32(&bar.q));
+          if (w.nt == 2)
+            tma_queries(sq + tc::kTileBytes, &qmap, w.q0[1], w.group[1] * a.hb * a.qh, hk * a.qh, b * a.qb, smem_u32(&bar.q));
         }
-        for (int c = 0; c < 2 * w.tiles; ++c) {   // keys of key tile c / 2 (c even), then its values
+        for (int c = 2 * w.begin; c < 2 * w.end; ++c) {   // keys of key tile c / 2 (c even), then its values
           const int j0 = w.j0(c >> 1);
           const uint32_t dst = ring + slot * tc::kTileBytes, full = smem_u32(&bar.full[slot]);
           wait(smem_u32(&bar.empty[slot]), par);
@@ -461,19 +493,19 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       ++turn;
     };
     for (int n = 0;; ++n) {
-      const Work w = work_of(a, it.z, it.y, it.x);
-      if (w.nt > 0 && w.tiles > 0) {
+      const Work w = work_of<SPLIT>(a, it.z, it.x);
+      if (w.nt > 0 && w.begin < w.end) {
         const Tile tile = tile_of(w, t);
         bool more = false, before = false, clear = false;
         int vslot = 0, vpar = 0;     // the last step's values
         wait(smem_u32(&bar.q), q_par);
         q_par ^= 1;
         // after a wait that gave up no lane leads, nothing more is issued, and the others' waits run out
-        for (int i = 0; i <= w.tiles; ++i) {
+        for (int i = w.begin; i <= w.end; ++i) {
           // this step's scores from key tile i, behind the last step's sums over value tile i - 1
-          const bool keys = i < w.tiles, here = keys && tile.sees(i, w.ts);
+          const bool keys = i < w.end, here = keys && tile.sees(i, w.ts);
           const uint64_t kd = k0 + slot * desc_step(tc::kTileBytes), vd = v0 + vslot * desc_step(tc::kTileBytes);
-          if (i > 0) {
+          if (i > w.begin) {
             wait(smem_u32(&bar.full[vslot]), vpar);
             if (clear) {
               wait(smem_u32(&bar.fix[vslot]), (fixed >> vslot) & 1);
@@ -522,9 +554,9 @@ __global__ void __launch_bounds__(kWaThreads, 1)
           }
           before = here;
           if (lead) {
-            if (i > 0) tc::commit(smem_u32(&bar.empty[vslot]));
+            if (i > w.begin) tc::commit(smem_u32(&bar.empty[vslot]));
             if (keys) tc::commit(smem_u32(&bar.empty[slot]));
-            if (i == w.tiles - 1) tc::commit(smem_u32(&bar.qfree));   // the last scores
+            if (i == w.end - 1) tc::commit(smem_u32(&bar.qfree));   // the last scores
           }
           if (keys) {   // the values of tile i follow its keys in the ring
             clear = hidden_rows(a, w, w.j0(i)).any();
@@ -545,12 +577,12 @@ __global__ void __launch_bounds__(kWaThreads, 1)
     int s_par = 0, o_par = 0;
     for (int n = 0;; ++n) {
       const int b = it.z;
-      const Work w = work_of(a, b, it.y, it.x);
+      const Work w = work_of<SPLIT>(a, b, it.x);
       const Tile tile = tile_of(w, t);
       if (tile.live) {
-        const int p = tile.pa + row;
+        const int p = tile.pa + row % a.tb;
         Row r;
-        for (int i = 0; i < w.tiles; ++i) {
+        for (int i = w.begin; i < w.end; ++i) {
           if (!tile.sees(i, w.ts)) continue;
           const int j0 = w.j0(i);
           wait(smem_u32(&bar.s[t]), s_par);
@@ -563,10 +595,13 @@ __global__ void __launch_bounds__(kWaThreads, 1)
           o_par ^= 1;
         }
         tc::fence_after_sync();
-        const int q = tile.q0 + row;
-        float inv = r.l == 0.f ? 0.f : 1.f / r.l;
+        const int sub = row / a.tb, q = tile.q0 + row - sub * a.tb, h = tile.group * a.hb + sub;   // the row's query and head
+        const bool write = sub < a.hb && h < a.rep && q < w.ql;
+        const int head = it.y * a.rep + h;
+        const int64_t at = (static_cast<int64_t>(b) * a.Hq + head) * a.Tq + q;
+        float inv = SPLIT ? 1.f : r.l == 0.f ? 0.f : 1.f / r.l;
         if (!wait.ok) inv = __int_as_float(0x7fffffff);
-        uint8_t* dst = a.out.row(b, tile.head, q);
+        uint8_t* dst = !SPLIT ? a.out.row(b, head, q) : reinterpret_cast<uint8_t*>(a.part + (w.split * a.rows + at) * kD);
 #pragma unroll 1
         for (int c = 0; c < kD; c += 32) {
           float o[32];
@@ -577,22 +612,32 @@ __global__ void __launch_bounds__(kWaThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0.f;
           }
-          if (q < w.ql) {
-            uint32_t u[16];
+          if (write) {
+            uint32_t u[32];
+            if (!SPLIT) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) u[e] = pack2<BF>(o[2 * e] * inv, o[2 * e + 1] * inv);
-            if (a.wide_out) {
-              st_global32(dst + c * 2, u);
-              st_global32(dst + c * 2 + 32, u + 8);
-            } else {
+              for (int e = 0; e < 16; ++e) u[e] = pack2<BF>(o[2 * e] * inv, o[2 * e + 1] * inv);
+              if (a.wide_out) {
+                st_global32(dst + c * 2, u);
+                st_global32(dst + c * 2 + 32, u + 8);
+              } else {
 #pragma unroll
-              for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(dst + (c + 2 * e) * 2) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+                for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(dst + (c + 2 * e) * 2) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+              }
+            } else if (tile.last >= 0) {   // a part without a visible key is told by its sum of 0
+#pragma unroll
+              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * inv);
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) st_global32(dst + (c + e) * 4, u + e);
             }
           }
         }
-        if (q < w.ql && a.lse) {
+        if (SPLIT && write) {
+          float2* ml = reinterpret_cast<float2*>(a.part + a.splits * a.rows * kD);
+          ml[w.split * a.rows + at] = make_float2(r.m * a.scale, wait.ok ? r.l : inv);
+        } else if (!SPLIT && write && a.lse) {
           const float v = r.l == 0.f ? -INFINITY : (r.m * a.scale + (log2f(r.l) - Weights<BF>::shift)) * 0.6931471805599453f;
-          a.lse[(static_cast<int64_t>(b) * a.Hq + tile.head) * a.Tq + q] = wait.ok ? v : inv;
+          a.lse[at] = wait.ok ? v : inv;
         }
         tc::fence_before_sync();   // the sums are read before the next item's products overwrite them
       }
@@ -604,6 +649,63 @@ __global__ void __launch_bounds__(kWaThreads, 1)
   __syncthreads();
   if (warp == kWaMmaWarp) tc::tmem_dealloc(tmem, kWaCols);
 }
+
+// Joins the parts of one query row: a warp per row, four channels a lane.
+template <bool BF>
+__global__ void __launch_bounds__(128) window_join_kernel(const WindowArgs a) {
+  pdl_wait();
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (at >= a.rows) return;
+  const int lane = threadIdx.x & 31;
+  const int q = static_cast<int>(at % a.Tq), head = static_cast<int>(at / a.Tq % a.Hq), b = static_cast<int>(at / a.Tq / a.Hq);
+  if (a.q_lens && q >= min(max(a.q_lens[b], 0), a.Tq)) return;
+  const float2* ml = reinterpret_cast<const float2*>(a.part + a.splits * a.rows * kD) + at;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < a.splits; ++s) {
+    const float2 x = ml[s * a.rows];
+    if (x.y == 0.f) continue;   // nothing seen there, and no sums written
+    const float4 os = reinterpret_cast<const float4*>(a.part + (s * a.rows + at) * kD)[lane];
+    const float mn = fmaxf(m, x.x), sub = mn == -INFINITY ? 0.f : mn;
+    const float f = ex2(m - sub), fs = ex2(x.x - sub);
+    l = l * f + x.y * fs;
+    o = make_float4(o.x * f + os.x * fs, o.y * f + os.y * fs, o.z * f + os.z * fs, o.w * f + os.w * fs);
+    m = mn;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<uint2*>(a.out.row(b, head, q) + lane * 8) = make_uint2(pack2<BF>(o.x * inv, o.y * inv), pack2<BF>(o.z * inv, o.w * inv));
+  if (lane == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + (log2f(l) - Weights<BF>::shift)) * 0.6931471805599453f;
+}
+
+// The split of a call: rows and heads of a tile, items, and parts of each item.
+struct Plan {
+  int tb, hb, groups, blocks, splits;
+  bool pair_heads;
+  int64_t per_head;   // items of one key head and batch row, without the splits
+};
+// `pack`: heads of a group may share a tile (their rows are apart in memory).
+Plan plan_of(int B, int Hq, int Hkv, int Tq, int Tk, int window, int sinks, bool pack) {
+  Plan p;
+  const int rep = Hq / Hkv;
+  p.hb = pack ? std::min(rep, std::max(1, kWaRows / Tq)) : 1;
+  p.tb = p.hb > 1 ? Tq : kWaRows;
+  p.groups = (rep + p.hb - 1) / p.hb;
+  const int blocks = (Tq + p.tb - 1) / p.tb;
+  p.pair_heads = p.groups % 2 == 0 || blocks == 1;
+  p.blocks = p.pair_heads ? blocks : (blocks + 1) / 2;
+  p.per_head = static_cast<int64_t>(p.blocks) * (p.pair_heads ? (p.groups + 1) / 2 : p.groups);
+  // Parts of an item, where the items would leave half the SMs idle or more: as many as fill them
+  // once, two key tiles each at least.  A part costs its sums' way through memory, 64 KB a tile
+  // out and in, about what two key tiles take.
+  const int64_t items = p.per_head * Hkv * B;
+  int64_t keys = Tk;
+  if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + sinks + (p.pair_heads ? 1 : 2) * p.tb);
+  const int64_t tiles = (keys + kWaRows - 1) / kWaRows;
+  p.splits = static_cast<int>(std::max<int64_t>(1, std::min(kNumSMs / items, tiles / 2)));
+  return p;
+}
+size_t part_bytes(const Plan& p, int64_t rows) { return p.splits > 1 ? static_cast<size_t>(p.splits) * rows * (kD + 2) * 4 : 0; }
+bool packs(const mikv_rows& q, int Hq) { return Hq == 1 || q.stride_h >= kD; }
 
 // 4-D tensor map (channel, row, head, batch row) of a strided view, box 64 x 128 x 1 x 1 with
 // 128-byte swizzle.  A dimension of stride 0 (a repeated head or batch row) has one entry in
@@ -622,15 +724,43 @@ int encode_view(CUtensorMap* map, const mikv_rows& r, int T, int H, int B, const
   if (e != CUDA_SUCCESS) return fail(MIKV_ECUDA, "window_attention: tensor map of %s (error %d)", name, static_cast<int>(e));
   return MIKV_OK;
 }
+// The queries' map: (channel, row, head of the group, key head, batch row), box 64 x tb x hb x 1 x 1.
+int encode_queries(CUtensorMap* map, const mikv_rows& r, int T, int rep, int Hkv, int B, const Plan& p, int* mb, int* mh) {
+  const auto enc = tc::tensor_map_encoder();
+  if (!enc) return fail(MIKV_ECUDA, "window_attention: cuTensorMapEncodeTiled unavailable");
+  *mh = rep * Hkv > 1 && r.stride_h != 0;
+  *mb = B > 1 && r.stride_b != 0;
+  const cuuint64_t row = T > 1 ? static_cast<cuuint64_t>(r.stride_t) * 2 : kD * 2;
+  const cuuint64_t head = *mh ? static_cast<cuuint64_t>(r.stride_h) * 2 : row;
+  const cuuint64_t dims[5] = {kD, static_cast<cuuint64_t>(T), *mh ? static_cast<cuuint64_t>(rep) : 1, *mh ? static_cast<cuuint64_t>(Hkv) : 1,
+                              *mb ? static_cast<cuuint64_t>(B) : 1};
+  const cuuint64_t strides[4] = {row, head, head * static_cast<cuuint64_t>(*mh ? rep : 1), *mb ? static_cast<cuuint64_t>(r.stride_b) * 2 : row};
+  const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(p.tb), static_cast<cuuint32_t>(p.hb), 1, 1}, estr[5] = {1, 1, 1, 1, 1};
+  const CUresult e = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, r.data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (e != CUDA_SUCCESS) return fail(MIKV_ECUDA, "window_attention: tensor map of q (error %d)", static_cast<int>(e));
+  return MIKV_OK;
+}
 
 }  // namespace
 }  // namespace mikv
 
 using namespace mikv;
 
+extern "C" size_t mikv_window_attention_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk, int window, int sinks) {
+  if (B < 1 || B > 65535 || Hkv < 1 || Hkv > 65535 || Hq < 1 || Hq % Hkv || Tq < 1 || Tk < 1 || Tq > kMaxRows || Tk > kMaxRows ||
+      window < 0 || sinks < 0)
+    return 0;
+  size_t most = 0;   // heads that repeat one another's rows are not packed
+  for (bool pack : {true, false})
+    most = std::max(most, part_bytes(plan_of(B, Hq, Hkv, Tq, Tk, window >= Tk ? 0 : window, std::min(sinks, Tk), pack),
+                                     static_cast<int64_t>(B) * Hq * Tq));
+  return most;
+}
+
 extern "C" int mikv_window_attention(const mikv_rows* q, const mikv_rows* k, const mikv_rows* v, int B, int Hq, int Hkv, int Tq,
                                      int Tk, int D, int type, const int32_t* q_lens, const int32_t* k_lens, int window, int sinks,
-                                     const mikv_rows* out, float* lse, void* stream) {
+                                     const mikv_rows* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
   clear_error();
   if (type != MIKV_PAGES_FP16 && type != MIKV_PAGES_BF16) return fail(MIKV_EINVAL, "window_attention: type=%d", type);
   if (D != kD) return fail(MIKV_EUNSUPPORTED, "window_attention: D=%d (only %d)", D, kD);
@@ -657,19 +787,36 @@ extern "C" int mikv_window_attention(const mikv_rows* q, const mikv_rows* k, con
   a.Tk = Tk;
   a.window = window >= Tk ? 0 : window;   // one that reaches every key is none
   a.sinks = std::min(sinks, Tk);
-  a.pair_heads = a.rep % 2 == 0;
+  a.rows = static_cast<int64_t>(B) * Hq * Tq;
   a.wide_out = ((reinterpret_cast<uintptr_t>(out->data) | static_cast<uintptr_t>(a.out.sb | a.out.sh | a.out.st)) & 31u) == 0;
   a.scale = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
-  const int rows = a.pair_heads ? kWaRows : 2 * kWaRows;
-  a.blocks = (Tq + rows - 1) / rows;
-  const int64_t ctas = static_cast<int64_t>(a.blocks) * (a.pair_heads ? a.rep / 2 : a.rep);
-  if (ctas > 0x7fffffffLL) return fail(MIKV_ESHAPE, "window_attention: Tq=%d Hq=%d", Tq, Hq);
-  if (int e = encode_view(&qm, *q, Tq, Hq, B, "q", &a.qb, &a.qh)) return e;
+  const Plan p = plan_of(B, Hq, Hkv, Tq, Tk, a.window, a.sinks, packs(*q, Hq));
+  a.tb = p.tb;
+  a.hb = p.hb;
+  a.groups = p.groups;
+  a.blocks = p.blocks;
+  a.pair_heads = p.pair_heads;
+  a.splits = p.splits;
+  if (p.per_head * p.splits > 0x7fffffffLL) return fail(MIKV_ESHAPE, "window_attention: Tq=%d Hq=%d", Tq, Hq);
+  const size_t need = part_bytes(p, a.rows);
+  if (need > 0) {
+    if (!ws) return fail(MIKV_EINVAL, "window_attention: null workspace");
+    if (reinterpret_cast<uintptr_t>(ws) & 31u) return fail(MIKV_EALIGN, "window_attention: workspace must be 32-byte aligned");
+    if (ws_bytes < need) return fail(MIKV_ESHAPE, "window_attention: workspace %zu < %zu", ws_bytes, need);
+  }
+  a.part = static_cast<float*>(ws);
+  if (int e = encode_queries(&qm, *q, Tq, a.rep, Hkv, B, p, &a.qb, &a.qh)) return e;
   if (int e = encode_view(&km, *k, Tk, Hkv, B, "k", &a.kb, &a.kh)) return e;
   if (int e = encode_view(&vm, *v, Tk, Hkv, B, "v", &a.vb, &a.vh)) return e;
-  const auto kern = type == MIKV_PAGES_BF16 ? window_attention_kernel<true> : window_attention_kernel<false>;
+  const bool bf = type == MIKV_PAGES_BF16;
+  const auto kern = bf ? p.splits > 1 ? window_attention_kernel<true, true> : window_attention_kernel<true, false>
+                       : p.splits > 1 ? window_attention_kernel<false, true> : window_attention_kernel<false, false>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kWaSmem);
   if (e != cudaSuccess) return check_launch_after(e, "window_attention_kernel");
-  kern<<<dim3(static_cast<unsigned>(ctas), Hkv, B), kWaThreads, kWaSmem, as_stream(stream)>>>(qm, km, vm, a);
-  return check_launch("window_attention_kernel");
+  const cudaStream_t st = as_stream(stream);
+  kern<<<dim3(static_cast<unsigned>(p.per_head * p.splits), Hkv, B), kWaThreads, kWaSmem, st>>>(qm, km, vm, a);
+  if (int r = check_launch("window_attention_kernel")) return r;
+  if (p.splits == 1) return MIKV_OK;
+  const auto join = bf ? window_join_kernel<true> : window_join_kernel<false>;
+  return check_launch_after(launch_after(join, dim3(static_cast<unsigned>((a.rows + 3) / 4)), dim3(128), 0, st, a), "window_join_kernel");
 }

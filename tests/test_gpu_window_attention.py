@@ -59,6 +59,22 @@ def test_window_and_sinks(dtype, Tq, Tk, window, sinks):
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("B,Hkv,rep,Tq,Tk", [(1, 1, 4, 1, 4000), (2, 2, 3, 5, 3000), (1, 1, 7, 18, 2500), (1, 2, 16, 8, 1500),
+                                             (3, 1, 5, 33, 900), (1, 1, 2, 64, 5000), (1, 1, 2, 65, 2000), (1, 2, 1, 9, 6000),
+                                             (1, 1, 40, 3, 2600), (1, 1, 3, 200, 4000)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 5), (300, 400)])
+def test_few_rows_over_many_keys(dtype, B, Hkv, rep, Tq, Tk, window, sinks):
+    """Tiles that pack the rows of several heads, and items split over the keys; lengths of their own."""
+    q = _make(B, Hkv * rep, Tq, dtype, "bthd", 1)
+    k, v = _make(B, Hkv, Tk, dtype, "bhtd", 2), _make(B, Hkv, Tk, dtype, "bthd", 3)
+    assert _lib.load().mikv_window_attention_workspace_bytes(B, Hkv * rep, Hkv, Tq, Tk, window, sinks) > 0
+    _check(q, k, v, window, sinks)
+    ql, kl = [max(0, Tq - 2 * b) for b in range(B)], [Tk - 131 * b for b in range(B)]
+    kl[-1] = min(kl[-1], 200)                   # most parts see nothing
+    _check(q, k, v, window, sinks, ql, kl)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (40, 3)])
 def test_padded_batches(dtype, window, sinks):
     """Lengths from none to all, more queries than keys; NaN behind every row's end."""
@@ -138,6 +154,11 @@ def test_lse_may_be_left_out_and_rows_broadcast():
     k, v = k[:1].expand(2, 2, 90, 128), v[:, :1].expand(2, 2, 90, 128)
     out = torch.empty_like(q)
     _lib.mikv_window_attention(q, k, v, 0, 0, out)
+    for qb in (q[:, :1].expand(2, 2, 90, 128), q[:, :1, :3].expand(2, 2, 3, 128)):    # repeated query heads
+        ob = torch.empty(qb.shape, dtype=q.dtype, device=ph.DEV)
+        _lib.mikv_window_attention(qb, k, v, 0, 0, ob)
+        wb, _, mb = op.window_attention(ph.f64(qb), ph.f64(k), ph.f64(v), 0, 0)
+        ph.close(ob, wb, mb, 2.0 ** -11, 2.0 ** -11)
     want, _, mag = op.window_attention(ph.f64(q), ph.f64(k), ph.f64(v), 0, 0)
     ph.close(out, want, mag, 2.0 ** -11, 2.0 ** -11)
 

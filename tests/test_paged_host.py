@@ -124,14 +124,22 @@ def test_attention_calls_refuse(lib):
     # a workspace for no window serves every window
     assert lib.mikv_paged_attention_workspace_bytes(p, 2, 4, 0, 0) >= lib.mikv_paged_attention_workspace_bytes(p, 2, 4, 17, 3)
 
-    def wa(q=_rows(), k=_rows(), v=_rows(), out=_rows(), B=1, Hq=4, Hkv=2, Tq=8, Tk=8, D=128, type=0, window=0, sinks=0):
-        return lib.mikv_window_attention(q, k, v, B, Hq, Hkv, Tq, Tk, D, type, None, None, window, sinks, out, None, None)
+    def wa(q=_rows(), k=_rows(), v=_rows(), out=_rows(), B=1, Hq=4, Hkv=2, Tq=8, Tk=8, D=128, type=0, window=0, sinks=0, ws=None, nb=0):
+        return lib.mikv_window_attention(q, k, v, B, Hq, Hkv, Tq, Tk, D, type, None, None, window, sinks, out, None, ws, nb, None)
     assert wa(B=0) == 0
     for kw in (dict(B=-1), dict(B=65536), dict(Hq=5), dict(Hkv=0), dict(Tq=0), dict(Tk=0)):
         assert wa(**kw) == ESHAPE, kw
     for kw in (dict(type=2), dict(window=-1), dict(sinks=-1), dict(q=None), dict(out=None), dict(v=_rows(sb=-8))):
         assert wa(**kw) == EINVAL, kw
     assert wa(D=64) == EUNSUP
+    # a chunk of few rows behind many keys is split, and needs a workspace
+    many = dict(Tk=8192, Tq=16, k=_rows(sb=1 << 21, sh=1 << 20), v=_rows(sb=1 << 21, sh=1 << 20))
+    need = lib.mikv_window_attention_workspace_bytes(1, 4, 2, 16, 8192, 0, 0)
+    assert need >= 2 * 4 * 16 * 130 * 4
+    assert wa(**many) == EINVAL and wa(ws=FAKE, nb=need - 1, **many) == ESHAPE and wa(ws=FAKE + 16, nb=need, **many) == EALIGN
+    assert lib.mikv_window_attention_workspace_bytes(8, 64, 8, 4096, 4096, 0, 0) == 0
+    assert lib.mikv_window_attention_workspace_bytes(1, 5, 2, 16, 8192, 0, 0) == 0
+    assert wa(q=_rows(st=64)) == EINVAL and wa(out=_rows(sh=0)) == EINVAL and wa(k=_rows(st=0)) == EINVAL   # rows overlap
     for kw in (dict(q=_rows(st=132)), dict(k=_rows(data=FAKE + 4)), dict(v=_rows(sh=4)), dict(out=_rows(sb=2))):
         assert wa(**kw) == EALIGN, kw
 
