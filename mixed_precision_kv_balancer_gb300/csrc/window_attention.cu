@@ -40,6 +40,7 @@ int window_attention_status(unsigned* out, bool clear) { return tc::wait_giveups
 namespace {
 
 constexpr int kWaRows = 128;                     // query rows and key rows of a tile
+constexpr int kWaNarrow = 32;                    // columns of a tile that holds the last few sinks
 constexpr int kWaRing = 5;
 constexpr int kMaxRows = 1 << 30;                // of q or k: positions and their differences fit 32 bits
 constexpr int kWaThreads = 352;                  // 2 x 4 softmax warps, the TMA warp, 2 MMA warps
@@ -148,6 +149,11 @@ __device__ __forceinline__ Work work_of(const WindowArgs& a, int b, int x) {
 // Whether all rows of a query tile see all of the key tile at j0.
 __device__ __forceinline__ bool tile_whole(const WindowArgs& a, const Tile& t, int j0) {
   return j0 + kWaRows - 1 <= t.pa && (a.window == 0 || j0 > t.pb - a.window || j0 + kWaRows <= a.sinks);
+}
+// Whether a key tile counts with its first kWaNarrow columns alone: the sinks' last tile, mostly
+// (a window of 1024 with 4 sinks is ten tiles, one of them for the sinks: 79 -> 75 us).
+__device__ __forceinline__ bool tile_narrow(const WindowArgs& a, const Work& w, int i) {
+  return i < w.ts && a.sinks - w.j0(i) <= kWaNarrow;
 }
 // Rows [z0, z1) and [z2, 128) of the value tile at j0 that no query of the call sees.
 struct Hidden {
@@ -265,21 +271,21 @@ struct Row {
 // The n lowest bits set, for any n.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 
-// One tile of scores: 128 columns of this thread's lane at `ts` become weights; the accumulator
+// One tile of scores: COLS columns of this thread's lane at `ts` become weights; the accumulator
 // at `to` is rescaled where some row of the warp needs it.
 // Each half of the weights is announced (`ready`, one arrival a warp) as soon as it is written.
-template <bool BF>
+template <bool BF, int COLS>
 __device__ __forceinline__ void softmax_tile(const WindowArgs& a, uint32_t ts, uint32_t to, bool whole, int p, int j0, Row& r,
                                              const uint32_t (&ready)[2]) {
-  float s[kWaRows];
+  float s[COLS];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) ld32(ts + c * 32, s + c * 32);
+  for (int c = 0; c < COLS / 32; ++c) ld32(ts + c * 32, s + c * 32);
   wait_ld();
   if (!whole) {
     // the row sees columns lo .. hi and those below sk; 32 columns whole to the warp's rows are left alone
     const int hi = p - j0, lo = a.window > 0 ? hi - a.window + 1 : 0, sk = a.sinks - j0;
 #pragma unroll
-    for (int c = 0; c < kWaRows; c += 32) {
+    for (int c = 0; c < COLS; c += 32) {
       const uint32_t m = low_bits(hi + 1 - c) & (~low_bits(lo - c) | low_bits(sk - c));
       if (!__all_sync(0xffffffffu, m == 0xffffffffu)) {
 #pragma unroll
@@ -290,9 +296,9 @@ __device__ __forceinline__ void softmax_tile(const WindowArgs& a, uint32_t ts, u
   }
   float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-  for (int c = 4; c < kWaRows; c += 8)
+  for (int c = 4; c < COLS; c += 8)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) mx[u] = fmaxf(fmaxf(mx[u], s[c + u]), c + 4 + u < kWaRows ? s[c + 4 + u] : -INFINITY);
+    for (int u = 0; u < 4; ++u) mx[u] = fmaxf(fmaxf(mx[u], s[c + u]), c + 4 + u < COLS ? s[c + 4 + u] : -INFINITY);
   const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
   const bool grew = (top - r.m) * a.scale > Weights<BF>::grow;   // from -inf too; never by NaN
   if (__any_sync(0xffffffffu, grew)) {
@@ -318,7 +324,7 @@ __device__ __forceinline__ void softmax_tile(const WindowArgs& a, uint32_t ts, u
   const float neg = r.m == -INFINITY ? 0.f : Weights<BF>::shift - r.m * a.scale;
   float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-  for (int c = 0; c < kWaRows; c += 32) {
+  for (int c = 0; c < COLS; c += 32) {
     uint32_t u[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -328,11 +334,14 @@ __device__ __forceinline__ void softmax_tile(const WindowArgs& a, uint32_t ts, u
       u[i] = pack2<BF>(e.x, e.y);
     }
     st16(ts + c / 2, u);
-    if (c % 64 == 32) {
+    if (c % 64 == 32 || COLS == 32) {
       wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if ((threadIdx.x & 31) == 0) tc::mbar_arrive(ready[c / 64]);
+      if ((threadIdx.x & 31) == 0) {
+        tc::mbar_arrive(ready[c / 64]);
+        if (COLS == 32) tc::mbar_arrive(ready[1]);
+      }
     }
   }
   r.l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -478,7 +487,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
     const int t = warp - kWaMmaWarp;
     bool lead = elect_one();
     constexpr uint32_t kType = BF ? (1u << 7) | (1u << 10) : 0u;
-    constexpr uint32_t kScores = tc::idesc_f16(kWaRows, kWaRows) | kType;
+    constexpr uint32_t kScores = tc::idesc_f16(kWaRows, kWaRows) | kType, kFew = tc::idesc_f16(kWaRows, kWaNarrow) | kType;
     constexpr uint32_t kValues = tc::idesc_f16(kWaRows, kD) | kType | (1u << 16);   // B: rows along the contraction
     const uint32_t ts = tmem + t * 128, to = tmem + kWaO + t * 128;
     const uint64_t qd = tc::smem_desc(sq + t * tc::kTileBytes), k0 = tc::smem_desc(ring), v0 = value_desc(ring);
@@ -496,7 +505,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       const Work w = work_of<SPLIT>(a, it.z, it.x);
       if (w.nt > 0 && w.begin < w.end) {
         const Tile tile = tile_of(w, t);
-        bool more = false, before = false, clear = false;
+        bool more = false, before = false, clear = false, few = false;
         int vslot = 0, vpar = 0;     // the last step's values
         wait(smem_u32(&bar.q), q_par);
         q_par ^= 1;
@@ -523,7 +532,11 @@ __global__ void __launch_bounds__(kWaThreads, 1)
               for (int c = c0; c < c1; ++c) mma_ts(to, ts + c * 8, vd + desc_step(c * 2048), kValues, more || c > 0);
             };
             // the tensor core's queue holds about two products: a wait between them leaves it idle
-            if (__all_sync(0xffffffffu, tc::mbar_wait(smem_u32(&bar.p[t][1]), p_par, 1))) {
+            if (few) {
+              wait(smem_u32(&bar.p[t][1]), p_par);
+              lead &= __all_sync(0xffffffffu, wait.ok) != 0;
+              if (lead) sums(0, kWaNarrow / 16);
+            } else if (__all_sync(0xffffffffu, tc::mbar_wait(smem_u32(&bar.p[t][1]), p_par, 1))) {
               tc::fence_after_sync();
               if (lead) sums(0, kWaRows / 16);
             } else {
@@ -536,6 +549,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
             p_par ^= 1;
             more = true;
           }
+          const uint32_t scores = keys && tile_narrow(a, w, i) ? kFew : kScores;
           if (lead) {
             if (before && i - 1 == tile.last) tc::commit(smem_u32(&bar.o[t]));
             // the turn passes on a little early: the other warp takes as long to wake as the
@@ -544,7 +558,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
 #pragma unroll
               for (int c = 0; c < kD / 16; ++c) {
                 const uint64_t off = desc_step((c >> 2) * tc::kKBlock + (c & 3) * 32);
-                tc::mma_f16(ts, qd + off, kd + off, kScores, c > 0);
+                tc::mma_f16(ts, qd + off, kd + off, scores, c > 0);
                 if (c == 4) tc::mbar_arrive(smem_u32(&bar.turn[t ^ 1]));
               }
               tc::commit(smem_u32(&bar.s[t]));
@@ -553,6 +567,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
             }
           }
           before = here;
+          few = keys && tile_narrow(a, w, i);
           if (lead) {
             if (i > w.begin) tc::commit(smem_u32(&bar.empty[vslot]));
             if (keys) tc::commit(smem_u32(&bar.empty[slot]));
@@ -588,7 +603,10 @@ __global__ void __launch_bounds__(kWaThreads, 1)
           wait(smem_u32(&bar.s[t]), s_par);
           s_par ^= 1;
           tc::fence_after_sync();
-          softmax_tile<BF>(a, ts, to, tile_whole(a, tile, j0), p, j0, r, ready);
+          if (tile_narrow(a, w, i))
+            softmax_tile<BF, kWaNarrow>(a, ts, to, false, p, j0, r, ready);
+          else
+            softmax_tile<BF, kWaRows>(a, ts, to, tile_whole(a, tile, j0), p, j0, r, ready);
         }
         if (tile.last >= 0) {
           wait(smem_u32(&bar.o[t]), o_par);
