@@ -1,12 +1,11 @@
 // Rows into pages and back: append and gather of the paged cache.
 //
-// A CTA moves 64 tokens of one (sequence, key head): its first threads look their pages up,
-// then every thread copies 16-byte pieces with several loads in flight.  Both operators are
-// bound by HBM: each row is read and written once.
+// A CTA moves 32 tokens of one (sequence, key head): its first warp looks their pages up, and
+// every thread copies four 16-byte pieces of keys and of values, all requested before the first
+// is written.  Both operators are bound by HBM: each row is read and written once.
 #include <cuda_bf16.h>
 
 #include "paged.cuh"
-#include "quant_device.cuh"
 #include "tcgen05.cuh"
 
 namespace mikv {
@@ -15,8 +14,8 @@ int paged_rows_status(unsigned* out, bool clear) { return tc::wait_giveups(out, 
 
 namespace {
 
-constexpr int kRowThreads = 256;
-constexpr int kRowTokens = 64;
+constexpr int kRowThreads = 128;
+constexpr int kRowTokens = 32;
 
 // Pool rows of tokens slot0 .. slot0 + rows - 1 of sequence s, head h, into `at`.
 __device__ __forceinline__ void find_rows(const Pool& p, int32_t s, int h, int slot0, int rows, uint32_t* at) {
@@ -32,7 +31,50 @@ __device__ __forceinline__ void find_rows(const Pool& p, int32_t s, int h, int s
   __syncthreads();
 }
 
-// CTA (chunk, head, row i): source tokens chunk * 64 .. of row i to slots start + t of its
+// The quantiser of the contiguous cache at 8 bits on 8 fp16 channels a lane, 8 lanes a group, with
+// its arithmetic: s = fp16(fl(fl(mx - mn) / 255)), z = fp16(mn), code = clamp(rint_even(fl(fl(x - z) / s))).
+__device__ __forceinline__ uint2 quantize8(const uint4& x, uint32_t& meta) {
+  const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __half2 h = *reinterpret_cast<const __half2*>(&in[j]);
+    f[2 * j] = __low2float(h);
+    f[2 * j + 1] = __high2float(h);
+  }
+  float mn = f[0], mx = f[0];
+#pragma unroll
+  for (int j = 1; j < 8; ++j) {
+    mn = fminf(mn, f[j]);
+    mx = fmaxf(mx, f[j]);
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  }
+  const __half sh = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), 255.f)), zh = __float2half_rn(mn);
+  const float s = __half2float(sh), z = __half2float(zh);
+  meta = pack_half2(sh, zh);
+  uint32_t c[2] = {0, 0};
+  if (s != 0.f) {
+    // A product with the reciprocal is within 2^-13 of the quotient (at most 300 after the clamp),
+    // so both round to the same code unless the product lies that near to a half: then, and for
+    // what is no number, the division decides.  1.5 * 2^23 added leaves rint in the last bits.
+    const float r = __frcp_rn(s);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float d = __fsub_rn(f[j], z), t = fminf(__fmul_rn(d, r), 300.f);
+      const float big = __fadd_rn(t, 12582912.f);
+      int q = __float_as_int(big) - 0x4B400000;
+      if (!(fabsf(t - (big - 12582912.f)) < 0.49f)) q = __float2int_rn(__fdiv_rn(d, s));
+      c[j >> 2] |= static_cast<uint32_t>(min(max(q, 0), 255)) << (8 * (j & 3));
+    }
+  }
+  return make_uint2(c[0], c[1]);
+}
+
+// CTA (chunk, head, row i): source tokens chunk * 32 .. of row i to slots start + t of its
 // sequence.  Rows of a sequence that an earlier row of the call names are skipped.
 template <bool Q8>
 __global__ void __launch_bounds__(kRowThreads) paged_append_kernel(const Pool p, int layer, RowView k, RowView v, int T,
@@ -44,79 +86,82 @@ __global__ void __launch_bounds__(kRowThreads) paged_append_kernel(const Pool p,
   const int i = blockIdx.z, h = blockIdx.y, t0 = blockIdx.x * kRowTokens;
   const int count = counts ? min(counts[i], T) : T;
   if (t0 >= count) return;
+  // the source rows are requested before anything is looked up; piece c of a row: 16 bytes
+  uint4 a[4], b[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int c = threadIdx.x + u * kRowThreads, r = c >> 4;
+    a[u] = b[u] = make_uint4(0, 0, 0, 0);
+    if (t0 + r < count) {
+      a[u] = *reinterpret_cast<const uint4*>(k.row(i, h, t0 + r) + (c & 15) * 16);
+      b[u] = *reinterpret_cast<const uint4*>(v.row(i, h, t0 + r) + (c & 15) * 16);
+    }
+  }
   const int32_t s = seqs ? seqs[i] : i;
   if (static_cast<uint32_t>(s) >= static_cast<uint32_t>(p.max_seqs)) return;
   const int len = p.len_of(s);
   const int first = start ? start[i] : len - count;
   if (first < 0) return;                                 // a refused reservation, or more tokens than slots
-  if (threadIdx.x == 0) twice = 0;
-  __syncthreads();
-  if (seqs)
+  if (seqs) {
+    if (threadIdx.x == 0) twice = 0;
+    __syncthreads();
     for (int j = threadIdx.x; j < i; j += kRowThreads)
       if (seqs[j] == s) twice = 1;
-  __syncthreads();
-  if (twice) return;
+    __syncthreads();
+    if (twice) return;
+  }
   const int64_t slot0 = static_cast<int64_t>(first) + t0;
   const int rows = static_cast<int>(min(static_cast<int64_t>(min(kRowTokens, count - t0)), len - slot0));
   if (rows <= 0) return;                                 // slots past the sequence's length
   find_rows(p, s, h, static_cast<int>(slot0), rows, at);
   const size_t lrow = p.layer_rows() * layer;
-  if (!Q8) {
-    uint4 a[4], b[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int c = threadIdx.x + u * kRowThreads, r = c >> 4;
-      if (r < rows && at[r] != kNoRow) {
-        a[u] = *reinterpret_cast<const uint4*>(k.row(i, h, t0 + r) + (c & 15) * 16);
-        b[u] = *reinterpret_cast<const uint4*>(v.row(i, h, t0 + r) + (c & 15) * 16);
+  for (int u = 0; u < 4; ++u) {
+    const int c = threadIdx.x + u * kRowThreads, r = c >> 4, piece = c & 15;
+    const bool ok = r < rows && at[r] != kNoRow;
+    const size_t row = lrow + (ok ? at[r] : 0);
+    if (!Q8) {
+      if (ok) {
+        *reinterpret_cast<uint4*>(p.k + row * (kD * 2) + piece * 16) = a[u];
+        *reinterpret_cast<uint4*>(p.v + row * (kD * 2) + piece * 16) = b[u];
       }
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int c = threadIdx.x + u * kRowThreads, r = c >> 4;
-      if (r < rows && at[r] != kNoRow) {
-        const size_t off = (lrow + at[r]) * (kD * 2) + (c & 15) * 16;
-        *reinterpret_cast<uint4*>(p.k + off) = a[u];
-        *reinterpret_cast<uint4*>(p.v + off) = b[u];
-      }
-    }
-  } else {
-    // one warp per token, 4 channels a lane: the quantiser of the contiguous cache
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll 2
-    for (int r = w; r < rows; r += kRowThreads / 32) {
-      if (at[r] == kNoRow) continue;  // uniform over the warp
-      const Row4 xk = load_fp16x4(reinterpret_cast<const __half*>(k.row(i, h, t0 + r)) + lane * 4);
-      const Row4 xv = load_fp16x4(reinterpret_cast<const __half*>(v.row(i, h, t0 + r)) + lane * 4);
+    } else {   // 16 lanes a row: all of a warp quantise
       uint32_t mk, mv;
-      const uint32_t ck = quantize4(xk, 8, mk), cv = quantize4(xv, 8, mv);
-      const size_t row = lrow + at[r];
-      store_codes(p.k + row * kD, lane, 8, ck);
-      store_codes(p.v + row * kD, lane, 8, cv);
-      store_meta(reinterpret_cast<__half2*>(p.km + row * kMetaBytes), lane, mk);
-      store_meta(reinterpret_cast<__half2*>(p.vm + row * kMetaBytes), lane, mv);
+      const uint2 ck = quantize8(a[u], mk), cv = quantize8(b[u], mv);
+      if (ok) {
+        *reinterpret_cast<uint2*>(p.k + row * kD + piece * 8) = ck;
+        *reinterpret_cast<uint2*>(p.v + row * kD + piece * 8) = cv;
+        if ((piece & 7) == 0) {
+          reinterpret_cast<uint32_t*>(p.km + row * kMetaBytes)[piece >> 3] = mk;
+          reinterpret_cast<uint32_t*>(p.vm + row * kMetaBytes)[piece >> 3] = mv;
+        }
+      }
     }
   }
 }
 
-// 8 codes to 8 fp16 values fp16(s * code + z), one fp32 rounding before the last.
+// 8 codes to 8 fp16 values fp16(s * code + z), one fp32 rounding before the last (s * code is exact:
+// 11 + 8 bits).  A code becomes fp32 as the last bits of 2^23 + code: two full-rate operations,
+// where a conversion would take a quarter-rate one.
 __device__ __forceinline__ uint4 values_of(uint2 c, __half2 m) {
   const float s = __low2float(m), z = __high2float(m);
   uint32_t w[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t x = (j < 2 ? c.x : c.y) >> (16 * (j & 1));
-    const __half lo = __float2half_rn(__fadd_rn(__fmul_rn(s, static_cast<float>(x & 0xffu)), z));
-    const __half hi = __float2half_rn(__fadd_rn(__fmul_rn(s, static_cast<float>((x >> 8) & 0xffu)), z));
-    w[j] = pack_half2(lo, hi);
+    float f[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      f[e] = fmaf(s, __uint_as_float(__byte_perm(j < 2 ? c.x : c.y, 0x4B000000u, 0x7440u + 2 * (j & 1) + e)) - 8388608.f, z);
+    const __half2 h = __floats2half2_rn(f[0], f[1]);
+    w[j] = *reinterpret_cast<const uint32_t*>(&h);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// CTA (chunk, head, row i): slots chunk * 64 .. of row i's sequence, as far as it reaches, to
+// CTA (chunk, head, row i): slots chunk * 32 .. of row i's sequence, as far as it reaches, to
 // rows of k and v.  Rows past the sequence's end keep what they hold.
 template <bool Q8>
-__global__ void __launch_bounds__(kRowThreads) paged_gather_kernel(const Pool p, int layer, RowView k, RowView v, int T,
+__global__ void __launch_bounds__(kRowThreads, 10) paged_gather_kernel(const Pool p, int layer, RowView k, RowView v, int T,
                                                                    const int32_t* __restrict__ seqs) {
   __shared__ uint32_t at[kRowTokens];
   const int i = blockIdx.z, h = blockIdx.y, t0 = blockIdx.x * kRowTokens;

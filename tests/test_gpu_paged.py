@@ -220,6 +220,34 @@ def test_append_and_gather(type, ps, T, layout):
                 assert torch.equal(ko[s, :, n:], k0[s, :, n:]) and torch.equal(vo[s, :, n:], v0[s, :, n:])
 
 
+def test_codes_at_halves_and_extremes():
+    """Groups whose quotients lie on halves, tiny and huge ranges, equal values: the codes are the
+    definition's, which divides in fp32."""
+    T = 64
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(1, 1, T, 128, generator=g)
+    for t in range(40):                        # scale 2^e / 8: quotients k / 2 of many codes are exact halves
+        step = 2.0 ** (t % 10 - 5)
+        x[0, 0, t] = torch.randint(0, 511, (128,), generator=g) * (step / 2)
+        x[0, 0, t, ::64], x[0, 0, t, 1::64] = 0.0, 255 * step
+    x[0, 0, 40:44] *= 1e-6                     # scales among fp16's subnormal numbers, and below them
+    x[0, 0, 44:46] *= 6e-8
+    x[0, 0, 46:50] = torch.randn(4, 128, generator=g) * 2e4
+    x[0, 0, 50, 3], x[0, 0, 50, 70] = 65504.0, -65504.0
+    x[0, 0, 51] = 1.25
+    x[0, 0, 52] = 65504.0
+    x[0, 0, 52, ::2] = -65504.0
+    x = x.half()
+    cache = ph.make([T], 16, 1, "int8", poison=False)
+    cache.append(0, x.to(ph.DEV), x.to(ph.DEV))
+    codes, meta = ph.quantize(x)
+    at = torch.arange(T)
+    page = cache.table[0].cpu().long()[at // 16]
+    for stored, sm in ((cache.k, cache.k_meta), (cache.v, cache.v_meta)):
+        assert torch.equal(stored[0].cpu()[page, 0, at % 16], codes[0, 0])
+        assert torch.equal(sm[0].cpu()[page, 0, at % 16], meta[0, 0])
+
+
 def test_append_skips_what_it_may_not_write():
     cache = ph.make([40, 40, 40], 16, 2, "fp16", poison=False)
     x = ph.normal((4, 2, 10, 128), 3, torch.float16).to(ph.DEV)
