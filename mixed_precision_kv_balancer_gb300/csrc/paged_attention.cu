@@ -22,7 +22,8 @@
 // out of fp16's subnormal range (down to 2^-29 of the largest).  INT8 codes enter the products
 // as exact integers: q . (s c + z) = s (q . c) + z sum(q) per group of 64 channels (fp16), and
 // sum_j p_j (s_j c_j + z_j) = sum_j (p_j s_j) (c_j - 128) + sum_j p_j (z_j + 128 s_j), where the
-// weights p_j s_j and the codes are bf16, whose range takes any scale.
+// weights p_j s_j carry the factor 2^15 / cap, cap the power of two above every s_j so far (the
+// sums are rescaled where it moves).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -47,12 +48,13 @@ struct Shape {
   static constexpr int tw = q8 ? 32 : 16;             // slots of a tile
   static constexpr int row = q8 ? kD : kD * 2;        // bytes of a stored row
   static constexpr int shift = TYPE == MIKV_PAGES_FP16 ? 15 : 0;  // the weights' factor, log2
-  static constexpr int pv = q8 ? MIKV_PAGES_BF16 : TYPE;          // type of the weights and values in products
   static constexpr int stages = 3;
   static constexpr int k_bytes = tw * row;
   static constexpr int meta = q8 ? tw * kMetaBytes : 0;
-  static constexpr int stage = 2 * k_bytes + 2 * meta + 16;  // + the mask of valid slots
-  static constexpr int smem = kPaWarps * stages * stage;
+  // + the mask of valid slots; stages begin at multiples of 256 bytes, so that swizzled addresses
+  // are one exclusive or
+  static constexpr int stage = (2 * k_bytes + 2 * meta + 16 + 255) / 256 * 256;
+  static constexpr int smem = kPaWarps * stages * stage + 256;
 };
 
 struct AttendArgs {
@@ -150,16 +152,17 @@ struct Acc {
   float m[NH][2];            // maximum, log2 units (the same in the 8 lanes of a column)
   float l[NH][2];            // this thread's part of the sum
   float z[NH][2][2];         // INT8: this thread's part of sum p (z + 128 s), per group of channels
+  float cap[2];              // INT8: power of two not below any scale of a value so far, per group
 };
 
-// Shared-memory address of 16-byte piece c of row r of a stage's keys or values.
+// Shared-memory address of 16-byte piece c of row r of a stage's keys or values, as k_row ^ (c << 4), v_row ^ (c << 4).
 template <bool Q8>
-__device__ __forceinline__ uint32_t k_at(uint32_t s, int r, int c) {
-  return Q8 ? s + r * kD + ((c ^ ((r & 1) << 2)) << 4) : s + r * (kD * 2) + ((c ^ (r & 7)) << 4);
+__device__ __forceinline__ uint32_t k_row(uint32_t s, int r) {
+  return Q8 ? s + r * kD + ((r & 1) << 6) : s + r * (kD * 2) + ((r & 7) << 4);
 }
 template <bool Q8>
-__device__ __forceinline__ uint32_t v_at(uint32_t s, int r, int c) {
-  return s + r * (Q8 ? kD : kD * 2) + ((c ^ (r & 7)) << 4);
+__device__ __forceinline__ uint32_t v_row(uint32_t s, int r) {
+  return s + r * (Q8 ? kD : kD * 2) + ((r & 7) << 4);
 }
 
 // The pool row of visible slot `i`, kNoRow past the last one or where the table names no page.
@@ -186,8 +189,8 @@ __device__ __forceinline__ void issue(const Pool& p, size_t lrow, uint32_t st, u
     const uint32_t src = __shfl_sync(0xffffffffu, my_row, r);
     const bool ok = src != kNoRow;
     const size_t off = ok ? static_cast<size_t>(src) * S::row + c * 16 : 0;
-    cp_async16_once(k_at<S::q8>(st, r, c), kb + off, ok, policy);
-    cp_async16_once(v_at<S::q8>(st + S::k_bytes, r, c), vb + off, ok, policy);
+    cp_async16_once(k_row<S::q8>(st, r) ^ (c << 4), kb + off, ok, policy);
+    cp_async16_once(v_row<S::q8>(st + S::k_bytes, r) ^ (c << 4), vb + off, ok, policy);
   }
   if (S::q8) {
     const bool ok = my_row != kNoRow;
@@ -201,21 +204,13 @@ __device__ __forceinline__ void issue(const Pool& p, size_t lrow, uint32_t st, u
 
 __device__ __forceinline__ float meta_s(uint32_t m) { return __half2float(__ushort_as_half(m & 0xffffu)); }
 __device__ __forceinline__ float meta_z(uint32_t m) { return __half2float(__ushort_as_half(m >> 16)); }
-// The codes in two bytes of x (`sel` puts them under 0x64) as an fp16 pair: 0x64cc is 1024 + c.
-__device__ __forceinline__ uint32_t codes_f16(uint32_t x, uint32_t sel) {
-  const uint32_t w = __byte_perm(x, 0x64646464u, sel), bias = 0x64006400u;
+// The codes in two bytes of x (`sel` puts them under 0x64) as an fp16 pair, exactly: 0x64cc is
+// 1024 + c, and `bias` twice 1024, or 1152 for c - 128.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t x, uint32_t sel, uint32_t bias) {
+  const uint32_t w = __byte_perm(x, 0x64646464u, sel);
   const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&w), *reinterpret_cast<const __half2*>(&bias));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// Codes minus 128 as a bf16 pair: 0x4300 is 128 and its last seven bits count ones, so
-// (128 + c mod 128) - (c < 128 ? 256 : 128) = c - 128; 0x4380 is 256.
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t x, uint32_t sel) {
-  const uint32_t w = __byte_perm(x, 0x43434343u, sel);
-  const uint32_t a = w & 0xff7fff7fu, b = (~w & 0x00800080u) | 0x43004300u;
-  const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // One tile: scores of its slots, the running softmax, and their values.
 // `qf`: the queries as B fragments; `qsum`: INT8, sums of each query's two groups.
 template <int TYPE, int NH>
@@ -225,6 +220,8 @@ __device__ __forceinline__ void consume(uint32_t st, const uint32_t (&qf)[kD / 1
   constexpr int KT = S::tw / 16;
   const int lane = threadIdx.x & 31, g = lane >> 2;
   const uint32_t mask = lds32(st + 2 * S::k_bytes + 2 * S::meta);
+  // this lane's row and first piece of the keys (rows 8 and 16 apart swizzle alike)
+  const uint32_t kr = S::q8 ? k_row<S::q8>(st, g) ^ ((lane & 3) << 4) : k_row<S::q8>(st, lane & 15) ^ ((lane >> 4) << 4);
   float s[KT][NH][4];   // slots 16 kt + g and + 8, heads as in Acc
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) {
@@ -233,7 +230,7 @@ __device__ __forceinline__ void consume(uint32_t st, const uint32_t (&qf)[kD / 1
 #pragma unroll
       for (int ks = 0; ks < kD / 16; ++ks) {
         uint32_t a[4];
-        ldsm_x4(k_at<S::q8>(st, kt * 16 + (lane & 15), ks * 2 + (lane >> 4)), a[0], a[1], a[2], a[3]);
+        ldsm_x4((kr ^ (ks << 5)) + kt * 16 * S::row, a[0], a[1], a[2], a[3]);
 #pragma unroll
         for (int nh = 0; nh < NH; ++nh) mma<TYPE>(d[nh], a, qf[ks][nh][0], qf[ks][nh][1]);
       }
@@ -246,13 +243,13 @@ __device__ __forceinline__ void consume(uint32_t st, const uint32_t (&qf)[kD / 1
 #pragma unroll
       for (int grp = 0; grp < 2; ++grp) {
         // 16 codes of slots g and g + 8; the channels' order is the queries' too
-        const uint4 c0 = lds128(k_at<S::q8>(st, kt * 16 + g, grp * 4 + (lane & 3)));
-        const uint4 c1 = lds128(k_at<S::q8>(st, kt * 16 + g + 8, grp * 4 + (lane & 3)));
+        const uint4 c0 = lds128((kr ^ (grp << 6)) + kt * 16 * S::row);
+        const uint4 c1 = lds128((kr ^ (grp << 6)) + (kt * 16 + 8) * S::row);
         const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          const uint32_t a[4] = {codes_f16(w0[kk], 0x4140u), codes_f16(w1[kk], 0x4140u), codes_f16(w0[kk], 0x4342u),
-                                 codes_f16(w1[kk], 0x4342u)};
+          const uint32_t a[4] = {codes_f16(w0[kk], 0x4140u, 0x64006400u), codes_f16(w1[kk], 0x4140u, 0x64006400u), codes_f16(w0[kk], 0x4342u, 0x64006400u),
+                                 codes_f16(w1[kk], 0x4342u, 0x64006400u)};
 #pragma unroll
           for (int nh = 0; nh < NH; ++nh) mma<TYPE>(d[grp][nh], a, qf[grp * 4 + kk][nh][0], qf[grp * 4 + kk][nh][1]);
         }
@@ -322,7 +319,39 @@ __device__ __forceinline__ void consume(uint32_t st, const uint32_t (&qf)[kD / 1
         s[kt][nh][j] = ex2(s[kt][nh][j] - sub[nh][j & 1]);
         acc.l[nh][j & 1] += s[kt][nh][j];
       }
-  const uint32_t vs = st + S::k_bytes;
+  const uint32_t vr = S::q8 ? v_row<S::q8>(st + S::k_bytes, lane & 15) ^ ((lane >> 4) << 4)
+                            : v_row<S::q8>(st + S::k_bytes, (lane & 7) + (lane >> 4) * 8) ^ (((lane >> 3) & 1) << 4);
+  uint2 vm[KT][2];   // INT8: (scale, zero) of both groups of the values of slots 16 kt + g and + 8
+  float vf[2] = {1.f, 1.f};
+  if (S::q8) {
+    __half2 top = __float2half2_rn(0.f);
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        vm[kt][r] = lds64(st + 2 * S::k_bytes + S::meta + (kt * 16 + g + 8 * r) * kMetaBytes);
+        const uint32_t sc = __byte_perm(vm[kt][r].x, vm[kt][r].y, 0x5410u);
+        top = __hmax2(top, *reinterpret_cast<const __half2*>(&sc));
+      }
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) top = __hmax2(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const float tops[2] = {__low2float(top), __high2float(top)};
+#pragma unroll
+    for (int grp = 0; grp < 2; ++grp) {
+      if (tops[grp] > acc.cap[grp]) {   // the same in all lanes
+        const float cap = __uint_as_float((__float_as_uint(tops[grp]) & 0x7f800000u) + 0x00800000u);   // the power of two above
+        const float f = acc.cap[grp] / cap;
+        acc.cap[grp] = cap;
+#pragma unroll
+        for (int mt = grp * 4; mt < grp * 4 + 4; ++mt)
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc.o[mt][nh][j] *= f;
+      }
+      vf[grp] = 32768.f / acc.cap[grp];
+    }
+  }
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) {
     // weights as B fragments (slots x heads): pairs of heads, transposed into pairs of slots
@@ -330,8 +359,7 @@ __device__ __forceinline__ void consume(uint32_t st, const uint32_t (&qf)[kD / 1
     uint32_t hi[G][NH][2], lo[G][NH][2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      uint2 m = make_uint2(0, 0);
-      if (S::q8) m = lds64(st + 2 * S::k_bytes + S::meta + (kt * 16 + g + 8 * r) * kMetaBytes);
+      const uint2 m = S::q8 ? vm[kt][r] : make_uint2(0, 0);
 #pragma unroll
       for (int grp = 0; grp < G; ++grp) {
         const float sc = S::q8 ? meta_s(grp ? m.y : m.x) : 1.f;
@@ -340,7 +368,7 @@ __device__ __forceinline__ void consume(uint32_t st, const uint32_t (&qf)[kD / 1
         for (int nh = 0; nh < NH; ++nh) {
           const float p0 = s[kt][nh][2 * r], p1 = s[kt][nh][2 * r + 1];
           uint32_t h, l;
-          split_pair<S::pv>(p0 * sc, p1 * sc, h, l);
+          split_pair<TYPE>(S::q8 ? p0 * (sc * vf[grp]) : p0, S::q8 ? p1 * (sc * vf[grp]) : p1, h, l);
           hi[grp][nh][r] = movmatrix_t(h);
           lo[grp][nh][r] = movmatrix_t(l);
           if (S::q8) {
@@ -354,11 +382,11 @@ __device__ __forceinline__ void consume(uint32_t st, const uint32_t (&qf)[kD / 1
 #pragma unroll
       for (int mt = 0; mt < kD / 16; ++mt) {
         uint32_t a[4];
-        ldsm_x4_t(v_at<S::q8>(vs, kt * 16 + (lane & 7) + (lane >> 4) * 8, 2 * mt + ((lane >> 3) & 1)), a[0], a[1], a[2], a[3]);
+        ldsm_x4_t((vr ^ (mt << 5)) + kt * 16 * S::row, a[0], a[1], a[2], a[3]);
 #pragma unroll
         for (int nh = 0; nh < NH; ++nh) {
-          mma<S::pv>(acc.o[mt][nh], a, hi[0][nh][0], hi[0][nh][1]);
-          mma<S::pv>(acc.o[mt][nh], a, lo[0][nh][0], lo[0][nh][1]);
+          mma<TYPE>(acc.o[mt][nh], a, hi[0][nh][0], hi[0][nh][1]);
+          mma<TYPE>(acc.o[mt][nh], a, lo[0][nh][0], lo[0][nh][1]);
         }
       }
     } else {
@@ -367,16 +395,17 @@ __device__ __forceinline__ void consume(uint32_t st, const uint32_t (&qf)[kD / 1
 #pragma unroll
       for (int mt = 0; mt < kD / 16; mt += 2) {
         uint32_t x[4];
-        ldsm_x4_t(v_at<S::q8>(vs, kt * 16 + (lane & 15), mt + (lane >> 4)), x[0], x[1], x[2], x[3]);
+        ldsm_x4_t((vr ^ (mt << 4)) + kt * 16 * S::row, x[0], x[1], x[2], x[3]);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const int grp = (mt + b) >> 2;
-          const uint32_t a[4] = {codes_bf16(x[2 * b], 0x4240u), codes_bf16(x[2 * b], 0x4341u), codes_bf16(x[2 * b + 1], 0x4240u),
-                                 codes_bf16(x[2 * b + 1], 0x4341u)};
+          constexpr uint32_t kBias = 0x64806480u;
+          const uint32_t a[4] = {codes_f16(x[2 * b], 0x4240u, kBias), codes_f16(x[2 * b], 0x4341u, kBias),
+                                 codes_f16(x[2 * b + 1], 0x4240u, kBias), codes_f16(x[2 * b + 1], 0x4341u, kBias)};
 #pragma unroll
           for (int nh = 0; nh < NH; ++nh) {
-            mma<S::pv>(acc.o[mt + b][nh], a, hi[grp][nh][0], hi[grp][nh][1]);
-            mma<S::pv>(acc.o[mt + b][nh], a, lo[grp][nh][0], lo[grp][nh][1]);
+            mma<TYPE>(acc.o[mt + b][nh], a, hi[grp][nh][0], hi[grp][nh][1]);
+            mma<TYPE>(acc.o[mt + b][nh], a, lo[grp][nh][0], lo[grp][nh][1]);
           }
         }
       }
@@ -439,8 +468,8 @@ __device__ __forceinline__ void store_unit(const AttendArgs& a, int b, int u, Ac
           const float z = column_sum(acc.z[nh][j][grp]);
 #pragma unroll
           for (int mt = grp * 4; mt < grp * 4 + 4; ++mt) {
-            acc.o[mt][nh][j] += z;
-            acc.o[mt][nh][j + 2] += z;
+            acc.o[mt][nh][j] = fmaf(acc.o[mt][nh][j], acc.cap[grp] * (1.f / 32768.f), z);
+            acc.o[mt][nh][j + 2] = fmaf(acc.o[mt][nh][j + 2], acc.cap[grp] * (1.f / 32768.f), z);
           }
         }
       }
@@ -541,7 +570,7 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSM) paged_partial_kernel
   at.u = static_cast<int>((begin - before) / at.tiles);
   at.t = static_cast<int>((begin - before) % at.tiles);
 
-  const uint32_t ring = smem_u32(smem) + w * S::stages * S::stage;
+  const uint32_t ring = ((smem_u32(smem) + 255u) & ~255u) + w * S::stages * S::stage;
   const size_t lrow = p.layer_rows() * a.layer;
   const uint64_t policy = l2_evict_first_policy();
   Cursor ahead = at;   // the next tile to be requested
@@ -602,6 +631,7 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSM) paged_partial_kernel
       }
     }
     Acc<NH> acc;
+    acc.cap[0] = acc.cap[1] = 0x1p-26f;   // below every fp16 number but 0
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
 #pragma unroll
