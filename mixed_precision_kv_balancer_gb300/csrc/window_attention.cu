@@ -8,8 +8,8 @@
 //
 // A CTA holds two tiles of 128 query rows over one key head: the same rows of two heads of the
 // group, or 256 rows of one head where the group is odd.  Where a chunk has 64 rows or fewer, a
-// tile packs the rows of several heads of the group.  Where the items of a call leave SMs idle,
-// each is split over its key tiles and the parts are joined by a second kernel.  Key and value
+// tile packs the rows of several heads of the group.  Where the items of a call would leave SMs
+// idle, each is split over its key tiles and the parts are joined by a second kernel.  Key and value
 // tiles of 128 rows come through a ring of five 32 KB buffers (TMA, 128-byte swizzle); tiles
 // that none of the rows sees are not read.  Per key tile i and query tile t
 //   S_t = Q_t K_i^T     tcgen05, both operands in shared memory, 128 fp32 TMEM columns
@@ -29,6 +29,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "paged.cuh"
 #include "tcgen05.cuh"
@@ -669,7 +670,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
 }
 
 // Joins the parts of one query row: a warp per row, four channels a lane.
-template <bool BF>
+template <bool BF, int kBatch>
 __global__ void __launch_bounds__(128) window_join_kernel(const WindowArgs a) {
   pdl_wait();
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
@@ -680,15 +681,25 @@ __global__ void __launch_bounds__(128) window_join_kernel(const WindowArgs a) {
   const float2* ml = reinterpret_cast<const float2*>(a.part + a.splits * a.rows * kD) + at;
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < a.splits; ++s) {
-    const float2 x = ml[s * a.rows];
-    if (x.y == 0.f) continue;   // nothing seen there, and no sums written
-    const float4 os = reinterpret_cast<const float4*>(a.part + (s * a.rows + at) * kD)[lane];
-    const float mn = fmaxf(m, x.x), sub = mn == -INFINITY ? 0.f : mn;
-    const float f = ex2(m - sub), fs = ex2(x.x - sub);
-    l = l * f + x.y * fs;
-    o = make_float4(o.x * f + os.x * fs, o.y * f + os.y * fs, o.z * f + os.z * fs, o.w * f + os.w * fs);
-    m = mn;
+  for (int s0 = 0; s0 < a.splits; s0 += kBatch) {
+    float2 x[kBatch];
+    float4 os[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) x[e] = s0 + e < a.splits ? ml[(s0 + e) * a.rows] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      os[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      // a sum of 0: nothing seen there, and no sums written
+      if (x[e].y != 0.f) os[e] = reinterpret_cast<const float4*>(a.part + ((s0 + e) * a.rows + at) * kD)[lane];
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const float mn = fmaxf(m, x[e].x), sub = mn == -INFINITY ? 0.f : mn;
+      const float f = ex2(m - sub), fs = ex2(x[e].x - sub);
+      l = l * f + x[e].y * fs;
+      o = make_float4(o.x * f + os[e].x * fs, o.y * f + os[e].y * fs, o.z * f + os[e].z * fs, o.w * f + os[e].w * fs);
+      m = mn;
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   *reinterpret_cast<uint2*>(a.out.row(b, head, q) + lane * 8) = make_uint2(pack2<BF>(o.x * inv, o.y * inv), pack2<BF>(o.z * inv, o.w * inv));
@@ -712,14 +723,31 @@ Plan plan_of(int B, int Hq, int Hkv, int Tq, int Tk, int window, int sinks, bool
   p.pair_heads = p.groups % 2 == 0 || blocks == 1;
   p.blocks = p.pair_heads ? blocks : (blocks + 1) / 2;
   p.per_head = static_cast<int64_t>(p.blocks) * (p.pair_heads ? (p.groups + 1) / 2 : p.groups);
-  // Parts of an item, where the items would leave half the SMs idle or more: as many as fill them
-  // once, two key tiles each at least.  A part costs its sums' way through memory, 64 KB a tile
-  // out and in, about what two key tiles take.
+  // Parts of an item: the number that ends soonest by this estimate, in key tiles of an item's two
+  // query tiles (1.4 us each).  An item costs 3 beside its tiles, a part 12 (its sums go out to
+  // memory, 128 KB, and come back); the longest item bounds the end, and items of about one length
+  // run in whole waves.  Measured: 8192 causal rows of 4 heads, 128 items, 93 us whole and 72 in
+  // two parts each; 4096 rows of 8 heads, 128 items, 52 whole and 66 in two; 64 rows of 8 heads
+  // behind 16384 keys, 4 items, 26 us in 32 parts and 33 in 64.
   const int64_t items = p.per_head * Hkv * B;
-  int64_t keys = Tk;
-  if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + sinks + (p.pair_heads ? 1 : 2) * p.tb);
-  const int64_t tiles = (keys + kWaRows - 1) / kWaRows;
-  p.splits = static_cast<int>(std::max<int64_t>(1, std::min(kNumSMs / items, tiles / 2)));
+  const int64_t rows = static_cast<int64_t>(p.pair_heads ? 1 : 2) * p.tb;
+  double longest = Tk, mean = Tk - 0.5 * std::min(Tq, Tk);
+  if (window > 0) {
+    longest = std::min<double>(longest, static_cast<double>(window) + sinks + rows);
+    mean = std::min(mean, longest);
+  }
+  longest = std::max(1.0, longest / kWaRows);
+  mean = std::max(1.0, mean / kWaRows);
+  double best = 1e30;
+  for (int s = 1; s == 1 || (s <= 32 && longest / s >= 2.0); ++s) {
+    const double cost = s == 1 ? 3 : 12, waves = static_cast<double>(items) * s / kNumSMs;
+    const double even = mean > 0.75 * longest ? std::ceil(waves) : waves + 0.5;
+    const double est = std::max(longest / s + cost, even * (mean / s + cost));
+    if (est < best - 1e-9) {
+      best = est;
+      p.splits = s;
+    }
+  }
   return p;
 }
 size_t part_bytes(const Plan& p, int64_t rows) { return p.splits > 1 ? static_cast<size_t>(p.splits) * rows * (kD + 2) * 4 : 0; }
@@ -835,6 +863,8 @@ extern "C" int mikv_window_attention(const mikv_rows* q, const mikv_rows* k, con
   kern<<<dim3(static_cast<unsigned>(p.per_head * p.splits), Hkv, B), kWaThreads, kWaSmem, st>>>(qm, km, vm, a);
   if (int r = check_launch("window_attention_kernel")) return r;
   if (p.splits == 1) return MIKV_OK;
-  const auto join = bf ? window_join_kernel<true> : window_join_kernel<false>;
+  // parts requested together: few where there are few, so that more rows are under way
+  const auto join = p.splits <= 4 ? bf ? window_join_kernel<true, 2> : window_join_kernel<false, 2>
+                                  : bf ? window_join_kernel<true, 8> : window_join_kernel<false, 8>;
   return check_launch_after(launch_after(join, dim3(static_cast<unsigned>((a.rows + 3) / 4)), dim3(128), 0, st, a), "window_join_kernel");
 }

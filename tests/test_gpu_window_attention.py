@@ -67,7 +67,8 @@ def test_few_rows_over_many_keys(dtype, B, Hkv, rep, Tq, Tk, window, sinks):
     """Tiles that pack the rows of several heads, and items split over the keys; lengths of their own."""
     q = _make(B, Hkv * rep, Tq, dtype, "bthd", 1)
     k, v = _make(B, Hkv, Tk, dtype, "bhtd", 2), _make(B, Hkv, Tk, dtype, "bthd", 3)
-    assert _lib.load().mikv_window_attention_workspace_bytes(B, Hkv * rep, Hkv, Tq, Tk, window, sinks) > 0
+    if window == 0 and Tk >= 2500:      # long enough to be split
+        assert _lib.load().mikv_window_attention_workspace_bytes(B, Hkv * rep, Hkv, Tq, Tk, 0, 0) > 0
     _check(q, k, v, window, sinks)
     ql, kl = [max(0, Tq - 2 * b) for b in range(B)], [Tk - 131 * b for b in range(B)]
     kl[-1] = min(kl[-1], 200)                   # most parts see nothing
