@@ -92,6 +92,7 @@ struct Work {
   int pa[2], pb[2];       // positions of its first and last row
   int begin, end;         // the item's key tiles: of ts of the sinks, then tw0, tw0 + 1, ...
   int ts, tw0;
+  int ns;                 // key tiles that hold sinks, of either part of the list
   int from[2], last[2];   // query tile t sees the sinks' key tiles and tiles from .. last; last -1: none
   int nt;                 // query tiles
   __device__ __forceinline__ int j0(int i) const { return (i < ts ? i : tw0 + i - ts) * kWaRows; }
@@ -101,7 +102,7 @@ struct Tile {
   bool live;
   int group, q0, pa, pb, from, last;
   // Whether any of its rows sees key tile i.
-  __device__ __forceinline__ bool sees(int i, int ts) const { return i <= last && (i < ts || i >= from); }
+  __device__ __forceinline__ bool sees(int i, int ns) const { return i <= last && (i < ns || i >= from); }
 };
 __device__ __forceinline__ Tile tile_of(const Work& w, int t) {
   return {t < w.nt, t ? w.group[1] : w.group[0], t ? w.q0[1] : w.q0[0], t ? w.pa[1] : w.pa[0], t ? w.pb[1] : w.pb[0],
@@ -129,8 +130,12 @@ __device__ __forceinline__ Work work_of(const WindowArgs& a, int b, int x) {
   const int lo = a.window > 0 ? max(w.pa[0] - a.window + 1, 0) : 0;
   const int end = p1 < 0 ? 0 : p1 / kWaRows + 1;
   w.tw0 = min(lo / kWaRows, end);
-  w.ts = a.window > 0 ? min((min(a.sinks, w.kl) + kWaRows - 1) / kWaRows, w.tw0) : 0;
+  const int sink_tiles = a.window > 0 ? (min(a.sinks, w.kl) + kWaRows - 1) / kWaRows : 0;
+  w.ts = min(sink_tiles, w.tw0);
   const int tiles = w.ts + end - w.tw0;
+  // where the window begins among the sinks the list is 0, 1, 2, ... and its first sink_tiles hold
+  // sinks, which a later query tile sees though its own window begins behind them
+  w.ns = max(w.ts, min(sink_tiles, sink_tiles > w.tw0 ? tiles : w.ts));
   w.begin = SPLIT ? static_cast<int>(static_cast<int64_t>(tiles) * w.split / a.splits) : 0;
   w.end = SPLIT ? static_cast<int>(static_cast<int64_t>(tiles) * (w.split + 1) / a.splits) : tiles;
 #pragma unroll
@@ -140,7 +145,7 @@ __device__ __forceinline__ Work work_of(const WindowArgs& a, int b, int x) {
     int last = t >= w.nt || e < 0 ? -1 : e - w.tw0 + w.ts;
     if (SPLIT) {   // the last one of this part
       last = min(last, w.end - 1);
-      if (last < w.from[t]) last = min(last, w.ts - 1);
+      if (last < w.from[t]) last = min(last, w.ns - 1);
       if (last < w.begin) last = -1;
     }
     w.last[t] = last;
@@ -513,7 +518,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         // after a wait that gave up no lane leads, nothing more is issued, and the others' waits run out
         for (int i = w.begin; i <= w.end; ++i) {
           // this step's scores from key tile i, behind the last step's sums over value tile i - 1
-          const bool keys = i < w.end, here = keys && tile.sees(i, w.ts);
+          const bool keys = i < w.end, here = keys && tile.sees(i, w.ns);
           const uint64_t kd = k0 + slot * desc_step(tc::kTileBytes), vd = v0 + vslot * desc_step(tc::kTileBytes);
           if (i > w.begin) {
             wait(smem_u32(&bar.full[vslot]), vpar);
@@ -599,7 +604,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         const int p = tile.pa + row % a.tb;
         Row r;
         for (int i = w.begin; i < w.end; ++i) {
-          if (!tile.sees(i, w.ts)) continue;
+          if (!tile.sees(i, w.ns)) continue;
           const int j0 = w.j0(i);
           wait(smem_u32(&bar.s[t]), s_par);
           s_par ^= 1;

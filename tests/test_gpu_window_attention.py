@@ -89,6 +89,17 @@ def test_padded_batches(dtype, window, sinks):
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("rep", [1, 3])
+@pytest.mark.parametrize("Tq,Tk,window,sinks", [(500, 500, 100, 200), (400, 900, 128, 400), (300, 700, 1, 257), (700, 700, 130, 140),
+                                                (513, 513, 64, 513), (300, 3000, 600, 2500)])
+def test_windows_that_begin_among_the_sinks(dtype, rep, Tq, Tk, window, sinks):
+    """Odd groups: a CTA's two tiles are row blocks, and the second one's window begins later."""
+    q, k, v = _make(1, rep, Tq, dtype, "bhtd", 1), _make(1, 1, Tk, dtype, "bhtd", 2), _make(1, 1, Tk, dtype, "bhtd", 3)
+    _check(q, k, v, window, sinks)
+    _check(q, k, v, window, sinks, [Tq - 130], [Tk - 7])
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("Tq,Tk,window,sinks", [(20, 900, 100, 5), (300, 700, 30, 0), (1, 400, 1, 130), (5, 300, 40, 64),
                                                 (130, 1000, 513, 200)])
 def test_rows_that_no_query_sees_hold_anything(dtype, Tq, Tk, window, sinks):
