@@ -498,7 +498,7 @@ int mikv_paged_gather(const mikv_pages* p, int layer, const int32_t* seqs, int n
  *   l_j = q_h . k~_j / sqrt(D), out_h = sum_j exp(l_j - lse) v~_j, lse_h = log sum_j exp(l_j)
  * q, out [n][Hq][D] fp16 (bf16 for BF16 pages), lse fp32 [n][Hq] (natural log; NULL: not
  * written).  A sequence of length 0, or a number out of range, gives out 0 and lse -inf.
- * Hq a multiple of Hkv, any number of query heads per key head; slots that are not seen may
+ * Hq a multiple of Hkv, up to 1024 query heads per key head; slots that are not seen may
  * hold anything.  ws >= mikv_paged_attention_workspace_bytes(p, n, Hq, window, sinks), 16-byte
  * aligned; two calls must not share a workspace concurrently.
  * Errors: EINVAL (null, window < 0, sinks < 0), ESHAPE (layer, n outside 0..65535, Hq, workspace), EALIGN,
@@ -555,7 +555,9 @@ int mikv_set_attention_events(void* begin, void* end);
  * issues no further copy or MMA, its later waits poll only ~1000 times each (so a stuck
  * pipeline still ends in a bounded time, and what was issued before has that long to land),
  * the kernel writes NaN into the outputs of the affected CTA (prefill scores and -lse rows,
- * V.W_O norms, perturbation and y partial sums) and sets a bit in a device-side status word.
+ * V.W_O norms, perturbation and y partial sums, windowed attention's rows under way; rows that
+ * its CTA had taken over and not begun are left as they were) and sets a bit in a device-side
+ * status word.
  * The call that launched it has already returned MIKV_OK (launches are asynchronous).
  * mikv_wait_status stores the OR of the bits set since the last clear in *bits:
  *   1 = K3 pass 1 (row log-sum-exp), 2 = K3 pass 2 (column sums), 4 = K6 (V.W_O norms),

@@ -181,7 +181,7 @@ def mikv_score_update(mode, cache, q=None, k=None, T=0, hi_logits=None, lse=None
     w, nb = None, 0
     if mode == MIKV_PREFILL:
         dev = q.device
-        w, nb = _ws(lib.mikv_score_workspace_bytes(c.B, c.Hq, T), dev, ws)
+        w, nb = _ws(lib.mikv_score_workspace_bytes(c.B, c.Hq, T), dev, ws, stream)
     _check("mikv_score_update", lib.mikv_score_update(
         mode, _ptr(q), _ptr(k), T, _ptr(hi_logits), _ptr(lse), ctypes.byref(c),
         _ptr(scores_full), _ptr(scores_head), _ptr(w), nb, _stream(stream)))
@@ -193,7 +193,7 @@ def mikv_select(policy, cache, L, budget_pct, window, alpha=0.5, scores=None, sc
     lib = load()
     c = cache.struct if hasattr(cache, "struct") else cache
     dev = (scores if scores is not None else evict_pos).device
-    w, nb = _ws(lib.mikv_select_workspace_bytes(policy, c.B, c.Hkv, c.Hq, L, hidden), dev, ws)
+    w, nb = _ws(lib.mikv_select_workspace_bytes(policy, c.B, c.Hkv, c.Hq, L, hidden), dev, ws, stream)
     _check("mikv_select", lib.mikv_select(
         policy, ctypes.byref(c), L, budget_pct, window, float(alpha), _ptr(scores),
         _ptr(scores_head), _ptr(v), _ptr(w_o), hidden, _ptr(vwo_norm), _ptr(keep_pos),
@@ -301,12 +301,20 @@ def _rows(t, name, dtype, shape, device):
                      f"last dimension, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
-def _ws_on(nbytes, device, ws):
-    """(pointer, bytes, tensor to keep) of the workspace given, or of a new one of nbytes()."""
+def _ws_on(nbytes, device, ws, stream):
+    """(pointer, bytes, tensor to keep) of the workspace given, or of a new one of nbytes(), which
+    belongs to the stream of the call: freed on return, it is not handed out again before that
+    stream has come past the call."""
     if ws is None:
         n = nbytes()
-        ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
-        return (None, 0, None) if ws is None else (ws.data_ptr(), n, ws)
+        if n == 0:
+            return None, 0, None
+        if stream is None:
+            ws = torch.empty(n, dtype=torch.uint8, device=device)
+        else:
+            with torch.cuda.stream(stream):
+                ws = torch.empty(n, dtype=torch.uint8, device=device)
+        return ws.data_ptr(), n, ws
     if ws.device != device or not ws.is_contiguous():
         raise ValueError(f"ws: expected a contiguous tensor on {device}, got one on {ws.device}")
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
@@ -316,7 +324,7 @@ def mikv_page_reserve(pages, seqs, add, start, ws=None, stream=None):
     """Room for add int32 [n] more tokens behind sequences seqs (int32 [n], None: 0 .. n - 1);
     start int32 [n] receives each one's first new slot, or -1 where it was refused."""
     lib, dev, n = load(), pages.device, add.shape[0]
-    w, nb, _keep = _ws_on(lambda: lib.mikv_page_workspace_bytes(pages.ref, n), dev, ws)
+    w, nb, _keep = _ws_on(lambda: lib.mikv_page_workspace_bytes(pages.ref, n), dev, ws, stream)
     _launch(dev, stream, lib.mikv_page_reserve, pages.ref, _need(seqs, "seqs", torch.int32, (n,), dev),
             _need(add, "add", torch.int32, (n,), dev), n, _need(start, "start", torch.int32, (n,), dev), w, nb)
 
@@ -324,7 +332,7 @@ def mikv_page_reserve(pages, seqs, add, start, ws=None, stream=None):
 def mikv_page_fork(pages, parent, child, ok, ws=None, stream=None):
     """child[i] becomes a copy of parent[i] (int32 [n] each); ok int32 [n] receives 1, or 0 where refused."""
     lib, dev, n = load(), pages.device, parent.shape[0]
-    w, nb, _keep = _ws_on(lambda: lib.mikv_page_workspace_bytes(pages.ref, n), dev, ws)
+    w, nb, _keep = _ws_on(lambda: lib.mikv_page_workspace_bytes(pages.ref, n), dev, ws, stream)
     _launch(dev, stream, lib.mikv_page_fork, pages.ref, _need(parent, "parent", torch.int32, (n,), dev),
             _need(child, "child", torch.int32, (n,), dev), n, _need(ok, "ok", torch.int32, (n,), dev), w, nb)
 
@@ -347,7 +355,7 @@ def mikv_page_compact(pages, seqs, keep_pos, keep_n, ok, ws=None, stream=None):
     """Sequence seqs[i] keeps keep_n[i] slots per key head: keep_pos int32 [layers][n][Hkv][max_keep],
     keep_n and ok int32 [n]."""
     lib, dev, n, s = load(), pages.device, keep_n.shape[0], pages.struct
-    w, nb, _keep = _ws_on(lambda: lib.mikv_page_workspace_bytes(pages.ref, n), dev, ws)
+    w, nb, _keep = _ws_on(lambda: lib.mikv_page_workspace_bytes(pages.ref, n), dev, ws, stream)
     most = keep_pos.shape[-1]
     _launch(dev, stream, lib.mikv_page_compact, pages.ref, _need(seqs, "seqs", torch.int32, (n,), dev),
             _need(keep_pos, "keep_pos", torch.int32, (s.layers, n, s.Hkv, most), dev),
@@ -379,7 +387,7 @@ def mikv_paged_attention(q, pages, layer, window, sinks, out, lse=None, seqs=Non
     lib, dev, s = load(), pages.device, pages.struct
     n, Hq, _ = q.shape
     shape, dt = (n, Hq, s.D), _PAGE_DTYPE[s.type]
-    w, nb, _keep = _ws_on(lambda: lib.mikv_paged_attention_workspace_bytes(pages.ref, n, Hq, window, sinks), dev, ws)
+    w, nb, _keep = _ws_on(lambda: lib.mikv_paged_attention_workspace_bytes(pages.ref, n, Hq, window, sinks), dev, ws, stream)
     _launch(dev, stream, lib.mikv_paged_attention, _need(q, "q", dt, shape, dev), pages.ref, layer,
             _need(seqs, "seqs", torch.int32, (n,), dev), n, Hq, window, sinks, _need(out, "out", dt, shape, dev),
             _need(lse, "lse", torch.float32, (n, Hq), dev), w, nb)
@@ -394,7 +402,7 @@ def mikv_window_attention(q, k, v, window, sinks, out, lse=None, q_lens=None, k_
     if not q.is_cuda or dt not in (torch.float16, torch.bfloat16):
         raise ValueError(f"q: expected fp16 or bf16 on a CUDA device, got {dt} on {dev}")
     qs, ks = (B, Hq, Tq, D), (B, Hkv, Tk, D)
-    w, nb, _keep = _ws_on(lambda: lib.mikv_window_attention_workspace_bytes(B, Hq, Hkv, Tq, Tk, window, sinks), dev, ws)
+    w, nb, _keep = _ws_on(lambda: lib.mikv_window_attention_workspace_bytes(B, Hq, Hkv, Tq, Tk, window, sinks), dev, ws, stream)
     _launch(dev, stream, lib.mikv_window_attention, _rows(q, "q", dt, qs, dev), _rows(k, "k", dt, ks, dev),
             _rows(v, "v", dt, ks, dev), B, Hq, Hkv, Tq, Tk, D,
             MIKV_PAGES_BF16 if dt is torch.bfloat16 else MIKV_PAGES_FP16, _need(q_lens, "q_lens", torch.int32, (B,), dev),

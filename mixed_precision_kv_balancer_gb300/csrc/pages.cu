@@ -80,25 +80,26 @@ struct PlanArgs {
   int32_t* first;         // workspace: request i's first entry of `fresh`
 };
 
-// Inclusive sum over the block of `v`; `total` receives the block's sum.  `warp_sums` holds 32 ints.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+// Inclusive sum over the block of `v`; `total` receives the block's sum.  `warp_sums` holds 32 values.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T* warp_sums, T& total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    const T u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   __syncthreads();  // the previous call's sums have been read
   if (lane == 31) warp_sums[w] = v;
   __syncthreads();
-  int s = lane < (blockDim.x >> 5) ? warp_sums[lane] : 0;
+  T s = lane < (blockDim.x >> 5) ? warp_sums[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, s, o);
+    const T u = __shfl_up_sync(0xffffffffu, s, o);
     if (lane >= o) s += u;
   }
   total = __shfl_sync(0xffffffffu, s, (blockDim.x >> 5) - 1);
-  const int before = __shfl_sync(0xffffffffu, s, (w + 31) & 31);
+  const T before = __shfl_sync(0xffffffffu, s, (w + 31) & 31);
   return w ? v + before : v;
 }
 
@@ -120,8 +121,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const Pool p, c
   extern __shared__ int32_t sm[];
   int32_t* s_seq = sm;            // [n]
   int32_t* s_other = sm + a.n;    // [n]
-  int32_t* s_need = sm + 2 * a.n; // [n]: inclusive sums of the needs, later of the served ones
+  int32_t* s_need = sm + 2 * a.n; // [n]: new pages, -1 where the request is not valid
   __shared__ int warp_sums[32];
+  __shared__ int64_t warp_sums64[32];
   const int tid = threadIdx.x;
   pdl_wait();
   pdl_trigger();
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const Pool p, c
     s_other[i] = a.other[i];
   }
   __syncthreads();
-  int base = 0;
+  int64_t base = 0;   // of all requests: past 32 bits where they ask for more than any pool has
   for (int i0 = 0; i0 < a.n; i0 += kPlanThreads) {
     const int i = i0 + tid;
     int need = 0, ok = 0;
@@ -155,11 +157,11 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const Pool p, c
         }
       }
     }
-    int sum;
-    const int incl = block_scan(need, warp_sums, sum);
+    int64_t sum;
+    const int64_t incl = block_scan<int64_t>(need, warp_sums64, sum);
     if (i < a.n) {
-      s_need[i] = ok ? base + incl : -1;
-      a.first[i] = base + incl - need;
+      s_need[i] = ok ? need : -1;
+      a.first[i] = static_cast<int32_t>(min(base + incl - need, static_cast<int64_t>(0x7fffffff)));
     }
     base += sum;
   }
@@ -186,18 +188,22 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const Pool p, c
     found += sum;
   }
   __syncthreads();  // `fresh` and `first` are read below (and by the next launch)
-  const int avail = min(found, base);
+  const int64_t avail = min(static_cast<int64_t>(found), base);
+  const auto served = [&](int i) {
+    const int need = s_need[i];
+    return need == 0 || (need > 0 && static_cast<int64_t>(a.first[i]) + need <= avail);
+  };
   if (OP == Op::kReserve) {
     const int w = tid >> 5, lane = tid & 31;
     for (int i = w; i < a.n; i += kPlanThreads / 32) {
-      const int incl = s_need[i], f = a.first[i];
-      const bool ok = incl >= 0 && (incl <= avail || incl == f);
+      const int need = s_need[i], f = a.first[i];
+      const bool ok = served(i);
       const int32_t s = s_seq[i];
       const int len = ok ? p.len_of(s) : 0;
       __syncwarp();
       if (ok) {
         int32_t* row = p.table + static_cast<size_t>(s) * p.max_pages + pages_of(len, p.ps);
-        for (int j = lane; j < incl - f; j += 32) {
+        for (int j = lane; j < need; j += 32) {
           const int32_t page = a.fresh[f + j];
           row[j] = page;
           p.refs[page] = 1;
@@ -207,12 +213,10 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const Pool p, c
       if (lane == 0) a.flag[i] = ok ? len : -1;
     }
   } else {
-    for (int i = tid; i < a.n; i += kPlanThreads)
-      a.flag[i] = s_need[i] >= 0 && (s_need[i] <= avail || s_need[i] == a.first[i]);
+    for (int i = tid; i < a.n; i += kPlanThreads) a.flag[i] = served(i);
   }
 }
 
-// 16 bytes a lane; the copies below keep kUnroll of them in flight a thread.
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 64;   // rows of one CTA's move
 

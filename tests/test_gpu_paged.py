@@ -166,6 +166,30 @@ def test_other_streams_and_two_calls_at_once():
             assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
 
 
+def test_a_stream_given_by_name_owns_its_workspace():
+    """Calls on a stream that is not the current one, whose workspaces the binding makes itself."""
+    cache = ph.make([4000, 700], 16, 2, "fp16")
+    q = _query(2, 8, "fp16")
+    k, v = (ph.normal((1, 1, 5000, 128), s, torch.float16).to(ph.DEV) for s in (1, 2))
+    x = ph.normal((1, 2, 9, 128), 3, torch.float16).to(ph.DEV)
+    want = cache.attend(0, q)
+    ww = torch.empty_like(x)
+    _lib.mikv_window_attention(x, k, v, 0, 0, ww)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(20):
+        out, lse, wo = torch.empty_like(q), torch.empty(2, 8, device=ph.DEV), torch.empty_like(x)
+        side.wait_stream(torch.cuda.current_stream())
+        _lib.mikv_paged_attention(q, cache, 0, 0, 0, out, lse, stream=side)
+        _lib.mikv_window_attention(x, k, v, 0, 0, wo, stream=side)
+        torch.full((1 << 22,), float("nan"), device=ph.DEV)          # memory of the current stream, written at once
+        got.append((out, lse, wo))
+    torch.cuda.synchronize()
+    for out, lse, wo in got:
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(wo, ww)
+
+
 # --- rows in and out --------------------------------------------------------------------
 
 def _strided(shape, dtype, seed, layout):
@@ -374,6 +398,25 @@ def test_free_pages_are_found_anywhere(n_pages):
     assert start.tolist() == [0, 0, -1]
     got = cache.table[0, :1].tolist() + cache.table[1, :len(free) - 1].tolist()
     assert got == free and int(cache.refs.min()) == 1 and cache.lens.tolist() == [1, len(free) - 1, 0]
+
+
+def test_requests_whose_sum_passes_32_bits():
+    """4096 requests of 600000 pages each: only those that fit, in order, are served, and those that
+    need no page; the sum of all is 2.4e9."""
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GB of device memory")
+    S, width = 4096, 600000
+    cache = PagedCache(1, 700000, 1, 1, 128, S, width)
+    add = torch.full((S,), width, dtype=torch.int32, device=ph.DEV)
+    add[5] = add[S - 1] = 0
+    add[0] = 100000
+    start = cache.reserve(add)
+    want = torch.full((S,), -1, dtype=torch.int32, device=ph.DEV)
+    want[0] = want[1] = want[5] = want[S - 1] = 0
+    assert torch.equal(start, want)
+    assert int(cache.refs.sum()) == 700000 and cache.lens[:3].tolist() == [100000, 600000, 0] and int(cache.lens[2:].sum()) == 0
+    assert torch.equal(cache.table[1], torch.arange(100000, 700000, dtype=torch.int32, device=ph.DEV))
+    assert (cache.table[2:] == -1).all()
 
 
 def test_many_requests_of_one_call():
