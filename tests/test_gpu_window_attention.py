@@ -119,6 +119,14 @@ def test_rows_that_no_query_sees_hold_anything(dtype, Tq, Tk, window, sinks):
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("Hkv,rep,T,window,sinks", [(12, 2, 1200, 0, 0), (24, 1, 1900, 150, 3), (3, 5, 2500, 300, 140), (40, 2, 130, 0, 0)])
+def test_many_items_of_one_cta(dtype, Hkv, rep, T, window, sinks):
+    """Several items after one another in every CTA, of many lengths, empty ones among them."""
+    q, k, v = (_make(4, H, T, dtype, "bthd", s) for H, s in ((Hkv * rep, 1), (Hkv, 2), (Hkv, 3)))
+    _check(q, k, v, window, sinks, [T, T // 3, 0, T - 1], [T, T // 2, 9, T - 2])
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("drop", [9.0, 10.5, 14.0])
 def test_many_small_weights_beside_a_large_one(dtype, drop):
     q = torch.full((1, 1, 40, 128), 0.25, dtype=dtype, device=ph.DEV)
