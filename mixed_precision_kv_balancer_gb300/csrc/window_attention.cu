@@ -674,41 +674,67 @@ __global__ void __launch_bounds__(kWaThreads, 1)
   if (warp == kWaMmaWarp) tc::tmem_dealloc(tmem, kWaCols);
 }
 
-// Joins the parts of one query row: a warp per row, four channels a lane.
-template <bool BF, int kBatch>
+// One partial result of a row: maximum (log2 units), sum, four channels of the lane.
+struct Part {
+  float m, l;
+  float4 o;
+  __device__ __forceinline__ void add(float mb, float lb, const float4& ob) {
+    const float mn = fmaxf(m, mb), sub = mn == -INFINITY ? 0.f : mn;
+    const float f = ex2(m - sub), fb = ex2(mb - sub);
+    l = l * f + lb * fb;
+    o = make_float4(o.x * f + ob.x * fb, o.y * f + ob.y * fb, o.z * f + ob.z * fb, o.w * f + ob.w * fb);
+    m = mn;
+  }
+};
+// Joins the parts of query rows, in a fixed order, four channels a lane.  WARPS warps share a row,
+// each with every WARPS-th part, BATCH of them requested together.
+template <bool BF, int WARPS, int BATCH>
 __global__ void __launch_bounds__(128) window_join_kernel(const WindowArgs a) {
+  constexpr int kRows = 4 / WARPS;   // rows of a CTA
+  __shared__ float4 s_o[4][32];
+  __shared__ float2 s_ml[4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = warp % WARPS;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * kRows + warp / WARPS;
   pdl_wait();
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (at >= a.rows) return;
-  const int lane = threadIdx.x & 31;
-  const int q = static_cast<int>(at % a.Tq), head = static_cast<int>(at / a.Tq % a.Hq), b = static_cast<int>(at / a.Tq / a.Hq);
-  if (a.q_lens && q >= min(max(a.q_lens[b], 0), a.Tq)) return;
-  const float2* ml = reinterpret_cast<const float2*>(a.part + a.splits * a.rows * kD) + at;
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < a.splits; s0 += kBatch) {
-    float2 x[kBatch];
-    float4 os[kBatch];
+  bool live = at < a.rows;
+  const int64_t row = live ? at : 0;
+  const int q = static_cast<int>(row % a.Tq), head = static_cast<int>(row / a.Tq % a.Hq), b = static_cast<int>(row / a.Tq / a.Hq);
+  live = live && !(a.q_lens && q >= min(max(a.q_lens[b], 0), a.Tq));
+  Part sum = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (live) {
+    const float2* ml = reinterpret_cast<const float2*>(a.part + a.splits * a.rows * kD) + row;
+    for (int s0 = first; s0 < a.splits; s0 += BATCH * WARPS) {
+      float2 x[BATCH];
+      float4 os[BATCH];
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e) x[e] = s0 + e < a.splits ? ml[(s0 + e) * a.rows] : make_float2(-INFINITY, 0.f);
+      for (int e = 0; e < BATCH; ++e) {
+        const int s = s0 + e * WARPS;
+        x[e] = s < a.splits ? ml[s * a.rows] : make_float2(-INFINITY, 0.f);
+      }
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
-      os[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-      // a sum of 0: nothing seen there, and no sums written
-      if (x[e].y != 0.f) os[e] = reinterpret_cast<const float4*>(a.part + ((s0 + e) * a.rows + at) * kD)[lane];
-    }
+      for (int e = 0; e < BATCH; ++e) {
+        os[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        // a sum of 0: nothing seen there, and no sums written
+        if (x[e].y != 0.f) os[e] = reinterpret_cast<const float4*>(a.part + ((s0 + e * WARPS) * a.rows + row) * kD)[lane];
+      }
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
-      const float mn = fmaxf(m, x[e].x), sub = mn == -INFINITY ? 0.f : mn;
-      const float f = ex2(m - sub), fs = ex2(x[e].x - sub);
-      l = l * f + x[e].y * fs;
-      o = make_float4(o.x * f + os[e].x * fs, o.y * f + os[e].y * fs, o.z * f + os[e].z * fs, o.w * f + os[e].w * fs);
-      m = mn;
+      for (int e = 0; e < BATCH; ++e) sum.add(x[e].x, x[e].y, os[e]);
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<uint2*>(a.out.row(b, head, q) + lane * 8) = make_uint2(pack2<BF>(o.x * inv, o.y * inv), pack2<BF>(o.z * inv, o.w * inv));
-  if (lane == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + (log2f(l) - Weights<BF>::shift)) * 0.6931471805599453f;
+  if (WARPS > 1) {
+    s_o[warp][lane] = sum.o;
+    if (lane == 0) s_ml[warp] = make_float2(sum.m, sum.l);
+    __syncthreads();
+    if (first != 0) return;
+#pragma unroll
+    for (int e = 1; e < WARPS; ++e) sum.add(s_ml[warp + e].x, s_ml[warp + e].y, s_o[warp + e][lane]);
+  }
+  if (!live) return;
+  const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
+  *reinterpret_cast<uint2*>(a.out.row(b, head, q) + lane * 8) =
+      make_uint2(pack2<BF>(sum.o.x * inv, sum.o.y * inv), pack2<BF>(sum.o.z * inv, sum.o.w * inv));
+  if (lane == 0 && a.lse)
+    a.lse[row] = sum.l == 0.f ? -INFINITY : (sum.m + (log2f(sum.l) - Weights<BF>::shift)) * 0.6931471805599453f;
 }
 
 // The split of a call: rows and heads of a tile, items, and parts of each item.
@@ -868,8 +894,14 @@ extern "C" int mikv_window_attention(const mikv_rows* q, const mikv_rows* k, con
   kern<<<dim3(static_cast<unsigned>(p.per_head * p.splits), Hkv, B), kWaThreads, kWaSmem, st>>>(qm, km, vm, a);
   if (int r = check_launch("window_attention_kernel")) return r;
   if (p.splits == 1) return MIKV_OK;
-  // parts requested together: few where there are few, so that more rows are under way
-  const auto join = p.splits <= 4 ? bf ? window_join_kernel<true, 2> : window_join_kernel<false, 2>
-                                  : bf ? window_join_kernel<true, 8> : window_join_kernel<false, 8>;
-  return check_launch_after(launch_after(join, dim3(static_cast<unsigned>((a.rows + 3) / 4)), dim3(128), 0, st, a), "window_join_kernel");
+  // Two parts at a time of rows enough to hide it, eight where a row has more; and four warps a row
+  // where there are not eight rows an SM (five rows of 8 heads, 32 parts: 18 us with one warp a row,
+  // 13 with four; 4096 rows, 9 parts: 30 and 35).
+  const bool few = p.splits <= 4, wide = !few && a.rows <= 8 * kNumSMs;
+  const auto join = few    ? bf ? window_join_kernel<true, 1, 2> : window_join_kernel<false, 1, 2>
+                    : wide ? bf ? window_join_kernel<true, 4, 8> : window_join_kernel<false, 4, 8>
+                           : bf ? window_join_kernel<true, 1, 8> : window_join_kernel<false, 1, 8>;
+  const int64_t per = wide ? 1 : 4;
+  return check_launch_after(launch_after(join, dim3(static_cast<unsigned>((a.rows + per - 1) / per)), dim3(128), 0, st, a),
+                            "window_join_kernel");
 }
