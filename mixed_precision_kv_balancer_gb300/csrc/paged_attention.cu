@@ -663,13 +663,29 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSM) paged_partial_kernel
   }
 }
 
-// CTA (unit, row b): joins the parts of a unit that several warps held, in their order, and
-// answers for the units without a visible slot.  A warp per query head, four channels a lane.
-template <int TYPE>
+// One partial result of a query head: maximum, sum, four channels of the lane.
+struct Part {
+  float m, l;
+  float4 o;
+  __device__ __forceinline__ void add(float mb, float lb, const float4& ob) {
+    const float mn = fmaxf(m, mb), sub = mn == -INFINITY ? 0.f : mn;
+    const float f = ex2(m - sub), fb = ex2(mb - sub);
+    l = l * f + lb * fb;
+    o = make_float4(o.x * f + ob.x * fb, o.y * f + ob.y * fb, o.z * f + ob.z * fb, o.w * f + ob.w * fb);
+    m = mn;
+  }
+};
+
+// CTA (unit, row b, and where WARPS is 4 the query head): joins the parts of a unit that several
+// warps held, in a fixed order, and answers for the units without a visible slot.  Four channels
+// a lane; WARPS warps share a head, each with every WARPS-th part, BATCH of them requested together.
+template <int TYPE, int WARPS, int BATCH>
 __global__ void __launch_bounds__(kPaThreads) paged_merge_kernel(const AttendArgs a, int warps) {
   using S = Shape<TYPE>;
   __shared__ int64_t warp_sums[kPaWarps];
-  const int units = a.p.Hkv * a.groups, b = blockIdx.y, u = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  __shared__ float4 s_o[kPaWarps][32];
+  __shared__ float2 s_ml[kPaWarps];
+  const int units = a.p.Hkv * a.groups, b = blockIdx.y, u = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rows = min(a.heads, a.rep - u % a.groups * a.heads);
   int64_t mine = 0, below = 0, total, base;
   for (int i = tid; i < a.n; i += kPaThreads) {
@@ -682,32 +698,45 @@ __global__ void __launch_bounds__(kPaThreads) paged_merge_kernel(const AttendArg
   const int tiles = row_tiles<S::tw>(a, b);
   const int workers = workers_of(total, warps);
   const int64_t first = base + static_cast<int64_t>(u) * tiles;
-  const int c0 = tiles ? split_owner(total, workers, first) : 0, c1 = tiles ? split_owner(total, workers, first + tiles - 1) : 0;
+  const int c0 = tiles ? split_owner(total, workers, first) : 0, c1 = tiles ? split_owner(total, workers, first + tiles - 1) : -1;
+  const int skip = tiles && split_begin(total, workers, c0) < first ? 1 : 0;   // c0 holds it as its second part
   pdl_wait();
   if (tiles > 0 && c0 == c1) return;   // finished by its warp
-  const int skip = tiles && split_begin(total, workers, c0) < first ? 1 : 0;   // c0 holds it as its second part
-  for (int row = tid >> 5; row < rows; row += kPaWarps) {
-    const size_t at = static_cast<size_t>(b) * a.Hq + u / a.groups * a.rep + u % a.groups * a.heads + row;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (tiles > 0) {
-#pragma unroll 4
-      for (int c = c0; c <= c1; ++c) {
-        const float* q = a.part + (static_cast<size_t>(c) * 2 + (c == c0 ? skip : 0)) * kPartFloats;
-        const float mc = q[kPaRows * kD + row], lc = q[kPaRows * kD + kPaRows + row];
-        const float4 oc = reinterpret_cast<const float4*>(q + row * kD)[lane];
-        const float mn = fmaxf(m, mc), sub = mn == -INFINITY ? 0.f : mn;
-        const float f = ex2(m - sub), fc = ex2(mc - sub);
-        l = l * f + lc * fc;
-        o = make_float4(o.x * f + oc.x * fc, o.y * f + oc.y * fc, o.z * f + oc.z * fc, o.w * f + oc.w * fc);
-        m = mn;
+  for (int row = WARPS > 1 ? blockIdx.z : warp; row < rows; row += WARPS > 1 ? rows : kPaWarps) {
+    Part sum = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int cb = c0 + (WARPS > 1 ? warp : 0); cb <= c1; cb += BATCH * WARPS) {
+      float m[BATCH], l[BATCH];
+      float4 o[BATCH];
+#pragma unroll
+      for (int e = 0; e < BATCH; ++e) {
+        const int c = cb + e * WARPS;
+        m[e] = -INFINITY;
+        l[e] = 0.f;
+        o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c <= c1) {
+          const float* q = a.part + (static_cast<size_t>(c) * 2 + (c == c0 ? skip : 0)) * kPartFloats;
+          m[e] = q[kPaRows * kD + row];
+          l[e] = q[kPaRows * kD + kPaRows + row];
+          o[e] = reinterpret_cast<const float4*>(q + row * kD)[lane];
+        }
       }
+#pragma unroll
+      for (int e = 0; e < BATCH; ++e) sum.add(m[e], l[e], o[e]);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (WARPS > 1) {
+      s_o[warp][lane] = sum.o;
+      if (lane == 0) s_ml[warp] = make_float2(sum.m, sum.l);
+      __syncthreads();
+      if (warp != 0) return;
+#pragma unroll
+      for (int e = 1; e < WARPS; ++e) sum.add(s_ml[e].x, s_ml[e].y, s_o[e][lane]);
+    }
+    const size_t at = static_cast<size_t>(b) * a.Hq + u / a.groups * a.rep + u % a.groups * a.heads + row;
+    const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
     *reinterpret_cast<uint2*>(a.out + at * kD + 4 * lane) =
-        make_uint2(static_cast<uint32_t>(to_out<TYPE>(o.x * inv)) | static_cast<uint32_t>(to_out<TYPE>(o.y * inv)) << 16,
-                   static_cast<uint32_t>(to_out<TYPE>(o.z * inv)) | static_cast<uint32_t>(to_out<TYPE>(o.w * inv)) << 16);
-    if (lane == 0 && a.lse) a.lse[at] = lse_of<TYPE>(m, l);
+        make_uint2(static_cast<uint32_t>(to_out<TYPE>(sum.o.x * inv)) | static_cast<uint32_t>(to_out<TYPE>(sum.o.y * inv)) << 16,
+                   static_cast<uint32_t>(to_out<TYPE>(sum.o.z * inv)) | static_cast<uint32_t>(to_out<TYPE>(sum.o.w * inv)) << 16);
+    if (lane == 0 && a.lse) a.lse[at] = lse_of<TYPE>(sum.m, sum.l);
   }
 }
 
@@ -729,8 +758,12 @@ int launch(const AttendArgs& a, int grid, cudaStream_t st) {
   if (e != cudaSuccess) return check_launch_after(e, "paged_partial_kernel");
   kern<<<grid, kPaThreads, Shape<TYPE>::smem, st>>>(a);
   if (int r = check_launch("paged_partial_kernel")) return r;
-  return check_launch_after(launch_after(paged_merge_kernel<TYPE>, dim3(a.p.Hkv * a.groups, a.n), dim3(kPaThreads), 0, st, a, grid * kPaWarps),
-                            "paged_merge_kernel");
+  // Few units have many parts each: a CTA per query head then, four warps with eight parts at a time.
+  const int units = a.p.Hkv * a.groups;
+  const bool many = static_cast<int64_t>(units) * a.n * 8 <= grid * kPaWarps;
+  const auto merge = many ? paged_merge_kernel<TYPE, kPaWarps, 8> : paged_merge_kernel<TYPE, 1, 4>;
+  return check_launch_after(
+      launch_after(merge, dim3(units, a.n, many ? a.heads : 1), dim3(kPaThreads), 0, st, a, grid * kPaWarps), "paged_merge_kernel");
 }
 
 }  // namespace
