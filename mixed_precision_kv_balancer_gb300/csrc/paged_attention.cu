@@ -41,6 +41,7 @@ constexpr int kPaThreads = 128;
 constexpr int kPaWarps = 4;
 constexpr int kPaRows = 16;       // query heads of a unit at most: two column blocks of the mma
 constexpr int kPaCtasPerSM = 2;
+constexpr int kMergeWarps = 16;   // of one head's join, where it has many parts
 
 template <int TYPE>
 struct Shape {
@@ -122,6 +123,7 @@ __device__ __forceinline__ int row_tiles(const AttendArgs& a, int b) {
 }
 
 // Sums over the block's threads below this one (inclusive) and over all of them.
+template <int W = kPaWarps>
 __device__ __forceinline__ int64_t scan64(int64_t v, int64_t* warp_sums, int64_t& total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
@@ -135,7 +137,7 @@ __device__ __forceinline__ int64_t scan64(int64_t v, int64_t* warp_sums, int64_t
   int64_t before = 0;
   total = 0;
 #pragma unroll
-  for (int i = 0; i < kPaWarps; ++i) {
+  for (int i = 0; i < W; ++i) {
     if (i < w) before += warp_sums[i];
     total += warp_sums[i];
   }
@@ -676,25 +678,26 @@ struct Part {
   }
 };
 
-// CTA (unit, row b, and where WARPS is 4 the query head): joins the parts of a unit that several
+// CTA (unit, row b, and where WARPS is above 1 the query head): joins the parts of a unit that several
 // warps held, in a fixed order, and answers for the units without a visible slot.  Four channels
 // a lane; WARPS warps share a head, each with every WARPS-th part, BATCH of them requested together.
 template <int TYPE, int WARPS, int BATCH>
-__global__ void __launch_bounds__(kPaThreads) paged_merge_kernel(const AttendArgs a, int warps) {
+__global__ void __launch_bounds__(WARPS > 1 ? WARPS * 32 : kPaThreads) paged_merge_kernel(const AttendArgs a, int warps) {
   using S = Shape<TYPE>;
-  __shared__ int64_t warp_sums[kPaWarps];
-  __shared__ float4 s_o[kPaWarps][32];
-  __shared__ float2 s_ml[kPaWarps];
+  constexpr int W = WARPS > 1 ? WARPS : kPaWarps;   // warps of the CTA
+  __shared__ int64_t warp_sums[W];
+  __shared__ float4 s_o[W][32];
+  __shared__ float2 s_ml[W];
   const int units = a.p.Hkv * a.groups, b = blockIdx.y, u = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rows = min(a.heads, a.rep - u % a.groups * a.heads);
   int64_t mine = 0, below = 0, total, base;
-  for (int i = tid; i < a.n; i += kPaThreads) {
+  for (int i = tid; i < a.n; i += W * 32) {
     const int x = row_tiles<S::tw>(a, i);
     mine += x;
     if (i < b) below += x;
   }
-  scan64(mine * units, warp_sums, total);
-  scan64(below * units, warp_sums, base);
+  scan64<W>(mine * units, warp_sums, total);
+  scan64<W>(below * units, warp_sums, base);
   const int tiles = row_tiles<S::tw>(a, b);
   const int workers = workers_of(total, warps);
   const int64_t first = base + static_cast<int64_t>(u) * tiles;
@@ -758,12 +761,13 @@ int launch(const AttendArgs& a, int grid, cudaStream_t st) {
   if (e != cudaSuccess) return check_launch_after(e, "paged_partial_kernel");
   kern<<<grid, kPaThreads, Shape<TYPE>::smem, st>>>(a);
   if (int r = check_launch("paged_partial_kernel")) return r;
-  // Few units have many parts each: a CTA per query head then, four warps with eight parts at a time.
+  // Few units have many parts each: a CTA per query head then, 16 warps with eight parts at a time (one
+  // sequence of 65536 slots, one key head, 1216 parts: 661 us with a warp per head, 68 with four, 21 so).
   const int units = a.p.Hkv * a.groups;
   const bool many = static_cast<int64_t>(units) * a.n * 8 <= grid * kPaWarps;
-  const auto merge = many ? paged_merge_kernel<TYPE, kPaWarps, 8> : paged_merge_kernel<TYPE, 1, 4>;
+  const auto merge = many ? paged_merge_kernel<TYPE, kMergeWarps, 8> : paged_merge_kernel<TYPE, 1, 4>;
   return check_launch_after(
-      launch_after(merge, dim3(units, a.n, many ? a.heads : 1), dim3(kPaThreads), 0, st, a, grid * kPaWarps), "paged_merge_kernel");
+      launch_after(merge, dim3(units, a.n, many ? a.heads : 1), dim3(many ? kMergeWarps * 32 : kPaThreads), 0, st, a, grid * kPaWarps), "paged_merge_kernel");
 }
 
 }  // namespace

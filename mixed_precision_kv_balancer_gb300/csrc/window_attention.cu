@@ -308,9 +308,10 @@ __device__ __forceinline__ void softmax_tile(const WindowArgs& a, uint32_t ts, u
   const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
   const bool grew = (top - r.m) * a.scale > Weights<BF>::grow;   // from -inf too; never by NaN
   if (__any_sync(0xffffffffu, grew)) {
-    const float m = fmaxf(r.m, top);
-    const float alpha = m == -INFINITY ? 1.f : ex2((r.m - m) * a.scale);
-    r.m = m;
+    // a row whose own maximum has not outgrown its reference keeps it: its result does not hang on
+    // the other rows of the warp, which may be rows that do not count
+    const float alpha = grew ? ex2((r.m - top) * a.scale) : 1.f;
+    if (grew) r.m = top;
     r.l *= alpha;
     if (!r.first) {
 #pragma unroll 1

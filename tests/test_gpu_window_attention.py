@@ -169,6 +169,23 @@ def test_the_same_bits_every_time_and_in_a_graph():
     assert torch.equal(out, again) and not torch.equal(out, want[0])
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_rows_do_not_hang_on_rows_that_do_not_count(dtype):
+    """The same bits whatever lies behind the queries' end, and beside them in a tile."""
+    q, k, v = _make(1, 2, 40, dtype, "bhtd", 1), _make(1, 1, 3000, dtype, "bhtd", 2), _make(1, 1, 3000, dtype, "bhtd", 3)
+    k[..., 0] = torch.linspace(-6, 6, 3000, device=ph.DEV).to(dtype)      # the maxima move along the keys
+    out, lse = _run(q, k, v, 0, 0, [9], [2500])
+    for fill in (100.0, float("inf"), float("nan"), 0.0):
+        q[:, :, 9:] = fill
+        o2, l2 = _run(q, k, v, 0, 0, [9], [2500])
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+    want = [x[:, :, :1] for x in _run(q[:, :, :9].contiguous(), k, v, 0, 0, [9], [2500])]
+    for n in range(20):                                                    # tiles that hold what the last call left
+        _run(_make(1, 2, 128, dtype, "bhtd", n) * 30, k, v, 0, 0)
+        got = _run(q[:, :, :9].contiguous(), k, v, 0, 0, [9], [2500])
+        assert all(torch.equal(a[:, :, :1], b) for a, b in zip(got, want))
+
+
 def test_lse_may_be_left_out_and_rows_broadcast():
     q, k, v = (_make(2, 2, 90, torch.float16, "bhtd", s) for s in (1, 2, 3))
     k, v = k[:1].expand(2, 2, 90, 128), v[:, :1].expand(2, 2, 90, 128)
