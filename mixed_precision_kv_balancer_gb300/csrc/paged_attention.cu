@@ -761,13 +761,18 @@ int launch(const AttendArgs& a, int grid, cudaStream_t st) {
   if (e != cudaSuccess) return check_launch_after(e, "paged_partial_kernel");
   kern<<<grid, kPaThreads, Shape<TYPE>::smem, st>>>(a);
   if (int r = check_launch("paged_partial_kernel")) return r;
-  // Few units have many parts each: a CTA per query head then, 16 warps with eight parts at a time (one
-  // sequence of 65536 slots, one key head, 1216 parts: 661 us with a warp per head, 68 with four, 21 so).
+  // Parts that a unit has where all are of one length, and the warps that join a head: one sequence
+  // of 65536 slots and one key head, 1216 parts: 661 us with one warp a head, 68 with four, 22 with
+  // 16; 16 sequences of 2048 and 8 key heads, 9 parts: 30, 27 and 35 us.
   const int units = a.p.Hkv * a.groups;
-  const bool many = static_cast<int64_t>(units) * a.n * 8 <= grid * kPaWarps;
-  const auto merge = many ? paged_merge_kernel<TYPE, kMergeWarps, 8> : paged_merge_kernel<TYPE, 1, 4>;
-  return check_launch_after(
-      launch_after(merge, dim3(units, a.n, many ? a.heads : 1), dim3(many ? kMergeWarps * 32 : kPaThreads), 0, st, a, grid * kPaWarps), "paged_merge_kernel");
+  const int64_t parts = grid * kPaWarps / (static_cast<int64_t>(units) * a.n);
+  const bool many = parts >= 16, some = !many && parts >= 5;
+  const auto merge = many   ? paged_merge_kernel<TYPE, kMergeWarps, 8>
+                     : some ? paged_merge_kernel<TYPE, kPaWarps, 8>
+                            : paged_merge_kernel<TYPE, 1, 4>;
+  return check_launch_after(launch_after(merge, dim3(units, a.n, many || some ? a.heads : 1),
+                                         dim3(many ? kMergeWarps * 32 : kPaThreads), 0, st, a, grid * kPaWarps),
+                            "paged_merge_kernel");
 }
 
 }  // namespace
