@@ -27,6 +27,7 @@ attention  decode attention over the two-tier cache (float64); post-attention to
 perturbation  the step after attention: o . W_O and the CriticalKV per-head perturbation
 channel_quant  per-channel key quantisation with pending-token buffering (Appendix C alternative)
 pipeline   prefill + decode steps composed into one cache, the whole path
+paged      pages of a cache (reserve, fork, free, copy, compact), attention under a window with sinks
 
 Parity pins for every function live in ``tests/test_oracle_*.py``.
 """
