@@ -6,6 +6,7 @@ There is no fallback; if the library is missing or a call fails, this raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -393,6 +394,11 @@ def mikv_paged_attention(q, pages, layer, window, sinks, out, lse=None, seqs=Non
             _need(lse, "lse", torch.float32, (n, Hq), dev), w, nb)
 
 
+@functools.lru_cache(maxsize=1024)
+def _window_workspace_bytes(*dims):   # a function of the dimensions alone
+    return load().mikv_window_attention_workspace_bytes(*dims)
+
+
 def mikv_window_attention(q, k, v, window, sinks, out, lse=None, q_lens=None, k_lens=None, ws=None, stream=None):
     """A prompt's or a chunk's attention: q, out [B][Hq][Tq][D], k, v [B][Hkv][Tk][D] (strided; all fp16 or
     all bf16), lse fp32 [B][Hq][Tq], q_lens, k_lens int32 [B] (None: Tq, Tk)."""
@@ -402,7 +408,7 @@ def mikv_window_attention(q, k, v, window, sinks, out, lse=None, q_lens=None, k_
     if not q.is_cuda or dt not in (torch.float16, torch.bfloat16):
         raise ValueError(f"q: expected fp16 or bf16 on a CUDA device, got {dt} on {dev}")
     qs, ks = (B, Hq, Tq, D), (B, Hkv, Tk, D)
-    w, nb, _keep = _ws_on(lambda: lib.mikv_window_attention_workspace_bytes(B, Hq, Hkv, Tq, Tk, window, sinks), dev, ws, stream)
+    w, nb, _keep = _ws_on(lambda: _window_workspace_bytes(B, Hq, Hkv, Tq, Tk, window, sinks), dev, ws, stream)
     _launch(dev, stream, lib.mikv_window_attention, _rows(q, "q", dt, qs, dev), _rows(k, "k", dt, ks, dev),
             _rows(v, "v", dt, ks, dev), B, Hq, Hkv, Tq, Tk, D,
             MIKV_PAGES_BF16 if dt is torch.bfloat16 else MIKV_PAGES_FP16, _need(q_lens, "q_lens", torch.int32, (B,), dev),

@@ -552,11 +552,11 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSM) paged_partial_kernel
       const int64_t v = b0 == 0 ? head : b < a.n ? row_tiles<S::tw>(a, b) : 0;
       incl = before + scan64(v * units, warp_sums, sum);
     }
-    __syncthreads();   // the last round's sums have been read
+    __syncthreads();   // the last pass's sums have been read
     s_incl[tid] = incl;
     __syncthreads();
     if (!idle && at.b < 0 && begin < before + sum) {
-      int below = 0;   // rows of this round that end at or before `begin`
+      int below = 0;   // rows of this pass that end at or before `begin`
 #pragma unroll
       for (int i = 0; i < kPaThreads; i += 32) below += __popc(__ballot_sync(0xffffffffu, s_incl[i + lane] <= begin));
       at.b = b0 + below;
