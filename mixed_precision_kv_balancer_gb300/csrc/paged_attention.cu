@@ -678,7 +678,7 @@ struct Part {
   }
 };
 
-// CTA (unit, row b, and where WARPS is above 1 the query head): joins the parts of a unit that several
+// CTA (unit, row b, query head, or four heads where WARPS is 1): joins the parts of a unit that several
 // warps held, in a fixed order, and answers for the units without a visible slot.  Four channels
 // a lane; WARPS warps share a head, each with every WARPS-th part, BATCH of them requested together.
 template <int TYPE, int WARPS, int BATCH>
@@ -705,7 +705,8 @@ __global__ void __launch_bounds__(WARPS > 1 ? WARPS * 32 : kPaThreads) paged_mer
   const int skip = tiles && split_begin(total, workers, c0) < first ? 1 : 0;   // c0 holds it as its second part
   pdl_wait();
   if (tiles > 0 && c0 == c1) return;   // finished by its warp
-  for (int row = WARPS > 1 ? blockIdx.z : warp; row < rows; row += WARPS > 1 ? rows : kPaWarps) {
+  const int row = WARPS > 1 ? blockIdx.z : blockIdx.z * kPaWarps + warp;   // the query head of the group
+  if (row < rows) {
     Part sum = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     for (int cb = c0 + (WARPS > 1 ? warp : 0); cb <= c1; cb += BATCH * WARPS) {
       float m[BATCH], l[BATCH];
@@ -766,11 +767,12 @@ int launch(const AttendArgs& a, int grid, cudaStream_t st) {
   // 16; 16 sequences of 2048 and 8 key heads, 9 parts: 30, 27 and 35 us.
   const int units = a.p.Hkv * a.groups;
   const int64_t parts = grid * kPaWarps / (static_cast<int64_t>(units) * a.n);
-  const bool many = parts >= 16, some = !many && parts >= 5;
+  const int64_t joins = static_cast<int64_t>(units) * a.n * a.heads;   // CTAs of the two wider forms
+  const bool many = parts >= 16 && joins <= 2 * kNumSMs, some = !many && parts >= 5 && joins <= 8 * kNumSMs;
   const auto merge = many   ? paged_merge_kernel<TYPE, kMergeWarps, 8>
                      : some ? paged_merge_kernel<TYPE, kPaWarps, 8>
                             : paged_merge_kernel<TYPE, 1, 4>;
-  return check_launch_after(launch_after(merge, dim3(units, a.n, many || some ? a.heads : 1),
+  return check_launch_after(launch_after(merge, dim3(units, a.n, many || some ? a.heads : (a.heads + kPaWarps - 1) / kPaWarps),
                                          dim3(many ? kMergeWarps * 32 : kPaThreads), 0, st, a, grid * kPaWarps),
                             "paged_merge_kernel");
 }

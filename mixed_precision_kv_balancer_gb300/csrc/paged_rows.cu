@@ -161,7 +161,7 @@ __device__ __forceinline__ uint4 values_of(uint2 c, __half2 m) {
 // CTA (chunk, head, row i): slots chunk * 32 .. of row i's sequence, as far as it reaches, to
 // rows of k and v.  Rows past the sequence's end keep what they hold.
 template <bool Q8>
-__global__ void __launch_bounds__(kRowThreads, 10) paged_gather_kernel(const Pool p, int layer, RowView k, RowView v, int T,
+__global__ void __launch_bounds__(kRowThreads, 8) paged_gather_kernel(const Pool p, int layer, RowView k, RowView v, int T,
                                                                    const int32_t* __restrict__ seqs) {
   __shared__ uint32_t at[kRowTokens];
   const int i = blockIdx.z, h = blockIdx.y, t0 = blockIdx.x * kRowTokens;
@@ -172,22 +172,31 @@ __global__ void __launch_bounds__(kRowThreads, 10) paged_gather_kernel(const Poo
   find_rows(p, s, h, t0, rows, at);
   const size_t lrow = p.layer_rows() * layer;
   uint4 a[4], b[4];
+  bool ok[4];
+  uint2 ca[4], cb[4];
+  __half2 ma[4], mb[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {   // all requested before the first is used; without a page, row 0 of the layer
+    const int c = threadIdx.x + u * kRowThreads, r = c >> 4, piece = c & 15;
+    ok[u] = r < rows && at[r] != kNoRow;
+    const size_t row = lrow + (ok[u] ? at[r] : 0);
+    if (!Q8) {
+      a[u] = *reinterpret_cast<const uint4*>(p.k + row * (kD * 2) + piece * 16);
+      b[u] = *reinterpret_cast<const uint4*>(p.v + row * (kD * 2) + piece * 16);
+    } else {
+      ca[u] = *reinterpret_cast<const uint2*>(p.k + row * kD + piece * 8);
+      cb[u] = *reinterpret_cast<const uint2*>(p.v + row * kD + piece * 8);
+      ma[u] = reinterpret_cast<const __half2*>(p.km + row * kMetaBytes)[piece >> 3];
+      mb[u] = reinterpret_cast<const __half2*>(p.vm + row * kMetaBytes)[piece >> 3];
+    }
+  }
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const int c = threadIdx.x + u * kRowThreads, r = c >> 4, piece = c & 15;
-    if (r >= rows || at[r] == kNoRow) {
-      a[u] = b[u] = make_uint4(0, 0, 0, 0);  // a slot without a page reads as zeros
-    } else if (!Q8) {
-      const size_t off = (lrow + at[r]) * (kD * 2) + piece * 16;
-      a[u] = *reinterpret_cast<const uint4*>(p.k + off);
-      b[u] = *reinterpret_cast<const uint4*>(p.v + off);
-    } else {
-      const size_t row = lrow + at[r];
-      const __half2* mk = reinterpret_cast<const __half2*>(p.km + row * kMetaBytes);
-      const __half2* mv = reinterpret_cast<const __half2*>(p.vm + row * kMetaBytes);
-      a[u] = values_of(*reinterpret_cast<const uint2*>(p.k + row * kD + piece * 8), mk[piece >> 3]);
-      b[u] = values_of(*reinterpret_cast<const uint2*>(p.v + row * kD + piece * 8), mv[piece >> 3]);
+    if (Q8) {
+      a[u] = values_of(ca[u], ma[u]);
+      b[u] = values_of(cb[u], mb[u]);
     }
+    if (!ok[u]) a[u] = b[u] = make_uint4(0, 0, 0, 0);  // a slot without a page reads as zeros
   }
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
