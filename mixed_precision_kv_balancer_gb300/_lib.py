@@ -182,7 +182,7 @@ def mikv_score_update(mode, cache, q=None, k=None, T=0, hi_logits=None, lse=None
     w, nb = None, 0
     if mode == MIKV_PREFILL:
         dev = q.device
-        w, nb = _ws(lib.mikv_score_workspace_bytes(c.B, c.Hq, T), dev, ws, stream)
+        w, nb = _ws(lib.mikv_score_workspace_bytes(c.B, c.Hq, T), dev, ws)
     _check("mikv_score_update", lib.mikv_score_update(
         mode, _ptr(q), _ptr(k), T, _ptr(hi_logits), _ptr(lse), ctypes.byref(c),
         _ptr(scores_full), _ptr(scores_head), _ptr(w), nb, _stream(stream)))
@@ -194,7 +194,7 @@ def mikv_select(policy, cache, L, budget_pct, window, alpha=0.5, scores=None, sc
     lib = load()
     c = cache.struct if hasattr(cache, "struct") else cache
     dev = (scores if scores is not None else evict_pos).device
-    w, nb = _ws(lib.mikv_select_workspace_bytes(policy, c.B, c.Hkv, c.Hq, L, hidden), dev, ws, stream)
+    w, nb = _ws(lib.mikv_select_workspace_bytes(policy, c.B, c.Hkv, c.Hq, L, hidden), dev, ws)
     _check("mikv_select", lib.mikv_select(
         policy, ctypes.byref(c), L, budget_pct, window, float(alpha), _ptr(scores),
         _ptr(scores_head), _ptr(v), _ptr(w_o), hidden, _ptr(vwo_norm), _ptr(keep_pos),
