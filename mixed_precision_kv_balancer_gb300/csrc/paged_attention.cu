@@ -539,38 +539,38 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSM) paged_partial_kernel
   const int64_t head = mine;
   for (int b = tid + kPaThreads; b < a.n; b += kPaThreads) mine += row_tiles<S::tw>(a, b);
   int64_t incl = scan64(mine * units, warp_sums, total);
+  if (total == 0) return;   // nothing is seen: the join answers
   const int workers = workers_of(total, gridDim.x * kPaWarps), c = w * gridDim.x + blockIdx.x;
   const int64_t begin = split_begin(total, workers, c), end = split_begin(total, workers, c + 1);
   const bool idle = c >= workers;
   Cursor at;
   at.b = -1;
-  int64_t before = 0;
+  int64_t pass = 0, base = 0;   // tiles before this pass's rows (all warps alike), and before this warp's row
   for (int b0 = 0; b0 < a.n; b0 += kPaThreads) {
     int64_t sum = total;
     if (a.n > kPaThreads) {
       const int b = b0 + tid;
       const int64_t v = b0 == 0 ? head : b < a.n ? row_tiles<S::tw>(a, b) : 0;
-      incl = before + scan64(v * units, warp_sums, sum);
+      incl = pass + scan64(v * units, warp_sums, sum);
     }
     __syncthreads();   // the last pass's sums have been read
     s_incl[tid] = incl;
     __syncthreads();
-    if (!idle && at.b < 0 && begin < before + sum) {
+    if (!idle && at.b < 0 && begin < pass + sum) {
       int below = 0;   // rows of this pass that end at or before `begin`
 #pragma unroll
       for (int i = 0; i < kPaThreads; i += 32) below += __popc(__ballot_sync(0xffffffffu, s_incl[i + lane] <= begin));
       at.b = b0 + below;
-      before = below ? s_incl[below - 1] : before;   // the row's first tile; not read again once found
-    } else if (at.b < 0) {
-      before += sum;
+      base = below ? s_incl[below - 1] : pass;
     }
+    pass += sum;
     if (__syncthreads_and(idle || at.b >= 0)) break;
   }
   if (idle) return;
   const int n = static_cast<int>(end - begin);   // tiles of this warp: below 2^31 / tw a row, far fewer a warp
   open_row<TYPE>(a, at);
-  at.u = static_cast<int>((begin - before) / at.tiles);
-  at.t = static_cast<int>((begin - before) % at.tiles);
+  at.u = static_cast<int>((begin - base) / at.tiles);
+  at.t = static_cast<int>((begin - base) % at.tiles);
 
   const uint32_t ring = ((smem_u32(smem) + 255u) & ~255u) + w * S::stages * S::stage;
   const size_t lrow = p.layer_rows() * a.layer;

@@ -564,6 +564,71 @@ def test_a_decode_step_in_a_graph():
     assert caches[0].lens.tolist() == [65, 122, 60]
 
 
+def test_page_calls_in_a_graph():
+    """Release, fork, compact, reserve and copy, captured once and replayed as sequences grow."""
+    def calls(c, b):
+        c.free(b["child"], ok=b["ok"][0])
+        c.fork(b["parent"], b["child"], ok=b["ok"][1], ws=b["ws"])
+        c.compact(b["keep"], b["kn"], seqs=b["child"], ok=b["ok"][2], ws=b["ws"])
+        c.reserve(b["add"], seqs=b["both"], start=b["start"], ws=b["ws"])
+        c.copy(b["src"], b["dst"], ok=b["ok"][3])
+
+    caches = [ph.make([37, 64, 0, 0], 16, 2, "int8", layers=2, spare=60, max_pages=30, poison=False) for _ in range(2)]
+    g = torch.Generator().manual_seed(9)
+    keep = torch.stack([torch.randperm(30, generator=g)[:20].sort().values for _ in range(8)]).view(2, 2, 2, 20).int().to(ph.DEV)
+    bufs = [{"child": ints([2, 3]), "parent": ints([0, 1]), "ok": torch.zeros(4, 2, dtype=torch.int32, device=ph.DEV), "keep": keep,
+             "kn": ints([20, 7]), "add": ints([3, 5]), "both": ints([0, 1]), "start": ints([0, 0]), "src": ints([1, 2]),
+             "dst": ints([5, 6]), "ws": c.page_workspace(2)} for c in caches]
+    names = ("table", "lens", "refs", "k", "v", "k_meta", "v_meta")
+    state = [getattr(caches[0], x).clone() for x in names]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls(caches[0], bufs[0])
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls(caches[0], bufs[0])
+    for x, y in zip(names, state):
+        getattr(caches[0], x).copy_(y)
+    for _ in range(40):
+        graph.replay()
+        calls(caches[1], bufs[1])
+        assert torch.equal(bufs[0]["ok"], bufs[1]["ok"]) and torch.equal(bufs[0]["start"], bufs[1]["start"])
+        for x in names:
+            assert torch.equal(getattr(caches[0], x), getattr(caches[1], x)), x
+    assert caches[0].lens.tolist() == [157, 264, 20, 7]
+
+
+@pytest.mark.parametrize("type", ["fp16", "bf16", "int8"])
+@pytest.mark.parametrize("n", [129, 256, 257, 700])
+def test_batches_past_one_pass_of_the_search(type, n):
+    """More rows than the threads that look for a warp's first one; long, short and empty sequences."""
+    lens = np.random.RandomState(n).choice([0, 0, 1, 17, 60, 333], size=n)
+    cache = ph.make(lens, 16, 2, type)
+    _check(cache, _query(n, 4, type))
+    _check(cache, _query(n, 4, type), 40, 3)
+
+
+@pytest.mark.parametrize("type", ["fp16", "int8"])
+def test_the_largest_batch(type):
+    """65535 sequences of one to three slots: one of length 1 answers with its own value row."""
+    n = 65535
+    lens = 1 + np.arange(n) % 3
+    cache = ph.make(lens, 2, 1, type, poison=False)
+    q = _query(n, 2, type)
+    out, lse = cache.attend(0, q)
+    for i in (0, 3, 6, 32766, 65532):
+        assert lens[i] == 1
+        _, v = ph.sequence(cache, 0, i)
+        want = torch.from_numpy(v[0, 0]).to(ph.DTYPE[type]).to(ph.DEV)
+        assert torch.equal(out[i, 0], want) and torch.equal(out[i, 1], want)
+    pick = [1, 2, 40000, 65534]
+    want, wl, mag = ph.expect(cache, q[pick], 0, 0, 0, pick)
+    ph.close(out[pick], want, mag, ph.HALF_STEP[type], 2.0 ** -16)
+    ph.close_lse(lse[pick], wl)
+
+
 def test_the_binding_refuses():
     cache = ph.make([20, 20], 16, 2, "bf16")
     q = _query(2, 4, "bf16")

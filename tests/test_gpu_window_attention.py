@@ -186,6 +186,54 @@ def test_rows_do_not_hang_on_rows_that_do_not_count(dtype):
         assert all(torch.equal(a[:, :, :1], b) for a, b in zip(got, want))
 
 
+def test_two_calls_at_once_and_split_keys_in_a_graph():
+    """Calls on two streams, one of them split over its keys, eager and replayed."""
+    calls = [(_make(1, 8, 5, torch.float16, "bhtd", 1), _make(1, 2, 7000, torch.float16, "bhtd", 2), _make(1, 2, 7000, torch.float16, "bhtd", 3)),
+             (_make(2, 6, 900, torch.bfloat16, "bthd", 4), _make(2, 3, 900, torch.bfloat16, "bthd", 5), _make(2, 3, 900, torch.bfloat16, "bthd", 6))]
+    want = [_run(*c, 500, 3) for c in calls]
+    outs = [(torch.empty_like(c[0]), torch.empty(c[0].shape[:3], device=ph.DEV)) for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    sizes = [_lib.load().mikv_window_attention_workspace_bytes(c[0].shape[0], c[0].shape[1], c[1].shape[1], c[0].shape[2],
+                                                               c[1].shape[2], 500, 3) for c in calls]
+    ws = [torch.empty(max(n, 32), dtype=torch.uint8, device=ph.DEV) for n in sizes]
+    go = lambda i: _lib.mikv_window_attention(*calls[i], 500, 3, *outs[i], ws=ws[i])
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                go(i)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(outs[i], want[i]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go(0)
+        go(1)
+    for _ in range(5):
+        for o in outs:
+            for x in o:
+                x.zero_()
+        graph.replay()
+        for i in range(2):
+            assert all(torch.equal(a, b) for a, b in zip(outs[i], want[i]))
+
+
+def test_rows_past_32_bit_offsets():
+    """2.4e9 values a tensor; under a window of one every query answers with its own value row."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    H, T = 63, 301000
+    k = torch.ones(1, 1, T, 128, dtype=torch.bfloat16, device=ph.DEV).expand(1, H, T, 128)
+    v = torch.empty(1, H, T, 128, dtype=torch.bfloat16, device=ph.DEV).normal_()
+    q = torch.empty_like(v).normal_()
+    out = torch.empty_like(v)
+    lse = torch.empty(1, H, T, device=ph.DEV)
+    _lib.mikv_window_attention(q, k, v, 1, 0, out, lse)
+    assert torch.equal(out, v)
+    got, want = lse[0, -1, -9:], q[0, -1, -9:].double().sum(-1) / 128 ** 0.5
+    assert (got.double() - want).abs().max() < 1e-3
+
+
 def test_lse_may_be_left_out_and_rows_broadcast():
     q, k, v = (_make(2, 2, 90, torch.float16, "bhtd", s) for s in (1, 2, 3))
     k, v = k[:1].expand(2, 2, 90, 128), v[:, :1].expand(2, 2, 90, 128)
