@@ -265,89 +265,94 @@ def mikv_channel_quantize(k, bits, codes, meta, stream=None):
 _PAGE_DTYPE = {MIKV_PAGES_FP16: torch.float16, MIKV_PAGES_BF16: torch.bfloat16, MIKV_PAGES_INT8: torch.float16}
 
 
-def _launch(device, stream, call, *args):
-    """call(*args, stream) on the device its tensors are on: on that device's current stream unless
-    one is given, with the device made current for the launch.  The status is checked under
-    the call's name."""
-    index = device.index
-    st = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if index == torch.cuda.current_device():
+def _launch(dev, stream, call, *args):
+    """call(*args, stream) on CUDA device `dev` (its number), where the tensors are: on that device's
+    current stream unless one is given, with the device made current for the launch.  The
+    status is checked under the call's name."""
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
         rc = call(*args, st)
     else:
-        with torch.cuda.device(index):
+        with torch.cuda.device(dev):
             rc = call(*args, st)
     if rc != 0:
         raise MikvError(call.__name__, rc, load().mikv_last_error().decode())
 
 
-def _need(t, name, dtype, shape, device):
-    """Pointer of a contiguous tensor of this dtype, shape and device; None for None."""
+def _need(t, name, dtype, shape, dev):
+    """Pointer of a contiguous tensor of this dtype and shape on device `dev`; None for None."""
     if t is None:
         return None
-    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
-    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, got "
                      f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _rows(t, name, dtype, shape, device):
+def _rows(t, name, dtype, shape, dev):
     """mikv_rows of a [B][H][T][D] tensor whose last dimension is contiguous."""
-    if t.dtype is dtype and t.shape == shape and t.device == device:
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
         sb, sh, st, sd = t.stride()
         if sd == 1 or shape[3] <= 1:
             # a dimension of one element is never stepped along: its stride may be anything
-            return ctypes.byref(mikv_rows(t.data_ptr(), sb if shape[0] > 1 else 0, sh if shape[1] > 1 else 0,
-                                          st if shape[2] > 1 else 0))
-    raise ValueError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)} on {device} with a contiguous "
+            return mikv_rows(t.data_ptr(), sb if shape[0] > 1 else 0, sh if shape[1] > 1 else 0, st if shape[2] > 1 else 0)
+    raise ValueError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)} on cuda:{dev} with a contiguous "
                      f"last dimension, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
-def _ws_on(nbytes, device, ws, stream):
-    """(pointer, bytes, tensor to keep) of the workspace given, or of a new one of nbytes(), which
-    belongs to the stream of the call: freed on return, it is not handed out again before that
-    stream has come past the call."""
-    if ws is None:
-        n = nbytes()
-        if n == 0:
-            return None, 0, None
-        if stream is None:
-            ws = torch.empty(n, dtype=torch.uint8, device=device)
-        else:
-            with torch.cuda.stream(stream):
-                ws = torch.empty(n, dtype=torch.uint8, device=device)
-        return ws.data_ptr(), n, ws
-    if ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws: expected a contiguous tensor on {device}, got one on {ws.device}")
-    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+def _ws_given(ws, dev):
+    """(pointer, bytes, tensor to keep) of a workspace that the caller keeps."""
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous tensor on cuda:{dev}, got one on {ws.device}")
+    return ws.data_ptr(), ws.nbytes, ws
+
+
+def _ws_new(n, dev, stream):
+    """The same of a new one of n bytes, which belongs to the stream of the call: freed on return,
+    it is not handed out again before that stream has come past the call."""
+    if n == 0:
+        return None, 0, None
+    if stream is None:
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    else:
+        with torch.cuda.stream(stream):
+            ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    return ws.data_ptr(), n, ws
+
+
+def _page_ws(pages, n, ws, stream):
+    if ws is not None:
+        return _ws_given(ws, pages.index)
+    return _ws_new(load().mikv_page_workspace_bytes(pages.ref, n), pages.index, stream)
 
 
 def mikv_page_reserve(pages, seqs, add, start, ws=None, stream=None):
     """Room for add int32 [n] more tokens behind sequences seqs (int32 [n], None: 0 .. n - 1);
     start int32 [n] receives each one's first new slot, or -1 where it was refused."""
-    lib, dev, n = load(), pages.device, add.shape[0]
-    w, nb, _keep = _ws_on(lambda: lib.mikv_page_workspace_bytes(pages.ref, n), dev, ws, stream)
+    lib, dev, n = load(), pages.index, add.shape[0]
+    w, nb, _keep = _page_ws(pages, n, ws, stream)
     _launch(dev, stream, lib.mikv_page_reserve, pages.ref, _need(seqs, "seqs", torch.int32, (n,), dev),
             _need(add, "add", torch.int32, (n,), dev), n, _need(start, "start", torch.int32, (n,), dev), w, nb)
 
 
 def mikv_page_fork(pages, parent, child, ok, ws=None, stream=None):
     """child[i] becomes a copy of parent[i] (int32 [n] each); ok int32 [n] receives 1, or 0 where refused."""
-    lib, dev, n = load(), pages.device, parent.shape[0]
-    w, nb, _keep = _ws_on(lambda: lib.mikv_page_workspace_bytes(pages.ref, n), dev, ws, stream)
+    lib, dev, n = load(), pages.index, parent.shape[0]
+    w, nb, _keep = _page_ws(pages, n, ws, stream)
     _launch(dev, stream, lib.mikv_page_fork, pages.ref, _need(parent, "parent", torch.int32, (n,), dev),
             _need(child, "child", torch.int32, (n,), dev), n, _need(ok, "ok", torch.int32, (n,), dev), w, nb)
 
 
 def mikv_page_free(pages, seqs, ok, stream=None):
     """Sequences seqs (int32 [n], None: 0 .. n - 1) give their pages back; ok int32 [n]."""
-    lib, dev, n = load(), pages.device, ok.shape[0]
+    lib, dev, n = load(), pages.index, ok.shape[0]
     _launch(dev, stream, lib.mikv_page_free, pages.ref, _need(seqs, "seqs", torch.int32, (n,), dev), n,
             _need(ok, "ok", torch.int32, (n,), dev))
 
 
 def mikv_page_copy(pages, src, dst, ok, stream=None):
     """Page dst[i] takes what page src[i] holds, in all layers (int32 [n] each); ok int32 [n]."""
-    lib, dev, n = load(), pages.device, src.shape[0]
+    lib, dev, n = load(), pages.index, src.shape[0]
     _launch(dev, stream, lib.mikv_page_copy, pages.ref, _need(src, "src", torch.int32, (n,), dev),
             _need(dst, "dst", torch.int32, (n,), dev), n, _need(ok, "ok", torch.int32, (n,), dev))
 
@@ -355,8 +360,8 @@ def mikv_page_copy(pages, src, dst, ok, stream=None):
 def mikv_page_compact(pages, seqs, keep_pos, keep_n, ok, ws=None, stream=None):
     """Sequence seqs[i] keeps keep_n[i] slots per key head: keep_pos int32 [layers][n][Hkv][max_keep],
     keep_n and ok int32 [n]."""
-    lib, dev, n, s = load(), pages.device, keep_n.shape[0], pages.struct
-    w, nb, _keep = _ws_on(lambda: lib.mikv_page_workspace_bytes(pages.ref, n), dev, ws, stream)
+    lib, dev, n, s = load(), pages.index, keep_n.shape[0], pages.struct
+    w, nb, _keep = _page_ws(pages, n, ws, stream)
     most = keep_pos.shape[-1]
     _launch(dev, stream, lib.mikv_page_compact, pages.ref, _need(seqs, "seqs", torch.int32, (n,), dev),
             _need(keep_pos, "keep_pos", torch.int32, (s.layers, n, s.Hkv, most), dev),
@@ -366,7 +371,7 @@ def mikv_page_compact(pages, seqs, keep_pos, keep_n, ok, ws=None, stream=None):
 def mikv_paged_append(pages, layer, k, v, seqs=None, start=None, counts=None, stream=None):
     """Rows k, v [n][Hkv][T][D] (strided; fp16, bf16 for BF16 pages) into one layer: counts int32 [n]
     tokens each (None: T), from slot start int32 [n] (None: each sequence's last slots)."""
-    lib, dev, s = load(), pages.device, pages.struct
+    lib, dev, s = load(), pages.index, pages.struct
     n, _, T, _ = k.shape
     shape, dt = (n, s.Hkv, T, s.D), _PAGE_DTYPE[s.type]
     _launch(dev, stream, lib.mikv_paged_append, pages.ref, layer, _rows(k, "k", dt, shape, dev),
@@ -376,7 +381,7 @@ def mikv_paged_append(pages, layer, k, v, seqs=None, start=None, counts=None, st
 
 def mikv_paged_gather(pages, layer, k_out, v_out, seqs=None, stream=None):
     """The first T slots of each sequence of one layer as rows k_out, v_out [n][Hkv][T][D] (strided)."""
-    lib, dev, s = load(), pages.device, pages.struct
+    lib, dev, s = load(), pages.index, pages.struct
     n, _, T, _ = k_out.shape
     shape, dt = (n, s.Hkv, T, s.D), _PAGE_DTYPE[s.type]
     _launch(dev, stream, lib.mikv_paged_gather, pages.ref, layer, _need(seqs, "seqs", torch.int32, (n,), dev), n, T,
@@ -385,10 +390,11 @@ def mikv_paged_gather(pages, layer, k_out, v_out, seqs=None, stream=None):
 
 def mikv_paged_attention(q, pages, layer, window, sinks, out, lse=None, seqs=None, ws=None, stream=None):
     """One new token per sequence: q, out [n][Hq][D] fp16 (bf16 for BF16 pages), lse fp32 [n][Hq]."""
-    lib, dev, s = load(), pages.device, pages.struct
+    lib, dev, s = load(), pages.index, pages.struct
     n, Hq, _ = q.shape
     shape, dt = (n, Hq, s.D), _PAGE_DTYPE[s.type]
-    w, nb, _keep = _ws_on(lambda: lib.mikv_paged_attention_workspace_bytes(pages.ref, n, Hq, window, sinks), dev, ws, stream)
+    w, nb, _keep = _ws_given(ws, dev) if ws is not None else _ws_new(
+        lib.mikv_paged_attention_workspace_bytes(pages.ref, n, Hq, window, sinks), dev, stream)
     _launch(dev, stream, lib.mikv_paged_attention, _need(q, "q", dt, shape, dev), pages.ref, layer,
             _need(seqs, "seqs", torch.int32, (n,), dev), n, Hq, window, sinks, _need(out, "out", dt, shape, dev),
             _need(lse, "lse", torch.float32, (n, Hq), dev), w, nb)
@@ -402,13 +408,14 @@ def _window_workspace_bytes(*dims):   # a function of the dimensions alone
 def mikv_window_attention(q, k, v, window, sinks, out, lse=None, q_lens=None, k_lens=None, ws=None, stream=None):
     """A prompt's or a chunk's attention: q, out [B][Hq][Tq][D], k, v [B][Hkv][Tk][D] (strided; all fp16 or
     all bf16), lse fp32 [B][Hq][Tq], q_lens, k_lens int32 [B] (None: Tq, Tk)."""
-    lib, dev, dt = load(), q.device, q.dtype
+    lib, dev, dt = load(), q.get_device(), q.dtype
     B, Hq, Tq, D = q.shape
     Hkv, Tk = k.shape[1], k.shape[2]
-    if not q.is_cuda or dt not in (torch.float16, torch.bfloat16):
-        raise ValueError(f"q: expected fp16 or bf16 on a CUDA device, got {dt} on {dev}")
+    if dev < 0 or dt not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"q: expected fp16 or bf16 on a CUDA device, got {dt} on {q.device}")
     qs, ks = (B, Hq, Tq, D), (B, Hkv, Tk, D)
-    w, nb, _keep = _ws_on(lambda: _window_workspace_bytes(B, Hq, Hkv, Tq, Tk, window, sinks), dev, ws, stream)
+    w, nb, _keep = _ws_given(ws, dev) if ws is not None else _ws_new(
+        _window_workspace_bytes(B, Hq, Hkv, Tq, Tk, window, sinks), dev, stream)
     _launch(dev, stream, lib.mikv_window_attention, _rows(q, "q", dt, qs, dev), _rows(k, "k", dt, ks, dev),
             _rows(v, "v", dt, ks, dev), B, Hq, Hkv, Tq, Tk, D,
             MIKV_PAGES_BF16 if dt is torch.bfloat16 else MIKV_PAGES_FP16, _need(q_lens, "q_lens", torch.int32, (B,), dev),

@@ -49,10 +49,10 @@ class PagedCache:
         dtype = {"fp16": torch.float16, "bf16": torch.bfloat16, "int8": torch.uint8}[type]
         layers, n_pages, Hkv, ps, D = k.shape
         max_seqs, max_pages = table.shape
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
         if not k.is_cuda:
             raise ValueError("a paged cache lives on a CUDA device")
-        need = lambda t, name, dt, shape: _lib._need(t, name, dt, shape, self.device)
+        need = lambda t, name, dt, shape: _lib._need(t, name, dt, shape, self.index)
         s = _lib.mikv_pages()
         s.layers, s.n_pages, s.page_size, s.Hkv, s.D, s.type = layers, n_pages, ps, Hkv, D, TYPES[type]
         s.max_seqs, s.max_pages = max_seqs, max_pages
