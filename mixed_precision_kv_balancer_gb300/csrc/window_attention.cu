@@ -9,7 +9,8 @@
 // A CTA holds two tiles of 128 query rows over one key head: the same rows of two heads of the
 // group, or 256 rows of one head where the group is odd.  Where a chunk has 64 rows or fewer, a
 // tile packs the rows of several heads of the group.  Where the items of a call would leave SMs
-// idle, each is split over its key tiles and the parts are joined by a second kernel.  Key and value
+// idle, all their key tiles form one line, of which each CTA takes an equal part, and the items that
+// are cut are joined by a second kernel.  Key and value
 // tiles of 128 rows come through a ring of five 32 KB buffers (TMA, 128-byte swizzle); tiles
 // that none of the rows sees are not read.  Per key tile i and query tile t
 //   S_t = Q_t K_i^T     tcgen05, both operands in shared memory, 128 fp32 TMEM columns
@@ -33,6 +34,7 @@
 
 #include "paged.cuh"
 #include "tcgen05.cuh"
+#include "window_index.h"
 
 namespace mikv {
 
@@ -40,7 +42,7 @@ int window_attention_status(unsigned* out, bool clear) { return tc::wait_giveups
 
 namespace {
 
-constexpr int kWaRows = 128;                     // query rows and key rows of a tile
+constexpr int kWaRows = kKeyRows;                // query rows and key rows of a tile
 constexpr int kWaNarrow = 32;                    // columns of a tile that holds the last few sinks
 constexpr int kWaRing = 5;
 constexpr int kMaxRows = 1 << 30;                // of q or k: positions and their differences fit 32 bits
@@ -59,15 +61,17 @@ struct Weights {
 struct WindowArgs {
   RowView out;
   float* lse;
-  float* part;                   // splits > 1: [splits][B Hq Tq][128] sums, then [splits][B Hq Tq] (maximum, sum)
+  float* part;                   // the line's cut items, see part_sums and part_ml
   const int32_t *q_lens, *k_lens;
-  int Hq, rep, Tq, Tk, window, sinks, blocks;
-  int64_t rows;                  // B Hq Tq
-  int tb, hb, groups;            // a tile: tb rows of each of hb heads; groups = ceil(rep / hb)
-  int splits;
-  bool pair_heads;               // the CTA's tiles are two groups of heads, else two row blocks of one
+  int Hq, rep, Tq, Tk, B, Hkv;
+  QueryBlocks qb;                // rows of a tile, the mask
+  int hb, groups;                // a tile: qb.tb rows of each of hb heads; groups = ceil(rep / hb)
+  int per;                       // items of one row block and key head
+  int tile_rows;                 // rows of a tile that can count: min(qb.tb, Tq) hb
+  int ctas;                      // of the line
+  int share;                     // CTAs an item where each item has as many; 0: equal parts of the line
   bool wide_out;                 // rows of out begin at multiples of 32 bytes
-  int qb, qh, kb, kh, vb, vh;    // 1, or 0 where the view repeats one batch row or head
+  int qbat, qh, kb, kh, vb, vh;  // 1, or 0 where the view repeats one batch row or head
   float scale;                   // log2(e) / sqrt(D)
 };
 
@@ -84,10 +88,15 @@ struct WaBars {
 // registers, which the matrix instructions read.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
+// An item, or the part of one that a CTA of the line takes.
+struct Place {
+  int b, hk, blk, u;   // batch row, key head, row block, item of these
+  int t0, t1;          // the line: its key tiles
+  bool whole;          // all of the item
+};
 // What one CTA works on; every warp computes it alike.
 struct Work {
   int ql, kl, off;        // lengths; position of query 0
-  int split;
   int group[2], q0[2];    // per tile: group of heads and first row
   int pa[2], pb[2];       // positions of its first and last row
   int begin, end;         // the item's key tiles: of ts of the sinks, then tw0, tw0 + 1, ...
@@ -108,42 +117,35 @@ __device__ __forceinline__ Tile tile_of(const Work& w, int t) {
   return {t < w.nt, t ? w.group[1] : w.group[0], t ? w.q0[1] : w.q0[0], t ? w.pa[1] : w.pa[0], t ? w.pb[1] : w.pb[0],
           t ? w.from[1] : w.from[0], t ? w.last[1] : w.last[0]};
 }
-template <bool SPLIT>
-__device__ __forceinline__ Work work_of(const WindowArgs& a, int b, int x) {
+__device__ __forceinline__ int q_len(const WindowArgs& a, int b) { return a.q_lens ? min(max(a.q_lens[b], 0), a.Tq) : a.Tq; }
+__device__ __forceinline__ int k_len(const WindowArgs& a, int b) { return a.k_lens ? min(max(a.k_lens[b], 0), a.Tk) : a.Tk; }
+template <bool LINE>
+__device__ __forceinline__ Work work_of(const WindowArgs& a, const Place& pl) {
   Work w;
-  w.ql = a.q_lens ? min(max(uniform(a.q_lens[b]), 0), a.Tq) : a.Tq;
-  w.kl = a.k_lens ? min(max(uniform(a.k_lens[b]), 0), a.Tk) : a.Tk;
+  w.ql = uniform(q_len(a, pl.b));
+  w.kl = uniform(k_len(a, pl.b));
   w.off = w.kl - w.ql;
-  w.split = SPLIT ? x % a.splits : 0;
-  if (SPLIT) x /= a.splits;
-  const int per = a.pair_heads ? (a.groups + 1) / 2 : a.groups;   // items of one row block
-  const int blk = a.blocks - 1 - x / per, u = x % per;            // the last rows, which see the most, first
+  const int tb = a.qb.tb;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    w.group[t] = a.pair_heads ? 2 * u + t : u;
-    w.q0[t] = a.pair_heads ? blk * a.tb : (2 * blk + t) * a.tb;
+    w.group[t] = a.qb.pair_heads ? 2 * pl.u + t : pl.u;
+    w.q0[t] = first_row(a.qb, pl.blk) + (a.qb.pair_heads ? 0 : t * tb);
     w.pa[t] = w.off + w.q0[t];
-    w.pb[t] = w.off + min(w.q0[t] + a.tb, w.ql) - 1;
+    w.pb[t] = w.off + min(w.q0[t] + tb, w.ql) - 1;
   }
   w.nt = w.q0[0] >= w.ql ? 0 : w.q0[1] >= w.ql || w.group[1] >= a.groups ? 1 : 2;
-  const int p1 = w.nt == 2 ? w.pb[1] : w.pb[0];           // the largest position (tile 1's rows are not below tile 0's)
-  const int lo = a.window > 0 ? max(w.pa[0] - a.window + 1, 0) : 0;
-  const int end = p1 < 0 ? 0 : p1 / kWaRows + 1;
-  w.tw0 = min(lo / kWaRows, end);
-  const int sink_tiles = a.window > 0 ? (min(a.sinks, w.kl) + kWaRows - 1) / kWaRows : 0;
-  w.ts = min(sink_tiles, w.tw0);
-  const int tiles = w.ts + end - w.tw0;
-  // where the window begins among the sinks the list is 0, 1, 2, ... and its first sink_tiles hold
-  // sinks, which a later query tile sees though its own window begins behind them
-  w.ns = max(w.ts, min(sink_tiles, sink_tiles > w.tw0 ? tiles : w.ts));
-  w.begin = SPLIT ? static_cast<int>(static_cast<int64_t>(tiles) * w.split / a.splits) : 0;
-  w.end = SPLIT ? static_cast<int>(static_cast<int64_t>(tiles) * (w.split + 1) / a.splits) : tiles;
+  const KeyTiles k = key_tiles(a.qb, w.ql, w.kl, pl.blk);
+  w.ts = k.ts;
+  w.tw0 = k.tw0;
+  w.ns = k.ns;
+  w.begin = LINE ? min(pl.t0, k.tiles) : 0;
+  w.end = LINE ? min(pl.t1, k.tiles) : k.tiles;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int e = w.pb[t] < 0 ? -1 : w.pb[t] / kWaRows;
-    w.from[t] = w.ts + (a.window > 0 ? max(w.pa[t] - a.window + 1, 0) / kWaRows - w.tw0 : 0);
+    w.from[t] = w.ts + (a.qb.window > 0 ? max(w.pa[t] - a.qb.window + 1, 0) / kWaRows - w.tw0 : 0);
     int last = t >= w.nt || e < 0 ? -1 : e - w.tw0 + w.ts;
-    if (SPLIT) {   // the last one of this part
+    if (LINE) {   // the last one of this part
       last = min(last, w.end - 1);
       if (last < w.from[t]) last = min(last, w.ns - 1);
       if (last < w.begin) last = -1;
@@ -154,12 +156,12 @@ __device__ __forceinline__ Work work_of(const WindowArgs& a, int b, int x) {
 }
 // Whether all rows of a query tile see all of the key tile at j0.
 __device__ __forceinline__ bool tile_whole(const WindowArgs& a, const Tile& t, int j0) {
-  return j0 + kWaRows - 1 <= t.pa && (a.window == 0 || j0 > t.pb - a.window || j0 + kWaRows <= a.sinks);
+  return j0 + kWaRows - 1 <= t.pa && (a.qb.window == 0 || j0 > t.pb - a.qb.window || j0 + kWaRows <= a.qb.sinks);
 }
 // Whether a key tile counts with its first kWaNarrow columns alone: the sinks' last tile, mostly
 // (a window of 1024 with 4 sinks is ten tiles, one of them for the sinks: 79 -> 75 us).
 __device__ __forceinline__ bool tile_narrow(const WindowArgs& a, const Work& w, int i) {
-  return i < w.ts && a.sinks - w.j0(i) <= kWaNarrow;
+  return i < w.ts && a.qb.sinks - w.j0(i) <= kWaNarrow;
 }
 // Rows [z0, z1) and [z2, 128) of the value tile at j0 that no query of the call sees.
 struct Hidden {
@@ -168,8 +170,8 @@ struct Hidden {
 };
 __device__ __forceinline__ Hidden hidden_rows(const WindowArgs& a, const Work& w, int j0) {
   Hidden h;
-  h.z0 = min(max(a.sinks - j0, 0), kWaRows);
-  h.z1 = a.window > 0 ? min(max(w.off - a.window + 1 - j0, 0), kWaRows) : 0;
+  h.z0 = min(max(a.qb.sinks - j0, 0), kWaRows);
+  h.z1 = a.qb.window > 0 ? min(max(w.off - a.qb.window + 1 - j0, 0), kWaRows) : 0;
   h.z2 = min(max(w.kl - j0, 0), kWaRows);
   return h;
 }
@@ -289,7 +291,7 @@ __device__ __forceinline__ void softmax_tile(const WindowArgs& a, uint32_t ts, u
   wait_ld();
   if (!whole) {
     // the row sees columns lo .. hi and those below sk; 32 columns whole to the warp's rows are left alone
-    const int hi = p - j0, lo = a.window > 0 ? hi - a.window + 1 : 0, sk = a.sinks - j0;
+    const int hi = p - j0, lo = a.qb.window > 0 ? hi - a.qb.window + 1 : 0, sk = a.qb.sinks - j0;
 #pragma unroll
     for (int c = 0; c < COLS; c += 32) {
       const uint32_t m = low_bits(hi + 1 - c) & (~low_bits(lo - c) | low_bits(sk - c));
@@ -361,9 +363,6 @@ __device__ __forceinline__ void softmax_tile(const WindowArgs& a, uint32_t ts, u
 // the next one once it has requested all tiles of this one: two or three key tiles before the
 // end, early enough to hide the answer and late enough to keep long items from piling up (asked
 // at an item's start, 8192 causal tokens of 32 heads took 394 us instead of 349).
-struct Item {
-  int x, y, z;
-};
 __device__ __forceinline__ void ask_next(uint32_t answer, uint32_t mbar) {
   tc::mbar_expect_tx(mbar, 16);
   asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];\n" ::"r"(answer),
@@ -371,7 +370,7 @@ __device__ __forceinline__ void ask_next(uint32_t answer, uint32_t mbar) {
                : "memory");
 }
 // The answer to ask n, by the whole warp: false where nothing is left.
-__device__ __forceinline__ bool next_item(WaBars& bar, const uint4* answers, int n, tc::Waits& wait, Item& it) {
+__device__ __forceinline__ bool heard_next(WaBars& bar, const uint4* answers, int n, tc::Waits& wait, int& at_x, int& at_y, int& at_z) {
   const uint32_t at = smem_u32(&answers[n & 1]);
   wait(smem_u32(&bar.told[n & 1]), (n >> 1) & 1);
   uint32_t x = 0, y = 0, z = 0, ok = 0;
@@ -385,11 +384,154 @@ __device__ __forceinline__ bool next_item(WaBars& bar, const uint4* answers, int
   tc::fence_proxy_async();   // the answer is read before another overwrites it
   __syncwarp();
   if ((threadIdx.x & 31) == 0) tc::mbar_arrive(smem_u32(&bar.heard[n & 1]));
-  it = {uniform(x), uniform(y), uniform(z)};
+  at_x = uniform(x);
+  at_y = uniform(y);
+  at_z = uniform(z);
   return __all_sync(0xffffffffu, ok != 0 && wait.ok);
 }
 
-template <bool BF, bool SPLIT>
+// An entry of the line: the places before it, and those of each of its items.
+struct Spot {
+  int e, base, places;
+};
+__device__ __forceinline__ int places_of(const WindowArgs& a, int e) {
+  if (e >= a.B * a.qb.blocks) return 0;
+  const int b = e / a.qb.blocks;
+  return entry_places(a.qb, q_len(a, b), k_len(a, b), a.qb.blocks - 1 - e % a.qb.blocks);
+}
+// Places of 32 entries, one a lane, and their sums up to it.
+struct Sums {
+  int v, incl;
+};
+__device__ __forceinline__ Sums sums_of(const WindowArgs& a, int e0) {
+  const int lane = threadIdx.x & 31;
+  Sums s;
+  s.v = s.incl = places_of(a, e0 + lane);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, s.incl, o);
+    if (lane >= o) s.incl += u;
+  }
+  return s;
+}
+// All places, by a whole warp; the host keeps them below 2^31.  `first`: sums_of the first entries.
+__device__ __forceinline__ int line_total(const WindowArgs& a, const Sums& first) {
+  int sum = __shfl_sync(0xffffffffu, first.incl, 31);
+  for (int e0 = 32; e0 < a.B * a.qb.blocks; e0 += 32) sum += __reduce_add_sync(0xffffffffu, places_of(a, e0 + (threadIdx.x & 31)));
+  return uniform(sum) * a.Hkv * a.per;
+}
+// The entry that holds place `pos` (below the total), by a whole warp.
+__device__ __forceinline__ Spot spot_of(const WindowArgs& a, const Sums& first, int pos) {
+  const int items = a.Hkv * a.per;
+  Spot s = {0, 0, 0};
+  for (Sums n = first;; n = sums_of(a, s.e)) {
+    const int below = __popc(__ballot_sync(0xffffffffu, s.base + n.incl * items <= pos));   // entries that end at or before it
+    if (below < 32 || s.e + 32 >= a.B * a.qb.blocks) {
+      const int at = min(below, 31);
+      s.places = uniform(__shfl_sync(0xffffffffu, n.v, at));
+      s.base = uniform(s.base + (__shfl_sync(0xffffffffu, n.incl, at) - s.places) * items);
+      s.e = uniform(s.e + at);
+      return s;
+    }
+    s.base += __shfl_sync(0xffffffffu, n.incl, 31) * items;
+    s.e += 32;
+  }
+}
+
+// What a warp walks: the items that its CTA is given (the grid's, then taken over), or its part of
+// the line.
+template <bool LINE>
+struct Walk {
+  int x, y, z;   // the item; the line: the next place, the end
+  Spot at;       // the line: the entry of place x
+  int t0, t1;    // share > 0: the part of the item
+  bool idle;     // the line: nothing for this CTA
+  int4 cut;      // the line: the item that begins here and goes on in later CTAs: entry, item, last CTA (-1: none),
+                 // whether this CTA's part of it has items before
+
+  __device__ __forceinline__ explicit Walk(const WindowArgs& a) {
+    x = blockIdx.x;
+    y = blockIdx.y;
+    z = blockIdx.z;
+    at = {0, 0, 1};
+    idle = false;
+    cut = {0, 0, -1, 0};
+    t0 = t1 = 0;
+    if (LINE && a.share > 0) {
+      const int items = a.Hkv * a.per, part = x % a.share, item = x / a.share;
+      at = {uniform(item / items), 0, 0};
+      at.places = uniform(places_of(a, at.e));
+      idle = __all_sync(0xffffffffu, at.places == 0);
+      if (!idle && part == 0) cut = {at.e, item % items, x + a.share - 1, 0};
+      const int tiles = at.places - kItemPlaces;
+      t0 = uniform(line_begin(tiles, a.share, part));
+      t1 = uniform(line_begin(tiles, a.share, part + 1));
+      x = uniform(item % items);
+    } else if (LINE) {
+      const Sums first = sums_of(a, 0);
+      const int total = line_total(a, first), workers = line_workers(total, a.ctas), c = blockIdx.x;
+      idle = __all_sync(0xffffffffu, c >= workers || total == 0);
+      if (!idle) {
+        x = uniform(line_begin(total, workers, c));
+        y = uniform(line_begin(total, workers, c + 1));
+        at = spot_of(a, first, x);
+        const int before = (x - at.base) % at.places;
+        if (line_tile(before) == 0) x = uniform(x - before);
+        if (y < total) {   // an end among an item's first places is the item's begin
+          const Spot s = spot_of(a, first, y);
+          const int item = (y - s.base) / s.places, begin = s.base + item * s.places;
+          if (line_tile(y - begin) == 0)
+            y = uniform(begin);
+          else if (begin >= x && threadIdx.x < 32)   // who asks: see part_cut
+            cut = {s.e, item, split_owner(total, workers, begin + s.places - 1), begin > x};
+        }
+        idle = __all_sync(0xffffffffu, x >= y);
+      }
+    }
+  }
+  __device__ __forceinline__ Place place(const WindowArgs& a) const {
+    if (!LINE) return {z, y, a.qb.blocks - 1 - x / a.per, x % a.per, 0, 0, true};   // the last rows, which see the most, first
+    if (a.share > 0) {
+      const int b = uniform(at.e / a.qb.blocks), hk = uniform(x / a.per);
+      return {b, hk, uniform(a.qb.blocks - 1 - (at.e - b * a.qb.blocks)), uniform(x - hk * a.per), t0, t1, false};
+    }
+    const int item = (x - at.base) / at.places, in = x - at.base - item * at.places, tiles = at.places - kItemPlaces;
+    const int t0 = uniform(line_tile(in)), t1 = uniform(min(tiles, line_tile(in + y - x)));
+    const int b = uniform(at.e / a.qb.blocks), hk = uniform(item / a.per);
+    return {b, hk, uniform(a.qb.blocks - 1 - (at.e - b * a.qb.blocks)), uniform(item - hk * a.per), t0, t1, t1 - t0 == tiles};
+  }
+  // On to the next one, by the whole warp; false where there is none.
+  __device__ __forceinline__ bool next(const WindowArgs& a, WaBars& bar, const uint4* answers, int n, tc::Waits& wait) {
+    if (!LINE) return heard_next(bar, answers, n, wait, x, y, z);
+    if (a.share > 0) return false;
+    x += at.places - (x - at.base) % at.places;
+    if (!__all_sync(0xffffffffu, x < y && wait.ok)) return false;
+    if (__all_sync(0xffffffffu, x == at.base + at.places * a.Hkv * a.per)) {
+      at.base = x;
+      do at.places = uniform(places_of(a, ++at.e));
+      while (__all_sync(0xffffffffu, at.places == 0 && at.e < a.B * a.qb.blocks));
+    }
+    return __all_sync(0xffffffffu, at.places > 0);
+  }
+};
+
+// A CTA of the line has two slots for parts of items that others hold too, for its first and its last.
+// A slot: the rows of two query tiles, 128 sums each, as [query tile][8 channels][row][8], so that the rows of a warp
+// are written side by side; the rows' (maximum, sum) behind all slots.
+__device__ __forceinline__ float* part_sums(const WindowArgs& a, int slot, int t, int row, int ch) {
+  const int64_t tile = static_cast<int64_t>(slot) * 2 + t;
+  return a.part + ((tile * (kD / 8) + ch / 8) * a.tile_rows + row) * 8 + ch % 8;
+}
+__device__ __forceinline__ float2* part_ml(const WindowArgs& a, int slot, int t, int row) {
+  float2* ml = reinterpret_cast<float2*>(a.part + static_cast<int64_t>(a.ctas) * 4 * a.tile_rows * kD);
+  return ml + (static_cast<int64_t>(slot) * 2 + t) * a.tile_rows + row;
+}
+// Behind them what each CTA says of the item it cuts first (Walk::cut).
+__device__ __forceinline__ int4* part_cut(const WindowArgs& a, int c) {
+  return reinterpret_cast<int4*>(a.part + static_cast<int64_t>(a.ctas) * 4 * a.tile_rows * (kD + 2)) + c;
+}
+
+template <bool BF, bool LINE>
 __global__ void __launch_bounds__(kWaThreads, 1)
     window_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                             const __grid_constant__ CUtensorMap vmap, const WindowArgs a) {
@@ -422,24 +564,28 @@ __global__ void __launch_bounds__(kWaThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = uniform(tslot);
-  if (SPLIT) pdl_trigger();   // the joining kernel may be placed; it waits for this one's end
+  if (LINE) pdl_trigger();   // the joining kernel may be placed; it waits for this one's end
   const uint32_t sq = tc::smem_base(smem), ring = sq + 2 * tc::kTileBytes;
   tc::Waits wait;
-  Item it = {static_cast<int>(blockIdx.x), static_cast<int>(blockIdx.y), static_cast<int>(blockIdx.z)};
+  Walk<LINE> walk(a);
+  if (LINE && threadIdx.x == 0) *part_cut(a, blockIdx.x) = walk.cut;
 
-  if (warp == kWaTmaWarp) {
+  if (walk.idle) {
+    // more CTAs than parts
+  } else if (warp == kWaTmaWarp) {
     int slot = 0, par = 1, qs = 0;   // ring position; parity that an empty buffer shows; query loads
     for (int n = 0;; ++n) {
-      const int b = it.z, hk = it.y;
-      const Work w = work_of<SPLIT>(a, b, it.x);
+      const Place pl = walk.place(a);
+      const int b = pl.b, hk = pl.hk;
+      const Work w = work_of<LINE>(a, pl);
       if (w.nt > 0 && w.begin < w.end) {
         if (qs > 0) wait(smem_u32(&bar.qfree), (qs - 1) & 1);
         ++qs;
         if (lane == 0 && wait.ok) {
-          tc::mbar_expect_tx(smem_u32(&bar.q), w.nt * a.tb * a.hb * kD * 2);
-          tma_queries(sq, &qmap, w.q0[0], w.group[0] * a.hb * a.qh, hk * a.qh, b * a.qb, smem_u32(&bar.q));
+          tc::mbar_expect_tx(smem_u32(&bar.q), w.nt * a.qb.tb * a.hb * kD * 2);
+          tma_queries(sq, &qmap, w.q0[0], w.group[0] * a.hb * a.qh, hk * a.qh, b * a.qbat, smem_u32(&bar.q));
           if (w.nt == 2)
-            tma_queries(sq + tc::kTileBytes, &qmap, w.q0[1], w.group[1] * a.hb * a.qh, hk * a.qh, b * a.qb, smem_u32(&bar.q));
+            tma_queries(sq + tc::kTileBytes, &qmap, w.q0[1], w.group[1] * a.hb * a.qh, hk * a.qh, b * a.qbat, smem_u32(&bar.q));
         }
         for (int c = 2 * w.begin; c < 2 * w.end; ++c) {   // keys of key tile c / 2 (c even), then its values
           const int j0 = w.j0(c >> 1);
@@ -475,9 +621,11 @@ __global__ void __launch_bounds__(kWaThreads, 1)
           }
         }
       }
-      if (n >= 2) wait(smem_u32(&bar.heard[n & 1]), ((n >> 1) - 1) & 1);
-      if (lane == 0 && wait.ok) ask_next(smem_u32(&answers[n & 1]), smem_u32(&bar.told[n & 1]));
-      if (!next_item(bar, answers, n, wait, it)) break;
+      if (!LINE) {
+        if (n >= 2) wait(smem_u32(&bar.heard[n & 1]), ((n >> 1) - 1) & 1);
+        if (lane == 0 && wait.ok) ask_next(smem_u32(&answers[n & 1]), smem_u32(&bar.told[n & 1]));
+      }
+      if (!walk.next(a, bar, answers, n, wait)) break;
     }
     // every buffer's release has arrived before the CTA ends
     for (int c = 0; c < kWaRing; ++c) {
@@ -509,7 +657,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       ++turn;
     };
     for (int n = 0;; ++n) {
-      const Work w = work_of<SPLIT>(a, it.z, it.x);
+      const Work w = work_of<LINE>(a, walk.place(a));
       if (w.nt > 0 && w.begin < w.end) {
         const Tile tile = tile_of(w, t);
         bool more = false, before = false, clear = false, few = false;
@@ -589,7 +737,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
           }
         }
       }
-      if (!next_item(bar, answers, n, wait, it)) break;
+      if (!walk.next(a, bar, answers, n, wait)) break;
     }
   } else {
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;   // the thread's TMEM lane is its row
@@ -598,11 +746,12 @@ __global__ void __launch_bounds__(kWaThreads, 1)
     const uint32_t ready[2] = {smem_u32(&bar.p[t][0]), smem_u32(&bar.p[t][1])};
     int s_par = 0, o_par = 0;
     for (int n = 0;; ++n) {
-      const int b = it.z;
-      const Work w = work_of<SPLIT>(a, b, it.x);
+      const Place pl = walk.place(a);
+      const int b = pl.b;
+      const Work w = work_of<LINE>(a, pl);
       const Tile tile = tile_of(w, t);
       if (tile.live) {
-        const int p = tile.pa + row % a.tb;
+        const int p = tile.pa + row % a.qb.tb;
         Row r;
         for (int i = w.begin; i < w.end; ++i) {
           if (!tile.sees(i, w.ns)) continue;
@@ -620,13 +769,15 @@ __global__ void __launch_bounds__(kWaThreads, 1)
           o_par ^= 1;
         }
         tc::fence_after_sync();
-        const int sub = row / a.tb, q = tile.q0 + row - sub * a.tb, h = tile.group * a.hb + sub;   // the row's query and head
+        const int sub = row / a.qb.tb, q = tile.q0 + row - sub * a.qb.tb, h = tile.group * a.hb + sub;   // the row's query and head
         const bool write = sub < a.hb && h < a.rep && q < w.ql;
-        const int head = it.y * a.rep + h;
+        const int head = pl.hk * a.rep + h;
         const int64_t at = (static_cast<int64_t>(b) * a.Hq + head) * a.Tq + q;
-        float inv = SPLIT ? 1.f : r.l == 0.f ? 0.f : 1.f / r.l;
+        const bool part = LINE && !pl.whole;
+        const int slot = 2 * blockIdx.x + (n > 0);
+        float inv = part ? 1.f : r.l == 0.f ? 0.f : 1.f / r.l;
         if (!wait.ok) inv = __int_as_float(0x7fffffff);
-        uint8_t* dst = !SPLIT ? a.out.row(b, head, q) : reinterpret_cast<uint8_t*>(a.part + (w.split * a.rows + at) * kD);
+        uint8_t* dst = a.out.row(b, head, q);
 #pragma unroll 1
         for (int c = 0; c < kD; c += 32) {
           float o[32];
@@ -639,7 +790,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
           }
           if (write) {
             uint32_t u[32];
-            if (!SPLIT) {
+            if (!part) {
 #pragma unroll
               for (int e = 0; e < 16; ++e) u[e] = pack2<BF>(o[2 * e] * inv, o[2 * e + 1] * inv);
               if (a.wide_out) {
@@ -653,20 +804,19 @@ __global__ void __launch_bounds__(kWaThreads, 1)
 #pragma unroll
               for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * inv);
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) st_global32(dst + (c + e) * 4, u + e);
+              for (int e = 0; e < 32; e += 8) st_global32(part_sums(a, slot, t, row, c + e), u + e);
             }
           }
         }
-        if (SPLIT && write) {
-          float2* ml = reinterpret_cast<float2*>(a.part + a.splits * a.rows * kD);
-          ml[w.split * a.rows + at] = make_float2(r.m * a.scale, wait.ok ? r.l : inv);
-        } else if (!SPLIT && write && a.lse) {
+        if (part && write) {
+          *part_ml(a, slot, t, row) = make_float2(r.m * a.scale, wait.ok ? r.l : inv);
+        } else if (write && a.lse) {
           const float v = r.l == 0.f ? -INFINITY : (r.m * a.scale + (log2f(r.l) - Weights<BF>::shift)) * 0.6931471805599453f;
           a.lse[at] = wait.ok ? v : inv;
         }
         tc::fence_before_sync();   // the sums are read before the next item's products overwrite them
       }
-      if (!next_item(bar, answers, n, wait, it)) break;
+      if (!walk.next(a, bar, answers, n, wait)) break;
     }
   }
   if (!wait.ok) tc::report_giveup(tc::kGiveupWindow);
@@ -675,94 +825,137 @@ __global__ void __launch_bounds__(kWaThreads, 1)
   if (warp == kWaMmaWarp) tc::tmem_dealloc(tmem, kWaCols);
 }
 
-// One partial result of a row: maximum (log2 units), sum, four channels of the lane.
-struct Part {
-  float m, l;
-  float4 o;
-  __device__ __forceinline__ void add(float mb, float lb, const float4& ob) {
-    const float mn = fmaxf(m, mb), sub = mn == -INFINITY ? 0.f : mn;
-    const float f = ex2(m - sub), fb = ex2(mb - sub);
-    l = l * f + lb * fb;
-    o = make_float4(o.x * f + ob.x * fb, o.y * f + ob.y * fb, o.z * f + ob.z * fb, o.w * f + ob.w * fb);
-    m = mn;
-  }
-};
-// Joins the parts of query rows, in a fixed order, four channels a lane.  WARPS warps share a row,
-// each with every WARPS-th part, BATCH of them requested together.
-template <bool BF, int WARPS, int BATCH>
-__global__ void __launch_bounds__(128) window_join_kernel(const WindowArgs a) {
-  constexpr int kRows = 4 / WARPS;   // rows of a CTA
-  __shared__ float4 s_o[4][32];
-  __shared__ float2 s_ml[4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = warp % WARPS;
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * kRows + warp / WARPS;
+constexpr int kLineWords = (kNumSMs + 31) / 32;
+// CTA (slice, k): joins ROWS rows of the k-th item of the line that is cut, in a fixed order.  A thread
+// takes 8 channels of a row (a part's rows lie side by side); GROUPS sets of threads share the parts,
+// BATCH of them requested together.
+template <bool BF, int ROWS, int GROUPS, int BATCH>
+__global__ void __launch_bounds__(ROWS * (kD / 8) * GROUPS) window_join_kernel(const WindowArgs a) {
+  constexpr int kThreads = ROWS * (kD / 8);   // of a group
+  __shared__ float s_o[GROUPS > 1 ? GROUPS - 1 : 1][8][kThreads];
+  __shared__ float2 s_ml[GROUPS > 1 ? GROUPS - 1 : 1][kThreads];
+  const int tid = threadIdx.x % kThreads, group = threadIdx.x / kThreads, lane = threadIdx.x & 31;
   pdl_wait();
-  bool live = at < a.rows;
-  const int64_t row = live ? at : 0;
-  const int q = static_cast<int>(row % a.Tq), head = static_cast<int>(row / a.Tq % a.Hq), b = static_cast<int>(row / a.Tq / a.Hq);
-  live = live && !(a.q_lens && q >= min(max(a.q_lens[b], 0), a.Tq));
-  Part sum = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  int c0 = -1;   // the first CTA of that item: the k-th that has begun one and not ended it
+  if (a.share > 0) {
+    c0 = blockIdx.y * a.share;
+  } else {
+    int k = blockIdx.y;
+    uint32_t begun[kLineWords];
+#pragma unroll
+    for (int w = 0; w < kLineWords; ++w) begun[w] = __ballot_sync(0xffffffffu, w * 32 + lane < a.ctas && part_cut(a, w * 32 + lane)->z >= 0);
+#pragma unroll
+    for (int w = 0; w < kLineWords; ++w) {
+      const uint32_t hit = __ballot_sync(0xffffffffu, (begun[w] >> lane & 1u) && __popc(begun[w] & ((1u << lane) - 1u)) == k);
+      if (hit) c0 = w * 32 + __ffs(hit) - 1;
+      k -= __popc(begun[w]);
+    }
+    if (c0 < 0) return;
+  }
+  const int4 cut = *part_cut(a, c0);
+  const int c1 = cut.z;
+  if (c1 < 0) return;
+  const int b = cut.x / a.qb.blocks, blk = a.qb.blocks - 1 - cut.x % a.qb.blocks, hk = cut.y / a.per, u = cut.y % a.per;
+  const int rows = a.tile_rows, ch = tid / ROWS * 8;
+  const int i = blockIdx.x * ROWS + tid % ROWS, t = i >= rows, row = i - t * rows, sub = row / a.qb.tb;
+  const int heads = a.qb.pair_heads ? 2 * u + t : u, h = heads * a.hb + sub;
+  const int q = first_row(a.qb, blk) + (a.qb.pair_heads ? 0 : t * a.qb.tb) + row - sub * a.qb.tb;
+  const bool live = i < 2 * rows && heads < a.groups && h < a.rep && q < q_len(a, b);
+  float m = -INFINITY, l = 0.f, o[8] = {};
+  const auto add = [&](float2 x, const float (&p)[8]) {
+    const float mn = fmaxf(m, x.x), ref = mn == -INFINITY ? 0.f : mn;
+    const float f = ex2(m - ref), fx = ex2(x.x - ref);
+    l = l * f + x.y * fx;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = o[e] * f + p[e] * fx;
+    m = mn;
+  };
   if (live) {
-    const float2* ml = reinterpret_cast<const float2*>(a.part + a.splits * a.rows * kD) + row;
-    for (int s0 = first; s0 < a.splits; s0 += BATCH * WARPS) {
+    for (int p0 = c0 + group; p0 <= c1; p0 += BATCH * GROUPS) {
       float2 x[BATCH];
-      float4 os[BATCH];
+      float4 v[BATCH][2];
 #pragma unroll
       for (int e = 0; e < BATCH; ++e) {
-        const int s = s0 + e * WARPS;
-        x[e] = s < a.splits ? ml[s * a.rows] : make_float2(-INFINITY, 0.f);
+        const int p = p0 + e * GROUPS, slot = 2 * p + (p == c0 ? cut.w : 0);
+        x[e] = make_float2(-INFINITY, 0.f);
+        v[e][0] = v[e][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p <= c1) {
+          const float4* sums = reinterpret_cast<const float4*>(part_sums(a, slot, t, row, ch));
+          x[e] = *part_ml(a, slot, t, row);
+          v[e][0] = sums[0];
+          v[e][1] = sums[1];
+        }
       }
 #pragma unroll
       for (int e = 0; e < BATCH; ++e) {
-        os[e] = make_float4(0.f, 0.f, 0.f, 0.f);
         // a sum of 0: nothing seen there, and no sums written
-        if (x[e].y != 0.f) os[e] = reinterpret_cast<const float4*>(a.part + ((s0 + e * WARPS) * a.rows + row) * kD)[lane];
+        const bool none = x[e].y == 0.f;
+        const float w[8] = {none ? 0.f : v[e][0].x, none ? 0.f : v[e][0].y, none ? 0.f : v[e][0].z, none ? 0.f : v[e][0].w,
+                            none ? 0.f : v[e][1].x, none ? 0.f : v[e][1].y, none ? 0.f : v[e][1].z, none ? 0.f : v[e][1].w};
+        add(x[e], w);
       }
-#pragma unroll
-      for (int e = 0; e < BATCH; ++e) sum.add(x[e].x, x[e].y, os[e]);
     }
   }
-  if (WARPS > 1) {
-    s_o[warp][lane] = sum.o;
-    if (lane == 0) s_ml[warp] = make_float2(sum.m, sum.l);
-    __syncthreads();
-    if (first != 0) return;
+  if (GROUPS > 1) {
+    if (group > 0) {
 #pragma unroll
-    for (int e = 1; e < WARPS; ++e) sum.add(s_ml[warp + e].x, s_ml[warp + e].y, s_o[warp + e][lane]);
+      for (int e = 0; e < 8; ++e) s_o[group - 1][e][tid] = o[e];
+      s_ml[group - 1][tid] = make_float2(m, l);
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 0; g < GROUPS - 1; ++g) {
+      float w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = s_o[g][e][tid];
+      add(s_ml[g][tid], w);
+    }
   }
   if (!live) return;
-  const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
-  *reinterpret_cast<uint2*>(a.out.row(b, head, q) + lane * 8) =
-      make_uint2(pack2<BF>(sum.o.x * inv, sum.o.y * inv), pack2<BF>(sum.o.z * inv, sum.o.w * inv));
-  if (lane == 0 && a.lse)
-    a.lse[row] = sum.l == 0.f ? -INFINITY : (sum.m + (log2f(sum.l) - Weights<BF>::shift)) * 0.6931471805599453f;
+  const int head = hk * a.rep + h;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<uint4*>(a.out.row(b, head, q) + ch * 2) =
+      make_uint4(pack2<BF>(o[0] * inv, o[1] * inv), pack2<BF>(o[2] * inv, o[3] * inv), pack2<BF>(o[4] * inv, o[5] * inv),
+                 pack2<BF>(o[6] * inv, o[7] * inv));
+  if (ch == 0 && a.lse)
+    a.lse[(static_cast<int64_t>(b) * a.Hq + head) * a.Tq + q] =
+        l == 0.f ? -INFINITY : (m + (log2f(l) - Weights<BF>::shift)) * 0.6931471805599453f;
 }
 
-// The split of a call: rows and heads of a tile, items, and parts of each item.
+// The layout of a call: rows and heads of a tile, items, and whether their key tiles form a line.
 struct Plan {
-  int tb, hb, groups, blocks, splits;
-  bool pair_heads;
-  int64_t per_head;   // items of one key head and batch row, without the splits
+  QueryBlocks qb;
+  int hb, groups, per, tile_rows, ctas, share;   // ctas: of the line; 0: a CTA an item
+  int64_t per_head;            // items of one key head and batch row
 };
 // `pack`: heads of a group may share a tile (their rows are apart in memory).
 Plan plan_of(int B, int Hq, int Hkv, int Tq, int Tk, int window, int sinks, bool pack) {
   Plan p;
   const int rep = Hq / Hkv;
   p.hb = pack ? std::min(rep, std::max(1, kWaRows / Tq)) : 1;
-  p.tb = p.hb > 1 ? Tq : kWaRows;
+  p.qb.tb = p.hb > 1 ? Tq : kWaRows;
+  p.tile_rows = std::min(p.qb.tb, Tq) * p.hb;
+  p.qb.window = window;
+  p.qb.sinks = sinks;
   p.groups = (rep + p.hb - 1) / p.hb;
-  const int blocks = (Tq + p.tb - 1) / p.tb;
-  p.pair_heads = p.groups % 2 == 0 || blocks == 1;
-  p.blocks = p.pair_heads ? blocks : (blocks + 1) / 2;
-  p.per_head = static_cast<int64_t>(p.blocks) * (p.pair_heads ? (p.groups + 1) / 2 : p.groups);
-  // Parts of an item: the number that ends soonest by this estimate, in key tiles of an item's two
-  // query tiles (1.4 us each).  An item costs 3 beside its tiles, a part 12 (its sums go out to
-  // memory, 128 KB, and come back); the longest item bounds the end, and items of about one length
-  // run in whole waves.  Measured: 8192 causal rows of 4 heads, 128 items, 93 us whole and 72 in
-  // two parts each; 4096 rows of 8 heads, 128 items, 52 whole and 66 in two; 64 rows of 8 heads
-  // behind 16384 keys, 4 items, 26 us in 32 parts and 33 in 64.
+  const int blocks = (Tq + p.qb.tb - 1) / p.qb.tb;
+  p.qb.pair_heads = p.groups % 2 == 0 || blocks == 1;
+  p.qb.blocks = p.qb.pair_heads ? blocks : (blocks + 1) / 2;
+  p.per = p.qb.pair_heads ? (p.groups + 1) / 2 : p.groups;
+  p.per_head = static_cast<int64_t>(p.qb.blocks) * p.per;
+  p.ctas = p.share = 0;
+  // How the call ends soonest, by estimates in key tiles of an item's two query tiles (1.4 us each; an
+  // item costs 3 beside its own).
+  //   a CTA an item: the longest item bounds the end, and items of about one length run in whole waves
+  //   up to half as many items as SMs: `share` CTAs each (the sums of cut items go out to memory and come
+  //     back: 3, and 0.7 for every 16 parts)
+  //   more: equal parts of the line, 13 and 3 a wave for the cuts
+  // Measured, a CTA an item / cut: 8192 causal rows of 4 heads, 128 items, 99 / 66 us; 4096 of 8 heads, 128
+  // items, 54 / 46; 2048 of 32, 256 items, 46 / 49; 64 rows of 8 heads behind 16384 keys, 4 items, 184 / 22; 2 x
+  // 256 rows of 16 heads behind 2744, 64 items, 36 / 22 (and 25 as a line).
   const int64_t items = p.per_head * Hkv * B;
-  const int64_t rows = static_cast<int64_t>(p.pair_heads ? 1 : 2) * p.tb;
+  const int64_t rows = static_cast<int64_t>(p.qb.pair_heads ? 1 : 2) * p.qb.tb;
   double longest = Tk, mean = Tk - 0.5 * std::min(Tq, Tk);
   if (window > 0) {
     longest = std::min<double>(longest, static_cast<double>(window) + sinks + rows);
@@ -770,19 +963,25 @@ Plan plan_of(int B, int Hq, int Hkv, int Tq, int Tk, int window, int sinks, bool
   }
   longest = std::max(1.0, longest / kWaRows);
   mean = std::max(1.0, mean / kWaRows);
-  double best = 1e30;
-  for (int s = 1; s == 1 || (s <= 32 && longest / s >= 2.0); ++s) {
-    const double cost = s == 1 ? 3 : 12, waves = static_cast<double>(items) * s / kNumSMs;
-    const double even = mean > 0.75 * longest ? std::ceil(waves) : waves + 0.5;
-    const double est = std::max(longest / s + cost, even * (mean / s + cost));
-    if (est < best - 1e-9) {
-      best = est;
-      p.splits = s;
+  const double waves = static_cast<double>(items) / kNumSMs;
+  double best = std::max(longest + 3, (mean > 0.75 * longest ? std::ceil(waves) : waves + 0.5) * (mean + 3));
+  if (items <= kNumSMs / 2) {
+    for (int s = 2; s <= kNumSMs / items && longest / s >= 2.0; ++s) {
+      const double est = longest / s + 6 + 0.7 * ((s + 15) / 16);
+      if (est < best - 1e-9) {
+        best = est;
+        p.share = s;
+        p.ctas = static_cast<int>(items) * s;
+      }
     }
+  } else if (waves * (mean + 6) + 13 < best && items <= 8 * kNumSMs && static_cast<int64_t>(B) * p.qb.blocks <= 256 &&
+             static_cast<double>(items) * (static_cast<double>(Tk) / kWaRows + 2 + kItemPlaces) < 2147483647.0) {
+    // (a warp adds up the entries in a few steps, and places stay below 2^31)
+    p.ctas = kNumSMs;
   }
   return p;
 }
-size_t part_bytes(const Plan& p, int64_t rows) { return p.splits > 1 ? static_cast<size_t>(p.splits) * rows * (kD + 2) * 4 : 0; }
+size_t part_bytes(const Plan& p) { return static_cast<size_t>(p.ctas) * 4 * p.tile_rows * (kD + 2) * 4 + p.ctas * 16; }
 bool packs(const mikv_rows& q, int Hq) { return Hq == 1 || q.stride_h >= kD; }
 
 // 4-D tensor map (channel, row, head, batch row) of a strided view, box 64 x 128 x 1 x 1 with
@@ -813,7 +1012,7 @@ int encode_queries(CUtensorMap* map, const mikv_rows& r, int T, int rep, int Hkv
   const cuuint64_t dims[5] = {kD, static_cast<cuuint64_t>(T), *mh ? static_cast<cuuint64_t>(rep) : 1, *mh ? static_cast<cuuint64_t>(Hkv) : 1,
                               *mb ? static_cast<cuuint64_t>(B) : 1};
   const cuuint64_t strides[4] = {row, head, head * static_cast<cuuint64_t>(*mh ? rep : 1), *mb ? static_cast<cuuint64_t>(r.stride_b) * 2 : row};
-  const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(p.tb), static_cast<cuuint32_t>(p.hb), 1, 1}, estr[5] = {1, 1, 1, 1, 1};
+  const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(p.qb.tb), static_cast<cuuint32_t>(p.hb), 1, 1}, estr[5] = {1, 1, 1, 1, 1};
   const CUresult e = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, r.data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (e != CUDA_SUCCESS) return fail(MIKV_ECUDA, "window_attention: tensor map of q (error %d)", static_cast<int>(e));
@@ -831,8 +1030,7 @@ extern "C" size_t mikv_window_attention_workspace_bytes(int B, int Hq, int Hkv, 
     return 0;
   size_t most = 0;   // heads that repeat one another's rows are not packed
   for (bool pack : {true, false})
-    most = std::max(most, part_bytes(plan_of(B, Hq, Hkv, Tq, Tk, window >= Tk ? 0 : window, std::min(sinks, Tk), pack),
-                                     static_cast<int64_t>(B) * Hq * Tq));
+    most = std::max(most, part_bytes(plan_of(B, Hq, Hkv, Tq, Tk, window >= Tk ? 0 : window, std::min(sinks, Tk), pack)));
   return most;
 }
 
@@ -863,46 +1061,50 @@ extern "C" int mikv_window_attention(const mikv_rows* q, const mikv_rows* k, con
   a.rep = Hq / Hkv;
   a.Tq = Tq;
   a.Tk = Tk;
-  a.window = window >= Tk ? 0 : window;   // one that reaches every key is none
-  a.sinks = std::min(sinks, Tk);
-  a.rows = static_cast<int64_t>(B) * Hq * Tq;
+  a.B = B;
+  a.Hkv = Hkv;
   a.wide_out = ((reinterpret_cast<uintptr_t>(out->data) | static_cast<uintptr_t>(a.out.sb | a.out.sh | a.out.st)) & 31u) == 0;
   a.scale = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
-  const Plan p = plan_of(B, Hq, Hkv, Tq, Tk, a.window, a.sinks, packs(*q, Hq));
-  a.tb = p.tb;
+  // a window that reaches every key is none
+  const Plan p = plan_of(B, Hq, Hkv, Tq, Tk, window >= Tk ? 0 : window, std::min(sinks, Tk), packs(*q, Hq));
+  a.qb = p.qb;
   a.hb = p.hb;
   a.groups = p.groups;
-  a.blocks = p.blocks;
-  a.pair_heads = p.pair_heads;
-  a.splits = p.splits;
-  if (p.per_head * p.splits > 0x7fffffffLL) return fail(MIKV_ESHAPE, "window_attention: Tq=%d Hq=%d", Tq, Hq);
-  const size_t need = part_bytes(p, a.rows);
+  a.per = p.per;
+  a.tile_rows = p.tile_rows;
+  a.ctas = p.ctas;
+  a.share = p.share;
+  if (p.per_head > 0x7fffffffLL) return fail(MIKV_ESHAPE, "window_attention: Tq=%d Hq=%d", Tq, Hq);
+  const size_t need = mikv_window_attention_workspace_bytes(B, Hq, Hkv, Tq, Tk, window, sinks);   // whatever q's strides
   if (need > 0) {
     if (!ws) return fail(MIKV_EINVAL, "window_attention: null workspace");
     if (reinterpret_cast<uintptr_t>(ws) & 31u) return fail(MIKV_EALIGN, "window_attention: workspace must be 32-byte aligned");
     if (ws_bytes < need) return fail(MIKV_ESHAPE, "window_attention: workspace %zu < %zu", ws_bytes, need);
   }
   a.part = static_cast<float*>(ws);
-  if (int e = encode_queries(&qm, *q, Tq, a.rep, Hkv, B, p, &a.qb, &a.qh)) return e;
+  if (int e = encode_queries(&qm, *q, Tq, a.rep, Hkv, B, p, &a.qbat, &a.qh)) return e;
   if (int e = encode_view(&km, *k, Tk, Hkv, B, "k", &a.kb, &a.kh)) return e;
   if (int e = encode_view(&vm, *v, Tk, Hkv, B, "v", &a.vb, &a.vh)) return e;
   const bool bf = type == MIKV_PAGES_BF16;
-  const auto kern = bf ? p.splits > 1 ? window_attention_kernel<true, true> : window_attention_kernel<true, false>
-                       : p.splits > 1 ? window_attention_kernel<false, true> : window_attention_kernel<false, false>;
+  const bool line = p.ctas > 0;
+  const auto kern = bf ? line ? window_attention_kernel<true, true> : window_attention_kernel<true, false>
+                       : line ? window_attention_kernel<false, true> : window_attention_kernel<false, false>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kWaSmem);
   if (e != cudaSuccess) return check_launch_after(e, "window_attention_kernel");
   const cudaStream_t st = as_stream(stream);
-  kern<<<dim3(static_cast<unsigned>(p.per_head * p.splits), Hkv, B), kWaThreads, kWaSmem, st>>>(qm, km, vm, a);
+  const dim3 grid = line ? dim3(p.ctas) : dim3(static_cast<unsigned>(p.per_head), Hkv, B);
+  kern<<<grid, kWaThreads, kWaSmem, st>>>(qm, km, vm, a);
   if (int r = check_launch("window_attention_kernel")) return r;
-  if (p.splits == 1) return MIKV_OK;
-  // Two parts at a time of rows enough to hide it, eight where a row has more; and four warps a row
-  // where there are not eight rows an SM (five rows of 8 heads, 32 parts: 18 us with one warp a row,
-  // 13 with four; 4096 rows, 9 parts: 30 and 35).
-  const bool few = p.splits <= 4, wide = !few && a.rows <= 8 * kNumSMs;
-  const auto join = few    ? bf ? window_join_kernel<true, 1, 2> : window_join_kernel<false, 1, 2>
-                    : wide ? bf ? window_join_kernel<true, 4, 8> : window_join_kernel<false, 4, 8>
-                           : bf ? window_join_kernel<true, 1, 8> : window_join_kernel<false, 1, 8>;
-  const int64_t per = wide ? 1 : 4;
-  return check_launch_after(launch_after(join, dim3(static_cast<unsigned>((a.rows + per - 1) / per)), dim3(128), 0, st, a),
+  if (p.ctas < 2) return MIKV_OK;
+  // With 12 parts an item and more, few rows a CTA and 32 parts requested together: five rows of 8 heads, 32
+  // parts: 13 us in all, 16 with 16 rows a CTA; with few parts the other way round (64 items of two parts: 22
+  // and 33 us).
+  const int64_t items = p.per_head * Hkv * B;
+  const bool wide = p.ctas >= 12 * items;
+  const auto join = wide ? bf ? window_join_kernel<true, 4, 8, 4> : window_join_kernel<false, 4, 8, 4>
+                         : bf ? window_join_kernel<true, 16, 1, 4> : window_join_kernel<false, 16, 1, 4>;
+  const int rows = wide ? 4 : 16;
+  const dim3 joins((2 * a.tile_rows + rows - 1) / rows, static_cast<unsigned>(std::min<int64_t>(p.ctas - 1, items)));
+  return check_launch_after(launch_after(join, joins, dim3(wide ? 512 : 256), 0, st, a),
                             "window_join_kernel");
 }

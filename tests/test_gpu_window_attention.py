@@ -76,6 +76,27 @@ def test_few_rows_over_many_keys(dtype, B, Hkv, rep, Tq, Tk, window, sinks):
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("B,Hkv,rep,Tq,Tk,window,sinks", [
+    (1, 9, 1, 2500, 2500, 0, 0), (1, 3, 5, 1300, 5000, 0, 0), (1, 3, 5, 1300, 5000, 4000, 200), (2, 40, 2, 130, 3500, 0, 0),
+    (40, 2, 8, 40, 2000, 0, 0)])
+def test_key_tiles_shared_out_as_one_line(dtype, B, Hkv, rep, Tq, Tk, window, sinks):
+    """More items than half the SMs, cut where a CTA's equal part ends; ragged, empty and blind rows beside whole ones."""
+    q = _make(B, Hkv * rep, Tq, dtype, "bthd", 1)
+    k, v = _make(B, Hkv, Tk, dtype, "bhtd", 2), _make(B, Hkv, Tk, dtype, "bthd", 3)
+    assert _lib.load().mikv_window_attention_workspace_bytes(B, Hkv * rep, Hkv, Tq, Tk, window, sinks) > 0
+    _check(q, k, v, window, sinks)
+    ql, kl = [max(0, Tq - 301 * (b % 7)) for b in range(B)], [max(0, Tk - 411 * (b % 9)) for b in range(B)]
+    if B > 2:
+        kl[1], ql[2], kl[5] = 10, 0, 0          # rows that see nothing, no rows, no keys
+    _check(q, k, v, window, sinks, ql, kl)
+    out, lse = _run(q, k, v, window, sinks, ql, kl)
+    again = _run(q, k, v, window, sinks, ql, kl)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    _check(q, k, v, window, sinks, [0] * B, kl)          # nothing is asked: nothing is written
+    _check(q, k, v, window, sinks, ql, [0] * B)          # no keys at all
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (40, 3)])
 def test_padded_batches(dtype, window, sinks):
     """Lengths from none to all, more queries than keys; NaN behind every row's end."""
