@@ -949,11 +949,12 @@ Plan plan_of(int B, int Hq, int Hkv, int Tq, int Tk, int window, int sinks, bool
   // item costs 3 beside its own).
   //   a CTA an item: the longest item bounds the end, and items of about one length run in whole waves
   //   up to half as many items as SMs: `share` CTAs each (the sums of cut items go out to memory and come
-  //     back: 3, and 0.7 for every 16 parts)
+  //     back: 2, and 0.7 for every 16 parts)
   //   more: equal parts of the line, 13 and 3 a wave for the cuts
   // Measured, a CTA an item / cut: 8192 causal rows of 4 heads, 128 items, 99 / 66 us; 4096 of 8 heads, 128
-  // items, 54 / 46; 2048 of 32, 256 items, 46 / 49; 64 rows of 8 heads behind 16384 keys, 4 items, 184 / 22; 2 x
-  // 256 rows of 16 heads behind 2744, 64 items, 36 / 22 (and 25 as a line).
+  // items, 54 / 46; 2048 of 32, 256 items, 46 / 49; 64 rows of 8 heads behind 16384 keys, 4 items, 184 / 17; one row
+  // of 32 heads behind 700 keys, 8 items, 13 / 11, behind 300, 9 / 10; 2 x 256 rows of 16 heads behind 2744, 64
+  // items, two CTAs each 22 us, as a line 25.
   const int64_t items = p.per_head * Hkv * B;
   const int64_t rows = static_cast<int64_t>(p.qb.pair_heads ? 1 : 2) * p.qb.tb;
   double longest = Tk, mean = Tk - 0.5 * std::min(Tq, Tk);
@@ -966,8 +967,8 @@ Plan plan_of(int B, int Hq, int Hkv, int Tq, int Tk, int window, int sinks, bool
   const double waves = static_cast<double>(items) / kNumSMs;
   double best = std::max(longest + 3, (mean > 0.75 * longest ? std::ceil(waves) : waves + 0.5) * (mean + 3));
   if (items <= kNumSMs / 2) {
-    for (int s = 2; s <= kNumSMs / items && longest / s >= 2.0; ++s) {
-      const double est = longest / s + 6 + 0.7 * ((s + 15) / 16);
+    for (int s = 2; s <= kNumSMs / items && longest / s >= 1.0; ++s) {
+      const double est = longest / s + 5 + 0.7 * ((s + 15) / 16);
       if (est < best - 1e-9) {
         best = est;
         p.share = s;
@@ -1097,8 +1098,8 @@ extern "C" int mikv_window_attention(const mikv_rows* q, const mikv_rows* k, con
   if (int r = check_launch("window_attention_kernel")) return r;
   if (p.ctas < 2) return MIKV_OK;
   // With 12 parts an item and more, few rows a CTA and 32 parts requested together: five rows of 8 heads, 32
-  // parts: 13 us in all, 16 with 16 rows a CTA; with few parts the other way round (64 items of two parts: 22
-  // and 33 us).
+  // parts: 12.6 us in all, 15.9 with 16 rows a CTA and 16 parts; with few parts many rows a CTA (64 items of two
+  // parts: 22 us, 33 with threads that find no part).
   const int64_t items = p.per_head * Hkv * B;
   const bool wide = p.ctas >= 12 * items;
   const auto join = wide ? bf ? window_join_kernel<true, 4, 8, 4> : window_join_kernel<false, 4, 8, 4>
