@@ -525,7 +525,7 @@ size_t mikv_paged_attention_workspace_bytes(const mikv_pages* p, int n, int Hq, 
  * The softmax weights are rounded to the inputs' type before they meet the values; sums and
  * statistics are fp32.
  * ws >= mikv_window_attention_workspace_bytes(B, Hq, Hkv, Tq, Tk, window, sinks), 32-byte
- * aligned: sums of calls with few query rows, whose keys are split over the SMs (0 bytes, and
+ * aligned: sums of calls whose rows would leave SMs idle, and whose keys are shared out (0 bytes, and
  * ws may be NULL, otherwise); two calls must not share a workspace concurrently.
  * Errors: EINVAL (null, type, window, sinks), ESHAPE, EALIGN, EUNSUPPORTED (D), ECUDA.
  */
@@ -556,7 +556,7 @@ int mikv_set_attention_events(void* begin, void* end);
  * pipeline still ends in a bounded time, and what was issued before has that long to land),
  * the kernel writes NaN into the outputs of the affected CTA (prefill scores and -lse rows,
  * V.W_O norms, perturbation and y partial sums, windowed attention's rows under way; rows that
- * its CTA had taken over and not begun are left as they were) and sets a bit in a device-side
+ * its CTA had taken over and not begun are left as they were, or joined from what the workspace held) and sets a bit in a device-side
  * status word.
  * The call that launched it has already returned MIKV_OK (launches are asynchronous).
  * mikv_wait_status stores the OR of the bits set since the last clear in *bits:
