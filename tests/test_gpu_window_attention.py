@@ -96,6 +96,38 @@ def test_key_tiles_shared_out_as_one_line(dtype, B, Hkv, rep, Tq, Tk, window, si
     _check(q, k, v, window, sinks, ql, [0] * B)          # no keys at all
 
 
+@pytest.mark.parametrize("B,Hkv,rep,Tq,Tk,window,sinks", [(4, 3, 5, 700, 4000, 0, 0), (4, 3, 5, 700, 4000, 2000, 150), (2, 2, 3, 5, 3000, 0, 0),
+                                                          (3, 2, 16, 70, 2500, 900, 5)])
+def test_shared_out_keys_under_replay(B, Hkv, rep, Tq, Tk, window, sinks):
+    """Lengths that change between the replays of one graph, whose workspace holds NaN before each."""
+    q = _make(B, Hkv * rep, Tq, torch.float16, "bhtd", 1)
+    k, v = _make(B, Hkv, Tk, torch.float16, "bthd", 2), _make(B, Hkv, Tk, torch.float16, "bhtd", 3)
+    n = _lib.load().mikv_window_attention_workspace_bytes(B, Hkv * rep, Hkv, Tq, Tk, window, sinks)
+    assert n > 0
+    ws = torch.empty(n, dtype=torch.uint8, device=ph.DEV)
+    ql, kl = ph.ints([Tq] * B), ph.ints([Tk] * B)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device=ph.DEV)
+    go = lambda: _lib.mikv_window_attention(q, k, v, window, sinks, out, lse, q_lens=ql, k_lens=kl, ws=ws)
+    go()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go()
+    for turn in range(4):
+        lens = [([Tq] * B, [Tk] * B), ([Tq - 3 * b for b in range(B)], [Tk - 700 * b for b in range(B)]), ([0] * (B - 1) + [1], [77] * B),
+                ([Tq] * B, [Tq // 2] * B)][turn]
+        ql.copy_(ph.ints(lens[0]))
+        kl.copy_(ph.ints(lens[1]))
+        ws.fill_(255)
+        out.fill_(7)
+        lse.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = _run(q, k, v, window, sinks, *lens)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        _check(q, k, v, window, sinks, *lens)
+
+
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (40, 3)])
 def test_padded_batches(dtype, window, sinks):
