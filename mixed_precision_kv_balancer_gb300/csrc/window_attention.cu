@@ -10,9 +10,8 @@
 // group, or 256 rows of one head where the group is odd.  Where a chunk has 64 rows or fewer, a
 // tile packs the rows of several heads of the group.  Where the items of a call would leave SMs
 // idle, all their key tiles form one line, of which each CTA takes an equal part, and the items that
-// are cut are joined by a second kernel.  Key and value
-// tiles of 128 rows come through a ring of five 32 KB buffers (TMA, 128-byte swizzle); tiles
-// that none of the rows sees are not read.  Per key tile i and query tile t
+// are cut are joined by a second kernel.  Key and value tiles of 128 rows come through a ring of four
+// 32 KB buffers (TMA, 128-byte swizzle; a fifth was no faster); tiles that none of the rows sees are not read.  Per key tile i and query tile t
 //   S_t = Q_t K_i^T     tcgen05, both operands in shared memory, 128 fp32 TMEM columns
 //   P_t = exp2(...)     four warps, one query row a thread, written over S_t as 16-bit pairs
 //   O_t += P_t V_i      tcgen05, P from TMEM, V as it lies (rows are the contraction)
@@ -44,11 +43,12 @@ namespace {
 
 constexpr int kWaRows = kKeyRows;                // query rows and key rows of a tile
 constexpr int kWaNarrow = 32;                    // columns of a tile that holds the last few sinks
-constexpr int kWaRing = 5;
+constexpr int kWaRing = 4;
 constexpr int kMaxRows = 1 << 30;                // of q or k: positions and their differences fit 32 bits
 constexpr int kWaThreads = 352;                  // 2 x 4 softmax warps, the TMA warp, 2 MMA warps
 constexpr int kWaTmaWarp = 8, kWaMmaWarp = 9;
-constexpr int kWaSmem = (2 + kWaRing) * tc::kTileBytes + 1024;
+constexpr int kWaOut = 4096;                     // a warp's 32 output rows, 64 channels of them
+constexpr int kWaSmem = (2 + kWaRing) * tc::kTileBytes + 8 * kWaOut + 1024;
 constexpr uint32_t kWaCols = 512;                // S_0, S_1, O_0, O_1: 128 columns each
 constexpr uint32_t kWaO = 256;
 
@@ -534,7 +534,7 @@ __device__ __forceinline__ int4* part_cut(const WindowArgs& a, int c) {
 template <bool BF, bool LINE>
 __global__ void __launch_bounds__(kWaThreads, 1)
     window_attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                            const __grid_constant__ CUtensorMap vmap, const WindowArgs a) {
+                            const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap, const WindowArgs a) {
   extern __shared__ uint8_t smem[];
   __shared__ WaBars bar;
   __shared__ __align__(16) uint4 answers[2];
@@ -778,33 +778,72 @@ __global__ void __launch_bounds__(kWaThreads, 1)
         float inv = part ? 1.f : r.l == 0.f ? 0.f : 1.f / r.l;
         if (!wait.ok) inv = __int_as_float(0x7fffffff);
         uint8_t* dst = a.out.row(b, head, q);
+        // A warp whose 32 rows follow one another, and count as far as there are any, hands them to the TMA
+        // through a buffer of its own: written by the threads, 32 rows an instruction, they hold the warp up
+        // (2 x 16384 rows of 4 heads under a window of 1024: 73 us, 69 this way).
+        const int q_first = tile.q0 + (warp & 3) * 32;
+        const bool whole_rows = !part && a.hb == 1 && h < a.rep && q_first < w.ql && (q_first + 32 <= w.ql || w.ql == a.Tq);
+        if (__all_sync(0xffffffffu, whole_rows)) {
+          const uint32_t stage = ring + kWaRing * tc::kTileBytes + warp * kWaOut;
 #pragma unroll 1
-        for (int c = 0; c < kD; c += 32) {
-          float o[32];
-          if (tile.last >= 0) {
-            ld32(to + c, o);
-            wait_ld();
-          } else {
+          for (int c = 0; c < kD; c += 64) {
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");   // the buffer is free
+            __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.f;
-          }
-          if (write) {
-            uint32_t u[32];
-            if (!part) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) u[e] = pack2<BF>(o[2 * e] * inv, o[2 * e + 1] * inv);
-              if (a.wide_out) {
-                st_global32(dst + c * 2, u);
-                st_global32(dst + c * 2 + 32, u + 8);
+            for (int half = 0; half < 2; ++half) {
+              float o[32];
+              if (tile.last >= 0) {
+                ld32(to + c + half * 32, o);
+                wait_ld();
               } else {
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(dst + (c + 2 * e) * 2) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+                for (int e = 0; e < 32; ++e) o[e] = 0.f;
               }
-            } else if (tile.last >= 0) {   // a part without a visible key is told by its sum of 0
 #pragma unroll
-              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * inv);
+              for (int k = 0; k < 4; ++k)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(stage + lane * 128 + (((half * 4 + k) ^ (lane & 7)) << 4)),
+                             "r"(pack2<BF>(o[8 * k] * inv, o[8 * k + 1] * inv)), "r"(pack2<BF>(o[8 * k + 2] * inv, o[8 * k + 3] * inv)),
+                             "r"(pack2<BF>(o[8 * k + 4] * inv, o[8 * k + 5] * inv)), "r"(pack2<BF>(o[8 * k + 6] * inv, o[8 * k + 7] * inv))
+                             : "memory");
+            }
+            tc::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];\n" ::"l"(&omap), "r"(c),
+                           "r"(q_first), "r"(head), "r"(b), "r"(stage)
+                           : "memory");
+              asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < kD; c += 32) {
+            float o[32];
+            if (tile.last >= 0) {
+              ld32(to + c, o);
+              wait_ld();
+            } else {
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) st_global32(part_sums(a, slot, t, row, c + e), u + e);
+              for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            }
+            if (write) {
+              uint32_t u[32];
+              if (!part) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) u[e] = pack2<BF>(o[2 * e] * inv, o[2 * e + 1] * inv);
+                if (a.wide_out) {
+                  st_global32(dst + c * 2, u);
+                  st_global32(dst + c * 2 + 32, u + 8);
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(dst + (c + 2 * e) * 2) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+                }
+              } else if (tile.last >= 0) {   // a part without a visible key is told by its sum of 0
+#pragma unroll
+                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * inv);
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) st_global32(part_sums(a, slot, t, row, c + e), u + e);
+              }
             }
           }
         }
@@ -818,6 +857,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
       }
       if (!walk.next(a, bar, answers, n, wait)) break;
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");   // the last rows are written before the CTA ends
   }
   if (!wait.ok) tc::report_giveup(tc::kGiveupWindow);
   tc::fence_before_sync();
@@ -988,7 +1028,7 @@ bool packs(const mikv_rows& q, int Hq) { return Hq == 1 || q.stride_h >= kD; }
 // 4-D tensor map (channel, row, head, batch row) of a strided view, box 64 x 128 x 1 x 1 with
 // 128-byte swizzle.  A dimension of stride 0 (a repeated head or batch row) has one entry in
 // the map; *mb and *mh tell whether the coordinate counts.
-int encode_view(CUtensorMap* map, const mikv_rows& r, int T, int H, int B, const char* name, int* mb, int* mh) {
+int encode_view(CUtensorMap* map, const mikv_rows& r, int T, int H, int B, int rows, const char* name, int* mb, int* mh) {
   const auto enc = tc::tensor_map_encoder();
   if (!enc) return fail(MIKV_ECUDA, "window_attention: cuTensorMapEncodeTiled unavailable");
   *mh = H > 1 && r.stride_h != 0;
@@ -996,7 +1036,7 @@ int encode_view(CUtensorMap* map, const mikv_rows& r, int T, int H, int B, const
   const cuuint64_t row = T > 1 ? static_cast<cuuint64_t>(r.stride_t) * 2 : kD * 2;
   const cuuint64_t dims[4] = {kD, static_cast<cuuint64_t>(T), *mh ? static_cast<cuuint64_t>(H) : 1, *mb ? static_cast<cuuint64_t>(B) : 1};
   const cuuint64_t strides[3] = {row, *mh ? static_cast<cuuint64_t>(r.stride_h) * 2 : row, *mb ? static_cast<cuuint64_t>(r.stride_b) * 2 : row};
-  const cuuint32_t box[4] = {64, kWaRows, 1, 1}, estr[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1}, estr[4] = {1, 1, 1, 1};
   const CUresult e = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, r.data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (e != CUDA_SUCCESS) return fail(MIKV_ECUDA, "window_attention: tensor map of %s (error %d)", name, static_cast<int>(e));
@@ -1052,7 +1092,7 @@ extern "C" int mikv_window_attention(const mikv_rows* q, const mikv_rows* k, con
   if ((Tq > 1 && (q->stride_t < kD || out->stride_t < kD)) || (Tk > 1 && (k->stride_t < kD || v->stride_t < kD)) ||
       (Hq > 1 && out->stride_h < kD) || (B > 1 && out->stride_b < kD))
     return fail(MIKV_EINVAL, "window_attention: rows overlap");
-  CUtensorMap qm, km, vm;
+  CUtensorMap qm, km, vm, om;
   WindowArgs a;
   a.out = row_view(*out);
   a.lse = lse;
@@ -1084,8 +1124,10 @@ extern "C" int mikv_window_attention(const mikv_rows* q, const mikv_rows* k, con
   }
   a.part = static_cast<float*>(ws);
   if (int e = encode_queries(&qm, *q, Tq, a.rep, Hkv, B, p, &a.qbat, &a.qh)) return e;
-  if (int e = encode_view(&km, *k, Tk, Hkv, B, "k", &a.kb, &a.kh)) return e;
-  if (int e = encode_view(&vm, *v, Tk, Hkv, B, "v", &a.vb, &a.vh)) return e;
+  if (int e = encode_view(&km, *k, Tk, Hkv, B, kWaRows, "k", &a.kb, &a.kh)) return e;
+  if (int e = encode_view(&vm, *v, Tk, Hkv, B, kWaRows, "v", &a.vb, &a.vh)) return e;
+  int ob, oh;   // rows of out are apart: both coordinates count where there is more than one
+  if (int e = encode_view(&om, *out, Tq, Hq, B, 32, "out", &ob, &oh)) return e;
   const bool bf = type == MIKV_PAGES_BF16;
   const bool line = p.ctas > 0;
   const auto kern = bf ? line ? window_attention_kernel<true, true> : window_attention_kernel<true, false>
@@ -1094,7 +1136,7 @@ extern "C" int mikv_window_attention(const mikv_rows* q, const mikv_rows* k, con
   if (e != cudaSuccess) return check_launch_after(e, "window_attention_kernel");
   const cudaStream_t st = as_stream(stream);
   const dim3 grid = line ? dim3(p.ctas) : dim3(static_cast<unsigned>(p.per_head), Hkv, B);
-  kern<<<grid, kWaThreads, kWaSmem, st>>>(qm, km, vm, a);
+  kern<<<grid, kWaThreads, kWaSmem, st>>>(qm, km, vm, om, a);
   if (int r = check_launch("window_attention_kernel")) return r;
   if (p.ctas < 2) return MIKV_OK;
   // With 12 parts an item and more, few rows a CTA and 32 parts requested together: five rows of 8 heads, 32
