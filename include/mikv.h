@@ -475,7 +475,8 @@ size_t mikv_page_workspace_bytes(const mikv_pages* p, int n);
  * above T is T, one below 1 writes nothing).  start: what mikv_page_reserve wrote, rows with
  * start < 0 are skipped; NULL: the sequence's last counts[i] slots.  Slots at or past the
  * sequence's length are not written, nor are rows whose sequence is out of range or named by
- * an earlier row.  INT8: quantised as in mikv_quantize_append.
+ * an earlier row.  INT8: quantised as in mikv_quantize_append; NaN does not count for a group's
+ * extremes, and a quotient that is no number (NaN, infinity / infinity) gives code 0.
  */
 int mikv_paged_append(const mikv_pages* p, int layer, const mikv_rows* k, const mikv_rows* v, int n, int T,
                       const int32_t* seqs, const int32_t* start, const int32_t* counts, void* stream);

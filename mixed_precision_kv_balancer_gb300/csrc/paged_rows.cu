@@ -31,8 +31,16 @@ __device__ __forceinline__ void find_rows(const Pool& p, int32_t s, int h, int s
   __syncthreads();
 }
 
+// The smaller one, or NaN where one is no number (fminf gives the other).
+__device__ __forceinline__ float min_or_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;\n" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // The quantiser of the contiguous cache at 8 bits on 8 fp16 channels a lane, 8 lanes a group, with
-// its arithmetic: s = fp16(fl(fl(mx - mn) / 255)), z = fp16(mn), code = clamp(rint_even(fl(fl(x - z) / s))).
+// its arithmetic: s = fp16(fl(fl(mx - mn) / 255)), z = fp16(mn), code = clamp(rint_even(fl(fl(x - z) / s))),
+// 0 where the quotient is no number.  NaN does not count for mn and mx.
 __device__ __forceinline__ uint2 quantize8(const uint4& x, uint32_t& meta) {
   const uint32_t in[4] = {x.x, x.y, x.z, x.w};
   float f[8];
@@ -60,11 +68,11 @@ __device__ __forceinline__ uint2 quantize8(const uint4& x, uint32_t& meta) {
   if (s != 0.f) {
     // A product with the reciprocal is within 2^-13 of the quotient (at most 300 after the clamp),
     // so both round to the same code unless the product lies that near to a half: then, and for
-    // what is no number, the division decides.  1.5 * 2^23 added leaves rint in the last bits.
+    // what is no number, the division decides (its conversion gives 0).  1.5 * 2^23 added leaves rint in the last bits.
     const float r = __frcp_rn(s);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float d = __fsub_rn(f[j], z), t = fminf(__fmul_rn(d, r), 300.f);
+      const float d = __fsub_rn(f[j], z), t = min_or_nan(__fmul_rn(d, r), 300.f);
       const float big = __fadd_rn(t, 12582912.f);
       int q = __float_as_int(big) - 0x4B400000;
       if (!(fabsf(t - (big - 12582912.f)) < 0.49f)) q = __float2int_rn(__fdiv_rn(d, s));
