@@ -382,7 +382,8 @@ int mikv_channel_quantize(const uint16_t* k, int units, int n, int D, int bits, 
  *   lens    int32 [max_seqs]: slots of each sequence, 0 for one that is not in use; the
  *           sequence owns the first ceil(len / page_size) entries of its row
  *   refs    int32 [n_pages]: how many sequences own the page; 0 = free.  A page whose count
- *           the caller raises itself is never handed out.
+ *           the caller raises itself is never handed out, and not appended to while the count
+ *           is above 1.
  * table, lens and refs are device arrays: the calls below read and change them on the stream,
  * so a whole step can be captured into a CUDA graph.  A new cache has lens 0 and refs 0.
  * Calls that change the same cache must be ordered (one stream, or events), like writes to any
@@ -439,6 +440,8 @@ int mikv_page_reserve(const mikv_pages* p, const int32_t* seqs, const int32_t* a
  * page is copied in all layers (its filled rows), so either sequence can grow.  ok[i]
  * (written) is 1, or 0 where refused: also where the child's length is not 0, or where the
  * child is a parent of the same call.  One parent may have several children in one call.
+ * Append the slots that a parent has reserved before it is forked: the pages they fill are
+ * shared by then and no longer written.
  */
 int mikv_page_fork(const mikv_pages* p, const int32_t* parent, const int32_t* child, int n, int32_t* ok, void* ws,
                    size_t ws_bytes, void* stream);
@@ -475,8 +478,11 @@ size_t mikv_page_workspace_bytes(const mikv_pages* p, int n);
  * above T is T, one below 1 writes nothing).  start: what mikv_page_reserve wrote, rows with
  * start < 0 are skipped; NULL: the sequence's last counts[i] slots.  Slots at or past the
  * sequence's length are not written, nor are rows whose sequence is out of range or named by
- * an earlier row.  INT8: quantised as in mikv_quantize_append; NaN does not count for a group's
- * extremes, and a quotient that is no number (NaN, infinity / infinity) gives code 0.
+ * an earlier row.  Nor are slots on a page whose count is above 1, which a fork shares: they
+ * are left as every owner reads them, and reported (mikv_wait_status, bit 128).  Slots that are
+ * reserved behind a sequence's last fork never lie on one.  INT8: quantised as in
+ * mikv_quantize_append; NaN does not count for a group's extremes, and a quotient that is no
+ * number (NaN, infinity / infinity) gives code 0.
  */
 int mikv_paged_append(const mikv_pages* p, int layer, const mikv_rows* k, const mikv_rows* v, int n, int T,
                       const int32_t* seqs, const int32_t* start, const int32_t* counts, void* stream);
@@ -565,6 +571,7 @@ int mikv_set_attention_events(void* begin, void* end);
  *   8 = K9 (output perturbation), 16 = mikv_wait_probe, 32 = mikv_window_attention,
  *   64 = no wait: an append, a gather or an attention over pages met a table entry outside the
  *   pool (its slots are skipped, read as zeros, or not seen)
+ *   128 = no wait: an append met a page that several sequences own (its slots are skipped)
  * and clears them if `clear` is non-zero.  It copies synchronously: call it after the work
  * in question has completed (e.g. after synchronising its stream).
  * Errors: EINVAL (null bits), ECUDA (the copy failed).

@@ -88,6 +88,7 @@ constexpr unsigned kGiveupPerturb = 8u;  // K9, perturb_tc_kernel
 constexpr unsigned kGiveupProbe = 16u;   // wait_probe_kernel (mikv_wait_probe)
 constexpr unsigned kGiveupWindow = 32u;  // window_attention_kernel
 constexpr unsigned kBadPage = 64u;       // no wait: a paged kernel met a table entry outside the pool
+constexpr unsigned kSharedPage = 128u;   // no wait: an append met a page that several sequences own
 
 // The wait-status word of the translation unit that includes this header (internal
 // linkage: one word per source file, each read by that file's wait_giveups()).
