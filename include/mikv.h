@@ -396,7 +396,9 @@ int mikv_channel_quantize(const uint16_t* k, int units, int n, int D, int bits, 
  *   - a sequence number is outside 0 .. max_seqs - 1, or an earlier request of the same call
  *     names the same sequence,
  *   - its own rule below is broken, or
- *   - the free pages do not suffice for it and all valid requests before it.
+ *   - it needs pages, and the free ones do not suffice for it and all requests before it that
+ *     keep the first two rules (served or not; a compaction's positions are checked later, so
+ *     one that is refused for them alone counts too).  A request that needs no page is served.
  * New pages are the free pages of lowest number, in request order.  n is at most 4096 for
  * reserve, fork and compact, 65535 otherwise; n == 0 does nothing.
  */

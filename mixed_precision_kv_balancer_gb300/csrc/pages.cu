@@ -113,8 +113,9 @@ __device__ __forceinline__ bool among(const int32_t* a, int n, int32_t x) {
 
 // One CTA: validates the requests, gives each its pages of `fresh`, and (reserve) carries them
 // out.  A request that is not valid needs nothing and is refused; of the valid ones, in order,
-// those are served whose pages, together with all earlier requests', do not exceed the free
-// ones.  Bound by latency: the references are read kScanInts a thread at a time until enough
+// those are served that need no page, or whose pages, together with all earlier valid requests',
+// do not exceed the free ones.  (A compaction's positions are not looked at here: one that
+// page_check_kernel refuses for them has counted.)  Bound by latency: the references are read kScanInts a thread at a time until enough
 // free pages are found (65,536 pages: four passes).
 template <Op OP>
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const Pool p, const PlanArgs a) {
