@@ -66,4 +66,9 @@ MIKV_HD int32_t split_owner(int64_t total, int32_t workers, int64_t t) {
   return static_cast<int32_t>(((t + 1) * workers - 1) / total);
 }
 
+// Parts of a unit of `tiles` tiles where the `units` of a call are alike: a warp takes a tile at least.
+MIKV_HD int64_t parts_of_unit(int64_t tiles, int64_t units, int64_t warps) {
+  return tiles < warps / units ? tiles : warps / units;
+}
+
 }  // namespace mikv

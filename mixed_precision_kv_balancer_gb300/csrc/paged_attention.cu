@@ -744,19 +744,23 @@ __global__ void __launch_bounds__(WARPS > 1 ? WARPS * 32 : kPaThreads) paged_mer
   }
 }
 
-// CTAs of the split: two per SM, or as many as give every tile a warp where that is fewer.
-int grid_of(const mikv_pages* p, int n, int Hq, int window, int sinks) {
+// Tiles of the longest unit that the table can hold.
+int64_t tiles_of(const mikv_pages* p, int window, int sinks) {
   const int tile = p->type == MIKV_PAGES_INT8 ? Shape<MIKV_PAGES_INT8>::tw : Shape<MIKV_PAGES_FP16>::tw;
-  const int rep = Hq / p->Hkv, groups = (rep + kPaRows - 1) / kPaRows;
   int64_t slots = static_cast<int64_t>(p->max_pages) * p->page_size;
   if (window > 0) slots = std::min(slots, static_cast<int64_t>(window) + sinks);
-  const int64_t tiles = (slots + tile - 1) / tile;
+  return (slots + tile - 1) / tile;
+}
+// CTAs of the split: two per SM, or one a tile where that is fewer (one of its warps then has the
+// tile, so that few tiles lie on as many SMs).
+int grid_of(const mikv_pages* p, int n, int Hq, int window, int sinks) {
+  const int rep = Hq / p->Hkv, groups = (rep + kPaRows - 1) / kPaRows;
   const int64_t most = static_cast<int64_t>(kPaCtasPerSM) * kNumSMs;
-  return static_cast<int>(std::max<int64_t>(1, std::min(most, tiles * n * p->Hkv * groups)));
+  return static_cast<int>(std::max<int64_t>(1, std::min(most, tiles_of(p, window, sinks) * n * p->Hkv * groups)));
 }
 
 template <int TYPE, int NH>
-int launch(const AttendArgs& a, int grid, cudaStream_t st) {
+int launch(const AttendArgs& a, int grid, int64_t tiles, cudaStream_t st) {
   const auto kern = paged_partial_kernel<TYPE, NH>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<TYPE>::smem);
   if (e != cudaSuccess) return check_launch_after(e, "paged_partial_kernel");
@@ -764,9 +768,10 @@ int launch(const AttendArgs& a, int grid, cudaStream_t st) {
   if (int r = check_launch("paged_partial_kernel")) return r;
   // Parts that a unit has where all are of one length, and the warps that join a head: one sequence
   // of 65536 slots and one key head, 1216 parts: 661 us with one warp a head, 68 with four, 22 with
-  // 16; 16 sequences of 2048 and 8 key heads, 9 parts: 30, 27 and 35 us.
+  // 16; 16 sequences of 2048 and 8 key heads, 9 parts: 30, 27 and 35 us; one of 77 and 8 key heads, five
+  // parts, in a graph: 5.8 us with four, 6.5 with 16.
   const int units = a.p.Hkv * a.groups;
-  const int64_t parts = grid * kPaWarps / (static_cast<int64_t>(units) * a.n);
+  const int64_t parts = parts_of_unit(tiles, static_cast<int64_t>(units) * a.n, grid * kPaWarps);
   const int64_t joins = static_cast<int64_t>(units) * a.n * a.heads;   // CTAs of the two wider forms
   const bool many = parts >= 16 && joins <= 2 * kNumSMs, some = !many && parts >= 5 && joins <= 8 * kNumSMs;
   const auto merge = many   ? paged_merge_kernel<TYPE, kMergeWarps, 8>
@@ -819,9 +824,10 @@ extern "C" int mikv_paged_attention(const void* q, const mikv_pages* pages, int 
   a.scale = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
   const cudaStream_t st = as_stream(stream);
   const bool wide = a.heads > 8;
+  const int64_t tiles = tiles_of(pages, window, sinks);
   switch (a.p.type) {
-    case MIKV_PAGES_FP16: return wide ? launch<MIKV_PAGES_FP16, 2>(a, grid, st) : launch<MIKV_PAGES_FP16, 1>(a, grid, st);
-    case MIKV_PAGES_BF16: return wide ? launch<MIKV_PAGES_BF16, 2>(a, grid, st) : launch<MIKV_PAGES_BF16, 1>(a, grid, st);
-    default: return wide ? launch<MIKV_PAGES_INT8, 2>(a, grid, st) : launch<MIKV_PAGES_INT8, 1>(a, grid, st);
+    case MIKV_PAGES_FP16: return wide ? launch<MIKV_PAGES_FP16, 2>(a, grid, tiles, st) : launch<MIKV_PAGES_FP16, 1>(a, grid, tiles, st);
+    case MIKV_PAGES_BF16: return wide ? launch<MIKV_PAGES_BF16, 2>(a, grid, tiles, st) : launch<MIKV_PAGES_BF16, 1>(a, grid, tiles, st);
+    default: return wide ? launch<MIKV_PAGES_INT8, 2>(a, grid, tiles, st) : launch<MIKV_PAGES_INT8, 1>(a, grid, tiles, st);
   }
 }
