@@ -463,8 +463,8 @@ int mikv_page_copy(const mikv_pages* p, const int32_t* src, const int32_t* dst, 
 
 /*
  * Compact: sequence i keeps keep_n[i] of its slots; slot j of key head h in layer l becomes
- * what slot keep_pos[l][i][h][j] was (keep_pos int32 [layers][n][Hkv][max_keep], e.g. the
- * keep_pos that mikv_select writes; any order, a slot may be kept twice).  The kept rows move
+ * what slot keep_pos[l][i][h][j] was (keep_pos int32 [layers][n][Hkv][max_keep], e.g. in each
+ * layer's part the keep_pos that mikv_select writes; any order, a slot may be kept twice).  The kept rows move
  * into new pages and the old ones are given back, so a sequence that shares pages may be
  * compacted; the new pages have to be free before the old ones are.  ok[i] (written): 1, or 0
  * where refused: also keep_n[i] outside 0 .. min(max_keep, length), or a position outside the

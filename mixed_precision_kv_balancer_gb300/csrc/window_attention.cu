@@ -19,8 +19,10 @@
 // weights, and the other way round.  S_t(i + 1) is committed behind O_t(i), so a thread that
 // holds new scores may rescale its accumulator row without another wait.
 //
-// Weights are rounded to the inputs' type once (2^-9 or 2^-12 of each on average); their sum is
-// taken before that, in fp32.  fp16 weights carry a factor 2^kShift, which keeps weights down
+// Weights are rounded to the inputs' type once, which is what the value products take (a second part
+// would be half as many products again, and they bound the kernel); their sum is taken before that, in
+// fp32.  Error against 64 bits of 8192 causal rows in BF16 2.1e-3, with 32-bit weights 1.6e-3; chunks
+// of 500 in FP16 2.9e-4 and 2.1e-4.  fp16 weights carry a factor 2^kShift, which keeps weights down
 // to 2^-27 of the row's largest out of fp16's subnormal range; 2^(kShift + kGrow) stays below
 // its largest number.
 //
