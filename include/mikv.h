@@ -544,6 +544,112 @@ int mikv_window_attention(const mikv_rows* q, const mikv_rows* k, const mikv_row
 size_t mikv_window_attention_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk, int window, int sinks);
 
 /*
+ * Packed batches: the new tokens of many requests, one request after the other, as rows
+ * [rows][H][D] (chunks of prompts beside single tokens).  A row's sequence, position and slot are
+ * worked out once a step (mikv_batch_rows) and serve every layer.
+ *
+ * Request i < n concerns sequence seqs[i] (NULL: i) and has counts[i] rows (below 0: none); its
+ * row t stands at position start[i] + t (start: what mikv_page_reserve wrote; NULL: the rows are the
+ * sequence's last ones).  Written, with row arrays int32 [rows]:
+ *   row_start int32 [n + 1]   rows before request i, at most `rows`; [n]: all of them
+ *   row_seq, row_pos          sequence and position; -1, -1 where the request was refused (start < 0, a
+ *                             sequence number out of range, more rows than slots with start NULL),
+ *                             where an earlier request names its sequence too, and past the last row
+ *   row_slot                  the slot of the pool, page * page_size + position % page_size; -1 also at or
+ *                             past the sequence's length and on a page outside the pool (reported,
+ *                             mikv_wait_status bit 64)
+ * Rows of requests that were refused keep their places: a batch is laid out from its counts alone.
+ * n at most 4096; n_pages * page_size < 2^31; n == 0 with rows == 0 does nothing.
+ * Errors: EINVAL (null), ESHAPE, and the cache's (EALIGN, EUNSUPPORTED), ECUDA.
+ */
+int mikv_batch_rows(const mikv_pages* p, const int32_t* seqs, const int32_t* start, const int32_t* counts, int n, int rows,
+                    int32_t* row_start, int32_t* row_seq, int32_t* row_pos, int32_t* row_slot, void* stream);
+
+/*
+ * Append by slot: row r of k and v ([rows][Hkv][D] by stride_t and stride_h, stride_b unused; fp16,
+ * bf16 for BF16 pages) goes to slot slots[r] of one layer; rows with a slot below 0 are skipped.
+ * Stored, quantised and kept off shared pages as by mikv_paged_append; a slot outside the pool is
+ * skipped and reported (mikv_wait_status, bit 64).  The slots of a call differ (those of
+ * mikv_batch_rows do, for pages of one owner): one that is named twice is left with parts of either row.
+ */
+int mikv_slot_append(const mikv_pages* p, int layer, const mikv_rows* k, const mikv_rows* v, int rows, const int32_t* slots,
+                     void* stream);
+
+/*
+ * Bounds of the keys of pages, for mikv_block_select: per (layer, page, key head) the smallest and
+ * largest value of every channel over the page's filled slots, in 8 bits.
+ *   scale = fl(max_c max(|lo_c|, |hi_c|) / 127),  codes floor(fl(lo_c / scale)), ceil(fl(hi_c / scale)),
+ * held inside -127 .. 127, all 0 where scale is 0.  The keys are the stored values (INT8: fl(fl(s *
+ * code) + z)).  A page that holds a key that is no finite number has scale infinity and codes 0.
+ *   bounds  int8 [layers][n_pages][Hkv][2][D] (lo, hi), 16-byte aligned
+ *   scales  fp32 [layers][n_pages][Hkv]
+ * The pages that hold the positions (row_seq[r], row_pos[r]), as mikv_batch_rows writes them, are
+ * done anew from all that they hold: call it behind each append.  Pages that mikv_page_fork,
+ * _copy or _compact have filled need it too: with rows for all their positions (mikv_batch_rows
+ * with counts = lengths), in every layer.  Rows without a sequence, or at or past its length, are skipped.
+ */
+int mikv_page_bounds(const mikv_pages* p, int layer, const int32_t* row_seq, const int32_t* row_pos, int rows, int8_t* bounds,
+                     float* scales, void* stream);
+
+/*
+ * Blocks to read: for each row and key head, the `keep` blocks (pages of its sequence, in table
+ * order) that score highest among those with a position up to the row's own.  Rows as in
+ * mikv_page_bounds; row_seq NULL: row r is sequence r; row_pos NULL: the sequence's last slot (a position
+ * at or past the length counts as the last slot too).
+ * With c = rint(fl(q_c / s_q)), s_q = fl(max_c |q_c| / 127) of each query head, the score of a block is
+ *   max over the group's heads of fl(fl(u * scale) * s_q),  u = sum_c (c_c > 0 ? c_c hi_c : c_c lo_c),
+ * u exact.  A score that is no number counts as +infinity, so that blocks which hold one are read.
+ * Always among the blocks: the first `first` and the last `recent` ones (recent >= 1, first + recent <= keep);
+ * equal scores go to the lower block.  A row with `keep` blocks or fewer reads them all.
+ *   sel int32 [rows][Hkv][keep]: the blocks in ascending order, -1 behind them;  n_sel int32 [rows][Hkv]
+ * q [rows][Hq][D] fp16 (bf16 for BF16 pages).  rows * Hkv <= 65535, Hq a multiple of Hkv, up to 1024 query heads
+ * per key head.  ws >= mikv_block_select_workspace_bytes(p, rows), 16-byte aligned; two calls must
+ * not share a workspace concurrently.
+ * Errors: EINVAL (null, keep, first, recent), ESHAPE, EALIGN, EUNSUPPORTED, ECUDA.
+ */
+int mikv_block_select(const void* q, const mikv_pages* p, int layer, const int8_t* bounds, const float* scales,
+                      const int32_t* row_seq, const int32_t* row_pos, int rows, int Hq, int keep, int first, int recent,
+                      int32_t* sel, int32_t* n_sel, void* ws, size_t ws_bytes, void* stream);
+size_t mikv_block_select_workspace_bytes(const mikv_pages* p, int rows);
+
+/*
+ * Attention of each row over the blocks that sel and n_sel name (as mikv_block_select writes them, or
+ * in any order; entries past n_sel, which is held inside 0 .. keep, are not read), as far as their
+ * slots lie at or before the row's position.  A block named twice counts twice; one that is none of
+ * the row's is not seen and reported (mikv_wait_status, bit 64).  Otherwise as mikv_paged_attention:
+ * out [rows][Hq][D], lse fp32 [rows][Hq] or NULL, over the seen slots alone.
+ * ws >= mikv_block_attention_workspace_bytes(p, rows, Hq, keep), 16-byte aligned; two calls must not
+ * share a workspace concurrently.
+ */
+int mikv_block_attention(const void* q, const mikv_pages* p, int layer, const int32_t* row_seq, const int32_t* row_pos,
+                         const int32_t* sel, const int32_t* n_sel, int rows, int Hq, int keep, void* out, float* lse, void* ws,
+                         size_t ws_bytes, void* stream);
+size_t mikv_block_attention_workspace_bytes(const mikv_pages* p, int rows, int Hq, int keep);
+
+/*
+ * Attention of the rows of a packed batch over one layer of the paged cache.  Rows row_start[i] ..
+ * row_start[i + 1] - 1 (held inside 0 .. rows; int32 [n + 1], ascending, as mikv_batch_rows writes
+ * it) are request i's, of sequence seqs[i] (NULL: i); row t of a request stands at position start[i] + t
+ * (NULL: the rows are the sequence's last ones) and sees slot j of its sequence (j below the
+ * length) as in mikv_paged_attention.  Append the rows' keys and values first.
+ * q, out [rows][Hq][D] by stride_t and stride_h (stride_b unused), fp16 (bf16 for BF16 pages); lse fp32
+ * [rows][Hq], or NULL.  A row that sees nothing (its request was refused, its sequence is empty or out of
+ * range, its position is below 0) gives out 0 and lse -inf.  Rows of no request are not written.
+ * Several requests may name one sequence.  Slots that are not seen by any row of a request may
+ * hold anything; a value row that one of them sees must be finite, or it may reach the request's
+ * other rows.  The softmax weights, and INT8 pages' keys and values, are rounded once to 16 bits
+ * before the products; sums and statistics are fp32.
+ * n at most 4096, Hq a multiple of Hkv, up to 1024 query heads per key head; n == 0 or rows == 0 does nothing.
+ * ws >= mikv_chunk_attention_workspace_bytes(p, n, rows, Hq), 32-byte aligned; two calls must not share
+ * a workspace concurrently.
+ * Errors: EINVAL (null, window, sinks, rows of out that overlap), ESHAPE, EALIGN, EUNSUPPORTED, ECUDA.
+ */
+int mikv_chunk_attention(const mikv_rows* q, const mikv_pages* p, int layer, const int32_t* seqs, const int32_t* start,
+                         const int32_t* row_start, int n, int rows, int Hq, int window, int sinks, const mikv_rows* out, float* lse,
+                         void* ws, size_t ws_bytes, void* stream);
+size_t mikv_chunk_attention_workspace_bytes(const mikv_pages* p, int n, int rows, int Hq);
+
+/*
  * Measurement hook (no counterpart in the papers): while set, every
  * mikv_decode_attention and mikv_decode_step call made by this thread records
  * `begin` (a cudaEvent_t) on its stream just before the split-K attention
@@ -571,8 +677,8 @@ int mikv_set_attention_events(void* begin, void* end);
  * mikv_wait_status stores the OR of the bits set since the last clear in *bits:
  *   1 = K3 pass 1 (row log-sum-exp), 2 = K3 pass 2 (column sums), 4 = K6 (V.W_O norms),
  *   8 = K9 (output perturbation), 16 = mikv_wait_probe, 32 = mikv_window_attention,
- *   64 = no wait: an append, a gather or an attention over pages met a table entry outside the
- *   pool (its slots are skipped, read as zeros, or not seen)
+ *   64 = no wait: an append, a gather, row maps, bounds, a choice of blocks or an attention over pages
+ *   met a table entry, slot or block outside the pool (skipped, read as zeros, or not seen)
  *   128 = no wait: an append met a page that several sequences own (its slots are skipped)
  * and clears them if `clear` is non-zero.  It copies synchronously: call it after the work
  * in question has completed (e.g. after synchronising its stream).

@@ -34,6 +34,9 @@ EXPORTS = (
     "mikv_page_workspace_bytes", "mikv_paged_append", "mikv_paged_gather",
     "mikv_paged_attention", "mikv_paged_attention_workspace_bytes",
     "mikv_window_attention", "mikv_window_attention_workspace_bytes",
+    "mikv_batch_rows", "mikv_slot_append", "mikv_page_bounds", "mikv_block_select", "mikv_block_select_workspace_bytes",
+    "mikv_block_attention", "mikv_block_attention_workspace_bytes", "mikv_chunk_attention",
+    "mikv_chunk_attention_workspace_bytes",
     "mikv_set_attention_events", "mikv_wait_status", "mikv_wait_probe", "mikv_last_error",
 )
 
@@ -119,6 +122,15 @@ def load() -> ctypes.CDLL:
         "mikv_paged_attention_workspace_bytes": (S, [GP, I, I, I, I]),
         "mikv_window_attention": (I, [RP, RP, RP, I, I, I, I, I, I, I, P, P, I, I, RP, P, P, S, P]),
         "mikv_window_attention_workspace_bytes": (S, [I, I, I, I, I, I, I]),
+        "mikv_batch_rows": (I, [GP, P, P, P, I, I, P, P, P, P, P]),
+        "mikv_slot_append": (I, [GP, I, RP, RP, I, P, P]),
+        "mikv_page_bounds": (I, [GP, I, P, P, I, P, P, P]),
+        "mikv_block_select": (I, [P, GP, I, P, P, P, P, I, I, I, I, I, P, P, P, S, P]),
+        "mikv_block_select_workspace_bytes": (S, [GP, I]),
+        "mikv_block_attention": (I, [P, GP, I, P, P, P, P, I, I, I, P, P, P, S, P]),
+        "mikv_block_attention_workspace_bytes": (S, [GP, I, I, I]),
+        "mikv_chunk_attention": (I, [RP, GP, I, P, P, P, I, I, I, I, I, RP, P, P, S, P]),
+        "mikv_chunk_attention_workspace_bytes": (S, [GP, I, I, I]),
         "mikv_set_attention_events": (I, [P, P]),
         "mikv_wait_status": (I, [ctypes.POINTER(ctypes.c_uint), I]),
         "mikv_wait_probe": (I, [ctypes.c_int64, I, P]),
@@ -423,6 +435,91 @@ def mikv_window_attention(q, k, v, window, sinks, out, lse=None, q_lens=None, k_
             _need(lse, "lse", torch.float32, (B, Hq, Tq), dev), w, nb)
 
 
+# --- packed batches over the paged cache -------------------------------------------------
+
+def _packed(t, name, dtype, shape, dev):
+    """mikv_rows of a [rows][H][D] tensor whose last dimension is contiguous."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        st, sh, sd = t.stride()
+        if sd == 1 or shape[2] <= 1:
+            return mikv_rows(t.data_ptr(), 0, sh if shape[1] > 1 else 0, st if shape[0] > 1 else 0)
+    raise ValueError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)} on cuda:{dev} with a contiguous "
+                     f"last dimension, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+
+
+def mikv_batch_rows(pages, counts, row_start, row_seq, row_pos, row_slot, seqs=None, start=None, stream=None):
+    """Rows of requests with counts int32 [n] rows each: row_start int32 [n + 1]; row_seq, row_pos, row_slot
+    int32 [rows] receive each row's sequence, position and slot (-1: none)."""
+    lib, dev, n, rows = load(), pages.index, counts.shape[0], row_seq.shape[0]
+    i32 = torch.int32
+    _launch(dev, stream, lib.mikv_batch_rows, pages.ref, _need(seqs, "seqs", i32, (n,), dev), _need(start, "start", i32, (n,), dev),
+            _need(counts, "counts", i32, (n,), dev), n, rows, _need(row_start, "row_start", i32, (n + 1,), dev),
+            _need(row_seq, "row_seq", i32, (rows,), dev), _need(row_pos, "row_pos", i32, (rows,), dev),
+            _need(row_slot, "row_slot", i32, (rows,), dev))
+
+
+def mikv_slot_append(pages, layer, k, v, slots, stream=None):
+    """Rows k, v [rows][Hkv][D] (strided; fp16, bf16 for BF16 pages) into the slots int32 [rows] of one layer."""
+    lib, dev, s, rows = load(), pages.index, pages.struct, k.shape[0]
+    shape, dt = (rows, s.Hkv, s.D), _PAGE_DTYPE[s.type]
+    _launch(dev, stream, lib.mikv_slot_append, pages.ref, layer, _packed(k, "k", dt, shape, dev), _packed(v, "v", dt, shape, dev),
+            rows, _need(slots, "slots", torch.int32, (rows,), dev))
+
+
+def _bounds_of(s, bounds, scales, dev):
+    return (_need(bounds, "bounds", torch.int8, (s.layers, s.n_pages, s.Hkv, 2, s.D), dev),
+            _need(scales, "scales", torch.float32, (s.layers, s.n_pages, s.Hkv), dev))
+
+
+def mikv_page_bounds(pages, layer, row_seq, row_pos, bounds, scales, stream=None):
+    """Bounds int8 [layers][n_pages][Hkv][2][D] and scales fp32 [layers][n_pages][Hkv] of the keys of the pages
+    that hold the rows (row_seq, row_pos) int32 [rows], in one layer."""
+    lib, dev, rows = load(), pages.index, row_seq.shape[0]
+    _launch(dev, stream, lib.mikv_page_bounds, pages.ref, layer, _need(row_seq, "row_seq", torch.int32, (rows,), dev),
+            _need(row_pos, "row_pos", torch.int32, (rows,), dev), rows, *_bounds_of(pages.struct, bounds, scales, dev))
+
+
+def mikv_block_select(q, pages, layer, bounds, scales, first, recent, sel, n_sel, row_seq=None, row_pos=None, ws=None, stream=None):
+    """The blocks that rows q [rows][Hq][D] read: sel int32 [rows][Hkv][keep], n_sel int32 [rows][Hkv]."""
+    lib, dev, s = load(), pages.index, pages.struct
+    rows, Hq, _ = q.shape
+    keep = sel.shape[-1]
+    w, nb, _keep = _ws_given(ws, dev) if ws is not None else _ws_new(
+        lib.mikv_block_select_workspace_bytes(pages.ref, rows), dev, stream)
+    _launch(dev, stream, lib.mikv_block_select, _need(q, "q", _PAGE_DTYPE[s.type], (rows, Hq, s.D), dev), pages.ref, layer,
+            *_bounds_of(s, bounds, scales, dev), _need(row_seq, "row_seq", torch.int32, (rows,), dev),
+            _need(row_pos, "row_pos", torch.int32, (rows,), dev), rows, Hq, keep, first, recent,
+            _need(sel, "sel", torch.int32, (rows, s.Hkv, keep), dev), _need(n_sel, "n_sel", torch.int32, (rows, s.Hkv), dev), w, nb)
+
+
+def mikv_block_attention(q, pages, layer, sel, n_sel, out, lse=None, row_seq=None, row_pos=None, ws=None, stream=None):
+    """Rows q, out [rows][Hq][D] over the blocks sel int32 [rows][Hkv][keep], n_sel int32 [rows][Hkv]; lse fp32 [rows][Hq]."""
+    lib, dev, s = load(), pages.index, pages.struct
+    rows, Hq, _ = q.shape
+    keep = sel.shape[-1]
+    shape, dt = (rows, Hq, s.D), _PAGE_DTYPE[s.type]
+    w, nb, _keep = _ws_given(ws, dev) if ws is not None else _ws_new(
+        lib.mikv_block_attention_workspace_bytes(pages.ref, rows, Hq, keep), dev, stream)
+    _launch(dev, stream, lib.mikv_block_attention, _need(q, "q", dt, shape, dev), pages.ref, layer,
+            _need(row_seq, "row_seq", torch.int32, (rows,), dev), _need(row_pos, "row_pos", torch.int32, (rows,), dev),
+            _need(sel, "sel", torch.int32, (rows, s.Hkv, keep), dev), _need(n_sel, "n_sel", torch.int32, (rows, s.Hkv), dev),
+            rows, Hq, keep, _need(out, "out", dt, shape, dev), _need(lse, "lse", torch.float32, (rows, Hq), dev), w, nb)
+
+
+def mikv_chunk_attention(q, pages, layer, row_start, window, sinks, out, lse=None, seqs=None, start=None, ws=None, stream=None):
+    """Packed rows q, out [rows][Hq][D] (strided) of n requests, request i's from row_start[i] (int32 [n + 1]) on, at
+    positions start[i] + t (int32 [n]; None: its sequence's last ones); lse fp32 [rows][Hq]."""
+    lib, dev, s = load(), pages.index, pages.struct
+    rows, Hq, _ = q.shape
+    n = row_start.shape[0] - 1
+    shape, dt, i32 = (rows, Hq, s.D), _PAGE_DTYPE[s.type], torch.int32
+    w, nb, _keep = _ws_given(ws, dev) if ws is not None else _ws_new(
+        lib.mikv_chunk_attention_workspace_bytes(pages.ref, n, rows, Hq), dev, stream)
+    _launch(dev, stream, lib.mikv_chunk_attention, _packed(q, "q", dt, shape, dev), pages.ref, layer,
+            _need(seqs, "seqs", i32, (n,), dev), _need(start, "start", i32, (n,), dev), _need(row_start, "row_start", i32, (n + 1,), dev),
+            n, rows, Hq, window, sinks, _packed(out, "out", dt, shape, dev), _need(lse, "lse", torch.float32, (rows, Hq), dev), w, nb)
+
+
 def mikv_set_attention_events(begin=None, end=None):
     """Record two torch.cuda.Event objects around the split-K attention launch of every
     following decode call of this thread (None, None clears).  Each event must have been
@@ -434,7 +531,7 @@ def mikv_set_attention_events(begin=None, end=None):
 
 WAIT_BITS = {1: "K3 pass 1 (row log-sum-exp)", 2: "K3 pass 2 (column sums)", 4: "K6 (V.W_O norms)",
              8: "K9 (output perturbation)", 16: "mikv_wait_probe", 32: "mikv_window_attention",
-             64: "a page outside the pool", 128: "an append into a shared page"}
+             64: "a page, slot or block outside the pool", 128: "an append into a shared page"}
 
 
 def mikv_wait_status(clear=True) -> int:

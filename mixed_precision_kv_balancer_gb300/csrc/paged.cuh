@@ -34,6 +34,10 @@ int check_rows(const mikv_rows* r, const char* what, const char* name);
 int paged_attention_status(unsigned* out, bool clear);
 int paged_rows_status(unsigned* out, bool clear);
 int window_attention_status(unsigned* out, bool clear);
+int batch_rows_status(unsigned* out, bool clear);
+int page_bounds_status(unsigned* out, bool clear);
+int block_select_status(unsigned* out, bool clear);
+int chunk_attention_status(unsigned* out, bool clear);
 
 // A strided view with its data typed as bytes; strides in bytes.
 struct RowView {

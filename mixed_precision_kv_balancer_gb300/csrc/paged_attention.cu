@@ -68,6 +68,9 @@ struct AttendArgs {
   float* lse;
   float* part;    // [2 * warps of the grid][kPartFloats]
   float scale;    // log2(e) / sqrt(D)
+  // picked blocks: n = packed rows * key heads, and a "row" below is one of these; sel [n][keep], n_sel [n]
+  const int32_t *row_seq, *row_pos, *sel, *n_sel;
+  int keep;
 };
 constexpr int kPartFloats = kPaRows * kD + 2 * kPaRows;  // O, then m, then l
 
@@ -110,16 +113,26 @@ __device__ __forceinline__ uint16_t to_out(float x) {
   return __half_as_ushort(__float2half_rn(x));
 }
 
-// Visible slots of row b's sequence; none for a sequence number out of range.
+// Visible slots of row b's sequence; none for a sequence number out of range.  Picked blocks (SEL): all
+// slots of the row's blocks are numbered, of which those up to `skip`, the last position, are seen.
+template <bool SEL>
 __device__ __forceinline__ Visible row_visible(const AttendArgs& a, int b, int32_t& seq) {
+  if (SEL) {
+    const int r = b / a.p.Hkv;
+    seq = a.row_seq ? a.row_seq[r] : r;
+    if (static_cast<uint32_t>(seq) >= static_cast<uint32_t>(a.p.max_seqs)) return {0, 0, 0};
+    const int32_t last = a.p.len_of(seq) - 1, at = a.row_pos ? min(a.row_pos[r], last) : last;
+    if (at < 0) return {0, 0, 0};
+    return {min(max(a.n_sel[b], 0), a.keep) * static_cast<int32_t>(a.p.ps.d), 0, at};
+  }
   seq = a.seqs ? a.seqs[b] : b;
   if (static_cast<uint32_t>(seq) >= static_cast<uint32_t>(a.p.max_seqs)) return {0, 0, 0};
   return visible_slots(a.p.len_of(seq), a.window, a.sinks);
 }
-template <int TILE>
+template <int TILE, bool SEL>
 __device__ __forceinline__ int row_tiles(const AttendArgs& a, int b) {
   int32_t s;
-  return (row_visible(a, b, s).count + TILE - 1) / TILE;
+  return (row_visible<SEL>(a, b, s).count + TILE - 1) / TILE;
 }
 
 // Sums over the block's threads below this one (inclusive) and over all of them.
@@ -172,6 +185,20 @@ __device__ __forceinline__ uint32_t slot_row(const Pool& p, const int32_t* row, 
   if (i >= vis.count) return kNoRow;
   const uint32_t slot = visible_slot(vis, static_cast<int32_t>(i)), pg = div_of(slot, p.ps);
   const uint32_t r = pool_row(__ldg(row + pg), p.n_pages, p.Hkv, h, p.ps.d, slot - pg * p.ps.d);
+  if (r == kNoRow) tc::report_giveup(tc::kBadPage);
+  return r;
+}
+
+// The same of numbered slot `i` of picked blocks; a block that is none of the row's counts as a bad page.
+__device__ __forceinline__ uint32_t picked_row(const Pool& p, const int32_t* row, const Visible& vis, const int32_t* sel, int h, int64_t i) {
+  if (i >= vis.count) return kNoRow;
+  const uint32_t e = div_of(static_cast<uint32_t>(i), p.ps), in = static_cast<uint32_t>(i) - e * p.ps.d;
+  const int32_t block = __ldg(sel + e);
+  uint32_t r = kNoRow;
+  if (static_cast<uint32_t>(block) <= div_of(static_cast<uint32_t>(vis.skip), p.ps)) {
+    if (static_cast<int32_t>(block * p.ps.d + in) > vis.skip) return kNoRow;   // behind the row's position
+    r = pool_row(__ldg(row + block), p.n_pages, p.Hkv, h, p.ps.d, in);
+  }
   if (r == kNoRow) tc::report_giveup(tc::kBadPage);
   return r;
 }
@@ -426,38 +453,51 @@ __device__ __forceinline__ float column_sum(float x) {
   return x;
 }
 
+// Units of a row: one per key head and group of its query heads; picked blocks: a row has one key head.
+template <bool SEL>
+__device__ __forceinline__ int units_of(const AttendArgs& a) {
+  return SEL ? a.groups : a.p.Hkv * a.groups;
+}
+// The first query head of unit u of row b, counted through all rows of q, and the heads of the unit.
+template <bool SEL>
+__device__ __forceinline__ size_t head_of(const AttendArgs& a, int b, int u) {
+  if (SEL) return static_cast<size_t>(b) * a.rep + u * a.heads;   // row b / Hkv, key head b % Hkv
+  return static_cast<size_t>(b) * a.Hq + u / a.groups * a.rep + u % a.groups * a.heads;
+}
+__device__ __forceinline__ int heads_of(const AttendArgs& a, int u) { return min(a.heads, a.rep - u % a.groups * a.heads); }
+
 // A warp's place in the line of tiles: tile t of `tiles` of unit u of row b.
 struct Cursor {
   int b, u, t, tiles;
   int32_t seq;
   Visible vis;
 };
-template <int TYPE>
+template <int TYPE, bool SEL>
 __device__ __forceinline__ void open_row(const AttendArgs& a, Cursor& c) {   // the first row from c.b on that has tiles
   for (;; ++c.b) {
-    c.vis = row_visible(a, c.b, c.seq);
+    c.vis = row_visible<SEL>(a, c.b, c.seq);
     c.tiles = (c.vis.count + Shape<TYPE>::tw - 1) / Shape<TYPE>::tw;
     if (c.tiles > 0) return;
   }
 }
 // To the next unit; the caller knows that there is one.
-template <int TYPE>
+template <int TYPE, bool SEL>
 __device__ __forceinline__ void next_unit(const AttendArgs& a, Cursor& c) {
   c.t = 0;
-  if (++c.u == a.p.Hkv * a.groups) {
+  if (++c.u == units_of<SEL>(a)) {
     c.u = 0;
     ++c.b;
-    open_row<TYPE>(a, c);
+    open_row<TYPE, SEL>(a, c);
   }
 }
 
 // Writes a finished unit, or a part of one for the join (`part` not null).
-template <int TYPE, int NH>
+template <int TYPE, int NH, bool SEL>
 __device__ __forceinline__ void store_unit(const AttendArgs& a, int b, int u, Acc<NH>& acc, float* part) {
   using S = Shape<TYPE>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int head0 = u / a.groups * a.rep + u % a.groups * a.heads, rows = min(a.heads, a.rep - u % a.groups * a.heads);
-  const size_t at = static_cast<size_t>(b) * a.Hq + head0;
+  const int rows = heads_of(a, u);
+  const size_t at = head_of<SEL>(a, b, u);
 #pragma unroll
   for (int nh = 0; nh < NH; ++nh) {
     float l[2], inv[2];
@@ -523,7 +563,7 @@ __device__ __forceinline__ void store_unit(const AttendArgs& a, int b, int u, Ac
   }
 }
 
-template <int TYPE, int NH>
+template <int TYPE, int NH, bool SEL>
 __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSM) paged_partial_kernel(const AttendArgs a) {
   using S = Shape<TYPE>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -532,12 +572,12 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSM) paged_partial_kernel
   pdl_trigger();
   const Pool& p = a.p;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int units = p.Hkv * a.groups;
+  const int units = units_of<SEL>(a);
   // this warp's part of the line of tiles, and the row it begins in; consecutive parts lie on
   // different SMs, so that a few of them do not share one
-  int64_t mine = tid < a.n ? row_tiles<S::tw>(a, tid) : 0, total;
+  int64_t mine = tid < a.n ? row_tiles<S::tw, SEL>(a, tid) : 0, total;
   const int64_t head = mine;
-  for (int b = tid + kPaThreads; b < a.n; b += kPaThreads) mine += row_tiles<S::tw>(a, b);
+  for (int b = tid + kPaThreads; b < a.n; b += kPaThreads) mine += row_tiles<S::tw, SEL>(a, b);
   int64_t incl = scan64(mine * units, warp_sums, total);
   if (total == 0) return;   // nothing is seen: the join answers
   const int workers = workers_of(total, gridDim.x * kPaWarps), c = w * gridDim.x + blockIdx.x;
@@ -550,7 +590,7 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSM) paged_partial_kernel
     int64_t sum = total;
     if (a.n > kPaThreads) {
       const int b = b0 + tid;
-      const int64_t v = b0 == 0 ? head : b < a.n ? row_tiles<S::tw>(a, b) : 0;
+      const int64_t v = b0 == 0 ? head : b < a.n ? row_tiles<S::tw, SEL>(a, b) : 0;
       incl = pass + scan64(v * units, warp_sums, sum);
     }
     __syncthreads();   // the last pass's sums have been read
@@ -568,7 +608,7 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSM) paged_partial_kernel
   }
   if (idle) return;
   const int n = static_cast<int>(end - begin);   // tiles of this warp: below 2^31 / tw a row, far fewer a warp
-  open_row<TYPE>(a, at);
+  open_row<TYPE, SEL>(a, at);
   at.u = static_cast<int>((begin - base) / at.tiles);
   at.t = static_cast<int>((begin - base) % at.tiles);
 
@@ -581,10 +621,12 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSM) paged_partial_kernel
   const auto find = [&] {
     uint32_t r = kNoRow;
     if (asked < n) {
+      const int32_t* table = p.table + static_cast<size_t>(ahead.seq) * p.max_pages;
+      const int64_t i = static_cast<int64_t>(ahead.t) * S::tw + lane;
       if (lane < S::tw)
-        r = slot_row(p, p.table + static_cast<size_t>(ahead.seq) * p.max_pages, ahead.vis, ahead.u / a.groups,
-                     static_cast<int64_t>(ahead.t) * S::tw + lane);
-      if (++ahead.t == ahead.tiles && asked + 1 < n) next_unit<TYPE>(a, ahead);
+        r = SEL ? picked_row(p, table, ahead.vis, a.sel + static_cast<size_t>(ahead.b) * a.keep, ahead.b % p.Hkv, i)
+                : slot_row(p, table, ahead.vis, ahead.u / a.groups, i);
+      if (++ahead.t == ahead.tiles && asked + 1 < n) next_unit<TYPE, SEL>(a, ahead);
       ++asked;
     }
     return r;
@@ -599,8 +641,8 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSM) paged_partial_kernel
   int rd = 0, wr = S::stages - 1, left = n;
   bool first = true;
   while (left > 0) {
-    const int head0 = at.u / a.groups * a.rep + at.u % a.groups * a.heads;
-    const int rows = min(a.heads, a.rep - at.u % a.groups * a.heads);
+    const size_t head0 = head_of<SEL>(a, at.b, at.u);
+    const int rows = heads_of(a, at.u);
     // the queries as B fragments (INT8: channels in the order the codes are read)
     uint32_t qf[kD / 16][NH][2];
     float qsum[NH][2][2] = {};
@@ -614,7 +656,7 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSM) paged_partial_kernel
           const int ch = S::q8 ? 64 * (ks >> 2) + 16 * t + 4 * (ks & 3) + 2 * j : 16 * ks + 8 * j + 2 * t;
           uint32_t x = 0;
           if (nh * 8 + g < rows)
-            x = *reinterpret_cast<const uint32_t*>(a.q + (static_cast<size_t>(at.b) * a.Hq + head0 + nh * 8 + g) * kD + ch);
+            x = *reinterpret_cast<const uint32_t*>(a.q + (head0 + nh * 8 + g) * kD + ch);
           qf[ks][nh][j] = x;
           if (S::q8) {
             const __half2 x2 = *reinterpret_cast<const __half2*>(&x);
@@ -658,10 +700,10 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSM) paged_partial_kernel
       wr = wr + 1 == S::stages ? 0 : wr + 1;
     }
     const bool whole = count == at.tiles;
-    store_unit<TYPE, NH>(a, at.b, at.u, acc, whole ? nullptr : a.part + (static_cast<size_t>(c) * 2 + (first ? 0 : 1)) * kPartFloats);
+    store_unit<TYPE, NH, SEL>(a, at.b, at.u, acc, whole ? nullptr : a.part + (static_cast<size_t>(c) * 2 + (first ? 0 : 1)) * kPartFloats);
     first = false;
     left -= count;
-    if (left > 0) next_unit<TYPE>(a, at);
+    if (left > 0) next_unit<TYPE, SEL>(a, at);
   }
 }
 
@@ -681,24 +723,24 @@ struct Part {
 // CTA (unit, row b, query head, or four heads where WARPS is 1): joins the parts of a unit that several
 // warps held, in a fixed order, and answers for the units without a visible slot.  Four channels
 // a lane; WARPS warps share a head, each with every WARPS-th part, BATCH of them requested together.
-template <int TYPE, int WARPS, int BATCH>
+template <int TYPE, int WARPS, int BATCH, bool SEL>
 __global__ void __launch_bounds__(WARPS > 1 ? WARPS * 32 : kPaThreads) paged_merge_kernel(const AttendArgs a, int warps) {
   using S = Shape<TYPE>;
   constexpr int W = WARPS > 1 ? WARPS : kPaWarps;   // warps of the CTA
   __shared__ int64_t warp_sums[W];
   __shared__ float4 s_o[W][32];
   __shared__ float2 s_ml[W];
-  const int units = a.p.Hkv * a.groups, b = blockIdx.y, u = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rows = min(a.heads, a.rep - u % a.groups * a.heads);
+  const int units = units_of<SEL>(a), b = blockIdx.y, u = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rows = heads_of(a, u);
   int64_t mine = 0, below = 0, total, base;
   for (int i = tid; i < a.n; i += W * 32) {
-    const int x = row_tiles<S::tw>(a, i);
+    const int x = row_tiles<S::tw, SEL>(a, i);
     mine += x;
     if (i < b) below += x;
   }
   scan64<W>(mine * units, warp_sums, total);
   scan64<W>(below * units, warp_sums, base);
-  const int tiles = row_tiles<S::tw>(a, b);
+  const int tiles = row_tiles<S::tw, SEL>(a, b);
   const int workers = workers_of(total, warps);
   const int64_t first = base + static_cast<int64_t>(u) * tiles;
   const int c0 = tiles ? split_owner(total, workers, first) : 0, c1 = tiles ? split_owner(total, workers, first + tiles - 1) : -1;
@@ -735,7 +777,7 @@ __global__ void __launch_bounds__(WARPS > 1 ? WARPS * 32 : kPaThreads) paged_mer
 #pragma unroll
       for (int e = 1; e < WARPS; ++e) sum.add(s_ml[e].x, s_ml[e].y, s_o[e][lane]);
     }
-    const size_t at = static_cast<size_t>(b) * a.Hq + u / a.groups * a.rep + u % a.groups * a.heads + row;
+    const size_t at = head_of<SEL>(a, b, u) + row;
     const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
     *reinterpret_cast<uint2*>(a.out + at * kD + 4 * lane) =
         make_uint2(static_cast<uint32_t>(to_out<TYPE>(sum.o.x * inv)) | static_cast<uint32_t>(to_out<TYPE>(sum.o.y * inv)) << 16,
@@ -744,24 +786,31 @@ __global__ void __launch_bounds__(WARPS > 1 ? WARPS * 32 : kPaThreads) paged_mer
   }
 }
 
-// Tiles of the longest unit that the table can hold.
-int64_t tiles_of(const mikv_pages* p, int window, int sinks) {
+// Tiles of the longest unit that the table can hold, and of one that has all its `keep` blocks.
+int64_t tiles_in(const mikv_pages* p, int64_t slots) {
   const int tile = p->type == MIKV_PAGES_INT8 ? Shape<MIKV_PAGES_INT8>::tw : Shape<MIKV_PAGES_FP16>::tw;
+  return (slots + tile - 1) / tile;
+}
+int64_t tiles_of(const mikv_pages* p, int window, int sinks) {
   int64_t slots = static_cast<int64_t>(p->max_pages) * p->page_size;
   if (window > 0) slots = std::min(slots, static_cast<int64_t>(window) + sinks);
-  return (slots + tile - 1) / tile;
+  return tiles_in(p, slots);
+}
+int64_t picked_tiles(const mikv_pages* p, int keep) {
+  return tiles_in(p, static_cast<int64_t>(std::min(keep, p->max_pages)) * p->page_size);
 }
 // CTAs of the split: two per SM, or one a tile where that is fewer (one of its warps then has the
 // tile, so that few tiles lie on as many SMs).
-int grid_of(const mikv_pages* p, int n, int Hq, int window, int sinks) {
+int grid_of(const mikv_pages* p, int n, int Hq, int64_t tiles) {
   const int rep = Hq / p->Hkv, groups = (rep + kPaRows - 1) / kPaRows;
   const int64_t most = static_cast<int64_t>(kPaCtasPerSM) * kNumSMs;
-  return static_cast<int>(std::max<int64_t>(1, std::min(most, tiles_of(p, window, sinks) * n * p->Hkv * groups)));
+  return static_cast<int>(std::max<int64_t>(1, std::min(most, tiles * n * p->Hkv * groups)));
 }
+size_t part_bytes(int grid) { return static_cast<size_t>(grid) * kPaWarps * 2 * kPartFloats * sizeof(float); }
 
-template <int TYPE, int NH>
+template <int TYPE, int NH, bool SEL>
 int launch(const AttendArgs& a, int grid, int64_t tiles, cudaStream_t st) {
-  const auto kern = paged_partial_kernel<TYPE, NH>;
+  const auto kern = paged_partial_kernel<TYPE, NH, SEL>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<TYPE>::smem);
   if (e != cudaSuccess) return check_launch_after(e, "paged_partial_kernel");
   kern<<<grid, kPaThreads, Shape<TYPE>::smem, st>>>(a);
@@ -770,16 +819,43 @@ int launch(const AttendArgs& a, int grid, int64_t tiles, cudaStream_t st) {
   // of 65536 slots and one key head, 1216 parts: 661 us with one warp a head, 68 with four, 22 with
   // 16; 16 sequences of 2048 and 8 key heads, 9 parts: 30, 27 and 35 us; one of 77 and 8 key heads, five
   // parts, in a graph: 5.8 us with four, 6.5 with 16.
-  const int units = a.p.Hkv * a.groups;
+  const int units = SEL ? a.groups : a.p.Hkv * a.groups;
   const int64_t parts = parts_of_unit(tiles, static_cast<int64_t>(units) * a.n, grid * kPaWarps);
   const int64_t joins = static_cast<int64_t>(units) * a.n * a.heads;   // CTAs of the two wider forms
   const bool many = parts >= 16 && joins <= 2 * kNumSMs, some = !many && parts >= 5 && joins <= 8 * kNumSMs;
-  const auto merge = many   ? paged_merge_kernel<TYPE, kMergeWarps, 8>
-                     : some ? paged_merge_kernel<TYPE, kPaWarps, 8>
-                            : paged_merge_kernel<TYPE, 1, 4>;
+  const auto merge = many   ? paged_merge_kernel<TYPE, kMergeWarps, 8, SEL>
+                     : some ? paged_merge_kernel<TYPE, kPaWarps, 8, SEL>
+                            : paged_merge_kernel<TYPE, 1, 4, SEL>;
   return check_launch_after(launch_after(merge, dim3(units, a.n, many || some ? a.heads : (a.heads + kPaWarps - 1) / kPaWarps),
                                          dim3(many ? kMergeWarps * 32 : kPaThreads), 0, st, a, grid * kPaWarps),
                             "paged_merge_kernel");
+}
+
+// What both calls set; the rest is none.
+void fill_args(AttendArgs& a, const void* q, int layer, int n, int Hq, void* out, float* lse, void* ws) {
+  a.q = static_cast<const uint16_t*>(q);
+  a.layer = layer;
+  a.n = n;
+  a.Hq = Hq;
+  a.rep = Hq / a.p.Hkv;
+  a.groups = (a.rep + kPaRows - 1) / kPaRows;
+  a.heads = (a.rep + a.groups - 1) / a.groups;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.part = static_cast<float*>(ws);
+  a.scale = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
+  a.seqs = a.row_seq = a.row_pos = a.sel = a.n_sel = nullptr;
+  a.window = a.sinks = a.keep = 0;
+}
+
+template <bool SEL>
+int dispatch(const AttendArgs& a, int grid, int64_t tiles, cudaStream_t st) {
+  const bool wide = a.heads > 8;
+  switch (a.p.type) {
+    case MIKV_PAGES_FP16: return wide ? launch<MIKV_PAGES_FP16, 2, SEL>(a, grid, tiles, st) : launch<MIKV_PAGES_FP16, 1, SEL>(a, grid, tiles, st);
+    case MIKV_PAGES_BF16: return wide ? launch<MIKV_PAGES_BF16, 2, SEL>(a, grid, tiles, st) : launch<MIKV_PAGES_BF16, 1, SEL>(a, grid, tiles, st);
+    default: return wide ? launch<MIKV_PAGES_INT8, 2, SEL>(a, grid, tiles, st) : launch<MIKV_PAGES_INT8, 1, SEL>(a, grid, tiles, st);
+  }
 }
 
 }  // namespace
@@ -790,7 +866,7 @@ using namespace mikv;
 extern "C" size_t mikv_paged_attention_workspace_bytes(const mikv_pages* p, int n, int Hq, int window, int sinks) {
   Pool pool;
   if (check_pages(p, "paged_attention", &pool) || n < 1 || n > 65535 || Hq < 1 || Hq % p->Hkv || window < 0 || sinks < 0) return 0;
-  return static_cast<size_t>(grid_of(p, n, Hq, window, sinks)) * kPaWarps * 2 * kPartFloats * sizeof(float);
+  return part_bytes(grid_of(p, n, Hq, tiles_of(p, window, sinks)));
 }
 
 extern "C" int mikv_paged_attention(const void* q, const mikv_pages* pages, int layer, const int32_t* seqs, int n, int Hq,
@@ -805,29 +881,49 @@ extern "C" int mikv_paged_attention(const void* q, const mikv_pages* pages, int 
   if (n == 0) return MIKV_OK;
   if (!q || !out || !ws) return fail(MIKV_EINVAL, "paged_attention: null pointer");
   if (!aligned16(q) || !aligned16(out) || !aligned16(ws)) return fail(MIKV_EALIGN, "paged_attention: 16-byte alignment");
-  const int grid = grid_of(pages, n, Hq, window, sinks);
-  const size_t need = static_cast<size_t>(grid) * kPaWarps * 2 * kPartFloats * sizeof(float);
+  const int64_t tiles = tiles_of(pages, window, sinks);
+  const int grid = grid_of(pages, n, Hq, tiles);
+  const size_t need = part_bytes(grid);
   if (ws_bytes < need) return fail(MIKV_ESHAPE, "paged_attention: workspace %zu < %zu", ws_bytes, need);
-  a.q = static_cast<const uint16_t*>(q);
+  fill_args(a, q, layer, n, Hq, out, lse, ws);
   a.seqs = seqs;
-  a.layer = layer;
-  a.n = n;
-  a.Hq = Hq;
-  a.rep = Hq / a.p.Hkv;
-  a.groups = (a.rep + kPaRows - 1) / kPaRows;
-  a.heads = (a.rep + a.groups - 1) / a.groups;
   a.window = window;
   a.sinks = sinks;
-  a.out = static_cast<uint16_t*>(out);
-  a.lse = lse;
-  a.part = static_cast<float*>(ws);
-  a.scale = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
-  const cudaStream_t st = as_stream(stream);
-  const bool wide = a.heads > 8;
-  const int64_t tiles = tiles_of(pages, window, sinks);
-  switch (a.p.type) {
-    case MIKV_PAGES_FP16: return wide ? launch<MIKV_PAGES_FP16, 2>(a, grid, tiles, st) : launch<MIKV_PAGES_FP16, 1>(a, grid, tiles, st);
-    case MIKV_PAGES_BF16: return wide ? launch<MIKV_PAGES_BF16, 2>(a, grid, tiles, st) : launch<MIKV_PAGES_BF16, 1>(a, grid, tiles, st);
-    default: return wide ? launch<MIKV_PAGES_INT8, 2>(a, grid, tiles, st) : launch<MIKV_PAGES_INT8, 1>(a, grid, tiles, st);
-  }
+  return dispatch<false>(a, grid, tiles, as_stream(stream));
+}
+
+extern "C" size_t mikv_block_attention_workspace_bytes(const mikv_pages* p, int rows, int Hq, int keep) {
+  Pool pool;
+  if (check_pages(p, "block_attention", &pool) || rows < 1 || static_cast<int64_t>(rows) * p->Hkv > 65535 || Hq < 1 || Hq % p->Hkv ||
+      keep < 1)
+    return 0;
+  return part_bytes(grid_of(p, rows, Hq, picked_tiles(p, keep)));
+}
+
+extern "C" int mikv_block_attention(const void* q, const mikv_pages* pages, int layer, const int32_t* row_seq, const int32_t* row_pos,
+                                    const int32_t* sel, const int32_t* n_sel, int rows, int Hq, int keep, void* out, float* lse, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  clear_error();
+  AttendArgs a;
+  if (int e = check_pages(pages, "block_attention", &a.p)) return e;
+  if (layer < 0 || layer >= a.p.layers) return fail(MIKV_ESHAPE, "block_attention: layer=%d of %d", layer, a.p.layers);
+  if (rows < 0 || static_cast<int64_t>(rows) * a.p.Hkv > 65535 || (!row_seq && rows > a.p.max_seqs))
+    return fail(MIKV_ESHAPE, "block_attention: rows=%d Hkv=%d", rows, a.p.Hkv);
+  if (Hq < 1 || Hq % a.p.Hkv || Hq / a.p.Hkv > 1024) return fail(MIKV_ESHAPE, "block_attention: Hq=%d Hkv=%d", Hq, a.p.Hkv);
+  if (keep < 1 || static_cast<int64_t>(keep) * pages->page_size > 0x7fffffffLL - 4096)
+    return fail(MIKV_ESHAPE, "block_attention: keep=%d blocks of %d", keep, pages->page_size);
+  if (rows == 0) return MIKV_OK;
+  if (!q || !sel || !n_sel || !out || !ws) return fail(MIKV_EINVAL, "block_attention: null pointer");
+  if (!aligned16(q) || !aligned16(out) || !aligned16(ws)) return fail(MIKV_EALIGN, "block_attention: 16-byte alignment");
+  const int64_t tiles = picked_tiles(pages, keep);
+  const int grid = grid_of(pages, rows, Hq, tiles);
+  const size_t need = part_bytes(grid);
+  if (ws_bytes < need) return fail(MIKV_ESHAPE, "block_attention: workspace %zu < %zu", ws_bytes, need);
+  fill_args(a, q, layer, rows * a.p.Hkv, Hq, out, lse, ws);
+  a.row_seq = row_seq;
+  a.row_pos = row_pos;
+  a.sel = sel;
+  a.n_sel = n_sel;
+  a.keep = keep;
+  return dispatch<true>(a, grid, tiles, as_stream(stream));
 }

@@ -91,6 +91,36 @@ __device__ __forceinline__ uint2 quantize8(const uint4& x, uint32_t& meta) {
   return make_uint2(c[0], c[1]);
 }
 
+// The first `rows` of a CTA's 32 source rows (four pieces of keys and of values a thread) to the pool rows `at` behind row
+// `lrow`; those without one are dropped.
+template <bool Q8>
+__device__ __forceinline__ void store_rows(const Pool& p, size_t lrow, const uint4 (&a)[4], const uint4 (&b)[4], const uint32_t* at,
+                                           int rows) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int c = threadIdx.x + u * kRowThreads, r = c >> 4, piece = c & 15;
+    const bool ok = r < rows && at[r] != kNoRow;
+    const size_t row = lrow + (ok ? at[r] : 0);
+    if (!Q8) {
+      if (ok) {
+        *reinterpret_cast<uint4*>(p.k + row * (kD * 2) + piece * 16) = a[u];
+        *reinterpret_cast<uint4*>(p.v + row * (kD * 2) + piece * 16) = b[u];
+      }
+    } else {   // 16 lanes a row: all of a warp quantise
+      uint32_t mk, mv;
+      const uint2 ck = quantize8(a[u], mk), cv = quantize8(b[u], mv);
+      if (ok) {
+        *reinterpret_cast<uint2*>(p.k + row * kD + piece * 8) = ck;
+        *reinterpret_cast<uint2*>(p.v + row * kD + piece * 8) = cv;
+        if ((piece & 7) == 0) {
+          reinterpret_cast<uint32_t*>(p.km + row * kMetaBytes)[piece >> 3] = mk;
+          reinterpret_cast<uint32_t*>(p.vm + row * kMetaBytes)[piece >> 3] = mv;
+        }
+      }
+    }
+  }
+}
+
 // CTA (chunk, head, row i): source tokens chunk * 32 .. of row i to slots start + t of its
 // sequence.  Rows of a sequence that an earlier row of the call names are skipped.
 template <bool Q8>
@@ -131,30 +161,44 @@ __global__ void __launch_bounds__(kRowThreads) paged_append_kernel(const Pool p,
   const int rows = static_cast<int>(min(static_cast<int64_t>(min(kRowTokens, count - t0)), len - slot0));
   if (rows <= 0) return;                                 // slots past the sequence's length
   find_rows<true>(p, s, h, static_cast<int>(slot0), rows, at);
-  const size_t lrow = p.layer_rows() * layer;
+  store_rows<Q8>(p, p.layer_rows() * layer, a, b, at, rows);
+}
+
+// CTA (chunk, head): packed rows chunk * 32 .. to the slots that `slots` names, as far as it names one.
+// Against paged_append_kernel, which looks up a sequence, its length and its table, a row's place is
+// one read away.
+template <bool Q8>
+__global__ void __launch_bounds__(kRowThreads) slot_append_kernel(const Pool p, int layer, RowView k, RowView v, int rows,
+                                                                  const int32_t* __restrict__ slots) {
+  __shared__ uint32_t at[kRowTokens];
+  const int h = blockIdx.y, t0 = blockIdx.x * kRowTokens;
+  uint4 a[4], b[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const int c = threadIdx.x + u * kRowThreads, r = c >> 4, piece = c & 15;
-    const bool ok = r < rows && at[r] != kNoRow;
-    const size_t row = lrow + (ok ? at[r] : 0);
-    if (!Q8) {
-      if (ok) {
-        *reinterpret_cast<uint4*>(p.k + row * (kD * 2) + piece * 16) = a[u];
-        *reinterpret_cast<uint4*>(p.v + row * (kD * 2) + piece * 16) = b[u];
-      }
-    } else {   // 16 lanes a row: all of a warp quantise
-      uint32_t mk, mv;
-      const uint2 ck = quantize8(a[u], mk), cv = quantize8(b[u], mv);
-      if (ok) {
-        *reinterpret_cast<uint2*>(p.k + row * kD + piece * 8) = ck;
-        *reinterpret_cast<uint2*>(p.v + row * kD + piece * 8) = cv;
-        if ((piece & 7) == 0) {
-          reinterpret_cast<uint32_t*>(p.km + row * kMetaBytes)[piece >> 3] = mk;
-          reinterpret_cast<uint32_t*>(p.vm + row * kMetaBytes)[piece >> 3] = mv;
-        }
-      }
+    const int c = threadIdx.x + u * kRowThreads, r = c >> 4;
+    a[u] = b[u] = make_uint4(0, 0, 0, 0);
+    if (t0 + r < rows) {
+      a[u] = *reinterpret_cast<const uint4*>(k.row(0, h, t0 + r) + (c & 15) * 16);
+      b[u] = *reinterpret_cast<const uint4*>(v.row(0, h, t0 + r) + (c & 15) * 16);
     }
   }
+  if (static_cast<int>(threadIdx.x) < kRowTokens) {
+    uint32_t r = kNoRow;
+    const int32_t slot = t0 + static_cast<int>(threadIdx.x) < rows ? slots[t0 + threadIdx.x] : -1;
+    if (slot >= 0) {
+      const uint32_t page = div_of(slot, p.ps);
+      r = pool_row(static_cast<int32_t>(page), p.n_pages, p.Hkv, h, p.ps.d, slot - page * p.ps.d);
+      if (r == kNoRow) {
+        tc::report_giveup(tc::kBadPage);
+      } else if (p.refs[page] > 1) {
+        tc::report_giveup(tc::kSharedPage);
+        r = kNoRow;
+      }
+    }
+    at[threadIdx.x] = r;
+  }
+  __syncthreads();
+  store_rows<Q8>(p, p.layer_rows() * layer, a, b, at, kRowTokens);
 }
 
 // 8 codes to 8 fp16 values fp16(s * code + z), one fp32 rounding before the last (s * code is exact:
@@ -267,4 +311,20 @@ extern "C" int mikv_paged_gather(const mikv_pages* pages, int layer, const int32
   const auto kern = p.type == MIKV_PAGES_INT8 ? paged_gather_kernel<true> : paged_gather_kernel<false>;
   kern<<<move_grid(p, n, T), kRowThreads, 0, as_stream(stream)>>>(p, layer, row_view(*k_out), row_view(*v_out), T, seqs);
   return check_launch("paged_gather_kernel");
+}
+
+extern "C" int mikv_slot_append(const mikv_pages* pages, int layer, const mikv_rows* k, const mikv_rows* v, int rows,
+                                const int32_t* slots, void* stream) {
+  clear_error();
+  Pool p;
+  if (int e = check_pages(pages, "slot_append", &p)) return e;
+  if (layer < 0 || layer >= p.layers) return fail(MIKV_ESHAPE, "slot_append: layer=%d of %d", layer, p.layers);
+  if (rows < 0) return fail(MIKV_ESHAPE, "slot_append: rows=%d", rows);
+  if (rows == 0) return MIKV_OK;
+  if (int e = check_rows(k, "slot_append", "k")) return e;
+  if (int e = check_rows(v, "slot_append", "v")) return e;
+  if (!slots) return fail(MIKV_EINVAL, "slot_append: null slots");
+  const auto kern = p.type == MIKV_PAGES_INT8 ? slot_append_kernel<true> : slot_append_kernel<false>;
+  kern<<<dim3((rows - 1) / kRowTokens + 1, p.Hkv), kRowThreads, 0, as_stream(stream)>>>(p, layer, row_view(*k), row_view(*v), rows, slots);
+  return check_launch("slot_append_kernel");
 }

@@ -67,6 +67,10 @@ extern "C" int mikv_wait_status(unsigned* bits, int clear) {
   if (int e = mikv::window_attention_status(&v, clear != 0)) return e;
   if (int e = mikv::paged_attention_status(&v, clear != 0)) return e;
   if (int e = mikv::paged_rows_status(&v, clear != 0)) return e;
+  if (int e = mikv::batch_rows_status(&v, clear != 0)) return e;
+  if (int e = mikv::page_bounds_status(&v, clear != 0)) return e;
+  if (int e = mikv::block_select_status(&v, clear != 0)) return e;
+  if (int e = mikv::chunk_attention_status(&v, clear != 0)) return e;
   if (int e = mikv::tc::wait_giveups(&v, clear != 0)) return e;  // the probe's word
   *bits = v;
   return MIKV_OK;

@@ -5,6 +5,8 @@ The buffers are torch tensors; every operation on them is one of the library's C
   prompt  reserve -> append (every layer) -> mikv_window_attention; a later chunk attends to
           what gather reads back
   decode  reserve (one token each) -> append (every layer) -> attend (every layer)
+  mixed   chunks of prompts beside single tokens, as packed rows: reserve -> rows -> in every layer put, then
+          attend_rows; or, where each row reads a part of its sequence alone, renew, pick and attend_blocks
   fork    sequences that share a prefix; compact: eviction to the positions mikv_select keeps;
           free: a finished sequence
 
@@ -14,6 +16,7 @@ step can be captured into a CUDA graph.
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple
 
 import torch
 
@@ -75,6 +78,22 @@ class PagedCache:
         """For attend of n sequences; one for window 0 serves every window."""
         return self._bytes(_lib.load().mikv_paged_attention_workspace_bytes(self.ref, n, Hq, window, sinks))
 
+    def chunk_workspace(self, n, rows, Hq):
+        """For attend_rows of n requests with `rows` rows."""
+        return self._bytes(_lib.load().mikv_chunk_attention_workspace_bytes(self.ref, n, rows, Hq))
+
+    def block_workspace(self, rows, Hq, keep):
+        """For pick and for attend_blocks, one behind the other."""
+        lib = _lib.load()
+        return self._bytes(max(lib.mikv_block_select_workspace_bytes(self.ref, rows),
+                               lib.mikv_block_attention_workspace_bytes(self.ref, rows, Hq, keep)))
+
+    def bounds_buffers(self):
+        """(bounds, scales) of all pages' keys, for renew and pick."""
+        layers, n_pages, Hkv, _, D = self.k.shape
+        return (torch.zeros(layers, n_pages, Hkv, 2, D, dtype=torch.int8, device=self.device),
+                torch.zeros(layers, n_pages, Hkv, dtype=torch.float32, device=self.device))
+
     def _bytes(self, nbytes):
         if nbytes == 0:
             raise ValueError("the library has no workspace size for these dimensions")
@@ -123,3 +142,55 @@ class PagedCache:
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=self.device) if lse is None else lse
         _lib.mikv_paged_attention(q, self, layer, window, sinks, out, lse, seqs=seqs, ws=ws)
         return out, lse
+
+    # --- packed batches ----------------------------------------------------------------
+    def rows(self, counts, rows, seqs=None, start=None):
+        """BatchRows of requests with counts [n] rows each, in arrays of `rows` rows."""
+        b = BatchRows(self._ints(counts.shape[0] + 1), *torch.empty(3, rows, dtype=torch.int32, device=self.device), seqs, start)
+        _lib.mikv_batch_rows(self, counts, b.row_start, b.seq, b.pos, b.slot, seqs=seqs, start=start)
+        return b
+
+    def put(self, layer, k, v, batch):
+        """Rows k, v [rows][Hkv][D] of a batch into their slots."""
+        _lib.mikv_slot_append(self, layer, k, v, batch.slot)
+
+    def renew(self, layer, batch, bounds):
+        """bounds: (bounds, scales) of the pages that the batch's rows lie on, done anew."""
+        _lib.mikv_page_bounds(self, layer, batch.seq, batch.pos, *bounds)
+
+    def attend_rows(self, layer, q, batch, window=0, sinks=0, out=None, lse=None, ws=None):
+        """Rows q [rows][Hq][D] of a batch against their sequences; returns out and lse fp32 [rows][Hq].  Rows
+        of no request are left as they were (outputs made here: 0)."""
+        out = torch.zeros(q.shape, dtype=q.dtype, device=self.device) if out is None else out
+        lse = torch.zeros(q.shape[:2], dtype=torch.float32, device=self.device) if lse is None else lse
+        _lib.mikv_chunk_attention(q, self, layer, batch.row_start, window, sinks, out, lse, seqs=batch.seqs, start=batch.start, ws=ws)
+        return out, lse
+
+    def pick(self, layer, q, bounds, keep, first=0, recent=1, batch=None, sel=None, n_sel=None, ws=None):
+        """The `keep` blocks that each row of q [rows][Hq][D] reads (batch None: row r is sequence r's last token):
+        sel int32 [rows][Hkv][keep] and n_sel int32 [rows][Hkv]."""
+        rows, Hkv = q.shape[0], self.k.shape[2]
+        sel = torch.empty(rows, Hkv, keep, dtype=torch.int32, device=self.device) if sel is None else sel
+        n_sel = torch.empty(rows, Hkv, dtype=torch.int32, device=self.device) if n_sel is None else n_sel
+        seq, pos = (None, None) if batch is None else (batch.seq, batch.pos)
+        _lib.mikv_block_select(q, self, layer, *bounds, first, recent, sel, n_sel, row_seq=seq, row_pos=pos, ws=ws)
+        return sel, n_sel
+
+    def attend_blocks(self, layer, q, sel, n_sel, batch=None, out=None, lse=None, ws=None):
+        """Rows q [rows][Hq][D] against their picked blocks; returns out and lse fp32 [rows][Hq]."""
+        out = torch.empty_like(q) if out is None else out
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=self.device) if lse is None else lse
+        seq, pos = (None, None) if batch is None else (batch.seq, batch.pos)
+        _lib.mikv_block_attention(q, self, layer, sel, n_sel, out, lse, row_seq=seq, row_pos=pos, ws=ws)
+        return out, lse
+
+
+class BatchRows(NamedTuple):
+    """Rows of a packed batch: row_start int32 [n + 1]; each row's sequence, position and slot int32 [rows]; and
+    the requests' sequences and first slots that they were made from."""
+    row_start: torch.Tensor
+    seq: torch.Tensor
+    pos: torch.Tensor
+    slot: torch.Tensor
+    seqs: torch.Tensor | None
+    start: torch.Tensor | None

@@ -1,0 +1,288 @@
+"""Attention of packed rows over pages against the oracle in 64 bits, and whole serving steps of packed batches."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.batch as ob
+import paged_helpers as ph
+from mixed_precision_kv_balancer_gb300 import _lib
+from mixed_precision_kv_balancer_gb300.paged import PagedCache
+
+pytestmark = pytest.mark.gpu
+ints = ph.ints
+TYPES = ["fp16", "bf16", "int8"]
+
+
+def _rows(rows, Hq, type, layout="rows", seed=5):
+    if layout == "heads":
+        return ph.normal((Hq, rows, 128), seed, ph.DTYPE[type]).to(ph.DEV).transpose(0, 1)
+    if layout == "padded":
+        return ph.normal((rows + 2, Hq + 1, 136), seed, ph.DTYPE[type]).to(ph.DEV)[1:rows + 1, 1:, :128]
+    return ph.normal((rows, Hq, 128), seed, ph.DTYPE[type]).to(ph.DEV)
+
+
+def held(cache, layer, s):
+    """A sequence's keys and values as the products take them: INT8 rounded once to fp16."""
+    k, v = ph.sequence(cache, layer, s)
+    if cache.type == "int8":
+        k, v = k.astype(np.float16).astype(np.float64), v.astype(np.float16).astype(np.float64)
+    return k, v
+
+
+def expect(cache, q, row_start, window, sinks, seqs=None, start=None, layer=0):
+    """(out, lse, mag); NaN for rows of no request."""
+    rows, Hq, D = q.shape
+    out, mag, lse = np.full((rows, Hq, D), np.nan), np.full((rows, Hq, D), np.nan), np.full((rows, Hq), np.nan)
+    qn = ph.f64(q)
+    for i in range(len(row_start) - 1):
+        r0, r1 = min(max(row_start[i], 0), rows), min(max(row_start[i + 1], 0), rows)
+        if r1 <= r0:
+            continue
+        s = i if seqs is None else seqs[i]
+        out[r0:r1], mag[r0:r1], lse[r0:r1] = 0, 0, -np.inf
+        if not 0 <= s < cache.lens.numel() or int(cache.lens[s]) <= 0 or (start is not None and start[i] < 0):
+            continue
+        k, v = held(cache, layer, s)
+        first = k.shape[1] - (r1 - r0) if start is None else start[i]
+        out[r0:r1], lse[r0:r1], mag[r0:r1] = ob.attend(qn[r0:r1], k, v, first + np.arange(r1 - r0), window, sinks)
+    return out, lse, mag
+
+
+def check(cache, q, row_start, window=0, sinks=0, seqs=None, start=None, layer=0, status=0):
+    rows, Hq, _ = q.shape
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device=ph.DEV)
+    lse = torch.full((rows, Hq), 7.0, device=ph.DEV)
+    _lib.mikv_chunk_attention(q, cache, layer, ints(row_start), window, sinks, out, lse, seqs=None if seqs is None else ints(seqs),
+                              start=None if start is None else ints(start))
+    want, wl, mag = expect(cache, q, row_start, window, sinks, seqs, start, layer)
+    ph.close(out, want, mag, ph.HALF_STEP[cache.type], weights=ph.HALF_STEP[cache.type])   # weights rounded once
+    ph.close_lse(lse, wl)
+    left = np.isnan(wl)
+    assert (ph.f64(out)[left] == 7).all() and (ph.f64(lse)[left] == 7).all()
+    assert _lib.mikv_wait_status() == status
+    return out, lse
+
+
+def starts(counts):
+    return [0] + np.cumsum(counts).tolist()
+
+
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("lens,ps,Hkv,rep,counts", [
+    ([1], 16, 1, 1, [1]), ([9], 4, 1, 2, [9]), ([0, 1, 15, 16, 17, 200], 16, 2, 4, [0, 1, 3, 16, 5, 1]), ([333, 500], 7, 1, 8, [130, 40]),
+    ([600, 30], 1, 2, 5, [64, 30]), ([1000, 40], 20, 3, 9, [257, 1]), ([900], 16, 1, 17, [128]), ([300, 300], 128, 2, 16, [300, 7]),
+    ([1500, 2000, 100], 32, 2, 3, [700, 1, 100]), ([130], 64, 1, 1, [129]), ([700], 100, 1, 3, [385]), ([258, 257, 256], 16, 1, 1, [258, 257, 256])])
+def test_chunks(type, lens, ps, Hkv, rep, counts):
+    cache = ph.make(lens, ps, Hkv, type, layers=2)
+    check(cache, _rows(sum(counts), Hkv * rep, type), starts(counts), layer=1)
+
+
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (17, 0), (64, 4), (128, 130), (200, 1), (513, 300), (5000, 9), (0, 5)])
+def test_window_and_sinks(type, window, sinks):
+    cache = ph.make([0, 1, 5, 700, 64, 900], 16, 2, type)
+    counts = [0, 1, 2, 300, 64, 1]
+    check(cache, _rows(sum(counts), 6, type), starts(counts), window, sinks)
+
+
+@pytest.mark.parametrize("type", ["fp16", "int8"])
+@pytest.mark.parametrize("layout", ["heads", "padded"])
+def test_strided_rows(type, layout):
+    cache = ph.make([300, 77], 16, 2, type)
+    q = _rows(150, 8, type, layout)
+    out, lse = check(cache, q, [0, 140, 150])
+    into = _rows(150, 8, type, layout, seed=9)
+    cache.attend_rows(0, q, cache.rows(ints([140, 10]), 150), out=into)
+    assert torch.equal(into, out)
+
+
+@pytest.mark.parametrize("type", TYPES)
+def test_many_single_tokens_beside_chunks(type):
+    rng = np.random.RandomState(3)
+    lens = rng.randint(1, 900, 90).tolist()
+    counts = [1] * 90
+    counts[3], counts[40], lens[3], lens[40] = 200, 33, 700, 33
+    cache = ph.make(lens, 16, 2, type)
+    q = _rows(sum(counts), 8, type)
+    out, lse = check(cache, q, starts(counts))
+    again = cache.attend_rows(0, q, cache.rows(ints(counts), sum(counts)))
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("type", TYPES)
+def test_long_sequences_are_shared_out(type):
+    cache = ph.make([20000, 6000, 3, 0, 9000], 64, 1, type)
+    counts = [3, 150, 3, 0, 1]
+    q = _rows(sum(counts), 4, type)
+    out, lse = check(cache, q, starts(counts))
+    for _ in range(3):
+        again = cache.attend_rows(0, q, cache.rows(ints(counts), sum(counts)))
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    check(cache, q, starts(counts), 5000, 130)
+
+
+@pytest.mark.parametrize("type", TYPES)
+def test_requests_of_every_kind(type):
+    """Refused, out of range, empty, named twice, behind the length, not the last rows; rows of no request."""
+    cache = ph.make([90, 0, 400, 33], 16, 2, type)
+    seqs = [2, 0, -1, 4, 1, 3, 2, 3, 0]
+    start = [250, -1, 0, 0, 0, 30, 399, 2 ** 31 - 3, 0]
+    counts = [40, 5, 3, 3, 4, 8, 1, 5, 0]
+    rows = sum(counts) + 9
+    check(cache, _rows(rows, 8, type), starts(counts), seqs=seqs, start=start)
+    check(cache, _rows(rows, 8, type), starts(counts), 50, 3, seqs=seqs, start=start)
+    check(cache, _rows(rows, 8, type), starts(counts), seqs=seqs)                # more rows than slots: some see nothing
+    at = starts(counts)
+    at[1], at[-1] = 38, rows + 100                                               # rows between requests, past the end
+    check(cache, _rows(rows, 8, type), [min(x, rows) if i else -3 for i, x in enumerate(at)], seqs=seqs, start=start)
+
+
+def test_pages_outside_the_pool_are_not_seen():
+    _lib.mikv_wait_status()
+    cache = ph.make([200, 64], 16, 2, "fp16", poison=False)
+    q = _rows(41, 4, "fp16")
+    cache.table[0, 3] = -1
+    cache.table[1, :4] = 2 ** 31 - 1
+    out, lse = cache.attend_rows(0, q, cache.rows(ints([40, 1]), 41))
+    assert _lib.mikv_wait_status() == 64
+    cache.table[0, 3] = 0
+    k, v = held(cache, 0, 0)
+    p, j = 160 + np.arange(40)[:, None], np.arange(200)[None]
+    seen = (j <= p) & ((j < 48) | (j >= 64))
+    for h in range(4):
+        l = np.where(seen, ph.f64(q)[:40, h] @ k[h // 2].T / 128 ** 0.5, -np.inf)
+        w = np.exp(l - l.max(1, keepdims=True))
+        want = (w @ v[h // 2]) / w.sum(1, keepdims=True)
+        mag = (w @ np.abs(v[h // 2])) / w.sum(1, keepdims=True)
+        ph.close(out[:40, h], want, mag, 2.0 ** -11, 2.0 ** -11)
+    assert (out[40] == 0).all() and torch.isneginf(lse[40]).all()
+
+
+@pytest.mark.parametrize("type", TYPES)
+def test_slots_that_no_row_sees_hold_anything(type):
+    cache = ph.make([500], 16, 1, type, poison=False)
+    q = _rows(3, 2, type)
+    want = check(cache, q, [0, 3], 100, 5)
+    page = cache.table[0].long()
+    bad = cache.k if cache.k_meta is None else cache.k_meta
+    badv = cache.v if cache.v_meta is None else cache.v_meta
+    for t in (bad, badv):
+        t[0, page[1:24]] = float("nan")              # slots 16 .. 383: the first row sees 0 .. 4 and 398 ..
+        t[0, page[0], :, 5:] = float("inf")
+        t[0, page[31], :, 4:] = float("nan")         # behind the last slot
+    got = cache.attend_rows(0, q, cache.rows(ints([3]), 3), 100, 5)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+# --- a serving step -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("type", TYPES)
+def test_serving_steps(type):
+    """Prompts in chunks beside single tokens: reserve, maps, append, bounds, dense and picked attention; a fork
+    and a compaction between; against a plain copy of what was stored."""
+    H, rep, ps = 2, 4, 16
+    cache = PagedCache(2, 120, ps, H, 128, 5, 30, type=type)
+    buf = cache.bounds_buffers()
+    rng = np.random.RandomState(0)
+    steps = [[40, 0, 100, 1, 0], [37, 3, 1, 1, 0], [1, 1, 1, 200, 0], [1, 30, 1, 1, 0], [1, 1, 5, 1, 7]]
+    for step, counts in enumerate(steps):
+        n = sum(counts)
+        rows = n + 5
+        c = ints(counts)
+        start = cache.reserve(c)
+        batch = cache.rows(c, rows, start=start)
+        for layer in range(2):
+            k, v, q = (ph.normal((rows, h, 128), 100 * step + 10 * layer + i, ph.DTYPE[type]).to(ph.DEV)
+                       for i, h in ((0, H), (1, H), (2, H * rep)))
+            cache.put(layer, k, v, batch)
+            cache.renew(layer, batch, buf)
+            out, lse = cache.attend_rows(layer, q, batch, window=60 * layer, sinks=2 * layer)
+            want, wl, mag = expect(cache, q, starts(counts), 60 * layer, 2 * layer, start=start.tolist(), layer=layer)
+            ph.close(out, want, mag, ph.HALF_STEP[type], weights=ph.HALF_STEP[type])
+            ph.close_lse(lse, wl)
+            assert (out[n:] == 0).all()
+            # picked blocks: of every row with no more than 6, all; bounds are those of the whole cache done anew
+            sel, n_sel = cache.pick(layer, q[:n], buf, 6, 1, 2, batch=_first(batch, n))
+            anew = cache.bounds_buffers()
+            lens = cache.lens.clone()
+            cache.renew(layer, cache.rows(lens, int(lens.sum())), anew)
+            used = cache.refs > 0
+            assert torch.equal(buf[0][layer, used], anew[0][layer, used]) and torch.equal(buf[1][layer, used], anew[1][layer, used])
+            out, lse = cache.attend_blocks(layer, q[:n], sel, n_sel, _first(batch, n))
+            blocks = batch.pos[:n] // ps + 1
+            assert torch.equal(n_sel, blocks.clamp(max=6)[:, None].expand(-1, H).int())
+            few = (blocks <= 6).cpu().numpy()
+            want, wl, mag = expect(cache, q[:n], starts(counts), 0, 0, start=start.tolist(), layer=layer)
+            if type != "int8":
+                ph.close(out[few], want[few], mag[few], ph.HALF_STEP[type], weights=2.0 ** -16)
+                ph.close_lse(lse[few], wl[few])
+        if step == 2:
+            cache.fork(ints([0]), ints([4]))         # shares full pages, copies the last one
+            keep = torch.arange(0, 64, 2, dtype=torch.int32, device=ph.DEV).expand(2, 1, H, 32).contiguous()
+            assert cache.compact(keep, ints([32]), seqs=ints([2])).tolist() == [1]
+            for layer in range(2):
+                cache.renew(layer, cache.rows(cache.lens[[2, 4]].contiguous(), int(cache.lens[2] + cache.lens[4]), seqs=ints([2, 4])), buf)
+    assert _lib.mikv_wait_status() == 0
+
+
+def _first(batch, n):
+    return batch._replace(seq=batch.seq[:n].contiguous(), pos=batch.pos[:n].contiguous())
+
+
+@pytest.mark.parametrize("type", TYPES)
+def test_a_captured_step_follows_the_lengths(type):
+    """A step of fixed row arrays, captured once, replayed while the sequences grow, next to the same calls made eagerly."""
+    H, rep = 2, 3
+    caches = [PagedCache(1, 64, 16, H, 128, 4, 16, type=type) for _ in range(2)]
+    rows, step = 48, 6
+    counts = torch.zeros(4, dtype=torch.int32, device=ph.DEV)
+    k, v, q = (torch.zeros(rows, h, 128, dtype=ph.DTYPE[type], device=ph.DEV) for h in (H, H, H * rep))
+
+    def run(cache, buf, out, ws, ws2):
+        start = cache.reserve(counts, start=buf[2])
+        batch = cache.rows(counts, rows, start=start)
+        cache.put(0, k, v, batch)
+        cache.renew(0, batch, buf[:2])
+        cache.attend_rows(0, q, batch, out=out[0], lse=out[1], ws=ws)
+        sel, n_sel = cache.pick(0, q, buf[:2], 4, 1, 1, batch=batch, ws=ws2)
+        return cache.attend_blocks(0, q, sel, n_sel, batch, ws=ws2)
+
+    state = []
+    for cache in caches:
+        out = (torch.zeros_like(q), torch.zeros(rows, H * rep, device=ph.DEV))
+        buf = (*cache.bounds_buffers(), torch.zeros(4, dtype=torch.int32, device=ph.DEV))
+        state.append((cache, buf, out, cache.chunk_workspace(4, rows, H * rep), cache.block_workspace(rows, H * rep, 4)))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(*state[1])                               # nothing to add yet
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        blocks = run(*state[1])
+    for i, c in enumerate([[30, 0, 17, 1], [1, 40, 1, 1], [1, 1, 1, 1], [0, 0, 0, 45], [20, 1, 1, 1], [1, 1, 1, 1]][:step]):
+        counts.copy_(ints(c))
+        for j, t in enumerate((k, v, q)):
+            t.copy_(ph.normal(t.shape, 50 * i + j, t.dtype))
+        for s in state:
+            s[2][0].fill_(3), s[2][1].fill_(3)
+        want = run(*state[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(state[0][2][0], state[1][2][0]) and torch.equal(state[0][2][1], state[1][2][1])
+        assert torch.equal(state[0][1][0], state[1][1][0]) and torch.equal(state[0][1][1], state[1][1][1])
+        n = sum(c)
+        assert torch.equal(want[0][:n], blocks[0][:n]) and torch.equal(want[1][:n], blocks[1][:n])
+
+
+def test_calls_on_another_stream():
+    cache = ph.make([700, 300], 16, 2, "fp16")
+    q = _rows(120, 8, "fp16")
+    batch = cache.rows(ints([100, 20]), 120)
+    want = cache.attend_rows(0, q, batch)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out, lse = torch.zeros_like(q), torch.zeros(120, 8, device=ph.DEV)
+    _lib.mikv_chunk_attention(q, cache, 0, batch.row_start, 0, 0, out, lse, stream=side)
+    side.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
