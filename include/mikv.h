@@ -637,9 +637,9 @@ size_t mikv_block_attention_workspace_bytes(const mikv_pages* p, int rows, int H
  * range, its position is below 0) gives out 0 and lse -inf.  Rows of no request are not written.
  * Several requests may name one sequence.  Slots that are not seen by any row of a request may
  * hold anything; a value row that one of them sees must be finite, or it may reach the request's
- * other rows.  The softmax weights, and INT8 pages' keys and values, are rounded once to 16 bits
- * before the products; sums and statistics are fp32.
- * n at most 4096, Hq a multiple of Hkv, up to 1024 query heads per key head; n == 0 or rows == 0 does nothing.
+ * other rows.  Slots on a page outside the pool read as zeros (reported, mikv_wait_status bit 64).
+ * start is held at 2^30.  The softmax weights are rounded once to 16 bits before they meet the values; sums and statistics are fp32.
+ * rows at most 2^20, max_pages * page_size at most 2^30, n at most 4096, Hq a multiple of Hkv, up to 1024 query heads per key head; n == 0 or rows == 0 does nothing.
  * ws >= mikv_chunk_attention_workspace_bytes(p, n, rows, Hq), 32-byte aligned; two calls must not share
  * a workspace concurrently.
  * Errors: EINVAL (null, window, sinks, rows of out that overlap), ESHAPE, EALIGN, EUNSUPPORTED, ECUDA.
@@ -679,6 +679,7 @@ int mikv_set_attention_events(void* begin, void* end);
  *   8 = K9 (output perturbation), 16 = mikv_wait_probe, 32 = mikv_window_attention,
  *   64 = no wait: an append, a gather, row maps, bounds, a choice of blocks or an attention over pages
  *   met a table entry, slot or block outside the pool (skipped, read as zeros, or not seen)
+ *   256 = mikv_chunk_attention
  *   128 = no wait: an append met a page that several sequences own (its slots are skipped)
  * and clears them if `clear` is non-zero.  It copies synchronously: call it after the work
  * in question has completed (e.g. after synchronising its stream).

@@ -531,7 +531,8 @@ def mikv_set_attention_events(begin=None, end=None):
 
 WAIT_BITS = {1: "K3 pass 1 (row log-sum-exp)", 2: "K3 pass 2 (column sums)", 4: "K6 (V.W_O norms)",
              8: "K9 (output perturbation)", 16: "mikv_wait_probe", 32: "mikv_window_attention",
-             64: "a page, slot or block outside the pool", 128: "an append into a shared page"}
+             64: "a page, slot or block outside the pool", 128: "an append into a shared page",
+             256: "mikv_chunk_attention"}
 
 
 def mikv_wait_status(clear=True) -> int:

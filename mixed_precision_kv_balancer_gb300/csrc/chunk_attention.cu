@@ -1,13 +1,31 @@
-// Attention of the rows of a packed batch over the paged cache: chunks of prompts and single tokens
-// side by side, under a sliding window with sinks.
+// Attention of the rows of a packed batch over the paged cache: chunks of prompts and single tokens side
+// by side, under a sliding window with sinks (tcgen05).
 //
 // Mathematics: one pass over the visible keys, out = sum_j p_j v_j / sum_j p_j with p_j = exp2(l_j - m)
-// and a running maximum m.  First form: a CTA per (row, query head), whose warps take every fourth
-// group of 32 keys, a key a lane, and join at the end.
-#include <cuda_bf16.h>
+// and a reference m per row (attention_tile.cuh).  Bound by the tensor cores where a request has many
+// rows (4 * 128 flop per visible query-key pair), by HBM where it has few (512 or 272 bytes a slot and
+// key head).
+//
+// A CTA holds two tiles of 128 query rows over one key head (chunk_index.h), and walks key tiles of 128
+// slots: per key tile i and query tile t
+//   S_t = Q_t K_i^T     tcgen05, both operands in shared memory, 128 fp32 TMEM columns
+//   P_t = exp2(...)     four warps, one query row a thread, written over S_t as 16-bit pairs
+//   O_t += P_t V_i      tcgen05, P from TMEM, V as it lies (rows are the contraction)
+// Lengths are known on the device alone and differ from request to request, so that all key tiles of a
+// call form one line, of which each CTA takes an equal part; a CTA finds its part in sums over the
+// requests, which all of its threads make before it begins.  Items that are cut are joined by a second kernel.
+//
+// Two warps bring keys and values from the pages to a ring of four 32 KB buffers (128-byte swizzle), row by
+// row: a page has any number of rows, and a tile begins and ends inside pages.  Rows that no query of
+// the item sees are zeros there, so that they may hold anything.  The first of the two walks the line,
+// and tells the other warps what each item is.
+//
+// INT8 pages: s * code + z is held as two fp16 numbers, the nearest one and what is left (22 bits), and each
+// product is two: keys rounded to fp16 alone put 1e-4 into lse and half as much again into the outputs.
+#include <algorithm>
 
-#include "paged.cuh"
-#include "tcgen05.cuh"
+#include "attention_tile.cuh"
+#include "chunk_index.h"
 
 namespace mikv {
 
@@ -15,111 +33,857 @@ int chunk_attention_status(unsigned* out, bool clear) { return tc::wait_giveups(
 
 namespace {
 
-constexpr int kCaThreads = 128;
-constexpr int kCaWarps = kCaThreads / 32;
+using namespace at;
 
+constexpr int kCaRows = kKeyRows;
+constexpr int kCaNarrow = 32;               // columns of a tile that holds the last few sinks
+constexpr int kCaRing = 4;
+constexpr int kCaThreads = 384;             // 2 x 4 softmax warps, 2 MMA warps, 2 loading warps
+constexpr int kCaMmaWarp = 8, kCaLoadWarp = 10, kCaLoaders = 2;
+constexpr int kCaTold = 4;                  // items that the other warps may be behind
+constexpr int kCaSmem = (2 + kCaRing) * tc::kTileBytes + 1024;
+constexpr uint32_t kCaCols = 512;           // S_0, S_1, O_0, O_1: 128 columns each
+constexpr uint32_t kCaO = 256;
+constexpr int kMaxRequests = 4096;
+constexpr int kMaxChunkRows = 1 << 20;      // of a call: the sums of its blocks fit the ring
+
+struct Mask {
+  int32_t window, sinks;
+};
 struct ChunkArgs {
   Pool p;
   RowView q, out;
   float* lse;
+  float* part;                 // the line's cut items, see part_sums and part_ml
   const int32_t *seqs, *start, *row_start;
-  int layer, n, rows, Hq, rep, window, sinks;
-  float scale;
+  int layer, n, rows, Hq, rep, ctas;
+  int tile_rows;               // rows of a tile that can count
+  Mask qb;
+  bool wide_out;               // rows of out begin at multiples of 32 bytes
+  float scale;                 // log2(e) / sqrt(D)
 };
 
-template <int TYPE>
-__device__ __forceinline__ float elem(const uint8_t* x, const uint8_t* meta, size_t row, int c) {
-  if (TYPE == MIKV_PAGES_INT8) {
-    const __half2 m = reinterpret_cast<const __half2*>(meta + row * kMetaBytes)[c / kGS];
-    return __half2float(__float2half_rn(fmaf(__low2float(m), static_cast<float>(x[row * kD + c]), __high2float(m))));
+struct CaBars {
+  uint64_t told[kCaTold], heard[kCaTold];   // the item is known; every warp is done with it
+  uint64_t full[kCaRing], empty[kCaRing];   // buffer landed; the products that read it are done
+  uint64_t turn[2];                         // the tile's products may be issued
+  uint64_t qfree;                           // the products that read the queries are done
+  uint64_t q, s[2], p[2][2], o[2];          // queries landed; scores, half the weights, last sums written
+};
+
+// A request as every warp reads it.
+struct Request {
+  int row0, seq;
+  Rows r;
+  RowTiles t;
+};
+__device__ __forceinline__ int request_row(const ChunkArgs& a, int i) { return min(max(a.row_start[i], 0), a.rows); }
+__device__ __forceinline__ Request request_of(const ChunkArgs& a, int i) {
+  Request q;
+  q.row0 = request_row(a, i);
+  const int rows = max(request_row(a, i + 1) - q.row0, 0);
+  q.seq = a.seqs ? a.seqs[i] : i;
+  const bool there = static_cast<uint32_t>(q.seq) < static_cast<uint32_t>(a.p.max_seqs);
+  q.r = rows_of(rows, there && rows > 0 ? a.p.len_of(q.seq) : 0, a.start != nullptr, a.start ? a.start[i] : 0);
+  q.t = row_tiles_of(rows, a.rep);
+  return q;
+}
+
+// What of an item that is cut the joining kernel has to know; written by the CTA that begins it.
+struct Cut {
+  int last;          // the CTA that ends it; -1: none is cut
+  int before;        // whether that CTA's part of the line has items before
+  int row0, rows, q0[2], head[2], heads[2], tb;   // per tile: first row of the request, first head of q, heads (0: no tile)
+  int pad;
+};
+
+// What one CTA works on, in shared memory: written by the first loading warp, read by the others.
+struct Work {
+  int head[2], heads[2], q0[2];   // per tile: first head of q, heads of it that count; first row of the request
+  int pa[2], pb[2];       // positions of its first and last row
+  int from[2], last[2];   // query tile t sees the sinks' key tiles and tiles from .. last; last -1: none
+  int begin, end;         // key tiles of this part: of ts of the sinks, then tw0, tw0 + 1, ...
+  int ts, tw0;
+  int ns;                 // key tiles that hold sinks, of either part of the list
+  int nt;                 // query tiles; -1: there is no further item
+  int whole;              // all of the item
+  int row0, rows, keys, tb, seq;   // of the request
+  __device__ __forceinline__ int j0(int i) const { return (i < ts ? i : tw0 + i - ts) * kCaRows; }
+  __device__ __forceinline__ bool sees(int t, int i) const { return i <= last[t] && (i < ns || i >= from[t]); }
+};
+// Item `item` of block `blk`, key tiles t0 .. t1 of it.
+__device__ __forceinline__ Work work_of(const ChunkArgs& a, const Request& q, int blk, int item, int t0, int t1) {
+  Work w;
+  const int hk = item / q.t.per, u = item - hk * q.t.per;
+  const int q0 = block_row(q.t, blk);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int group = q.t.pair_heads ? 2 * u + t : u;
+    w.head[t] = hk * a.rep + group * q.t.hb;
+    w.heads[t] = min(q.t.hb, a.rep - group * q.t.hb);
+    w.q0[t] = q0 + (q.t.pair_heads ? 0 : t * q.t.tb);
+    w.pa[t] = q.r.off + w.q0[t];
+    w.pb[t] = q.r.off + min(w.q0[t] + q.t.tb, q.r.rows) - 1;
   }
-  const uint16_t h = reinterpret_cast<const uint16_t*>(x)[row * kD + c];
-  return TYPE == MIKV_PAGES_BF16 ? __uint_as_float(static_cast<uint32_t>(h) << 16) : __half2float(__ushort_as_half(h));
+  w.nt = w.q0[1] >= q.r.rows || w.heads[1] <= 0 ? 1 : 2;
+  const KeyTiles k = chunk_tiles(q.t, q.r, a.qb.window, a.qb.sinks, blk);
+  w.ts = k.ts;
+  w.tw0 = k.tw0;
+  w.ns = k.ns;
+  w.begin = min(t0, k.tiles);
+  w.end = min(t1, k.tiles);
+  w.whole = t0 == 0 && t1 >= k.tiles;
+  w.row0 = q.row0;
+  w.rows = q.r.rows;
+  w.keys = q.r.keys;
+  w.tb = q.t.tb;
+  w.seq = q.seq;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int e = min(w.pb[t], q.r.keys - 1) < 0 ? -1 : min(w.pb[t], q.r.keys - 1) / kCaRows;
+    w.from[t] = w.ts + (a.qb.window > 0 ? max(w.pa[t] - a.qb.window + 1, 0) / kCaRows - w.tw0 : 0);
+    int last = t >= w.nt || e < 0 ? -1 : e - w.tw0 + w.ts;   // the last one of this part
+    last = min(last, w.end - 1);
+    if (last < w.from[t]) last = min(last, w.ns - 1);
+    if (last < w.begin) last = -1;
+    w.last[t] = last;
+  }
+  return w;
+}
+// Whether all rows of query tile t see all of the key tile at j0.
+__device__ __forceinline__ bool tile_whole(const ChunkArgs& a, int pa, int pb, int keys, int j0) {
+  return j0 + kCaRows - 1 <= min(pa, keys - 1) && (a.qb.window == 0 || j0 > pb - a.qb.window || j0 + kCaRows <= a.qb.sinks);
+}
+// Whether key tile i, at j0, counts with its first kCaNarrow columns alone: the sinks' last tile, mostly.
+__device__ __forceinline__ bool tile_narrow(const ChunkArgs& a, int ts, int i, int j0) { return i < ts && a.qb.sinks - j0 <= kCaNarrow; }
+
+// A CTA's part of the line, walked by its first loading warp.
+struct Walk {
+  int req, blk, item;    // the item
+  int places, t0, t1;    // its places, and its key tiles of this part
+  int left;              // items of the block behind it
+  int64_t to_go;         // places of this CTA's part from the item's begin on
+  Request q;
+  bool idle;
+
+  __device__ __forceinline__ void open(const ChunkArgs& a) {   // places of block `blk`
+    places = uniform(chunk_places(q.t, q.r, a.qb.window, a.qb.sinks, blk));
+  }
+  __device__ __forceinline__ void load(const ChunkArgs& a) {
+    q = request_of(a, req);
+    q.row0 = uniform(q.row0);
+    q.seq = uniform(q.seq);
+    q.r.rows = uniform(q.r.rows);
+    q.r.off = uniform(q.r.off);
+    q.r.keys = uniform(q.r.keys);
+  }
+  __device__ __forceinline__ Work work(const ChunkArgs& a) const { return work_of(a, q, blk, item, t0, t1); }
+  // On to the next item, by the whole warp; false where there is none.
+  __device__ __forceinline__ bool next(const ChunkArgs& a, bool ok) {
+    to_go -= places;
+    if (!__all_sync(0xffffffffu, to_go > 0 && ok)) return false;
+    if (--left < 0) {
+      if (++blk == q.t.blocks) {
+        blk = 0;
+        do {
+          if (++req >= a.n) return false;   // never: the part would be longer than the line
+          load(a);
+        } while (__all_sync(0xffffffffu, q.r.rows == 0));
+      }
+      left = a.p.Hkv * q.t.per - 1;
+      item = 0;
+      open(a);
+    } else {
+      ++item;
+    }
+    t0 = 0;
+    t1 = uniform(to_go >= places ? places - kItemPlaces : line_tile(static_cast<int>(to_go)));
+    return true;
+  }
+};
+
+// A CTA has two slots for parts of items that others hold too, for its first and its last.  A slot: the
+// rows of two query tiles, 128 sums each, as [query tile][8 channels][row][8], so that the rows of a warp are written
+// side by side; the rows' (maximum, sum) behind all slots, and behind them what each CTA cuts.
+__device__ __forceinline__ float* part_sums(const ChunkArgs& a, int slot, int t, int row, int ch) {
+  const int64_t tile = static_cast<int64_t>(slot) * 2 + t;
+  return a.part + ((tile * (kD / 8) + ch / 8) * a.tile_rows + row) * 8 + ch % 8;
+}
+__device__ __forceinline__ float2* part_ml(const ChunkArgs& a, int slot, int t, int row) {
+  float2* ml = reinterpret_cast<float2*>(a.part + static_cast<int64_t>(a.ctas) * 4 * a.tile_rows * kD);
+  return ml + (static_cast<int64_t>(slot) * 2 + t) * a.tile_rows + row;
+}
+__device__ __forceinline__ Cut* part_cut(const ChunkArgs& a, int c) {
+  return reinterpret_cast<Cut*>(a.part + static_cast<int64_t>(a.ctas) * 4 * a.tile_rows * (kD + 2)) + c;
+}
+
+// Inclusive sum over the block; `sums` holds a value a warp.
+__device__ __forceinline__ int64_t scan_block(int64_t v, int64_t* sums, int64_t& total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();   // the last pass's sums have been read
+  if (lane == 31) sums[w] = v;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < kCaThreads / 32; ++i) {
+    const int64_t s = sums[i];
+    if (i < w) v += s;
+    total += s;
+  }
+  return v;
+}
+// The entry e of `n` with base[e] <= x < base[e + 1].
+template <typename T>
+__device__ __forceinline__ int find_entry(const T* base, int n, int64_t x) {
+  int lo = 0, hi = n;   // base[lo] <= x < base[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (base[mid] <= x)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// This CTA's part of the line, by all threads of it, for its first loading warp.  `scratch`: (n + 1) * 4 bytes for the blocks before each
+// request, and 8 bytes a block for the places before it.
+__device__ __forceinline__ Walk find_part(const ChunkArgs& a, uint8_t* scratch, int64_t* sums) {
+  const int tid = threadIdx.x;
+  int64_t* place = reinterpret_cast<int64_t*>(scratch);
+  int32_t* blocks = reinterpret_cast<int32_t*>(place + a.rows / kCaRows + a.n + 2);   // a request has a block more than rows / 128 at most
+  int64_t done = 0, total;
+  for (int i0 = 0; i0 < a.n; i0 += kCaThreads) {
+    const int i = i0 + tid;
+    int64_t v = 0;
+    if (i < a.n) {
+      const int rows = max(request_row(a, i + 1) - request_row(a, i), 0);
+      v = row_tiles_of(rows, a.rep).blocks;
+    }
+    v = scan_block(v, sums, total);
+    if (i < a.n) blocks[i + 1] = static_cast<int32_t>(done + v);
+    done += total;
+  }
+  if (tid == 0) blocks[0] = 0;
+  __syncthreads();
+  // requests whose rows overlap (row_start does not ascend) could have more blocks than there is room for
+  const int entries = static_cast<int>(min(done, static_cast<int64_t>(a.rows / kCaRows + a.n + 1)));
+  done = 0;
+  for (int e0 = 0; e0 < entries; e0 += kCaThreads) {
+    const int e = e0 + tid;
+    int64_t v = 0;
+    if (e < entries) {
+      const int i = find_entry(blocks, a.n, e);
+      const Request q = request_of(a, i);
+      v = static_cast<int64_t>(chunk_places(q.t, q.r, a.qb.window, a.qb.sinks, e - blocks[i])) * a.p.Hkv * q.t.per;
+    }
+    v = scan_block(v, sums, total);
+    if (e < entries) place[e + 1] = done + v;
+    done += total;
+  }
+  if (tid == 0) place[0] = 0;
+  __syncthreads();
+  Walk w;
+  w.idle = true;
+  if (tid / 32 != kCaLoadWarp) return w;
+  const int workers = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(a.ctas), done / 2))), c = blockIdx.x;
+  Cut cut = {};
+  cut.last = -1;
+  if (c < workers && done > 0) {
+    int64_t x = split_begin(done, workers, c), y = split_begin(done, workers, c + 1);
+    const int e = find_entry(place, entries, x);
+    w.req = uniform(find_entry(blocks, a.n, e));
+    w.blk = uniform(e - blocks[w.req]);
+    w.load(a);
+    w.open(a);
+    const int in = static_cast<int>((x - place[e]) % w.places);
+    w.item = uniform(static_cast<int>((x - place[e]) / w.places));
+    w.left = a.p.Hkv * w.q.t.per - 1 - w.item;
+    w.t0 = uniform(line_tile(in));
+    if (w.t0 == 0) x -= in;            // a boundary among an item's first places is its begin
+    const int64_t begin = x - (w.t0 == 0 ? 0 : in);
+    if (y < done) {
+      const int f = find_entry(place, entries, y), i = find_entry(blocks, a.n, f);
+      const Request q = request_of(a, i);
+      const int blk = f - blocks[i], places = chunk_places(q.t, q.r, a.qb.window, a.qb.sinks, blk);
+      const int item = static_cast<int>((y - place[f]) / places);
+      const int64_t b = place[f] + static_cast<int64_t>(item) * places;
+      if (line_tile(static_cast<int>(y - b)) == 0) {
+        y = b;
+      } else if (b >= x) {   // begun here, and goes on in later CTAs
+        const Work k = work_of(a, q, blk, item, 0, places);
+        cut.last = split_owner(done, workers, b + places - 1);
+        cut.before = b > x;
+        cut.row0 = q.row0;
+        cut.rows = q.r.rows;
+        cut.tb = q.t.tb;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          cut.q0[t] = k.q0[t];
+          cut.head[t] = k.head[t];
+          cut.heads[t] = t < k.nt ? k.heads[t] : 0;
+        }
+      }
+    }
+    w.idle = x >= y;
+    w.to_go = y - begin;
+    w.t1 = uniform(w.to_go >= w.places ? w.places - kItemPlaces : line_tile(static_cast<int>(w.to_go)));
+  }
+  if ((tid & 31) == 0) *part_cut(a, c) = cut;
+  return w;
+}
+
+// Rows of a tile into shared memory by one of the loading warps: rows r0 .. r0 + 63 of it, lane l holding the
+// addresses of rows r0 + l and r0 + 32 + l (null: zeros).
+__device__ __forceinline__ void copy_rows(uint32_t dst, int r0, const uint8_t* src0, const uint8_t* src1, const uint8_t* any) {
+  const int lane = threadIdx.x & 31, piece = lane & 15;
+#pragma unroll 8
+  for (int j = 0; j < 32; ++j) {   // two rows an instruction
+    const int e = 2 * (j & 15) + (lane >> 4), r = r0 + (j >> 4) * 32 + e;
+    const uint64_t src = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(j < 16 ? src0 : src1), e);
+    cp_async16(dst + (piece >> 3) * tc::kKBlock + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
+               src ? reinterpret_cast<const uint8_t*>(src) + piece * 16 : any, src != 0);
+  }
+}
+
+// Copies of a loading warp that are under way, oldest first: the barriers that wait for them.
+struct Flight {
+  uint32_t a = 0, b = 0;
+  __device__ __forceinline__ static void land(uint32_t bar) {
+    tc::fence_proxy_async();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+  }
+  __device__ __forceinline__ void push(uint32_t bar) {   // copies have been started
+    cp_async_commit();
+    if (a) {
+      cp_async_wait<2>();
+      land(a);
+    }
+    a = b;
+    b = bar;
+  }
+  __device__ __forceinline__ void flush() {
+    cp_async_wait<0>();
+    if (a) land(a);
+    if (b) land(b);
+    a = b = 0;
+  }
+};
+
+// The value s * code + z of 16 codes as two fp16 numbers each, hi and what is left.
+__device__ __forceinline__ void split16(const uint4& c, __half2 m, uint32_t (&hi)[8], uint32_t (&lo)[8]) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  const float s = __low2float(m), z = __high2float(m);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    // a code as the last bits of 2^23 + code; s * code is exact
+    const float x0 = __uint_as_float(__byte_perm(w[e >> 1], 0x4B000000u, 0x7440u + 2 * (e & 1))) - 8388608.f;
+    const float x1 = __uint_as_float(__byte_perm(w[e >> 1], 0x4B000000u, 0x7441u + 2 * (e & 1))) - 8388608.f;
+    const float f0 = fmaf(s, x0, z), f1 = fmaf(s, x1, z);
+    // (the largest values may lie a little above fp16's largest number: held there, the rest is in the second)
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;\n" : "=r"(hi[e]) : "f"(f1), "f"(f0));
+    const __half2 h = *reinterpret_cast<const __half2*>(&hi[e]);
+    lo[e] = pack2<false>(f0 - __low2float(h), f1 - __high2float(h));
+  }
+}
+// Rows r0 .. r0 + 63 of an INT8 tile into its two buffers; lane l holds the pool rows of rows r0 + l and r0 + 32 + l.
+__device__ __forceinline__ void convert_rows(const uint32_t (&dst)[2], int r0, const uint8_t* codes, const uint8_t* meta, uint32_t at0,
+                                             uint32_t at1) {
+  const int lane = threadIdx.x & 31, piece = lane & 7;
+#pragma unroll 1
+  for (int j0 = 0; j0 < 16; j0 += 4) {   // four rows an instruction
+    uint4 c[4];
+    __half2 m[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = 4 * ((j0 + j) & 7) + (lane >> 3);
+      const uint32_t row = __shfl_sync(0xffffffffu, j0 < 8 ? at0 : at1, e);
+      c[j] = make_uint4(0, 0, 0, 0);
+      m[j] = __float2half2_rn(0.f);
+      if (row != kNoRow) {
+        c[j] = *reinterpret_cast<const uint4*>(codes + static_cast<size_t>(row) * kD + piece * 16);
+        m[j] = reinterpret_cast<const __half2*>(meta + static_cast<size_t>(row) * kMetaBytes)[piece >> 2];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = r0 + 4 * (j0 + j) + (lane >> 3);
+      uint32_t x[2][8];
+      split16(c[j], m[j], x[0], x[1]);
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {   // channels 16 piece + 8 half ..
+          const int ch = (piece & 3) * 2 + half;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(dst[part] + (piece >> 2) * tc::kKBlock + r * 128 + ((ch ^ (r & 7)) << 4)),
+                       "r"(x[part][4 * half]), "r"(x[part][4 * half + 1]), "r"(x[part][4 * half + 2]), "r"(x[part][4 * half + 3])
+                       : "memory");
+        }
+    }
+  }
 }
 
 template <int TYPE>
-__global__ void __launch_bounds__(kCaThreads) chunk_rows_kernel(const ChunkArgs a) {
-  __shared__ float s_q[kD], s_o[kCaWarps][kD], s_m[kCaWarps], s_l[kCaWarps];
-  const int r = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  int lo = 0, hi = a.n;
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (a.row_start[mid + 1] > r)
-      hi = mid;
-    else
-      lo = mid + 1;
-  }
-  if (lo >= a.n || a.row_start[lo] > r) return;
-  const int first = max(a.row_start[lo], 0), count = min(a.row_start[lo + 1], a.rows) - first;
-  const int32_t s = a.seqs ? a.seqs[lo] : lo;
-  int64_t pos = -1;
-  int32_t len = 0;
-  if (static_cast<uint32_t>(s) < static_cast<uint32_t>(a.p.max_seqs)) {
-    len = a.p.len_of(s);
-    const int32_t from = a.start ? a.start[lo] : len - count;
-    if (!a.start || from >= 0) pos = static_cast<int64_t>(from) + (r - first);
-  }
-  const int end = static_cast<int>(min(pos + 1, static_cast<int64_t>(len)));
-  const uint16_t x = reinterpret_cast<const uint16_t*>(a.q.row(0, h, r))[tid];
-  s_q[tid] = TYPE == MIKV_PAGES_BF16 ? __uint_as_float(static_cast<uint32_t>(x) << 16) : __half2float(__ushort_as_half(x));
-  __syncthreads();
-  const size_t layer0 = a.p.layer_rows() * a.layer;
-  float m = -INFINITY, l = 0.f, o[4] = {};
-  for (int j0 = w * 32; j0 < end; j0 += kCaThreads) {
-    const int j = j0 + lane;
-    const bool seen = j < end && (a.window == 0 || j > pos - a.window || j < a.sinks);
-    uint32_t row = kNoRow;
-    if (seen) {
-      const uint32_t pg = div_of(j, a.p.ps);
-      row = pool_row(a.p.table[static_cast<size_t>(s) * a.p.max_pages + pg], a.p.n_pages, a.p.Hkv, h / a.rep, a.p.ps.d, j - pg * a.p.ps.d);
-      if (row == kNoRow) tc::report_giveup(tc::kBadPage);
+__global__ void __launch_bounds__(kCaThreads, 1) chunk_attention_kernel(const ChunkArgs a) {
+  constexpr bool BF = TYPE == MIKV_PAGES_BF16, Q8 = TYPE == MIKV_PAGES_INT8;
+  constexpr int kParts = Q8 ? 2 : 1;   // buffers of a tile of keys, or of values
+  extern __shared__ uint8_t smem[];
+  __shared__ CaBars bar;
+  __shared__ Work works[kCaTold];
+  __shared__ int64_t sums[kCaThreads / 32];
+  __shared__ uint32_t tslot;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kCaRing; ++i) {
+      tc::mbar_init(smem_u32(&bar.full[i]), kCaLoaders);
+      tc::mbar_init(smem_u32(&bar.empty[i]), 2);
     }
-    float d = -INFINITY;
-    if (row != kNoRow) {
-      d = 0.f;
-      for (int c = 0; c < kD; ++c) d += s_q[c] * elem<TYPE>(a.p.k, a.p.km, layer0 + row, c);
-      d *= a.scale;
+    for (int i = 0; i < kCaTold; ++i) {
+      tc::mbar_init(smem_u32(&bar.told[i]), 1);
+      tc::mbar_init(smem_u32(&bar.heard[i]), kCaThreads / 32 - 1);
     }
-    float mx = d;
+    tc::mbar_init(smem_u32(&bar.q), kCaLoaders);
+    tc::mbar_init(smem_u32(&bar.qfree), 2);
+    for (int t = 0; t < 2; ++t) {
+      tc::mbar_init(smem_u32(&bar.turn[t]), 1);
+      tc::mbar_init(smem_u32(&bar.s[t]), 1);
+      tc::mbar_init(smem_u32(&bar.p[t][0]), 4);
+      tc::mbar_init(smem_u32(&bar.p[t][1]), 4);
+      tc::mbar_init(smem_u32(&bar.o[t]), 1);
+    }
+    tc::mbar_init_fence();
+  }
+  if (warp == kCaMmaWarp) tc::tmem_alloc(smem_u32(&tslot), kCaCols);
+  const uint32_t sq = tc::smem_base(smem), ring = sq + 2 * tc::kTileBytes;
+  Walk walk = find_part(a, smem + (sq - smem_u32(smem)), sums);
+  tc::fence_before_sync();
+  __syncthreads();     // the sums have been read: the tiles may be written over them
+  tc::fence_after_sync();
+  const uint32_t tmem = uniform(tslot);
+  pdl_trigger();       // the joining kernel may be placed; it waits for this one's end
+  tc::Waits wait;
+  // Item n, as the first loading warp tells it; null behind the last one, or where a wait gave up.
+  const auto hear = [&](int n) -> const Work* {
+    wait(smem_u32(&bar.told[n % kCaTold]), (n / kCaTold) & 1);
+    const Work* w = &works[n % kCaTold];
+    return __all_sync(0xffffffffu, wait.ok) && uniform(w->nt) >= 0 ? w : nullptr;
+  };
+  const auto heard = [&](int n) {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(smem_u32(&bar.heard[n % kCaTold]));
+  };
+
+  if (warp >= kCaLoadWarp) {
+    const bool walks = warp == kCaLoadWarp;
+    const int r0 = (warp - kCaLoadWarp) * (kCaRows / kCaLoaders);
+    const size_t layer0 = a.p.layer_rows() * a.layer;
+    const uint8_t* k0 = a.p.k + layer0 * (Q8 ? kD : kD * 2);
+    const uint8_t* v0 = a.p.v + layer0 * (Q8 ? kD : kD * 2);
+    int slot = 0, par = 1, qs = 0;   // ring position; parity that an empty buffer shows; query loads
+    bool some = !walk.idle;
+    Flight flight;
+    for (int n = 0;; ++n) {
+      if (walks) {
+        // Only copies of the last item are under way here, so that whoever is behind can go on.
+        if (n >= kCaTold) wait(smem_u32(&bar.heard[n % kCaTold]), (n / kCaTold - 1) & 1);
+        Work next;
+        if (some) next = walk.work(a);
+        if (lane == 0) {
+          if (some)
+            works[n % kCaTold] = next;
+          else
+            works[n % kCaTold].nt = -1;
+          tc::mbar_arrive(smem_u32(&bar.told[n % kCaTold]));
+        }
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, some && wait.ok)) break;
+      }
+      const Work* told = walks ? &works[n % kCaTold] : hear(n);
+      if (!told) break;
+      const Work& w = *told;
+      const int begin = uniform(w.begin), end = uniform(w.end);
+      if (begin < end) {
+        const int32_t* table = a.p.table + static_cast<size_t>(uniform(w.seq)) * a.p.max_pages;
+        const int hk = uniform(w.head[0] / a.rep), keys = uniform(w.keys);
+        // the pool row of slot j, kNoRow for one that no row of the item sees
+        const int first = uniform(a.qb.window > 0 ? max(w.pa[0] - a.qb.window + 1, 0) : 0);
+        const auto place = [&](int i, int r) {
+          const int j = w.j0(i) + r;
+          uint32_t row = kNoRow;
+          if (i < end && j < keys && (j >= first || j < a.qb.sinks)) {
+            const uint32_t pg = div_of(static_cast<uint32_t>(j), a.p.ps);
+            row = pool_row(__ldg(table + pg), a.p.n_pages, a.p.Hkv, hk, a.p.ps.d, j - pg * a.p.ps.d);
+            if (row == kNoRow) tc::report_giveup(tc::kBadPage);
+          }
+          return row;
+        };
+        uint32_t at0 = place(begin, r0 + lane), at1 = place(begin, r0 + 32 + lane);
+        for (int i = begin; i < end; ++i) {
+          const uint32_t next0 = place(i + 1, r0 + lane), next1 = place(i + 1, r0 + 32 + lane);   // looked up ahead
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint8_t* x = kv ? v0 : k0;
+            uint32_t dst[kParts], full[kParts];
 #pragma unroll
-    for (int e = 16; e; e >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, e));
-    const float mn = fmaxf(m, mx);
-    if (mn == -INFINITY) continue;
-    const float f = exp2f(m - mn), p = exp2f(d - mn);
+            for (int part = 0; part < kParts; ++part) {
+              wait(smem_u32(&bar.empty[slot]), par);
+              dst[part] = ring + slot * tc::kTileBytes;
+              full[part] = smem_u32(&bar.full[slot]);
+              if (++slot == kCaRing) {
+                slot = 0;
+                par ^= 1;
+              }
+            }
+            if (__all_sync(0xffffffffu, wait.ok)) {
+              if constexpr (Q8) {
+                convert_rows(dst, r0, x, (kv ? a.p.vm : a.p.km) + layer0 * kMetaBytes, at0, at1);
+                Flight::land(full[0]);
+                Flight::land(full[1]);
+              } else {
+                copy_rows(dst[0], r0, at0 == kNoRow ? nullptr : x + static_cast<size_t>(at0) * (kD * 2),
+                          at1 == kNoRow ? nullptr : x + static_cast<size_t>(at1) * (kD * 2), k0);
+                flight.push(full[0]);
+              }
+            }
+          }
+          if (i == begin) {   // the queries behind the first tile: the last item's products still read theirs
+            if (qs > 0) {
+              flight.flush();
+              wait(smem_u32(&bar.qfree), (qs - 1) & 1);
+            }
+            ++qs;
+            if (__all_sync(0xffffffffu, wait.ok)) {
+              for (int t = 0; t < w.nt; ++t) {
+                const uint8_t* src[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int r = r0 + e * 32 + lane, sub = r / w.tb, q = w.q0[t] + r - sub * w.tb;
+                  src[e] = sub < w.heads[t] && q < w.rows ? a.q.row(0, w.head[t] + sub, w.row0 + q) : nullptr;
+                }
+                copy_rows(sq + t * tc::kTileBytes, r0, src[0], src[1], a.q.p);
+              }
+              flight.push(smem_u32(&bar.q));
+              if (Q8) flight.flush();
+            }
+          }
+          at0 = next0;
+          at1 = next1;
+        }
+      } else {
+        flight.flush();
+      }
+      if (walks)
+        some = walk.next(a, wait.ok);
+      else
+        heard(n);
+    }
+    flight.flush();
+    // every buffer's release has arrived before the CTA ends
+    for (int c = 0; c < kCaRing; ++c) {
+      wait(smem_u32(&bar.empty[slot]), par);
+      if (++slot == kCaRing) {
+        slot = 0;
+        par ^= 1;
+      }
+    }
+    if (qs > 0) wait(smem_u32(&bar.qfree), (qs - 1) & 1);
+  } else if (warp >= kCaMmaWarp) {
+    // One warp per query tile, so that neither waits in the other's place.  The whole warp walks
+    // the steps, so that addresses and descriptors stay uniform; one elected lane issues.
+    const int t = warp - kCaMmaWarp;
+    bool lead = elect_one();
+    constexpr uint32_t kType = BF ? (1u << 7) | (1u << 10) : 0u;
+    constexpr uint32_t kScores = tc::idesc_f16(kCaRows, kCaRows) | kType, kFew = tc::idesc_f16(kCaRows, kCaNarrow) | kType;
+    constexpr uint32_t kValues = tc::idesc_f16(kCaRows, kD) | kType | (1u << 16);   // B: rows along the contraction
+    const uint32_t ts = tmem + t * 128, to = tmem + kCaO + t * 128;
+    const uint64_t qd = tc::smem_desc(sq + t * tc::kTileBytes), k0 = tc::smem_desc(ring), v0 = value_desc(ring);
+    int p_par = 0, q_par = 0;        // parity of the next weights, and queries
+    int slot = 0, par = 0;           // ring position and parity
+    // The two warps issue in turns, one step each: the tiles then stay half a step apart, and one's
+    // weights are made while the tensor core works for the other.
+    int turn = t;   // tile 0 begins without waiting
+    const auto take_turn = [&] {
+      if (turn > 0) wait(smem_u32(&bar.turn[t]), (turn - 1) & 1);
+      ++turn;
+    };
+    for (int n = 0;; ++n) {
+      const Work* told = hear(n);
+      if (!told) break;
+      const Work& w = *told;
+      const int begin = uniform(w.begin), end = uniform(w.end);
+      if (begin < end) {
+        const int last = uniform(w.last[t]), from = uniform(w.from[t]), ns = uniform(w.ns), sinks = uniform(w.ts);
+        const auto narrow = [&](int i) { return tile_narrow(a, sinks, i, i * kCaRows); };
+        bool more = false, before = false, few = false;
+        int vslot = 0, vpar = 0;     // the last step's values
+        wait(smem_u32(&bar.q), q_par);
+        q_par ^= 1;
+        // after a wait that gave up no lane leads, nothing more is issued, and the others' waits run out
+        for (int i = begin; i <= end; ++i) {
+          // this step's scores from key tile i, behind the last step's sums over value tile i - 1
+          const bool keys = i < end, here = keys && i <= last && (i < ns || i >= from);
+          const uint64_t kd = k0 + slot * desc_step(tc::kTileBytes), vd = v0 + vslot * desc_step(tc::kTileBytes);
+#pragma unroll
+          for (int part = 0; part < kParts; ++part) {   // (parts of a tile lie side by side in the ring)
+            if (i > begin) wait(smem_u32(&bar.full[vslot + part]), vpar);
+            if (keys) wait(smem_u32(&bar.full[slot + part]), par);
+          }
+          if (before) wait(smem_u32(&bar.p[t][0]), p_par);
+          take_turn();
+          lead &= __all_sync(0xffffffffu, wait.ok) != 0;
+          tc::fence_after_sync();
+          if (before) {
+            const auto sums = [&](int c0, int c1) {
+#pragma unroll
+              for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                for (int c = c0; c < c1; ++c)
+                  mma_ts(to, ts + c * 8, vd + desc_step(part * tc::kTileBytes + c * 2048), kValues, more || c > 0 || part > 0);
+            };
+            // the tensor core's queue holds about two products: a wait between them leaves it idle
+            if (few) {
+              wait(smem_u32(&bar.p[t][1]), p_par);
+              lead &= __all_sync(0xffffffffu, wait.ok) != 0;
+              if (lead) sums(0, kCaNarrow / 16);
+            } else if (__all_sync(0xffffffffu, tc::mbar_wait(smem_u32(&bar.p[t][1]), p_par, 1))) {
+              tc::fence_after_sync();
+              if (lead) sums(0, kCaRows / 16);
+            } else {
+              if (lead) sums(0, kCaRows / 32);
+              wait(smem_u32(&bar.p[t][1]), p_par);
+              lead &= __all_sync(0xffffffffu, wait.ok) != 0;
+              tc::fence_after_sync();
+              if (lead) sums(kCaRows / 32, kCaRows / 16);
+            }
+            p_par ^= 1;
+            more = true;
+          }
+          const uint32_t scores = keys && narrow(i) ? kFew : kScores;
+          if (lead) {
+            if (before && i - 1 == last) tc::commit(smem_u32(&bar.o[t]));
+            // the turn passes on a little early: the other warp takes as long to wake as the
+            // last products take to issue
+            if (here) {
+#pragma unroll
+              for (int c = 0; c < kParts * kD / 16; ++c) {
+                const uint64_t off = desc_step(((c & 7) >> 2) * tc::kKBlock + (c & 3) * 32);
+                tc::mma_f16(ts, qd + off, kd + off + desc_step((c >> 3) * tc::kTileBytes), scores, c > 0);
+                if (c == kParts * kD / 16 - 4) tc::mbar_arrive(smem_u32(&bar.turn[t ^ 1]));
+              }
+              tc::commit(smem_u32(&bar.s[t]));
+            } else {
+              tc::mbar_arrive(smem_u32(&bar.turn[t ^ 1]));
+            }
+          }
+          before = here;
+          few = keys && narrow(i);
+          if (lead) {
+#pragma unroll
+            for (int part = 0; part < kParts; ++part) {
+              if (i > begin) tc::commit(smem_u32(&bar.empty[vslot + part]));
+              if (keys) tc::commit(smem_u32(&bar.empty[slot + part]));
+            }
+            if (i == end - 1) tc::commit(smem_u32(&bar.qfree));   // the last scores
+          }
+          if (keys) {   // the values of tile i follow its keys in the ring
+            vslot = slot + kParts == kCaRing ? 0 : slot + kParts;
+            vpar = vslot == 0 ? par ^ 1 : par;
+            slot = vslot + kParts == kCaRing ? 0 : vslot + kParts;
+            par = slot == 0 ? vpar ^ 1 : vpar;
+          }
+        }
+      }
+      heard(n);
+    }
+  } else {
+    const int t = warp >> 2, row = (warp & 3) * 32 + lane;   // the thread's TMEM lane is its row
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + kCaO + t * 128;
+    const uint32_t ready[2] = {smem_u32(&bar.p[t][0]), smem_u32(&bar.p[t][1])};
+    int s_par = 0, o_par = 0;
+    for (int n = 0;; ++n) {
+      const Work* told = hear(n);
+      if (!told) break;
+      const Work& w = *told;
+      if (t < w.nt) {
+        Row r;
+        {
+          const int p = w.pa[t] + row % w.tb, last = min(p, w.keys - 1);
+          for (int i = w.begin; i < w.end; ++i) {
+            if (!w.sees(t, i)) continue;
+            const int j0 = w.j0(i);
+            const bool whole = tile_whole(a, w.pa[t], w.pb[t], w.keys, j0), few = tile_narrow(a, w.ts, i, j0);
+            wait(smem_u32(&bar.s[t]), s_par);
+            s_par ^= 1;
+            tc::fence_after_sync();
+            if (few)
+              softmax_tile<BF, kCaNarrow>(a, ts, to, false, p, last, j0, r, ready);
+            else
+              softmax_tile<BF, kCaRows>(a, ts, to, whole, p, last, j0, r, ready);
+          }
+        }
+        const bool any = w.last[t] >= 0;
+        if (any) {
+          wait(smem_u32(&bar.o[t]), o_par);
+          o_par ^= 1;
+        }
+        tc::fence_after_sync();
+        const int sub = row / w.tb, q = w.q0[t] + row - sub * w.tb, head = w.head[t] + sub;   // the row's query and head
+        const bool write = sub < w.heads[t] && q < w.rows, part = !w.whole;
+        const int slot = 2 * blockIdx.x + (n > 0), at = w.row0 + q;
+        float inv = part ? 1.f : r.l == 0.f ? 0.f : 1.f / r.l;
+        if (!wait.ok) inv = __int_as_float(0x7fffffff);
+        uint8_t* dst = a.out.row(0, head, at);
+#pragma unroll 1
+        for (int c = 0; c < kD; c += 32) {
+          float o[32];
+          if (any) {
+            ld32(to + c, o);
+            wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
+          if (write) {
+            uint32_t u[32];
+            if (!part) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) u[e] = pack2<BF>(o[2 * e] * inv, o[2 * e + 1] * inv);
+              if (a.wide_out) {
+                st_global32(dst + c * 2, u);
+                st_global32(dst + c * 2 + 32, u + 8);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(dst + (c + 2 * e) * 2) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+              }
+            } else if (any) {   // a part without a visible key is told by its sum of 0
+#pragma unroll
+              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * inv);
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) st_global32(part_sums(a, slot, t, row, c + e), u + e);
+            }
+          }
+        }
+        if (part && write) {
+          *part_ml(a, slot, t, row) = make_float2(r.m * a.scale, wait.ok ? r.l : inv);
+        } else if (write && a.lse) {
+          const float v = r.l == 0.f ? -INFINITY : (r.m * a.scale + (log2f(r.l) - Weights<BF>::shift)) * 0.6931471805599453f;
+          a.lse[static_cast<int64_t>(at) * a.Hq + head] = wait.ok ? v : inv;
+        }
+        tc::fence_before_sync();   // the sums are read before the next item's products overwrite them
+      }
+      heard(n);
+    }
+  }
+  if (!wait.ok) tc::report_giveup(tc::kGiveupChunk);
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kCaMmaWarp) tc::tmem_dealloc(tmem, kCaCols);
+}
+
+// CTA (slice, c): joins kJoinRows rows of the item that CTA c has begun and not ended, in a fixed order.  A thread
+// takes 8 channels of a row (a part's rows lie side by side); kJoinGroups sets of threads share the parts,
+// kJoinBatch of them requested together.
+constexpr int kJoinRows = 8, kJoinGroups = 2, kJoinBatch = 4;
+template <bool BF>
+__global__ void __launch_bounds__(kJoinRows * (kD / 8) * kJoinGroups) chunk_join_kernel(const ChunkArgs a) {
+  constexpr int kThreads = kJoinRows * (kD / 8);   // of a group
+  __shared__ float s_o[kJoinGroups - 1][8][kThreads];
+  __shared__ float2 s_ml[kJoinGroups - 1][kThreads];
+  const int tid = threadIdx.x % kThreads, group = threadIdx.x / kThreads, c0 = blockIdx.y;
+  pdl_wait();
+  const Cut cut = *part_cut(a, c0);
+  const int c1 = cut.last;
+  if (c1 < 0) return;
+  const int ch = tid / kJoinRows * 8, i = blockIdx.x * kJoinRows + tid % kJoinRows, t = i >= a.tile_rows, row = i - t * a.tile_rows;
+  const int sub = row / cut.tb, q = (t ? cut.q0[1] : cut.q0[0]) + row - sub * cut.tb;
+  const bool live = i < 2 * a.tile_rows && sub < (t ? cut.heads[1] : cut.heads[0]) && q < cut.rows;
+  float m = -INFINITY, l = 0.f, o[8] = {};
+  const auto add = [&](float2 x, const float (&p)[8]) {
+    const float mn = fmaxf(m, x.x), ref = mn == -INFINITY ? 0.f : mn;
+    const float f = ex2(m - ref), fx = ex2(x.x - ref);
+    l = l * f + x.y * fx;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = o[e] * f + p[e] * fx;
     m = mn;
-    l = l * f + p;
+  };
+  if (live) {
+    for (int p0 = c0 + group; p0 <= c1; p0 += kJoinBatch * kJoinGroups) {
+      float2 x[kJoinBatch];
+      float4 v[kJoinBatch][2];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) o[c] *= f;
-    for (int e = 0; e < 32; ++e) {
-      const uint32_t re = __shfl_sync(0xffffffffu, row, e);
-      const float pe = __shfl_sync(0xffffffffu, p, e);
-      if (re == kNoRow) continue;
+      for (int e = 0; e < kJoinBatch; ++e) {
+        const int p = p0 + e * kJoinGroups, slot = 2 * p + (p == c0 ? cut.before : 0);
+        x[e] = make_float2(-INFINITY, 0.f);
+        v[e][0] = v[e][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p <= c1) {
+          const float4* sums = reinterpret_cast<const float4*>(part_sums(a, slot, t, row, ch));
+          x[e] = *part_ml(a, slot, t, row);
+          v[e][0] = sums[0];
+          v[e][1] = sums[1];
+        }
+      }
 #pragma unroll
-      for (int c = 0; c < 4; ++c) o[c] += pe * elem<TYPE>(a.p.v, a.p.vm, layer0 + re, lane * 4 + c);
+      for (int e = 0; e < kJoinBatch; ++e) {
+        // a sum of 0: nothing seen there, and no sums written
+        const bool none = x[e].y == 0.f;
+        const float w[8] = {none ? 0.f : v[e][0].x, none ? 0.f : v[e][0].y, none ? 0.f : v[e][0].z, none ? 0.f : v[e][0].w,
+                            none ? 0.f : v[e][1].x, none ? 0.f : v[e][1].y, none ? 0.f : v[e][1].z, none ? 0.f : v[e][1].w};
+        add(x[e], w);
+      }
     }
   }
+  if (kJoinGroups > 1) {
+    if (group > 0) {
 #pragma unroll
-  for (int e = 16; e; e >>= 1) l += __shfl_xor_sync(0xffffffffu, l, e);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) s_o[w][lane * 4 + c] = o[c];
-  if (lane == 0) {
-    s_m[w] = m;
-    s_l[w] = l;
-  }
-  __syncthreads();
-  float top = -INFINITY, sum = 0.f, v = 0.f;
-  for (int e = 0; e < kCaWarps; ++e) top = fmaxf(top, s_m[e]);
-  if (top != -INFINITY)
-    for (int e = 0; e < kCaWarps; ++e) {
-      const float f = exp2f(s_m[e] - top);
-      sum += s_l[e] * f;
-      v += s_o[e][tid] * f;
+      for (int e = 0; e < 8; ++e) s_o[group - 1][e][tid] = o[e];
+      s_ml[group - 1][tid] = make_float2(m, l);
     }
-  v = sum > 0.f ? v / sum : 0.f;
-  uint16_t* dst = reinterpret_cast<uint16_t*>(a.out.row(0, h, r));
-  dst[tid] = TYPE == MIKV_PAGES_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
-  if (tid == 0 && a.lse)
-    a.lse[static_cast<size_t>(r) * a.Hq + h] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 0; g < kJoinGroups - 1; ++g) {
+      float w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = s_o[g][e][tid];
+      add(s_ml[g][tid], w);
+    }
+  }
+  if (!live) return;
+  const int head = (t ? cut.head[1] : cut.head[0]) + sub, at = cut.row0 + q;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<uint4*>(a.out.row(0, head, at) + ch * 2) =
+      make_uint4(pack2<BF>(o[0] * inv, o[1] * inv), pack2<BF>(o[2] * inv, o[3] * inv), pack2<BF>(o[4] * inv, o[5] * inv),
+                 pack2<BF>(o[6] * inv, o[7] * inv));
+  if (ch == 0 && a.lse)
+    a.lse[static_cast<int64_t>(at) * a.Hq + head] = l == 0.f ? -INFINITY : (m + (log2f(l) - Weights<BF>::shift)) * 0.6931471805599453f;
+}
+
+int tile_rows_of(int rows, int rep) { return static_cast<int>(std::min<int64_t>(kCaRows, static_cast<int64_t>(rows) * rep)); }
+size_t part_bytes(int rows, int rep) {
+  return static_cast<size_t>(kNumSMs) * (static_cast<size_t>(4) * tile_rows_of(rows, rep) * (kD + 2) * 4 + sizeof(Cut));
+}
+bool sizes_ok(const mikv_pages* p, int n, int rows, int Hq) {
+  return n >= 0 && n <= kMaxRequests && rows >= 0 && rows <= kMaxChunkRows && Hq >= 1 && Hq % p->Hkv == 0 && Hq / p->Hkv <= 1024 &&
+         static_cast<int64_t>(p->max_pages) * p->page_size <= kMaxPos;
+}
+
+template <int TYPE>
+int launch(const ChunkArgs& a, cudaStream_t st) {
+  const auto kern = chunk_attention_kernel<TYPE>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCaSmem);
+  if (e != cudaSuccess) return check_launch_after(e, "chunk_attention_kernel");
+  kern<<<a.ctas, kCaThreads, kCaSmem, st>>>(a);
+  if (int r = check_launch("chunk_attention_kernel")) return r;
+  const dim3 joins((2 * a.tile_rows + kJoinRows - 1) / kJoinRows, a.ctas);
+  return check_launch_after(launch_after(chunk_join_kernel<TYPE == MIKV_PAGES_BF16>, joins, dim3(kJoinRows * (kD / 8) * kJoinGroups), 0, st, a),
+                            "chunk_join_kernel");
 }
 
 }  // namespace
@@ -129,8 +893,8 @@ using namespace mikv;
 
 extern "C" size_t mikv_chunk_attention_workspace_bytes(const mikv_pages* p, int n, int rows, int Hq) {
   Pool pool;
-  if (check_pages(p, "chunk_attention", &pool) || n < 1 || n > 4096 || rows < 1 || Hq < 1 || Hq % p->Hkv) return 0;
-  return 16;
+  if (check_pages(p, "chunk_attention", &pool) || n < 1 || rows < 1 || !sizes_ok(p, n, rows, Hq)) return 0;
+  return part_bytes(rows, Hq / p->Hkv);
 }
 
 extern "C" int mikv_chunk_attention(const mikv_rows* q, const mikv_pages* pages, int layer, const int32_t* seqs, const int32_t* start,
@@ -140,23 +904,26 @@ extern "C" int mikv_chunk_attention(const mikv_rows* q, const mikv_pages* pages,
   ChunkArgs a;
   if (int e = check_pages(pages, "chunk_attention", &a.p)) return e;
   if (layer < 0 || layer >= a.p.layers) return fail(MIKV_ESHAPE, "chunk_attention: layer=%d of %d", layer, a.p.layers);
-  if (n < 0 || n > 4096 || rows < 0 || (!seqs && n > a.p.max_seqs)) return fail(MIKV_ESHAPE, "chunk_attention: n=%d rows=%d", n, rows);
-  if (Hq < 1 || Hq % a.p.Hkv || Hq / a.p.Hkv > 1024) return fail(MIKV_ESHAPE, "chunk_attention: Hq=%d Hkv=%d", Hq, a.p.Hkv);
+  if (!sizes_ok(pages, n, rows, Hq) || (!seqs && n > a.p.max_seqs))
+    return fail(MIKV_ESHAPE, "chunk_attention: n=%d rows=%d Hq=%d Hkv=%d max_pages=%d page_size=%d", n, rows, Hq, a.p.Hkv, a.p.max_pages,
+                pages->page_size);
   if (window < 0 || sinks < 0) return fail(MIKV_EINVAL, "chunk_attention: window=%d sinks=%d", window, sinks);
   if (n == 0 || rows == 0) return MIKV_OK;
   if (int e = check_rows(q, "chunk_attention", "q")) return e;
   if (int e = check_rows(out, "chunk_attention", "out")) return e;
-  const int64_t st = out->stride_t, sh = out->stride_h;   // rows apart: the heads of a row side by side, or the rows of a head
-  if ((Hq == 1 || st < (Hq - 1) * sh + kD || sh < kD) && (rows == 1 || sh < (rows - 1) * st + kD || st < kD) &&
-      !(Hq == 1 && (rows == 1 || st >= kD)) && !(rows == 1 && sh >= kD))
-    return fail(MIKV_EINVAL, "chunk_attention: rows of out overlap");
+  const int64_t st = out->stride_t, sh = out->stride_h;   // apart: the heads of a row side by side, or the rows of a head
+  const bool heads_in = (Hq == 1 || sh >= kD) && (rows == 1 || st >= (Hq - 1) * sh + kD);
+  const bool rows_in = (rows == 1 || st >= kD) && (Hq == 1 || sh >= (rows - 1) * st + kD);
+  if (!heads_in && !rows_in) return fail(MIKV_EINVAL, "chunk_attention: rows of out overlap");
   if (!row_start || !ws) return fail(MIKV_EINVAL, "chunk_attention: null pointer");
   if (reinterpret_cast<uintptr_t>(ws) & 31u) return fail(MIKV_EALIGN, "chunk_attention: workspace must be 32-byte aligned");
-  const size_t need = mikv_chunk_attention_workspace_bytes(pages, n, rows, Hq);
+  a.rep = Hq / a.p.Hkv;
+  const size_t need = part_bytes(rows, a.rep);
   if (ws_bytes < need) return fail(MIKV_ESHAPE, "chunk_attention: workspace %zu < %zu", ws_bytes, need);
   a.q = row_view(*q);
   a.out = row_view(*out);
   a.lse = lse;
+  a.part = static_cast<float*>(ws);
   a.seqs = seqs;
   a.start = start;
   a.row_start = row_start;
@@ -164,13 +931,15 @@ extern "C" int mikv_chunk_attention(const mikv_rows* q, const mikv_pages* pages,
   a.n = n;
   a.rows = rows;
   a.Hq = Hq;
-  a.rep = Hq / a.p.Hkv;
-  a.window = window;
-  a.sinks = sinks;
+  a.ctas = kNumSMs;
+  a.tile_rows = tile_rows_of(rows, a.rep);
+  a.qb.window = window > kMaxPos ? 0 : window;   // one that reaches every key is none
+  a.qb.sinks = std::min(sinks, kMaxPos);
+  a.wide_out = ((reinterpret_cast<uintptr_t>(out->data) | static_cast<uintptr_t>(a.out.sh | a.out.st)) & 31u) == 0;
   a.scale = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
-  const auto kern = a.p.type == MIKV_PAGES_INT8   ? chunk_rows_kernel<MIKV_PAGES_INT8>
-                    : a.p.type == MIKV_PAGES_BF16 ? chunk_rows_kernel<MIKV_PAGES_BF16>
-                                                  : chunk_rows_kernel<MIKV_PAGES_FP16>;
-  kern<<<dim3(rows, Hq), kCaThreads, 0, as_stream(stream)>>>(a);
-  return check_launch("chunk_rows_kernel");
+  switch (a.p.type) {
+    case MIKV_PAGES_FP16: return launch<MIKV_PAGES_FP16>(a, as_stream(stream));
+    case MIKV_PAGES_BF16: return launch<MIKV_PAGES_BF16>(a, as_stream(stream));
+    default: return launch<MIKV_PAGES_INT8>(a, as_stream(stream));
+  }
 }

@@ -1,0 +1,68 @@
+// Index arithmetic of the attention of packed rows, plain C++ for host and device (internal; not part
+// of the C ABI): how the rows of a request form tiles, which key tiles a block of them sees, and the
+// line that all key tiles of a call form.
+//
+// A request of c rows over a group of rep query heads: a tile has 128 rows of one head or, where the
+// request has 64 rows or fewer, all its rows of several heads.  A block is what a pair of tiles covers:
+// the same rows of two tiles' heads, or two tiles' rows of one head where the group's tiles are odd.
+#pragma once
+
+#include "window_index.h"
+
+namespace mikv {
+
+struct RowTiles {
+  int32_t tb, hb;       // rows of a tile, and heads
+  int32_t groups;       // tiles side by side in a group of query heads
+  int32_t blocks, per;  // blocks of rows, and pairs of tiles of one block and key head
+  bool pair_heads;
+};
+MIKV_HD RowTiles row_tiles_of(int32_t rows, int32_t rep) {
+  RowTiles t;
+  t.hb = rows <= kKeyRows / 2 ? min_of(rep, kKeyRows / max_of(rows, 1)) : 1;
+  t.tb = t.hb > 1 ? max_of(rows, 1) : kKeyRows;
+  t.groups = (rep + t.hb - 1) / t.hb;
+  const int32_t tiles = (rows + t.tb - 1) / t.tb;
+  t.pair_heads = t.groups % 2 == 0 || tiles <= 1;
+  t.blocks = t.pair_heads ? tiles : (tiles + 1) / 2;
+  t.per = t.pair_heads ? (t.groups + 1) / 2 : t.groups;
+  return t;
+}
+MIKV_HD int32_t block_row(const RowTiles& t, int32_t blk) { return (t.pair_heads ? blk : 2 * blk) * t.tb; }
+
+// A request's rows: `rows` of them, the first at position `off` (below 0: it sees nothing), over `keys` keys.
+struct Rows {
+  int32_t rows, off, keys;
+};
+constexpr int32_t kMaxPos = 1 << 30;   // positions of a request's first row are held here, and slots lie below
+// `held`: slots of its sequence.  A request that is refused has none.
+MIKV_HD Rows rows_of(int32_t rows, int32_t held, bool from_start, int32_t start) {
+  Rows r;
+  r.rows = rows;
+  r.off = from_start ? min_of(start, kMaxPos) : held - rows;
+  // keys that its last row sees: below 2^30 + 2^20
+  r.keys = (from_start && start < 0) || held <= 0 ? 0 : max_of(0, min_of(held, r.off + rows));
+  return r;
+}
+
+// The key tiles that the rows of a block see, as KeyTiles says.
+MIKV_HD KeyTiles chunk_tiles(const RowTiles& t, const Rows& r, int32_t window, int32_t sinks, int32_t blk) {
+  const int32_t q0 = block_row(t, blk);
+  const int32_t p1 = r.off + min_of(q0 + (t.pair_heads ? t.tb : 2 * t.tb), r.rows) - 1;   // the largest position
+  const int32_t last = min_of(p1, r.keys - 1);
+  const int32_t lo = window > 0 ? max_of(r.off + q0 - window + 1, 0) : 0;
+  const int32_t end = last < 0 ? 0 : last / kKeyRows + 1;
+  const int32_t st = window > 0 && sinks > 0 ? (min_of(sinks, max_of(r.keys, 1)) - 1) / kKeyRows + 1 : 0;
+  KeyTiles k;
+  k.tw0 = min_of(lo / kKeyRows, end);
+  k.ts = min_of(st, k.tw0);
+  k.tiles = k.ts + end - k.tw0;
+  k.ns = max_of(k.ts, min_of(st, st > k.tw0 ? k.tiles : k.ts));
+  return k;
+}
+// Places of each item of a block on the line.
+MIKV_HD int32_t chunk_places(const RowTiles& t, const Rows& r, int32_t window, int32_t sinks, int32_t blk) {
+  return kItemPlaces + max_of(1, chunk_tiles(t, r, window, sinks, blk).tiles);
+}
+
+}  // namespace mikv

@@ -87,6 +87,7 @@ constexpr unsigned kGiveupVwo = 4u;      // K6, vwo_norm_tc_kernel
 constexpr unsigned kGiveupPerturb = 8u;  // K9, perturb_tc_kernel
 constexpr unsigned kGiveupProbe = 16u;   // wait_probe_kernel (mikv_wait_probe)
 constexpr unsigned kGiveupWindow = 32u;  // window_attention_kernel
+constexpr unsigned kGiveupChunk = 256u;  // chunk_attention_kernel
 constexpr unsigned kBadPage = 64u;       // no wait: a paged kernel met a table entry outside the pool
 constexpr unsigned kSharedPage = 128u;   // no wait: an append met a page that several sequences own
 
