@@ -15,10 +15,11 @@
 // call form one line, of which each CTA takes an equal part; a CTA finds its part in sums over the
 // requests, which all of its threads make before it begins.  Items that are cut are joined by a second kernel.
 //
-// Two warps bring keys and values from the pages to a ring of four 32 KB buffers (128-byte swizzle), row by
-// row: a page has any number of rows, and a tile begins and ends inside pages.  Rows that no query of
-// the item sees are zeros there, so that they may hold anything.  The first of the two walks the line,
-// and tells the other warps what each item is.
+// Four warps bring keys and values from the pages to a ring of four 32 KB buffers (128-byte swizzle), row by
+// row: a page has any number of rows, and a tile begins and ends inside pages.  Each has a buffer of its own,
+// and says so when it has landed (two warps that shared every buffer, and signalled one while they started the
+// next but one, took 781 us for 8192 causal rows of 32 heads).  Rows that no query of the item sees are zeros
+// there, so that they may hold anything.  One more warp walks the line, and tells the others what each item is.
 //
 // INT8 pages: s * code + z is held as two fp16 numbers, the nearest one and what is left (22 bits), and each
 // product is two: keys rounded to fp16 alone put 1e-4 into lse and half as much again into the outputs.
@@ -38,8 +39,11 @@ using namespace at;
 constexpr int kCaRows = kKeyRows;
 constexpr int kCaNarrow = 32;               // columns of a tile that holds the last few sinks
 constexpr int kCaRing = 4;
-constexpr int kCaThreads = 384;             // 2 x 4 softmax warps, 2 MMA warps, 2 loading warps
-constexpr int kCaMmaWarp = 8, kCaLoadWarp = 10, kCaLoaders = 2;
+constexpr int kCaThreads = 512;             // 2 x 4 softmax warps, 4 loading warps, 2 MMA warps, the walking warp, an idle one
+constexpr int kCaLoadWarp = 8, kCaLoaders = 4, kCaMmaWarp = 12, kCaWalkWarp = 14;
+// Registers of a thread, by warpgroups; 128 each at launch, 65,536 in all.
+constexpr int kCaSoftmaxRegs = 176, kCaLoadRegs = 88, kCaMmaRegs = 72;
+static_assert(256 * kCaSoftmaxRegs + 128 * (kCaLoadRegs + kCaMmaRegs) == kCaThreads * 128, "register split");
 constexpr int kCaTold = 4;                  // items that the other warps may be behind
 constexpr int kCaSmem = (2 + kCaRing) * tc::kTileBytes + 1024;
 constexpr uint32_t kCaCols = 512;           // S_0, S_1, O_0, O_1: 128 columns each
@@ -97,7 +101,7 @@ struct Cut {
   int pad;
 };
 
-// What one CTA works on, in shared memory: written by the first loading warp, read by the others.
+// What one CTA works on, in shared memory: written by the walking warp, read by the others.
 struct Work {
   int head[2], heads[2], q0[2];   // per tile: first head of q, heads of it that count; first row of the request
   int pa[2], pb[2];       // positions of its first and last row
@@ -157,7 +161,7 @@ __device__ __forceinline__ bool tile_whole(const ChunkArgs& a, int pa, int pb, i
 // Whether key tile i, at j0, counts with its first kCaNarrow columns alone: the sinks' last tile, mostly.
 __device__ __forceinline__ bool tile_narrow(const ChunkArgs& a, int ts, int i, int j0) { return i < ts && a.qb.sinks - j0 <= kCaNarrow; }
 
-// A CTA's part of the line, walked by its first loading warp.
+// A CTA's part of the line, walked by one warp of it.
 struct Walk {
   int req, blk, item;    // the item
   int places, t0, t1;    // its places, and its key tiles of this part
@@ -251,7 +255,7 @@ __device__ __forceinline__ int find_entry(const T* base, int n, int64_t x) {
   return lo;
 }
 
-// This CTA's part of the line, by all threads of it, for its first loading warp.  `scratch`: (n + 1) * 4 bytes for the blocks before each
+// This CTA's part of the line, by all threads of it, for its walking warp.  `scratch`: (n + 1) * 4 bytes for the blocks before each
 // request, and 8 bytes a block for the places before it.
 __device__ __forceinline__ Walk find_part(const ChunkArgs& a, uint8_t* scratch, int64_t* sums) {
   const int tid = threadIdx.x;
@@ -290,7 +294,7 @@ __device__ __forceinline__ Walk find_part(const ChunkArgs& a, uint8_t* scratch, 
   __syncthreads();
   Walk w;
   w.idle = true;
-  if (tid / 32 != kCaLoadWarp) return w;
+  if (tid / 32 != kCaWalkWarp) return w;
   const int workers = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(a.ctas), done / 2))), c = blockIdx.x;
   Cut cut = {};
   cut.last = -1;
@@ -338,43 +342,43 @@ __device__ __forceinline__ Walk find_part(const ChunkArgs& a, uint8_t* scratch, 
   return w;
 }
 
-// Rows of a tile into shared memory by one of the loading warps: rows r0 .. r0 + 63 of it, lane l holding the
-// addresses of rows r0 + l and r0 + 32 + l (null: zeros).
-__device__ __forceinline__ void copy_rows(uint32_t dst, int r0, const uint8_t* src0, const uint8_t* src1, const uint8_t* any) {
-  const int lane = threadIdx.x & 31, piece = lane & 15;
-#pragma unroll 8
-  for (int j = 0; j < 32; ++j) {   // two rows an instruction
-    const int e = 2 * (j & 15) + (lane >> 4), r = r0 + (j >> 4) * 32 + e;
-    const uint64_t src = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(j < 16 ? src0 : src1), e);
-    cp_async16(dst + (piece >> 3) * tc::kKBlock + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
-               src ? reinterpret_cast<const uint8_t*>(src) + piece * 16 : any, src != 0);
+// A tile of 128 rows into shared memory by one warp, two rows an instruction; lane l holds the pool rows of rows l, 32 + l,
+// 64 + l and 96 + l (kNoRow: zeros).
+__device__ __forceinline__ void copy_tile(uint32_t dst, const uint8_t* rows, const uint32_t (&at)[4]) {
+  const int lane = threadIdx.x & 31, piece = lane & 15, odd = lane >> 4;
+  rows += piece * 16;
+  dst += (piece >> 3) * tc::kKBlock + odd * 128;
+  uint32_t swz[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) swz[e] = dst + (((piece & 7) ^ (2 * e + odd)) << 4);
+#pragma unroll
+  for (int j = 0; j < kCaRows / 2; ++j) {
+    const uint32_t row = __shfl_sync(0xffffffffu, at[j >> 4], 2 * (j & 15) + odd);
+    const bool ok = row != kNoRow;
+    cp_async16(swz[j & 3] + j * 256, rows + static_cast<size_t>(ok ? row : 0u) * (kD * 2), ok);
   }
 }
-
-// Copies of a loading warp that are under way, oldest first: the barriers that wait for them.
-struct Flight {
-  uint32_t a = 0, b = 0;
-  __device__ __forceinline__ static void land(uint32_t bar) {
-    tc::fence_proxy_async();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+// 32 rows of a query tile from row r0 on by one warp, lane l holding the address of row r0 + l (null: zeros).
+__device__ __forceinline__ void copy_queries(uint32_t dst, int r0, const uint8_t* src, const uint8_t* any) {
+  const int lane = threadIdx.x & 31, piece = lane & 15;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const int e = 2 * j + (lane >> 4), r = r0 + e;
+    const uint64_t x = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), e);
+    cp_async16(dst + (piece >> 3) * tc::kKBlock + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
+               x ? reinterpret_cast<const uint8_t*>(x) + piece * 16 : any, x != 0);
   }
-  __device__ __forceinline__ void push(uint32_t bar) {   // copies have been started
-    cp_async_commit();
-    if (a) {
-      cp_async_wait<2>();
-      land(a);
-    }
-    a = b;
-    b = bar;
-  }
-  __device__ __forceinline__ void flush() {
-    cp_async_wait<0>();
-    if (a) land(a);
-    if (b) land(b);
-    a = b = 0;
-  }
-};
+}
+// This warp's copies and stores so far are in shared memory, for the tensor core too: an arrival at `bar`.
+__device__ __forceinline__ void land(uint32_t bar) {
+  tc::fence_proxy_async();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+}
+template <int REGS>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS)); }
+template <int REGS>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(REGS)); }
 
 // The value s * code + z of 16 codes as two fp16 numbers each, hi and what is left.
 __device__ __forceinline__ void split16(const uint4& c, __half2 m, uint32_t (&hi)[8], uint32_t (&lo)[8]) {
@@ -392,40 +396,42 @@ __device__ __forceinline__ void split16(const uint4& c, __half2 m, uint32_t (&hi
     lo[e] = pack2<false>(f0 - __low2float(h), f1 - __high2float(h));
   }
 }
-// Rows r0 .. r0 + 63 of an INT8 tile into its two buffers; lane l holds the pool rows of rows r0 + l and r0 + 32 + l.
-__device__ __forceinline__ void convert_rows(const uint32_t (&dst)[2], int r0, const uint8_t* codes, const uint8_t* meta, uint32_t at0,
-                                             uint32_t at1) {
+// 32 rows of an INT8 tile: the codes and scales that a lane takes of them, four rows an instruction, 16 channels of each.
+struct CodeRows {
+  uint4 c[8];
+  __half2 m[8];
+};
+__device__ __forceinline__ void load_codes(CodeRows& x, const uint8_t* codes, const uint8_t* meta, uint32_t at) {   // lane l: the pool row of row l
   const int lane = threadIdx.x & 31, piece = lane & 7;
-#pragma unroll 1
-  for (int j0 = 0; j0 < 16; j0 += 4) {   // four rows an instruction
-    uint4 c[4];
-    __half2 m[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int e = 4 * ((j0 + j) & 7) + (lane >> 3);
-      const uint32_t row = __shfl_sync(0xffffffffu, j0 < 8 ? at0 : at1, e);
-      c[j] = make_uint4(0, 0, 0, 0);
-      m[j] = __float2half2_rn(0.f);
-      if (row != kNoRow) {
-        c[j] = *reinterpret_cast<const uint4*>(codes + static_cast<size_t>(row) * kD + piece * 16);
-        m[j] = reinterpret_cast<const __half2*>(meta + static_cast<size_t>(row) * kMetaBytes)[piece >> 2];
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t row = __shfl_sync(0xffffffffu, at, 4 * j + (lane >> 3));
+    x.c[j] = make_uint4(0, 0, 0, 0);
+    x.m[j] = __float2half2_rn(0.f);
+    if (row != kNoRow) {
+      x.c[j] = *reinterpret_cast<const uint4*>(codes + static_cast<size_t>(row) * kD + piece * 16);
+      x.m[j] = reinterpret_cast<const __half2*>(meta + static_cast<size_t>(row) * kMetaBytes)[piece >> 2];
+    }
+  }
+}
+// Rows r0 .. r0 + 31 of a tile into its two buffers, at dst and behind it.
+__device__ __forceinline__ void store_codes(const CodeRows& x, uint32_t dst, int r0) {
+  const int lane = threadIdx.x & 31, piece = lane & 7;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int r = r0 + 4 * j + (lane >> 3);
+    uint32_t v[2][8];
+    split16(x.c[j], x.m[j], v[0], v[1]);
+#pragma unroll
+    for (int part = 0; part < 2; ++part)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {   // channels 16 piece + 8 half ..
+        const int ch = (piece & 3) * 2 + half;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(dst + part * tc::kTileBytes + (piece >> 2) * tc::kKBlock + r * 128 +
+                                                                        ((ch ^ (r & 7)) << 4)),
+                     "r"(v[part][4 * half]), "r"(v[part][4 * half + 1]), "r"(v[part][4 * half + 2]), "r"(v[part][4 * half + 3])
+                     : "memory");
       }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = r0 + 4 * (j0 + j) + (lane >> 3);
-      uint32_t x[2][8];
-      split16(c[j], m[j], x[0], x[1]);
-#pragma unroll
-      for (int part = 0; part < 2; ++part)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {   // channels 16 piece + 8 half ..
-          const int ch = (piece & 3) * 2 + half;
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(dst[part] + (piece >> 2) * tc::kKBlock + r * 128 + ((ch ^ (r & 7)) << 4)),
-                       "r"(x[part][4 * half]), "r"(x[part][4 * half + 1]), "r"(x[part][4 * half + 2]), "r"(x[part][4 * half + 3])
-                       : "memory");
-        }
-    }
   }
 }
 
@@ -441,12 +447,12 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attention_kernel(const Ch
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kCaRing; ++i) {
-      tc::mbar_init(smem_u32(&bar.full[i]), kCaLoaders);
+      tc::mbar_init(smem_u32(&bar.full[i]), Q8 ? kCaLoaders : 1);
       tc::mbar_init(smem_u32(&bar.empty[i]), 2);
     }
     for (int i = 0; i < kCaTold; ++i) {
       tc::mbar_init(smem_u32(&bar.told[i]), 1);
-      tc::mbar_init(smem_u32(&bar.heard[i]), kCaThreads / 32 - 1);
+      tc::mbar_init(smem_u32(&bar.heard[i]), kCaMmaWarp + 2);   // all but the last two warps
     }
     tc::mbar_init(smem_u32(&bar.q), kCaLoaders);
     tc::mbar_init(smem_u32(&bar.qfree), 2);
@@ -468,7 +474,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attention_kernel(const Ch
   const uint32_t tmem = uniform(tslot);
   pdl_trigger();       // the joining kernel may be placed; it waits for this one's end
   tc::Waits wait;
-  // Item n, as the first loading warp tells it; null behind the last one, or where a wait gave up.
+  // Item n, as the walking warp tells it; null behind the last one, or where a wait gave up.
   const auto hear = [&](int n) -> const Work* {
     wait(smem_u32(&bar.told[n % kCaTold]), (n / kCaTold) & 1);
     const Work* w = &works[n % kCaTold];
@@ -479,120 +485,24 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attention_kernel(const Ch
     if (lane == 0) tc::mbar_arrive(smem_u32(&bar.heard[n % kCaTold]));
   };
 
-  if (warp >= kCaLoadWarp) {
-    const bool walks = warp == kCaLoadWarp;
-    const int r0 = (warp - kCaLoadWarp) * (kCaRows / kCaLoaders);
-    const size_t layer0 = a.p.layer_rows() * a.layer;
-    const uint8_t* k0 = a.p.k + layer0 * (Q8 ? kD : kD * 2);
-    const uint8_t* v0 = a.p.v + layer0 * (Q8 ? kD : kD * 2);
-    int slot = 0, par = 1, qs = 0;   // ring position; parity that an empty buffer shows; query loads
+  if (warp >= kCaMmaWarp) fewer_registers<kCaMmaRegs>();   // (one instruction for all of a warpgroup)
+  if (warp >= kCaWalkWarp) {
     bool some = !walk.idle;
-    Flight flight;
-    for (int n = 0;; ++n) {
-      if (walks) {
-        // Only copies of the last item are under way here, so that whoever is behind can go on.
-        if (n >= kCaTold) wait(smem_u32(&bar.heard[n % kCaTold]), (n / kCaTold - 1) & 1);
-        Work next;
-        if (some) next = walk.work(a);
-        if (lane == 0) {
-          if (some)
-            works[n % kCaTold] = next;
-          else
-            works[n % kCaTold].nt = -1;
-          tc::mbar_arrive(smem_u32(&bar.told[n % kCaTold]));
-        }
-        __syncwarp();
-        if (!__all_sync(0xffffffffu, some && wait.ok)) break;
+    for (int n = 0; warp == kCaWalkWarp; ++n) {
+      if (n >= kCaTold) wait(smem_u32(&bar.heard[n % kCaTold]), (n / kCaTold - 1) & 1);
+      Work next;
+      if (some) next = walk.work(a);
+      if (lane == 0) {
+        if (some)
+          works[n % kCaTold] = next;
+        else
+          works[n % kCaTold].nt = -1;
+        tc::mbar_arrive(smem_u32(&bar.told[n % kCaTold]));
       }
-      const Work* told = walks ? &works[n % kCaTold] : hear(n);
-      if (!told) break;
-      const Work& w = *told;
-      const int begin = uniform(w.begin), end = uniform(w.end);
-      if (begin < end) {
-        const int32_t* table = a.p.table + static_cast<size_t>(uniform(w.seq)) * a.p.max_pages;
-        const int hk = uniform(w.head[0] / a.rep), keys = uniform(w.keys);
-        // the pool row of slot j, kNoRow for one that no row of the item sees
-        const int first = uniform(a.qb.window > 0 ? max(w.pa[0] - a.qb.window + 1, 0) : 0);
-        const auto place = [&](int i, int r) {
-          const int j = w.j0(i) + r;
-          uint32_t row = kNoRow;
-          if (i < end && j < keys && (j >= first || j < a.qb.sinks)) {
-            const uint32_t pg = div_of(static_cast<uint32_t>(j), a.p.ps);
-            row = pool_row(__ldg(table + pg), a.p.n_pages, a.p.Hkv, hk, a.p.ps.d, j - pg * a.p.ps.d);
-            if (row == kNoRow) tc::report_giveup(tc::kBadPage);
-          }
-          return row;
-        };
-        uint32_t at0 = place(begin, r0 + lane), at1 = place(begin, r0 + 32 + lane);
-        for (int i = begin; i < end; ++i) {
-          const uint32_t next0 = place(i + 1, r0 + lane), next1 = place(i + 1, r0 + 32 + lane);   // looked up ahead
-#pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv) {
-            const uint8_t* x = kv ? v0 : k0;
-            uint32_t dst[kParts], full[kParts];
-#pragma unroll
-            for (int part = 0; part < kParts; ++part) {
-              wait(smem_u32(&bar.empty[slot]), par);
-              dst[part] = ring + slot * tc::kTileBytes;
-              full[part] = smem_u32(&bar.full[slot]);
-              if (++slot == kCaRing) {
-                slot = 0;
-                par ^= 1;
-              }
-            }
-            if (__all_sync(0xffffffffu, wait.ok)) {
-              if constexpr (Q8) {
-                convert_rows(dst, r0, x, (kv ? a.p.vm : a.p.km) + layer0 * kMetaBytes, at0, at1);
-                Flight::land(full[0]);
-                Flight::land(full[1]);
-              } else {
-                copy_rows(dst[0], r0, at0 == kNoRow ? nullptr : x + static_cast<size_t>(at0) * (kD * 2),
-                          at1 == kNoRow ? nullptr : x + static_cast<size_t>(at1) * (kD * 2), k0);
-                flight.push(full[0]);
-              }
-            }
-          }
-          if (i == begin) {   // the queries behind the first tile: the last item's products still read theirs
-            if (qs > 0) {
-              flight.flush();
-              wait(smem_u32(&bar.qfree), (qs - 1) & 1);
-            }
-            ++qs;
-            if (__all_sync(0xffffffffu, wait.ok)) {
-              for (int t = 0; t < w.nt; ++t) {
-                const uint8_t* src[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int r = r0 + e * 32 + lane, sub = r / w.tb, q = w.q0[t] + r - sub * w.tb;
-                  src[e] = sub < w.heads[t] && q < w.rows ? a.q.row(0, w.head[t] + sub, w.row0 + q) : nullptr;
-                }
-                copy_rows(sq + t * tc::kTileBytes, r0, src[0], src[1], a.q.p);
-              }
-              flight.push(smem_u32(&bar.q));
-              if (Q8) flight.flush();
-            }
-          }
-          at0 = next0;
-          at1 = next1;
-        }
-      } else {
-        flight.flush();
-      }
-      if (walks)
-        some = walk.next(a, wait.ok);
-      else
-        heard(n);
+      __syncwarp();
+      if (!__all_sync(0xffffffffu, some && wait.ok)) break;
+      some = walk.next(a, wait.ok);
     }
-    flight.flush();
-    // every buffer's release has arrived before the CTA ends
-    for (int c = 0; c < kCaRing; ++c) {
-      wait(smem_u32(&bar.empty[slot]), par);
-      if (++slot == kCaRing) {
-        slot = 0;
-        par ^= 1;
-      }
-    }
-    if (qs > 0) wait(smem_u32(&bar.qfree), (qs - 1) & 1);
   } else if (warp >= kCaMmaWarp) {
     // One warp per query tile, so that neither waits in the other's place.  The whole warp walks
     // the steps, so that addresses and descriptors stay uniform; one elected lane issues.
@@ -701,7 +611,108 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attention_kernel(const Ch
       }
       heard(n);
     }
+  } else if (warp >= kCaLoadWarp) {
+    fewer_registers<kCaLoadRegs>();
+    const int me = warp - kCaLoadWarp;
+    const size_t layer0 = a.p.layer_rows() * a.layer;
+    const uint8_t* k0 = a.p.k + layer0 * (Q8 ? kD : kD * 2);
+    const uint8_t* v0 = a.p.v + layer0 * (Q8 ? kD : kD * 2);
+    int used = 0, qs = 0;   // uses of this warp's buffer (INT8: of every buffer); items whose queries were loaded
+    int ahead = 0;          // buffers of all items before, modulo the ring
+    for (int n = 0;; ++n) {
+      const Work* told = hear(n);
+      if (!told) break;
+      const Work& w = *told;
+      const int begin = uniform(w.begin), end = uniform(w.end);
+      if (begin < end) {
+        const int32_t* table = a.p.table + static_cast<size_t>(uniform(w.seq)) * a.p.max_pages;
+        const int hk = uniform(w.head[0] / a.rep), keys = uniform(w.keys);
+        // the pool row of slot j, kNoRow for one that no row of the item sees
+        const int first = uniform(a.qb.window > 0 ? max(w.pa[0] - a.qb.window + 1, 0) : 0);
+        const auto place = [&](int i, int r) {
+          const int j = w.j0(i) + r;
+          uint32_t row = kNoRow;
+          if (i < end && j < keys && (j >= first || j < a.qb.sinks)) {
+            const uint32_t pg = div_of(static_cast<uint32_t>(j), a.p.ps);
+            row = pool_row(__ldg(table + pg), a.p.n_pages, a.p.Hkv, hk, a.p.ps.d, j - pg * a.p.ps.d);
+            if (row == kNoRow) tc::report_giveup(tc::kBadPage);
+          }
+          return row;
+        };
+        // a quarter of the queries; the last item's products still read theirs
+        const auto queries = [&] {
+          if (qs > 0) wait(smem_u32(&bar.qfree), (qs - 1) & 1);
+          ++qs;
+          if (!__all_sync(0xffffffffu, wait.ok)) return;
+          const int r = me * 32 + lane, sub = r / w.tb;
+          for (int t = 0; t < w.nt; ++t) {
+            const int q = w.q0[t] + r - sub * w.tb;
+            copy_queries(sq + t * tc::kTileBytes, me * 32,
+                         sub < w.heads[t] && q < w.rows ? a.q.row(0, w.head[t] + sub, w.row0 + q) : nullptr, a.q.p);
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+          land(smem_u32(&bar.q));
+        };
+        if constexpr (Q8) {
+          // every warp has 32 rows of each tile; the next one's codes are under way meanwhile
+          CodeRows x;
+          uint32_t at = place(begin, me * 32 + lane);
+          load_codes(x, k0, a.p.km + layer0 * kMetaBytes, at);
+          for (int i = begin; i < end; ++i) {
+            const uint32_t next = place(i + 1, me * 32 + lane);
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+              wait(smem_u32(&bar.empty[2 * kv]), (used & 1) ^ 1);
+              wait(smem_u32(&bar.empty[2 * kv + 1]), (used & 1) ^ 1);
+              if (!__all_sync(0xffffffffu, wait.ok)) break;
+              store_codes(x, ring + 2 * kv * tc::kTileBytes, me * 32);
+              land(smem_u32(&bar.full[2 * kv]));
+              land(smem_u32(&bar.full[2 * kv + 1]));
+              if (kv == 0)
+                load_codes(x, v0, a.p.vm + layer0 * kMetaBytes, at);
+              else if (i + 1 < end)
+                load_codes(x, k0, a.p.km + layer0 * kMetaBytes, next);
+            }
+            ++used;
+            if (i == begin) queries();
+            at = next;
+          }
+        } else {
+          // this warp has every fourth buffer: keys (c even) or values of tile begin + c / 2
+          int c = (me - ahead) & (kCaRing - 1);
+          const int count = 2 * (end - begin);
+          uint32_t at[4];
+          const auto look = [&](int i) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) at[e] = place(i, e * 32 + lane);
+          };
+          look(begin + (c >> 1));
+          for (bool one = true; c < count || one; c += kCaRing) {
+            if (c < count) {
+              wait(smem_u32(&bar.empty[me]), (used & 1) ^ 1);
+              ++used;
+              if (__all_sync(0xffffffffu, wait.ok)) {
+                copy_tile(ring + me * tc::kTileBytes, c & 1 ? v0 : k0, at);
+                cp_async_commit();
+                look(begin + (c >> 1) + 2);   // the next one's places are looked up meanwhile
+                cp_async_wait<0>();
+                land(smem_u32(&bar.full[me]));
+              }
+            }
+            if (one) queries();   // behind the item's first buffers
+            one = false;
+          }
+          ahead = (ahead + count) & (kCaRing - 1);
+        }
+      }
+      heard(n);
+    }
+    // every release of this warp's buffer has arrived before the CTA ends
+    wait(smem_u32(&bar.empty[me]), (used & 1) ^ 1);
+    if (qs > 0) wait(smem_u32(&bar.qfree), (qs - 1) & 1);
   } else {
+    more_registers<kCaSoftmaxRegs>();
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;   // the thread's TMEM lane is its row
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + kCaO + t * 128;
