@@ -15,11 +15,11 @@
 // call form one line, of which each CTA takes an equal part; a CTA finds its part in sums over the
 // requests, which all of its threads make before it begins.  Items that are cut are joined by a second kernel.
 //
-// Four warps bring keys and values from the pages to a ring of four 32 KB buffers (128-byte swizzle), row by
-// row: a page has any number of rows, and a tile begins and ends inside pages.  Each has a buffer of its own,
-// and says so when it has landed (two warps that shared every buffer, and signalled one while they started the
-// next but one, took 781 us for 8192 causal rows of 32 heads).  Rows that no query of the item sees are zeros
-// there, so that they may hold anything.  One more warp walks the line, and tells the others what each item is.
+// Four warps bring keys and values from the pages to a ring of four 32 KB buffers (128-byte swizzle), each
+// to a buffer of its own: by TMA where the pages' size is a multiple of 8 rows, a page or the largest power of
+// two that divides it in a box; row by row (cp.async) otherwise, where a tile begins and ends inside pages.
+// Rows that no query of the item sees may hold anything: values are cleared there behind the TMA, or never
+// copied.  One more warp walks the line, and tells the others what each item is.
 //
 // INT8 pages: s * code + z is held as two fp16 numbers, the nearest one and what is left (22 bits), and each
 // product is two: keys rounded to fp16 alone put 1e-4 into lse and half as much again into the outputs.
@@ -63,6 +63,7 @@ struct ChunkArgs {
   int layer, n, rows, Hq, rep, ctas;
   int tile_rows;               // rows of a tile that can count
   Mask qb;
+  int box;                     // rows of a TMA box: a power of two from 8 on that divides a page and a tile; 0: no TMA
   bool wide_out;               // rows of out begin at multiples of 32 bytes
   float scale;                 // log2(e) / sqrt(D)
 };
@@ -70,6 +71,7 @@ struct ChunkArgs {
 struct CaBars {
   uint64_t told[kCaTold], heard[kCaTold];   // the item is known; every warp is done with it
   uint64_t full[kCaRing], empty[kCaRing];   // buffer landed; the products that read it are done
+  uint64_t boxes[kCaRing];                  // its boxes landed: rows of it have to be cleared yet
   uint64_t turn[2];                         // the tile's products may be issued
   uint64_t qfree;                           // the products that read the queries are done
   uint64_t q, s[2], p[2][2], o[2];          // queries landed; scores, half the weights, last sums written
@@ -375,6 +377,16 @@ __device__ __forceinline__ void land(uint32_t bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
 }
+// A box of pool rows, both halves of the channels, by one lane.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t row, uint32_t bar) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+            dst + j * tc::kKBlock),
+        "l"(map), "r"(j * 64), "r"(row), "r"(bar)
+        : "memory");
+}
 template <int REGS>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS)); }
 template <int REGS>
@@ -436,7 +448,8 @@ __device__ __forceinline__ void store_codes(const CodeRows& x, uint32_t dst, int
 }
 
 template <int TYPE>
-__global__ void __launch_bounds__(kCaThreads, 1) chunk_attention_kernel(const ChunkArgs a) {
+__global__ void __launch_bounds__(kCaThreads, 1)
+    chunk_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const ChunkArgs a) {
   constexpr bool BF = TYPE == MIKV_PAGES_BF16, Q8 = TYPE == MIKV_PAGES_INT8;
   constexpr int kParts = Q8 ? 2 : 1;   // buffers of a tile of keys, or of values
   extern __shared__ uint8_t smem[];
@@ -449,6 +462,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attention_kernel(const Ch
     for (int i = 0; i < kCaRing; ++i) {
       tc::mbar_init(smem_u32(&bar.full[i]), Q8 ? kCaLoaders : 1);
       tc::mbar_init(smem_u32(&bar.empty[i]), 2);
+      tc::mbar_init(smem_u32(&bar.boxes[i]), 1);
     }
     for (int i = 0; i < kCaTold; ++i) {
       tc::mbar_init(smem_u32(&bar.told[i]), 1);
@@ -470,6 +484,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attention_kernel(const Ch
   Walk walk = find_part(a, smem + (sq - smem_u32(smem)), sums);
   tc::fence_before_sync();
   __syncthreads();     // the sums have been read: the tiles may be written over them
+  tc::fence_proxy_async();
   tc::fence_after_sync();
   const uint32_t tmem = uniform(tslot);
   pdl_trigger();       // the joining kernel may be placed; it waits for this one's end
@@ -619,6 +634,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attention_kernel(const Ch
     const uint8_t* v0 = a.p.v + layer0 * (Q8 ? kD : kD * 2);
     int used = 0, qs = 0;   // uses of this warp's buffer (INT8: of every buffer); items whose queries were loaded
     int ahead = 0;          // buffers of all items before, modulo the ring
+    int cleared = 0;        // of this warp's tiles so far, those with rows to clear
     for (int n = 0;; ++n) {
       const Work* told = hear(n);
       if (!told) break;
@@ -682,17 +698,58 @@ __global__ void __launch_bounds__(kCaThreads, 1) chunk_attention_kernel(const Ch
           // this warp has every fourth buffer: keys (c even) or values of tile begin + c / 2
           int c = (me - ahead) & (kCaRing - 1);
           const int count = 2 * (end - begin);
-          uint32_t at[4];
+          uint32_t at[4];   // pool rows of the tile's rows 32 e + lane; with TMA, of box `lane`
           const auto look = [&](int i) {
+            if (a.box > 0) {
+              at[0] = at[1] = kNoRow;
+              const int r = lane * a.box, j = i < end ? w.j0(i) + r : 0;
+              // boxes with a row that is seen; at[1] tells one whose page lies outside the pool
+              if (i < end && r < kCaRows && j < keys && (j + a.box > first || j < a.qb.sinks)) {
+                const uint32_t pg = div_of(static_cast<uint32_t>(j), a.p.ps);
+                at[0] = pool_row(__ldg(table + pg), a.p.n_pages, a.p.Hkv, hk, a.p.ps.d, j - pg * a.p.ps.d);
+                if (at[0] == kNoRow) {
+                  tc::report_giveup(tc::kBadPage);
+                  at[1] = 0;
+                }
+              }
+              return;
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) at[e] = place(i, e * 32 + lane);
+          };
+          // the boxes of tile i to this warp's buffer
+          const auto fetch = [&](int i, bool values) {
+            const uint32_t dst = ring + me * tc::kTileBytes;
+            const uint32_t boxes = __ballot_sync(0xffffffffu, at[0] != kNoRow), bad = __ballot_sync(0xffffffffu, at[1] != kNoRow);
+            const int j0 = w.j0(i);
+            const int z0 = min(max(a.qb.sinks - j0, 0), kCaRows), z1 = min(first - j0, kCaRows), z2 = min(keys - j0, kCaRows);
+            const bool clear = bad != 0 || (values && (z0 < z1 || z2 < kCaRows));
+            const uint32_t on = smem_u32(clear ? &bar.boxes[me] : &bar.full[me]);
+            if (lane == 0) tc::mbar_expect_tx(on, __popc(boxes) * a.box * kD * 2);
+            __syncwarp();
+            if (at[0] != kNoRow) tma_box(dst + lane * a.box * 128, values ? &vmap : &kmap, at[0], on);
+            __syncwarp();
+            if (!clear) return;
+            const int shift = 31 - __clz(a.box);
+            wait(on, cleared++ & 1);
+            for (int e = lane; e < kCaRows * 16; e += 32) {   // 16-byte pieces, both channel blocks
+              const int r = e >> 4, piece = e & 15;
+              if ((r >= z0 && r < z1) || r >= z2 || (bad >> (r >> shift) & 1u))
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(dst + (piece >> 3) * tc::kKBlock + r * 128 + (piece & 7) * 16),
+                             "r"(0)
+                             : "memory");
+            }
+            land(smem_u32(&bar.full[me]));
           };
           look(begin + (c >> 1));
           for (bool one = true; c < count || one; c += kCaRing) {
             if (c < count) {
               wait(smem_u32(&bar.empty[me]), (used & 1) ^ 1);
               ++used;
-              if (__all_sync(0xffffffffu, wait.ok)) {
+              if (a.box > 0) {
+                if (__all_sync(0xffffffffu, wait.ok)) fetch(begin + (c >> 1), c & 1);
+                look(begin + (c >> 1) + 2);
+              } else if (__all_sync(0xffffffffu, wait.ok)) {
                 copy_tile(ring + me * tc::kTileBytes, c & 1 ? v0 : k0, at);
                 cp_async_commit();
                 look(begin + (c >> 1) + 2);   // the next one's places are looked up meanwhile
@@ -885,12 +942,30 @@ bool sizes_ok(const mikv_pages* p, int n, int rows, int Hq) {
          static_cast<int64_t>(p->max_pages) * p->page_size <= kMaxPos;
 }
 
+// Rows of one layer of the pool as [rows][D], boxes of a.box rows and 64 channels.
+int encode_pool(CUtensorMap* map, const uint8_t* base, const ChunkArgs& a, const char* name) {
+  const auto enc = tc::tensor_map_encoder();
+  if (!enc) return fail(MIKV_ECUDA, "chunk_attention: cuTensorMapEncodeTiled unavailable");
+  const cuuint64_t dims[2] = {kD, static_cast<cuuint64_t>(a.p.layer_rows())}, strides[1] = {kD * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(a.box)}, estr[2] = {1, 1};
+  const CUresult e = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<uint8_t*>(base + a.p.layer_rows() * a.layer * (kD * 2)), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (e != CUDA_SUCCESS) return fail(MIKV_ECUDA, "chunk_attention: tensor map of %s (error %d)", name, static_cast<int>(e));
+  return MIKV_OK;
+}
+
 template <int TYPE>
 int launch(const ChunkArgs& a, cudaStream_t st) {
+  CUtensorMap km{}, vm{};
+  if (a.box > 0) {
+    if (int e = encode_pool(&km, a.p.k, a, "keys")) return e;
+    if (int e = encode_pool(&vm, a.p.v, a, "values")) return e;
+  }
   const auto kern = chunk_attention_kernel<TYPE>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCaSmem);
   if (e != cudaSuccess) return check_launch_after(e, "chunk_attention_kernel");
-  kern<<<a.ctas, kCaThreads, kCaSmem, st>>>(a);
+  kern<<<a.ctas, kCaThreads, kCaSmem, st>>>(km, vm, a);
   if (int r = check_launch("chunk_attention_kernel")) return r;
   const dim3 joins((2 * a.tile_rows + kJoinRows - 1) / kJoinRows, a.ctas);
   return check_launch_after(launch_after(chunk_join_kernel<TYPE == MIKV_PAGES_BF16>, joins, dim3(kJoinRows * (kD / 8) * kJoinGroups), 0, st, a),
@@ -946,6 +1021,9 @@ extern "C" int mikv_chunk_attention(const mikv_rows* q, const mikv_pages* pages,
   a.tile_rows = tile_rows_of(rows, a.rep);
   a.qb.window = window > kMaxPos ? 0 : window;   // one that reaches every key is none
   a.qb.sinks = std::min(sinks, kMaxPos);
+  a.box = std::min(kCaRows, pages->page_size & -pages->page_size);
+  // (coordinates are signed)
+  if (a.p.type == MIKV_PAGES_INT8 || a.box < 8 || a.p.layer_rows() > 0x7fffffffULL) a.box = 0;
   a.wide_out = ((reinterpret_cast<uintptr_t>(out->data) | static_cast<uintptr_t>(a.out.sh | a.out.st)) & 31u) == 0;
   a.scale = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
   switch (a.p.type) {
