@@ -107,13 +107,28 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xfffffff
 // at `to` is rescaled where some row of the warp needs it.
 // Each half of the weights is announced (`ready`, one arrival a warp) as soon as it is written.
 // `last`: the last key that the row may see, its position p or less.  Args: qb.window, qb.sinks and scale.
-template <bool BF, int COLS, class Args>
+// PARTS 2: the scores are the sum of two products, the second COLS columns behind the first.
+template <bool BF, int COLS, int PARTS, class Args>
 __device__ __forceinline__ void softmax_tile(const Args& a, uint32_t ts, uint32_t to, bool whole, int p, int last, int j0, Row& r,
                                              const uint32_t (&ready)[2]) {
   float s[COLS];
 #pragma unroll
   for (int c = 0; c < COLS / 32; ++c) ld32(ts + c * 32, s + c * 32);
   wait_ld();
+  if (PARTS == 2) {
+#pragma unroll
+    for (int c = 0; c < COLS; c += 32) {
+      float x[32];
+      ld32(ts + COLS + c, x);
+      wait_ld();
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float2 y = __fadd2_rn(make_float2(s[c + i], s[c + i + 1]), make_float2(x[i], x[i + 1]));
+        s[c + i] = y.x;
+        s[c + i + 1] = y.y;
+      }
+    }
+  }
   if (!whole) {
     // the row sees columns lo .. hi and those below sk; 32 columns whole to the warp's rows are left alone
     const int hi = last - j0, lo = a.qb.window > 0 ? p - j0 - a.qb.window + 1 : 0, sk = a.qb.sinks - j0;
@@ -174,7 +189,7 @@ __device__ __forceinline__ void softmax_tile(const Args& a, uint32_t ts, uint32_
       __syncwarp();
       if ((threadIdx.x & 31) == 0) {
         tc::mbar_arrive(ready[c / 64]);
-        if (COLS == 32) tc::mbar_arrive(ready[1]);
+        if (COLS <= 64) tc::mbar_arrive(ready[1]);
       }
     }
   }

@@ -21,8 +21,10 @@
 // Rows that no query of the item sees may hold anything: values are cleared there behind the TMA, or never
 // copied.  One more warp walks the line, and tells the others what each item is.
 //
-// INT8 pages: s * code + z is held as two fp16 numbers, the nearest one and what is left (22 bits), and each
-// product is two: keys rounded to fp16 alone put 1e-4 into lse and half as much again into the outputs.
+// INT8 pages: s * code + z is held as two fp16 numbers, the nearest one and what is left (22 bits): keys rounded
+// to fp16 alone put 1e-4 into lse and half as much again into the outputs.  A key tile has 64 keys then, the
+// two parts of each 64 rows apart in its buffer, so that all copies and products are as above: S_t has the two parts'
+// scores side by side, and P_t meets both parts of the values.
 #include <algorithm>
 
 #include "attention_tile.cuh"
@@ -36,14 +38,20 @@ namespace {
 
 using namespace at;
 
-constexpr int kCaRows = kKeyRows;
+constexpr int kCaRows = kKeyRows;           // query rows of a tile, and rows of a buffer
 constexpr int kCaNarrow = 32;               // columns of a tile that holds the last few sinks
 constexpr int kCaRing = 4;
 constexpr int kCaThreads = 512;             // 2 x 4 softmax warps, 4 loading warps, 2 MMA warps, the walking warp, an idle one
 constexpr int kCaLoadWarp = 8, kCaLoaders = 4, kCaMmaWarp = 12, kCaWalkWarp = 14;
 // Registers of a thread, by warpgroups; 128 each at launch, 65,536 in all.
-constexpr int kCaSoftmaxRegs = 176, kCaLoadRegs = 88, kCaMmaRegs = 72;
-static_assert(256 * kCaSoftmaxRegs + 128 * (kCaLoadRegs + kCaMmaRegs) == kCaThreads * 128, "register split");
+constexpr int kCaMmaRegs = 72;
+template <bool Q8>
+struct Split {
+  static constexpr int softmax = Q8 ? 152 : 176, load = Q8 ? 136 : 88;
+  static_assert(256 * softmax + 128 * (load + kCaMmaRegs) == kCaThreads * 128, "register split");
+};
+template <int TYPE>
+constexpr int kKeys = TYPE == MIKV_PAGES_INT8 ? 64 : kCaRows;   // of a tile
 constexpr int kCaTold = 4;                  // items that the other warps may be behind
 constexpr int kCaSmem = (2 + kCaRing) * tc::kTileBytes + 1024;
 constexpr uint32_t kCaCols = 512;           // S_0, S_1, O_0, O_1: 128 columns each
@@ -114,10 +122,12 @@ struct Work {
   int nt;                 // query tiles; -1: there is no further item
   int whole;              // all of the item
   int row0, rows, keys, tb, seq;   // of the request
-  __device__ __forceinline__ int j0(int i) const { return (i < ts ? i : tw0 + i - ts) * kCaRows; }
+  template <int KT>
+  __device__ __forceinline__ int j0(int i) const { return (i < ts ? i : tw0 + i - ts) * KT; }
   __device__ __forceinline__ bool sees(int t, int i) const { return i <= last[t] && (i < ns || i >= from[t]); }
 };
 // Item `item` of block `blk`, key tiles t0 .. t1 of it.
+template <int KT>
 __device__ __forceinline__ Work work_of(const ChunkArgs& a, const Request& q, int blk, int item, int t0, int t1) {
   Work w;
   const int hk = item / q.t.per, u = item - hk * q.t.per;
@@ -132,7 +142,7 @@ __device__ __forceinline__ Work work_of(const ChunkArgs& a, const Request& q, in
     w.pb[t] = q.r.off + min(w.q0[t] + q.t.tb, q.r.rows) - 1;
   }
   w.nt = w.q0[1] >= q.r.rows || w.heads[1] <= 0 ? 1 : 2;
-  const KeyTiles k = chunk_tiles(q.t, q.r, a.qb.window, a.qb.sinks, blk);
+  const KeyTiles k = chunk_tiles<KT>(q.t, q.r, a.qb.window, a.qb.sinks, blk);
   w.ts = k.ts;
   w.tw0 = k.tw0;
   w.ns = k.ns;
@@ -146,8 +156,8 @@ __device__ __forceinline__ Work work_of(const ChunkArgs& a, const Request& q, in
   w.seq = q.seq;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int e = min(w.pb[t], q.r.keys - 1) < 0 ? -1 : min(w.pb[t], q.r.keys - 1) / kCaRows;
-    w.from[t] = w.ts + (a.qb.window > 0 ? max(w.pa[t] - a.qb.window + 1, 0) / kCaRows - w.tw0 : 0);
+    const int e = min(w.pb[t], q.r.keys - 1) < 0 ? -1 : min(w.pb[t], q.r.keys - 1) / KT;
+    w.from[t] = w.ts + (a.qb.window > 0 ? max(w.pa[t] - a.qb.window + 1, 0) / KT - w.tw0 : 0);
     int last = t >= w.nt || e < 0 ? -1 : e - w.tw0 + w.ts;   // the last one of this part
     last = min(last, w.end - 1);
     if (last < w.from[t]) last = min(last, w.ns - 1);
@@ -157,13 +167,15 @@ __device__ __forceinline__ Work work_of(const ChunkArgs& a, const Request& q, in
   return w;
 }
 // Whether all rows of query tile t see all of the key tile at j0.
+template <int KT>
 __device__ __forceinline__ bool tile_whole(const ChunkArgs& a, int pa, int pb, int keys, int j0) {
-  return j0 + kCaRows - 1 <= min(pa, keys - 1) && (a.qb.window == 0 || j0 > pb - a.qb.window || j0 + kCaRows <= a.qb.sinks);
+  return j0 + KT - 1 <= min(pa, keys - 1) && (a.qb.window == 0 || j0 > pb - a.qb.window || j0 + KT <= a.qb.sinks);
 }
 // Whether key tile i, at j0, counts with its first kCaNarrow columns alone: the sinks' last tile, mostly.
 __device__ __forceinline__ bool tile_narrow(const ChunkArgs& a, int ts, int i, int j0) { return i < ts && a.qb.sinks - j0 <= kCaNarrow; }
 
 // A CTA's part of the line, walked by one warp of it.
+template <int KT>
 struct Walk {
   int req, blk, item;    // the item
   int places, t0, t1;    // its places, and its key tiles of this part
@@ -173,7 +185,7 @@ struct Walk {
   bool idle;
 
   __device__ __forceinline__ void open(const ChunkArgs& a) {   // places of block `blk`
-    places = uniform(chunk_places(q.t, q.r, a.qb.window, a.qb.sinks, blk));
+    places = uniform(chunk_places<KT>(q.t, q.r, a.qb.window, a.qb.sinks, blk));
   }
   __device__ __forceinline__ void load(const ChunkArgs& a) {
     q = request_of(a, req);
@@ -183,7 +195,7 @@ struct Walk {
     q.r.off = uniform(q.r.off);
     q.r.keys = uniform(q.r.keys);
   }
-  __device__ __forceinline__ Work work(const ChunkArgs& a) const { return work_of(a, q, blk, item, t0, t1); }
+  __device__ __forceinline__ Work work(const ChunkArgs& a) const { return work_of<KT>(a, q, blk, item, t0, t1); }
   // On to the next item, by the whole warp; false where there is none.
   __device__ __forceinline__ bool next(const ChunkArgs& a, bool ok) {
     to_go -= places;
@@ -259,7 +271,8 @@ __device__ __forceinline__ int find_entry(const T* base, int n, int64_t x) {
 
 // This CTA's part of the line, by all threads of it, for its walking warp.  `scratch`: (n + 1) * 4 bytes for the blocks before each
 // request, and 8 bytes a block for the places before it.
-__device__ __forceinline__ Walk find_part(const ChunkArgs& a, uint8_t* scratch, int64_t* sums) {
+template <int KT>
+__device__ __forceinline__ Walk<KT> find_part(const ChunkArgs& a, uint8_t* scratch, int64_t* sums) {
   const int tid = threadIdx.x;
   int64_t* place = reinterpret_cast<int64_t*>(scratch);
   int32_t* blocks = reinterpret_cast<int32_t*>(place + a.rows / kCaRows + a.n + 2);   // a request has a block more than rows / 128 at most
@@ -286,7 +299,7 @@ __device__ __forceinline__ Walk find_part(const ChunkArgs& a, uint8_t* scratch, 
     if (e < entries) {
       const int i = find_entry(blocks, a.n, e);
       const Request q = request_of(a, i);
-      v = static_cast<int64_t>(chunk_places(q.t, q.r, a.qb.window, a.qb.sinks, e - blocks[i])) * a.p.Hkv * q.t.per;
+      v = static_cast<int64_t>(chunk_places<KT>(q.t, q.r, a.qb.window, a.qb.sinks, e - blocks[i])) * a.p.Hkv * q.t.per;
     }
     v = scan_block(v, sums, total);
     if (e < entries) place[e + 1] = done + v;
@@ -294,7 +307,7 @@ __device__ __forceinline__ Walk find_part(const ChunkArgs& a, uint8_t* scratch, 
   }
   if (tid == 0) place[0] = 0;
   __syncthreads();
-  Walk w;
+  Walk<KT> w;
   w.idle = true;
   if (tid / 32 != kCaWalkWarp) return w;
   const int workers = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(a.ctas), done / 2))), c = blockIdx.x;
@@ -316,13 +329,13 @@ __device__ __forceinline__ Walk find_part(const ChunkArgs& a, uint8_t* scratch, 
     if (y < done) {
       const int f = find_entry(place, entries, y), i = find_entry(blocks, a.n, f);
       const Request q = request_of(a, i);
-      const int blk = f - blocks[i], places = chunk_places(q.t, q.r, a.qb.window, a.qb.sinks, blk);
+      const int blk = f - blocks[i], places = chunk_places<KT>(q.t, q.r, a.qb.window, a.qb.sinks, blk);
       const int item = static_cast<int>((y - place[f]) / places);
       const int64_t b = place[f] + static_cast<int64_t>(item) * places;
       if (line_tile(static_cast<int>(y - b)) == 0) {
         y = b;
       } else if (b >= x) {   // begun here, and goes on in later CTAs
-        const Work k = work_of(a, q, blk, item, 0, places);
+        const Work k = work_of<KT>(a, q, blk, item, 0, places);
         cut.last = split_owner(done, workers, b + places - 1);
         cut.before = b > x;
         cut.row0 = q.row0;
@@ -408,15 +421,15 @@ __device__ __forceinline__ void split16(const uint4& c, __half2 m, uint32_t (&hi
     lo[e] = pack2<false>(f0 - __low2float(h), f1 - __high2float(h));
   }
 }
-// 32 rows of an INT8 tile: the codes and scales that a lane takes of them, four rows an instruction, 16 channels of each.
+// 16 keys of an INT8 tile: the codes and scales that a lane takes of them, four keys an instruction, 16 channels of each.
 struct CodeRows {
-  uint4 c[8];
-  __half2 m[8];
+  uint4 c[4];
+  __half2 m[4];
 };
-__device__ __forceinline__ void load_codes(CodeRows& x, const uint8_t* codes, const uint8_t* meta, uint32_t at) {   // lane l: the pool row of row l
+__device__ __forceinline__ void load_codes(CodeRows& x, const uint8_t* codes, const uint8_t* meta, uint32_t at) {   // lane l < 16: the pool row of key l
   const int lane = threadIdx.x & 31, piece = lane & 7;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 4; ++j) {
     const uint32_t row = __shfl_sync(0xffffffffu, at, 4 * j + (lane >> 3));
     x.c[j] = make_uint4(0, 0, 0, 0);
     x.m[j] = __float2half2_rn(0.f);
@@ -426,11 +439,11 @@ __device__ __forceinline__ void load_codes(CodeRows& x, const uint8_t* codes, co
     }
   }
 }
-// Rows r0 .. r0 + 31 of a tile into its two buffers, at dst and behind it.
+// Keys r0 .. r0 + 15 of a tile into its buffer: the numbers' first parts in rows 0 .. 63, the second ones behind.
 __device__ __forceinline__ void store_codes(const CodeRows& x, uint32_t dst, int r0) {
   const int lane = threadIdx.x & 31, piece = lane & 7;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 4; ++j) {
     const int r = r0 + 4 * j + (lane >> 3);
     uint32_t v[2][8];
     split16(x.c[j], x.m[j], v[0], v[1]);
@@ -439,7 +452,7 @@ __device__ __forceinline__ void store_codes(const CodeRows& x, uint32_t dst, int
 #pragma unroll
       for (int half = 0; half < 2; ++half) {   // channels 16 piece + 8 half ..
         const int ch = (piece & 3) * 2 + half;
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(dst + part * tc::kTileBytes + (piece >> 2) * tc::kKBlock + r * 128 +
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(dst + (piece >> 2) * tc::kKBlock + (part * kKeys<MIKV_PAGES_INT8> + r) * 128 +
                                                                         ((ch ^ (r & 7)) << 4)),
                      "r"(v[part][4 * half]), "r"(v[part][4 * half + 1]), "r"(v[part][4 * half + 2]), "r"(v[part][4 * half + 3])
                      : "memory");
@@ -451,7 +464,7 @@ template <int TYPE>
 __global__ void __launch_bounds__(kCaThreads, 1)
     chunk_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const ChunkArgs a) {
   constexpr bool BF = TYPE == MIKV_PAGES_BF16, Q8 = TYPE == MIKV_PAGES_INT8;
-  constexpr int kParts = Q8 ? 2 : 1;   // buffers of a tile of keys, or of values
+  constexpr int KT = kKeys<TYPE>;
   extern __shared__ uint8_t smem[];
   __shared__ CaBars bar;
   __shared__ Work works[kCaTold];
@@ -481,7 +494,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   }
   if (warp == kCaMmaWarp) tc::tmem_alloc(smem_u32(&tslot), kCaCols);
   const uint32_t sq = tc::smem_base(smem), ring = sq + 2 * tc::kTileBytes;
-  Walk walk = find_part(a, smem + (sq - smem_u32(smem)), sums);
+  Walk<KT> walk = find_part<KT>(a, smem + (sq - smem_u32(smem)), sums);
   tc::fence_before_sync();
   __syncthreads();     // the sums have been read: the tiles may be written over them
   tc::fence_proxy_async();
@@ -544,7 +557,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       const int begin = uniform(w.begin), end = uniform(w.end);
       if (begin < end) {
         const int last = uniform(w.last[t]), from = uniform(w.from[t]), ns = uniform(w.ns), sinks = uniform(w.ts);
-        const auto narrow = [&](int i) { return tile_narrow(a, sinks, i, i * kCaRows); };
+        const auto narrow = [&](int i) { return !Q8 && tile_narrow(a, sinks, i, i * KT); };
         bool more = false, before = false, few = false;
         int vslot = 0, vpar = 0;     // the last step's values
         wait(smem_u32(&bar.q), q_par);
@@ -554,11 +567,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           // this step's scores from key tile i, behind the last step's sums over value tile i - 1
           const bool keys = i < end, here = keys && i <= last && (i < ns || i >= from);
           const uint64_t kd = k0 + slot * desc_step(tc::kTileBytes), vd = v0 + vslot * desc_step(tc::kTileBytes);
-#pragma unroll
-          for (int part = 0; part < kParts; ++part) {   // (parts of a tile lie side by side in the ring)
-            if (i > begin) wait(smem_u32(&bar.full[vslot + part]), vpar);
-            if (keys) wait(smem_u32(&bar.full[slot + part]), par);
-          }
+          if (i > begin) wait(smem_u32(&bar.full[vslot]), vpar);
+          if (keys) wait(smem_u32(&bar.full[slot]), par);
           if (before) wait(smem_u32(&bar.p[t][0]), p_par);
           take_turn();
           lead &= __all_sync(0xffffffffu, wait.ok) != 0;
@@ -566,16 +576,19 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           if (before) {
             const auto sums = [&](int c0, int c1) {
 #pragma unroll
-              for (int part = 0; part < kParts; ++part)
-#pragma unroll
-                for (int c = c0; c < c1; ++c)
-                  mma_ts(to, ts + c * 8, vd + desc_step(part * tc::kTileBytes + c * 2048), kValues, more || c > 0 || part > 0);
+              for (int c = c0; c < c1; ++c)   // (INT8: the same weights meet both parts)
+                mma_ts(to, ts + (Q8 ? c & 3 : c) * 8, vd + desc_step(c * 2048), kValues, more || c > 0);
             };
             // the tensor core's queue holds about two products: a wait between them leaves it idle
             if (few) {
               wait(smem_u32(&bar.p[t][1]), p_par);
               lead &= __all_sync(0xffffffffu, wait.ok) != 0;
               if (lead) sums(0, kCaNarrow / 16);
+            } else if (Q8) {
+              wait(smem_u32(&bar.p[t][1]), p_par);
+              lead &= __all_sync(0xffffffffu, wait.ok) != 0;
+              tc::fence_after_sync();
+              if (lead) sums(0, kCaRows / 16);
             } else if (__all_sync(0xffffffffu, tc::mbar_wait(smem_u32(&bar.p[t][1]), p_par, 1))) {
               tc::fence_after_sync();
               if (lead) sums(0, kCaRows / 16);
@@ -596,10 +609,10 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             // last products take to issue
             if (here) {
 #pragma unroll
-              for (int c = 0; c < kParts * kD / 16; ++c) {
-                const uint64_t off = desc_step(((c & 7) >> 2) * tc::kKBlock + (c & 3) * 32);
-                tc::mma_f16(ts, qd + off, kd + off + desc_step((c >> 3) * tc::kTileBytes), scores, c > 0);
-                if (c == kParts * kD / 16 - 4) tc::mbar_arrive(smem_u32(&bar.turn[t ^ 1]));
+              for (int c = 0; c < kD / 16; ++c) {
+                const uint64_t off = desc_step((c >> 2) * tc::kKBlock + (c & 3) * 32);
+                tc::mma_f16(ts, qd + off, kd + off, scores, c > 0);
+                if (c == 4) tc::mbar_arrive(smem_u32(&bar.turn[t ^ 1]));
               }
               tc::commit(smem_u32(&bar.s[t]));
             } else {
@@ -609,17 +622,14 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           before = here;
           few = keys && narrow(i);
           if (lead) {
-#pragma unroll
-            for (int part = 0; part < kParts; ++part) {
-              if (i > begin) tc::commit(smem_u32(&bar.empty[vslot + part]));
-              if (keys) tc::commit(smem_u32(&bar.empty[slot + part]));
-            }
+            if (i > begin) tc::commit(smem_u32(&bar.empty[vslot]));
+            if (keys) tc::commit(smem_u32(&bar.empty[slot]));
             if (i == end - 1) tc::commit(smem_u32(&bar.qfree));   // the last scores
           }
           if (keys) {   // the values of tile i follow its keys in the ring
-            vslot = slot + kParts == kCaRing ? 0 : slot + kParts;
+            vslot = slot + 1 == kCaRing ? 0 : slot + 1;
             vpar = vslot == 0 ? par ^ 1 : par;
-            slot = vslot + kParts == kCaRing ? 0 : vslot + kParts;
+            slot = vslot + 1 == kCaRing ? 0 : vslot + 1;
             par = slot == 0 ? vpar ^ 1 : vpar;
           }
         }
@@ -627,12 +637,15 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       heard(n);
     }
   } else if (warp >= kCaLoadWarp) {
-    fewer_registers<kCaLoadRegs>();
+    if constexpr (Split<Q8>::load < 128)
+      fewer_registers<Split<Q8>::load>();
+    else
+      more_registers<Split<Q8>::load>();
     const int me = warp - kCaLoadWarp;
     const size_t layer0 = a.p.layer_rows() * a.layer;
     const uint8_t* k0 = a.p.k + layer0 * (Q8 ? kD : kD * 2);
     const uint8_t* v0 = a.p.v + layer0 * (Q8 ? kD : kD * 2);
-    int used = 0, qs = 0;   // uses of this warp's buffer (INT8: of every buffer); items whose queries were loaded
+    int used = 0, qs = 0;   // uses of this warp's buffer (INT8: buffers so far); items whose queries were loaded
     int ahead = 0;          // buffers of all items before, modulo the ring
     int cleared = 0;        // of this warp's tiles so far, those with rows to clear
     for (int n = 0;; ++n) {
@@ -646,7 +659,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         // the pool row of slot j, kNoRow for one that no row of the item sees
         const int first = uniform(a.qb.window > 0 ? max(w.pa[0] - a.qb.window + 1, 0) : 0);
         const auto place = [&](int i, int r) {
-          const int j = w.j0(i) + r;
+          const int j = w.j0<KT>(i) + r;
           uint32_t row = kNoRow;
           if (i < end && j < keys && (j >= first || j < a.qb.sinks)) {
             const uint32_t pg = div_of(static_cast<uint32_t>(j), a.p.ps);
@@ -671,28 +684,27 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           land(smem_u32(&bar.q));
         };
         if constexpr (Q8) {
-          // every warp has 32 rows of each tile; the next one's codes are under way meanwhile
-          CodeRows x;
-          uint32_t at = place(begin, me * 32 + lane);
-          load_codes(x, k0, a.p.km + layer0 * kMetaBytes, at);
+          // every warp has 16 keys of each tile; the next one's codes are under way meanwhile
+          const auto at = [&](int i) { return lane < 16 ? place(i, me * 16 + lane) : kNoRow; };
+          CodeRows k, v;
+          uint32_t now = at(begin), next = at(begin + 1);
+          load_codes(k, k0, a.p.km + layer0 * kMetaBytes, now);
+          load_codes(v, v0, a.p.vm + layer0 * kMetaBytes, now);
           for (int i = begin; i < end; ++i) {
-            const uint32_t next = place(i + 1, me * 32 + lane);
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-              wait(smem_u32(&bar.empty[2 * kv]), (used & 1) ^ 1);
-              wait(smem_u32(&bar.empty[2 * kv + 1]), (used & 1) ^ 1);
-              if (!__all_sync(0xffffffffu, wait.ok)) break;
-              store_codes(x, ring + 2 * kv * tc::kTileBytes, me * 32);
-              land(smem_u32(&bar.full[2 * kv]));
-              land(smem_u32(&bar.full[2 * kv + 1]));
-              if (kv == 0)
-                load_codes(x, v0, a.p.vm + layer0 * kMetaBytes, at);
-              else if (i + 1 < end)
-                load_codes(x, k0, a.p.km + layer0 * kMetaBytes, next);
-            }
-            ++used;
+            const auto put = [&](const CodeRows& x) {
+              const int slot = used & (kCaRing - 1);
+              wait(smem_u32(&bar.empty[slot]), (used / kCaRing & 1) ^ 1);
+              ++used;
+              if (!__all_sync(0xffffffffu, wait.ok)) return;
+              store_codes(x, ring + slot * tc::kTileBytes, me * 16);
+              land(smem_u32(&bar.full[slot]));
+            };
+            put(k);
+            if (i + 1 < end) load_codes(k, k0, a.p.km + layer0 * kMetaBytes, next);
+            put(v);
+            if (i + 1 < end) load_codes(v, v0, a.p.vm + layer0 * kMetaBytes, next);
+            next = at(i + 2);
             if (i == begin) queries();
-            at = next;
           }
         } else {
           // this warp has every fourth buffer: keys (c even) or values of tile begin + c / 2
@@ -702,7 +714,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           const auto look = [&](int i) {
             if (a.box > 0) {
               at[0] = at[1] = kNoRow;
-              const int r = lane * a.box, j = i < end ? w.j0(i) + r : 0;
+              const int r = lane * a.box, j = i < end ? w.j0<KT>(i) + r : 0;
               // boxes with a row that is seen; at[1] tells one whose page lies outside the pool
               if (i < end && r < kCaRows && j < keys && (j + a.box > first || j < a.qb.sinks)) {
                 const uint32_t pg = div_of(static_cast<uint32_t>(j), a.p.ps);
@@ -721,7 +733,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           const auto fetch = [&](int i, bool values) {
             const uint32_t dst = ring + me * tc::kTileBytes;
             const uint32_t boxes = __ballot_sync(0xffffffffu, at[0] != kNoRow), bad = __ballot_sync(0xffffffffu, at[1] != kNoRow);
-            const int j0 = w.j0(i);
+            const int j0 = w.j0<KT>(i);
             const int z0 = min(max(a.qb.sinks - j0, 0), kCaRows), z1 = min(first - j0, kCaRows), z2 = min(keys - j0, kCaRows);
             const bool clear = bad != 0 || (values && (z0 < z1 || z2 < kCaRows));
             const uint32_t on = smem_u32(clear ? &bar.boxes[me] : &bar.full[me]);
@@ -766,10 +778,11 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       heard(n);
     }
     // every release of this warp's buffer has arrived before the CTA ends
+    if (Q8) used = (used + kCaRing - 1 - me) / kCaRing;
     wait(smem_u32(&bar.empty[me]), (used & 1) ^ 1);
     if (qs > 0) wait(smem_u32(&bar.qfree), (qs - 1) & 1);
   } else {
-    more_registers<kCaSoftmaxRegs>();
+    more_registers<Split<Q8>::softmax>();
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;   // the thread's TMEM lane is its row
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + kCaO + t * 128;
@@ -785,15 +798,15 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           const int p = w.pa[t] + row % w.tb, last = min(p, w.keys - 1);
           for (int i = w.begin; i < w.end; ++i) {
             if (!w.sees(t, i)) continue;
-            const int j0 = w.j0(i);
-            const bool whole = tile_whole(a, w.pa[t], w.pb[t], w.keys, j0), few = tile_narrow(a, w.ts, i, j0);
+            const int j0 = w.j0<KT>(i);
+            const bool whole = tile_whole<KT>(a, w.pa[t], w.pb[t], w.keys, j0), few = !Q8 && tile_narrow(a, w.ts, i, j0);
             wait(smem_u32(&bar.s[t]), s_par);
             s_par ^= 1;
             tc::fence_after_sync();
             if (few)
-              softmax_tile<BF, kCaNarrow>(a, ts, to, false, p, last, j0, r, ready);
+              softmax_tile<BF, kCaNarrow, 1>(a, ts, to, false, p, last, j0, r, ready);
             else
-              softmax_tile<BF, kCaRows>(a, ts, to, whole, p, last, j0, r, ready);
+              softmax_tile<BF, KT, Q8 ? 2 : 1>(a, ts, to, whole, p, last, j0, r, ready);
           }
         }
         const bool any = w.last[t] >= 0;

@@ -45,24 +45,26 @@ MIKV_HD Rows rows_of(int32_t rows, int32_t held, bool from_start, int32_t start)
   return r;
 }
 
-// The key tiles that the rows of a block see, as KeyTiles says.
+// The key tiles of KT keys that the rows of a block see, as KeyTiles says.
+template <int KT>
 MIKV_HD KeyTiles chunk_tiles(const RowTiles& t, const Rows& r, int32_t window, int32_t sinks, int32_t blk) {
   const int32_t q0 = block_row(t, blk);
   const int32_t p1 = r.off + min_of(q0 + (t.pair_heads ? t.tb : 2 * t.tb), r.rows) - 1;   // the largest position
   const int32_t last = min_of(p1, r.keys - 1);
   const int32_t lo = window > 0 ? max_of(r.off + q0 - window + 1, 0) : 0;
-  const int32_t end = last < 0 ? 0 : last / kKeyRows + 1;
-  const int32_t st = window > 0 && sinks > 0 ? (min_of(sinks, max_of(r.keys, 1)) - 1) / kKeyRows + 1 : 0;
+  const int32_t end = last < 0 ? 0 : last / KT + 1;
+  const int32_t st = window > 0 && sinks > 0 ? (min_of(sinks, max_of(r.keys, 1)) - 1) / KT + 1 : 0;
   KeyTiles k;
-  k.tw0 = min_of(lo / kKeyRows, end);
+  k.tw0 = min_of(lo / KT, end);
   k.ts = min_of(st, k.tw0);
   k.tiles = k.ts + end - k.tw0;
   k.ns = max_of(k.ts, min_of(st, st > k.tw0 ? k.tiles : k.ts));
   return k;
 }
 // Places of each item of a block on the line.
+template <int KT>
 MIKV_HD int32_t chunk_places(const RowTiles& t, const Rows& r, int32_t window, int32_t sinks, int32_t blk) {
-  return kItemPlaces + max_of(1, chunk_tiles(t, r, window, sinks, blk).tiles);
+  return kItemPlaces + max_of(1, chunk_tiles<KT>(t, r, window, sinks, blk).tiles);
 }
 
 }  // namespace mikv

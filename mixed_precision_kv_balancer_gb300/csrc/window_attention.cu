@@ -594,9 +594,9 @@ __global__ void __launch_bounds__(kWaThreads, 1)
           s_par ^= 1;
           tc::fence_after_sync();
           if (tile_narrow(a, w, i))
-            softmax_tile<BF, kWaNarrow>(a, ts, to, false, p, p, j0, r, ready);
+            softmax_tile<BF, kWaNarrow, 1>(a, ts, to, false, p, p, j0, r, ready);
           else
-            softmax_tile<BF, kWaRows>(a, ts, to, tile_whole(a, tile, j0), p, p, j0, r, ready);
+            softmax_tile<BF, kWaRows, 1>(a, ts, to, tile_whole(a, tile, j0), p, p, j0, r, ready);
         }
         if (tile.last >= 0) {
           wait(smem_u32(&bar.o[t]), o_par);

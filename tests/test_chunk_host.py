@@ -41,17 +41,18 @@ static int check_rows(int rows, int rep) {
 }
 
 // the tiles of a block's list are those that one of its rows sees, each once, sinks first
+template <int KT>
 static int check_tiles(const RowTiles& t, const Rows& r, int window, int sinks) {
   for (int blk = 0; blk < t.blocks; ++blk) {
     const int q0 = block_row(t, blk), q1 = min_of(q0 + (t.pair_heads ? t.tb : 2 * t.tb), r.rows);
-    const KeyTiles k = chunk_tiles(t, r, window, sinks, blk);
-    std::vector<int> sees(r.keys / kKeyRows + 1, 0), sink(sees.size(), 0), listed(sees.size(), 0);
+    const KeyTiles k = chunk_tiles<KT>(t, r, window, sinks, blk);
+    std::vector<int> sees(r.keys / KT + 1, 0), sink(sees.size(), 0), listed(sees.size(), 0);
     for (int i = q0; i < q1; ++i) {
       const int p = r.off + i;
       for (int j = 0; j <= p && j < r.keys; ++j)
-        if (window == 0 || j > p - window || j < sinks) sees[j / kKeyRows] = 1;
+        if (window == 0 || j > p - window || j < sinks) sees[j / KT] = 1;
     }
-    for (int j = 0; j < min_of(sinks, r.keys); ++j) sink[j / kKeyRows] = window > 0;
+    for (int j = 0; j < min_of(sinks, r.keys); ++j) sink[j / KT] = window > 0;
     for (int i = 0; i < k.tiles; ++i) {
       const int tile = i < k.ts ? i : k.tw0 + i - k.ts;
       CHECK(tile >= 0 && tile < (int)sees.size() && !listed[tile]);
@@ -62,13 +63,14 @@ static int check_tiles(const RowTiles& t, const Rows& r, int window, int sinks) 
     int seen = 0;
     for (int x : sees) seen += x;
     CHECK(k.tiles <= seen + 1);
-    CHECK(chunk_places(t, r, window, sinks, blk) == kItemPlaces + max_of(1, k.tiles));
+    CHECK(chunk_places<KT>(t, r, window, sinks, blk) == kItemPlaces + max_of(1, k.tiles));
   }
   return 0;
 }
 
 // CTAs walk their parts as the kernel does: every item's tiles are taken once and in order; an item that is cut has
 // its parts in slots of their own, which the CTA that begins it can tell
+template <int KT>
 static int check_line(const std::vector<Rows>& reqs, int rep, int heads, int window, int sinks, int ctas) {
   struct Entry { int req, blk, places, items; long long base; };
   std::vector<Entry> line;
@@ -76,7 +78,7 @@ static int check_line(const std::vector<Rows>& reqs, int rep, int heads, int win
   for (size_t i = 0; i < reqs.size(); ++i) {
     const RowTiles t = row_tiles_of(reqs[i].rows, rep);
     for (int b = 0; b < t.blocks; ++b) {
-      const int p = chunk_places(t, reqs[i], window, sinks, b);
+      const int p = chunk_places<KT>(t, reqs[i], window, sinks, b);
       line.push_back({(int)i, b, p, heads * t.per, total});
       total += (long long)p * heads * t.per;
     }
@@ -159,12 +161,14 @@ int main() {
     const Rows r = request();
     CHECK(r.keys >= 0 && r.keys <= 900);
     const int window = pick(0, 3) ? pick(1, 700) : 0, sinks = pick(0, 2) ? pick(0, 300) : 0;
-    if (check_tiles(row_tiles_of(r.rows, pick(1, 17)), r, window, sinks)) return 1;
+    const RowTiles t = row_tiles_of(r.rows, pick(1, 17));
+    if (check_tiles<128>(t, r, window, sinks) || check_tiles<64>(t, r, window, sinks)) return 1;
   }
   for (int n = 0; n < 4000; ++n) {
     std::vector<Rows> reqs(pick(1, 30));
     for (Rows& r : reqs) r = request();
-    if (check_line(reqs, pick(1, 17), pick(1, 4), pick(0, 1) * pick(1, 500), pick(0, 200), pick(0, 3) ? 152 : pick(1, 152))) return 1;
+    const int rep = pick(1, 17), heads = pick(1, 4), window = pick(0, 1) * pick(1, 500), sinks = pick(0, 200), ctas = pick(0, 3) ? 152 : pick(1, 152);
+    if (check_line<128>(reqs, rep, heads, window, sinks, ctas) || check_line<64>(reqs, rep, heads, window, sinks, ctas)) return 1;
   }
   // positions at their limits stay inside 32 bits
   for (int rows : {1, 64, 65, 1 << 20})
@@ -175,7 +179,7 @@ int main() {
             const Rows r = rows_of(rows, held, true, start);
             const RowTiles t = row_tiles_of(rows, 3);
             CHECK(r.off <= kMaxPos && r.keys <= held);
-            for (int blk : {0, t.blocks - 1}) CHECK(chunk_tiles(t, r, window, sinks, blk).tiles >= 0);
+            for (int blk : {0, t.blocks - 1}) CHECK(chunk_tiles<64>(t, r, window, sinks, blk).tiles >= 0);
           }
   CHECK(rows_of(1 << 20, 5, false, 0).off == 5 - (1 << 20));
   return 0;
