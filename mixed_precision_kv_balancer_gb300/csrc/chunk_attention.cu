@@ -41,23 +41,24 @@ using namespace at;
 constexpr int kCaRows = kKeyRows;           // query rows of a tile, and rows of a buffer
 constexpr int kCaNarrow = 32;               // columns of a tile that holds the last few sinks
 constexpr int kCaRing = 4;
-constexpr int kCaThreads = 512;             // 2 x 4 softmax warps, 4 loading warps, 2 MMA warps, the walking warp, an idle one
-constexpr int kCaLoadWarp = 8, kCaLoaders = 4, kCaMmaWarp = 12, kCaWalkWarp = 14;
-// Registers of a thread, by warpgroups; 128 each at launch, 65,536 in all.
-constexpr int kCaMmaRegs = 72;
+// Warps: 2 x 4 for the softmax of a query tile each, the loading ones, 2 that issue products, the walking one, an idle one.
+// INT8 takes eight loading warps: converting codes is most of the work beside the products (four of them
+// bring 64 single tokens behind up to 8192 slots in 463 us, eight in 365).  Registers of a thread, by warpgroups, are shares of those at launch.
 template <bool Q8>
-struct Split {
-  static constexpr int softmax = Q8 ? 152 : 176, load = Q8 ? 136 : 88;
-  static_assert(256 * softmax + 128 * (load + kCaMmaRegs) == kCaThreads * 128, "register split");
+struct Warps {
+  static constexpr int load = 8, loaders = Q8 ? 8 : 4, mma = load + loaders, walk = mma + 2, threads = (mma + 4) * 32;
+  static constexpr int launch_regs = Q8 ? 96 : 128, softmax_regs = Q8 ? 128 : 176, load_regs = Q8 ? 80 : 88, mma_regs = Q8 ? 64 : 72;
+  static_assert(256 * softmax_regs + 32 * loaders * load_regs + 128 * mma_regs <= threads * launch_regs && threads * launch_regs <= 65536,
+                "register split");
 };
-template <int TYPE>
-constexpr int kKeys = TYPE == MIKV_PAGES_INT8 ? 64 : kCaRows;   // of a tile
 constexpr int kCaTold = 4;                  // items that the other warps may be behind
 constexpr int kCaSmem = (2 + kCaRing) * tc::kTileBytes + 1024;
 constexpr uint32_t kCaCols = 512;           // S_0, S_1, O_0, O_1: 128 columns each
 constexpr uint32_t kCaO = 256;
 constexpr int kMaxRequests = 4096;
 constexpr int kMaxChunkRows = 1 << 20;      // of a call: the sums of its blocks fit the ring
+template <int TYPE>
+constexpr int kKeys = TYPE == MIKV_PAGES_INT8 ? 64 : kCaRows;   // of a tile
 
 struct Mask {
   int32_t window, sinks;
@@ -236,6 +237,7 @@ __device__ __forceinline__ Cut* part_cut(const ChunkArgs& a, int c) {
 }
 
 // Inclusive sum over the block; `sums` holds a value a warp.
+template <int THREADS>
 __device__ __forceinline__ int64_t scan_block(int64_t v, int64_t* sums, int64_t& total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
@@ -248,7 +250,7 @@ __device__ __forceinline__ int64_t scan_block(int64_t v, int64_t* sums, int64_t&
   __syncthreads();
   total = 0;
 #pragma unroll
-  for (int i = 0; i < kCaThreads / 32; ++i) {
+  for (int i = 0; i < THREADS / 32; ++i) {
     const int64_t s = sums[i];
     if (i < w) v += s;
     total += s;
@@ -271,20 +273,20 @@ __device__ __forceinline__ int find_entry(const T* base, int n, int64_t x) {
 
 // This CTA's part of the line, by all threads of it, for its walking warp.  `scratch`: (n + 1) * 4 bytes for the blocks before each
 // request, and 8 bytes a block for the places before it.
-template <int KT>
+template <int KT, class W>
 __device__ __forceinline__ Walk<KT> find_part(const ChunkArgs& a, uint8_t* scratch, int64_t* sums) {
   const int tid = threadIdx.x;
   int64_t* place = reinterpret_cast<int64_t*>(scratch);
   int32_t* blocks = reinterpret_cast<int32_t*>(place + a.rows / kCaRows + a.n + 2);   // a request has a block more than rows / 128 at most
   int64_t done = 0, total;
-  for (int i0 = 0; i0 < a.n; i0 += kCaThreads) {
+  for (int i0 = 0; i0 < a.n; i0 += W::threads) {
     const int i = i0 + tid;
     int64_t v = 0;
     if (i < a.n) {
       const int rows = max(request_row(a, i + 1) - request_row(a, i), 0);
       v = row_tiles_of(rows, a.rep).blocks;
     }
-    v = scan_block(v, sums, total);
+    v = scan_block<W::threads>(v, sums, total);
     if (i < a.n) blocks[i + 1] = static_cast<int32_t>(done + v);
     done += total;
   }
@@ -293,7 +295,7 @@ __device__ __forceinline__ Walk<KT> find_part(const ChunkArgs& a, uint8_t* scrat
   // requests whose rows overlap (row_start does not ascend) could have more blocks than there is room for
   const int entries = static_cast<int>(min(done, static_cast<int64_t>(a.rows / kCaRows + a.n + 1)));
   done = 0;
-  for (int e0 = 0; e0 < entries; e0 += kCaThreads) {
+  for (int e0 = 0; e0 < entries; e0 += W::threads) {
     const int e = e0 + tid;
     int64_t v = 0;
     if (e < entries) {
@@ -301,7 +303,7 @@ __device__ __forceinline__ Walk<KT> find_part(const ChunkArgs& a, uint8_t* scrat
       const Request q = request_of(a, i);
       v = static_cast<int64_t>(chunk_places<KT>(q.t, q.r, a.qb.window, a.qb.sinks, e - blocks[i])) * a.p.Hkv * q.t.per;
     }
-    v = scan_block(v, sums, total);
+    v = scan_block<W::threads>(v, sums, total);
     if (e < entries) place[e + 1] = done + v;
     done += total;
   }
@@ -309,7 +311,7 @@ __device__ __forceinline__ Walk<KT> find_part(const ChunkArgs& a, uint8_t* scrat
   __syncthreads();
   Walk<KT> w;
   w.idle = true;
-  if (tid / 32 != kCaWalkWarp) return w;
+  if (tid / 32 != W::walk) return w;
   const int workers = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(a.ctas), done / 2))), c = blockIdx.x;
   Cut cut = {};
   cut.last = -1;
@@ -373,11 +375,12 @@ __device__ __forceinline__ void copy_tile(uint32_t dst, const uint8_t* rows, con
     cp_async16(swz[j & 3] + j * 256, rows + static_cast<size_t>(ok ? row : 0u) * (kD * 2), ok);
   }
 }
-// 32 rows of a query tile from row r0 on by one warp, lane l holding the address of row r0 + l (null: zeros).
+// ROWS rows of a query tile from row r0 on by one warp, lane l holding the address of row r0 + l (null: zeros).
+template <int ROWS>
 __device__ __forceinline__ void copy_queries(uint32_t dst, int r0, const uint8_t* src, const uint8_t* any) {
   const int lane = threadIdx.x & 31, piece = lane & 15;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
+  for (int j = 0; j < ROWS / 2; ++j) {
     const int e = 2 * j + (lane >> 4), r = r0 + e;
     const uint64_t x = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), e);
     cp_async16(dst + (piece >> 3) * tc::kKBlock + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
@@ -405,20 +408,22 @@ __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec
 template <int REGS>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(REGS)); }
 
-// The value s * code + z of 16 codes as two fp16 numbers each, hi and what is left.
+// The value s * code + z of 16 codes as two fp16 numbers each: the first rounded towards zero, so that none passes
+// fp16's largest number, and what is left.
 __device__ __forceinline__ void split16(const uint4& c, __half2 m, uint32_t (&hi)[8], uint32_t (&lo)[8]) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
   const float s = __low2float(m), z = __high2float(m);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     // a code as the last bits of 2^23 + code; s * code is exact
-    const float x0 = __uint_as_float(__byte_perm(w[e >> 1], 0x4B000000u, 0x7440u + 2 * (e & 1))) - 8388608.f;
-    const float x1 = __uint_as_float(__byte_perm(w[e >> 1], 0x4B000000u, 0x7441u + 2 * (e & 1))) - 8388608.f;
-    const float f0 = fmaf(s, x0, z), f1 = fmaf(s, x1, z);
-    // (the largest values may lie a little above fp16's largest number: held there, the rest is in the second)
-    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;\n" : "=r"(hi[e]) : "f"(f1), "f"(f0));
-    const __half2 h = *reinterpret_cast<const __half2*>(&hi[e]);
-    lo[e] = pack2<false>(f0 - __low2float(h), f1 - __high2float(h));
+    const float2 x = make_float2(__uint_as_float(__byte_perm(w[e >> 1], 0x4B000000u, 0x7440u + 2 * (e & 1))),
+                                 __uint_as_float(__byte_perm(w[e >> 1], 0x4B000000u, 0x7441u + 2 * (e & 1))));
+    const float2 f = __ffma2_rn(__fadd2_rn(x, make_float2(-8388608.f, -8388608.f)), make_float2(s, s), make_float2(z, z));
+    // (cut to fp16's 11 bits by a mask: a conversion back costs more)
+    const float2 h = make_float2(__uint_as_float(__float_as_uint(f.x) & 0xffffe000u), __uint_as_float(__float_as_uint(f.y) & 0xffffe000u));
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;\n" : "=r"(hi[e]) : "f"(h.y), "f"(h.x));
+    const float2 r = __fadd2_rn(f, make_float2(-h.x, -h.y));
+    lo[e] = pack2<false>(r.x, r.y);
   }
 }
 // 16 keys of an INT8 tile: the codes and scales that a lane takes of them, four keys an instruction, 16 channels of each.
@@ -461,27 +466,28 @@ __device__ __forceinline__ void store_codes(const CodeRows& x, uint32_t dst, int
 }
 
 template <int TYPE>
-__global__ void __launch_bounds__(kCaThreads, 1)
+__global__ void __launch_bounds__(Warps<TYPE == MIKV_PAGES_INT8>::threads, 1)
     chunk_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const ChunkArgs a) {
   constexpr bool BF = TYPE == MIKV_PAGES_BF16, Q8 = TYPE == MIKV_PAGES_INT8;
   constexpr int KT = kKeys<TYPE>;
+  using W = Warps<Q8>;
   extern __shared__ uint8_t smem[];
   __shared__ CaBars bar;
   __shared__ Work works[kCaTold];
-  __shared__ int64_t sums[kCaThreads / 32];
+  __shared__ int64_t sums[W::threads / 32];
   __shared__ uint32_t tslot;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kCaRing; ++i) {
-      tc::mbar_init(smem_u32(&bar.full[i]), Q8 ? kCaLoaders : 1);
+      tc::mbar_init(smem_u32(&bar.full[i]), Q8 ? W::loaders / 2 : 1);
       tc::mbar_init(smem_u32(&bar.empty[i]), 2);
       tc::mbar_init(smem_u32(&bar.boxes[i]), 1);
     }
     for (int i = 0; i < kCaTold; ++i) {
       tc::mbar_init(smem_u32(&bar.told[i]), 1);
-      tc::mbar_init(smem_u32(&bar.heard[i]), kCaMmaWarp + 2);   // all but the last two warps
+      tc::mbar_init(smem_u32(&bar.heard[i]), W::walk);   // all but the last two warps
     }
-    tc::mbar_init(smem_u32(&bar.q), kCaLoaders);
+    tc::mbar_init(smem_u32(&bar.q), W::loaders);
     tc::mbar_init(smem_u32(&bar.qfree), 2);
     for (int t = 0; t < 2; ++t) {
       tc::mbar_init(smem_u32(&bar.turn[t]), 1);
@@ -492,9 +498,9 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     }
     tc::mbar_init_fence();
   }
-  if (warp == kCaMmaWarp) tc::tmem_alloc(smem_u32(&tslot), kCaCols);
+  if (warp == W::mma) tc::tmem_alloc(smem_u32(&tslot), kCaCols);
   const uint32_t sq = tc::smem_base(smem), ring = sq + 2 * tc::kTileBytes;
-  Walk<KT> walk = find_part<KT>(a, smem + (sq - smem_u32(smem)), sums);
+  Walk<KT> walk = find_part<KT, W>(a, smem + (sq - smem_u32(smem)), sums);
   tc::fence_before_sync();
   __syncthreads();     // the sums have been read: the tiles may be written over them
   tc::fence_proxy_async();
@@ -513,10 +519,10 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     if (lane == 0) tc::mbar_arrive(smem_u32(&bar.heard[n % kCaTold]));
   };
 
-  if (warp >= kCaMmaWarp) fewer_registers<kCaMmaRegs>();   // (one instruction for all of a warpgroup)
-  if (warp >= kCaWalkWarp) {
+  if (warp >= W::mma) fewer_registers<W::mma_regs>();   // (one instruction for all of a warpgroup)
+  if (warp >= W::walk) {
     bool some = !walk.idle;
-    for (int n = 0; warp == kCaWalkWarp; ++n) {
+    for (int n = 0; warp == W::walk; ++n) {
       if (n >= kCaTold) wait(smem_u32(&bar.heard[n % kCaTold]), (n / kCaTold - 1) & 1);
       Work next;
       if (some) next = walk.work(a);
@@ -531,10 +537,10 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       if (!__all_sync(0xffffffffu, some && wait.ok)) break;
       some = walk.next(a, wait.ok);
     }
-  } else if (warp >= kCaMmaWarp) {
+  } else if (warp >= W::mma) {
     // One warp per query tile, so that neither waits in the other's place.  The whole warp walks
     // the steps, so that addresses and descriptors stay uniform; one elected lane issues.
-    const int t = warp - kCaMmaWarp;
+    const int t = warp - W::mma;
     bool lead = elect_one();
     constexpr uint32_t kType = BF ? (1u << 7) | (1u << 10) : 0u;
     constexpr uint32_t kScores = tc::idesc_f16(kCaRows, kCaRows) | kType, kFew = tc::idesc_f16(kCaRows, kCaNarrow) | kType;
@@ -636,16 +642,13 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       }
       heard(n);
     }
-  } else if (warp >= kCaLoadWarp) {
-    if constexpr (Split<Q8>::load < 128)
-      fewer_registers<Split<Q8>::load>();
-    else
-      more_registers<Split<Q8>::load>();
-    const int me = warp - kCaLoadWarp;
+  } else if (warp >= W::load) {
+    fewer_registers<W::load_regs>();
+    const int me = warp - W::load;
     const size_t layer0 = a.p.layer_rows() * a.layer;
     const uint8_t* k0 = a.p.k + layer0 * (Q8 ? kD : kD * 2);
     const uint8_t* v0 = a.p.v + layer0 * (Q8 ? kD : kD * 2);
-    int used = 0, qs = 0;   // uses of this warp's buffer (INT8: buffers so far); items whose queries were loaded
+    int used = 0, qs = 0;   // uses of this warp's buffer (INT8: tiles so far); items whose queries were loaded
     int ahead = 0;          // buffers of all items before, modulo the ring
     int cleared = 0;        // of this warp's tiles so far, those with rows to clear
     for (int n = 0;; ++n) {
@@ -668,15 +671,16 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           }
           return row;
         };
-        // a quarter of the queries; the last item's products still read theirs
+        // this warp's share of the queries; the last item's products still read theirs
         const auto queries = [&] {
           if (qs > 0) wait(smem_u32(&bar.qfree), (qs - 1) & 1);
           ++qs;
           if (!__all_sync(0xffffffffu, wait.ok)) return;
-          const int r = me * 32 + lane, sub = r / w.tb;
+          constexpr int kRows = kCaRows / W::loaders;
+          const int r = me * kRows + lane % kRows, sub = r / w.tb;
           for (int t = 0; t < w.nt; ++t) {
             const int q = w.q0[t] + r - sub * w.tb;
-            copy_queries(sq + t * tc::kTileBytes, me * 32,
+            copy_queries<kRows>(sq + t * tc::kTileBytes, me * kRows,
                          sub < w.heads[t] && q < w.rows ? a.q.row(0, w.head[t] + sub, w.row0 + q) : nullptr, a.q.p);
           }
           cp_async_commit();
@@ -684,25 +688,23 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           land(smem_u32(&bar.q));
         };
         if constexpr (Q8) {
-          // every warp has 16 keys of each tile; the next one's codes are under way meanwhile
-          const auto at = [&](int i) { return lane < 16 ? place(i, me * 16 + lane) : kNoRow; };
-          CodeRows k, v;
-          uint32_t now = at(begin), next = at(begin + 1);
-          load_codes(k, k0, a.p.km + layer0 * kMetaBytes, now);
-          load_codes(v, v0, a.p.vm + layer0 * kMetaBytes, now);
+          // four warps for the keys and four for the values, 16 of each tile; the next one's codes are under way meanwhile
+          const int kv = me >> 2, r0 = (me & 3) * 16;
+          const uint8_t* codes = kv ? v0 : k0;
+          const uint8_t* meta = (kv ? a.p.vm : a.p.km) + layer0 * kMetaBytes;
+          const auto at = [&](int i) { return lane < 16 ? place(i, r0 + lane) : kNoRow; };
+          CodeRows x;
+          load_codes(x, codes, meta, at(begin));
+          uint32_t next = at(begin + 1);
           for (int i = begin; i < end; ++i) {
-            const auto put = [&](const CodeRows& x) {
-              const int slot = used & (kCaRing - 1);
-              wait(smem_u32(&bar.empty[slot]), (used / kCaRing & 1) ^ 1);
-              ++used;
-              if (!__all_sync(0xffffffffu, wait.ok)) return;
-              store_codes(x, ring + slot * tc::kTileBytes, me * 16);
+            const int slot = (2 * used + kv) & (kCaRing - 1);
+            wait(smem_u32(&bar.empty[slot]), (used / 2 & 1) ^ 1);
+            ++used;
+            if (__all_sync(0xffffffffu, wait.ok)) {
+              store_codes(x, ring + slot * tc::kTileBytes, r0);
               land(smem_u32(&bar.full[slot]));
-            };
-            put(k);
-            if (i + 1 < end) load_codes(k, k0, a.p.km + layer0 * kMetaBytes, next);
-            put(v);
-            if (i + 1 < end) load_codes(v, v0, a.p.vm + layer0 * kMetaBytes, next);
+            }
+            if (i + 1 < end) load_codes(x, codes, meta, next);
             next = at(i + 2);
             if (i == begin) queries();
           }
@@ -778,11 +780,11 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       heard(n);
     }
     // every release of this warp's buffer has arrived before the CTA ends
-    if (Q8) used = (used + kCaRing - 1 - me) / kCaRing;
-    wait(smem_u32(&bar.empty[me]), (used & 1) ^ 1);
+    for (int c = Q8 ? me >> 2 : me; c < kCaRing; c += Q8 ? 2 : kCaRing)   // INT8: tile u's keys or values were in buffer (2 u + kv) % 4
+      wait(smem_u32(&bar.empty[c]), ((Q8 ? (used + 1 - (c >> 1)) / 2 : used) & 1) ^ 1);
     if (qs > 0) wait(smem_u32(&bar.qfree), (qs - 1) & 1);
   } else {
-    more_registers<Split<Q8>::softmax>();
+    more_registers<W::softmax_regs>();
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;   // the thread's TMEM lane is its row
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + kCaO + t * 128;
@@ -865,7 +867,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   if (!wait.ok) tc::report_giveup(tc::kGiveupChunk);
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == kCaMmaWarp) tc::tmem_dealloc(tmem, kCaCols);
+  if (warp == W::mma) tc::tmem_dealloc(tmem, kCaCols);
 }
 
 // CTA (slice, c): joins STEPS * ROWS rows of the item that CTA c has begun and not ended, in a fixed order.  A thread
@@ -1001,10 +1003,18 @@ int launch(const ChunkArgs& a, cudaStream_t st) {
     if (int e = encode_pool(&km, a.p.k, a, "keys")) return e;
     if (int e = encode_pool(&vm, a.p.v, a, "values")) return e;
   }
+  using W = Warps<TYPE == MIKV_PAGES_INT8>;
   const auto kern = chunk_attention_kernel<TYPE>;
+  // the warps share out what the block has at launch: with less of it they would wait for ever
+  static const cudaError_t built = [&] {
+    cudaFuncAttributes f;
+    const cudaError_t e = cudaFuncGetAttributes(&f, kern);
+    return e != cudaSuccess ? e : f.numRegs == W::launch_regs ? cudaSuccess : cudaErrorLaunchOutOfResources;
+  }();
+  if (built != cudaSuccess) return check_launch_after(built, "chunk_attention_kernel");
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCaSmem);
   if (e != cudaSuccess) return check_launch_after(e, "chunk_attention_kernel");
-  kern<<<a.ctas, kCaThreads, kCaSmem, st>>>(km, vm, a);
+  kern<<<a.ctas, W::threads, kCaSmem, st>>>(km, vm, a);
   if (int r = check_launch("chunk_attention_kernel")) return r;
   // Few rows an item: many parts, perhaps, and threads that share them; else 64 rows a CTA, so that all CTAs
   // of a call fit the SMs at once.
