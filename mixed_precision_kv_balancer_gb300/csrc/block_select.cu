@@ -9,8 +9,9 @@
 // heads of a group read one set of blocks: a block's score is the largest of theirs.
 //
 // Two kernels: scores of all blocks (bound by HBM: 260 bytes a block and key head, against 64 four-term
-// integer products a query head), and the choice of the `keep` best of each (row, key head) by
-// a radix search of the scores' bits, written in the blocks' order.
+// integer products a query head), and the choice of the `keep` best of each (row, key head), written in the
+// blocks' order.  The choice is a search by digits of the scores' bits, but of digits that begin below what all
+// of a unit's scores share: scores of one unit lie close together, and counters of their first bits would all be hit at once.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -26,10 +27,11 @@ namespace {
 
 constexpr int kBsThreads = 128;
 constexpr int kBsWarps = kBsThreads / 32;
-constexpr int kBsHeads = 8;            // query heads of a pass
-constexpr int kBsPass = 2;             // warp-steps of 32 blocks a warp makes
-constexpr int kBsBlocks = kBsThreads * kBsPass;   // blocks of a CTA
+constexpr int kBsSteps = 2;                       // of 32 blocks a warp
+constexpr int kBsBlocks = kBsThreads * kBsSteps;  // blocks of a CTA
+constexpr int kBsSmem = kBsSteps * kBsWarps * 32 * 2 * kD;   // their bounds
 constexpr int kPickThreads = 512;
+constexpr int kPickDigit = 11;                    // bits of a digit
 constexpr uint32_t kAlways = 0xffffffffu;   // above every score
 
 struct SelectArgs {
@@ -63,12 +65,14 @@ __device__ __forceinline__ uint32_t ordered(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// CTA: kBsBlocks blocks of one (row, key head).  A warp brings the bounds of 32 blocks to shared memory in
-// whole lines; then a lane has a block of its own, so that no sum crosses lanes.
+// CTA: kBsBlocks blocks of one (row, key head), all requested before anything else is done.  A warp brings the
+// bounds of 32 blocks to shared memory in whole lines; then a lane has a block of its own, so that no
+// sum crosses lanes.  HEADS query heads a pass.
+template <int HEADS>
 __global__ void __launch_bounds__(kBsThreads) block_score_kernel(const SelectArgs a) {
-  __shared__ __align__(16) uint4 s_b[kBsWarps][32 * 16];              // 16 pieces a block, swizzled by the block
-  __shared__ __align__(16) uint32_t s_q[kBsHeads][2 * kD / 4];        // codes below 0, codes above 0
-  __shared__ float s_scale[kBsHeads];
+  extern __shared__ __align__(16) uint4 s_b[];                       // [step][warp][32 blocks][16 pieces], swizzled by the block
+  __shared__ __align__(16) uint32_t s_q[HEADS][2 * kD / 4];          // codes below 0, codes above 0
+  __shared__ float s_scale[HEADS];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int unit = blockIdx.x / a.chunks, b0 = (blockIdx.x - unit * a.chunks) * kBsBlocks;
   const int r = unit / a.p.Hkv, h = unit - r * a.p.Hkv;
@@ -79,11 +83,30 @@ __global__ void __launch_bounds__(kBsThreads) block_score_kernel(const SelectArg
   const bool bf = a.p.type == MIKV_PAGES_BF16;
   const int32_t* table = a.p.table + static_cast<size_t>(seq) * a.p.max_pages;
   const size_t layer0 = static_cast<size_t>(a.layer) * a.p.n_pages * a.p.Hkv;
-  float best[kBsPass];
+  const auto block_of = [&](int i) { return b0 + (i * kBsWarps + w) * 32 + lane; };
+  const auto pieces = [&](int i) { return s_b + (i * kBsWarps + w) * (32 * 16); };
+  bool there[kBsSteps];
+  float sb[kBsSteps], best[kBsSteps];
 #pragma unroll
-  for (int i = 0; i < kBsPass; ++i) best[i] = -INFINITY;
-  for (int g0 = 0; g0 < a.rep; g0 += kBsHeads) {
-    const int heads = min(kBsHeads, a.rep - g0);
+  for (int i = 0; i < kBsSteps; ++i) {
+    const int b = block_of(i);
+    const int32_t page = b < nb ? table[b] : -1;
+    there[i] = a.p.has(page);
+    const uint32_t at = there[i] ? static_cast<uint32_t>(page) * a.p.Hkv + h : 0;   // (below 2^32, like the pool's rows)
+    sb[i] = there[i] ? a.scales[layer0 + at] : 0.f;
+    best[i] = -INFINITY;
+    uint4* dst = pieces(i);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {   // two blocks an instruction
+      const int e = 2 * j + (lane >> 4), piece = lane & 15;
+      const uint32_t src = __shfl_sync(0xffffffffu, at, e);
+      const bool ok = __shfl_sync(0xffffffffu, static_cast<int>(there[i]), e);
+      cp_async16(smem_u32(dst + e * 16 + (piece ^ (e & 15))), a.bounds + (layer0 + src) * (2 * kD) + piece * 16, ok);
+    }
+    cp_async_commit();
+  }
+  for (int g0 = 0; g0 < a.rep; g0 += HEADS) {
+    const int heads = min(HEADS, a.rep - g0);
     if (g0 > 0) __syncthreads();
     for (int e = w; e < heads; e += kBsWarps) {   // a warp per query head: four channels a lane
       const uint2 v = reinterpret_cast<const uint2*>(a.q + (static_cast<size_t>(r) * a.Hq + h * a.rep + g0 + e) * kD)[lane];
@@ -114,62 +137,50 @@ __global__ void __launch_bounds__(kBsThreads) block_score_kernel(const SelectArg
       s_q[e][kD / 4 + lane] = pos;
       if (lane == 0) s_scale[e] = s;
     }
+    cp_async_wait<0>();
     __syncthreads();
+    int u[kBsSteps][HEADS] = {};
+#pragma unroll 2
+    for (int c = 0; c < 16; ++c) {
+      uint4 x[kBsSteps];
 #pragma unroll
-    for (int i = 0; i < kBsPass; ++i) {
-      const int b = b0 + (i * kBsWarps + w) * 32;
-      if (b >= nb) break;
-      const int32_t page = b + lane < nb ? table[b + lane] : -1;
-      const bool there = a.p.has(page);
-      const size_t at = layer0 + static_cast<size_t>(there ? page : 0) * a.p.Hkv + h;
-      __syncwarp();   // the last step's pieces have been read
+      for (int i = 0; i < kBsSteps; ++i) x[i] = pieces(i)[lane * 16 + (c ^ (lane & 15))];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {   // two blocks an instruction
-        const int e = 2 * j + (lane >> 4), piece = lane & 15;
-        const size_t src = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(at), e);
-        const bool ok = __shfl_sync(0xffffffffu, static_cast<int>(there), e);
-        cp_async16(smem_u32(&s_b[w][e * 16 + (piece ^ (e & 15))]), a.bounds + src * (2 * kD) + piece * 16, ok);
-      }
-      cp_async_commit();
-      const float sb = there ? a.scales[at] : 0.f;
-      cp_async_wait<0>();
-      __syncwarp();
-      int u[kBsHeads];
+      for (int e = 0; e < HEADS; ++e) {
+        const uint4 y = reinterpret_cast<const uint4*>(s_q[e])[c];
 #pragma unroll
-      for (int e = 0; e < kBsHeads; ++e) u[e] = 0;
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const uint4 x = s_b[w][lane * 16 + (c ^ (lane & 15))];
-#pragma unroll
-        for (int e = 0; e < kBsHeads; ++e) {
-          const uint4 y = reinterpret_cast<const uint4*>(s_q[e])[c];
-          u[e] = __dp4a(static_cast<int>(x.x), static_cast<int>(y.x), u[e]);
-          u[e] = __dp4a(static_cast<int>(x.y), static_cast<int>(y.y), u[e]);
-          u[e] = __dp4a(static_cast<int>(x.z), static_cast<int>(y.z), u[e]);
-          u[e] = __dp4a(static_cast<int>(x.w), static_cast<int>(y.w), u[e]);
+        for (int i = 0; i < kBsSteps; ++i) {
+          u[i][e] = __dp4a(static_cast<int>(x[i].x), static_cast<int>(y.x), u[i][e]);
+          u[i][e] = __dp4a(static_cast<int>(x[i].y), static_cast<int>(y.y), u[i][e]);
+          u[i][e] = __dp4a(static_cast<int>(x[i].z), static_cast<int>(y.z), u[i][e]);
+          u[i][e] = __dp4a(static_cast<int>(x[i].w), static_cast<int>(y.w), u[i][e]);
         }
-      }
-#pragma unroll
-      for (int e = 0; e < kBsHeads; ++e)
-        if (e < heads) {
-          const float s = __fmul_rn(__fmul_rn(static_cast<float>(u[e]), sb), s_scale[e]);
-          best[i] = fmaxf(best[i], isnan(s) ? INFINITY : s);
-        }
-      if (g0 + kBsHeads >= a.rep && b + lane < nb) {
-        const int x = b + lane;
-        uint32_t key = ordered(best[i]);
-        if (!there) {   // a block without a page is the last choice
-          key = 0;
-          tc::report_giveup(tc::kBadPage);
-        }
-        if (x < a.first || x >= nb - a.recent) key = kAlways;
-        a.keys[static_cast<size_t>(unit) * a.p.max_pages + x] = key;
       }
     }
+#pragma unroll
+    for (int i = 0; i < kBsSteps; ++i)
+#pragma unroll
+      for (int e = 0; e < HEADS; ++e)
+        if (e < heads) {
+          const float s = __fmul_rn(__fmul_rn(static_cast<float>(u[i][e]), sb[i]), s_scale[e]);
+          best[i] = fmaxf(best[i], isnan(s) ? INFINITY : s);
+        }
+  }
+#pragma unroll
+  for (int i = 0; i < kBsSteps; ++i) {
+    const int b = block_of(i);
+    if (b >= nb) break;
+    uint32_t key = ordered(best[i]);
+    if (!there[i]) {   // a block without a page is the last choice
+      key = 0;
+      tc::report_giveup(tc::kBadPage);
+    }
+    if (b < a.first || b >= nb - a.recent) key = kAlways;
+    a.keys[static_cast<size_t>(unit) * a.p.max_pages + b] = key;
   }
 }
 
-// Inclusive sums of two counts over the block.
+// Inclusive sums of two counts (32 bits each) over the block.
 __device__ __forceinline__ uint64_t scan2(uint64_t v, uint64_t* warp_sums, uint64_t& total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
@@ -190,12 +201,16 @@ __device__ __forceinline__ uint64_t scan2(uint64_t v, uint64_t* warp_sums, uint6
   return v + before;
 }
 
-// CTA (row, key head): the `keep` largest keys, equal ones by their number, in the blocks' order.
+// CTA (row, key head): the `keep` largest keys, equal ones by their number, in the blocks' order.  KEYS > 0: a thread
+// holds KEYS keys that follow one another; 0: keys are read again for every digit, in passes over all of them.
+template <int KEYS>
 __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectArgs a) {
-  __shared__ uint32_t hist[256];
+  constexpr int kBins = 1 << kPickDigit, kOwn = kBins / kPickThreads;   // counters of a thread
+  constexpr int kMine = KEYS > 0 ? KEYS : 1;
+  __shared__ uint32_t hist[kBins];
   __shared__ uint64_t warp_sums[kPickThreads / 32];
-  __shared__ uint32_t s_digit, s_above;
-  const int tid = threadIdx.x, unit = blockIdx.x, r = unit / a.p.Hkv;
+  __shared__ uint32_t s_lo, s_hi, s_bin, s_above, s_count;
+  const int tid = threadIdx.x, lane = tid & 31, unit = blockIdx.x, r = unit / a.p.Hkv;
   int32_t seq;
   const int32_t nb = blocks_of_row(a, r, seq), n = min(nb, a.keep);
   int32_t* sel = a.sel + static_cast<size_t>(unit) * a.keep;
@@ -205,56 +220,122 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectAr
   pdl_wait();
   if (nb <= a.keep) return;
   const uint32_t* keys = a.keys + static_cast<size_t>(unit) * a.p.max_pages;
-  uint32_t prefix = 0, mask = 0;     // the digits of the smallest key taken, so far
-  int need = n;                      // how many keys with that prefix are taken
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kPickThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < nb; i += kPickThreads) {
-      const uint32_t k = keys[i];
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
-    }
-    __syncthreads();
-    if (tid < 32) {   // eight digits a lane, from the top
-      uint32_t own = 0;
+  uint32_t k[kMine];
+  if (KEYS > 0) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) own += hist[255 - (tid * 8 + e)];
-      uint32_t incl = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
-        if (tid >= o) incl += u;
-      }
-      uint32_t above = incl - own;
-      if (above < static_cast<uint32_t>(need) && incl >= static_cast<uint32_t>(need)) {
-#pragma unroll 1
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t c = hist[255 - (tid * 8 + e)];
-          if (above + c >= static_cast<uint32_t>(need)) {
-            s_digit = 255 - (tid * 8 + e);
-            s_above = above;
-            break;
-          }
-          above += c;
-        }
-      }
-    }
-    __syncthreads();
-    prefix |= s_digit << shift;
-    mask |= 255u << shift;
-    need -= static_cast<int>(s_above);
+    for (int e = 0; e < kMine; ++e) k[e] = tid * KEYS + e < nb ? keys[tid * KEYS + e] : 0u;
   }
-  uint64_t before = 0;   // (keys above the prefix, keys equal to it) of the blocks so far
-  for (int i0 = 0; i0 < nb; i0 += kPickThreads) {
-    const int i = i0 + tid;
-    const uint32_t k = i < nb ? keys[i] : 0u;
-    const bool gt = i < nb && k > prefix, eq = i < nb && k == prefix;
+  // f(key) for every key of this thread
+  const auto each = [&](auto f) {
+    if (KEYS > 0) {
+#pragma unroll
+      for (int e = 0; e < kMine; ++e)
+        if (tid * KEYS + e < nb) f(k[e]);
+    } else {
+      for (int i = tid; i < nb; i += kPickThreads) f(keys[i]);
+    }
+  };
+  // what is always taken needs no search; the range of the others
+  uint32_t lo = 0xffffffffu, hi = 0;
+  int always = 0;
+  each([&](uint32_t x) {
+    if (x == kAlways) {
+      ++always;
+    } else {
+      lo = min(lo, x);
+      hi = max(hi, x);
+    }
+  });
+  if (tid == 0) {
+    s_lo = 0xffffffffu;
+    s_hi = s_count = 0;
+  }
+  for (int i = tid; i < kBins; i += kPickThreads) hist[i] = 0;
+  __syncthreads();
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  always = __reduce_add_sync(0xffffffffu, always);
+  if (lane == 0) {
+    atomicMin(&s_lo, lo);
+    atomicMax(&s_hi, hi);
+    atomicAdd(&s_count, always);
+  }
+  __syncthreads();
+  lo = s_lo;
+  hi = s_hi;
+  int need = n - static_cast<int>(s_count);   // of the keys in lo .. hi: at least one is left out
+  while (need > 0 && lo < hi) {   // lo .. hi narrows to the smallest key taken
+    const int shift = max(0, 32 - __clz(hi - lo) - kPickDigit);
+    each([&](uint32_t x) {
+      if (x >= lo && x <= hi) atomicAdd(&hist[(x - lo) >> shift], 1u);
+    });
+    __syncthreads();
+    // sums of the counters from the top: thread t has bins kBins - 1 - kOwn t ..
+    uint32_t own[kOwn], sum = 0;
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) {
+      own[e] = hist[kBins - 1 - (tid * kOwn + e)];
+      sum += own[e];
+    }
     uint64_t total;
-    const uint64_t at = before + scan2((static_cast<uint64_t>(gt) << 32) | eq, warp_sums, total);
-    const uint32_t above = static_cast<uint32_t>(at >> 32), equal = static_cast<uint32_t>(at);
-    if (gt || (eq && equal <= static_cast<uint32_t>(need)))
-      sel[above + min(equal, static_cast<uint32_t>(need)) - 1] = i;
-    before += total;
+    uint32_t above = static_cast<uint32_t>(scan2(sum, warp_sums, total)) - sum;
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) {
+      if (above < static_cast<uint32_t>(need) && above + own[e] >= static_cast<uint32_t>(need)) {
+        s_bin = kBins - 1 - (tid * kOwn + e);
+        s_above = above;
+        s_count = own[e];
+      }
+      above += own[e];
+      hist[kBins - 1 - (tid * kOwn + e)] = 0;
+    }
+    __syncthreads();
+    need -= static_cast<int>(s_above);
+    lo += s_bin << shift;
+    hi = min(hi, lo + ((1u << shift) - 1u));
+    const bool all = static_cast<int>(s_count) == need;   // the whole bin is taken: no need to look closer
+    __syncthreads();
+    if (all) {
+      need = 0x7fffffff;   // every key from lo on
+      break;
+    }
+  }
+  // keys above lo (or, with all of them taken, from lo on), and the first `need` of those equal to it
+  if (need == 0) lo = hi;   // only those always taken
+  const bool from = need == 0x7fffffff;
+  const auto above_it = [&](uint32_t x) { return from ? x >= lo : need == 0 ? x == kAlways : x > lo; };
+  const auto equal_it = [&](uint32_t x) { return !from && need > 0 && x == lo; };
+  if (KEYS > 0) {
+    uint32_t gt = 0, eq = 0;
+#pragma unroll
+    for (int e = 0; e < kMine; ++e)
+      if (tid * KEYS + e < nb) {
+        gt += above_it(k[e]);
+        eq += equal_it(k[e]);
+      }
+    uint64_t total;
+    const uint64_t at = scan2((static_cast<uint64_t>(gt) << 32) | eq, warp_sums, total);
+    uint32_t g = static_cast<uint32_t>(at >> 32) - gt, q = static_cast<uint32_t>(at) - eq;
+#pragma unroll
+    for (int e = 0; e < kMine; ++e)
+      if (tid * KEYS + e < nb) {
+        const bool is_gt = above_it(k[e]), is_eq = equal_it(k[e]) && q < static_cast<uint32_t>(need);
+        if (is_gt || is_eq) sel[g + min(q, static_cast<uint32_t>(need))] = tid * KEYS + e;
+        g += is_gt;
+        q += equal_it(k[e]);
+      }
+  } else {
+    uint64_t before = 0;   // (keys above, keys equal) of the blocks so far
+    for (int i0 = 0; i0 < nb; i0 += kPickThreads) {
+      const int i = i0 + tid;
+      const uint32_t x = i < nb ? keys[i] : 0u;
+      const bool gt = i < nb && above_it(x), eq = i < nb && equal_it(x);
+      uint64_t total;
+      const uint64_t at = before + scan2((static_cast<uint64_t>(gt) << 32) | eq, warp_sums, total);
+      const uint32_t g = static_cast<uint32_t>(at >> 32) - gt, q = static_cast<uint32_t>(at) - eq;
+      if (gt || (eq && q < static_cast<uint32_t>(need))) sel[g + min(q, static_cast<uint32_t>(need))] = i;
+      before += total;
+    }
   }
 }
 
@@ -307,7 +388,14 @@ extern "C" int mikv_block_select(const void* q, const mikv_pages* pages, int lay
   const int64_t ctas = static_cast<int64_t>(a.chunks) * rows * a.p.Hkv;
   if (ctas > 0x7fffffffLL) return fail(MIKV_ESHAPE, "block_select: rows=%d max_pages=%d", rows, a.p.max_pages);
   const cudaStream_t st = as_stream(stream);
-  block_score_kernel<<<static_cast<unsigned>(ctas), kBsThreads, 0, st>>>(a);
-  if (int e = check_launch("block_score_kernel")) return e;
-  return check_launch_after(launch_after(block_pick_kernel, dim3(rows * a.p.Hkv), dim3(kPickThreads), 0, st, a), "block_pick_kernel");
+  const auto score = a.rep <= 4 ? block_score_kernel<4> : block_score_kernel<8>;
+  const cudaError_t e = cudaFuncSetAttribute(score, cudaFuncAttributeMaxDynamicSharedMemorySize, kBsSmem);
+  if (e != cudaSuccess) return check_launch_after(e, "block_score_kernel");
+  score<<<static_cast<unsigned>(ctas), kBsThreads, kBsSmem, st>>>(a);
+  if (int r = check_launch("block_score_kernel")) return r;
+  const auto pick = a.p.max_pages <= 2 * kPickThreads    ? block_pick_kernel<2>
+                    : a.p.max_pages <= 8 * kPickThreads  ? block_pick_kernel<8>
+                    : a.p.max_pages <= 32 * kPickThreads ? block_pick_kernel<32>
+                                                         : block_pick_kernel<0>;
+  return check_launch_after(launch_after(pick, dim3(rows * a.p.Hkv), dim3(kPickThreads), 0, st, a), "block_pick_kernel");
 }

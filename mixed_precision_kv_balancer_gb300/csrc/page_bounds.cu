@@ -8,6 +8,8 @@
 // bounds that it had: a page that was given back, copied or cut down needs no case of its own.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "paged.cuh"
 #include "tcgen05.cuh"
 
@@ -17,122 +19,228 @@ int page_bounds_status(unsigned* out, bool clear) { return tc::wait_giveups(out,
 
 namespace {
 
-constexpr int kBoundThreads = 128;
+constexpr int kBoundThreads = 256;
 constexpr int kBoundWarps = kBoundThreads / 32;
-constexpr int kBoundRows = 8;     // packed rows of a CTA
+constexpr int kWarpRows = 128;     // a page of more rows is shared by the CTA's warps
 
-// Four channels of a stored key, exactly (INT8: fl(s * code + z), s * code is exact).
+// The smaller and larger values of pairs; what is no number stays.
+template <bool BF>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t y;
+  if (BF)
+    asm("min.NaN.bf16x2 %0, %1, %2;\n" : "=r"(y) : "r"(a), "r"(b));
+  else
+    asm("min.NaN.f16x2 %0, %1, %2;\n" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t y;
+  if (BF)
+    asm("max.NaN.bf16x2 %0, %1, %2;\n" : "=r"(y) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.f16x2 %0, %1, %2;\n" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;\n" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// A lane's bounds: 8 channels of every second row (16-bit types: pairs, exactly as stored), or 16 of every fourth (INT8).
 template <int TYPE>
-__device__ __forceinline__ void key4(const Pool& p, size_t row, int lane, float (&x)[4]) {
-  if (TYPE == MIKV_PAGES_INT8) {
-    const uint32_t c = reinterpret_cast<const uint32_t*>(p.k + row * kD)[lane];
-    const __half2 m = reinterpret_cast<const __half2*>(p.km + row * kMetaBytes)[lane >> 4];
+struct Bounds {
+  static constexpr bool q8 = TYPE == MIKV_PAGES_INT8, bf = TYPE == MIKV_PAGES_BF16;
+  static constexpr int lanes = q8 ? 8 : 16, at_once = 32 / lanes, channels = kD / lanes, batch = q8 ? 4 : 8;
+  float lo[channels], hi[channels];
+
+  // Rows j, j + step, ... below n of the page whose rows begin at `row0`, `batch` of them requested together.
+  __device__ __forceinline__ void rows(const Pool& p, size_t row0, int j, int step, int n) {
+    const int piece = (threadIdx.x & 31) % lanes;
+    if (q8) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = fmaf(__low2float(m), static_cast<float>((c >> (8 * e)) & 255u), __high2float(m));
-  } else {
-    const uint2 v = reinterpret_cast<const uint2*>(p.k + row * (kD * 2))[lane];
-    const uint32_t w[2] = {v.x, v.y};
+      for (int c = 0; c < channels; ++c) {
+        lo[c] = INFINITY;
+        hi[c] = -INFINITY;
+      }
+      for (; j < n; j += batch * step) {
+        uint4 x[batch];
+        __half2 m[batch];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (TYPE == MIKV_PAGES_BF16) {
-        x[2 * e] = __uint_as_float(w[e] << 16);
-        x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-      } else {
-        const __half2 h = *reinterpret_cast<const __half2*>(&w[e]);
-        x[2 * e] = __low2float(h);
-        x[2 * e + 1] = __high2float(h);
+        for (int e = 0; e < batch; ++e) {
+          const size_t row = row0 + (j + e * step < n ? j + e * step : j);   // (a row again changes nothing)
+          x[e] = reinterpret_cast<const uint4*>(p.k + row * kD)[piece];
+          m[e] = reinterpret_cast<const __half2*>(p.km + row * kMetaBytes)[piece >> 2];
+        }
+#pragma unroll
+        for (int e = 0; e < batch; ++e) {
+          const uint32_t w[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+          const float s = __low2float(m[e]), z = __high2float(m[e]);
+#pragma unroll
+          for (int c = 0; c < channels; ++c) {   // fl(s * code + z): s * code is exact; a code as the last bits of 2^23 + code
+            const float v = fmaf(s, __uint_as_float(__byte_perm(w[(c >> 2) & 3], 0x4B000000u, 0x7440u + (c & 3))) - 8388608.f, z);
+            lo[c] = min_nan(lo[c], v);
+            hi[c] = max_nan(hi[c], v);
+          }
+        }
+      }
+    } else {
+      constexpr uint32_t kInf = bf ? 0x7f807f80u : 0x7c007c00u, kNegInf = kInf | 0x80008000u;
+      uint32_t l[4], h[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        l[c] = kInf;
+        h[c] = kNegInf;
+      }
+      for (; j < n; j += batch * step) {
+        uint4 x[batch];
+#pragma unroll
+        for (int e = 0; e < batch; ++e) x[e] = reinterpret_cast<const uint4*>(p.k + (row0 + (j + e * step < n ? j + e * step : j)) * (kD * 2))[piece];
+#pragma unroll
+        for (int e = 0; e < batch; ++e) {
+          const uint32_t w[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            l[c] = min2<bf>(l[c], w[c]);
+            h[c] = max2<bf>(h[c], w[c]);
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < channels; ++c) {
+        lo[c] = wide(l[(c >> 1) & 3] >> (16 * (c & 1)));
+        hi[c] = wide(h[(c >> 1) & 3] >> (16 * (c & 1)));
       }
     }
   }
-}
+  __device__ __forceinline__ static float wide(uint32_t x) {
+    return bf ? __uint_as_float(x << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(x)));
+  }
+  // Over the lanes that hold the same channels.
+  __device__ __forceinline__ void join_lanes() {
+#pragma unroll
+    for (int o = lanes; o < 32; o <<= 1)
+#pragma unroll
+      for (int c = 0; c < channels; ++c) {
+        lo[c] = min_nan(lo[c], __shfl_xor_sync(0xffffffffu, lo[c], o));
+        hi[c] = max_nan(hi[c], __shfl_xor_sync(0xffffffffu, hi[c], o));
+      }
+  }
+  // Codes and scale, by a whole warp.
+  __device__ __forceinline__ void store(int8_t* codes, float* scale_out) const {
+    const int lane = threadIdx.x & 31, piece = lane % lanes;
+    float top = 0.f;
+#pragma unroll
+    for (int c = 0; c < channels; ++c) top = max_nan(top, max_nan(fabsf(lo[c]), fabsf(hi[c])));
+#pragma unroll
+    for (int o = 1; o < lanes; o <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const bool bad = !(top <= 3.402823466e38f);   // a key that is no finite number
+    const float scale = bad ? INFINITY : __fdiv_rn(top, 127.f);
+    // every lane has the bounds of its channels' lanes: four channels each
+    const int group = lane / lanes;
+    float l4[4], h4[4];
+#pragma unroll
+    for (int c = 0; c < channels; ++c)
+      if (c / 4 == group) {
+        l4[c % 4] = lo[c];
+        h4[c % 4] = hi[c];
+      }
+    uint32_t out[2] = {0, 0};
+    if (!bad && scale > 0.f) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int a = static_cast<int>(fminf(fmaxf(floorf(__fdiv_rn(l4[e], scale)), -127.f), 127.f));
+        const int b = static_cast<int>(fminf(fmaxf(ceilf(__fdiv_rn(h4[e], scale)), -127.f), 127.f));
+        out[0] |= (static_cast<uint32_t>(a) & 255u) << (8 * e);
+        out[1] |= (static_cast<uint32_t>(b) & 255u) << (8 * e);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) *reinterpret_cast<uint32_t*>(codes + k * kD + piece * channels + group * 4) = out[k];
+    if (lane == 0) *scale_out = scale;
+  }
+};
 
-// CTA (rows, head): the pages that kBoundRows packed rows lie on, each once: by the first of the rows
-// that follow one another on it.
-template <int TYPE>
+// CTA: the pages that ROWS packed rows lie on, each once: by the first of the rows that follow one another on it.
+// A warp has a key head of a page to itself, unless the page is long.  (A CTA of 8 rows that took its pages one after the
+// other was bound by its reads' latency: 16 pages of 16 rows took 11.7 us, 3.6 this way.)
+template <int TYPE, int ROWS>
 __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const Pool p, int layer, const int32_t* __restrict__ row_seq,
                                                                     const int32_t* __restrict__ row_pos, int rows,
                                                                     int8_t* __restrict__ bounds, float* __restrict__ scales) {
-  __shared__ float4 s_lo[kBoundWarps][32], s_hi[kBoundWarps][32];
-  __shared__ int s_bad[kBoundWarps];
-  const int h = blockIdx.y, r0 = blockIdx.x * kBoundRows, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const size_t layer_row = p.layer_rows() * layer;
+  using B = Bounds<TYPE>;
+  __shared__ float s_lo[kBoundWarps][kD], s_hi[kBoundWarps][kD];
+  const int r0 = blockIdx.x * ROWS, lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
   // lane e of every warp looks at row r0 + e
   int32_t page = -1, fill = 0;
-  if (lane < kBoundRows && r0 + lane < rows) {
+  if (lane < ROWS && r0 + lane < rows) {
     const int r = r0 + lane;
-    const int32_t s = row_seq[r], at = row_pos[r];
+    const int32_t s = row_seq[r], at = row_pos[r], s1 = r > 0 ? row_seq[r - 1] : -1, at1 = r > 0 ? row_pos[r - 1] : -1;
     if (static_cast<uint32_t>(s) < static_cast<uint32_t>(p.max_seqs) && at >= 0) {
-      const int32_t len = p.len_of(s);
       const uint32_t b = div_of(static_cast<uint32_t>(at), p.ps);
-      const bool again = r > 0 && row_seq[r - 1] == s && row_pos[r - 1] >= 0 && div_of(static_cast<uint32_t>(row_pos[r - 1]), p.ps) == b;
-      if (at < len && !again) {
+      const bool again = s1 == s && at1 >= 0 && div_of(static_cast<uint32_t>(at1), p.ps) == b;
+      if (!again && at < p.cap) {
+        const int32_t len = p.len_of(s);
         page = p.table[static_cast<size_t>(s) * p.max_pages + b];
         fill = min(static_cast<int32_t>(p.ps.d), len - static_cast<int32_t>(b * p.ps.d));
-        if (!p.has(page)) {
+        if (at >= len) {
+          page = -1;
+        } else if (!p.has(page)) {
           if (threadIdx.x < 32) tc::report_giveup(tc::kBadPage);
           page = -1;
         }
       }
     }
   }
+  const bool shared = p.ps.d > kWarpRows;
+  int item = w;   // (page, key head) of this CTA, counted through all of its pages
   for (uint32_t live = __ballot_sync(0xffffffffu, page >= 0); live; live &= live - 1) {
     const int e = __ffs(live) - 1;
     const int32_t pg = __shfl_sync(0xffffffffu, page, e), n = __shfl_sync(0xffffffffu, fill, e);
-    const size_t unit = static_cast<size_t>(layer) * p.n_pages * p.Hkv + static_cast<size_t>(pg) * p.Hkv + h;
-    const size_t row0 = unit * p.ps.d;
-    float lo[4], hi[4];
+    int h = shared ? 0 : item;
+    for (; h < p.Hkv; h += shared ? 1 : warps) {
+      const size_t unit = (static_cast<size_t>(layer) * p.n_pages + pg) * p.Hkv + h;
+      const int j = lane / B::lanes, step = B::at_once;
+      B b;
+      b.rows(p, unit * p.ps.d, shared ? w * step + j : j, shared ? warps * step : step, n);
+      b.join_lanes();
+      if (shared) {
+        __syncthreads();   // the last values have been read
+        if (lane < B::lanes)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      lo[c] = INFINITY;
-      hi[c] = -INFINITY;
-    }
-    bool bad = false;   // a key that is no finite number
-#pragma unroll 4
-    for (int j = w; j < n; j += kBoundWarps) {
-      float x[4];
-      key4<TYPE>(p, row0 + j, lane, x);
+          for (int c = 0; c < B::channels; ++c) {
+            s_lo[w][lane * B::channels + c] = b.lo[c];
+            s_hi[w][lane * B::channels + c] = b.hi[c];
+          }
+        __syncthreads();
+        if (w > 0) continue;
+        for (int v = 1; v < warps; ++v)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        lo[c] = fminf(lo[c], x[c]);
-        hi[c] = fmaxf(hi[c], x[c]);
-        bad |= !(fabsf(x[c]) <= 3.402823466e38f);
+          for (int c = 0; c < B::channels; ++c) {
+            b.lo[c] = min_nan(b.lo[c], s_lo[v][lane % B::lanes * B::channels + c]);
+            b.hi[c] = max_nan(b.hi[c], s_hi[v][lane % B::lanes * B::channels + c]);
+          }
       }
+      b.store(bounds + unit * (2 * kD), scales + unit);
     }
-    bad = __any_sync(0xffffffffu, bad);
-    __syncthreads();   // the last page's values have been read
-    s_lo[w][lane] = make_float4(lo[0], lo[1], lo[2], lo[3]);
-    s_hi[w][lane] = make_float4(hi[0], hi[1], hi[2], hi[3]);
-    if (lane == 0) s_bad[w] = bad;
-    __syncthreads();
-    if (w > 0) continue;
-    float top = 0.f;
-#pragma unroll
-    for (int k = 1; k < kBoundWarps; ++k) {
-      const float4 a = s_lo[k][lane], b = s_hi[k][lane];
-      lo[0] = fminf(lo[0], a.x), lo[1] = fminf(lo[1], a.y), lo[2] = fminf(lo[2], a.z), lo[3] = fminf(lo[3], a.w);
-      hi[0] = fmaxf(hi[0], b.x), hi[1] = fmaxf(hi[1], b.y), hi[2] = fmaxf(hi[2], b.z), hi[3] = fmaxf(hi[3], b.w);
-      bad |= s_bad[k] != 0;
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) top = fmaxf(top, fmaxf(fabsf(lo[c]), fabsf(hi[c])));
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float scale = bad ? INFINITY : __fdiv_rn(top, 127.f);
-    uint32_t cl = 0, ch = 0;
-    if (!bad && scale > 0.f) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int a = static_cast<int>(fminf(fmaxf(floorf(__fdiv_rn(lo[c], scale)), -127.f), 127.f));
-        const int b = static_cast<int>(fminf(fmaxf(ceilf(__fdiv_rn(hi[c], scale)), -127.f), 127.f));
-        cl |= (static_cast<uint32_t>(a) & 255u) << (8 * c);
-        ch |= (static_cast<uint32_t>(b) & 255u) << (8 * c);
-      }
-    }
-    uint32_t* dst = reinterpret_cast<uint32_t*>(bounds + unit * (2 * kD));
-    dst[lane] = cl;
-    dst[kD / 4 + lane] = ch;
-    if (lane == 0) scales[unit] = scale;
+    item = h - p.Hkv;
   }
+}
+
+template <int TYPE>
+void launch_bounds(const Pool& p, int layer, const int32_t* row_seq, const int32_t* row_pos, int rows, int8_t* bounds, float* scales,
+                   cudaStream_t st) {
+  // Few rows are mostly of as many sequences, each with a page of its own; of many, most share a page with the row before.
+  const int each = rows <= 1024 ? 1 : 2;
+  const int warps = static_cast<int>(p.ps.d) > kWarpRows ? kBoundWarps : std::min(kBoundWarps, each * p.Hkv);
+  const auto kern = each == 1 ? page_bounds_kernel<TYPE, 1> : page_bounds_kernel<TYPE, 2>;
+  kern<<<(rows - 1) / each + 1, warps * 32, 0, st>>>(p, layer, row_seq, row_pos, rows, bounds, scales);
 }
 
 }  // namespace
@@ -150,9 +258,11 @@ extern "C" int mikv_page_bounds(const mikv_pages* pages, int layer, const int32_
   if (rows == 0) return MIKV_OK;
   if (!row_seq || !row_pos || !bounds || !scales) return fail(MIKV_EINVAL, "page_bounds: null pointer");
   if (!aligned16(bounds)) return fail(MIKV_EALIGN, "page_bounds: bounds must be 16-byte aligned");
-  const auto kern = p.type == MIKV_PAGES_INT8   ? page_bounds_kernel<MIKV_PAGES_INT8>
-                    : p.type == MIKV_PAGES_BF16 ? page_bounds_kernel<MIKV_PAGES_BF16>
-                                                : page_bounds_kernel<MIKV_PAGES_FP16>;
-  kern<<<dim3((rows - 1) / kBoundRows + 1, p.Hkv), kBoundThreads, 0, as_stream(stream)>>>(p, layer, row_seq, row_pos, rows, bounds, scales);
+  const cudaStream_t st = as_stream(stream);
+  switch (p.type) {
+    case MIKV_PAGES_FP16: launch_bounds<MIKV_PAGES_FP16>(p, layer, row_seq, row_pos, rows, bounds, scales, st); break;
+    case MIKV_PAGES_BF16: launch_bounds<MIKV_PAGES_BF16>(p, layer, row_seq, row_pos, rows, bounds, scales, st); break;
+    default: launch_bounds<MIKV_PAGES_INT8>(p, layer, row_seq, row_pos, rows, bounds, scales, st);
+  }
   return check_launch("page_bounds_kernel");
 }
