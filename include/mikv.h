@@ -603,14 +603,14 @@ int mikv_page_bounds(const mikv_pages* p, int layer, const int32_t* row_seq, con
  * equal scores go to the lower block.  A row with `keep` blocks or fewer reads them all.
  *   sel int32 [rows][Hkv][keep]: the blocks in ascending order, -1 behind them;  n_sel int32 [rows][Hkv]
  * q [rows][Hq][D] fp16 (bf16 for BF16 pages).  rows * Hkv <= 65535, Hq a multiple of Hkv, up to 1024 query heads
- * per key head.  ws >= mikv_block_select_workspace_bytes(p, rows), 16-byte aligned; two calls must
+ * per key head.  ws >= mikv_block_select_workspace_bytes(p, rows, Hq), 16-byte aligned; two calls must
  * not share a workspace concurrently.
  * Errors: EINVAL (null, keep, first, recent), ESHAPE, EALIGN, EUNSUPPORTED, ECUDA.
  */
 int mikv_block_select(const void* q, const mikv_pages* p, int layer, const int8_t* bounds, const float* scales,
                       const int32_t* row_seq, const int32_t* row_pos, int rows, int Hq, int keep, int first, int recent,
                       int32_t* sel, int32_t* n_sel, void* ws, size_t ws_bytes, void* stream);
-size_t mikv_block_select_workspace_bytes(const mikv_pages* p, int rows);
+size_t mikv_block_select_workspace_bytes(const mikv_pages* p, int rows, int Hq);
 
 /*
  * Attention of each row over the blocks that sel and n_sel name (as mikv_block_select writes them, or

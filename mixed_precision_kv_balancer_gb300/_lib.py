@@ -126,7 +126,7 @@ def load() -> ctypes.CDLL:
         "mikv_slot_append": (I, [GP, I, RP, RP, I, P, P]),
         "mikv_page_bounds": (I, [GP, I, P, P, I, P, P, P]),
         "mikv_block_select": (I, [P, GP, I, P, P, P, P, I, I, I, I, I, P, P, P, S, P]),
-        "mikv_block_select_workspace_bytes": (S, [GP, I]),
+        "mikv_block_select_workspace_bytes": (S, [GP, I, I]),
         "mikv_block_attention": (I, [P, GP, I, P, P, P, P, I, I, I, P, P, P, S, P]),
         "mikv_block_attention_workspace_bytes": (S, [GP, I, I, I]),
         "mikv_chunk_attention": (I, [RP, GP, I, P, P, P, I, I, I, I, I, RP, P, P, S, P]),
@@ -485,7 +485,7 @@ def mikv_block_select(q, pages, layer, bounds, scales, first, recent, sel, n_sel
     rows, Hq, _ = q.shape
     keep = sel.shape[-1]
     w, nb, _keep = _ws_given(ws, dev) if ws is not None else _ws_new(
-        lib.mikv_block_select_workspace_bytes(pages.ref, rows), dev, stream)
+        lib.mikv_block_select_workspace_bytes(pages.ref, rows, Hq), dev, stream)
     _launch(dev, stream, lib.mikv_block_select, _need(q, "q", _PAGE_DTYPE[s.type], (rows, Hq, s.D), dev), pages.ref, layer,
             *_bounds_of(s, bounds, scales, dev), _need(row_seq, "row_seq", torch.int32, (rows,), dev),
             _need(row_pos, "row_pos", torch.int32, (rows,), dev), rows, Hq, keep, first, recent,

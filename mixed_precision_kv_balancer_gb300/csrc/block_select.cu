@@ -8,8 +8,10 @@
 // fl(fl(u s_b) s_q) is the same to the bit wherever it is computed, so that the choice is too.  The
 // heads of a group read one set of blocks: a block's score is the largest of theirs.
 //
-// Two kernels: scores of all blocks (bound by HBM: 260 bytes a block and key head, against 64 four-term
-// integer products a query head), and the choice of the `keep` best of each (row, key head), written in the
+// Three kernels: the queries' codes, in the order in which the products take them (once a (row, key head): 32 divisions
+// a lane are more than the scores of 128 blocks); scores of all blocks (bound by HBM: 260 bytes a block and key head; mma.sync on
+// fp16 numbers, which hold the codes exactly, as fp32 does the sums, with 16 blocks as its M and 8 query heads as its N;
+// four-term integer products took 34 us, 8-bit matrix instructions 37, for 192 units of up to 4096 blocks), and the choice of the `keep` best of each (row, key head), written in the
 // blocks' order.  The choice is a search by digits of the scores' bits, but of digits that begin below what all
 // of a unit's scores share: scores of one unit lie close together, and counters of their first bits would all be hit at once.
 #include <cuda_bf16.h>
@@ -25,11 +27,12 @@ int block_select_status(unsigned* out, bool clear) { return tc::wait_giveups(out
 
 namespace {
 
-constexpr int kBsThreads = 128;
-constexpr int kBsWarps = kBsThreads / 32;
-constexpr int kBsSteps = 2;                       // of 32 blocks a warp
-constexpr int kBsBlocks = kBsThreads * kBsSteps;  // blocks of a CTA
-constexpr int kBsSmem = kBsSteps * kBsWarps * 32 * 2 * kD;   // their bounds
+constexpr int kBsWarps = 4;
+constexpr int kBsSteps = 2;                    // of 32 blocks a warp
+constexpr int kBsBlocks = 32 * kBsSteps;       // blocks of a warp
+constexpr int kBsRing = 2;                     // steps that are under way
+constexpr int kBsHeads = 8;                    // query heads of a pass
+constexpr int kBsSmem = kBsWarps * kBsRing * 32 * 2 * kD;
 constexpr int kPickThreads = 512;
 constexpr int kPickDigit = 11;                    // bits of a digit
 constexpr uint32_t kAlways = 0xffffffffu;   // above every score
@@ -41,9 +44,12 @@ struct SelectArgs {
   const float* scales;
   const int32_t *row_seq, *row_pos;
   int layer, rows, Hq, rep, keep, first, recent;
-  int chunks;            // CTAs of a (row, key head)
+  int chunks;            // warps of a (row, key head)
+  int64_t warps;         // of all
   int32_t *sel, *n_sel;
   uint32_t* keys;        // [rows][Hkv][max_pages]: scores in the order of whole numbers
+  uint4* codes;          // [rows][Hkv][groups][8][32]: the queries' codes by lanes; behind them fp32 scales [rows][Hkv][groups][8]
+  int groups;            // of kBsHeads query heads
 };
 
 // Blocks that row r can read: all that hold a position up to its own; 0 for a row without a sequence.
@@ -65,113 +71,203 @@ __device__ __forceinline__ uint32_t ordered(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// CTA: kBsBlocks blocks of one (row, key head), all requested before anything else is done.  A warp brings the
-// bounds of 32 blocks to shared memory in whole lines; then a lane has a block of its own, so that no
-// sum crosses lanes.  HEADS query heads a pass.
-template <int HEADS>
-__global__ void __launch_bounds__(kBsThreads) block_score_kernel(const SelectArgs a) {
-  extern __shared__ __align__(16) uint4 s_b[];                       // [step][warp][32 blocks][16 pieces], swizzled by the block
-  __shared__ __align__(16) uint32_t s_q[HEADS][2 * kD / 4];          // codes below 0, codes above 0
-  __shared__ float s_scale[HEADS];
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int unit = blockIdx.x / a.chunks, b0 = (blockIdx.x - unit * a.chunks) * kBsBlocks;
-  const int r = unit / a.p.Hkv, h = unit - r * a.p.Hkv;
+// Two codes of x (the bytes' first bits turned over, `sel` puts them under 0x64) as an fp16 pair: 0x64cc is 1024 + cc.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t x, uint32_t sel) {
+  const uint32_t w = __byte_perm(x, 0x64646464u, sel);
+  const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&w), __float2half2_rn(1152.f));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float* query_scales(const SelectArgs& a, int unit, int group) {
+  float* s = reinterpret_cast<float*>(a.codes + static_cast<size_t>(a.rows) * a.p.Hkv * a.groups * 256);
+  return s + (static_cast<size_t>(unit) * a.groups + group) * kBsHeads;
+}
+// A warp: the codes of up to kBsHeads query heads of one (row, key head).
+__global__ void __launch_bounds__(kBsWarps * 32) block_query_kernel(const SelectArgs a) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   pdl_trigger();
-  int32_t seq;
+  const int id = blockIdx.x * kBsWarps + (threadIdx.x >> 5);
+  if (id >= a.rows * a.p.Hkv * a.groups) return;
+  const int unit = id / a.groups, g0 = (id - unit * a.groups) * kBsHeads;
+  const bool bf = a.p.type == MIKV_PAGES_BF16;
+  // the codes of query head g0 + g, channels 64 k + 16 t .. + 15, in the order in which those of the blocks are read:
+  // below 0 (met by lo), then above (by hi)
+  uint32_t q[16][2];
+  float sq = 0.f;
+  const bool there = g0 + g < a.rep;
+  {
+    uint4 v[2][2];
+    float top = 0.f;
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        v[k][e] = make_uint4(0, 0, 0, 0);
+        if (there)
+          v[k][e] = reinterpret_cast<const uint4*>(a.q + (static_cast<size_t>(unit) * a.rep + g0 + g) * kD)[8 * k + 2 * t + e];
+      }
+    const auto word = [&](int k, int c) {   // channels 2 c, 2 c + 1 of the lane's 16
+      const uint4& x = v[k][c >> 2];
+      return (c & 3) == 0 ? x.x : (c & 3) == 1 ? x.y : (c & 3) == 2 ? x.z : x.w;
+    };
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x = fabsf(to_float(word(k, c) >> (16 * e) & 0xffffu, bf));
+          top = fmaxf(top, x);
+          bad |= !(x <= 3.402823466e38f);
+        }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      bad |= __shfl_xor_sync(0xffffffffu, static_cast<int>(bad), o) != 0;
+    }
+    sq = bad ? INFINITY : __fdiv_rn(top, 127.f);   // no finite query: its scores are 0 * infinity
+    const bool some = !bad && sq > 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        float x[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          x[e] = some ? fminf(fmaxf(rintf(__fdiv_rn(to_float(word(k, c) >> (16 * e) & 0xffffu, bf), sq)), -127.f), 127.f) : 0.f;
+        q[4 * k + (c >> 1)][c & 1] = pack_half2(__float2half_rn(fminf(x[0], 0.f)), __float2half_rn(fminf(x[1], 0.f)));
+        q[8 + 4 * k + (c >> 1)][c & 1] = pack_half2(__float2half_rn(fmaxf(x[0], 0.f)), __float2half_rn(fmaxf(x[1], 0.f)));
+      }
+  }
+  uint4* codes = a.codes + static_cast<size_t>(id) * 256 + lane;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) codes[e * 32] = make_uint4(q[2 * e][0], q[2 * e][1], q[2 * e + 1][0], q[2 * e + 1][1]);
+  if (t == 0) query_scales(a, unit, g0 / kBsHeads)[g] = sq;
+}
+
+// A warp: kBsBlocks blocks of one (row, key head), 32 a step; the warps of a CTA have the heads of the same blocks side by
+// side, whose bounds lie side by side.  Lane 4 g + t holds the codes of query head g, as the products take them.
+__global__ void __launch_bounds__(kBsWarps * 32) block_score_kernel(const SelectArgs a) {
+  extern __shared__ __align__(16) uint4 s_b[];   // [warp][ring][32 blocks][16 pieces], swizzled by the block
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  pdl_trigger();
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kBsWarps + w;
+  if (id >= a.warps) return;
+  const int64_t rest = id / a.p.Hkv;
+  const int h = static_cast<int>(id - rest * a.p.Hkv), r = static_cast<int>(rest / a.chunks);
+  const int b0 = static_cast<int>(rest - static_cast<int64_t>(r) * a.chunks) * kBsBlocks;
+  int32_t seq = a.row_seq ? a.row_seq[r] : r, page[kBsSteps];
+  if (static_cast<uint32_t>(seq) >= static_cast<uint32_t>(a.p.max_seqs)) return;
+  const int32_t* table = a.p.table + static_cast<size_t>(seq) * a.p.max_pages;
+#pragma unroll
+  for (int i = 0; i < kBsSteps; ++i)   // asked for beside the length that tells whether they count
+    page[i] = b0 + 32 * i + lane < a.p.max_pages ? table[b0 + 32 * i + lane] : -1;
   const int32_t nb = blocks_of_row(a, r, seq);
   if (b0 >= nb || nb <= a.keep) return;
-  const bool bf = a.p.type == MIKV_PAGES_BF16;
-  const int32_t* table = a.p.table + static_cast<size_t>(seq) * a.p.max_pages;
+  const int unit = r * a.p.Hkv + h;
   const size_t layer0 = static_cast<size_t>(a.layer) * a.p.n_pages * a.p.Hkv;
-  const auto block_of = [&](int i) { return b0 + (i * kBsWarps + w) * 32 + lane; };
-  const auto pieces = [&](int i) { return s_b + (i * kBsWarps + w) * (32 * 16); };
-  bool there[kBsSteps];
-  float sb[kBsSteps], best[kBsSteps];
+  const int steps = min(kBsSteps, (nb - b0 + 31) / 32);
+  const uint32_t ring = smem_u32(s_b) + w * (kBsRing * 32 * 2 * kD);
+  uint32_t at[kBsSteps];   // (page, key head) of the lane's block, kNoRow without one
 #pragma unroll
   for (int i = 0; i < kBsSteps; ++i) {
-    const int b = block_of(i);
-    const int32_t page = b < nb ? table[b] : -1;
-    there[i] = a.p.has(page);
-    const uint32_t at = there[i] ? static_cast<uint32_t>(page) * a.p.Hkv + h : 0;   // (below 2^32, like the pool's rows)
-    sb[i] = there[i] ? a.scales[layer0 + at] : 0.f;
-    best[i] = -INFINITY;
-    uint4* dst = pieces(i);
+    const bool ok = b0 + 32 * i + lane < nb && a.p.has(page[i]);
+    at[i] = ok ? static_cast<uint32_t>(page[i]) * a.p.Hkv + h : kNoRow;   // (below 2^32, like the pool's rows)
+  }
+  const auto fetch = [&](int i, uint32_t from) {
+    const uint32_t dst = ring + i % kBsRing * (32 * 2 * kD);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {   // two blocks an instruction
       const int e = 2 * j + (lane >> 4), piece = lane & 15;
-      const uint32_t src = __shfl_sync(0xffffffffu, at, e);
-      const bool ok = __shfl_sync(0xffffffffu, static_cast<int>(there[i]), e);
-      cp_async16(smem_u32(dst + e * 16 + (piece ^ (e & 15))), a.bounds + (layer0 + src) * (2 * kD) + piece * 16, ok);
+      const uint32_t src = __shfl_sync(0xffffffffu, from, e);
+      const bool ok = src != kNoRow;
+      cp_async16(dst + e * (2 * kD) + ((piece ^ ((e & 1) << 2)) << 4), a.bounds + (layer0 + (ok ? src : 0)) * (2 * kD) + piece * 16, ok);
     }
-    cp_async_commit();
-  }
-  for (int g0 = 0; g0 < a.rep; g0 += HEADS) {
-    const int heads = min(HEADS, a.rep - g0);
-    if (g0 > 0) __syncthreads();
-    for (int e = w; e < heads; e += kBsWarps) {   // a warp per query head: four channels a lane
-      const uint2 v = reinterpret_cast<const uint2*>(a.q + (static_cast<size_t>(r) * a.Hq + h * a.rep + g0 + e) * kD)[lane];
-      const float x[4] = {to_float(v.x & 0xffffu, bf), to_float(v.x >> 16, bf), to_float(v.y & 0xffffu, bf), to_float(v.y >> 16, bf)};
-      float top = 0.f;
-      bool bad = false;
+  };
+  float best[kBsSteps];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        top = fmaxf(top, fabsf(x[c]));
-        bad |= !(fabsf(x[c]) <= 3.402823466e38f);
-      }
+  for (int i = 0; i < kBsSteps; ++i) best[i] = -INFINITY;
+  float sb[kBsSteps];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      bad = __any_sync(0xffffffffu, bad);
-      const float s = bad ? INFINITY : __fdiv_rn(top, 127.f);   // no finite query: its scores are 0 * infinity
-      uint32_t neg = 0, pos = 0;
-      if (!bad && s > 0.f) {
+  for (int i = 0; i < kBsSteps; ++i) sb[i] = at[i] != kNoRow ? a.scales[layer0 + at[i]] : 0.f;
+  for (int g0 = 0; g0 < a.rep; g0 += kBsHeads) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int code = min(max(__float2int_rn(__fdiv_rn(x[c], s)), -127), 127);
-          if (code > 0)
-            pos |= static_cast<uint32_t>(code) << (8 * c);
-          else
-            neg |= (static_cast<uint32_t>(code) & 255u) << (8 * c);
+    for (int i = 0; i < kBsRing; ++i) {
+      if (i < steps) fetch(i, at[i]);
+      cp_async_commit();
+    }
+    if (g0 == 0) pdl_wait();   // the queries' codes are there
+    uint32_t q[16][2];
+    const uint4* codes = a.codes + (static_cast<size_t>(unit) * a.groups + g0 / kBsHeads) * 256 + lane;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint4 x = codes[e * 32];
+      q[2 * e][0] = x.x;
+      q[2 * e][1] = x.y;
+      q[2 * e + 1][0] = x.z;
+      q[2 * e + 1][1] = x.w;
+    }
+    const float sq = query_scales(a, unit, g0 / kBsHeads)[g];
+    // scales of the heads whose sums this lane holds
+    const float s2[2] = {__shfl_sync(0xffffffffu, sq, 8 * t), __shfl_sync(0xffffffffu, sq, 8 * t + 4)};
+#pragma unroll
+    for (int i = 0; i < kBsSteps; ++i) {
+      if (i >= steps) break;
+      cp_async_wait<kBsRing - 1>();
+      __syncwarp();
+      const uint32_t src = ring + i % kBsRing * (32 * 2 * kD);
+      float top[2][2];   // blocks 16 mt + g and + 8
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        float d[4] = {};
+        const uint32_t row = src + (mt * 16 + g) * (2 * kD) + ((t ^ ((g & 1) << 2)) << 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {   // 64 codes: of lo, lo, hi, hi
+          const uint4 x = lds128(row ^ (k << 6)), y = lds128((row ^ (k << 6)) + 8 * 2 * kD);
+          const uint32_t c0[4] = {x.x, x.y, x.z, x.w}, c1[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const uint32_t u0 = c0[s] ^ 0x80808080u, u1 = c1[s] ^ 0x80808080u;
+            mma16816(d, codes_f16(u0, 0x4140u), codes_f16(u1, 0x4140u), codes_f16(u0, 0x4342u), codes_f16(u1, 0x4342u), q[4 * k + s][0],
+                     q[4 * k + s][1]);
+          }
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float scale = __shfl_sync(0xffffffffu, sb[i], mt * 16 + half * 8 + g);
+          top[mt][half] = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (g0 + 2 * t + j < a.rep) {
+              const float x = __fmul_rn(__fmul_rn(d[2 * half + j], scale), s2[j]);
+              top[mt][half] = fmaxf(top[mt][half], isnan(x) ? INFINITY : x);
+            }
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) top[mt][half] = fmaxf(top[mt][half], __shfl_xor_sync(0xffffffffu, top[mt][half], o));
         }
       }
-      s_q[e][lane] = neg;
-      s_q[e][kD / 4 + lane] = pos;
-      if (lane == 0) s_scale[e] = s;
+      // block `lane` of the step
+      float mine = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = __shfl_sync(0xffffffffu, top[e >> 1][e & 1], (lane & 7) * 4);
+        if (lane >> 3 == e) mine = x;
+      }
+      best[i] = fmaxf(best[i], mine);
+      __syncwarp();   // the step's pieces have been read
+      if (i + kBsRing < kBsSteps && i + kBsRing < steps) fetch(i + kBsRing, at[(i + kBsRing) % kBsSteps]);
+      cp_async_commit();
     }
     cp_async_wait<0>();
-    __syncthreads();
-    int u[kBsSteps][HEADS] = {};
-#pragma unroll 2
-    for (int c = 0; c < 16; ++c) {
-      uint4 x[kBsSteps];
-#pragma unroll
-      for (int i = 0; i < kBsSteps; ++i) x[i] = pieces(i)[lane * 16 + (c ^ (lane & 15))];
-#pragma unroll
-      for (int e = 0; e < HEADS; ++e) {
-        const uint4 y = reinterpret_cast<const uint4*>(s_q[e])[c];
-#pragma unroll
-        for (int i = 0; i < kBsSteps; ++i) {
-          u[i][e] = __dp4a(static_cast<int>(x[i].x), static_cast<int>(y.x), u[i][e]);
-          u[i][e] = __dp4a(static_cast<int>(x[i].y), static_cast<int>(y.y), u[i][e]);
-          u[i][e] = __dp4a(static_cast<int>(x[i].z), static_cast<int>(y.z), u[i][e]);
-          u[i][e] = __dp4a(static_cast<int>(x[i].w), static_cast<int>(y.w), u[i][e]);
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kBsSteps; ++i)
-#pragma unroll
-      for (int e = 0; e < HEADS; ++e)
-        if (e < heads) {
-          const float s = __fmul_rn(__fmul_rn(static_cast<float>(u[i][e]), sb[i]), s_scale[e]);
-          best[i] = fmaxf(best[i], isnan(s) ? INFINITY : s);
-        }
+    __syncwarp();
   }
 #pragma unroll
   for (int i = 0; i < kBsSteps; ++i) {
-    const int b = block_of(i);
+    const int b = b0 + 32 * i + lane;
     if (b >= nb) break;
     uint32_t key = ordered(best[i]);
-    if (!there[i]) {   // a block without a page is the last choice
+    if (at[i] == kNoRow) {   // a block without a page is the last choice
       key = 0;
       tc::report_giveup(tc::kBadPage);
     }
@@ -339,17 +435,23 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectAr
   }
 }
 
-size_t key_bytes(const mikv_pages* p, int rows) { return static_cast<size_t>(rows) * p->Hkv * p->max_pages * 4; }
+int groups_of(int rep) { return (rep + kBsHeads - 1) / kBsHeads; }
+size_t key_bytes(const mikv_pages* p, int rows) { return align_up(static_cast<size_t>(rows) * p->Hkv * p->max_pages * 4, 16); }
+size_t select_bytes(const mikv_pages* p, int rows, int Hq) {
+  return key_bytes(p, rows) + static_cast<size_t>(rows) * p->Hkv * groups_of(Hq / p->Hkv) * (256 * 16 + kBsHeads * 4);
+}
 
 }  // namespace
 }  // namespace mikv
 
 using namespace mikv;
 
-extern "C" size_t mikv_block_select_workspace_bytes(const mikv_pages* p, int rows) {
+extern "C" size_t mikv_block_select_workspace_bytes(const mikv_pages* p, int rows, int Hq) {
   Pool pool;
-  if (check_pages(p, "block_select", &pool) || rows < 1 || static_cast<int64_t>(rows) * p->Hkv > 65535) return 0;
-  return align_up(key_bytes(p, rows), 16);
+  if (check_pages(p, "block_select", &pool) || rows < 1 || static_cast<int64_t>(rows) * p->Hkv > 65535 || Hq < 1 || Hq % p->Hkv ||
+      Hq / p->Hkv > 1024)
+    return 0;
+  return select_bytes(p, rows, Hq);
 }
 
 extern "C" int mikv_block_select(const void* q, const mikv_pages* pages, int layer, const int8_t* bounds, const float* scales,
@@ -367,7 +469,7 @@ extern "C" int mikv_block_select(const void* q, const mikv_pages* pages, int lay
   if (rows == 0) return MIKV_OK;
   if (!q || !bounds || !scales || !sel || !n_sel || !ws) return fail(MIKV_EINVAL, "block_select: null pointer");
   if (!aligned16(q) || !aligned16(bounds) || !aligned16(ws)) return fail(MIKV_EALIGN, "block_select: 16-byte alignment");
-  const size_t need = key_bytes(pages, rows);
+  const size_t need = select_bytes(pages, rows, Hq);
   if (ws_bytes < need) return fail(MIKV_ESHAPE, "block_select: workspace %zu < %zu", ws_bytes, need);
   a.q = static_cast<const uint16_t*>(q);
   a.bounds = bounds;
@@ -384,15 +486,20 @@ extern "C" int mikv_block_select(const void* q, const mikv_pages* pages, int lay
   a.sel = sel;
   a.n_sel = n_sel;
   a.keys = static_cast<uint32_t*>(ws);
+  a.codes = reinterpret_cast<uint4*>(static_cast<uint8_t*>(ws) + key_bytes(pages, rows));
+  a.groups = groups_of(a.rep);
   a.chunks = (a.p.max_pages - 1) / kBsBlocks + 1;
-  const int64_t ctas = static_cast<int64_t>(a.chunks) * rows * a.p.Hkv;
+  a.warps = static_cast<int64_t>(a.chunks) * rows * a.p.Hkv;
+  const int64_t ctas = (a.warps - 1) / kBsWarps + 1;
   if (ctas > 0x7fffffffLL) return fail(MIKV_ESHAPE, "block_select: rows=%d max_pages=%d", rows, a.p.max_pages);
   const cudaStream_t st = as_stream(stream);
-  const auto score = a.rep <= 4 ? block_score_kernel<4> : block_score_kernel<8>;
-  const cudaError_t e = cudaFuncSetAttribute(score, cudaFuncAttributeMaxDynamicSharedMemorySize, kBsSmem);
+  const cudaError_t e = cudaFuncSetAttribute(block_score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBsSmem);
   if (e != cudaSuccess) return check_launch_after(e, "block_score_kernel");
-  score<<<static_cast<unsigned>(ctas), kBsThreads, kBsSmem, st>>>(a);
-  if (int r = check_launch("block_score_kernel")) return r;
+  block_query_kernel<<<(rows * a.p.Hkv * a.groups - 1) / kBsWarps + 1, kBsWarps * 32, 0, st>>>(a);
+  if (int r = check_launch("block_query_kernel")) return r;
+  if (int r = check_launch_after(launch_after(block_score_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kBsWarps * 32), kBsSmem, st, a),
+                                 "block_score_kernel"))
+    return r;
   const auto pick = a.p.max_pages <= 2 * kPickThreads    ? block_pick_kernel<2>
                     : a.p.max_pages <= 8 * kPickThreads  ? block_pick_kernel<8>
                     : a.p.max_pages <= 32 * kPickThreads ? block_pick_kernel<32>

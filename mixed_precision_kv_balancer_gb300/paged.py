@@ -85,7 +85,7 @@ class PagedCache:
     def block_workspace(self, rows, Hq, keep):
         """For pick and for attend_blocks, one behind the other."""
         lib = _lib.load()
-        return self._bytes(max(lib.mikv_block_select_workspace_bytes(self.ref, rows),
+        return self._bytes(max(lib.mikv_block_select_workspace_bytes(self.ref, rows, Hq),
                                lib.mikv_block_attention_workspace_bytes(self.ref, rows, Hq, keep)))
 
     def bounds_buffers(self):

@@ -28,7 +28,7 @@ def test_every_call_checks_the_cache(lib, kw, code):
     assert lib.mikv_block_select(FAKE, p, 0, FAKE, FAKE, None, None, 1, 4, 2, 0, 1, FAKE, FAKE, FAKE, BIG, None) == code
     assert lib.mikv_block_attention(FAKE, p, 0, None, None, FAKE, FAKE, 1, 4, 2, FAKE, None, FAKE, BIG, None) == code
     assert lib.mikv_chunk_attention(_rows(), p, 0, None, None, FAKE, 1, 1, 4, 0, 0, _rows(), None, FAKE, BIG, None) == code
-    assert lib.mikv_block_select_workspace_bytes(p, 1) == 0
+    assert lib.mikv_block_select_workspace_bytes(p, 1, 4) == 0
     assert lib.mikv_block_attention_workspace_bytes(p, 1, 4, 2) == 0
     assert lib.mikv_chunk_attention_workspace_bytes(p, 1, 1, 4) == 0
 
@@ -61,9 +61,9 @@ def test_slot_append_and_bounds_refuse(lib):
 
 def test_block_calls_refuse(lib):
     p = _pages()
-    need = lib.mikv_block_select_workspace_bytes(p, 3)
-    assert need >= 3 * 2 * 4 * 4 and lib.mikv_block_select_workspace_bytes(p, 0) == 0
-    assert lib.mikv_block_select_workspace_bytes(p, 32768) == 0                   # 2 key heads: 65536 units
+    need = lib.mikv_block_select_workspace_bytes(p, 3, 4)
+    assert need >= 3 * 2 * 4 * 4 and lib.mikv_block_select_workspace_bytes(p, 0, 4) == 0
+    assert lib.mikv_block_select_workspace_bytes(p, 32768, 4) == 0                   # 2 key heads: 65536 units
     call = lambda q=FAKE, layer=0, b=FAKE, s=FAKE, seq=None, rows=3, Hq=4, keep=3, first=1, recent=1, sel=FAKE, n_sel=FAKE, ws=FAKE, nb=BIG: \
         lib.mikv_block_select(q, p, layer, b, s, seq, None, rows, Hq, keep, first, recent, sel, n_sel, ws, nb, None)
     assert call(rows=0, q=None, ws=None) == 0
