@@ -179,7 +179,8 @@ __device__ __forceinline__ bool tile_narrow(const ChunkArgs& a, int ts, int i, i
 template <int KT>
 struct Walk {
   int req, blk, item;    // the item
-  int places, t0, t1;    // its places, and its key tiles of this part
+  int places, weight;    // its places, and those of a key tile
+  int t0, t1;            // its key tiles of this part
   int left;              // items of the block behind it
   int64_t to_go;         // places of this CTA's part from the item's begin on
   Request q;
@@ -187,9 +188,11 @@ struct Walk {
 
   __device__ __forceinline__ void open(const ChunkArgs& a) {   // places of block `blk`
     places = uniform(chunk_places<KT>(q.t, q.r, a.qb.window, a.qb.sinks, blk));
+    weight = uniform(tile_weight<KT>(q.t));
   }
-  __device__ __forceinline__ void load(const ChunkArgs& a) {
-    q = request_of(a, req);
+  __device__ __forceinline__ void load(const ChunkArgs& a) { load(request_of(a, req)); }
+  __device__ __forceinline__ void load(const Request& r) {
+    q = r;
     q.row0 = uniform(q.row0);
     q.seq = uniform(q.seq);
     q.r.rows = uniform(q.r.rows);
@@ -197,6 +200,7 @@ struct Walk {
     q.r.keys = uniform(q.r.keys);
   }
   __device__ __forceinline__ Work work(const ChunkArgs& a) const { return work_of<KT>(a, q, blk, item, t0, t1); }
+  __device__ __forceinline__ void set_end() { t1 = uniform(chunk_tile(static_cast<int>(min(to_go, static_cast<int64_t>(places))), weight)); }
   // On to the next item, by the whole warp; false where there is none.
   __device__ __forceinline__ bool next(const ChunkArgs& a, bool ok) {
     to_go -= places;
@@ -216,7 +220,7 @@ struct Walk {
       ++item;
     }
     t0 = 0;
-    t1 = uniform(to_go >= places ? places - kItemPlaces : line_tile(static_cast<int>(to_go)));
+    set_end();
     return true;
   }
 };
@@ -271,20 +275,26 @@ __device__ __forceinline__ int find_entry(const T* base, int n, int64_t x) {
   return lo;
 }
 
-// This CTA's part of the line, by all threads of it, for its walking warp.  `scratch`: (n + 1) * 4 bytes for the blocks before each
-// request, and 8 bytes a block for the places before it.
+// This CTA's part of the line, by all threads of it, for its walking warp.  `scratch`: 16 bytes a request, (n + 1) * 4
+// for the blocks before each, and 8 bytes a block for the places before it (180 KB at most).
 template <int KT, class W>
 __device__ __forceinline__ Walk<KT> find_part(const ChunkArgs& a, uint8_t* scratch, int64_t* sums) {
   const int tid = threadIdx.x;
-  int64_t* place = reinterpret_cast<int64_t*>(scratch);
+  int4* reqs = reinterpret_cast<int4*>(scratch);   // first row, rows, first position, keys
+  int64_t* place = reinterpret_cast<int64_t*>(reqs + a.n);
+  const auto request = [&](int i) {
+    const int4 x = reqs[i];
+    return Request{x.x, a.seqs ? a.seqs[i] : i, {x.y, x.z, x.w}, row_tiles_of(x.y, a.rep)};
+  };
   int32_t* blocks = reinterpret_cast<int32_t*>(place + a.rows / kCaRows + a.n + 2);   // a request has a block more than rows / 128 at most
   int64_t done = 0, total;
   for (int i0 = 0; i0 < a.n; i0 += W::threads) {
     const int i = i0 + tid;
     int64_t v = 0;
     if (i < a.n) {
-      const int rows = max(request_row(a, i + 1) - request_row(a, i), 0);
-      v = row_tiles_of(rows, a.rep).blocks;
+      const Request q = request_of(a, i);
+      reqs[i] = make_int4(q.row0, q.r.rows, q.r.off, q.r.keys);
+      v = q.t.blocks;
     }
     v = scan_block<W::threads>(v, sums, total);
     if (i < a.n) blocks[i + 1] = static_cast<int32_t>(done + v);
@@ -300,7 +310,7 @@ __device__ __forceinline__ Walk<KT> find_part(const ChunkArgs& a, uint8_t* scrat
     int64_t v = 0;
     if (e < entries) {
       const int i = find_entry(blocks, a.n, e);
-      const Request q = request_of(a, i);
+      const Request q = request(i);
       v = static_cast<int64_t>(chunk_places<KT>(q.t, q.r, a.qb.window, a.qb.sinks, e - blocks[i])) * a.p.Hkv * q.t.per;
     }
     v = scan_block<W::threads>(v, sums, total);
@@ -312,7 +322,7 @@ __device__ __forceinline__ Walk<KT> find_part(const ChunkArgs& a, uint8_t* scrat
   Walk<KT> w;
   w.idle = true;
   if (tid / 32 != W::walk) return w;
-  const int workers = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(a.ctas), done / 2))), c = blockIdx.x;
+  const int workers = chunk_workers(done, a.ctas), c = blockIdx.x;
   Cut cut = {};
   cut.last = -1;
   if (c < workers && done > 0) {
@@ -320,21 +330,21 @@ __device__ __forceinline__ Walk<KT> find_part(const ChunkArgs& a, uint8_t* scrat
     const int e = find_entry(place, entries, x);
     w.req = uniform(find_entry(blocks, a.n, e));
     w.blk = uniform(e - blocks[w.req]);
-    w.load(a);
+    w.load(request(w.req));
     w.open(a);
     const int in = static_cast<int>((x - place[e]) % w.places);
     w.item = uniform(static_cast<int>((x - place[e]) / w.places));
     w.left = a.p.Hkv * w.q.t.per - 1 - w.item;
-    w.t0 = uniform(line_tile(in));
+    w.t0 = uniform(chunk_tile(in, w.weight));
     if (w.t0 == 0) x -= in;            // a boundary among an item's first places is its begin
     const int64_t begin = x - (w.t0 == 0 ? 0 : in);
     if (y < done) {
       const int f = find_entry(place, entries, y), i = find_entry(blocks, a.n, f);
-      const Request q = request_of(a, i);
+      const Request q = request(i);
       const int blk = f - blocks[i], places = chunk_places<KT>(q.t, q.r, a.qb.window, a.qb.sinks, blk);
       const int item = static_cast<int>((y - place[f]) / places);
       const int64_t b = place[f] + static_cast<int64_t>(item) * places;
-      if (line_tile(static_cast<int>(y - b)) == 0) {
+      if (chunk_tile(static_cast<int>(y - b), tile_weight<KT>(q.t)) == 0) {
         y = b;
       } else if (b >= x) {   // begun here, and goes on in later CTAs
         const Work k = work_of<KT>(a, q, blk, item, 0, places);
@@ -353,7 +363,7 @@ __device__ __forceinline__ Walk<KT> find_part(const ChunkArgs& a, uint8_t* scrat
     }
     w.idle = x >= y;
     w.to_go = y - begin;
-    w.t1 = uniform(w.to_go >= w.places ? w.places - kItemPlaces : line_tile(static_cast<int>(w.to_go)));
+    w.set_end();
   }
   if ((tid & 31) == 0) *part_cut(a, c) = cut;
   return w;

@@ -63,7 +63,7 @@ static int check_tiles(const RowTiles& t, const Rows& r, int window, int sinks) 
     int seen = 0;
     for (int x : sees) seen += x;
     CHECK(k.tiles <= seen + 1);
-    CHECK(chunk_places<KT>(t, r, window, sinks, blk) == kItemPlaces + max_of(1, k.tiles));
+    CHECK(chunk_places<KT>(t, r, window, sinks, blk) == kChunkPlaces + tile_weight<KT>(t) * max_of(1, k.tiles));
   }
   return 0;
 }
@@ -72,19 +72,19 @@ static int check_tiles(const RowTiles& t, const Rows& r, int window, int sinks) 
 // its parts in slots of their own, which the CTA that begins it can tell
 template <int KT>
 static int check_line(const std::vector<Rows>& reqs, int rep, int heads, int window, int sinks, int ctas) {
-  struct Entry { int req, blk, places, items; long long base; };
+  struct Entry { int req, blk, places, items, weight; long long base; };
   std::vector<Entry> line;
   long long total = 0;
   for (size_t i = 0; i < reqs.size(); ++i) {
     const RowTiles t = row_tiles_of(reqs[i].rows, rep);
     for (int b = 0; b < t.blocks; ++b) {
       const int p = chunk_places<KT>(t, reqs[i], window, sinks, b);
-      line.push_back({(int)i, b, p, heads * t.per, total});
+      line.push_back({(int)i, b, p, heads * t.per, tile_weight<KT>(t), total});
       total += (long long)p * heads * t.per;
     }
   }
   if (total == 0) return 0;
-  const int workers = max_of(1, (int)(ctas < total / 2 ? ctas : total / 2));
+  const int workers = chunk_workers(total, ctas);
   struct Seg { int t0, t1, slot; };
   struct Cut { long long begin; int last, before; };
   std::vector<std::vector<Seg>> parts(total);
@@ -94,24 +94,26 @@ static int check_line(const std::vector<Rows>& reqs, int rep, int heads, int win
     long long x = split_begin(total, workers, c), y = split_begin(total, workers, c + 1);
     CHECK(x < y);
     int e = find(x), in = (int)((x - line[e].base) % line[e].places), item = (int)((x - line[e].base) / line[e].places);
-    int left = line[e].items - 1 - item, t0 = line_tile(in);
+    int left = line[e].items - 1 - item, t0 = chunk_tile(in, line[e].weight);
     if (t0 == 0) x -= in;
     const long long begin = x - (t0 == 0 ? 0 : in);
     Cut cut = {0, -1, 0};
     if (y < total) {
       const int f = find(y);
       const long long b = line[f].base + (y - line[f].base) / line[f].places * line[f].places;
-      if (line_tile((int)(y - b)) == 0) y = b;
+      if (chunk_tile((int)(y - b), line[f].weight) == 0) y = b;
       else if (b >= x) cut = {b, split_owner(total, workers, b + line[f].places - 1), b > x};
     }
     cuts.push_back(cut);
     if (x >= y) continue;
     long long to_go = y - begin, at = begin;
     int places = line[e].places;
-    int t1 = to_go >= places ? places - kItemPlaces : line_tile((int)to_go);
+    const auto end = [&] { return chunk_tile((int)(to_go < places ? to_go : places), line[e].weight); };
+    int t1 = end();
     for (int n = 0;; ++n) {
-      const bool whole = t0 == 0 && t1 == places - kItemPlaces;
-      CHECK(t1 > t0 && t1 <= places - kItemPlaces);
+      const int tiles = (places - kChunkPlaces) / line[e].weight;
+      const bool whole = t0 == 0 && t1 == tiles;
+      CHECK(t1 > t0 && t1 <= tiles);
       parts[at].push_back({t0, t1, whole ? -1 : 2 * c + (n > 0)});
       CHECK(whole || n == 0 || to_go <= places);   // cut items: a CTA's first and last
       to_go -= places;
@@ -123,7 +125,7 @@ static int check_line(const std::vector<Rows>& reqs, int rep, int heads, int win
         places = line[e].places;
       }
       t0 = 0;
-      t1 = to_go >= places ? places - kItemPlaces : line_tile((int)to_go);
+      t1 = end();
     }
   }
   std::vector<char> used(2 * ctas, 0), joined(total, 0);
@@ -143,7 +145,7 @@ static int check_line(const std::vector<Rows>& reqs, int rep, int heads, int win
       const auto& segs = parts[e.base + (long long)i * e.places];
       int next = 0;
       for (const Seg& s : segs) { CHECK(s.t0 == next); next = s.t1; }
-      CHECK(next == e.places - kItemPlaces);
+      CHECK(next == (e.places - kChunkPlaces) / e.weight);
       CHECK((segs.size() > 1) == (joined[e.base + (long long)i * e.places] != 0) && (segs.size() == 1) == (segs[0].slot < 0));
     }
   return 0;
