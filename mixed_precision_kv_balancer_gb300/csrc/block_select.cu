@@ -153,18 +153,20 @@ __global__ void __launch_bounds__(kBsWarps * 32) block_score_kernel(const Select
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   pdl_trigger();
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kBsWarps + w;
-  if (id >= a.warps) return;
+  // (who has nothing to do waits too: the grid is not done before the one before it)
+  const auto leave = [] { pdl_wait(); };
+  if (id >= a.warps) return leave();
   const int64_t rest = id / a.p.Hkv;
   const int h = static_cast<int>(id - rest * a.p.Hkv), r = static_cast<int>(rest / a.chunks);
   const int b0 = static_cast<int>(rest - static_cast<int64_t>(r) * a.chunks) * kBsBlocks;
   int32_t seq = a.row_seq ? a.row_seq[r] : r, page[kBsSteps];
-  if (static_cast<uint32_t>(seq) >= static_cast<uint32_t>(a.p.max_seqs)) return;
+  if (static_cast<uint32_t>(seq) >= static_cast<uint32_t>(a.p.max_seqs)) return leave();
   const int32_t* table = a.p.table + static_cast<size_t>(seq) * a.p.max_pages;
 #pragma unroll
   for (int i = 0; i < kBsSteps; ++i)   // asked for beside the length that tells whether they count
     page[i] = b0 + 32 * i + lane < a.p.max_pages ? table[b0 + 32 * i + lane] : -1;
   const int32_t nb = blocks_of_row(a, r, seq);
-  if (b0 >= nb || nb <= a.keep) return;
+  if (b0 >= nb || nb <= a.keep) return leave();
   const int unit = r * a.p.Hkv + h;
   const size_t layer0 = static_cast<size_t>(a.layer) * a.p.n_pages * a.p.Hkv;
   const int steps = min(kBsSteps, (nb - b0 + 31) / 32);

@@ -1026,12 +1026,12 @@ int launch(const ChunkArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return check_launch_after(e, "chunk_attention_kernel");
   kern<<<a.ctas, W::threads, kCaSmem, st>>>(km, vm, a);
   if (int r = check_launch("chunk_attention_kernel")) return r;
-  // Few rows an item: many parts, perhaps, and threads that share them; else 64 rows a CTA, so that all CTAs
-  // of a call fit the SMs at once.
+  // Few rows an item: many parts, perhaps, and threads that share them (one token behind 65536 slots, one key head,
+  // 152 parts: 31.5 us in all with four sets, 27 with eight); else 64 rows a CTA, so that all CTAs of a call fit the SMs at once.
   constexpr bool BF = TYPE == MIKV_PAGES_BF16;
-  const bool few = a.tile_rows <= 32;
-  const auto join = few ? chunk_join_kernel<BF, 1, 4, 4> : chunk_join_kernel<BF, 4, 1, 2>;
-  const int rows = few ? 4 : 64;
+  const bool few = a.tile_rows <= 32, fewest = a.tile_rows <= 8;
+  const auto join = fewest ? chunk_join_kernel<BF, 1, 8, 8> : few ? chunk_join_kernel<BF, 1, 4, 4> : chunk_join_kernel<BF, 4, 1, 2>;
+  const int rows = fewest ? 2 : few ? 4 : 64;
   return check_launch_after(launch_after(join, dim3((2 * a.tile_rows + rows - 1) / rows, a.ctas), dim3(kJoinThreads), 0, st, a),
                             "chunk_join_kernel");
 }
