@@ -108,9 +108,10 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xfffffff
 // Each half of the weights is announced (`ready`, one arrival a warp) as soon as it is written.
 // `last`: the last key that the row may see, its position p or less.  Args: qb.window, qb.sinks and scale.
 // PARTS 2: the scores are the sum of two products, the second COLS columns behind the first.
-template <bool BF, int COLS, int PARTS, class Args>
+// `settle` returns once all products into the accumulator that were issued are done; it is called before a rescaling.
+template <bool BF, int COLS, int PARTS, class Args, class Settle>
 __device__ __forceinline__ void softmax_tile(const Args& a, uint32_t ts, uint32_t to, bool whole, int p, int last, int j0, Row& r,
-                                             const uint32_t (&ready)[2]) {
+                                             const uint32_t (&ready)[2], const Settle& settle) {
   float s[COLS];
 #pragma unroll
   for (int c = 0; c < COLS / 32; ++c) ld32(ts + c * 32, s + c * 32);
@@ -156,6 +157,7 @@ __device__ __forceinline__ void softmax_tile(const Args& a, uint32_t ts, uint32_
     if (grew) r.m = top;
     r.l *= alpha;
     if (!r.first) {
+      settle();
 #pragma unroll 1
       for (int c = 0; c < kD; c += 32) {
         float o[32];

@@ -84,6 +84,7 @@ struct CaBars {
   uint64_t turn[2];                         // the tile's products may be issued
   uint64_t qfree;                           // the products that read the queries are done
   uint64_t q, s[2], p[2][2], o[2];          // queries landed; scores, half the weights, last sums written
+  uint64_t one_s[2], one_p[2][2], one_o;    // of an item of one query tile: its scores and weights by key tiles in turn; sums
 };
 
 // A request as every warp reads it.
@@ -499,12 +500,16 @@ __global__ void __launch_bounds__(Warps<TYPE == MIKV_PAGES_INT8>::threads, 1)
     }
     tc::mbar_init(smem_u32(&bar.q), W::loaders);
     tc::mbar_init(smem_u32(&bar.qfree), 2);
+    tc::mbar_init(smem_u32(&bar.one_o), 1);
     for (int t = 0; t < 2; ++t) {
       tc::mbar_init(smem_u32(&bar.turn[t]), 1);
       tc::mbar_init(smem_u32(&bar.s[t]), 1);
       tc::mbar_init(smem_u32(&bar.p[t][0]), 4);
       tc::mbar_init(smem_u32(&bar.p[t][1]), 4);
       tc::mbar_init(smem_u32(&bar.o[t]), 1);
+      tc::mbar_init(smem_u32(&bar.one_s[t]), 1);
+      tc::mbar_init(smem_u32(&bar.one_p[t][0]), 4);
+      tc::mbar_init(smem_u32(&bar.one_p[t][1]), 4);
     }
     tc::mbar_init_fence();
   }
@@ -558,6 +563,11 @@ __global__ void __launch_bounds__(Warps<TYPE == MIKV_PAGES_INT8>::threads, 1)
     const uint32_t ts = tmem + t * 128, to = tmem + kCaO + t * 128;
     const uint64_t qd = tc::smem_desc(sq + t * tc::kTileBytes), k0 = tc::smem_desc(ring), v0 = value_desc(ring);
     int p_par = 0, q_par = 0;        // parity of the next weights, and queries
+    uint32_t one_par = 0;            // of an item of one tile: of the next weights, by key tiles in turn
+    // Tile 1's scores and those of one tile's odd key tiles lie in the same columns, and two warps issue the products
+    // that read them: whoever comes next there waits until the other's last sums are made.
+    int sums[2] = {0, 0};            // items whose sums of tile 0, and of tile 1, have been announced
+    bool was_one = false;
     int slot = 0, par = 0;           // ring position and parity
     // The two warps issue in turns, one step each: the tiles then stay half a step apart, and one's
     // weights are made while the tensor core works for the other.
@@ -578,6 +588,72 @@ __global__ void __launch_bounds__(Warps<TYPE == MIKV_PAGES_INT8>::threads, 1)
         int vslot = 0, vpar = 0;     // the last step's values
         wait(smem_u32(&bar.q), q_par);
         q_par ^= 1;
+        const auto advance = [&] {   // the values of a tile follow its keys in the ring
+          vslot = slot + 1 == kCaRing ? 0 : slot + 1;
+          vpar = vslot == 0 ? par ^ 1 : par;
+          slot = vslot + 1 == kCaRing ? 0 : vslot + 1;
+          par = slot == 0 ? vpar ^ 1 : vpar;
+        };
+        if (uniform(w.nt) == 1) {
+          // One query tile: its scores lie in turn where both tiles' would, and those of the next key tile are made before
+          // this one's weights are there.
+          if (t == 0 && sums[1] > 0) wait(smem_u32(&bar.o[1]), (sums[1] - 1) & 1);
+          ++sums[0];
+          was_one = true;
+          for (int i = begin; i <= end; ++i) {
+            const bool keys = i < end;
+            if (keys) {
+              wait(smem_u32(&bar.full[slot]), par);
+              lead &= __all_sync(0xffffffffu, wait.ok) != 0;
+              tc::fence_after_sync();
+              if (lead && t == 0) {
+                const uint64_t kd = k0 + slot * desc_step(tc::kTileBytes);
+                const uint32_t scores = narrow(i) ? kFew : kScores;
+#pragma unroll
+                for (int c = 0; c < kD / 16; ++c) {
+                  const uint64_t off = desc_step((c >> 2) * tc::kKBlock + (c & 3) * 32);
+                  tc::mma_f16(tmem + (i & 1) * 128, qd + off, kd + off, scores, c > 0);
+                }
+                tc::commit(smem_u32(&bar.one_s[i & 1]));
+              }
+              if (lead) {
+                tc::commit(smem_u32(&bar.empty[slot]));
+                if (i == end - 1) tc::commit(smem_u32(&bar.qfree));
+              }
+            }
+            if (i > begin) {
+              wait(smem_u32(&bar.full[vslot]), vpar);
+              if (t == 0) {
+                const int b = (i - 1) & 1;
+                wait(smem_u32(&bar.one_p[b][0]), (one_par >> b) & 1);
+                wait(smem_u32(&bar.one_p[b][1]), (one_par >> b) & 1);
+                one_par ^= 1u << b;
+                lead &= __all_sync(0xffffffffu, wait.ok) != 0;
+                tc::fence_after_sync();
+                if (lead) {
+                  const uint64_t vd = v0 + vslot * desc_step(tc::kTileBytes);
+                  const int steps = few ? kCaNarrow / 16 : kCaRows / 16;
+#pragma unroll
+                  for (int c = 0; c < kCaRows / 16; ++c)
+                    if (c < steps) mma_ts(to, tmem + b * 128 + (Q8 ? c & 3 : c) * 8, vd + desc_step(c * 2048), kValues, more || c > 0);
+                  tc::commit(smem_u32(&bar.one_o));
+                  if (i == end) tc::commit(smem_u32(&bar.o[0]));
+                }
+                more = true;
+              }
+              lead &= __all_sync(0xffffffffu, wait.ok) != 0;
+              if (lead) tc::commit(smem_u32(&bar.empty[vslot]));
+            }
+            few = keys && narrow(i);
+            if (keys) advance();
+          }
+          heard(n);
+          continue;
+        }
+        if (t == 1 && was_one) wait(smem_u32(&bar.o[0]), (sums[0] - 1) & 1);
+        was_one = false;
+        sums[0] += uniform(w.last[0]) >= 0;
+        sums[1] += uniform(w.last[1]) >= 0;
         // after a wait that gave up no lane leads, nothing more is issued, and the others' waits run out
         for (int i = begin; i <= end; ++i) {
           // this step's scores from key tile i, behind the last step's sums over value tile i - 1
@@ -642,12 +718,7 @@ __global__ void __launch_bounds__(Warps<TYPE == MIKV_PAGES_INT8>::threads, 1)
             if (keys) tc::commit(smem_u32(&bar.empty[slot]));
             if (i == end - 1) tc::commit(smem_u32(&bar.qfree));   // the last scores
           }
-          if (keys) {   // the values of tile i follow its keys in the ring
-            vslot = slot + 1 == kCaRing ? 0 : slot + 1;
-            vpar = vslot == 0 ? par ^ 1 : par;
-            slot = vslot + 1 == kCaRing ? 0 : vslot + 1;
-            par = slot == 0 ? vpar ^ 1 : vpar;
-          }
+          if (keys) advance();
         }
       }
       heard(n);
@@ -797,31 +868,40 @@ __global__ void __launch_bounds__(Warps<TYPE == MIKV_PAGES_INT8>::threads, 1)
     more_registers<W::softmax_regs>();
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;   // the thread's TMEM lane is its row
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + kCaO + t * 128;
-    const uint32_t ready[2] = {smem_u32(&bar.p[t][0]), smem_u32(&bar.p[t][1])};
-    int s_par = 0, o_par = 0;
+    const uint32_t to = tmem + lanes + kCaO + t * 128;
+    uint32_t pars = 0;        // parities of the next scores: of a tile of two; of one tile's key tiles in turn
+    int done = 0, o_par = 0;  // key tiles of single tiles so far
     for (int n = 0;; ++n) {
       const Work* told = hear(n);
       if (!told) break;
       const Work& w = *told;
       if (t < w.nt) {
         Row r;
+        const bool one = w.nt == 1;   // (sees every key tile of its list)
         {
           const int p = w.pa[t] + row % w.tb, last = min(p, w.keys - 1);
           for (int i = w.begin; i < w.end; ++i) {
-            if (!w.sees(t, i)) continue;
+            if (!one && !w.sees(t, i)) continue;
             const int j0 = w.j0<KT>(i);
             const bool whole = tile_whole<KT>(a, w.pa[t], w.pb[t], w.keys, j0), few = !Q8 && tile_narrow(a, w.ts, i, j0);
-            wait(smem_u32(&bar.s[t]), s_par);
-            s_par ^= 1;
+            const int b = one ? i & 1 : t, which = one ? 1 + b : 0;
+            const uint32_t ts = tmem + lanes + b * 128;
+            const uint32_t first_half = smem_u32(one ? &bar.one_p[b][0] : &bar.p[t][0]), ready[2] = {first_half, first_half + 8};
+            const auto settle = [&] {   // one tile: the last sums were issued behind these scores
+              if (one) wait(smem_u32(&bar.one_o), (done - 1) & 1);
+              tc::fence_after_sync();
+            };
+            wait(smem_u32(one ? &bar.one_s[b] : &bar.s[t]), (pars >> which) & 1);
+            pars ^= 1u << which;
             tc::fence_after_sync();
             if (few)
-              softmax_tile<BF, kCaNarrow, 1>(a, ts, to, false, p, last, j0, r, ready);
+              softmax_tile<BF, kCaNarrow, 1>(a, ts, to, false, p, last, j0, r, ready, settle);
             else
-              softmax_tile<BF, KT, Q8 ? 2 : 1>(a, ts, to, whole, p, last, j0, r, ready);
+              softmax_tile<BF, KT, Q8 ? 2 : 1>(a, ts, to, whole, p, last, j0, r, ready, settle);
+            done += one;
           }
         }
-        const bool any = w.last[t] >= 0;
+        const bool any = one ? w.begin < w.end : w.last[t] >= 0;
         if (any) {
           wait(smem_u32(&bar.o[t]), o_par);
           o_par ^= 1;

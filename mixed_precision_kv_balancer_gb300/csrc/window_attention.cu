@@ -578,6 +578,7 @@ __global__ void __launch_bounds__(kWaThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + kWaO + t * 128;
     const uint32_t ready[2] = {smem_u32(&bar.p[t][0]), smem_u32(&bar.p[t][1])};
+    const auto settled = [] {};   // new scores are committed behind the sums before them
     int s_par = 0, o_par = 0;
     for (int n = 0;; ++n) {
       const Place pl = walk.place(a);
@@ -594,9 +595,9 @@ __global__ void __launch_bounds__(kWaThreads, 1)
           s_par ^= 1;
           tc::fence_after_sync();
           if (tile_narrow(a, w, i))
-            softmax_tile<BF, kWaNarrow, 1>(a, ts, to, false, p, p, j0, r, ready);
+            softmax_tile<BF, kWaNarrow, 1>(a, ts, to, false, p, p, j0, r, ready, settled);
           else
-            softmax_tile<BF, kWaRows, 1>(a, ts, to, tile_whole(a, tile, j0), p, p, j0, r, ready);
+            softmax_tile<BF, kWaRows, 1>(a, ts, to, tile_whole(a, tile, j0), p, p, j0, r, ready, settled);
         }
         if (tile.last >= 0) {
           wait(smem_u32(&bar.o[t]), o_par);
