@@ -26,6 +26,7 @@
 // two parts of each 64 rows apart in its buffer, so that all copies and products are as above: S_t has the two parts'
 // scores side by side, and P_t meets both parts of the values.
 #include <algorithm>
+#include <type_traits>
 
 #include "attention_tile.cuh"
 #include "chunk_index.h"
@@ -878,29 +879,37 @@ __global__ void __launch_bounds__(Warps<TYPE == MIKV_PAGES_INT8>::threads, 1)
       if (t < w.nt) {
         Row r;
         const bool one = w.nt == 1;   // (sees every key tile of its list)
-        {
+        // (one loop that asks for every tile which it is took 382 us where this takes 361: 8192 causal rows of 32 heads)
+        const auto tiles = [&](auto alone) {
+          constexpr bool kOne = decltype(alone)::value;
           const int p = w.pa[t] + row % w.tb, last = min(p, w.keys - 1);
           for (int i = w.begin; i < w.end; ++i) {
-            if (!one && !w.sees(t, i)) continue;
+            if (!kOne && !w.sees(t, i)) continue;
             const int j0 = w.j0<KT>(i);
             const bool whole = tile_whole<KT>(a, w.pa[t], w.pb[t], w.keys, j0), few = !Q8 && tile_narrow(a, w.ts, i, j0);
-            const int b = one ? i & 1 : t, which = one ? 1 + b : 0;
+            const int b = kOne ? i & 1 : t, which = kOne ? 1 + b : 0;
             const uint32_t ts = tmem + lanes + b * 128;
-            const uint32_t first_half = smem_u32(one ? &bar.one_p[b][0] : &bar.p[t][0]), ready[2] = {first_half, first_half + 8};
+            const uint32_t first_half = smem_u32(kOne ? &bar.one_p[b][0] : &bar.p[t][0]), ready[2] = {first_half, first_half + 8};
             const auto settle = [&] {   // one tile: the last sums were issued behind these scores
-              if (one) wait(smem_u32(&bar.one_o), (done - 1) & 1);
-              tc::fence_after_sync();
+              if (kOne) {
+                wait(smem_u32(&bar.one_o), (done - 1) & 1);
+                tc::fence_after_sync();
+              }
             };
-            wait(smem_u32(one ? &bar.one_s[b] : &bar.s[t]), (pars >> which) & 1);
+            wait(smem_u32(kOne ? &bar.one_s[b] : &bar.s[t]), (pars >> which) & 1);
             pars ^= 1u << which;
             tc::fence_after_sync();
             if (few)
               softmax_tile<BF, kCaNarrow, 1>(a, ts, to, false, p, last, j0, r, ready, settle);
             else
               softmax_tile<BF, KT, Q8 ? 2 : 1>(a, ts, to, whole, p, last, j0, r, ready, settle);
-            done += one;
+            done += kOne;
           }
-        }
+        };
+        if (one)
+          tiles(std::true_type{});
+        else
+          tiles(std::false_type{});
         const bool any = one ? w.begin < w.end : w.last[t] >= 0;
         if (any) {
           wait(smem_u32(&bar.o[t]), o_par);

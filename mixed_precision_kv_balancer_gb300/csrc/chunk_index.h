@@ -61,15 +61,15 @@ MIKV_HD KeyTiles chunk_tiles(const RowTiles& t, const Rows& r, int32_t window, i
   k.ns = max_of(k.ts, min_of(st, st > k.tw0 ? k.tiles : k.ts));
   return k;
 }
-// The line: every item takes kChunkPlaces places for what it costs beside its key tiles, and `weight` a tile: four
-// where two tiles of rows meet it, three where one does.  (Four chunks beside sixty single tokens, 304 us with equal
-// weights: 268 with 3 to 4, 281 with 2 to 3, 312 with 1 to 2; 8192 causal rows of 32 heads, 424 us with 8 places
-// an item, 377 with 12, 370 with 16, 374 with 20.)  INT8 tiles cost the same, whatever the rows: their codes'
-// conversion.
-constexpr int kChunkPlaces = 16;
+// The line: every item takes kChunkPlaces places for what it costs beside its key tiles, and `weight` a tile: eight
+// where two tiles of rows meet it, five where one does.  (Four chunks beside sixty single tokens, 304 us with equal
+// weights: 276 with 3 to 4, 258 with 5 to 8, 272 with 1 to 2; 8192 causal rows of 32 heads, 424 us with two tiles'
+// places an item, 377 with three, 370 with four, 374 with five.)  INT8 tiles cost the same, whatever the rows: their
+// codes' conversion.
+constexpr int kChunkPlaces = 32;
 template <int KT>
 MIKV_HD int32_t tile_weight(const RowTiles& t) {
-  return KT == kKeyRows && t.groups == 1 && t.blocks <= 1 ? 3 : 4;
+  return KT == kKeyRows && t.groups == 1 && t.blocks <= 1 ? 5 : 8;
 }
 // Places of each item of a block; the tile that a boundary `at` places behind an item's begin names (0: its begin).
 template <int KT>
@@ -79,7 +79,7 @@ MIKV_HD int32_t chunk_places(const RowTiles& t, const Rows& r, int32_t window, i
 MIKV_HD int32_t chunk_tile(int32_t at, int32_t weight) { return max_of(0, at - kChunkPlaces) / weight; }
 // CTAs that get a part: not fewer than two tiles each, as far as there are any.
 MIKV_HD int32_t chunk_workers(int64_t total, int32_t ctas) {
-  return total / 8 >= ctas ? ctas : max_of(1, static_cast<int32_t>(total / 8));
+  return total / 16 >= ctas ? ctas : max_of(1, static_cast<int32_t>(total / 16));
 }
 
 }  // namespace mikv
