@@ -8,8 +8,8 @@
 // fl(fl(u s_b) s_q) is the same to the bit wherever it is computed, so that the choice is too.  The
 // heads of a group read one set of blocks: a block's score is the largest of theirs.
 //
-// Three kernels: the queries' codes, in the order in which the products take them (once a (row, key head): 32 divisions
-// a lane are more than the scores of 128 blocks); scores of all blocks (bound by HBM: 260 bytes a block and key head; mma.sync on
+// Up to three kernels: the queries' codes, in the order in which the products take them, once a (row, key head), where there
+// are many warps that would make them anew; scores of all blocks (bound by HBM: 260 bytes a block and key head; mma.sync on
 // fp16 numbers, which hold the codes exactly, as fp32 does the sums, with 16 blocks as its M and 8 query heads as its N;
 // four-term integer products took 34 us, 8-bit matrix instructions 37, for 192 units of up to 4096 blocks), and the choice of the `keep` best of each (row, key head), written in the
 // blocks' order.  The choice is a search by digits of the scores' bits, but of digits that begin below what all
@@ -82,18 +82,11 @@ __device__ __forceinline__ float* query_scales(const SelectArgs& a, int unit, in
   float* s = reinterpret_cast<float*>(a.codes + static_cast<size_t>(a.rows) * a.p.Hkv * a.groups * 256);
   return s + (static_cast<size_t>(unit) * a.groups + group) * kBsHeads;
 }
-// A warp: the codes of up to kBsHeads query heads of one (row, key head).
-__global__ void __launch_bounds__(kBsWarps * 32) block_query_kernel(const SelectArgs a) {
+// The codes of query heads g0 .. of one (row, key head), by a warp: lane 4 g + t has those of head g0 + g, channels
+// 64 k + 16 t .. + 15, in the order in which those of the blocks are read: below 0 (met by lo), then above (by hi).
+__device__ __forceinline__ void query_codes(const SelectArgs& a, int unit, int g0, uint32_t (&q)[16][2], float& sq) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  pdl_trigger();
-  const int id = blockIdx.x * kBsWarps + (threadIdx.x >> 5);
-  if (id >= a.rows * a.p.Hkv * a.groups) return;
-  const int unit = id / a.groups, g0 = (id - unit * a.groups) * kBsHeads;
   const bool bf = a.p.type == MIKV_PAGES_BF16;
-  // the codes of query head g0 + g, channels 64 k + 16 t .. + 15, in the order in which those of the blocks are read:
-  // below 0 (met by lo), then above (by hi)
-  uint32_t q[16][2];
-  float sq = 0.f;
   const bool there = g0 + g < a.rep;
   {
     uint4 v[2][2];
@@ -127,34 +120,54 @@ __global__ void __launch_bounds__(kBsWarps * 32) block_query_kernel(const Select
       bad |= __shfl_xor_sync(0xffffffffu, static_cast<int>(bad), o) != 0;
     }
     sq = bad ? INFINITY : __fdiv_rn(top, 127.f);   // no finite query: its scores are 0 * infinity
+    // A product with the reciprocal is within 2^-15 of the quotient, so both round to the same whole number unless the
+    // product lies that near to a half: then, and where the reciprocal is no finite number, the division decides.
     const bool some = !bad && sq > 0.f;
+    const float inv = some ? __frcp_rn(sq) : 0.f;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         float x[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          x[e] = some ? fminf(fmaxf(rintf(__fdiv_rn(to_float(word(k, c) >> (16 * e) & 0xffffu, bf), sq)), -127.f), 127.f) : 0.f;
+        for (int e = 0; e < 2; ++e) {
+          const float v0 = to_float(word(k, c) >> (16 * e) & 0xffffu, bf), p = __fmul_rn(v0, inv);
+          float r = rintf(p);
+          if (!(fabsf(p - r) < 0.49f)) r = rintf(__fdiv_rn(v0, sq));
+          x[e] = some ? fminf(fmaxf(r, -127.f), 127.f) : 0.f;
+        }
         q[4 * k + (c >> 1)][c & 1] = pack_half2(__float2half_rn(fminf(x[0], 0.f)), __float2half_rn(fminf(x[1], 0.f)));
         q[8 + 4 * k + (c >> 1)][c & 1] = pack_half2(__float2half_rn(fmaxf(x[0], 0.f)), __float2half_rn(fmaxf(x[1], 0.f)));
       }
   }
+}
+__global__ void __launch_bounds__(kBsWarps * 32) block_query_kernel(const SelectArgs a) {
+  const int lane = threadIdx.x & 31;
+  pdl_trigger();
+  const int id = blockIdx.x * kBsWarps + (threadIdx.x >> 5);
+  if (id >= a.rows * a.p.Hkv * a.groups) return;
+  const int unit = id / a.groups, g0 = (id - unit * a.groups) * kBsHeads;
+  uint32_t q[16][2];
+  float sq;
+  query_codes(a, unit, g0, q, sq);
   uint4* codes = a.codes + static_cast<size_t>(id) * 256 + lane;
 #pragma unroll
   for (int e = 0; e < 8; ++e) codes[e * 32] = make_uint4(q[2 * e][0], q[2 * e][1], q[2 * e + 1][0], q[2 * e + 1][1]);
-  if (t == 0) query_scales(a, unit, g0 / kBsHeads)[g] = sq;
+  if ((lane & 3) == 0) query_scales(a, unit, g0 / kBsHeads)[lane >> 2] = sq;
 }
 
 // A warp: kBsBlocks blocks of one (row, key head), 32 a step; the warps of a CTA have the heads of the same blocks side by
-// side, whose bounds lie side by side.  Lane 4 g + t holds the codes of query head g, as the products take them.
+// side, whose bounds lie side by side.  OWN: it makes the queries' codes itself.
+template <bool OWN>
 __global__ void __launch_bounds__(kBsWarps * 32) block_score_kernel(const SelectArgs a) {
   extern __shared__ __align__(16) uint4 s_b[];   // [warp][ring][32 blocks][16 pieces], swizzled by the block
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   pdl_trigger();
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kBsWarps + w;
   // (who has nothing to do waits too: the grid is not done before the one before it)
-  const auto leave = [] { pdl_wait(); };
+  const auto leave = [] {
+    if (!OWN) pdl_wait();
+  };
   if (id >= a.warps) return leave();
   const int64_t rest = id / a.p.Hkv;
   const int h = static_cast<int>(id - rest * a.p.Hkv), r = static_cast<int>(rest / a.chunks);
@@ -199,18 +212,23 @@ __global__ void __launch_bounds__(kBsWarps * 32) block_score_kernel(const Select
       if (i < steps) fetch(i, at[i]);
       cp_async_commit();
     }
-    if (g0 == 0) pdl_wait();   // the queries' codes are there
     uint32_t q[16][2];
-    const uint4* codes = a.codes + (static_cast<size_t>(unit) * a.groups + g0 / kBsHeads) * 256 + lane;
+    float sq;
+    if (OWN) {
+      query_codes(a, unit, g0, q, sq);
+    } else {
+      if (g0 == 0) pdl_wait();   // the codes are there
+      const uint4* codes = a.codes + (static_cast<size_t>(unit) * a.groups + g0 / kBsHeads) * 256 + lane;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint4 x = codes[e * 32];
-      q[2 * e][0] = x.x;
-      q[2 * e][1] = x.y;
-      q[2 * e + 1][0] = x.z;
-      q[2 * e + 1][1] = x.w;
+      for (int e = 0; e < 8; ++e) {
+        const uint4 x = codes[e * 32];
+        q[2 * e][0] = x.x;
+        q[2 * e][1] = x.y;
+        q[2 * e + 1][0] = x.z;
+        q[2 * e + 1][1] = x.w;
+      }
+      sq = query_scales(a, unit, g0 / kBsHeads)[g];
     }
-    const float sq = query_scales(a, unit, g0 / kBsHeads)[g];
     // scales of the heads whose sums this lane holds
     const float s2[2] = {__shfl_sync(0xffffffffu, sq, 8 * t), __shfl_sync(0xffffffffu, sq, 8 * t + 4)};
 #pragma unroll
@@ -220,21 +238,26 @@ __global__ void __launch_bounds__(kBsWarps * 32) block_score_kernel(const Select
       __syncwarp();
       const uint32_t src = ring + i % kBsRing * (32 * 2 * kD);
       float top[2][2];   // blocks 16 mt + g and + 8
+      float d[2][2][4] = {};   // two sums each, so that products wait for one another less (whole numbers: any order gives the same)
+      const uint32_t row = src + g * (2 * kD) + ((t ^ ((g & 1) << 2)) << 4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {   // 64 codes: of lo, lo, hi, hi
+        uint4 x[2][2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e >> 1][e & 1] = lds128((row ^ (k << 6)) + e * 8 * 2 * kD);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            const uint4 &y0 = x[mt][0], &y1 = x[mt][1];
+            const uint32_t u0 = (s == 0 ? y0.x : s == 1 ? y0.y : s == 2 ? y0.z : y0.w) ^ 0x80808080u;
+            const uint32_t u1 = (s == 0 ? y1.x : s == 1 ? y1.y : s == 2 ? y1.z : y1.w) ^ 0x80808080u;
+            mma16816(d[mt][s & 1], codes_f16(u0, 0x4140u), codes_f16(u1, 0x4140u), codes_f16(u0, 0x4342u), codes_f16(u1, 0x4342u),
+                     q[4 * k + s][0], q[4 * k + s][1]);
+          }
+      }
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-        float d[4] = {};
-        const uint32_t row = src + (mt * 16 + g) * (2 * kD) + ((t ^ ((g & 1) << 2)) << 4);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {   // 64 codes: of lo, lo, hi, hi
-          const uint4 x = lds128(row ^ (k << 6)), y = lds128((row ^ (k << 6)) + 8 * 2 * kD);
-          const uint32_t c0[4] = {x.x, x.y, x.z, x.w}, c1[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const uint32_t u0 = c0[s] ^ 0x80808080u, u1 = c1[s] ^ 0x80808080u;
-            mma16816(d, codes_f16(u0, 0x4140u), codes_f16(u1, 0x4140u), codes_f16(u0, 0x4342u), codes_f16(u1, 0x4342u), q[4 * k + s][0],
-                     q[4 * k + s][1]);
-          }
-        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const float scale = __shfl_sync(0xffffffffu, sb[i], mt * 16 + half * 8 + g);
@@ -242,7 +265,7 @@ __global__ void __launch_bounds__(kBsWarps * 32) block_score_kernel(const Select
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             if (g0 + 2 * t + j < a.rep) {
-              const float x = __fmul_rn(__fmul_rn(d[2 * half + j], scale), s2[j]);
+              const float x = __fmul_rn(__fmul_rn(d[mt][0][2 * half + j] + d[mt][1][2 * half + j], scale), s2[j]);
               top[mt][half] = fmaxf(top[mt][half], isnan(x) ? INFINITY : x);
             }
 #pragma unroll
@@ -495,13 +518,22 @@ extern "C" int mikv_block_select(const void* q, const mikv_pages* pages, int lay
   const int64_t ctas = (a.warps - 1) / kBsWarps + 1;
   if (ctas > 0x7fffffffLL) return fail(MIKV_ESHAPE, "block_select: rows=%d max_pages=%d", rows, a.p.max_pages);
   const cudaStream_t st = as_stream(stream);
-  const cudaError_t e = cudaFuncSetAttribute(block_score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBsSmem);
+  // (one row of 8 key heads and 313 blocks takes 11 us either way, with a launch less where the codes are made in place; 24
+  // rows of up to 4096 blocks take 36 us with a kernel for them, 49 without)
+  const bool own = a.warps <= 8 * kNumSMs;
+  const auto score = own ? block_score_kernel<true> : block_score_kernel<false>;
+  const cudaError_t e = cudaFuncSetAttribute(score, cudaFuncAttributeMaxDynamicSharedMemorySize, kBsSmem);
   if (e != cudaSuccess) return check_launch_after(e, "block_score_kernel");
-  block_query_kernel<<<(rows * a.p.Hkv * a.groups - 1) / kBsWarps + 1, kBsWarps * 32, 0, st>>>(a);
-  if (int r = check_launch("block_query_kernel")) return r;
-  if (int r = check_launch_after(launch_after(block_score_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kBsWarps * 32), kBsSmem, st, a),
-                                 "block_score_kernel"))
-    return r;
+  if (own) {
+    score<<<static_cast<unsigned>(ctas), kBsWarps * 32, kBsSmem, st>>>(a);
+    if (int r = check_launch("block_score_kernel")) return r;
+  } else {
+    block_query_kernel<<<(rows * a.p.Hkv * a.groups - 1) / kBsWarps + 1, kBsWarps * 32, 0, st>>>(a);
+    if (int r = check_launch("block_query_kernel")) return r;
+    if (int r = check_launch_after(launch_after(score, dim3(static_cast<unsigned>(ctas)), dim3(kBsWarps * 32), kBsSmem, st, a),
+                                   "block_score_kernel"))
+      return r;
+  }
   const auto pick = a.p.max_pages <= 2 * kPickThreads    ? block_pick_kernel<2>
                     : a.p.max_pages <= 8 * kPickThreads  ? block_pick_kernel<8>
                     : a.p.max_pages <= 32 * kPickThreads ? block_pick_kernel<32>
