@@ -969,108 +969,82 @@ __global__ void __launch_bounds__(Warps<TYPE == MIKV_PAGES_INT8>::threads, 1)
   if (warp == W::mma) tc::tmem_dealloc(tmem, kCaCols);
 }
 
-// CTA (slice, c): joins STEPS * ROWS rows of the item that CTA c has begun and not ended, in a fixed order.  A thread
-// takes 8 channels of STEPS rows (a part's rows lie side by side); GROUPS sets of threads share the parts, BATCH of
-// them requested together.
+// CTA (slice, c): joins ROWS rows of the item that CTA c has begun and not ended, in a fixed order.  A thread takes 8
+// channels of a row (a part's rows lie side by side); GROUPS sets of threads share the parts, BATCH of them
+// requested together.
 constexpr int kJoinThreads = 256;
-template <bool BF, int STEPS, int GROUPS, int BATCH>
+template <bool BF, int GROUPS, int BATCH>
 __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkArgs a) {
-  constexpr int kThreads = kJoinThreads / GROUPS, kRows = kThreads / (kD / 8);   // of a group, and of a step
-  __shared__ float s_o[GROUPS > 1 ? GROUPS - 1 : 1][STEPS][8][kThreads];
-  __shared__ float2 s_ml[GROUPS > 1 ? GROUPS - 1 : 1][STEPS][kThreads];
+  constexpr int kThreads = kJoinThreads / GROUPS, kRows = kThreads / (kD / 8);   // of a group
+  __shared__ float s_o[GROUPS > 1 ? GROUPS - 1 : 1][8][kThreads];
+  __shared__ float2 s_ml[GROUPS > 1 ? GROUPS - 1 : 1][kThreads];
   const int tid = threadIdx.x % kThreads, group = threadIdx.x / kThreads, c0 = blockIdx.y;
   pdl_wait();
   const Cut cut = *part_cut(a, c0);
   const int c1 = cut.last;
   if (c1 < 0) return;
-  const int ch = tid / kRows * 8;
-  struct Sum {
-    float m = -INFINITY, l = 0.f, o[8] = {};
-    __device__ __forceinline__ void add(float2 x, const float (&p)[8]) {
-      const float mn = fmaxf(m, x.x), ref = mn == -INFINITY ? 0.f : mn;
-      const float f = ex2(m - ref), fx = ex2(x.x - ref);
-      l = l * f + x.y * fx;
+  const int ch = tid / kRows * 8, i = blockIdx.x * kRows + tid % kRows, t = i >= a.tile_rows, row = i - t * a.tile_rows;
+  const int sub = row / cut.tb, q = (t ? cut.q0[1] : cut.q0[0]) + row - sub * cut.tb;
+  const bool live = i < 2 * a.tile_rows && sub < (t ? cut.heads[1] : cut.heads[0]) && q < cut.rows;
+  float m = -INFINITY, l = 0.f, o[8] = {};
+  const auto add = [&](float2 x, const float (&p)[8]) {
+    const float mn = fmaxf(m, x.x), ref = mn == -INFINITY ? 0.f : mn;
+    const float f = ex2(m - ref), fx = ex2(x.x - ref);
+    l = l * f + x.y * fx;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = o[e] * f + p[e] * fx;
-      m = mn;
-    }
+    for (int e = 0; e < 8; ++e) o[e] = o[e] * f + p[e] * fx;
+    m = mn;
   };
-  Sum s[STEPS];
-  int at[STEPS], head[STEPS], tile[STEPS], row[STEPS];
-  bool live[STEPS];
+  if (live) {
+    for (int p0 = c0 + group; p0 <= c1; p0 += BATCH * GROUPS) {
+      float2 x[BATCH];
+      float4 v[BATCH][2];
 #pragma unroll
-  for (int k = 0; k < STEPS; ++k) {
-    const int i = (blockIdx.x * STEPS + k) * kRows + tid % kRows;
-    tile[k] = i >= a.tile_rows;
-    row[k] = i - tile[k] * a.tile_rows;
-    const int sub = row[k] / cut.tb, q = (tile[k] ? cut.q0[1] : cut.q0[0]) + row[k] - sub * cut.tb;
-    live[k] = i < 2 * a.tile_rows && sub < (tile[k] ? cut.heads[1] : cut.heads[0]) && q < cut.rows;
-    at[k] = cut.row0 + q;
-    head[k] = (tile[k] ? cut.head[1] : cut.head[0]) + sub;
-  }
-  for (int p0 = c0 + group; p0 <= c1; p0 += BATCH * GROUPS) {
-    float2 x[BATCH][STEPS];
-    float4 v[BATCH][STEPS][2];
-#pragma unroll
-    for (int e = 0; e < BATCH; ++e) {
-      const int p = p0 + e * GROUPS, slot = 2 * p + (p == c0 ? cut.before : 0);
-#pragma unroll
-      for (int k = 0; k < STEPS; ++k) {
-        x[e][k] = make_float2(-INFINITY, 0.f);
-        v[e][k][0] = v[e][k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p <= c1 && live[k]) {
-          const float4* sums = reinterpret_cast<const float4*>(part_sums(a, slot, tile[k], row[k], ch));
-          x[e][k] = *part_ml(a, slot, tile[k], row[k]);
-          v[e][k][0] = sums[0];
-          v[e][k][1] = sums[1];
+      for (int e = 0; e < BATCH; ++e) {
+        const int p = p0 + e * GROUPS, slot = 2 * p + (p == c0 ? cut.before : 0);
+        x[e] = make_float2(-INFINITY, 0.f);
+        v[e][0] = v[e][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p <= c1) {
+          const float4* sums = reinterpret_cast<const float4*>(part_sums(a, slot, t, row, ch));
+          x[e] = *part_ml(a, slot, t, row);
+          v[e][0] = sums[0];
+          v[e][1] = sums[1];
         }
       }
-    }
 #pragma unroll
-    for (int e = 0; e < BATCH; ++e)
-#pragma unroll
-      for (int k = 0; k < STEPS; ++k) {
+      for (int e = 0; e < BATCH; ++e) {
         // a sum of 0: nothing seen there, and no sums written
-        const bool none = x[e][k].y == 0.f;
-        const float4 y = v[e][k][0], z = v[e][k][1];
-        const float w[8] = {none ? 0.f : y.x, none ? 0.f : y.y, none ? 0.f : y.z, none ? 0.f : y.w,
-                            none ? 0.f : z.x, none ? 0.f : z.y, none ? 0.f : z.z, none ? 0.f : z.w};
-        s[k].add(x[e][k], w);
+        const bool none = x[e].y == 0.f;
+        const float w[8] = {none ? 0.f : v[e][0].x, none ? 0.f : v[e][0].y, none ? 0.f : v[e][0].z, none ? 0.f : v[e][0].w,
+                            none ? 0.f : v[e][1].x, none ? 0.f : v[e][1].y, none ? 0.f : v[e][1].z, none ? 0.f : v[e][1].w};
+        add(x[e], w);
       }
+    }
   }
   if (GROUPS > 1) {
     if (group > 0) {
 #pragma unroll
-      for (int k = 0; k < STEPS; ++k) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s_o[group - 1][k][e][tid] = s[k].o[e];
-        s_ml[group - 1][k][tid] = make_float2(s[k].m, s[k].l);
-      }
+      for (int e = 0; e < 8; ++e) s_o[group - 1][e][tid] = o[e];
+      s_ml[group - 1][tid] = make_float2(m, l);
     }
     __syncthreads();
     if (group > 0) return;
 #pragma unroll
-    for (int g = 0; g < GROUPS - 1; ++g)
+    for (int g = 0; g < GROUPS - 1; ++g) {
+      float w[8];
 #pragma unroll
-      for (int k = 0; k < STEPS; ++k) {
-        float w[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = s_o[g][k][e][tid];
-        s[k].add(s_ml[g][k][tid], w);
-      }
+      for (int e = 0; e < 8; ++e) w[e] = s_o[g][e][tid];
+      add(s_ml[g][tid], w);
+    }
   }
-#pragma unroll
-  for (int k = 0; k < STEPS; ++k) {
-    if (!live[k]) continue;
-    const float* o = s[k].o;
-    const float l = s[k].l, inv = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<uint4*>(a.out.row(0, head[k], at[k]) + ch * 2) =
-        make_uint4(pack2<BF>(o[0] * inv, o[1] * inv), pack2<BF>(o[2] * inv, o[3] * inv), pack2<BF>(o[4] * inv, o[5] * inv),
-                   pack2<BF>(o[6] * inv, o[7] * inv));
-    if (ch == 0 && a.lse)
-      a.lse[static_cast<int64_t>(at[k]) * a.Hq + head[k]] =
-          l == 0.f ? -INFINITY : (s[k].m + (log2f(l) - Weights<BF>::shift)) * 0.6931471805599453f;
-  }
+  if (!live) return;
+  const int head = (t ? cut.head[1] : cut.head[0]) + sub, at = cut.row0 + q;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<uint4*>(a.out.row(0, head, at) + ch * 2) =
+      make_uint4(pack2<BF>(o[0] * inv, o[1] * inv), pack2<BF>(o[2] * inv, o[3] * inv), pack2<BF>(o[4] * inv, o[5] * inv),
+                 pack2<BF>(o[6] * inv, o[7] * inv));
+  if (ch == 0 && a.lse)
+    a.lse[static_cast<int64_t>(at) * a.Hq + head] = l == 0.f ? -INFINITY : (m + (log2f(l) - Weights<BF>::shift)) * 0.6931471805599453f;
 }
 
 int tile_rows_of(int rows, int rep) { return static_cast<int>(std::min<int64_t>(kCaRows, static_cast<int64_t>(rows) * rep)); }
@@ -1116,11 +1090,12 @@ int launch(const ChunkArgs& a, cudaStream_t st) {
   kern<<<a.ctas, W::threads, kCaSmem, st>>>(km, vm, a);
   if (int r = check_launch("chunk_attention_kernel")) return r;
   // Few rows an item: many parts, perhaps, and threads that share them (one token behind 65536 slots, one key head,
-  // 152 parts: 31.5 us in all with four sets, 27 with eight); else 64 rows a CTA, so that all CTAs of a call fit the SMs at once.
+  // 152 parts: 31.5 us in all with four sets, 27 with eight); else 16 rows a CTA, whose few registers leave room for five an
+  // SM (2048 causal rows of 32 heads: 58 us in all with 64 rows a CTA, one an SM, 55 this way).
   constexpr bool BF = TYPE == MIKV_PAGES_BF16;
   const bool few = a.tile_rows <= 32, fewest = a.tile_rows <= 8;
-  const auto join = fewest ? chunk_join_kernel<BF, 1, 8, 8> : few ? chunk_join_kernel<BF, 1, 4, 4> : chunk_join_kernel<BF, 4, 1, 2>;
-  const int rows = fewest ? 2 : few ? 4 : 64;
+  const auto join = fewest ? chunk_join_kernel<BF, 8, 8> : few ? chunk_join_kernel<BF, 4, 4> : chunk_join_kernel<BF, 1, 2>;
+  const int rows = fewest ? 2 : few ? 4 : 16;
   return check_launch_after(launch_after(join, dim3((2 * a.tile_rows + rows - 1) / rows, a.ctas), dim3(kJoinThreads), 0, st, a),
                             "chunk_join_kernel");
 }
