@@ -184,9 +184,9 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const Pool p
     const int32_t s = row_seq[r], at = row_pos[r], s1 = r > 0 ? row_seq[r - 1] : -1, at1 = r > 0 ? row_pos[r - 1] : -1;
     if (static_cast<uint32_t>(s) < static_cast<uint32_t>(p.max_seqs) && at >= 0) {
       const uint32_t b = div_of(static_cast<uint32_t>(at), p.ps);
-      const bool again = s1 == s && at1 >= 0 && div_of(static_cast<uint32_t>(at1), p.ps) == b;
+      const int32_t len = p.len_of(s);
+      const bool again = s1 == s && at1 >= 0 && at1 < len && div_of(static_cast<uint32_t>(at1), p.ps) == b;
       if (!again && at < p.cap) {
-        const int32_t len = p.len_of(s);
         page = p.table[static_cast<size_t>(s) * p.max_pages + b];
         fill = min(static_cast<int32_t>(p.ps.d), len - static_cast<int32_t>(b * p.ps.d));
         if (at >= len) {

@@ -343,3 +343,12 @@ def test_all_blocks_are_dense_attention(type):
     want, wl, mag = ph.expect(cache, q, 0, 0, 0)
     ph.close(out, want, mag, ph.HALF_STEP[type], weights=2.0 ** -16)
     ph.close_lse(lse, wl)
+
+
+def test_bounds_behind_a_row_past_the_length():
+    """A row past its sequence's length does nothing, so that the next one on its page does the page."""
+    cache = ph.make([13], 8, 1, "fp16")
+    buf, want = cache.bounds_buffers(), _bounds_of_all(cache)
+    _lib.mikv_page_bounds(cache, 0, ints([0, 0, 0]), ints([15, 14, 9]), *buf)
+    page = int(cache.table[0, 1])
+    assert torch.equal(buf[0][0, page], want[0][0, page]) and torch.equal(buf[1][0, page], want[1][0, page]) and buf[1][0, page, 0] > 0
