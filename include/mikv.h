@@ -559,7 +559,7 @@ size_t mikv_window_attention_workspace_bytes(int B, int Hq, int Hkv, int Tq, int
  *                             past the sequence's length and on a page outside the pool (reported,
  *                             mikv_wait_status bit 64)
  * Rows of requests that were refused keep their places: a batch is laid out from its counts alone.
- * n at most 4096; n_pages * page_size < 2^31; n == 0 with rows == 0 does nothing.
+ * n at most 4096, rows at most 2^30; n_pages * page_size < 2^31; n == 0 with rows == 0 does nothing.
  * Errors: EINVAL (null), ESHAPE, and the cache's (EALIGN, EUNSUPPORTED), ECUDA.
  */
 int mikv_batch_rows(const mikv_pages* p, const int32_t* seqs, const int32_t* start, const int32_t* counts, int n, int rows,
@@ -571,6 +571,7 @@ int mikv_batch_rows(const mikv_pages* p, const int32_t* seqs, const int32_t* sta
  * Stored, quantised and kept off shared pages as by mikv_paged_append; a slot outside the pool is
  * skipped and reported (mikv_wait_status, bit 64).  The slots of a call differ (those of
  * mikv_batch_rows do, for pages of one owner): one that is named twice is left with parts of either row.
+ * rows at most 2^30.
  */
 int mikv_slot_append(const mikv_pages* p, int layer, const mikv_rows* k, const mikv_rows* v, int rows, const int32_t* slots,
                      void* stream);

@@ -18,6 +18,7 @@ namespace {
 constexpr int kMapThreads = 256;
 constexpr int kMapRows = 4 * kMapThreads;   // of a CTA
 constexpr int kMaxBatch = 4096;             // requests of a call
+constexpr int kMaxMapRows = 1 << 30;        // and its rows: numbers of a CTA behind the last one fit 32 bits too
 
 struct MapArgs {
   Pool p;
@@ -136,7 +137,7 @@ extern "C" int mikv_batch_rows(const mikv_pages* pages, const int32_t* seqs, con
   if (int e = check_pages(pages, "batch_rows", &a.p)) return e;
   if (static_cast<int64_t>(a.p.n_pages) * a.p.ps.d > 0x7fffffffLL)
     return fail(MIKV_ESHAPE, "batch_rows: n_pages * page_size above 2^31");
-  if (n < 0 || n > kMaxBatch || rows < 0 || (!seqs && n > a.p.max_seqs)) return fail(MIKV_ESHAPE, "batch_rows: n=%d rows=%d", n, rows);
+  if (n < 0 || n > kMaxBatch || rows < 0 || rows > kMaxMapRows || (!seqs && n > a.p.max_seqs)) return fail(MIKV_ESHAPE, "batch_rows: n=%d rows=%d", n, rows);
   if (n == 0 && rows == 0) return MIKV_OK;
   if (!row_start || (n && !counts) || (rows && (!row_seq || !row_pos || !row_slot))) return fail(MIKV_EINVAL, "batch_rows: null pointer");
   a.seqs = seqs;

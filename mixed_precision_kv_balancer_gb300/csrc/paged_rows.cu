@@ -320,7 +320,7 @@ extern "C" int mikv_slot_append(const mikv_pages* pages, int layer, const mikv_r
   Pool p;
   if (int e = check_pages(pages, "slot_append", &p)) return e;
   if (layer < 0 || layer >= p.layers) return fail(MIKV_ESHAPE, "slot_append: layer=%d of %d", layer, p.layers);
-  if (rows < 0) return fail(MIKV_ESHAPE, "slot_append: rows=%d", rows);
+  if (rows < 0 || rows > 1 << 30) return fail(MIKV_ESHAPE, "slot_append: rows=%d", rows);   // (a CTA's numbers fit 32 bits)
   if (rows == 0) return MIKV_OK;
   if (int e = check_rows(k, "slot_append", "k")) return e;
   if (int e = check_rows(v, "slot_append", "v")) return e;

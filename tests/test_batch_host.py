@@ -138,3 +138,9 @@ def test_a_score_bounds_every_logit():
         top = ob.scores(q, codes[None], np.array([s]))[0]
         slack = 0.5 * np.abs(q).max() / 127 * (np.abs(k).sum(1).max() + 128 * s) + 1e-3
         assert top >= (k @ q[0]).max() - slack
+
+
+def test_rows_beyond_what_a_call_numbers_are_refused(lib):
+    most = (1 << 30) + 1
+    assert lib.mikv_batch_rows(_pages(), None, None, FAKE, 2, most, FAKE, FAKE, FAKE, FAKE, None) == ESHAPE
+    assert lib.mikv_slot_append(_pages(), 0, _rows(), _rows(st=0), most, FAKE, None) == ESHAPE
