@@ -200,3 +200,32 @@ def test_index_arithmetic_of_packed_rows(tmp_path):
                     "-o", str(tmp_path / "chunk_index")], check=True)
     res = subprocess.run([str(tmp_path / "chunk_index")], capture_output=True, text=True)
     assert res.returncode == 0, res.stdout + res.stderr
+
+
+BELOW = r"""
+#include "chunk_index.h"
+using namespace mikv;
+int main() {   // requests that are refused, however far below 0: they see nothing, and no sum leaves 32 bits
+  for (int start : {-1, -2, -(1 << 30), -0x7fffffff - 1})
+    for (int window : {0, 1, 1 << 30})
+      for (int rows : {1, 65, 1 << 20}) {
+        const Rows r = rows_of(rows, 100, true, start);
+        const RowTiles t = row_tiles_of(rows, 3);
+        if (r.keys != 0 || chunk_tiles<128>(t, r, window, 4, 0).tiles != 0 || r.off >= 0) return 1;
+      }
+  return 0;
+}
+"""
+
+
+def test_positions_far_below_zero(tmp_path):
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no g++")
+    src = tmp_path / "below.cpp"
+    src.write_text(BELOW)
+    inc = os.path.join(ROOT, "mixed_precision_kv_balancer_gb300", "csrc")
+    subprocess.run([gxx, "-O1", "-std=c++17", "-fsanitize=undefined,address", "-fno-sanitize-recover", "-I", inc, str(src),
+                    "-o", str(tmp_path / "below")], check=True)
+    res = subprocess.run([str(tmp_path / "below")], capture_output=True, text=True)
+    assert res.returncode == 0, res.stdout + res.stderr
