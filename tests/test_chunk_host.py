@@ -203,6 +203,7 @@ def test_index_arithmetic_of_packed_rows(tmp_path):
 
 
 BELOW = r"""
+#include <initializer_list>
 #include "chunk_index.h"
 using namespace mikv;
 int main() {   // requests that are refused, however far below 0: they see nothing, and no sum leaves 32 bits
