@@ -733,6 +733,7 @@ __global__ void __launch_bounds__(Warps<TYPE == MIKV_PAGES_INT8>::threads, 1)
     int used = 0, qs = 0;   // uses of this warp's buffer (INT8: tiles so far); items whose queries were loaded
     int ahead = 0;          // buffers of all items before, modulo the ring
     int cleared = 0;        // of this warp's tiles so far, those with rows to clear
+    int boxed = 0;          // and those whose boxes were asked for
     for (int n = 0;; ++n) {
       const Work* told = hear(n);
       if (!told) break;
@@ -821,6 +822,7 @@ __global__ void __launch_bounds__(Warps<TYPE == MIKV_PAGES_INT8>::threads, 1)
             const int z0 = min(max(a.qb.sinks - j0, 0), kCaRows), z1 = min(first - j0, kCaRows), z2 = min(keys - j0, kCaRows);
             const bool clear = bad != 0 || (values && (z0 < z1 || z2 < kCaRows));
             const uint32_t on = smem_u32(clear ? &bar.boxes[me] : &bar.full[me]);
+            ++boxed;
             if (lane == 0) tc::mbar_expect_tx(on, __popc(boxes) * a.box * kD * 2);
             __syncwarp();
             if (at[0] != kNoRow) tma_box(dst + lane * a.box * 128, values ? &vmap : &kmap, at[0], on);
@@ -865,6 +867,8 @@ __global__ void __launch_bounds__(Warps<TYPE == MIKV_PAGES_INT8>::threads, 1)
     for (int c = Q8 ? me >> 2 : me; c < kCaRing; c += Q8 ? 2 : kCaRing)   // INT8: tile u's keys or values were in buffer (2 u + kv) % 4
       wait(smem_u32(&bar.empty[c]), ((Q8 ? (used + 1 - (c >> 1)) / 2 : used) & 1) ^ 1);
     if (qs > 0) wait(smem_u32(&bar.qfree), (qs - 1) & 1);
+    // after a wait that gave up nobody may have waited for the last boxes: they land before the CTA ends
+    if (!wait.ok && boxed > 0) wait(smem_u32(&bar.full[me]), (boxed - 1) & 1);
   } else {
     more_registers<W::softmax_regs>();
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;   // the thread's TMEM lane is its row
