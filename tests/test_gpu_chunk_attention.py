@@ -280,3 +280,153 @@ def test_calls_on_another_stream():
     _lib.mikv_chunk_attention(q, cache, 0, batch.row_start, 0, 0, out, lse, stream=side)
     side.synchronize()
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+# --- the largest, and what goes on beside one another -------------------------------------
+
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("ps", [5, 8, 24])
+def test_single_tokens_and_chunks_in_one_part_under_windows(type, ps):
+    """Items of one query tile and of two behind one another in a CTA, whose ring and barriers they share."""
+    rng = np.random.RandomState(ps)
+    counts = rng.choice([1, 1, 2, 30, 140, 260], 60).tolist()
+    lens = [c + int(x) for c, x in zip(counts, rng.randint(0, 600, 60))]
+    cache = ph.make(lens, ps, 3, type)
+    for window, sinks in ((0, 0), (100, 7), (300, 150)):
+        check(cache, _rows(sum(counts), 6, type), starts(counts), window, sinks)
+
+
+def _plain(q, k, v, seen):
+    """[rows][H][D] in 64 bits on the GPU, of k, v [keys][H][D]."""
+    l = torch.einsum("qhd,khd->hqk", q.double(), k.double()) / 128 ** 0.5
+    l = l.masked_fill(~seen, -float("inf"))
+    w = l.softmax(-1)
+    return (torch.einsum("hqk,khd->qhd", w, v.double()).cpu().numpy(), torch.logsumexp(l, -1).T.cpu().numpy(),
+            torch.einsum("hqk,khd->qhd", w, v.double().abs()).cpu().numpy())
+
+
+@pytest.mark.parametrize("type,ps", [("fp16", 16), ("bf16", 1), ("int8", 16)])
+def test_a_pool_whose_offsets_pass_32_bits(type, ps):
+    """Slots past 2^32 bytes of the keys' pool: rows appended there, their bounds, and both attentions."""
+    slots = (1 << 25 if type == "int8" else 1 << 24) + 64 * ps
+    n_pages, len0 = slots // ps, 300
+    cache = PagedCache(1, n_pages, ps, 1, 128, 2, -(-len0 // ps) + 4, type=type)
+    pages = -(-len0 // ps)
+    last = torch.arange(n_pages - pages, n_pages, dtype=torch.int32, device=ph.DEV).flip(0)
+    if ps == 1:                                      # the first 64 alone lie past the limit
+        last[64:] -= 1 << 20
+        last = last.roll(100)
+    cache.table[1, :pages] = last
+    cache.refs[last.long()] = 1
+    cache.lens[1] = len0
+    k, v, q = (ph.normal((len0, h, 128), 60 + i, ph.DTYPE[type]).to(ph.DEV) for i, h in ((0, 1), (1, 1), (2, 4)))
+    batch = cache.rows(ints([len0]), len0, seqs=ints([1]))
+    cache.put(0, k, v, batch)
+    buf = cache.bounds_buffers()
+    cache.renew(0, batch, buf)
+    if type == "int8":
+        k, v = (ph.values(*ph.quantize(t)) for t in (k, v))
+    seen = torch.ones(len0, len0, dtype=torch.bool, device=ph.DEV).tril()
+    want, wl, mag = _plain(q, k.expand(-1, 4, -1), v.expand(-1, 4, -1), seen)
+    out, lse = cache.attend_rows(0, q, batch)
+    ph.close(out, want, mag, ph.HALF_STEP[type], weights=ph.HALF_STEP[type])
+    ph.close_lse(lse, wl)
+    low, scale = ob.bounds(k[:ps, 0].float().cpu().numpy())
+    at = int(last[0])
+    assert float(buf[1][0, at, 0]) == scale and (buf[0][0, at, 0].cpu().numpy() == low).all()
+    sel, n_sel = cache.pick(0, q, buf, pages, batch=batch)
+    out, lse = cache.attend_blocks(0, q, sel, n_sel, batch)
+    ph.close(out, want, mag, ph.HALF_STEP[type], weights=2.0 ** -16)
+    ph.close_lse(lse, wl)
+    assert _lib.mikv_wait_status() == 0
+
+
+@pytest.mark.parametrize("type", ["bf16", "int8"])
+def test_the_most_requests_and_rows(type):
+    """4096 requests of 256 rows each, 2^20 in all; then of single tokens."""
+    n, c, H = 4096, 256, 2
+    cache = PagedCache(1, n * c // 32, 32, 1, 128, n, c // 32, type=type)
+    cache.table[:] = torch.randperm(n * c // 32, device=ph.DEV).int().view(n, c // 32)
+    cache.refs.fill_(1)
+    cache.lens.fill_(c)
+    g = torch.Generator(device=ph.DEV).manual_seed(1)
+    k, v, q = (torch.randn(n * c, h, 128, generator=g, device=ph.DEV).to(ph.DTYPE[type]) for h in (1, 1, H))
+    counts = torch.full((n,), c, dtype=torch.int32, device=ph.DEV)
+    batch = cache.rows(counts, n * c)
+    cache.put(0, k, v, batch)
+    out, lse = cache.attend_rows(0, q, batch, out=torch.full_like(q, float("nan")), lse=torch.full((n * c, H), float("nan"), device=ph.DEV))
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    if type == "int8":
+        k, v = (ph.values(*ph.quantize(t)) for t in (k, v))
+    seen = torch.ones(c, c, dtype=torch.bool, device=ph.DEV).tril()
+    for i in (0, 1, 777, 2048, 4094, 4095):
+        at = slice(i * c, i * c + c)
+        want, wl, mag = _plain(q[at], k[at].expand(-1, H, -1), v[at].expand(-1, H, -1), seen)
+        ph.close(out[at], want, mag, ph.HALF_STEP[type], weights=ph.HALF_STEP[type])
+        ph.close_lse(lse[at], wl)
+    last = torch.arange(c - 1, n * c, c, device=ph.DEV)
+    one, ones = cache.attend_rows(0, q[last], cache.rows(torch.ones_like(counts), n))
+    other, others = cache.attend(0, q[last])
+    # each is off by half a step of itself and, at most, the largest value times its weights' and fp32's share
+    half, a, b, top = ph.HALF_STEP[type], one.double(), other.double(), float(v.abs().max())
+    slack = top * (half + ph.FP32)
+    assert ((a - b).abs() <= 2 * half * (torch.maximum(a.abs(), b.abs()) + slack) + 2 * slack).all()
+    assert ((ones - others).abs() <= 4 * ph.FP32 + 2.0 ** -21 * others.abs()).all()
+    assert _lib.mikv_wait_status() == 0
+
+
+@pytest.mark.parametrize("type", TYPES)
+def test_two_calls_at_once(type):
+    """On two streams, with a workspace each."""
+    caches = [ph.make([900, 300, 5000], 16, 2, type, seed=s) for s in (1, 2)]
+    qs = [_rows(420, 8, type, seed=s) for s in (3, 4)]
+    counts = ints([300, 119, 1])
+    batches = [c.rows(counts, 420) for c in caches]
+    bufs = [c.bounds_buffers() for c in caches]
+    for c, buf in zip(caches, bufs):
+        lens = c.lens.clone()
+        c.renew(0, c.rows(lens, int(lens.sum())), buf)
+
+    def run(i):
+        out = caches[i].attend_rows(0, qs[i], batches[i])
+        sel, n_sel = caches[i].pick(0, qs[i], bufs[i], 5, batch=batches[i])
+        return (*out, sel, n_sel, *caches[i].attend_blocks(0, qs[i], sel, n_sel, batches[i]))
+
+    want = [run(0), run(1)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(run(i))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            for a, b in zip(g, want[i]):
+                assert torch.equal(a, b)
+    assert _lib.mikv_wait_status() == 0
+
+
+@pytest.mark.parametrize("type", TYPES)
+def test_replays_with_a_workspace_that_others_used(type):
+    """Two captured calls of different shapes share a workspace, which holds NaN at first."""
+    cache = ph.make([2000, 700, 60], 16, 2, type)
+    q = _rows(500, 8, type)
+    shapes = ([400, 99, 1], [1, 1, 1])
+    ws = torch.full((cache.chunk_workspace(3, 500, 8).numel(),), 255, dtype=torch.uint8, device=ph.DEV)
+    outs = [(torch.zeros_like(q), torch.zeros(500, 8, device=ph.DEV)) for _ in shapes]
+    batches = [cache.rows(ints(c), 500) for c in shapes]
+    want = [tuple(t.clone() for t in cache.attend_rows(0, q, b, 900, 20)) for b in batches]
+    graphs = []
+    for b, o in zip(batches, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            cache.attend_rows(0, q, b, 900, 20, out=o[0], lse=o[1], ws=ws)
+        graphs.append(g)
+    for _ in range(3):
+        for g, o, w in zip(graphs, outs, want):
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
