@@ -665,13 +665,13 @@ int mikv_set_attention_events(void* begin, void* end);
  * Wait status of the tensor-core kernels (no counterpart in the papers; a failure report).
  * The tcgen05 kernels (K3's two prefill score passes in mikv_score_update(MIKV_PREFILL),
  * K6's V.W_O norms in mikv_select(MIKV_CRITICALKV) with w_o, K9 in
- * mikv_output_perturbation, and mikv_window_attention) hand tiles between a TMA/MMA thread and their consumer warps
- * through mbarriers, and every wait there gives up after ~4 million polls instead of
+ * mikv_output_perturbation, mikv_window_attention and mikv_chunk_attention) hand tiles between a TMA/MMA thread and
+ * their consumer warps through mbarriers, and every wait there gives up after ~4 million polls instead of
  * spinning for ever.  No wait is expected to run out; if one does, the thread that gave up
  * issues no further copy or MMA, its later waits poll only ~1000 times each (so a stuck
  * pipeline still ends in a bounded time, and what was issued before has that long to land),
  * the kernel writes NaN into the outputs of the affected CTA (prefill scores and -lse rows,
- * V.W_O norms, perturbation and y partial sums, windowed attention's rows under way; rows that
+ * V.W_O norms, perturbation and y partial sums, the rows of windowed and packed rows' attention under way; rows that
  * its CTA had taken over and not begun are left as they were, or joined from what the workspace held) and sets a bit in a device-side
  * status word.
  * The call that launched it has already returned MIKV_OK (launches are asynchronous).
