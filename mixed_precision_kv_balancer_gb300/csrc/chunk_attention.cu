@@ -840,7 +840,14 @@ __global__ void __launch_bounds__(Warps<TYPE == MIKV_PAGES_INT8>::threads, 1)
             land(smem_u32(&bar.full[me]));
           };
           look(begin + (c >> 1));
-          for (bool one = true; c < count || one; c += kCaRing) {
+          // The item's queries, behind this warp's first buffer of it; before, where that one (the second values') is free only
+          // when the last item's products are all done, and its scores' are done before.
+          bool one = true;
+          if (c == kCaRing - 1) {
+            queries();
+            one = false;
+          }
+          for (; c < count || one; c += kCaRing) {
             if (c < count) {
               wait(smem_u32(&bar.empty[me]), (used & 1) ^ 1);
               ++used;
@@ -855,7 +862,7 @@ __global__ void __launch_bounds__(Warps<TYPE == MIKV_PAGES_INT8>::threads, 1)
                 land(smem_u32(&bar.full[me]));
               }
             }
-            if (one) queries();   // behind the item's first buffers
+            if (one) queries();
             one = false;
           }
           ahead = (ahead + count) & (kCaRing - 1);
