@@ -108,8 +108,9 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xfffffff
 // Each half of the weights is announced (`ready`, one arrival a warp) as soon as it is written.
 // `last`: the last key that the row may see, its position p or less.  Args: qb.window, qb.sinks and scale.
 // PARTS 2: the scores are the sum of two products, the second COLS columns behind the first.
+// W: the weights' factor, and how far the reference may lag.
 // `settle` returns once all products into the accumulator that were issued are done; it is called before a rescaling.
-template <bool BF, int COLS, int PARTS, class Args, class Settle>
+template <bool BF, int COLS, int PARTS, class W = Weights<BF>, class Args, class Settle>
 __device__ __forceinline__ void softmax_tile(const Args& a, uint32_t ts, uint32_t to, bool whole, int p, int last, int j0, Row& r,
                                              const uint32_t (&ready)[2], const Settle& settle) {
   float s[COLS];
@@ -149,7 +150,7 @@ __device__ __forceinline__ void softmax_tile(const Args& a, uint32_t ts, uint32_
 #pragma unroll
     for (int u = 0; u < 4; ++u) mx[u] = fmaxf(fmaxf(mx[u], s[c + u]), c + 4 + u < COLS ? s[c + 4 + u] : -INFINITY);
   const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-  const bool grew = (top - r.m) * a.scale > Weights<BF>::grow;   // from -inf too; never by NaN
+  const bool grew = (top - r.m) * a.scale > W::grow;   // from -inf too; never by NaN
   if (__any_sync(0xffffffffu, grew)) {
     // a row whose own maximum has not outgrown its reference keeps it: its result does not hang on
     // the other rows of the warp, which may be rows that do not count
@@ -172,7 +173,7 @@ __device__ __forceinline__ void softmax_tile(const Args& a, uint32_t ts, uint32_
     }
   }
   r.first = false;
-  const float neg = r.m == -INFINITY ? 0.f : Weights<BF>::shift - r.m * a.scale;
+  const float neg = r.m == -INFINITY ? 0.f : W::shift - r.m * a.scale;
   float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
   for (int c = 0; c < COLS; c += 32) {

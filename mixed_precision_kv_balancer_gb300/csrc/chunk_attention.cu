@@ -61,6 +61,13 @@ constexpr int kMaxChunkRows = 1 << 20;      // of a call: the sums of its blocks
 template <int TYPE>
 constexpr int kKeys = TYPE == MIKV_PAGES_INT8 ? 64 : kCaRows;   // of a tile
 
+// fp16 weights reach 2^15.9, and may grow by 2^7.9 before the reference follows: every rescaling of the sums holds up a
+// warp's 32 rows (with 2^13 and 2^2: four chunks of 512 behind 8192, 117 us instead of 109; chunk_window_int8's 158 instead of
+// 146).  A weight below 2^-22 of the largest is a subnormal number then, which the products keep, in steps of 2^-32.
+template <bool BF>
+struct RowWeights {
+  static constexpr float shift = BF ? 0.f : 8.f, grow = BF ? 8.f : 7.9375f;
+};
 struct Mask {
   int32_t window, sinks;
 };
@@ -911,9 +918,9 @@ __global__ void __launch_bounds__(Warps<TYPE == MIKV_PAGES_INT8>::threads, 1)
             pars ^= 1u << which;
             tc::fence_after_sync();
             if (few)
-              softmax_tile<BF, kCaNarrow, 1>(a, ts, to, false, p, last, j0, r, ready, settle);
+              softmax_tile<BF, kCaNarrow, 1, RowWeights<BF>>(a, ts, to, false, p, last, j0, r, ready, settle);
             else
-              softmax_tile<BF, KT, Q8 ? 2 : 1>(a, ts, to, whole, p, last, j0, r, ready, settle);
+              softmax_tile<BF, KT, Q8 ? 2 : 1, RowWeights<BF>>(a, ts, to, whole, p, last, j0, r, ready, settle);
             done += kOne;
           }
         };
@@ -966,7 +973,7 @@ __global__ void __launch_bounds__(Warps<TYPE == MIKV_PAGES_INT8>::threads, 1)
         if (part && write) {
           *part_ml(a, slot, t, row) = make_float2(r.m * a.scale, wait.ok ? r.l : inv);
         } else if (write && a.lse) {
-          const float v = r.l == 0.f ? -INFINITY : (r.m * a.scale + (log2f(r.l) - Weights<BF>::shift)) * 0.6931471805599453f;
+          const float v = r.l == 0.f ? -INFINITY : (r.m * a.scale + (log2f(r.l) - RowWeights<BF>::shift)) * 0.6931471805599453f;
           a.lse[static_cast<int64_t>(at) * a.Hq + head] = wait.ok ? v : inv;
         }
         tc::fence_before_sync();   // the sums are read before the next item's products overwrite them
@@ -1055,7 +1062,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkArg
       make_uint4(pack2<BF>(o[0] * inv, o[1] * inv), pack2<BF>(o[2] * inv, o[3] * inv), pack2<BF>(o[4] * inv, o[5] * inv),
                  pack2<BF>(o[6] * inv, o[7] * inv));
   if (ch == 0 && a.lse)
-    a.lse[static_cast<int64_t>(at) * a.Hq + head] = l == 0.f ? -INFINITY : (m + (log2f(l) - Weights<BF>::shift)) * 0.6931471805599453f;
+    a.lse[static_cast<int64_t>(at) * a.Hq + head] = l == 0.f ? -INFINITY : (m + (log2f(l) - RowWeights<BF>::shift)) * 0.6931471805599453f;
 }
 
 int tile_rows_of(int rows, int rep) { return static_cast<int>(std::min<int64_t>(kCaRows, static_cast<int64_t>(rows) * rep)); }

@@ -430,3 +430,28 @@ def test_replays_with_a_workspace_that_others_used(type):
             g.replay()
             torch.cuda.synchronize()
             assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
+
+
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("rows", [1, 200])
+@pytest.mark.parametrize("depth", [15, 21, 25])
+def test_many_small_weights_beside_a_large_one(type, rows, depth):
+    """One key of weight 1 whose value is 0, and 40000 of 2^-depth whose values are 1: fp16 weights that small are
+    subnormal numbers, and all of them count."""
+    n = 40000 + rows
+    cache = PagedCache(1, -(-n // 64), 64, 1, 128, 1, -(-n // 64), type=type)
+    cache.table[0] = torch.randperm(cache.refs.numel(), device=ph.DEV).int()
+    cache.refs.fill_(1)
+    cache.lens.fill_(n)
+    k, v = torch.zeros(n, 1, 128, device=ph.DEV), torch.ones(n, 1, 128, device=ph.DEV)
+    k[..., 0] = -depth * float(np.log(2.0)) * 128 ** 0.5       # against queries that are 1 there and 0 elsewhere
+    k[7] = 0
+    v[7] = 0
+    q = torch.zeros(rows, 4, 128, device=ph.DEV)
+    q[..., 0] = 1
+    k, v, q = (t.to(ph.DTYPE[type]) for t in (k, v, q))
+    cache.put(0, k, v, cache.rows(ints([n]), n))
+    check(cache, q, [0, rows])
+    out, _ = cache.attend_rows(0, q, cache.rows(ints([rows]), rows))
+    small = 30000 * 2.0 ** -depth                    # of 40000: the keys' rounding moves a weight by 2^-8 * 17.4 at most
+    assert (out >= small / (1 + small)).all()
