@@ -13,7 +13,8 @@
 //   O_t += P_t V_i      tcgen05, P from TMEM, V as it lies (rows are the contraction)
 // Lengths are known on the device alone and differ from request to request, so that all key tiles of a
 // call form one line, of which each CTA takes an equal part; a CTA finds its part in sums over the
-// requests, which all of its threads make before it begins.  Items that are cut are joined by a second kernel.
+// requests, which all of its threads make before it begins.  Items that are cut are joined by the CTA that begins them,
+// where the rest is there by then, or by a second kernel.
 //
 // Four warps bring keys and values from the pages to a ring of four 32 KB buffers (128-byte swizzle), each
 // to a buffer of its own: by TMA where the pages' size is a multiple of 8 rows, a page or the largest power of
@@ -26,6 +27,8 @@
 // two parts of each 64 rows apart in its buffer, so that all copies and products are as above: S_t has the two parts'
 // scores side by side, and P_t meets both parts of the values.
 #include <algorithm>
+#include <atomic>
+#include <random>
 #include <type_traits>
 
 #include "attention_tile.cuh"
@@ -83,6 +86,7 @@ struct ChunkArgs {
   int box;                     // rows of a TMA box: a power of two from 8 on that divides a page and a tile; 0: no TMA
   bool wide_out;               // rows of out begin at multiples of 32 bytes
   float scale;                 // log2(e) / sqrt(D)
+  uint64_t tag;                // of this call, see part_ready
 };
 
 struct CaBars {
@@ -118,8 +122,9 @@ struct Cut {
   int last;          // the CTA that ends it; -1: none is cut
   int before;        // whether that CTA's part of the line has items before
   int row0, rows, q0[2], head[2], heads[2], tb;   // per tile: first row of the request, first head of q, heads (0: no tile)
-  int pad;
+  uint8_t done[2][4];   // 32 rows of a tile that the CTA has joined itself
 };
+static_assert(kNumSMs * sizeof(Cut) % sizeof(uint64_t) == 0, "tags lie behind");
 
 // What one CTA works on, in shared memory: written by the walking warp, read by the others.
 struct Work {
@@ -131,6 +136,8 @@ struct Work {
   int ns;                 // key tiles that hold sinks, of either part of the list
   int nt;                 // query tiles; -1: there is no further item
   int whole;              // all of the item
+  int two;                // the next CTA has the rest of it
+  int rest;               // the end of an item that a CTA before begins, with more items behind
   int row0, rows, keys, tb, seq;   // of the request
   template <int KT>
   __device__ __forceinline__ int j0(int i) const { return (i < ts ? i : tw0 + i - ts) * KT; }
@@ -159,6 +166,7 @@ __device__ __forceinline__ Work work_of(const ChunkArgs& a, const Request& q, in
   w.begin = min(t0, k.tiles);
   w.end = min(t1, k.tiles);
   w.whole = t0 == 0 && t1 >= k.tiles;
+  w.two = w.rest = 0;
   w.row0 = q.row0;
   w.rows = q.r.rows;
   w.keys = q.r.keys;
@@ -192,6 +200,7 @@ struct Walk {
   int t0, t1;            // its key tiles of this part
   int left;              // items of the block behind it
   int64_t to_go;         // places of this CTA's part from the item's begin on
+  bool two;              // the item that this CTA begins and does not end is ended by the next one
   Request q;
   bool idle;
 
@@ -208,7 +217,12 @@ struct Walk {
     q.r.off = uniform(q.r.off);
     q.r.keys = uniform(q.r.keys);
   }
-  __device__ __forceinline__ Work work(const ChunkArgs& a) const { return work_of<KT>(a, q, blk, item, t0, t1); }
+  __device__ __forceinline__ Work work(const ChunkArgs& a) const {
+    Work w = work_of<KT>(a, q, blk, item, t0, t1);
+    w.two = two && t0 == 0 && !w.whole;
+    w.rest = t0 > 0 && to_go > places;
+    return w;
+  }
   __device__ __forceinline__ void set_end() { t1 = uniform(chunk_tile(static_cast<int>(min(to_go, static_cast<int64_t>(places))), weight)); }
   // On to the next item, by the whole warp; false where there is none.
   __device__ __forceinline__ bool next(const ChunkArgs& a, bool ok) {
@@ -247,6 +261,30 @@ __device__ __forceinline__ float2* part_ml(const ChunkArgs& a, int slot, int t, 
 }
 __device__ __forceinline__ Cut* part_cut(const ChunkArgs& a, int c) {
   return reinterpret_cast<Cut*>(a.part + static_cast<int64_t>(a.ctas) * 4 * a.tile_rows * (kD + 2)) + c;
+}
+
+// The tag of the call once the 32 rows that the warp holds of its first item's tile t lie in its slot; the joining kernel
+// clears it.  (A tag is one of 2^64 that the host draws anew for every call, so that what a workspace held before, or
+// what a call left that was captured with another tag, does not pass for it.)
+__device__ __forceinline__ uint64_t* part_ready(const ChunkArgs& a, int c, int t, int warp) {
+  return reinterpret_cast<uint64_t*>(part_cut(a, a.ctas)) + (c * 2 + t) * 4 + warp;
+}
+// Joins parts one after the other: the factors of what is there and of what comes.  Written out in single operations, so that
+// it is the same to the bit wherever a part is joined.
+struct Joined {
+  float m = -INFINITY, l = 0.f;
+  __device__ __forceinline__ float2 add(float2 x) {
+    const float mn = fmaxf(m, x.x), ref = mn == -INFINITY ? 0.f : mn;
+    const float f = ex2(m - ref), fx = ex2(x.x - ref);
+    l = __fmaf_rn(x.y, fx, __fmul_rn(l, f));
+    m = mn;
+    return make_float2(f, fx);
+  }
+};
+__device__ __forceinline__ float joined(float o, float p, float2 f) { return __fadd_rn(__fmaf_rn(p, f.y, __fmul_rn(o, f.x)), 0.f); }   // (never -0)
+template <bool BF>
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + (log2f(l) - RowWeights<BF>::shift)) * 0.6931471805599453f;
 }
 
 // Inclusive sum over the block; `sums` holds a value a warp.
@@ -371,6 +409,7 @@ __device__ __forceinline__ Walk<KT> find_part(const ChunkArgs& a, uint8_t* scrat
       }
     }
     w.idle = x >= y;
+    w.two = cut.last == c + 1;
     w.to_go = y - begin;
     w.set_end();
   }
@@ -935,9 +974,32 @@ __global__ void __launch_bounds__(Warps<TYPE == MIKV_PAGES_INT8>::threads, 1)
         }
         tc::fence_after_sync();
         const int sub = row / w.tb, q = w.q0[t] + row - sub * w.tb, head = w.head[t] + sub;   // the row's query and head
-        const bool write = sub < w.heads[t] && q < w.rows, part = !w.whole;
+        const bool write = sub < w.heads[t] && q < w.rows;
+        // An item of two parts is joined here if the next CTA, which begins with its end, is done with it: most are, as this
+        // CTA ends with the item's begin.  (All left to the second kernel: three chunks of 1500 rows of 20 heads under a window
+        // of 2048, 88 us instead of 84; chunk_window_int8 145 instead of 141.)  Whoever has that item alone does not look: both end at once.
+        bool join = false;
+        if (w.two && n > 0 && __all_sync(0xffffffffu, wait.ok)) {
+          uint64_t tag;
+          asm volatile("ld.acquire.gpu.global.b64 %0, [%1];\n" : "=l"(tag) : "l"(part_ready(a, blockIdx.x + 1, t, warp & 3)) : "memory");
+          join = __all_sync(0xffffffffu, tag == a.tag);
+        }
+        const bool part = !w.whole && !join;
         const int slot = 2 * blockIdx.x + (n > 0), at = w.row0 + q;
-        float inv = part ? 1.f : r.l == 0.f ? 0.f : 1.f / r.l;
+        Joined sum;
+        float2 own = make_float2(1.f, 1.f), other = make_float2(1.f, 0.f);
+        float rest = 0.f;   // the other part's sum of weights
+        if (join) {
+          own = sum.add(make_float2(r.m * a.scale, r.l));
+          if (write) {
+            const float2 x = __ldcg(part_ml(a, 2 * (blockIdx.x + 1), t, row));
+            other = sum.add(x);
+            rest = x.y;
+          }
+          if (lane == 0) part_cut(a, blockIdx.x)->done[t][warp & 3] = 1;
+        }
+        const float l = join ? sum.l : r.l;
+        float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
         if (!wait.ok) inv = __int_as_float(0x7fffffff);
         uint8_t* dst = a.out.row(0, head, at);
 #pragma unroll 1
@@ -949,6 +1011,20 @@ __global__ void __launch_bounds__(Warps<TYPE == MIKV_PAGES_INT8>::threads, 1)
           } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
+          if (join && write) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              float4 p[2] = {};
+              if (rest != 0.f) {
+                const float4* from = reinterpret_cast<const float4*>(part_sums(a, 2 * (blockIdx.x + 1), t, row, c + e));
+                p[0] = __ldcg(from);
+                p[1] = __ldcg(from + 1);
+              }
+              const float x[8] = {p[0].x, p[0].y, p[0].z, p[0].w, p[1].x, p[1].y, p[1].z, p[1].w};
+#pragma unroll
+              for (int k = 0; k < 8; ++k) o[e + k] = joined(joined(0.f, r.l == 0.f ? 0.f : o[e + k], own), x[k], other);
+            }
           }
           if (write) {
             uint32_t u[32];
@@ -973,8 +1049,13 @@ __global__ void __launch_bounds__(Warps<TYPE == MIKV_PAGES_INT8>::threads, 1)
         if (part && write) {
           *part_ml(a, slot, t, row) = make_float2(r.m * a.scale, wait.ok ? r.l : inv);
         } else if (write && a.lse) {
-          const float v = r.l == 0.f ? -INFINITY : (r.m * a.scale + (log2f(r.l) - RowWeights<BF>::shift)) * 0.6931471805599453f;
+          const float v = join ? lse_of<BF>(sum.m, sum.l) : lse_of<BF>(r.m * a.scale, r.l);
           a.lse[static_cast<int64_t>(at) * a.Hq + head] = wait.ok ? v : inv;
+        }
+        if (w.rest) {
+          __syncwarp();   // (the release covers what the other lanes have written before)
+          if (lane == 0)
+            asm volatile("st.release.gpu.global.b64 [%0], %1;\n" ::"l"(part_ready(a, blockIdx.x, t, warp & 3)), "l"(a.tag) : "memory");
         }
         tc::fence_before_sync();   // the sums are read before the next item's products overwrite them
       }
@@ -998,20 +1079,20 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkArg
   __shared__ float2 s_ml[GROUPS > 1 ? GROUPS - 1 : 1][kThreads];
   const int tid = threadIdx.x % kThreads, group = threadIdx.x / kThreads, c0 = blockIdx.y;
   pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x < 8) *part_ready(a, c0, threadIdx.x >> 2, threadIdx.x & 3) = 0;
   const Cut cut = *part_cut(a, c0);
   const int c1 = cut.last;
   if (c1 < 0) return;
   const int ch = tid / kRows * 8, i = blockIdx.x * kRows + tid % kRows, t = i >= a.tile_rows, row = i - t * a.tile_rows;
   const int sub = row / cut.tb, q = (t ? cut.q0[1] : cut.q0[0]) + row - sub * cut.tb;
-  const bool live = i < 2 * a.tile_rows && sub < (t ? cut.heads[1] : cut.heads[0]) && q < cut.rows;
-  float m = -INFINITY, l = 0.f, o[8] = {};
+  const bool live = i < 2 * a.tile_rows && sub < (t ? cut.heads[1] : cut.heads[0]) && q < cut.rows &&
+                    !part_cut(a, c0)->done[t & 1][row >> 5 & 3];
+  Joined sum;
+  float o[8] = {};
   const auto add = [&](float2 x, const float (&p)[8]) {
-    const float mn = fmaxf(m, x.x), ref = mn == -INFINITY ? 0.f : mn;
-    const float f = ex2(m - ref), fx = ex2(x.x - ref);
-    l = l * f + x.y * fx;
+    const float2 f = sum.add(x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = o[e] * f + p[e] * fx;
-    m = mn;
+    for (int e = 0; e < 8; ++e) o[e] = joined(o[e], p[e], f);
   };
   if (live) {
     for (int p0 = c0 + group; p0 <= c1; p0 += BATCH * GROUPS) {
@@ -1043,7 +1124,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkArg
     if (group > 0) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) s_o[group - 1][e][tid] = o[e];
-      s_ml[group - 1][tid] = make_float2(m, l);
+      s_ml[group - 1][tid] = make_float2(sum.m, sum.l);
     }
     __syncthreads();
     if (group > 0) return;
@@ -1057,17 +1138,24 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkArg
   }
   if (!live) return;
   const int head = (t ? cut.head[1] : cut.head[0]) + sub, at = cut.row0 + q;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
   *reinterpret_cast<uint4*>(a.out.row(0, head, at) + ch * 2) =
       make_uint4(pack2<BF>(o[0] * inv, o[1] * inv), pack2<BF>(o[2] * inv, o[3] * inv), pack2<BF>(o[4] * inv, o[5] * inv),
                  pack2<BF>(o[6] * inv, o[7] * inv));
   if (ch == 0 && a.lse)
-    a.lse[static_cast<int64_t>(at) * a.Hq + head] = l == 0.f ? -INFINITY : (m + (log2f(l) - RowWeights<BF>::shift)) * 0.6931471805599453f;
+    a.lse[static_cast<int64_t>(at) * a.Hq + head] = lse_of<BF>(sum.m, sum.l);
 }
 
 int tile_rows_of(int rows, int rep) { return static_cast<int>(std::min<int64_t>(kCaRows, static_cast<int64_t>(rows) * rep)); }
 size_t part_bytes(int rows, int rep) {
-  return static_cast<size_t>(kNumSMs) * (static_cast<size_t>(4) * tile_rows_of(rows, rep) * (kD + 2) * 4 + sizeof(Cut));
+  return static_cast<size_t>(kNumSMs) * (static_cast<size_t>(4) * tile_rows_of(rows, rep) * (kD + 2) * 4 + sizeof(Cut) + 8 * sizeof(uint64_t));
+}
+uint64_t new_tag() {
+  static std::atomic<uint64_t> calls{std::random_device{}() * 0x9E3779B97F4A7C15ull};
+  uint64_t x = calls += 0x9E3779B97F4A7C15ull;   // splitmix64 (Steele, Lea and Flood), a permutation of the counter
+  x = (x ^ x >> 30) * 0xBF58476D1CE4E5B9ull;
+  x = (x ^ x >> 27) * 0x94D049BB133111EBull;
+  return x ^ x >> 31;
 }
 bool sizes_ok(const mikv_pages* p, int n, int rows, int Hq) {
   return n >= 0 && n <= kMaxRequests && rows >= 0 && rows <= kMaxChunkRows && Hq >= 1 && Hq % p->Hkv == 0 && Hq / p->Hkv <= 1024 &&
@@ -1165,6 +1253,7 @@ extern "C" int mikv_chunk_attention(const mikv_rows* q, const mikv_pages* pages,
   a.Hq = Hq;
   a.ctas = kNumSMs;
   a.tile_rows = tile_rows_of(rows, a.rep);
+  a.tag = new_tag();
   a.qb.window = window > kMaxPos ? 0 : window;   // one that reaches every key is none
   a.qb.sinks = std::min(sinks, kMaxPos);
   a.box = std::min(kCaRows, pages->page_size & -pages->page_size);

@@ -455,3 +455,40 @@ def test_many_small_weights_beside_a_large_one(type, rows, depth):
     out, _ = cache.attend_rows(0, q, cache.rows(ints([rows]), rows))
     small = 30000 * 2.0 ** -depth                    # of 40000: the keys' rounding moves a weight by 2^-8 * 17.4 at most
     assert (out >= small / (1 + small)).all()
+
+
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 3)])
+def test_parts_of_many_items(type, window, sinks):
+    """Several items a CTA, those at its ends cut: joined in place or by the second kernel, the bits are the same."""
+    H, c, past = 32, 1500, [1300, 0]
+    cache = PagedCache(1, 200, 32, 8, 128, 2, 100, type=type)
+    total = ints([p + c for p in past])
+    cache.reserve(total)
+    n = int(total.sum())
+    k, v = (ph.normal((n, 8, 128), s, ph.DTYPE[type]).to(ph.DEV) for s in (1, 2))
+    cache.put(0, k, v, cache.rows(total, n))
+    q = ph.normal((2 * c, H, 128), 3, ph.DTYPE[type]).to(ph.DEV)
+    batch = cache.rows(ints([c, c]), 2 * c)
+    out, lse = cache.attend_rows(0, q, batch, window, sinks)
+    if type == "int8":
+        k, v = (ph.values(*ph.quantize(t)) for t in (k, v))
+    at = 0
+    for i, p in enumerate(past):
+        pos, j = p + torch.arange(c, device=ph.DEV)[:, None], torch.arange(p + c, device=ph.DEV)[None]
+        seen = (j <= pos) & ((j > pos - window) | (j < sinks)) if window else j <= pos
+        rows, keys = slice(i * c, i * c + c), slice(at, at + p + c)
+        for h in range(0, H, 8):
+            kv = [t[keys, h // 4:h // 4 + 2].repeat_interleave(4, 1) for t in (k, v)]
+            want, wl, mag = _plain(q[rows, h:h + 8], *kv, seen)
+            ph.close(out[rows, h:h + 8], want, mag, ph.HALF_STEP[type], weights=ph.HALF_STEP[type])
+            ph.close_lse(lse[rows, h:h + 8], wl)
+        at += p + c
+    side, beside = torch.cuda.Stream(), torch.randn(4096, 4096, device=ph.DEV)
+    ws = cache.chunk_workspace(2, 2 * c, H)
+    for i in range(12):
+        with torch.cuda.stream(side):                # something else on the SMs, so that CTAs begin and end at other times
+            beside = beside @ beside * 1e-3 if i % 3 else beside
+        again = cache.attend_rows(0, q, batch, window, sinks, ws=ws)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    assert _lib.mikv_wait_status() == 0
