@@ -28,7 +28,7 @@
 // scores side by side, and P_t meets both parts of the values.
 #include <algorithm>
 #include <atomic>
-#include <random>
+#include <chrono>
 #include <type_traits>
 
 #include "attention_tile.cuh"
@@ -1151,7 +1151,7 @@ size_t part_bytes(int rows, int rep) {
   return static_cast<size_t>(kNumSMs) * (static_cast<size_t>(4) * tile_rows_of(rows, rep) * (kD + 2) * 4 + sizeof(Cut) + 8 * sizeof(uint64_t));
 }
 uint64_t new_tag() {
-  static std::atomic<uint64_t> calls{std::random_device{}() * 0x9E3779B97F4A7C15ull};
+  static std::atomic<uint64_t> calls{static_cast<uint64_t>(std::chrono::system_clock::now().time_since_epoch().count())};
   uint64_t x = calls += 0x9E3779B97F4A7C15ull;   // splitmix64 (Steele, Lea and Flood), a permutation of the counter
   x = (x ^ x >> 30) * 0xBF58476D1CE4E5B9ull;
   x = (x ^ x >> 27) * 0x94D049BB133111EBull;
