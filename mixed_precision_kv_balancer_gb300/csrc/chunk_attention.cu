@@ -112,7 +112,8 @@ __device__ __forceinline__ Request request_of(const ChunkArgs& a, int i) {
   const int rows = max(request_row(a, i + 1) - q.row0, 0);
   q.seq = a.seqs ? a.seqs[i] : i;
   const bool there = static_cast<uint32_t>(q.seq) < static_cast<uint32_t>(a.p.max_seqs);
-  q.r = rows_of(rows, there && rows > 0 ? a.p.len_of(q.seq) : 0, a.start != nullptr, a.start ? a.start[i] : 0);
+  const int held = there ? a.p.len_of(q.seq) : 0;   // (asked for beside the rows that tell whether it counts)
+  q.r = rows_of(rows, rows > 0 ? held : 0, a.start != nullptr, a.start ? a.start[i] : 0);
   q.t = row_tiles_of(rows, a.rep);
   return q;
 }
