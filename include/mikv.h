@@ -558,7 +558,8 @@ size_t mikv_window_attention_workspace_bytes(int B, int Hq, int Hkv, int Tq, int
  *   row_slot                  the slot of the pool, page * page_size + position % page_size; -1 also at or
  *                             past the sequence's length and on a page outside the pool (reported,
  *                             mikv_wait_status bit 64)
- * Rows of requests that were refused keep their places: a batch is laid out from its counts alone.
+ * Rows of requests that were refused keep their places: a batch is laid out from its counts alone.  What
+ * lies past `rows` is cut off: with start NULL the rows that are left of a request are its sequence's last ones.
  * n at most 4096, rows at most 2^30; n_pages * page_size < 2^31; n == 0 with rows == 0 does nothing.
  * Errors: EINVAL (null), ESHAPE, and the cache's (EALIGN, EUNSUPPORTED), ECUDA.
  */

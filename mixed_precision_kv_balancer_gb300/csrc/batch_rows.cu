@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kMapThreads) batch_rows_kernel(const MapArgs a
       }
       if (mine) {
         const int32_t len = a.p.len_of(s);
-        const int32_t from = a.start ? a.start[lo] : len - max(a.counts[lo], 0);
+        const int32_t from = a.start ? a.start[lo] : len - (first[lo + 1] - first[lo]);   // the rows that the arrays hold
         if (from >= 0) {   // else refused, or more rows than slots
           const int64_t at = static_cast<int64_t>(from) + (r - first[lo]);
           seq = s;

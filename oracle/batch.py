@@ -16,7 +16,7 @@ def batch_rows(table, lens, ps, n_pages, seqs, start, counts, rows):
         named = seqs is not None and s in [int(x) for x in seqs[:i]]
         ok = 0 <= s < max_seqs and not named
         length = min(max(int(lens[s]), 0), table.shape[1] * ps) if ok else 0
-        first = length - c if start is None else int(start[i])
+        first = length - min(c, rows - at) if start is None else int(start[i])   # of the rows that the arrays hold
         for t in range(c):
             if at >= rows:
                 break

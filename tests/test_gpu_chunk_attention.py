@@ -492,3 +492,28 @@ def test_parts_of_many_items(type, window, sinks):
         again = cache.attend_rows(0, q, batch, window, sinks, ws=ws)
         assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
     assert _lib.mikv_wait_status() == 0
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_a_batch_that_its_arrays_cut_off(given):
+    """Maps and attention place the rows that are left of a request alike."""
+    cache = ph.make([90, 70, 50], 16, 2, "fp16")
+    counts, rows = ints([20, 30, 10]), 35
+    start = ints([70, 40, 40]) if given else None
+    batch = cache.rows(counts, rows, start=start)
+    assert batch.row_start.tolist() == [0, 20, 35, 35]
+    first = 40 if given else 70 - 15
+    assert batch.pos.tolist() == list(range(70, 90)) + list(range(first, first + 15)) and batch.seq.tolist() == [0] * 20 + [1] * 15
+    q = _rows(rows, 8, "fp16")
+    want, wl, mag = expect(cache, q, [0, 20, 35, 35], 0, 0, start=None if start is None else start.tolist())
+    out, lse = cache.attend_rows(0, q, batch)
+    ph.close(out, want, mag, 2.0 ** -11, weights=2.0 ** -11)
+    ph.close_lse(lse, wl)
+    # and picked blocks, all of them, see the same slots
+    buf = cache.bounds_buffers()
+    lens = cache.lens.clone()
+    cache.renew(0, cache.rows(lens, int(lens.sum())), buf)
+    sel, n_sel = cache.pick(0, q, buf, 6, batch=batch)
+    out, lse = cache.attend_blocks(0, q, sel, n_sel, batch)
+    ph.close(out, want, mag, 2.0 ** -11, weights=2.0 ** -16)
+    ph.close_lse(lse, wl)
