@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectAr
   if (tid == 0) a.n_sel[unit] = n;
   for (int i = tid; i < a.keep; i += kPickThreads)
     if (i >= n || nb <= a.keep) sel[i] = i < n ? i : -1;
-  pdl_wait();
+  pdl_wait();   // (what came before belongs to no kernel of this call, whose first began when all others were done)
   if (nb <= a.keep) return;
   const uint32_t* keys = a.keys + static_cast<size_t>(unit) * a.p.max_pages;
   uint32_t k[kMine];
