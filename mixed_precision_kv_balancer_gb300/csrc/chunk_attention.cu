@@ -1186,12 +1186,14 @@ int launch(const ChunkArgs& a, cudaStream_t st) {
   using W = Warps<TYPE == MIKV_PAGES_INT8>;
   const auto kern = chunk_attention_kernel<TYPE>;
   // the warps share out what the block has at launch: with less of it they would wait for ever
-  static const cudaError_t built = [&] {
+  static std::atomic<bool> known{false};
+  if (!known.load(std::memory_order_relaxed)) {
     cudaFuncAttributes f;
-    const cudaError_t e = cudaFuncGetAttributes(&f, kern);
-    return e != cudaSuccess ? e : f.numRegs == W::launch_regs ? cudaSuccess : cudaErrorLaunchOutOfResources;
-  }();
-  if (built != cudaSuccess) return check_launch_after(built, "chunk_attention_kernel");
+    cudaError_t e = cudaFuncGetAttributes(&f, kern);
+    if (e == cudaSuccess && f.numRegs != W::launch_regs) e = cudaErrorLaunchOutOfResources;
+    if (e != cudaSuccess) return check_launch_after(e, "chunk_attention_kernel");
+    known.store(true, std::memory_order_relaxed);
+  }
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCaSmem);
   if (e != cudaSuccess) return check_launch_after(e, "chunk_attention_kernel");
   kern<<<a.ctas, W::threads, kCaSmem, st>>>(km, vm, a);

@@ -1,4 +1,7 @@
 """Attention of packed rows over pages against the oracle in 64 bits, and whole serving steps of packed batches."""
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -517,3 +520,59 @@ def test_a_batch_that_its_arrays_cut_off(given):
     out, lse = cache.attend_blocks(0, q, sel, n_sel, batch)
     ph.close(out, want, mag, 2.0 ** -11, weights=2.0 ** -16)
     ph.close_lse(lse, wl)
+
+
+FIRST_CAPTURED = """
+import torch, sys
+sys.path[:0] = [{root!r}, {root!r} + "/tests"]
+import paged_helpers as ph
+cache = ph.make([300, 40], 16, 2, {type!r})
+q = ph.normal((60, 8, 128), 5, ph.DTYPE[{type!r}]).to(ph.DEV)
+counts, buf = ph.ints([50, 10]), cache.bounds_buffers()
+k, v = (ph.normal((60, 2, 128), i, ph.DTYPE[{type!r}]).to(ph.DEV) for i in (1, 2))
+ws, ws2 = cache.chunk_workspace(2, 60, 8), cache.block_workspace(60, 8, 3)
+def step():
+    batch = cache.rows(counts, 60)
+    cache.put(0, k, v, batch)
+    cache.renew(0, batch, buf)
+    out = cache.attend_rows(0, q, batch, ws=ws)
+    return (*out, *cache.attend_blocks(0, q, *cache.pick(0, q, buf, 3, batch=batch, ws=ws2), batch=batch, ws=ws2))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+want = step()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+print("alike")
+"""
+
+
+@pytest.mark.parametrize("type", TYPES)
+def test_first_calls_of_a_process_may_be_captured(type):
+    from conftest import ROOT
+    res = subprocess.run([sys.executable, "-c", FIRST_CAPTURED.format(root=ROOT, type=type)], capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0 and "alike" in res.stdout, res.stdout + res.stderr
+
+
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("lens,ps,Hkv,rep,counts", [([300, 90], 16, 1, 130, [1, 70]), ([77, 140], 8, 2, 65, [2, 3]), ([40], 4, 1, 1024, [1]),
+                                                    ([5000, 300], 2048, 1, 2, [200, 1]), ([900, 513], 256, 2, 4, [300, 9]), ([700], 12, 1, 4, [500])])
+def test_wide_groups_and_long_pages(type, lens, ps, Hkv, rep, counts):
+    cache = ph.make(lens, ps, Hkv, type)
+    q = _rows(sum(counts), Hkv * rep, type)
+    check(cache, q, starts(counts))
+    check(cache, q, starts(counts), 150, 7)
+    # the same rows over picked blocks, all of them
+    batch = cache.rows(ints(counts), sum(counts))
+    buf = cache.bounds_buffers()
+    held_ = cache.lens.clone()
+    cache.renew(0, cache.rows(held_, int(held_.sum())), buf)
+    blocks = -(-max(lens) // ps)
+    sel, n_sel = cache.pick(0, q, buf, blocks, batch=batch)
+    out, lse = cache.attend_blocks(0, q, sel, n_sel, batch)
+    want, wl, mag = expect(cache, q, starts(counts), 0, 0)
+    ph.close(out, want, mag, ph.HALF_STEP[type], weights=2.0 ** -16)
+    ph.close_lse(lse, wl)
+    assert _lib.mikv_wait_status() == 0
