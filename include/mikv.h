@@ -635,9 +635,10 @@ size_t mikv_block_attention_workspace_bytes(const mikv_pages* p, int rows, int H
  * (NULL: the rows are the sequence's last ones) and sees slot j of its sequence (j below the
  * length) as in mikv_paged_attention.  Append the rows' keys and values first.
  * q, out [rows][Hq][D] by stride_t and stride_h (stride_b unused), fp16 (bf16 for BF16 pages); lse fp32
- * [rows][Hq], or NULL.  A row that sees nothing (its request was refused, its sequence is empty or out of
- * range, its position is below 0) gives out 0 and lse -inf.  Rows of no request are not written.
- * Several requests may name one sequence.  Slots that are not seen by any row of a request may
+ * [rows][Hq], or NULL.  A row that sees nothing (its request has a start below 0, or without starts more rows than
+ * slots, its sequence is empty or out of range) gives out 0 and lse -inf.  Rows of no request are not written.
+ * Several requests may name one sequence: each is answered, also those that mikv_batch_rows gives no
+ * place to, as an earlier one has it.  Slots that are not seen by any row of a request may
  * hold anything; a value row that one of them sees must be finite, or it may reach the request's
  * other rows.  Slots on a page outside the pool read as zeros (reported, mikv_wait_status bit 64).
  * start is held at 2^30.  The softmax weights are rounded once to 16 bits before they meet the values; sums and statistics are fp32.

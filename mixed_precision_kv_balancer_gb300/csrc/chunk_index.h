@@ -35,13 +35,14 @@ struct Rows {
   int32_t rows, off, keys;
 };
 constexpr int32_t kMaxPos = 1 << 30;   // positions of a request's first row are held here, and slots lie below
-// `held`: slots of its sequence.  A request that is refused has none.
+// `held`: slots of its sequence.  A request that is refused has no keys: a start below 0, or without starts
+// more rows than slots, as in the row maps.
 MIKV_HD Rows rows_of(int32_t rows, int32_t held, bool from_start, int32_t start) {
   Rows r;
   r.rows = rows;
   r.off = from_start ? min_of(max_of(start, -1), kMaxPos) : held - rows;
   // keys that its last row sees: below 2^30 + 2^20
-  r.keys = (from_start && start < 0) || held <= 0 ? 0 : max_of(0, min_of(held, r.off + rows));
+  r.keys = (from_start ? start < 0 : rows > held) || held <= 0 ? 0 : max_of(0, min_of(held, r.off + rows));
   return r;
 }
 

@@ -230,3 +230,37 @@ def test_positions_far_below_zero(tmp_path):
                     "-o", str(tmp_path / "below")], check=True)
     res = subprocess.run([str(tmp_path / "below")], capture_output=True, text=True)
     assert res.returncode == 0, res.stdout + res.stderr
+
+
+MORE = r"""
+#include <cstdio>
+#include <initializer_list>
+#include "chunk_index.h"
+using namespace mikv;
+int main() {   // without a start, a request with more rows than its sequence has slots is refused: none of its rows sees a key
+  for (int held : {0, 1, 8, 300})
+    for (int rows : {1, 2, 8, 10, 64, 65, 301, 1 << 20})
+      for (int window : {0, 1, 100, 1 << 30})
+        for (int sinks : {0, 4}) {
+          const Rows r = rows_of(rows, held, false, 0);
+          const RowTiles t = row_tiles_of(rows, 3);
+          if (r.keys != (rows > held ? 0 : held)) return std::printf("%d rows, %d slots: %d keys\n", rows, held, r.keys), 1;
+          for (int blk = 0; rows > held && blk < t.blocks; ++blk)
+            if (chunk_tiles<128>(t, r, window, sinks, blk).tiles || chunk_tiles<64>(t, r, window, sinks, blk).tiles) return 1;
+        }
+  return 0;
+}
+"""
+
+
+def test_more_rows_than_slots_see_nothing(tmp_path):
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no g++")
+    src = tmp_path / "more.cpp"
+    src.write_text(MORE)
+    inc = os.path.join(ROOT, "mixed_precision_kv_balancer_gb300", "csrc")
+    subprocess.run([gxx, "-O1", "-std=c++17", "-fsanitize=undefined,address", "-fno-sanitize-recover", "-I", inc, str(src),
+                    "-o", str(tmp_path / "more")], check=True)
+    res = subprocess.run([str(tmp_path / "more")], capture_output=True, text=True)
+    assert res.returncode == 0, res.stdout + res.stderr

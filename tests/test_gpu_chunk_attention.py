@@ -576,3 +576,26 @@ def test_wide_groups_and_long_pages(type, lens, ps, Hkv, rep, counts):
     ph.close(out, want, mag, ph.HALF_STEP[type], weights=2.0 ** -16)
     ph.close_lse(lse, wl)
     assert _lib.mikv_wait_status() == 0
+
+
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (5, 2)])
+def test_more_rows_than_slots_are_refused_by_maps_and_attention_alike(type, window, sinks):
+    """Requests without a start: those that the maps refuse see nothing, as if their starts were -1."""
+    cache = ph.make([8, 40, 0, 200, 300], 16, 2, type)
+    counts = [10, 5, 3, 201, 300]
+    n = sum(counts)
+    q = _rows(n, 8, type)
+    batch = cache.rows(ints(counts), n)
+    refused = batch.seq < 0
+    assert refused.nonzero()[:, 0].tolist() == list(range(10)) + list(range(15, 219))
+    out, lse = (torch.full(s, 7.0, dtype=t, device=ph.DEV) for s, t in ((q.shape, q.dtype), (q.shape[:2], torch.float32)))
+    cache.attend_rows(0, q, batch, window, sinks, out=out, lse=lse)
+    assert (out[refused] == 0).all() and torch.isneginf(lse[refused]).all()
+    want = check(cache, q, starts(counts), window, sinks, start=[-1, 35, -1, -1, 0])
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    lens = cache.lens.clone()
+    buf = cache.bounds_buffers()
+    cache.renew(0, cache.rows(lens, int(lens.sum())), buf)
+    out, lse = cache.attend_blocks(0, q, *cache.pick(0, q, buf, 4, batch=batch), batch)
+    assert (out[refused] == 0).all() and torch.isneginf(lse[refused]).all() and torch.isfinite(lse[~refused]).all()
