@@ -19,6 +19,7 @@ constexpr int kMapThreads = 256;
 constexpr int kMapRows = 4 * kMapThreads;   // of a CTA
 constexpr int kMaxBatch = 4096;             // requests of a call
 constexpr int kMaxMapRows = 1 << 30;        // and its rows: numbers of a CTA behind the last one fit 32 bits too
+constexpr int kMapSmem = (kMaxBatch + 1 + 2 * 2 * kMaxBatch) * 4;   // the most that a call needs: sums, and a table of two words a slot
 
 struct MapArgs {
   Pool p;
@@ -152,9 +153,10 @@ extern "C" int mikv_batch_rows(const mikv_pages* pages, const int32_t* seqs, con
   a.slots = 0;
   if (seqs)
     for (a.slots = 64; a.slots < 2 * n;) a.slots *= 2;
-  const size_t smem = (static_cast<size_t>(n) + 1 + 2 * a.slots) * 4;   // at most 82 KB
+  const size_t smem = (static_cast<size_t>(n) + 1 + 2 * a.slots) * 4;
+  // The limit belongs to the kernel, not to the launch: all that set it set the same one, which holds for what other threads launch.
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(batch_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = cudaFuncSetAttribute(batch_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMapSmem);
     if (e != cudaSuccess) return check_launch_after(e, "batch_rows_kernel");
   }
   const int ctas = rows ? (rows - 1) / kMapRows + 1 : 1;

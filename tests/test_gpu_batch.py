@@ -1,5 +1,7 @@
 """Packed batches on the GPU: row maps, rows into slots, bounds of pages' keys, and the choice of blocks, against
 the oracle to the bit; attention over picked blocks and a whole serving step against it in 64 bits."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -352,3 +354,37 @@ def test_bounds_behind_a_row_past_the_length():
     _lib.mikv_page_bounds(cache, 0, ints([0, 0, 0]), ints([15, 14, 9]), *buf)
     page = int(cache.table[0, 1])
     assert torch.equal(buf[0][0, page], want[0][0, page]) and torch.equal(buf[1][0, page], want[1][0, page]) and buf[1][0, page, 0] > 0
+
+
+def test_row_maps_of_several_threads():
+    """Calls of different sizes whose tables of sequences need more shared memory than a kernel has unasked, each thread's
+    on a stream of its own: none fails for what another asks."""
+    lib, failed, done = _lib.load(), [], []
+    sizes = [2049, 2600, 3300, 4096]
+    cache = ph.make([3] * 4096, 8, 1, "fp16")
+    work = []
+    for n in sizes:
+        seqs, counts = torch.randperm(4096, device=ph.DEV)[:n].int(), torch.ones(n, dtype=torch.int32, device=ph.DEV)
+        work.append((n, seqs, counts, torch.empty(n + 1, dtype=torch.int32, device=ph.DEV),
+                     torch.empty(3, n, dtype=torch.int32, device=ph.DEV), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    begin = threading.Barrier(len(work))
+
+    def run(n, seqs, counts, row_start, maps, stream):
+        torch.cuda.set_device(0)
+        args = (cache.ref, seqs.data_ptr(), None, counts.data_ptr(), n, n, row_start.data_ptr(), *(m.data_ptr() for m in maps),
+                stream.cuda_stream)
+        begin.wait()
+        codes = {lib.mikv_batch_rows(*args) for _ in range(3000)}
+        stream.synchronize()
+        (done if codes == {0} else failed).append((n, codes))
+
+    threads = [threading.Thread(target=run, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed and len(done) == len(work), failed
+    for n, seqs, _, row_start, maps, _ in work:
+        assert torch.equal(row_start, torch.arange(n + 1, dtype=torch.int32, device=ph.DEV)) and torch.equal(maps[0], seqs)
+        assert (maps[1] == 2).all() and torch.equal(maps[2], cache.table[seqs.long(), 0] * 8 + 2)
