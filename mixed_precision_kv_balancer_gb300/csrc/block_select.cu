@@ -18,6 +18,7 @@
 
 #include <algorithm>
 
+#include "block_index.h"
 #include "paged.cuh"
 #include "tcgen05.cuh"
 
@@ -33,6 +34,7 @@ constexpr int kBsBlocks = 32 * kBsSteps;       // blocks of a warp
 constexpr int kBsRing = 2;                     // steps that are under way
 constexpr int kBsHeads = 8;                    // query heads of a pass
 constexpr int kBsSmem = kBsWarps * kBsRing * 32 * 2 * kD;
+static_assert(kBoundBytes == 2 * kD, "bounds of a block");
 constexpr int kPickThreads = 512;
 constexpr int kPickDigit = 11;                    // bits of a digit
 constexpr uint32_t kAlways = 0xffffffffu;   // above every score
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(kBsWarps * 32) block_score_kernel(const Select
       const int e = 2 * j + (lane >> 4), piece = lane & 15;
       const uint32_t src = __shfl_sync(0xffffffffu, from, e);
       const bool ok = src != kNoRow;
-      cp_async16(dst + e * (2 * kD) + ((piece ^ ((e & 1) << 2)) << 4), a.bounds + (layer0 + (ok ? src : 0)) * (2 * kD) + piece * 16, ok);
+      cp_async16(dst + bound_at(e, piece), a.bounds + (layer0 + (ok ? src : 0)) * (2 * kD) + piece * 16, ok);
     }
   };
   float best[kBsSteps];
@@ -239,12 +241,12 @@ __global__ void __launch_bounds__(kBsWarps * 32) block_score_kernel(const Select
       const uint32_t src = ring + i % kBsRing * (32 * 2 * kD);
       float top[2][2];   // blocks 16 mt + g and + 8
       float d[2][2][4] = {};   // two sums each, so that products wait for one another less (whole numbers: any order gives the same)
-      const uint32_t row = src + g * (2 * kD) + ((t ^ ((g & 1) << 2)) << 4);
+      const uint32_t at_lane = bound_at(g, t);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {   // 64 codes: of lo, lo, hi, hi
         uint4 x[2][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e >> 1][e & 1] = lds128((row ^ (k << 6)) + e * 8 * 2 * kD);
+        for (int e = 0; e < 4; ++e) x[e >> 1][e & 1] = lds128(src + bound_of_lane(at_lane, e, k));
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
