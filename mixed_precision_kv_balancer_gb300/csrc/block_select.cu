@@ -29,11 +29,10 @@ int block_select_status(unsigned* out, bool clear) { return tc::wait_giveups(out
 namespace {
 
 constexpr int kBsWarps = 4;
-constexpr int kBsSteps = 2;                    // of 32 blocks a warp
+constexpr int kBsSteps = 2;                    // of 32 blocks a warp, each with a buffer of its own: all are under way at once
 constexpr int kBsBlocks = 32 * kBsSteps;       // blocks of a warp
-constexpr int kBsRing = 2;                     // steps that are under way
 constexpr int kBsHeads = 8;                    // query heads of a pass
-constexpr int kBsSmem = kBsWarps * kBsRing * 32 * 2 * kD;
+constexpr int kBsSmem = kBsWarps * kBsSteps * 32 * 2 * kD;
 static_assert(kBoundBytes == 2 * kD, "bounds of a block");
 constexpr int kPickThreads = 512;
 constexpr int kPickDigit = 11;                    // bits of a digit
@@ -45,7 +44,7 @@ struct SelectArgs {
   const int8_t* bounds;
   const float* scales;
   const int32_t *row_seq, *row_pos;
-  int layer, rows, Hq, rep, keep, first, recent;
+  int layer, rows, rep, keep, first, recent;
   int chunks;            // warps of a (row, key head)
   int64_t warps;         // of all
   int32_t *sel, *n_sel;
@@ -162,7 +161,7 @@ __global__ void __launch_bounds__(kBsWarps * 32) block_query_kernel(const Select
 // side, whose bounds lie side by side.  OWN: it makes the queries' codes itself.
 template <bool OWN>
 __global__ void __launch_bounds__(kBsWarps * 32) block_score_kernel(const SelectArgs a) {
-  extern __shared__ __align__(16) uint4 s_b[];   // [warp][ring][32 blocks][16 pieces], swizzled by the block
+  extern __shared__ __align__(16) uint4 s_b[];   // [warp][step][32 blocks][16 pieces], swizzled by the block
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   pdl_trigger();
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kBsWarps + w;
@@ -185,7 +184,7 @@ __global__ void __launch_bounds__(kBsWarps * 32) block_score_kernel(const Select
   const int unit = r * a.p.Hkv + h;
   const size_t layer0 = static_cast<size_t>(a.layer) * a.p.n_pages * a.p.Hkv;
   const int steps = min(kBsSteps, (nb - b0 + 31) / 32);
-  const uint32_t ring = smem_u32(s_b) + w * (kBsRing * 32 * 2 * kD);
+  const uint32_t buffers = smem_u32(s_b) + w * (kBsSteps * 32 * 2 * kD);
   uint32_t at[kBsSteps];   // (page, key head) of the lane's block, kNoRow without one
 #pragma unroll
   for (int i = 0; i < kBsSteps; ++i) {
@@ -193,7 +192,7 @@ __global__ void __launch_bounds__(kBsWarps * 32) block_score_kernel(const Select
     at[i] = ok ? static_cast<uint32_t>(page[i]) * a.p.Hkv + h : kNoRow;   // (below 2^32, like the pool's rows)
   }
   const auto fetch = [&](int i, uint32_t from) {
-    const uint32_t dst = ring + i % kBsRing * (32 * 2 * kD);
+    const uint32_t dst = buffers + i * (32 * 2 * kD);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {   // two blocks an instruction
       const int e = 2 * j + (lane >> 4), piece = lane & 15;
@@ -210,7 +209,7 @@ __global__ void __launch_bounds__(kBsWarps * 32) block_score_kernel(const Select
   for (int i = 0; i < kBsSteps; ++i) sb[i] = at[i] != kNoRow ? a.scales[layer0 + at[i]] : 0.f;
   for (int g0 = 0; g0 < a.rep; g0 += kBsHeads) {
 #pragma unroll
-    for (int i = 0; i < kBsRing; ++i) {
+    for (int i = 0; i < kBsSteps; ++i) {
       if (i < steps) fetch(i, at[i]);
       cp_async_commit();
     }
@@ -236,9 +235,13 @@ __global__ void __launch_bounds__(kBsWarps * 32) block_score_kernel(const Select
 #pragma unroll
     for (int i = 0; i < kBsSteps; ++i) {
       if (i >= steps) break;
-      cp_async_wait<kBsRing - 1>();
+      static_assert(kBsSteps == 2, "the first step's copies, then all");
+      if (i == 0)
+        cp_async_wait<1>();
+      else
+        cp_async_wait<0>();
       __syncwarp();
-      const uint32_t src = ring + i % kBsRing * (32 * 2 * kD);
+      const uint32_t src = buffers + i * (32 * 2 * kD);
       float top[2][2];   // blocks 16 mt + g and + 8
       float d[2][2][4] = {};   // two sums each, so that products wait for one another less (whole numbers: any order gives the same)
       const uint32_t at_lane = bound_at(g, t);
@@ -282,12 +285,8 @@ __global__ void __launch_bounds__(kBsWarps * 32) block_score_kernel(const Select
         if (lane >> 3 == e) mine = x;
       }
       best[i] = fmaxf(best[i], mine);
-      __syncwarp();   // the step's pieces have been read
-      if (i + kBsRing < kBsSteps && i + kBsRing < steps) fetch(i + kBsRing, at[(i + kBsRing) % kBsSteps]);
-      cp_async_commit();
     }
-    cp_async_wait<0>();
-    __syncwarp();
+    __syncwarp();   // the pieces have been read: the next heads' copies may be written over them
   }
 #pragma unroll
   for (int i = 0; i < kBsSteps; ++i) {
@@ -505,7 +504,6 @@ extern "C" int mikv_block_select(const void* q, const mikv_pages* pages, int lay
   a.row_pos = row_pos;
   a.layer = layer;
   a.rows = rows;
-  a.Hq = Hq;
   a.rep = Hq / a.p.Hkv;
   a.keep = keep;
   a.first = first;
