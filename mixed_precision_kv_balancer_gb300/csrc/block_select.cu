@@ -524,6 +524,8 @@ extern "C" int mikv_block_select(const void* q, const mikv_pages* pages, int lay
   const auto score = own ? block_score_kernel<true> : block_score_kernel<false>;
   const cudaError_t e = cudaFuncSetAttribute(score, cudaFuncAttributeMaxDynamicSharedMemorySize, kBsSmem);
   if (e != cudaSuccess) return check_launch_after(e, "block_score_kernel");
+  // The first kernel stays a normal launch: those behind it read the rows, table, lengths and bounds, and write sel and n_sel,
+  // before they wait.
   if (own) {
     score<<<static_cast<unsigned>(ctas), kBsWarps * 32, kBsSmem, st>>>(a);
     if (int r = check_launch("block_score_kernel")) return r;

@@ -135,8 +135,12 @@ __device__ __forceinline__ void split_f16(float x, __half& hi, __half& lo) {
 // Programmatic dependent launch.  A kernel started by launch_after() may begin while the
 // kernel before it in the stream is still running; pdl_wait() returns once that kernel has
 // completed and its writes are visible (at once for a normal launch).  Every CTA of such a
-// kernel calls pdl_wait() before its first global access, so each kernel of a chain also
-// completes after its predecessor.  pdl_trigger() lets the next kernel start launching.
+// kernel calls pdl_wait(), so each kernel of a chain also completes after its predecessor, and
+// calls it before its first access to what a kernel of the chain writes.  Where the chain's
+// first kernel is a normal launch, which begins when all work before it is done, a kernel may
+// read the call's inputs and write outputs that no other kernel of the chain touches before that;
+// where the first kernel is itself started by launch_after(), nothing is touched before the wait.
+// pdl_trigger() lets the next kernel start launching.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;\n" ::); }
 
