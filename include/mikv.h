@@ -641,7 +641,8 @@ size_t mikv_block_attention_workspace_bytes(const mikv_pages* p, int rows, int H
  * place to, as an earlier one has it.  Slots that are not seen by any row of a request may
  * hold anything; a value row that one of them sees must be finite, or it may reach the request's
  * other rows.  Slots on a page outside the pool read as zeros (reported, mikv_wait_status bit 64).
- * start is held at 2^30.  The softmax weights are rounded once to 16 bits before they meet the values; sums and statistics are fp32.
+ * start is held at 2^30.  The softmax weights are rounded once to 16 bits before they meet the values, single tokens' too
+ * (mikv_paged_attention and mikv_block_attention keep two 16-bit parts of each); sums and statistics are fp32.
  * rows at most 2^20, max_pages * page_size at most 2^30, n at most 4096, Hq a multiple of Hkv, up to 1024 query heads per key head; n == 0 or rows == 0 does nothing.
  * ws >= mikv_chunk_attention_workspace_bytes(p, n, rows, Hq), 32-byte aligned; two calls must not share
  * a workspace concurrently.

@@ -109,6 +109,7 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xfffffff
 // `last`: the last key that the row may see, its position p or less.  Args: qb.window, qb.sinks and scale.
 // PARTS 2: the scores are the sum of two products, the second COLS columns behind the first.
 // W: the weights' factor, and how far the reference may lag.
+// A weight is rounded once to 16 bits, half a step of its own, as the products take it; why, the kernels say.
 // `settle` returns once all products into the accumulator that were issued are done; it is called before a rescaling.
 template <bool BF, int COLS, int PARTS, class W = Weights<BF>, class Args, class Settle>
 __device__ __forceinline__ void softmax_tile(const Args& a, uint32_t ts, uint32_t to, bool whole, int p, int last, int j0, Row& r,

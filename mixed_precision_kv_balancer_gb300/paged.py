@@ -160,7 +160,8 @@ class PagedCache:
 
     def attend_rows(self, layer, q, batch, window=0, sinks=0, out=None, lse=None, ws=None):
         """Rows q [rows][Hq][D] of a batch against their sequences; returns out and lse fp32 [rows][Hq].  Rows
-        of no request are left as they were (outputs made here: 0)."""
+        of no request are left as they were (outputs made here: 0).  Softmax weights are rounded once to 16 bits; attend and
+        attend_blocks keep two parts of each."""
         out = torch.zeros(q.shape, dtype=q.dtype, device=self.device) if out is None else out
         lse = torch.zeros(q.shape[:2], dtype=torch.float32, device=self.device) if lse is None else lse
         _lib.mikv_chunk_attention(q, self, layer, batch.row_start, window, sinks, out, lse, seqs=batch.seqs, start=batch.start, ws=ws)

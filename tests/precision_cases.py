@@ -77,3 +77,26 @@ def emulated(q, k, v, type, parts, rounded_sum):
         out[h] = to16((w @ v[h // rep].astype(np.float32)) / total, type)
         lse[h] = (s.max() + np.log2(total / factor)) * np.float32(np.log(2.0))
     return out, lse
+
+
+def codes_beyond_16_bits(n_keys, heads, key_heads, seed):
+    """q [heads][128], and 8-bit keys and values (codes [key_heads][n_keys][128] and (scale, zero) [...][2][2]) whose values no 16-bit
+    number holds.  Queries are 1/16 or -1/16 in four channels, the keys of a head all alike (roundings of many would average
+    out), spread over -16 .. 16 by channels: sum |q k| is at most 4.  Values are 1 + 2^-12 or -1 in turn."""
+    rng = np.random.RandomState(seed)
+    q = np.zeros((heads, 128))
+    for h in range(heads):
+        q[h, rng.permutation(128)[:4]] = rng.choice([-1, 1], 4) / 16.0
+    k = rng.randint(0, 256, (key_heads, 1, 128)).astype(np.uint8).repeat(n_keys, 1)
+    km = np.empty((key_heads, n_keys, 2, 2), np.float16)
+    km[..., 0], km[..., 1] = rng.uniform(0.1, 0.125, (key_heads, 1, 2)), -16
+    v = np.zeros(k.shape, np.uint8)
+    vm = np.zeros_like(km)
+    v[:, ::2], vm[:, ::2, :, 0], vm[:, ::2, :, 1], vm[:, 1::2, :, 1] = 1, 2.0 ** -12, 1, -1
+    return q, (k, km), (v, vm)
+
+
+def code_values(codes, meta):
+    """What 8-bit rows stand for, in 64 bits."""
+    x = codes.reshape(*codes.shape[:-1], 2, 64).astype(np.float64)
+    return (x * meta[..., :1].astype(np.float64) + meta[..., 1:].astype(np.float64)).reshape(codes.shape)

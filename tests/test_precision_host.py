@@ -32,3 +32,26 @@ def test_bounds_tell_the_weights_types_apart():
         want, _ = pc.softmax64(q, k, v)
         coarse, _ = pc.emulated(q, k, v, "bf16", 1, False)
         assert pc.out_error(coarse, want, pc.HALF_STEP["fp16"], pc.HALF_STEP["fp16"], n) > 1
+
+
+@pytest.mark.parametrize("n", [2, 18, 64, 200])
+def test_bounds_tell_codes_of_one_16_bit_number(n):
+    """8-bit keys that enter the products as one fp16 number miss the lse's bound, as two they keep it; values that do miss the
+    outputs' where all weights are alike."""
+    q, k, v = pc.codes_beyond_16_bits(n, 8, 2, n)
+    kv, vv = pc.code_values(*k), pc.code_values(*v)
+    assert np.abs(kv).max() <= 16 and (np.abs(q) @ np.abs(kv[0]).T).max() <= 4
+    want, wl = pc.softmax64(q, kv, vv)
+    share = 2.0 ** -20
+    one = pc.to16(kv, "fp16").astype(np.float64)
+    two = one + pc.to16(kv - one, "fp16")
+    for keys, keeps in ((one, False), (two, True)):
+        err = np.abs(pc.emulated(q, keys, vv, "fp16", 1, False)[1] - wl) - share
+        assert (pc.lse_error(wl + err, wl, n) < 1) == keeps
+    # no query: all weights are alike, and outputs are 2^-13
+    want, _ = pc.softmax64(0 * q, kv, vv)
+    assert (want == 2.0 ** -13).all()
+    one = pc.to16(vv, "fp16").astype(np.float64)
+    assert pc.out_error(pc.softmax64(0 * q, kv, one)[0], want, 2.0 ** -11, 2.0 ** -22, n) > 1
+    two = one + pc.to16(vv - one, "fp16")
+    assert pc.out_error(pc.softmax64(0 * q, kv, two)[0], want, 2.0 ** -11, 2.0 ** -22, n) < 1
