@@ -620,6 +620,8 @@ size_t mikv_block_select_workspace_bytes(const mikv_pages* p, int rows, int Hq);
  * slots lie at or before the row's position.  A block named twice counts twice; one that is none of
  * the row's is not seen and reported (mikv_wait_status, bit 64).  Otherwise as mikv_paged_attention:
  * out [rows][Hq][D], lse fp32 [rows][Hq] or NULL, over the seen slots alone.
+ * rows * Hkv <= 65535 (more rows: several calls, each with its part of every array), up to 1024 query heads per key head,
+ * keep * page_size at most 2^31 - 4097.
  * ws >= mikv_block_attention_workspace_bytes(p, rows, Hq, keep), 16-byte aligned; two calls must not
  * share a workspace concurrently.
  */

@@ -84,7 +84,7 @@ class PagedCache:
 
     def block_workspace(self, rows, Hq, keep):
         """For pick and for attend_blocks, one behind the other."""
-        lib = _lib.load()
+        lib, rows = _lib.load(), -(-rows // max(1, len(self._row_parts(rows))))
         return self._bytes(max(lib.mikv_block_select_workspace_bytes(self.ref, rows, Hq),
                                lib.mikv_block_attention_workspace_bytes(self.ref, rows, Hq, keep)))
 
@@ -173,17 +173,36 @@ class PagedCache:
         rows, Hkv = q.shape[0], self.k.shape[2]
         sel = torch.empty(rows, Hkv, keep, dtype=torch.int32, device=self.device) if sel is None else sel
         n_sel = torch.empty(rows, Hkv, dtype=torch.int32, device=self.device) if n_sel is None else n_sel
-        seq, pos = (None, None) if batch is None else (batch.seq, batch.pos)
-        _lib.mikv_block_select(q, self, layer, *bounds, first, recent, sel, n_sel, row_seq=seq, row_pos=pos, ws=ws)
+        for seq, pos, q, sl, ns in self._in_parts(batch, q, sel, n_sel):
+            _lib.mikv_block_select(q, self, layer, *bounds, first, recent, sl, ns, row_seq=seq, row_pos=pos, ws=ws)
         return sel, n_sel
 
     def attend_blocks(self, layer, q, sel, n_sel, batch=None, out=None, lse=None, ws=None):
-        """Rows q [rows][Hq][D] against their picked blocks; returns out and lse fp32 [rows][Hq]."""
+        """Rows q [rows][Hq][D] against their picked blocks; returns out and lse fp32 [rows][Hq].  (Rows whose number times the
+        key heads is above 65535 go in several calls, as those of pick do.)"""
         out = torch.empty_like(q) if out is None else out
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=self.device) if lse is None else lse
-        seq, pos = (None, None) if batch is None else (batch.seq, batch.pos)
-        _lib.mikv_block_attention(q, self, layer, sel, n_sel, out, lse, row_seq=seq, row_pos=pos, ws=ws)
+        for seq, pos, q, sl, ns, o, l in self._in_parts(batch, q, sel, n_sel, out, lse):
+            _lib.mikv_block_attention(q, self, layer, sl, ns, o, l, row_seq=seq, row_pos=pos, ws=ws)
         return out, lse
+
+    def _row_parts(self, rows):
+        """Bounds of the equal parts in which the calls over picked blocks take rows: 65535 (row, key head) pairs at most."""
+        n = -(-rows // max(1, 65535 // self.k.shape[2]))
+        return [(rows * i // n, rows * (i + 1) // n) for i in range(n)]
+
+    def _in_parts(self, batch, *tensors):
+        """(sequences, positions, *tensors) of each part of the rows."""
+        rows = tensors[0].shape[0]
+        tensors = (None, None, *tensors) if batch is None else (batch.seq, batch.pos, *tensors)
+        parts = self._row_parts(rows)
+        if len(parts) < 2:
+            return [tensors]
+        if any(t is not None and t.shape[0] != rows for t in tensors):
+            raise ValueError(f"expected tensors of {rows} rows, got {[None if t is None else t.shape[0] for t in tensors]}")
+        if batch is None:   # row r is sequence r
+            tensors = (torch.arange(rows, dtype=torch.int32, device=self.device), *tensors[1:])
+        return [tuple(None if t is None else t[a:b] for t in tensors) for a, b in parts]
 
 
 class BatchRows(NamedTuple):

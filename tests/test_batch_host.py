@@ -144,3 +144,30 @@ def test_rows_beyond_what_a_call_numbers_are_refused(lib):
     most = (1 << 30) + 1
     assert lib.mikv_batch_rows(_pages(), None, None, FAKE, 2, most, FAKE, FAKE, FAKE, FAKE, None) == ESHAPE
     assert lib.mikv_slot_append(_pages(), 0, _rows(), _rows(st=0), most, FAKE, None) == ESHAPE
+
+
+def test_rows_over_picked_blocks_go_in_parts():
+    """Each part is one that a call takes, and they are the rows in order."""
+    import types
+
+    import torch
+    from mixed_precision_kv_balancer_gb300.paged import PagedCache
+    for Hkv in (1, 2, 8, 32, 40000, 70000):
+        cache = types.SimpleNamespace(k=torch.empty(1, 1, Hkv, 1, 0), device="cpu")
+        cache._row_parts = lambda n, c=cache: PagedCache._row_parts(c, n)
+        for rows in (0, 1, 2, 100, 8191, 8192, 65535, 65536, 200001):
+            if Hkv >= 40000 and rows > 100:
+                continue
+            parts = cache._row_parts(rows)
+            assert all((b - a) * Hkv <= 65535 or b - a == 1 for a, b in parts) and max([b - a for a, b in parts], default=0) <= -(-rows // max(1, len(parts)))
+            assert [a for a, _ in parts] + [rows] * bool(parts) == [0] * bool(parts) + [b for _, b in parts]
+            assert (len(parts) <= 1) == (rows * Hkv <= 65535 or rows <= 1 or rows <= 65535 // Hkv)
+            q, sel = torch.arange(rows), torch.arange(rows) + 7
+            got = PagedCache._in_parts(cache, None, q, sel)
+            if len(parts) > 1:
+                assert torch.equal(torch.cat([g[0] for g in got]), q.int()) and all(g[1] is None for g in got)
+                assert torch.equal(torch.cat([g[3] for g in got]), sel)
+                with pytest.raises(ValueError, match="rows"):
+                    PagedCache._in_parts(cache, None, q, sel[1:])
+            else:
+                assert len(got) == 1 and got[0][0] is None and got[0][2] is q and got[0][3] is sel

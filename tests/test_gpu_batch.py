@@ -388,3 +388,49 @@ def test_row_maps_of_several_threads():
     for n, seqs, _, row_start, maps, _ in work:
         assert torch.equal(row_start, torch.arange(n + 1, dtype=torch.int32, device=ph.DEV)) and torch.equal(maps[0], seqs)
         assert (maps[1] == 2).all() and torch.equal(maps[2], cache.table[seqs.long(), 0] * 8 + 2)
+
+
+def _alike(a, la, b, lb, half_step, weights):
+    """Two answers of which each is off by half a step of itself, and its weights' and fp32's share of values below 8."""
+    a, b, slack = a.double(), b.double(), 8 * (weights + ph.FP32)
+    assert ((a - b).abs() <= 2 * half_step * (torch.maximum(a.abs(), b.abs()) + slack) + 2 * slack).all()
+    assert ((la - lb).abs() <= 4 * ph.FP32 + 2.0 ** -21 * lb.abs()).all()
+
+
+@pytest.mark.parametrize("type", TYPES)
+def test_more_rows_than_a_call_over_picked_blocks_takes(type):
+    """A batch of 2100 rows and 32 key heads, 67200 pairs: the same as its halves, and attention of packed rows over all blocks."""
+    H, n = 32, 2100
+    cache = ph.make([n - 300, 300], 64, H, type)
+    q = _query(n, H, type)
+    batch = cache.rows(ints([n - 300, 300]), n)
+    buf = cache.bounds_buffers()
+    cache.renew(0, batch, buf)
+    ws = cache.block_workspace(n, H, 3)
+    sel, n_sel = cache.pick(0, q, buf, 3, 1, 1, batch=batch, ws=ws)
+    out, lse = cache.attend_blocks(0, q, sel, n_sel, batch, ws=ws)
+    for at in (slice(0, 1000), slice(1000, n)):
+        half = batch._replace(seq=batch.seq[at].contiguous(), pos=batch.pos[at].contiguous())
+        s, c = cache.pick(0, q[at], buf, 3, 1, 1, batch=half)
+        assert torch.equal(s, sel[at]) and torch.equal(c, n_sel[at])
+    rows = [0, 1, 1049, 1050, 1051, 1799, 1800, 2098, 2099]
+    some = batch._replace(seq=batch.seq[rows].contiguous(), pos=batch.pos[rows].contiguous())
+    got = _check_blocks(cache, q[rows], sel[rows], n_sel[rows], some.seq.tolist(), some.pos.tolist())
+    _alike(out[rows], lse[rows], *got, ph.HALF_STEP[type], 2.0 ** -16)
+    all_blocks = -(-n // 64)
+    out, lse = cache.attend_blocks(0, q, *cache.pick(0, q, buf, all_blocks, batch=batch), batch)
+    dense, dense_lse = cache.attend_rows(0, q, batch)
+    _alike(out, lse, dense, dense_lse, ph.HALF_STEP[type], ph.HALF_STEP[type])
+
+
+def test_more_sequences_than_a_call_over_picked_blocks_takes():
+    """Without a batch, row r is sequence r in every part."""
+    H, n = 32, 2060
+    cache = ph.make([1 + i % 5 for i in range(n)], 2, H, "fp16")
+    q = _query(n, H, "fp16")
+    buf = _bounds_of_all(cache)
+    sel, n_sel = cache.pick(0, q, buf, 3)
+    assert torch.equal(n_sel, ((cache.lens + 1) // 2)[:, None].expand(-1, H))
+    out, lse = cache.attend_blocks(0, q, sel, n_sel)
+    want, wl = cache.attend(0, q)
+    _alike(out, lse, want, wl, 2.0 ** -11, 2.0 ** -16)
