@@ -540,13 +540,16 @@ __global__ void __launch_bounds__(kMaskThreads, kMaskMinBlocks) select_mask_kern
 // Rows of up to kSelStageMax / 5 keys are staged in shared memory (4 bytes of key and one of
 // flag per position); longer rows are read from global memory in every pass.  The candidate
 // list takes up to L / 8 entries of 6 bytes in what is left (none beyond 65536 positions).
+// (The limit of a kernel's shared memory belongs to the kernel, not to the launch: every call sets the same one, which holds
+// for what other threads launch.)
 constexpr int kSelStageMax = 200 * 1024;
+static_assert(kMaxSelectL <= kSelStageMax, "rows that are not staged");
 int launch_select(int units, const float* key1, long stride1, const float* key2, int L, int window, int take1,
                   int take2, int n_keep, int32_t* keep_pos, int32_t* evict_pos, float* keep_scores,
                   cudaStream_t s) {
   if (L <= kMaskRow) {
     const int smem = (L * 4 + 15) & ~15;
-    if (cudaFuncSetAttribute(select_mask_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    if (cudaFuncSetAttribute(select_mask_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaskRow * 4) != cudaSuccess)
       return check_launch("select_mask_kernel attribute");
     select_mask_kernel<<<units, kMaskThreads, smem, s>>>(key1, stride1, key2, L, window, take1, take2, n_keep,
                                                          keep_pos, evict_pos, keep_scores);
@@ -557,7 +560,7 @@ int launch_select(int units, const float* key1, long stride1, const float* key2,
   const int cap = L <= 65536 ? std::max(0, std::min(L / 8 + 32, (kSelStageMax - list_off) / 6)) : 0;
   const int smem = list_off + cap * 6;
   auto kern = stage ? select_kernel<true> : select_kernel<false>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelStageMax) != cudaSuccess)
     return check_launch("select_kernel attribute");
   kern<<<units, kSelThreads, smem, s>>>(key1, stride1, key2, L, window, take1, take2, n_keep, keep_pos,
                                                evict_pos, keep_scores, list_off, cap);
