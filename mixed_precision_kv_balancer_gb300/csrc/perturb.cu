@@ -395,8 +395,11 @@ extern "C" int mikv_output_perturbation(const float* o, const float* o_hat, cons
   if (int e = tc::encode_rows(&to, a, static_cast<long>(Hq) * nbb * kPtN, "output_perturbation: operand", kD, kPtN))
     return e;
   const int hmax = (Hq + nch - 1) / nch;  // heads of the largest chunk
-  const int smem = kPtSmem + hmax * 2 * kPtBatch * static_cast<int>(sizeof(float));
-  if (cudaFuncSetAttribute(perturb_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  constexpr int kScales = 2 * kPtBatch * static_cast<int>(sizeof(float));   // of a head
+  const int smem = kPtSmem + hmax * kScales;
+  // (the limit belongs to the kernel, not to the launch: the same one for every call, whatever other threads launch)
+  if (cudaFuncSetAttribute(perturb_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPtSmem + kPtMaxChunkHeads * kScales) !=
+      cudaSuccess)
     return check_launch("perturb_tc_kernel attribute");
   if (int e = check_launch_after(launch_after(perturb_tc_kernel, dim3(ncb, nch, nbb), dim3(kPtBlock), smem, s, tw, to,
                                               B, Hq, hidden, invs, ypart, part),

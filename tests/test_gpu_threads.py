@@ -51,3 +51,22 @@ def test_selections_of_different_lengths(lengths):
 
     _together([call(*w) for w in work], 3000)
     assert all(torch.equal(w[2], w[4]) for w in work)
+
+
+def test_perturbations_of_different_head_counts():
+    g = torch.Generator(device="cuda").manual_seed(2)
+    hidden, work = 16384, []          # a CTA a column block: its heads are all of them
+    for Hq in (1, 8, 24, 40):
+        o = torch.randn(1, Hq, 128, generator=g, device="cuda")
+        w = torch.randn(hidden, Hq * 128, generator=g, device="cuda").half()
+        y = torch.empty(1, hidden, device="cuda")
+        ws = torch.empty(_lib.load().mikv_output_perturbation_workspace_bytes(1, Hq, hidden), dtype=torch.uint8, device="cuda")
+        _lib.mikv_output_perturbation(o, None, w, y=y, ws=ws)
+        work.append((o, w, y, ws, y.clone()))
+
+    def call(o, w, y, ws, _):
+        return _lib.load().mikv_output_perturbation, (o.data_ptr(), None, w.data_ptr(), 1, o.shape[1], 128, hidden, y.data_ptr(), None,
+                                                      ws.data_ptr(), ws.numel())
+
+    _together([call(*w) for w in work], 1500)
+    assert all(torch.equal(w[2], w[4]) for w in work)
