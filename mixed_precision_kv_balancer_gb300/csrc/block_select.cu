@@ -518,8 +518,10 @@ extern "C" int mikv_block_select(const void* q, const mikv_pages* pages, int lay
   const int64_t ctas = (a.warps - 1) / kBsWarps + 1;
   if (ctas > 0x7fffffffLL) return fail(MIKV_ESHAPE, "block_select: rows=%d max_pages=%d", rows, a.p.max_pages);
   const cudaStream_t st = as_stream(stream);
-  // (one row of 8 key heads and 313 blocks takes 11 us either way, with a launch less where the codes are made in place; 24
-  // rows of up to 4096 blocks take 36 us with a kernel for them, 49 without)
+  // Whether the score kernel makes the queries' codes itself, a launch less, or one before it (8 key heads of 1 to 8 query heads,
+  // made in place / before): 40 to 320 warps 11 us either way, 640 11.7 / 12.7, 960 13.3 / 13.4, 2048 19.6 / 16.0, 8192 46.8 / 35.0;
+  // where no row has more blocks than it keeps 2.9 / 6.0.  (16 query heads, which every warp makes in two passes: 16.8 / 12.5 from
+  // 40 warps on, 30.9 / 20.5 at 2048.)
   const bool own = a.warps <= 8 * kNumSMs;
   const auto score = own ? block_score_kernel<true> : block_score_kernel<false>;
   const cudaError_t e = cudaFuncSetAttribute(score, cudaFuncAttributeMaxDynamicSharedMemorySize, kBsSmem);
