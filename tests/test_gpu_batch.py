@@ -434,3 +434,31 @@ def test_more_sequences_than_a_call_over_picked_blocks_takes():
     out, lse = cache.attend_blocks(0, q, sel, n_sel)
     want, wl = cache.attend(0, q)
     _alike(out, lse, want, wl, 2.0 ** -11, 2.0 ** -16)
+
+
+@pytest.mark.parametrize("type", TYPES)
+def test_batches_without_rows_do_nothing(type):
+    cache = ph.make([40, 0], 16, 2, type)
+    buf, dt = cache.bounds_buffers(), ph.DTYPE[type]
+    before = [ph.raw(t) for t in (cache.k, cache.v, *buf)]
+    for counts in ([], [0], [0, -3]):
+        batch = cache.rows(ints(counts), 0)
+        if counts:
+            assert batch.row_start.tolist() == [0] * (len(counts) + 1)
+        q, k = torch.empty(0, 8, 128, dtype=dt, device=ph.DEV), torch.empty(0, 2, 128, dtype=dt, device=ph.DEV)
+        cache.put(0, k, k, batch)
+        cache.renew(0, batch, buf)
+        out, lse = cache.attend_rows(0, q, batch)
+        sel, n_sel = cache.pick(0, q, buf, 3, batch=batch)
+        picked = cache.attend_blocks(0, q, sel, n_sel, batch)
+        assert [t.shape[0] for t in (out, lse, sel, n_sel, *picked)] == [0] * 6
+    batch = cache.rows(ints([]), 5)                  # rows of no request
+    assert batch.row_start.tolist() == [0] and all((t == -1).all() for t in batch[1:4])
+    q = _query(5, 8, type)
+    out, lse = cache.attend_rows(0, q, batch)
+    sel, n_sel = cache.pick(0, q, buf, 3, batch=batch)
+    picked = cache.attend_blocks(0, q, sel, n_sel, batch)
+    assert (out == 0).all() and (lse == 0).all() and (n_sel == 0).all() and (sel == -1).all()
+    assert (picked[0] == 0).all() and torch.isneginf(picked[1]).all()
+    cache.renew(0, batch, buf)
+    assert all((a == ph.raw(b)).all() for a, b in zip(before, (cache.k, cache.v, *buf))) and _lib.mikv_wait_status() == 0
